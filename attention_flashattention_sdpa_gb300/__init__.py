@@ -3,7 +3,9 @@
 Argument marshalling only: every step of the attention computation runs in the CUDA
 kernels of ``libsdpa_gb300.so``.  PyTorch supplies device memory and the current stream.
 The binding keeps the C names: :func:`sdpa_fwd`, :func:`sdpa_bwd`,
-:func:`sdpa_workspace_size`, :func:`sdpa_last_error_string`, :func:`sdpa_device_error`.
+:func:`sdpa_workspace_size`, :func:`sdpa_last_error_string`, :func:`sdpa_device_error`; for serving
+:func:`sdpa_rope_fwd`, :func:`sdpa_rope_bwd`, :func:`sdpa_cache_write`, :func:`sdpa_cache_read` and
+:func:`sdpa_decode`.
 
 Importing this package loads the library and raises ``ImportError`` if it has not been
 built (``python -m attention_flashattention_sdpa_gb300._build``); there is no fallback.
@@ -21,6 +23,9 @@ __all__ = [
     "sdpa_workspace_size", "sdpa_fwd", "sdpa_bwd", "sdpa_last_error_string", "causal_code",
     "sdpa_device_error", "sdpa_version", "sdpa_bwd_noalloc", "NOALLOC_SCRATCH_BYTES", "STATUS",
     "sdpa_dropout_mask_size", "sdpa_dropout_mask",
+    "RopeTable", "Rope", "Cache", "CacheRows", "Decode", "sdpa_rope_table", "sdpa_rope_fwd",
+    "sdpa_rope_bwd", "sdpa_cache_write", "sdpa_cache_read", "sdpa_decode",
+    "sdpa_decode_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsdpa_gb300.so")
@@ -65,26 +70,72 @@ class Problem(ctypes.Structure):
     ]
 
 
-def _packer():
-    """One struct.Struct that lays out a whole Problem at the offsets ctypes gives it, so
-    that a problem is marshalled by a single pack instead of one ctypes assignment per field."""
+class RopeTable(ctypes.Structure):
+    _fields_ = [
+        ("rot", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+        ("factor", ctypes.c_double), ("original_context", ctypes.c_double),
+        ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double), ("inv_freq", ctypes.c_void_p),
+    ]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [
+        ("b", ctypes.c_int32), ("h_q", ctypes.c_int32), ("h_k", ctypes.c_int32), ("s", ctypes.c_int32),
+        ("d", ctypes.c_int32), ("rot", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("attn_factor", ctypes.c_float), ("table", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p), ("positions_stride", ctypes.c_int64),
+        ("q", Strides), ("k", Strides), ("q_out", Strides), ("k_out", Strides),
+    ]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("h_kv", ctypes.c_int32),
+        ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("b", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_strides", Strides), ("v_strides", Strides), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+        ("page_table_stride", ctypes.c_int64), ("seq_lens_kv", ctypes.c_void_p),
+    ]
+
+
+class CacheRows(ctypes.Structure):
+    _fields_ = [
+        ("s", ctypes.c_int32), ("dtype", ctypes.c_int32), ("k", Strides), ("v", Strides),
+        ("seq_lens_q", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+    ]
+
+
+class Decode(ctypes.Structure):
+    _fields_ = [
+        ("h_q", ctypes.c_int32), ("s_q", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("causal", ctypes.c_int32), ("attn_scale", ctypes.c_float), ("q", Strides), ("o", Strides),
+        ("seq_lens_q", ctypes.c_void_p), ("tree_mask", ctypes.c_void_p),
+        ("tree_mask_stride", ctypes.c_int64),
+    ]
+
+
+def _packer(cls=Problem):
+    """One struct.Struct that lays out a whole ctypes structure at the offsets ctypes gives it, so
+    that it is marshalled by a single pack instead of one ctypes assignment per field."""
     fmt, pos = ["="], 0
-    codes = {ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_void_p: "Q"}
-    for name, typ in Problem._fields_:
-        off = getattr(Problem, name).offset
+    codes = {ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_void_p: "Q", ctypes.c_int64: "q"}
+    for name, typ in cls._fields_:
+        off = getattr(cls, name).offset
         fmt.append("x" * (off - pos))
         if typ is Strides:
             fmt.append("qqqq")
         else:
             fmt.append(codes[typ])
         pos = off + ctypes.sizeof(typ)
-    fmt.append("x" * (ctypes.sizeof(Problem) - pos))
+    fmt.append("x" * (ctypes.sizeof(cls) - pos))
     st = struct.Struct("".join(fmt))
-    assert st.size == ctypes.sizeof(Problem)
+    assert st.size == ctypes.sizeof(cls)
     return st
 
 
 _PACK = _packer()
+_PACK_ROPE, _PACK_CACHE, _PACK_ROWS, _PACK_DECODE = (_packer(c).pack for c in (Rope, Cache, CacheRows, Decode))
 _NO_STRIDES = (0, 0, 0, 1)
 
 
@@ -126,6 +177,20 @@ def _load():
     L.sdpa_version.restype = ctypes.c_int
     L.sdpa_problem_struct_size.argtypes = []
     L.sdpa_problem_struct_size.restype = SZ
+    # The serving structs are handed over as packed bytes.
+    L.sdpa_rope_table.argtypes = [VP, VP, ctypes.POINTER(ctypes.c_float)]
+    L.sdpa_rope_fwd.argtypes = L.sdpa_rope_bwd.argtypes = [VP, VP, VP, VP, VP, VP]
+    L.sdpa_cache_write.argtypes = L.sdpa_cache_read.argtypes = [VP, VP, VP, VP, VP]
+    L.sdpa_decode_workspace_size.argtypes = [VP, VP, ctypes.POINTER(SZ)]
+    L.sdpa_decode.argtypes = [VP, VP, VP, VP, VP, VP, SZ, VP]
+    for f in (L.sdpa_rope_table, L.sdpa_rope_fwd, L.sdpa_rope_bwd, L.sdpa_cache_write, L.sdpa_cache_read,
+              L.sdpa_decode_workspace_size, L.sdpa_decode):
+        f.restype = ctypes.c_int
+    L.sdpa_serving_struct_size.argtypes = [ctypes.c_int]
+    L.sdpa_serving_struct_size.restype = SZ
+    for i, cls in enumerate((RopeTable, Rope, Cache, CacheRows, Decode)):
+        if L.sdpa_serving_struct_size(i) != ctypes.sizeof(cls):
+            raise ImportError(f"{cls.__name__}: layout mismatch between the library and the binding")
     if L.sdpa_problem_struct_size() != ctypes.sizeof(Problem):
         raise ImportError("sdpa_problem_t layout mismatch between the library and the binding")
     return L
@@ -318,3 +383,235 @@ def sdpa_device_error() -> int:
     f = ctypes.c_uint32(0)
     _check(lib.sdpa_device_error(ctypes.byref(f)))
     return f.value
+
+
+# ---- serving: rotary positions, a paged cache, attention over it ------------------------------
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def sdpa_rope_table(rot: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                    original_context: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                    inv_freq=None, device="cuda"):
+    """(table, attn_factor) for the rotary calls: the turns per position of each of rot/2 pairs as an
+    int64 tensor of 64-bit binary fractions on ``device``, and the factor on the rotated values.
+
+    ``scaling``: "none", "linear", "ntk" or "yarn" (by parts), stretching by ``factor`` the
+    ``original_context``; or ``inv_freq``: rot/2 frequencies of the caller's own."""
+    import torch
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"unknown scaling {scaling!r}")
+    n = max(0, int(rot)) // 2
+    freqs = None
+    if inv_freq is not None:
+        vals = [float(f) for f in inv_freq]
+        if len(vals) != n:
+            raise ValueError(f"inv_freq needs rot/2 = {n} frequencies, got {len(vals)}")
+        freqs = (ctypes.c_double * max(1, n))(*vals)
+    cfg = RopeTable(int(rot), ROPE_SCALINGS[scaling], float(base), float(factor), float(original_context),
+                    float(beta_fast), float(beta_slow), ctypes.addressof(freqs) if freqs is not None else None)
+    out, att = torch.empty(n, dtype=torch.int64), ctypes.c_float(1.0)
+    _check(lib.sdpa_rope_table(ctypes.addressof(cfg), out.data_ptr() if n else ctypes.addressof(att), ctypes.byref(att)))
+    return out.to(device), att.value
+
+
+def _code(t, name: str) -> int:
+    try:
+        return dtype_code(t)
+    except KeyError:
+        raise ValueError(f"{name}: dtype {t.dtype} is not one the library takes") from None
+
+
+def _need(ok: bool, message: str):
+    if not ok:
+        raise ValueError(message)
+
+
+def _launch(fn, stream, like, *args):
+    """Calls ``fn(*args, stream)`` with the device of ``like`` current."""
+    import torch
+    dev = like.device.index
+    if dev == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream, like)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream, like)))
+
+
+def _same_device(like, *tensors):
+    dev = like.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors must be on one device ({dev} and {t.device} given)")
+
+
+def _ints(t, name: str, shape, dtype: str = "torch.int32"):
+    """A dense integer tensor of this shape (and nothing where it is None)."""
+    if t is not None:
+        _need(str(t.dtype) == dtype and tuple(t.shape) == shape and t.is_contiguous(),
+              f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _positions(positions, b: int, s: int):
+    """(pointer, elements between batches) of positions [b, s], or [s] or [1, s] for every batch."""
+    if positions is None:
+        return 0, 0
+    _need(str(positions.dtype) == "torch.int32" and tuple(positions.shape) in ((b, s), (1, s), (s,))
+          and (s == 1 or positions.stride(-1) == 1) and (positions.dim() == 1 or positions.stride(0) >= 0),
+          f"positions must be int32 of shape ({b}, {s}), (1, {s}) or ({s},) with a unit last stride")
+    shared = positions.dim() == 1 or (positions.shape[0] == 1 and b > 1)
+    return positions.data_ptr(), 0 if shared else positions.stride(0)
+
+
+def _rope(fn, q, k, q_out, k_out, table, positions, interleaved, attn_factor, stream):
+    _need(q.dim() == 4, "tensors are logical [b, h, s, d] views")
+    b, h_q, s, d = q.shape
+    dt, h_k = _code(q, "q"), 0
+    _need(q_out.shape == q.shape and q_out.dtype == q.dtype, "q_out must have q's shape and dtype")
+    _need((k is None) == (k_out is None), "k and k_out go together")
+    if k is not None:
+        _need(k.dim() == 4 and k.shape[0] == b and k.shape[2:] == q.shape[2:] and k.dtype == q.dtype,
+              "k must be [b, h_k, s, d] with q's b, s, d and dtype")
+        _need(k_out.shape == k.shape and k_out.dtype == k.dtype, "k_out must have k's shape and dtype")
+        h_k = k.shape[1]
+    _need(str(table.dtype) == "torch.int64" and table.dim() == 1 and table.is_contiguous(),
+          "table must be the int64 tensor of sdpa_rope_table")
+    pos, pos_stride = _positions(positions, b, s)
+    _same_device(q, k, q_out, k_out, table, positions)
+    p = _PACK_ROPE(b, h_q, h_k, s, d, 2 * table.shape[0], dt, 1 if interleaved else 0, float(attn_factor),
+                   table.data_ptr(), pos, pos_stride, *q.stride(), *_st4(k), *q_out.stride(), *_st4(k_out))
+    _launch(fn, stream, q, p, q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out))
+
+
+def sdpa_rope_fwd(q, k, q_out, k_out, table, positions=None, *, interleaved: bool = False,
+                  attn_factor: float = 1.0, stream=None) -> None:
+    """Rotary positions of Q and K ([b, h, s, d] views, f16/bf16) into q_out and k_out, which may be q
+    and k themselves; ``k`` and ``k_out`` may be None.
+
+    table: int64 CUDA tensor of :func:`sdpa_rope_table` (rot = twice its length; the elements of a head
+    behind rot are copied).  positions: int32 [b, s] or [s], or None: 0, 1, ... in every batch."""
+    _rope(lib.sdpa_rope_fwd, q, k, q_out, k_out, table, positions, interleaved, attn_factor, stream)
+
+
+def sdpa_rope_bwd(dq_out, dk_out, dq, dk, table, positions=None, *, interleaved: bool = False,
+                  attn_factor: float = 1.0, stream=None) -> None:
+    """Gradients of :func:`sdpa_rope_fwd`: dq, dk (overwritten) from the gradients of its outputs."""
+    _rope(lib.sdpa_rope_bwd, dq_out, dk_out, dq, dk, table, positions, interleaved, attn_factor, stream)
+
+
+def _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale):
+    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype,
+          "k_cache and v_cache must be [pages, h_kv, page_size, d] views of one shape and dtype")
+    pages, h_kv, page_size, d = k_cache.shape
+    _need(page_table.dim() == 2 and str(page_table.dtype) == "torch.int32"
+          and (page_table.shape[1] == 1 or page_table.stride(1) == 1),
+          "page_table must be int32 [b, max_pages] with a unit last stride")
+    b, wide = page_table.shape
+    _ints(seq_lens_kv, "seq_lens_kv", (b,))
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _ints(t, n, (pages, h_kv, page_size), "torch.float32")
+    _same_device(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
+    return _PACK_CACHE(pages, page_size, h_kv, d, _code(k_cache, "k_cache"), b, wide, k_cache.data_ptr(),
+                       v_cache.data_ptr(), *k_cache.stride(), *v_cache.stride(), _p0(k_scale), _p0(v_scale),
+                       page_table.data_ptr(), page_table.stride(0), seq_lens_kv.data_ptr())
+
+
+def _cache_rows(k, v, k_cache, page_table):
+    _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype,
+          "k and v must be [b, h_kv, s, d] views of one shape and dtype")
+    b, h, s, d = k.shape
+    _need(b == page_table.shape[0] and h == k_cache.shape[1] and d == k_cache.shape[3],
+          "k and v must have the cache's h_kv and d and a row of the page table for each sequence")
+    _same_device(k_cache, k, v)
+    return b, s
+
+
+def sdpa_cache_write(k, v, k_cache, v_cache, page_table, seq_lens_kv, *, seq_lens_q=None, k_scale=None,
+                     v_scale=None, rope_table=None, positions=None, interleaved: bool = False,
+                     attn_factor: float = 1.0, stream=None) -> None:
+    """Writes the new rows k, v ([b, h_kv, s, d], f16/bf16) into a paged cache.
+
+    k_cache, v_cache: [pages, h_kv, page_size, d] views (f16, bf16 or float8_e4m3fn; E4M3 needs k_scale and
+    v_scale, fp32 [pages, h_kv, page_size]).  page_table: int32 [b, max_pages]; seq_lens_kv: int32 [b] tokens
+    of each sequence with these; seq_lens_q: int32 [b] of them new (None: s).  Row i goes to position
+    len_kv - len_q + i.  With ``rope_table`` K is rotated first (positions None: each row's position)."""
+    c = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
+    b, s = _cache_rows(k, v, k_cache, page_table)
+    _ints(seq_lens_q, "seq_lens_q", (b,))
+    _same_device(k_cache, seq_lens_q, rope_table, positions)
+    rope, at = None, 0
+    if rope_table is not None:
+        _need(str(rope_table.dtype) == "torch.int64" and rope_table.dim() == 1 and rope_table.is_contiguous(),
+              "rope_table must be the int64 tensor of sdpa_rope_table")
+        pos, pos_stride = _positions(positions, b, s)
+        rope = ctypes.create_string_buffer(_PACK_ROPE(
+            0, 0, 0, 0, 0, 2 * rope_table.shape[0], 0, 1 if interleaved else 0, float(attn_factor),
+            rope_table.data_ptr(), pos, pos_stride, *(_NO_STRIDES * 4)))
+        at = ctypes.addressof(rope)
+    else:
+        _need(positions is None, "positions are those of a rope_table")
+    r = _PACK_ROWS(s, _code(k, "k"), *k.stride(), *v.stride(), _p0(seq_lens_q), at)
+    _launch(lib.sdpa_cache_write, stream, k_cache, c, r, k.data_ptr(), v.data_ptr())
+
+
+def sdpa_cache_read(k_cache, v_cache, page_table, seq_lens_kv, k, v, *, k_scale=None, v_scale=None,
+                    stream=None) -> None:
+    """Reads positions 0 .. s-1 of each sequence into dense k, v ([b, h_kv, s, d], f16/bf16); rows at
+    and behind its length are zeros.  Arguments as in :func:`sdpa_cache_write`."""
+    c = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
+    _, s = _cache_rows(k, v, k_cache, page_table)
+    r = _PACK_ROWS(s, _code(k, "k"), *k.stride(), *v.stride(), 0, 0)
+    _launch(lib.sdpa_cache_read, stream, k_cache, c, r, k.data_ptr(), v.data_ptr())
+
+
+def _decode(q, k_cache, page_table, o, seq_lens_q, attn_scale, causal, tree_mask):
+    _need(q.dim() == 4 and o.shape == q.shape and o.dtype == q.dtype, "q and o must be [b, h_q, s_q, d] views of one shape and dtype")
+    b, h_q, s_q, d = q.shape
+    _need(b == page_table.shape[0] and d == k_cache.shape[3], "q must have the cache's d and a row of the page table for each sequence")
+    _ints(seq_lens_q, "seq_lens_q", (b,))
+    stride = 0
+    if tree_mask is not None:
+        words = (s_q + 31) // 32
+        _need(str(tree_mask.dtype) in ("torch.int32", "torch.uint32") and tree_mask.dim() == 3
+              and tree_mask.shape[0] in (1, b) and tree_mask.shape[1:] == (s_q, words)
+              and tree_mask[0].is_contiguous() and tree_mask.stride(0) >= 0,
+              f"tree_mask must be int32 ({b} or 1, {s_q}, {words}), dense in its last two dimensions")
+        stride = tree_mask.stride(0) if tree_mask.shape[0] == b and b > 1 else 0
+    _same_device(k_cache, q, o, seq_lens_q, tree_mask)
+    scale = 1.0 / math.sqrt(d) if attn_scale is None else float(attn_scale)
+    return _PACK_DECODE(h_q, s_q, _code(q, "q"), causal_code(causal), scale, *q.stride(), *o.stride(),
+                        _p0(seq_lens_q), _p0(tree_mask), stride)
+
+
+def sdpa_decode_workspace_size(q, k_cache, v_cache, page_table, seq_lens_kv, *, k_scale=None, v_scale=None,
+                               tree_mask=None) -> int:
+    """Workspace bytes of :func:`sdpa_decode` for these sizes (whatever the lengths)."""
+    c = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
+    p = _decode(q, k_cache, page_table, q, None, 1.0, False, tree_mask)
+    n = ctypes.c_size_t(0)
+    import torch
+    with torch.cuda.device(q.device):
+        _check(lib.sdpa_decode_workspace_size(c, p, ctypes.byref(n)))
+    return n.value
+
+
+def sdpa_decode(q, k_cache, v_cache, page_table, seq_lens_kv, o, lse=None, *, workspace, seq_lens_q=None,
+                k_scale=None, v_scale=None, attn_scale: Optional[float] = None, causal=False, tree_mask=None,
+                stream=None) -> None:
+    """Attention of the newest tokens q ([b, h_q, s_q, d], already in the cache) over a paged cache: O, and
+    LSE when ``lse`` is given (fp32 [b, h_q, s_q] contiguous).
+
+    causal: False, or "bottom_right".  tree_mask: int32 [b or 1, s_q, ceil(s_q/32)], bit j%32 of word j/32 of
+    row i set where drafted token i sees drafted token j (itself among them); earlier positions are seen by
+    all.  seq_lens_q: rows that take part (None: all).  workspace: sdpa_decode_workspace_size bytes, not
+    shared with a call that may run at the same time."""
+    c = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
+    p = _decode(q, k_cache, page_table, o, seq_lens_q, attn_scale, causal, tree_mask)
+    if lse is not None:
+        _ints(lse, "lse", tuple(q.shape[:3]), "torch.float32")
+    _need(workspace is not None and workspace.is_contiguous(), "workspace must be a contiguous tensor")
+    _same_device(k_cache, lse, workspace)
+    _launch(lib.sdpa_decode, stream, k_cache, c, p, q.data_ptr(), o.data_ptr(), _ptr(lse), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())

@@ -313,6 +313,38 @@ float drop_scale_of(const sdpa_problem_t* p) {
 
 }  // namespace
 
+namespace sdpa {
+
+int api_fail(int st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(static_cast<sdpa_status_t>(st), "%s", buf);
+}
+
+int api_ok() { return ok(); }
+
+int api_finish(cudaError_t e, cudaStream_t stream, const char* what) { return finish_launch(e, stream, what); }
+
+int api_check_view(const char* name, const void* ptr, const int64_t (&st)[4], int b, int h, int s, int d, int es) {
+  return check_view(name, ptr, sdpa_strides_t{st[0], st[1], st[2], st[3]}, b, h, s, d, es);
+}
+
+int api_make_map(CUtensorMap* map, const char* name, const void* ptr, const int64_t (&st)[4], int b, int h, int s,
+                 int d, int dt, int box_rows) {
+  return make_map(map, name, ptr, sdpa_strides_t{st[0], st[1], st[2], st[3]}, b, h, s, d, dt, box_rows);
+}
+
+int api_num_sms() { return num_sms(); }
+
+int api_log_level() { return log_level(); }
+
+long long api_wait_limit() { return wait_limit_cycles(); }
+
+}  // namespace sdpa
+
 extern "C" {
 
 sdpa_status_t sdpa_workspace_size(const sdpa_problem_t* p, int is_backward, size_t* bytes) {

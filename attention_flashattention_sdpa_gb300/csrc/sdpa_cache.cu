@@ -1,0 +1,274 @@
+// sdpa_cache.cu — a paged key/value cache, written and read.
+//
+// Write: row i of a sequence's new rows goes to position len_kv - len_q + i, K rotated on the way
+// if asked.  E4M3: s = max(amax, 2^-60) / 448 for each token and head, code = x / s rounded to the
+// nearest of E4M3's values.  Read: code * s, dense, zeros behind the sequence.
+//
+// Bound: memory.  A row of d elements is spread over d / 16 lanes of 16 elements each, which find
+// the row's largest value by shuffles; a thread walks heads of one token, so that its angles and
+// its page are looked up once.
+#include <cuda_fp8.h>
+
+#include "sdpa_rope.cuh"
+
+namespace sdpa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kE4M3Max = 448.f;
+constexpr float kAmaxMin = 8.673617379884035e-19f;  // 2^-60
+
+__device__ __forceinline__ uint32_t pack4_e4m3(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return (lo & 0xFFFFu) | (hi << 16);
+}
+
+// Largest magnitude over the LANES lanes of a row.  As bits of non-negative fp32 values the
+// order of unsigned integers is that of the values, with infinity and then NaN above them all.
+template <int LANES>
+__device__ __forceinline__ float row_amax(const float (&x)[16]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = 1; o < LANES; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return __uint_as_float(m);
+}
+
+struct Slot {
+  int64_t page;   // -1: none
+  int slot;
+};
+
+__device__ __forceinline__ Slot find_slot(const CacheArgs& c, int bi, int pos) {
+  Slot r{-1, 0};
+  if (pos >= 0 && pos < c.max_len) {
+    const int col = pos / c.page_size;
+    const int page = __ldg(c.page_table + bi * c.page_table_stride + col);
+    if (page >= 0 && page < c.num_pages) r.page = page;
+    r.slot = pos - col * c.page_size;
+  }
+  return r;
+}
+
+__device__ __forceinline__ int clamp_len(const int32_t* lens, int i, int top) {
+  return lens ? min(max(__ldg(lens + i), 0), top) : top;
+}
+
+template <int DT>
+__device__ __forceinline__ void load_item(const void* base, int64_t row, int lo, int hi, float (&x)[16]) {
+  const uint16_t* p = static_cast<const uint16_t*>(base) + row;
+  uint4 u[2];
+  u[0] = *reinterpret_cast<const uint4*>(p + lo);
+  u[1] = *reinterpret_cast<const uint4*>(p + hi);
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = unpack16<DT>(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// Stores an item (16 values, runs at lo and hi) of one row; lane 0 of the row stores its scale.
+template <int D, int CT>
+__device__ __forceinline__ void store_item(uint8_t* row, float* scale_at, int m, int lo, int hi, const float (&x)[16],
+                                           bool live) {
+  if constexpr (CT == kE4M3) {
+    const float amax = row_amax<D / 16>(x);
+    const float scale = (amax < kAmaxMin ? kAmaxMin : amax) / kE4M3Max;   // a NaN stays one
+    const float inv = 1.f / scale;
+    if (!live) return;
+    uint2 a, b;
+    a.x = pack4_e4m3(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    a.y = pack4_e4m3(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+    b.x = pack4_e4m3(x[8] * inv, x[9] * inv, x[10] * inv, x[11] * inv);
+    b.y = pack4_e4m3(x[12] * inv, x[13] * inv, x[14] * inv, x[15] * inv);
+    if (hi == lo + 8) {
+      *reinterpret_cast<uint4*>(row + lo) = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+      *reinterpret_cast<uint2*>(row + lo) = a;
+      *reinterpret_cast<uint2*>(row + hi) = b;
+    }
+    if (m == 0) *scale_at = scale;
+  } else {
+    if (!live) return;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack16<CT>(x[2 * i], x[2 * i + 1]);
+    *reinterpret_cast<uint4*>(row + 2 * lo) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(row + 2 * hi) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// ROPE: 0 none, 1 rot a multiple of 16, 2 any even rot.
+template <int D, int DT, int CT, int ROPE>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheRowsParams p, int per) {
+  constexpr int LANES = D / 16;
+  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int m = static_cast<int>(idx % LANES);
+  const int64_t tokens = static_cast<int64_t>(p.c.b) * p.s;
+  const int64_t tok = (idx / LANES) % tokens;
+  const int grp = static_cast<int>(idx / LANES / tokens);
+  const int bi = static_cast<int>(tok / p.s), si = static_cast<int>(tok % p.s);
+  const int len_q = clamp_len(p.seq_lens_q, bi, p.s);
+  const int len_kv = clamp_len(p.c.seq_lens_kv, bi, p.c.max_len);
+  const int pos = len_kv - len_q + si;
+  Slot at{-1, 0};
+  if (grp * per < p.c.h_kv && si < len_q) at = find_slot(p.c, bi, pos);
+  const bool live = at.page >= 0;
+  // The lanes of a row leave together; a warp stays while any of its rows is live.
+  if (!__any_sync(0xffffffffu, live)) return;
+
+  RopeItem it{m * 16, m * 16 + 8, false};
+  int rpos = pos;
+  float c[8], s[8];
+  if constexpr (ROPE != 0) {
+    if (p.r.positions && live) rpos = p.r.positions[bi * p.r.positions_stride + si];
+  }
+  if constexpr (ROPE == 1) {
+    it = rope_item(p.r, m);
+    if (it.turned && live) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rope_angle(p.r, __ldg(p.r.table + m * 8 + i), rpos, c[i], s[i]);
+    }
+  }
+  const int h_end = min(p.c.h_kv, (grp + 1) * per);
+  // Every lane of the warp runs the same number of turns (the shuffles need them all).
+  for (int j = 0; j < per; ++j) {
+    const int h = grp * per + j;
+    const bool on = live && h < h_end;
+    float x[16], y[16];
+    if (on) {
+      const int64_t krow = bi * p.k_st[0] + h * p.k_st[1] + si * p.k_st[2];
+      load_item<DT>(p.k, krow, it.lo, it.hi, x);
+      load_item<DT>(p.v, bi * p.v_st[0] + h * p.v_st[1] + si * p.v_st[2], m * 16, m * 16 + 8, y);
+      if constexpr (ROPE == 1) {
+        if (it.turned) {
+          if (p.r.interleaved) rope_turn(true, x, c, s);
+          else rope_turn(false, x, c, s);
+        }
+      }
+      if constexpr (ROPE == 2) {
+        // 16 neighbours; each finds its own partner and angle.
+        const int half = p.r.rot / 2;
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+          const int e = m * 16 + i;
+          if (e >= p.r.rot) break;
+          const int pair = p.r.interleaved ? e / 2 : e % half;
+          const bool first = p.r.interleaved ? e % 2 == 0 : e < half;
+          const int other = p.r.interleaved ? e ^ 1 : (first ? e + half : e - half);
+          float cc, ss;
+          rope_angle(p.r, __ldg(p.r.table + pair), rpos, cc, ss);
+          const float a = load16<DT>(p.k, krow + e), b = load16<DT>(p.k, krow + other);
+          x[i] = first ? a * cc - b * ss : b * ss + a * cc;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = y[i] = 0.f;
+    }
+    const int64_t sc = (at.page * p.c.h_kv + h) * p.c.page_size + at.slot;
+    store_item<D, CT>(p.c.k + at.page * p.c.k_st[0] + h * p.c.k_st[1] + at.slot * p.c.k_st[2], p.c.k_scale + sc, m,
+                      it.lo, it.hi, x, on);
+    store_item<D, CT>(p.c.v + at.page * p.c.v_st[0] + h * p.c.v_st[1] + at.slot * p.c.v_st[2], p.c.v_scale + sc, m,
+                      m * 16, m * 16 + 8, y, on);
+  }
+}
+
+// One thread: 16 elements of K and of V of one row.
+template <int D, int DT, int CT>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheRowsParams p) {
+  constexpr int LANES = D / 16;
+  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int m = static_cast<int>(idx % LANES);
+  const int64_t row = idx / LANES;
+  const int h = static_cast<int>(row % p.c.h_kv);
+  const int64_t tok = row / p.c.h_kv;
+  if (tok >= static_cast<int64_t>(p.c.b) * p.s) return;
+  const int bi = static_cast<int>(tok / p.s), si = static_cast<int>(tok % p.s);
+  Slot at{-1, 0};
+  if (si < clamp_len(p.c.seq_lens_kv, bi, p.c.max_len)) at = find_slot(p.c, bi, si);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (at.page >= 0) {
+      const int64_t* st = t ? p.c.v_st : p.c.k_st;
+      const uint8_t* src = (t ? p.c.v : p.c.k) + at.page * st[0] + h * st[1] + at.slot * st[2];
+      if constexpr (CT == kE4M3) {
+        const float scale = __ldg((t ? p.c.v_scale : p.c.k_scale) + (at.page * p.c.h_kv + h) * p.c.page_size + at.slot);
+        const uint4 in = __ldg(reinterpret_cast<const uint4*>(src + m * 16));
+        const uint32_t iw[4] = {in.x, in.y, in.z, in.w};
+        uint32_t* ow = reinterpret_cast<uint32_t*>(out);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(iw[i / 2] >> (16 * (i % 2))), __NV_E4M3);
+          const float2 f = __half22float2(__half2(hr));
+          ow[i] = pack16<DT>(f.x * scale, f.y * scale);
+        }
+      } else {
+        out[0] = __ldg(reinterpret_cast<const uint4*>(src + m * 32));
+        out[1] = __ldg(reinterpret_cast<const uint4*>(src + m * 32 + 16));
+      }
+    }
+    const int64_t* st = t ? p.v_st : p.k_st;
+    uint16_t* dst = static_cast<uint16_t*>(t ? p.v : p.k) + bi * st[0] + h * st[1] + si * st[2] + m * 16;
+    reinterpret_cast<uint4*>(dst)[0] = out[0];
+    reinterpret_cast<uint4*>(dst)[1] = out[1];
+  }
+}
+
+template <int D, int DT, int CT>
+cudaError_t write_t(const CacheRowsParams& p, int num_sms, cudaStream_t st) {
+  const int64_t tokens = static_cast<int64_t>(p.c.b) * p.s;
+  int per = 8;   // heads a thread walks: as many as leave the GPU full
+  while (per > 1 && tokens * (D / 16) * ((p.c.h_kv + per - 1) / per) < static_cast<int64_t>(num_sms) * 1024) per /= 2;
+  const int groups = (p.c.h_kv + per - 1) / per;
+  const int64_t blocks = (tokens * (D / 16) * groups + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (!p.rope) cache_write_kernel<D, DT, CT, 0><<<grid, kThreads, 0, st>>>(p, per);
+  else if (p.r.rot % 16 == 0) cache_write_kernel<D, DT, CT, 1><<<grid, kThreads, 0, st>>>(p, per);
+  else cache_write_kernel<D, DT, CT, 2><<<grid, kThreads, 0, st>>>(p, per);
+  return cudaGetLastError();
+}
+
+template <int D, int DT, int CT>
+cudaError_t read_t(const CacheRowsParams& p, cudaStream_t st) {
+  const int64_t blocks = (static_cast<int64_t>(p.c.b) * p.s * p.c.h_kv * (D / 16) + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cache_read_kernel<D, DT, CT><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t write_d(const CacheRowsParams& p, int dt, int ct, int sms, cudaStream_t st) {
+  if (dt == kBF16) return ct == kE4M3 ? write_t<D, kBF16, kE4M3>(p, sms, st) : write_t<D, kBF16, kBF16>(p, sms, st);
+  return ct == kE4M3 ? write_t<D, kF16, kE4M3>(p, sms, st) : write_t<D, kF16, kF16>(p, sms, st);
+}
+
+template <int D>
+cudaError_t read_d(const CacheRowsParams& p, int dt, int ct, cudaStream_t st) {
+  if (dt == kBF16) return ct == kE4M3 ? read_t<D, kBF16, kE4M3>(p, st) : read_t<D, kBF16, kBF16>(p, st);
+  return ct == kE4M3 ? read_t<D, kF16, kE4M3>(p, st) : read_t<D, kF16, kF16>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheRowsParams& p, int dt, int ct, int num_sms, cudaStream_t st) {
+  if (p.d == 64) return write_d<64>(p, dt, ct, num_sms, st);
+  if (p.d == 128) return write_d<128>(p, dt, ct, num_sms, st);
+  if (p.d == 256) return write_d<256>(p, dt, ct, num_sms, st);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_cache_read(const CacheRowsParams& p, int dt, int ct, cudaStream_t st) {
+  if (p.d == 64) return read_d<64>(p, dt, ct, st);
+  if (p.d == 128) return read_d<128>(p, dt, ct, st);
+  if (p.d == 256) return read_d<256>(p, dt, ct, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace sdpa

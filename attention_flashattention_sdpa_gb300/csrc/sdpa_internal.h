@@ -184,6 +184,103 @@ constexpr int kFeatDBias = 8;   // only with kFeatBias
 constexpr int kFeatOneTile = 16;  // forward: one Q tile per work unit at d <= 128
 constexpr int kFeatPersist = 32;  // forward: persistent CTAs, each walking several work units
 
+// ---- shared by the C-ABI files -----------------------------------------------------------
+
+// Records a message for sdpa_last_error_string and returns `st`.
+int api_fail(int st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int api_ok();
+// Status of a launch: its CUDA error, and under SDPA_DEBUG_SYNC the kernels' own.
+int api_finish(cudaError_t e, cudaStream_t stream, const char* what);
+// Checks that a logical [b][h][s][d] view is 16-byte aligned with positive strides.
+int api_check_view(const char* name, const void* ptr, const int64_t (&st)[4], int b, int h, int s, int d, int es);
+// Tensor map of such a view: 128 bytes of d x box_rows rows, 128-byte swizzle.
+int api_make_map(CUtensorMap* map, const char* name, const void* ptr, const int64_t (&st)[4], int b, int h, int s,
+                 int d, int dt, int box_rows);
+int api_num_sms();
+int api_log_level();
+long long api_wait_limit();
+
+// ---- rotary positions ----------------------------------------------------------------------
+
+// What one row's rotation needs (in sdpa_rope_fwd/bwd and inside sdpa_cache_write).
+struct RopeArgs {
+  const int64_t* table;       // turns per position of each pair, 64-bit binary fractions
+  const int32_t* positions;   // or nullptr
+  int64_t positions_stride;
+  int rot;
+  int interleaved;
+  int sign;                   // +1 forward, -1 backward (the transposed rotation)
+  float factor;
+};
+
+struct RopeParams {
+  RopeArgs r;
+  const void* in[2];          // Q, K
+  void* out[2];
+  int64_t in_st[2][3];        // element strides b, h, s
+  int64_t out_st[2][3];
+  int in_place[2];            // nothing to do for the elements behind rot
+  int b, s, d, h_q, h_all;    // h_all = h_q + h_k
+};
+
+cudaError_t launch_rope(const RopeParams& p, int dtype, int num_sms, cudaStream_t st);
+
+// ---- paged cache ---------------------------------------------------------------------------
+
+struct CacheArgs {
+  uint8_t* k;
+  uint8_t* v;
+  int64_t k_st[3], v_st[3];    // BYTE strides of page, head, slot
+  float* k_scale;              // [num_pages][h_kv][page_size]
+  float* v_scale;
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  const int32_t* seq_lens_kv;
+  int num_pages, page_size, h_kv, b, max_pages;
+  int max_len;                 // min(max_pages * page_size, 2^31 - 1)
+};
+
+struct CacheRowsParams {
+  CacheArgs c;
+  RopeArgs r;                  // write with rotated K only
+  int rope;
+  void* k;                     // dense rows (read from for a write, written for a read)
+  void* v;
+  int64_t k_st[3], v_st[3];    // element strides b, h, s
+  const int32_t* seq_lens_q;
+  int s, d;
+};
+
+cudaError_t launch_cache_write(const CacheRowsParams& p, int row_dtype, int cache_dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheRowsParams& p, int row_dtype, int cache_dtype, cudaStream_t st);
+
+// ---- attention over the cache --------------------------------------------------------------
+
+struct DecodeParams {
+  CacheArgs c;
+  const void* q;
+  void* o;
+  float* lse;
+  int64_t q_st[3], o_st[3];    // element strides b, h, s
+  const int32_t* seq_lens_q;
+  const uint32_t* tree_mask;
+  int64_t tree_mask_stride;
+  int tree_words;              // 32-bit words of one row of the mask
+  int causal;
+  int h_q, s_q, group;
+  int rows;                    // s_q * group: query rows that share a KV head
+  int row_tiles;               // ceil(rows / rows of a tile)
+  float scale_log2;            // attn_scale * log2(e)
+  float* part_o;               // workspace: [2 * ctas][tile rows][d] unnormalised partial O
+  float* part_ml;              // workspace: [2 * ctas][tile rows][2] their max (log2 units) and sum
+  int ctas;
+};
+
+// CTAs of a launch over `b` sequences (from the sizes alone, so that workspace and launch agree).
+int decode_ctas(const DecodeParams& p, int num_sms);
+size_t decode_workspace_bytes(const DecodeParams& p, int d, int num_sms, size_t* ml_offset);
+cudaError_t launch_decode(const DecodeParams& p, int d, int q_dtype, int cache_dtype, cudaStream_t st);
+
 }  // namespace sdpa
 
 namespace sdpa {

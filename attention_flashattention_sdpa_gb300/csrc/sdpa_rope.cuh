@@ -1,0 +1,80 @@
+// sdpa_rope.cuh — rotary positions: the angle of a pair, and 16-bit packing, shared by the
+// rotation kernels and the cache write.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sdpa_internal.h"
+
+namespace sdpa {
+
+// cos and sin (times the factor) of pair i at position `pos`.  The table holds the turns per
+// position as 64-bit binary fractions, so pos * table[i] modulo 2^64 is the angle's exact
+// fraction of a turn: no range reduction, and no loss however far the position.  The top 32
+// bits, read as signed, are the angle in half turns over 2^31; as fp32 that is off by 2^-24 of
+// itself, less than the rounding of the outputs by 2^12 and more.
+__device__ __forceinline__ void rope_angle(const RopeArgs& r, int64_t turns, int pos, float& c, float& s) {
+  const uint64_t phase = static_cast<uint64_t>(turns) * static_cast<uint64_t>(static_cast<int64_t>(pos));
+  const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
+  sincospif(half_turns, &s, &c);
+  c *= r.factor;
+  s *= r.sign < 0 ? -r.factor : r.factor;
+}
+
+template <int DT>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+  if (DT == kBF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if (DT == kBF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int DT>
+__device__ __forceinline__ float load16(const void* p, int64_t i) {
+  const uint16_t w = static_cast<const uint16_t*>(p)[i];
+  if (DT == kBF16) return __uint_as_float(static_cast<uint32_t>(w) << 16);
+  return __half2float(*reinterpret_cast<const __half*>(&w));
+}
+
+template <int DT>
+__device__ __forceinline__ void store16(void* p, int64_t i, float x) {
+  static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(pack16<DT>(x, 0.f) & 0xFFFFu);
+}
+
+// A work item of 16 elements of a head, as two runs of 8: the two halves of 8 pairs (half
+// layout, inside the rotated part), or 16 neighbours.  rot and d are multiples of 16.
+struct RopeItem {
+  int lo, hi;      // first element of each run
+  bool turned;
+};
+
+__device__ __forceinline__ RopeItem rope_item(const RopeArgs& r, int m) {
+  RopeItem it;
+  it.turned = m * 16 < r.rot;
+  const bool halves = it.turned && !r.interleaved;
+  it.lo = halves ? m * 8 : m * 16;
+  it.hi = halves ? r.rot / 2 + m * 8 : m * 16 + 8;
+  return it;
+}
+
+// Rotates 16 values of an item (x[0..8) at lo, x[8..16) at hi) by its 8 angles.
+__device__ __forceinline__ void rope_turn(bool interleaved, float (&x)[16], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int ia = interleaved ? 2 * i : i, ib = interleaved ? 2 * i + 1 : i + 8;
+    const float a = x[ia], b = x[ib];
+    x[ia] = a * c[i] - b * s[i];
+    x[ib] = a * s[i] + b * c[i];
+  }
+}
+
+}  // namespace sdpa

@@ -252,6 +252,151 @@ SDPA_API sdpa_status_t sdpa_dropout_mask_size(const sdpa_problem_t* p, size_t* b
 SDPA_API sdpa_status_t sdpa_dropout_mask(const sdpa_problem_t* p, uint64_t seed, uint64_t offset,
                                          uint32_t* mask, uint32_t* mask_t, void* stream /* cudaStream_t */);
 
+/* ------------------------------------------------------------------------------------------
+ * Serving: rotary positions, a paged key/value cache, attention of new tokens over it.
+ *
+ * The conventions above hold for these entry points too: device pointers, logical
+ * [b][h][s][d] views with a unit d stride, 16-byte aligned bases and strides, caller-owned
+ * memory, asynchronous execution, validation on the host before any launch.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Frequencies of the rotary positions (Su et al., "RoFormer", 2021): pair i of rot/2 turns by
+ * f_i = base^(-2 i / rot) radians per position.  Scaled for contexts longer than the one a
+ * model was trained on (original_context), by `factor` >= 1:
+ *   0  none
+ *   1  linear: every f_i / factor (position interpolation, Chen et al., 2023)
+ *   2  NTK-aware: base * factor^(rot / (rot - 2)) instead of base
+ *   3  by parts (YaRN, Peng et al., 2023): with r_i = original_context * f_i / (2 pi), the turns
+ *      pair i makes over the original context, and g = clamp((r_i - beta_slow) /
+ *      (beta_fast - beta_slow), 0, 1): f_i * g + f_i / factor * (1 - g); the factor on the
+ *      rotated values is 0.1 ln(factor) + 1. */
+typedef struct {
+  int32_t rot;              /* rotated elements of a head: even, >= 2 */
+  int32_t scaling;          /* 0..3 as above */
+  double base;              /* > 0, usually 10000 */
+  double factor;            /* scalings 1..3: >= 1 */
+  double original_context;  /* scaling 3: > 0, tokens */
+  double beta_fast, beta_slow;  /* scaling 3: beta_fast > beta_slow, usually 32 and 1 */
+  const double* inv_freq;   /* NULL, or HOST pointer to rot/2 frequencies (radians per position)
+                               that replace all of the above; the factor is then 1 */
+} sdpa_rope_table_t;
+
+/* Fills table[0 .. rot/2) (HOST memory; the caller copies it to the device) with the turns per
+ * position of each pair as 64-bit binary fractions, table[i] = f_i / (2 pi) * 2^64 mod 2^64, and
+ * *attn_factor (may be NULL) with the factor on the rotated values.  A position times such a
+ * fraction, modulo 2^64, is the angle as an exact fraction of a turn however far the position. */
+SDPA_API sdpa_status_t sdpa_rope_table(const sdpa_rope_table_t* cfg, int64_t* table, float* attn_factor);
+
+/* Rotary positions of Q and K in one call. */
+typedef struct {
+  int32_t b, h_q, h_k;      /* h_k = 0: Q alone */
+  int32_t s;                /* rows (tokens) of each batch */
+  int32_t d;                /* head dim: a multiple of 8, 8..512 */
+  int32_t rot;              /* rotated elements, even, 2..d: the first `rot` of each head; the others
+                               are copied */
+  int32_t dtype;            /* F16 or BF16 */
+  int32_t interleaved;      /* pairs: 0 = elements (i, i + rot/2), 1 = elements (2i, 2i + 1) */
+  float attn_factor;        /* multiplies the rotated elements (1 = none) */
+  const int64_t* table;     /* DEVICE, rot/2 entries of sdpa_rope_table */
+  const int32_t* positions; /* DEVICE [b][s], or NULL: row i of every batch is at position i */
+  int64_t positions_stride; /* elements between two batches of positions (0: one row for all) */
+  sdpa_strides_t q, k;           /* inputs */
+  sdpa_strides_t q_out, k_out;   /* outputs */
+} sdpa_rope_t;
+
+/* y = factor * R(position) x for Q and K: pair (a, b) at angle t becomes
+ * (a cos t - b sin t, a sin t + b cos t), computed in fp32 and rounded once.
+ *   q_out may be q (with the same strides) and k_out may be k; otherwise outputs overlap no input. */
+SDPA_API sdpa_status_t sdpa_rope_fwd(const sdpa_rope_t* p, const void* q, const void* k, void* q_out,
+                                     void* k_out, void* stream);
+
+/* The gradient of sdpa_rope_fwd: dx = factor * R(position)^T dy.  dq_out/dk_out (the incoming
+ * gradients) have the views p->q/p->k, dq/dk the views p->q_out/p->k_out. */
+SDPA_API sdpa_status_t sdpa_rope_bwd(const sdpa_rope_t* p, const void* dq_out, const void* dk_out, void* dq,
+                                     void* dk, void* stream);
+
+/* A paged key/value cache.  Position j of sequence i lives in page page_table[i][j / page_size],
+ * slot j % page_size.  Keys and values are logical [num_pages][h_kv][page_size][d] views (the
+ * fields b, h, s, d of the strides are page, head, slot, element), so a page may be stored
+ * head-major or slot-major.  E4M3 caches have an fp32 scale for each token and head:
+ * value = code * scale. */
+typedef struct {
+  int32_t num_pages;        /* >= 1 */
+  int32_t page_size;        /* tokens of a page: a multiple of 16 */
+  int32_t h_kv;             /* >= 1 */
+  int32_t d;                /* 64, 128 or 256 */
+  int32_t dtype;            /* F16, BF16 or E4M3 */
+  int32_t b;                /* sequences */
+  int32_t max_pages;        /* columns of the page table */
+  void* k;
+  void* v;
+  sdpa_strides_t k_strides, v_strides;
+  float* k_scale;           /* E4M3: DEVICE [num_pages][h_kv][page_size] dense, 16-byte aligned; else NULL */
+  float* v_scale;
+  const int32_t* page_table;   /* DEVICE [b][max_pages]; columns a sequence does not reach are not read.
+                                  Positions whose page is outside [0, num_pages) hold no key: they are
+                                  not written, read back as zeros and hidden from every query */
+  int64_t page_table_stride;   /* elements between two sequences */
+  const int32_t* seq_lens_kv;  /* DEVICE [b]: tokens of each sequence, those of this call included
+                                  (clamped to [0, max_pages * page_size], and to 2^30) */
+} sdpa_cache_t;
+
+/* New rows for the cache (sdpa_cache_write), or dense rows read from it (sdpa_cache_read). */
+typedef struct {
+  int32_t s;                   /* rows of each sequence */
+  int32_t dtype;               /* F16 or BF16; the cache's own dtype unless that is E4M3 */
+  sdpa_strides_t k, v;         /* [b][h_kv][s][d] */
+  const int32_t* seq_lens_q;   /* write: DEVICE [b] new rows of each sequence (clamped to [0, s]), or NULL: s */
+  const sdpa_rope_t* rope;     /* write: NULL, or K is rotated first: rot, interleaved, attn_factor, table,
+                                  positions and positions_stride are read (positions NULL: each row's
+                                  position in its sequence) */
+} sdpa_cache_rows_t;
+
+/* Writes row i < len_q of each sequence to position len_kv - len_q + i (rows before position 0
+ * are not written).  16-bit caches take the (rotated) values rounded once; E4M3 caches take
+ * scale = max(amax, 2^-60) / 448 over the d elements of each row, and code = x * (1 / scale)
+ * rounded to the nearest E4M3 value (K: rotated in fp32, with no rounding in between).  A row that
+ * holds an infinity or a NaN reads back as NaN.  Two rows of one call must not map to the same
+ * slot.  Other slots are left as they are. */
+SDPA_API sdpa_status_t sdpa_cache_write(const sdpa_cache_t* c, const sdpa_cache_rows_t* r, const void* k,
+                                        const void* v, void* stream);
+
+/* Reads positions 0 .. s-1 of each sequence into dense rows, code * scale rounded once; rows at
+ * len_kv and behind are zeros (as sdpa_fwd with seq_lens_kv wants its padding). */
+SDPA_API sdpa_status_t sdpa_cache_read(const sdpa_cache_t* c, const sdpa_cache_rows_t* r, void* k, void* v,
+                                       void* stream);
+
+/* Attention of the newest tokens over the cache. */
+typedef struct {
+  int32_t h_q;                 /* h_q % h_kv == 0 */
+  int32_t s_q;                 /* rows (new tokens) of each sequence, >= 1 */
+  int32_t dtype;               /* F16 or BF16, of Q and O; the cache's own dtype unless that is E4M3 */
+  int32_t causal;              /* 0: every row sees the whole sequence.  2: bottom-right causal, row i sees
+                                  keys j <= i + len_kv - len_q */
+  float attn_scale;
+  sdpa_strides_t q, o;         /* [b][h_q][s_q][d] */
+  const int32_t* seq_lens_q;   /* DEVICE [b] rows that take part (clamped to [0, s_q]), or NULL: s_q */
+  const uint32_t* tree_mask;   /* NULL, or DEVICE [b][s_q][ceil(s_q/32)]: the rows are drafted tokens, already
+                                  in the cache as its last len_q positions; row i sees every earlier
+                                  position, and of the drafted ones those j with bit j%32 of word j/32
+                                  set.  causal must be 0 */
+  int64_t tree_mask_stride;    /* 32-bit words between two sequences' masks (0: one tree for all) */
+} sdpa_decode_t;
+
+/* Workspace bytes of sdpa_decode (a function of the sizes alone, not of the lengths). */
+SDPA_API sdpa_status_t sdpa_decode_workspace_size(const sdpa_cache_t* c, const sdpa_decode_t* p, size_t* bytes);
+
+/* O (and LSE when lse != NULL: fp32 [b][h_q][s_q] dense, natural log) of the new tokens over the
+ * cache.  Rows with no visible key, and rows >= len_q, give O = 0 and LSE = -inf.  Values at
+ * hidden positions may hold anything, NaN included.
+ *   workspace: >= sdpa_decode_workspace_size bytes, 256-byte aligned; contents on entry do not matter. */
+SDPA_API sdpa_status_t sdpa_decode(const sdpa_cache_t* c, const sdpa_decode_t* p, const void* q, void* o,
+                                   float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* sizeof of the structs above as compiled into the library: which = 0 sdpa_rope_table_t,
+ * 1 sdpa_rope_t, 2 sdpa_cache_t, 3 sdpa_cache_rows_t, 4 sdpa_decode_t (0 for any other). */
+SDPA_API size_t sdpa_serving_struct_size(int which);
+
 /* Message for the last non-OK status returned on the calling thread ("" if none).  The
  * pointer stays valid until the next library call on this thread [cuDNN 9 blog: errors
  * come with a retrievable last-error string]. */
