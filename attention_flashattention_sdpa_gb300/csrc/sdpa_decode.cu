@@ -580,46 +580,84 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
 }
 
 // Joins the partial results of every block of rows that more than one CTA worked on, and writes
-// the rows that no key reaches.  One CTA a block of rows.
+// the rows that no key reaches.  One CTA a row: its lanes weigh the parts side by side (a part is
+// a maximum, a sum and d values), then each warp adds up every fourth part, 8 loads in flight,
+// and the four sums meet.  The order is that of the parts, so results do not change between calls.
 template <int D, int QT>
-__global__ void __launch_bounds__(128) decode_combine_kernel(const __grid_constant__ DecodeParams p, float p_off) {
-  const int lane = threadIdx.x % 32;
+__global__ void __launch_bounds__(kThreads) decode_combine_kernel(const __grid_constant__ DecodeParams p, float p_off) {
+  constexpr int EL = D / 32;          // elements a lane owns
+  __shared__ float s_sum[kWarps][D];
+  __shared__ float s_l[kWarps];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rows_blk = min(p.rows, kRows);
   const int per_seq = p.c.h_kv * p.row_tiles;
-  const int bi = blockIdx.x / per_seq, blk = blockIdx.x % per_seq;
-  const int hk = blk / p.row_tiles, r0 = (blk % p.row_tiles) * kRows;
+  const int unit = blockIdx.x / rows_blk, r = blockIdx.x % rows_blk;
+  const int bi = unit / per_seq, blk = unit % per_seq;
+  const int hk = blk / p.row_tiles, row = blk % p.row_tiles * kRows + r, token = row / p.group;
   const int n_tiles = seq_tiles(p, bi);
   const SeqLens L = seq_lens(p, bi);
-  int c0 = 0, c1 = -1;     // (no tiles: c1 < c0, the rows below come out empty)
+  int c0 = 0, n = 0;                  // parts: CTAs c0 .. c0 + n - 1 (none where there are no tiles)
   if (n_tiles > 0) {
     const long long total = tiles_before(p, p.c.b, lane) * per_seq;
     const long long t0 = tiles_before(p, bi, lane) * per_seq + static_cast<long long>(blk) * n_tiles;
     c0 = cta_of(total, t0, working_ctas(p, total));
-    c1 = cta_of(total, t0 + n_tiles - 1, working_ctas(p, total));
+    n = cta_of(total, t0 + n_tiles - 1, working_ctas(p, total)) - c0 + 1;
   }
   griddep_wait();   // (by every CTA, so that this grid never ends before the one it follows)
-  if (c0 == c1) return;       // finished by that CTA
-  for (int idx = threadIdx.x; idx < kRows * D; idx += 128) {
-    const int r = idx / D, d = idx % D, row = r0 + r, token = row / p.group;
-    if (row >= p.rows) break;
-    float m = -INFINITY, l = 0.f, x = 0.f;
-    for (int k = c0; k <= c1; ++k) {
-      const int part = 2 * k + (k == c0 ? 1 : 0);
-      m = fmaxf(m, p.part_ml[(part * kRows + r) * 2]);
-    }
-    for (int k = c0; k <= c1; ++k) {
-      const int part = 2 * k + (k == c0 ? 1 : 0);
-      const float pm = p.part_ml[(part * kRows + r) * 2], pl = p.part_ml[(part * kRows + r) * 2 + 1];
-      if (pl == 0.f) continue;
-      const float f = pm == -INFINITY ? 1.f : ex2(pm - m);
-      l += pl * f;
-      x += p.part_o[(static_cast<int64_t>(part) * kRows + r) * D + d] * f;
-    }
-    const bool none = token >= L.len_q || l == 0.f;
-    store_o<QT>(p.o, row_offset(p, p.o_st, bi, hk, row) + d, none ? 0.f : x / l);
-    if (p.lse && d == 0)
-      p.lse[(static_cast<int64_t>(bi) * p.h_q + hk * p.group + row % p.group) * p.s_q + token] =
-          none ? -INFINITY : (m - p_off + __log2f(l)) * 0.6931471805599453f;
+  if (n == 1 || row >= p.rows) return;       // finished by that CTA
+  // Part k: the first holds its block's first tile and is that CTA's second part.
+  auto part = [&](int k) { return static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)) * kRows + r; };
+  float m = -INFINITY;
+  for (int k = lane; k < n; k += 32) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * part(k));
+    if (ml.y != 0.f) m = fmaxf(m, ml.x);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float x[EL], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < EL; ++e) x[e] = 0.f;
+  for (int k0 = warp; k0 < n; k0 += 8 * kWarps) {
+    float f[8], v[8][EL];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int k = k0 + u * kWarps;
+      f[u] = 0.f;
+#pragma unroll
+      for (int e = 0; e < EL; ++e) v[u][e] = 0.f;
+      if (k < n) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * part(k));
+        const float* src = p.part_o + part(k) * D + lane * EL;
+#pragma unroll
+        for (int e = 0; e < EL; e += 2) {
+          const float2 w = *reinterpret_cast<const float2*>(src + e);
+          v[u][e] = w.x;
+          v[u][e + 1] = w.y;
+        }
+        // A part without a visible key has sum 0 and weighs nothing.  (All sums NaN: m stays -inf.)
+        if (ml.y != 0.f) {
+          f[u] = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
+          l += ml.y * f[u];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int e = 0; e < EL; ++e) x[e] += f[u] == 0.f ? 0.f : v[u][e] * f[u];
+  }
+#pragma unroll
+  for (int e = 0; e < EL; ++e) s_sum[warp][lane * EL + e] = x[e];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  const bool none = token >= L.len_q || l == 0.f;
+  const int64_t at = row_offset(p, p.o_st, bi, hk, row);
+  for (int d = threadIdx.x; d < D; d += kThreads)
+    store_o<QT>(p.o, at + d, none ? 0.f : ((s_sum[0][d] + s_sum[1][d]) + (s_sum[2][d] + s_sum[3][d])) / l);
+  if (p.lse && threadIdx.x == 0)
+    p.lse[(static_cast<int64_t>(bi) * p.h_q + hk * p.group + row % p.group) * p.s_q + token] =
+        none ? -INFINITY : (m - p_off + __log2f(l)) * 0.6931471805599453f;
 }
 
 template <int D, int CT, int QT>
@@ -632,8 +670,8 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles * (p.rows < kRows ? p.rows : kRows));
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

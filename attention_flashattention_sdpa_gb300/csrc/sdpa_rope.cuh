@@ -9,15 +9,20 @@
 
 namespace sdpa {
 
-// cos and sin (times the factor) of pair i at position `pos`.  The table holds the turns per
-// position as 64-bit binary fractions, so pos * table[i] modulo 2^64 is the angle's exact
-// fraction of a turn: no range reduction, and no loss however far the position.  The top 32
-// bits, read as signed, are the angle in half turns over 2^31; as fp32 that is off by 2^-24 of
-// itself, less than the rounding of the outputs by 2^12 and more.
+// cos and sin (times the factor) of one pair at position `pos`.  The table holds the turns per
+// position as 64-bit binary fractions, so pos * table[i] modulo 2^64 is the angle's exact fraction
+// of a turn: no loss however far the position.  The nearest quarter turn is taken off in whole
+// numbers as well; the rest, at most an eighth of a turn, loses 2^-25 of itself as fp32.
 __device__ __forceinline__ void rope_angle(const RopeArgs& r, int64_t turns, int pos, float& c, float& s) {
   const uint64_t phase = static_cast<uint64_t>(turns) * static_cast<uint64_t>(static_cast<int64_t>(pos));
-  const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
-  sincospif(half_turns, &s, &c);
+  const uint32_t top = static_cast<uint32_t>(phase >> 32);
+  const uint32_t quarter = (top + (1u << 29)) >> 30;                   // 0..4
+  const int32_t rest = static_cast<int32_t>(top - (quarter << 30));    // [-2^29, 2^29) of 2^32 a turn
+  float sr, cr;
+  sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &sr, &cr);   // half turns: 2^-31
+  const float sw = quarter & 1 ? cr : sr, cw = quarter & 1 ? sr : cr;
+  c = (quarter + 1) & 2 ? -cw : cw;
+  s = quarter & 2 ? -sw : sw;
   c *= r.factor;
   s *= r.sign < 0 ? -r.factor : r.factor;
 }
