@@ -2,22 +2,26 @@
 //
 // The s_q tokens of a sequence times the query heads of a KV head's group are `rows` query rows
 // that share the cache of that KV head.  Work is counted in tiles of 64 keys of one (sequence, KV
-// head, block of 16 rows); every CTA takes an equal run of consecutive tiles over the whole batch,
-// so that ragged lengths balance by themselves, and a run may end one sequence and begin the
-// next.  A block that lies in one CTA's run is finished there; the others leave unnormalised
-// partial results (O, running max, sum) that decode_combine_kernel joins, in a fixed order.
+// head, block of rows); every CTA takes an equal run of consecutive tiles over the whole batch, so
+// that ragged lengths balance by themselves, and a run may end one sequence and begin the next.
+// A block that lies in one CTA's run is finished there; the others leave unnormalised partial
+// results (O, running max, sum) that decode_combine_kernel joins, in a fixed order.
 //
-// Bound: reading the cache once.  With 16 rows a key costs 2 x 16 x d multiply-adds for 2 d
-// elements read, far below what the tensor cores do in the time of the read; so the products are
-// warp-level m16n8k16 MMAs on registers (a 128-row tcgen05 tile would be 7/8 empty and put its P
-// through shared memory), and what counts is bytes in flight: each warp streams its own 16-key
-// slices through a ring of cp.async stages and needs no other warp until the end of a run.
+// Bound: reading the cache once.  With 8 rows a key costs 2 x 8 x d multiply-adds for 2 d elements
+// read, far below what the tensor cores do in the time of the read; so the products are warp-level
+// m16n8k16 MMAs on registers (a 128-row tcgen05 tile would be 15/16 empty and put its P through
+// shared memory), and what counts is bytes in flight and few instructions a key: each warp streams
+// its own 16-key slices through a ring of cp.async stages and needs no other warp until the end of
+// a run.
 //
-// Both products read the ring with 16-byte loads and no transposition:
-//   S = Q K^T sums over d in any order, so a lane takes 16 contiguous bytes of its key and Q's
+// Keys, and then elements of d, are the 16 rows of the MMAs, and query rows their 8 columns:
+//   S^T = K Q^T sums over d in any order, so a lane takes 16 contiguous bytes of its key and Q's
 //   fragments are permuted to match;
-//   O = P V wants pairs of keys in one register: a lane loads the same 16 bytes of two
-//   neighbouring keys and interleaves them with byte permutes.
+//   O^T = V^T P^T wants pairs of keys in one register: a lane loads the same 16 bytes of two
+//   neighbouring keys and interleaves them with byte permutes.  P^T turns from one product's
+//   result layout to the other's operand layout by an 8x8 transposition (movmatrix).
+// (Query rows as the 16 rows instead cost twice the MMAs, exponentials and registers for groups
+// of up to 8 heads: 209 us against 92 us of reading at 32 sequences of 1K..16K tokens.)
 //
 // E4M3 caches: codes widen exactly to F16; a key's scale multiplies its score, and the scale of
 // its value joins the exponent, w = 2^(s + log2 vs - max), so that O = sum w v_code and
@@ -25,6 +29,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "sdpa_internal.h"
@@ -37,11 +43,12 @@ using namespace ptx;
 constexpr int kWarps = 4;
 constexpr int kSlice = 16;                 // keys of a warp's slice
 constexpr int kTile = kWarps * kSlice;     // keys of a tile
-constexpr int kRows = 16;                  // query rows of a block
 constexpr int kThreads = kWarps * 32;
 
-template <int D, int CT>
+// NR: blocks of 8 query rows that a CTA works on at once.
+template <int D, int CT, int NR>
 struct DecCfg {
+  static constexpr int ROWS = 8 * NR;
   static constexpr int ES = CT == kE4M3 ? 1 : 2;
   static constexpr int RB = D * ES;                     // bytes of a row
   static constexpr int CH = RB / 16;                    // 16-byte chunks of a row
@@ -50,14 +57,18 @@ struct DecCfg {
   static constexpr int VB = RB >= 128 ? 16 : 8;         // bytes of a value row a lane reads at once
   static constexpr int EPV = VB / ES;                   // and elements
   static constexpr int VJ = D / (8 * EPV);              // such reads of a value row
+  static constexpr int NT = D / 16;                     // 16-element tiles of O^T
   static constexpr int SC_BYTES = CT == kE4M3 ? 2 * kSlice * 4 : 0;
   static constexpr int STAGE = 2 * kSlice * RB + SC_BYTES;
-  static constexpr int MERGE = kWarps * kRows * D * 4;  // the warps' partial O at the end of a run
-  static constexpr int NS = D == 256 ? (CT == kE4M3 ? 3 : 3) : (STAGE > 4608 ? 3 : 6);
+  static constexpr int MERGE = kWarps * ROWS * D * 4;   // the warps' partial O at the end of a run
+  static constexpr int CTAS = RB > 256 ? 1 : (D * NR > 256 || RB > 128 ? 2 : 3);   // of an SM
+  static constexpr int NS_FIT = (232448 / CTAS - 3072) / (kWarps * STAGE);
+  static constexpr int NS = NS_FIT > 6 ? 6 : NS_FIT;
   static constexpr int RING = kWarps * NS * STAGE;
   static constexpr int SMEM = RING > MERGE ? RING : MERGE;
   static constexpr float P_OFF = (CT == kBF16) ? 0.f : 6.f;   // F16 weights: kept away from F16's lowest
   static constexpr float THRESH = 8.f;                  // the running max moves when exceeded by this much
+  static_assert(NS >= 2 && NS * 5 <= 32, "ring");
 };
 
 // Position of 16-byte chunk `ch` of row `r` in a stage: neighbouring rows differ in bit 2 (the
@@ -80,18 +91,26 @@ __device__ __forceinline__ void cp_wait() {
 
 // D += A B, 16x8x16, F16 or BF16 with fp32 accumulators.
 template <bool BF>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
   if constexpr (BF) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   } else {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   }
+}
+
+// Transposes an 8x8 matrix of 16-bit elements held as rows of pairs by the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
@@ -215,20 +234,19 @@ __device__ float add_nonfinite(const DecodeParams& p, int bi, int hk, const SeqL
 
 // ---- main kernel -----------------------------------------------------------------------------
 
-template <int D, int CT, int QT>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant__ DecodeParams p) {
-  using C = DecCfg<D, CT>;
+template <int D, int CT, int QT, int NR>
+__global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kernel(const __grid_constant__ DecodeParams p) {
+  using C = DecCfg<D, CT, NR>;
   constexpr bool E4 = CT == kE4M3;
   constexpr bool BF = CT == kBF16;           // type of the products' operands
-  constexpr int NT = D / 8;                  // 8-column tiles of O
+  constexpr int ROWS = C::ROWS, NT = C::NT;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
   __shared__ int s_found;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, c = lane % 4;
   uint8_t* ring = smem + warp * C::NS * C::STAGE;
-  const uint32_t ring_a = smem_u32(ring);
 
   const int per_seq = p.c.h_kv * p.row_tiles;              // blocks of rows of a sequence
   const long long total = tiles_before(p, p.c.b, lane) * per_seq;
@@ -241,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
   // The sequence that holds tile t.
   int bi = 0;
   long long base = 0;    // first tile of sequence bi
-  for (;; ) {
+  for (;;) {
     const int i = bi + lane;
     const long long n = i < p.c.b ? static_cast<long long>(seq_tiles(p, i)) * per_seq : 0;
     long long incl = n;
@@ -262,6 +280,10 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
     if (bi >= p.c.b) return;   // not reached: t < total
   }
 
+  // cp.async: lane's chunk of rows (lane / CH) + x * RPX of a slice.
+  constexpr int RPX = 32 / C::CH;
+  const int ld_row = lane / C::CH, ld_ch = lane % C::CH;
+
   while (t < t_end) {
     const SeqLens L = seq_lens(p, bi);
     const int n_tiles = seq_tiles(p, bi);
@@ -271,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
       continue;
     }
     const int blk = static_cast<int>((t - base) / n_tiles);
-    const int hk = blk / p.row_tiles, r0 = (blk % p.row_tiles) * kRows;
+    const int hk = blk / p.row_tiles, r0 = (blk % p.row_tiles) * ROWS;
     const long long blk_t0 = base + static_cast<long long>(blk) * n_tiles;
     const int tile0 = static_cast<int>(t - blk_t0);
     const int tile1 = static_cast<int>(min(static_cast<long long>(n_tiles), t_end - blk_t0));
@@ -280,60 +302,71 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
 
     // ---- the ring: slice i of this warp is keys (tile0 + i) * 64 + warp * 16 ------------------
     const int n_slices = tile1 - tile0;
-    int page_cache = 0;    // lane i: page of slice (i of the last 32 asked for), or -1
-    auto page_of = [&](int i) {
-      if (i % 32 == 0) {
-        const int key = (tile0 + i + lane) * kTile + warp * kSlice;
-        page_cache = -1;
-        if (i + lane < n_slices && key < L.len_kv) {
-          const int page = __ldg(p.c.page_table + bi * p.c.page_table_stride + key / p.c.page_size);
-          if (page >= 0 && page < p.c.num_pages) page_cache = page;
-        }
-      }
-      return __shfl_sync(0xffffffffu, page_cache, i % 32);
-    };
-    unsigned valid_hist = 0;   // 5 bits a stage in flight: keys of the slice that exist
+    const int32_t* pages = p.c.page_table + bi * p.c.page_table_stride;
+    const uint8_t* k_lane = p.c.k + hk * p.c.k_st[1] + ld_row * p.c.k_st[2] + ld_ch * 16;
+    const uint8_t* v_lane = p.c.v + hk * p.c.v_st[1] + ld_row * p.c.v_st[2] + ld_ch * 16;
+    int my_page = -1, my_slot = 0;   // lane i: page and slot of slice i of the last 32 asked for
+    unsigned valid_hist = 0;         // 5 bits a stage: keys of its slice that exist
     auto load = [&](int i) {
       if (i < n_slices) {
-        const int key = (tile0 + i) * kTile + warp * kSlice;
-        const int page = page_of(i);
-        const int valid = page < 0 ? 0 : min(max(L.len_kv - key, 0), kSlice);
-        const int slot = key % p.c.page_size;
-        const int64_t pg = page < 0 ? 0 : page;
-        const uint8_t* kp = p.c.k + pg * p.c.k_st[0] + hk * p.c.k_st[1] + slot * p.c.k_st[2];
-        const uint8_t* vp = p.c.v + pg * p.c.v_st[0] + hk * p.c.v_st[1] + slot * p.c.v_st[2];
-        const uint32_t dst = ring_a + (i % C::NS) * C::STAGE;
+        if (i % 32 == 0) {
+          const int key = (tile0 + i + lane) * kTile + warp * kSlice;
+          my_page = -1;
+          if (i + lane < n_slices && key < L.len_kv) {
+            const int col = key / p.c.page_size;
+            my_slot = key - col * p.c.page_size;
+            my_page = __ldg(pages + col);
+            if (my_page >= p.c.num_pages) my_page = -1;
+          }
+        }
+        const int page = __shfl_sync(0xffffffffu, my_page, i % 32);
+        const int slot = __shfl_sync(0xffffffffu, my_slot, i % 32);
+        const int left = L.len_kv - ((tile0 + i) * kTile + warp * kSlice);
+        const int valid = page < 0 ? 0 : min(max(left, 0), kSlice);
+        const uint8_t* kp = k_lane + page * p.c.k_st[0] + slot * p.c.k_st[2];
+        const uint8_t* vp = v_lane + page * p.c.v_st[0] + slot * p.c.v_st[2];
+        const int stage = i % C::NS;
+        const uint32_t dst = smem_u32(ring) + stage * C::STAGE;
+        if (valid == kSlice) {
 #pragma unroll
-        for (int x = 0; x < kSlice * C::CH / 32; ++x) {
-          const int id = x * 32 + lane, r = id / C::CH, ch = id % C::CH;
-          const bool on = r < valid;
-          const uint32_t at = dst + r * C::RB + swz<C::CH>(r, ch) * 16;
-          cp_async16(at, on ? kp + r * p.c.k_st[2] + ch * 16 : p.c.k, on);
-          cp_async16(at + kSlice * C::RB, on ? vp + r * p.c.v_st[2] + ch * 16 : p.c.v, on);
+          for (int x = 0; x < kSlice / RPX; ++x) {
+            const uint32_t at = dst + (x * RPX + ld_row) * C::RB + swz<C::CH>(x * RPX + ld_row, ld_ch) * 16;
+            cp_async16(at, kp + x * RPX * p.c.k_st[2], true);
+            cp_async16(at + kSlice * C::RB, vp + x * RPX * p.c.v_st[2], true);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < kSlice / RPX; ++x) {
+            const bool on = x * RPX + ld_row < valid;
+            const uint32_t at = dst + (x * RPX + ld_row) * C::RB + swz<C::CH>(x * RPX + ld_row, ld_ch) * 16;
+            cp_async16(at, on ? kp + x * RPX * p.c.k_st[2] : p.c.k, on);
+            cp_async16(at + kSlice * C::RB, on ? vp + x * RPX * p.c.v_st[2] : p.c.v, on);
+          }
         }
         if constexpr (E4) {
           if (lane < 8) {
             const bool on = valid > 0;
-            const float* src = (lane < 4 ? p.c.k_scale : p.c.v_scale) + (pg * p.c.h_kv + hk) * p.c.page_size + slot + (lane % 4) * 4;
+            const float* src = (lane < 4 ? p.c.k_scale : p.c.v_scale) +
+                               (static_cast<int64_t>(page) * p.c.h_kv + hk) * p.c.page_size + slot + (lane % 4) * 4;
             cp_async16(dst + 2 * kSlice * C::RB + lane * 16, on ? src : p.c.k_scale, on);
           }
         }
-        valid_hist = (valid_hist & ~(31u << (5 * (i % C::NS)))) | (static_cast<unsigned>(valid) << (5 * (i % C::NS)));
+        valid_hist = (valid_hist & ~(31u << (5 * stage))) | (static_cast<unsigned>(valid) << (5 * stage));
       }
       cp_commit();
     };
-    static_assert(C::NS * 5 <= 32, "valid_hist");
     for (int i = 0; i < C::NS - 1; ++i) load(i);
 
-    // ---- Q fragments (rows g and g + 8), permuted to the order in which lanes read keys -------
-    uint32_t qf[D / 16][4];
-    float cs[2];
+    // ---- Q^T fragments (columns: rows g of each block of 8), permuted to the order in which
+    // lanes read keys ----------------------------------------------------------------------------
+    uint32_t qf[NR][D / 8];
+    float cs[NR][2];           // factor on the scores of this lane's result columns, rows 2c, 2c + 1
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int r = r0 + g + 8 * u;
+    for (int n = 0; n < NR; ++n) {
+      const int r = r0 + n * 8 + g;
       const bool on = r < p.rows && r / p.group < L.len_q;
       const uint16_t* row = static_cast<const uint16_t*>(p.q) + (on ? row_offset(p, p.q_st, bi, hk, r) : 0);
-      uint32_t w[D / 8];
+      uint32_t (&w)[D / 8] = qf[n];
 #pragma unroll
       for (int j = 0; j < C::KCH; ++j) {
 #pragma unroll
@@ -344,7 +377,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
           w[at] = x.x; w[at + 1] = x.y; w[at + 2] = x.z; w[at + 3] = x.w;
         }
       }
-      cs[u] = p.scale_log2;
+      cs[n][0] = cs[n][1] = p.scale_log2;
       if constexpr (E4 && QT == kBF16) {
         // The products of an E4M3 cache run in F16: a power of two brings the row's largest
         // element to [256, 512), where F16 holds every BF16 value down to 2^-22 of it exactly.
@@ -356,24 +389,26 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
         const int ex = static_cast<int>(m >> 7);           // biased exponent of the largest
         const int sh = (ex == 0 || ex == 255) ? 0 : min(127 + 8 - ex, 126);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-        cs[u] *= __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
           const float2 f = unpack_pair<true>(w[i]);
           w[i] = pack_pair<false>(f.x * up, f.y * up);
         }
-      }
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        qf[i][u] = w[2 * i];
-        qf[i][u + 2] = w[2 * i + 1];
+        for (int u = 0; u < 2; ++u)   // row 2c + u is held by lanes 4 (2c + u) ..
+          cs[n][u] *= __uint_as_float(static_cast<uint32_t>(127 - __shfl_sync(0xffffffffu, sh, 4 * (2 * c + u))) << 23);
       }
     }
 
-    float o[NT][4];
+    float o[NR][NT][4];
+    float m_ref[NR][2], l[NR][2];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int n = 0; n < NR; ++n) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+      m_ref[n][0] = m_ref[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
     bool found = false;
     if (threadIdx.x == 0) s_found = 0;
 
@@ -381,95 +416,126 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
       cp_wait<C::NS - 2>();
       __syncwarp();             // slice i has landed, and every lane is done with slice i - 1
       load(i + C::NS - 1);
-      const uint8_t* st = ring + (i % C::NS) * C::STAGE;
-      const int valid = (valid_hist >> (5 * (i % C::NS))) & 31;
+      const int stage = i % C::NS;
+      const uint8_t* st = ring + stage * C::STAGE;
+      const int valid = (valid_hist >> (5 * stage)) & 31;
+      if (valid == 0) continue;
       const int key0 = (tile0 + i) * kTile + warp * kSlice;
-      if (valid > 0) {
-        // ---- S = Q K^T -------------------------------------------------------------------
-        float s[2][4];
+      const bool tail = masked && key0 + kSlice > off;
+
+      // ---- S^T = K Q^T; lane: keys g, g + 8 by rows 2c, 2c + 1 ------------------------------------
+      float s[NR][4];
+      {
+        float s2[NR][4];     // two sums, so that the MMAs of one need not wait for each other
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-          const int r = n * 8 + g;
+        for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = s2[n][0] = s2[n][1] = s2[n][2] = s2[n][3] = 0.f;
 #pragma unroll
-          for (int j = 0; j < C::KCH; ++j) {
-            const uint4 k4 = *reinterpret_cast<const uint4*>(st + r * C::RB + swz<C::CH>(r, j * 4 + c) * 16);
-            const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
-            if constexpr (E4) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                mma16816<BF>(s[n], qf[4 * j + e], e4m3x2_to_f16x2(w[e] & 0xFFFFu), e4m3x2_to_f16x2(w[e] >> 16));
-            } else {
-              mma16816<BF>(s[n], qf[2 * j], w[0], w[1]);
-              mma16816<BF>(s[n], qf[2 * j + 1], w[2], w[3]);
-            }
-          }
-        }
-        // ---- scale, mask; thread: rows g, g + 8, keys 2c, 2c + 1 of each n ----------------------
-        float rvs[2][2];   // 1 / scale of a key's value (E4M3)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float ks = 1.f, lv = 0.f;
-            if constexpr (E4) {
-              const float* sc = reinterpret_cast<const float*>(st + 2 * kSlice * C::RB);
-              ks = sc[n * 8 + 2 * c + e];
-              float vs = sc[kSlice + n * 8 + 2 * c + e];
-              if (n * 8 + 2 * c + e >= valid) vs = 1.f;
-              lv = __log2f(vs);
-              rvs[n][e] = __fdividef(1.f, vs);
-            }
-            s[n][e] = fmaf(s[n][e], cs[0] * ks, lv);
-            s[n][e + 2] = fmaf(s[n][e + 2], cs[1] * ks, lv);
-          }
-        const bool tail = masked && key0 + kSlice > off;
-        if (valid < kSlice || tail) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
+        for (int j = 0; j < C::KCH; ++j) {
+          const uint4 ka = *reinterpret_cast<const uint4*>(st + g * C::RB + swz<C::CH>(g, j * 4 + c) * 16);
+          const uint4 kb = *reinterpret_cast<const uint4*>(st + (g + 8) * C::RB + swz<C::CH>(g + 8, j * 4 + c) * 16);
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+          if constexpr (E4) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int kk = n * 8 + 2 * c + (e & 1);
-              const int r = r0 + g + 8 * (e >> 1), token = r / p.group;
-              bool see = kk < valid;
-              if (see && tail && r < p.rows && token < L.len_q) see = row_sees(p, bi, L, token, key0 + kk);
-              if (!see) s[n][e] = -INFINITY;
+              const uint32_t a0 = e4m3x2_to_f16x2(wa[e] & 0xFFFFu), a1 = e4m3x2_to_f16x2(wb[e] & 0xFFFFu);
+              const uint32_t a2 = e4m3x2_to_f16x2(wa[e] >> 16), a3 = e4m3x2_to_f16x2(wb[e] >> 16);
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+                mma16816<BF>(e % 2 ? s2[n] : s[n], a0, a1, a2, a3, qf[n][8 * j + 2 * e], qf[n][8 * j + 2 * e + 1]);
             }
+          } else {
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+              mma16816<BF>(s[n], wa[0], wb[0], wa[1], wb[1], qf[n][4 * j], qf[n][4 * j + 1]);
+              mma16816<BF>(s2[n], wa[2], wb[2], wa[3], wb[3], qf[n][4 * j + 2], qf[n][4 * j + 3]);
+            }
+          }
         }
-        // ---- running max, weights, sums ----------------------------------------------------
-        uint32_t pa[4];
-        float alpha[2];
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
+      }
+
+      // ---- scale (log2 units), mask ----------------------------------------------------------------
+      float rvs[2] = {1.f, 1.f};   // 1 / scale of this lane's keys' values (E4M3)
+      if constexpr (E4) {
+        const float* sc = reinterpret_cast<const float*>(st + 2 * kSlice * C::RB);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float mx = fmaxf(fmaxf(s[0][2 * u], s[0][2 * u + 1]), fmaxf(s[1][2 * u], s[1][2 * u + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          alpha[u] = 1.f;
-          if (mx > m_ref[u] + C::THRESH) {
-            alpha[u] = ex2(m_ref[u] - mx);
-            m_ref[u] = mx;
-          }
-          const float nm = m_ref[u] == -INFINITY ? 0.f : C::P_OFF - m_ref[u];
-          float w[4];
+          const float ks = sc[g + 8 * u], vs = g + 8 * u < valid ? sc[kSlice + g + 8 * u] : 1.f;
+          const float lv = __log2f(vs);
+          rvs[u] = __fdividef(1.f, vs);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = ex2(s[e / 2][2 * u + e % 2] + nm);
-          float add;
-          if constexpr (E4) add = (w[0] * rvs[0][0] + w[1] * rvs[0][1]) + (w[2] * rvs[1][0] + w[3] * rvs[1][1]);
-          else add = (w[0] + w[1]) + (w[2] + w[3]);
-          l[u] = l[u] * alpha[u] + add;
-          pa[u] = pack_pair<BF>(w[0], w[1]);
-          pa[u + 2] = pack_pair<BF>(w[2], w[3]);
-        }
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-          for (int x = 0; x < NT; ++x) {
-            o[x][0] *= alpha[0];
-            o[x][1] *= alpha[0];
-            o[x][2] *= alpha[1];
-            o[x][3] *= alpha[1];
+          for (int n = 0; n < NR; ++n) {
+            s[n][2 * u] = fmaf(s[n][2 * u], cs[n][0] * ks, lv);
+            s[n][2 * u + 1] = fmaf(s[n][2 * u + 1], cs[n][1] * ks, lv);
           }
         }
-        // ---- O += P V ------------------------------------------------------------------------
+      } else {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] *= cs[n][e % 2];
+      }
+      if (valid < kSlice || tail) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int kk = g + 8 * (e / 2), r = r0 + n * 8 + 2 * c + e % 2, token = r / p.group;
+            bool see = kk < valid;
+            if (see && tail && r < p.rows && token < L.len_q) see = row_sees(p, bi, L, token, key0 + kk);
+            if (!see) s[n][e] = -INFINITY;
+          }
+      }
+
+      // ---- running max: moved, for the lanes of a row together, when a score exceeds it by 2^8 -------
+      bool over = false;
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) over |= s[n][e] > m_ref[n][e % 2] + C::THRESH;
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          float alpha[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float mx = fmaxf(s[n][u], s[n][u + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            alpha[u] = 1.f;
+            if (mx > m_ref[n][u] + C::THRESH) {
+              alpha[u] = ex2(m_ref[n][u] - mx);
+              m_ref[n][u] = mx;
+            }
+            l[n][u] *= alpha[u];
+          }
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][x][e] *= alpha[e % 2];
+        }
+      }
+      // ---- weights, sums, P^T ------------------------------------------------------------------------
+      uint32_t pb[NR][2];
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const float nm0 = m_ref[n][0] == -INFINITY ? 0.f : C::P_OFF - m_ref[n][0];
+        const float nm1 = m_ref[n][1] == -INFINITY ? 0.f : C::P_OFF - m_ref[n][1];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float w0 = ex2(s[n][2 * u] + nm0), w1 = ex2(s[n][2 * u + 1] + nm1);
+          l[n][0] = fmaf(w0, rvs[u], l[n][0]);
+          l[n][1] = fmaf(w1, rvs[u], l[n][1]);
+          pb[n][u] = transpose8x8(pack_pair<BF>(w0, w1));
+        }
+      }
+
+      // ---- O^T += V^T P^T; lane's part of a value: d = (8 j + g) * EPV + 0 .. EPV - 1 --------------------
+      auto product = [&](auto clear) {
 #pragma unroll
         for (int j = 0; j < C::VJ; ++j) {
           uint32_t v[4][C::VB / 4];   // keys 2c, 2c + 1, 2c + 8, 2c + 9
@@ -486,89 +552,107 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
             }
           }
 #pragma unroll
-          for (int x = 0; x < C::EPV; ++x) {
-            uint32_t b0, b1;
-            if constexpr (E4) {
-              const uint32_t sel = (x % 4) | ((x % 4 + 4) << 4);
-              b0 = e4m3x2_to_f16x2(prmt(v[0][x / 4], v[1][x / 4], sel));
-              b1 = e4m3x2_to_f16x2(prmt(v[2][x / 4], v[3][x / 4], sel));
-            } else {
-              const uint32_t sel = x % 2 ? 0x7632u : 0x5410u;
-              b0 = prmt(v[0][x / 2], v[1][x / 2], sel);
-              b1 = prmt(v[2][x / 2], v[3][x / 2], sel);
+          for (int x = 0; x < C::EPV; x += 2) {   // elements x, x + 1: rows g, g + 8 of one tile of O^T
+            uint32_t a[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if constexpr (E4) {
+                // bytes x, x + 1 of both keys: (key, key + 1) of x in the low half, of x + 1 in the high
+                const uint32_t two = prmt(v[2 * h][x / 4], v[2 * h + 1][x / 4], x % 4 ? 0x7362u : 0x5140u);
+                a[2 * h] = e4m3x2_to_f16x2(two & 0xFFFFu);
+                a[2 * h + 1] = e4m3x2_to_f16x2(two >> 16);
+              } else {
+                a[2 * h] = prmt(v[2 * h][x / 2], v[2 * h + 1][x / 2], 0x5410u);
+                a[2 * h + 1] = prmt(v[2 * h][x / 2], v[2 * h + 1][x / 2], 0x7632u);
+              }
             }
-            if (tail) {
-              b0 = finite_pair<BF>(b0, found);
-              b1 = finite_pair<BF>(b1, found);
+            if constexpr (decltype(clear)::value) {
+#pragma unroll
+              for (int h = 0; h < 4; ++h) a[h] = finite_pair<BF>(a[h], found);
             }
-            mma16816<BF>(o[j * C::EPV + x], pa, b0, b1);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) mma16816<BF>(o[n][(j * C::EPV + x) / 2], a[0], a[1], a[2], a[3], pb[n][0], pb[n][1]);
           }
         }
-      }
+      };
+      if (tail) product(std::true_type{});
+      else product(std::false_type{});
     }
     cp_wait<0>();
 
     // ---- the four warps' results meet -----------------------------------------------------------
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
-      l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
-      if (c == 0) {
-        s_m[warp][g + 8 * u] = m_ref[u];
-        s_l[warp][g + 8 * u] = l[u];
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[n][u] += __shfl_xor_sync(0xffffffffu, l[n][u], x);
+        if (g == 0) {
+          s_m[warp][n * 8 + 2 * c + u] = m_ref[n][u];
+          s_l[warp][n * 8 + 2 * c + u] = l[n][u];
+        }
       }
-    }
     __syncthreads();
     if (found) s_found = 1;
-    float big[2];
     float* merge = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int r = g + 8 * u;
-      big[u] = s_m[0][r];
-      for (int w = 1; w < kWarps; ++w) big[u] = fmaxf(big[u], s_m[w][r]);
-      const float f = m_ref[u] == -INFINITY ? 0.f : ex2(m_ref[u] - big[u]);
-      // Columns of 8-wide tile j * EPV + x: d = (j * 8 + n) * EPV + x for n = 2c, 2c + 1.
-      float* row = merge + (warp * kRows + r) * D;
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int j = 0; j < C::VJ; ++j)
+      for (int u = 0; u < 2; ++u) {
+        const int r = n * 8 + 2 * c + u;
+        float big = s_m[0][r];
+        for (int w = 1; w < kWarps; ++w) big = fmaxf(big, s_m[w][r]);
+        // A warp that saw no key (sum 0) adds nothing; a sum of NaN with no maximum stays NaN.
+        const bool none = m_ref[n][u] == -INFINITY;
+        const float f = none ? 1.f : ex2(m_ref[n][u] - big);
+        float* row = merge + (warp * ROWS + r) * D + g * C::EPV;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int j = 0; j < C::VJ; ++j)
 #pragma unroll
           for (int x = 0; x < C::EPV; x += 4) {
-            float4 q4;
-            q4.x = o[j * C::EPV + x][2 * u + n] * f;
-            q4.y = o[j * C::EPV + x + 1][2 * u + n] * f;
-            q4.z = o[j * C::EPV + x + 2][2 * u + n] * f;
-            q4.w = o[j * C::EPV + x + 3][2 * u + n] * f;
-            if (m_ref[u] == -INFINITY && f == 0.f && l[u] == 0.f) q4 = make_float4(0.f, 0.f, 0.f, 0.f);
-            *reinterpret_cast<float4*>(row + (j * 8 + 2 * c + n) * C::EPV + x) = q4;
+            const int i = (j * C::EPV + x) / 2;
+            float4 q4 = make_float4(o[n][i][u] * f, o[n][i][u + 2] * f, o[n][i + 1][u] * f, o[n][i + 1][u + 2] * f);
+            if (l[n][u] == 0.f) q4 = make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4*>(row + j * 8 * C::EPV + x) = q4;
           }
-    }
+      }
     __syncthreads();
     const bool whole = tile0 == 0 && tile1 == n_tiles;
     const int part = 2 * blockIdx.x + (tile0 == 0 ? 1 : 0);
     const bool fix = s_found != 0;
-    for (int idx = threadIdx.x; idx < kRows * D; idx += kThreads) {
-      const int r = idx / D, d = idx % D;
-      float mb = s_m[0][r], lb = 0.f, x = 0.f;
+    const int live = min(ROWS, p.rows - r0);
+    for (int idx = threadIdx.x; idx < live * (D / 4); idx += kThreads) {
+      const int r = idx / (D / 4), d = idx % (D / 4) * 4;
+      float mb = s_m[0][r], lb = 0.f;
       for (int w = 1; w < kWarps; ++w) mb = fmaxf(mb, s_m[w][r]);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        x += merge[(w * kRows + r) * D + d];
+        const float4 y = *reinterpret_cast<const float4*>(merge + (w * ROWS + r) * D + d);
+        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
         if (s_l[w][r] != 0.f) lb += s_l[w][r] * (s_m[w][r] == -INFINITY ? 1.f : ex2(s_m[w][r] - mb));
       }
       const int row = r0 + r, token = row / p.group;
-      const bool on = row < p.rows && token < L.len_q;
-      if (fix && on) x = add_nonfinite<D, CT>(p, bi, hk, L, row, d, tile0 * kTile, min(tile1 * kTile, L.len_kv), x);
+      const bool on = token < L.len_q;
+      if (fix && on) {
+        const int k0 = tile0 * kTile, k1 = min(tile1 * kTile, L.len_kv);
+        x.x = add_nonfinite<D, CT>(p, bi, hk, L, row, d, k0, k1, x.x);
+        x.y = add_nonfinite<D, CT>(p, bi, hk, L, row, d + 1, k0, k1, x.y);
+        x.z = add_nonfinite<D, CT>(p, bi, hk, L, row, d + 2, k0, k1, x.z);
+        x.w = add_nonfinite<D, CT>(p, bi, hk, L, row, d + 3, k0, k1, x.w);
+      }
       if (!whole) {
-        p.part_o[(static_cast<int64_t>(part) * kRows + r) * D + d] = x;
-        if (d == 0) {
-          p.part_ml[(part * kRows + r) * 2] = mb;
-          p.part_ml[(part * kRows + r) * 2 + 1] = lb;
-        }
-      } else if (row < p.rows) {
+        const int64_t at = static_cast<int64_t>(part) * ROWS + r;
+        *reinterpret_cast<float4*>(p.part_o + at * D + d) = x;
+        if (d == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(mb, lb);
+      } else {
         const bool none = !on || lb == 0.f;
-        store_o<QT>(p.o, row_offset(p, p.o_st, bi, hk, row) + d, none ? 0.f : x / lb);
+        const float inv = none ? 0.f : 1.f / lb;
+        if (none) x = make_float4(0.f, 0.f, 0.f, 0.f);
+        uint2 w;
+        w.x = pack_pair<QT == kBF16>(x.x * inv, x.y * inv);
+        w.y = pack_pair<QT == kBF16>(x.z * inv, x.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row_offset(p, p.o_st, bi, hk, row) + d) = w;
         if (p.lse && d == 0)
           p.lse[(static_cast<int64_t>(bi) * p.h_q + hk * p.group + row % p.group) * p.s_q + token] =
               none ? -INFINITY : (mb - C::P_OFF + __log2f(lb)) * 0.6931471805599453f;
@@ -589,11 +673,11 @@ __global__ void __launch_bounds__(kThreads) decode_combine_kernel(const __grid_c
   __shared__ float s_sum[kWarps][D];
   __shared__ float s_l[kWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int rows_blk = min(p.rows, kRows);
+  const int rows_blk = min(p.rows, p.tile_rows);
   const int per_seq = p.c.h_kv * p.row_tiles;
   const int unit = blockIdx.x / rows_blk, r = blockIdx.x % rows_blk;
   const int bi = unit / per_seq, blk = unit % per_seq;
-  const int hk = blk / p.row_tiles, row = blk % p.row_tiles * kRows + r, token = row / p.group;
+  const int hk = blk / p.row_tiles, row = blk % p.row_tiles * p.tile_rows + r, token = row / p.group;
   const int n_tiles = seq_tiles(p, bi);
   const SeqLens L = seq_lens(p, bi);
   int c0 = 0, n = 0;                  // parts: CTAs c0 .. c0 + n - 1 (none where there are no tiles)
@@ -606,7 +690,7 @@ __global__ void __launch_bounds__(kThreads) decode_combine_kernel(const __grid_c
   griddep_wait();   // (by every CTA, so that this grid never ends before the one it follows)
   if (n == 1 || row >= p.rows) return;       // finished by that CTA
   // Part k: the first holds its block's first tile and is that CTA's second part.
-  auto part = [&](int k) { return static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)) * kRows + r; };
+  auto part = [&](int k) { return static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)) * p.tile_rows + r; };
   float m = -INFINITY;
   for (int k = lane; k < n; k += 32) {
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * part(k));
@@ -660,17 +744,17 @@ __global__ void __launch_bounds__(kThreads) decode_combine_kernel(const __grid_c
         none ? -INFINITY : (m - p_off + __log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D, int CT, int QT>
+template <int D, int CT, int QT, int NR>
 cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
-  using C = DecCfg<D, CT>;
-  auto kern = decode_kernel<D, CT, QT>;
+  using C = DecCfg<D, CT, NR>;
+  auto kern = decode_kernel<D, CT, QT, NR>;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<p.ctas, kThreads, C::SMEM, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles * (p.rows < kRows ? p.rows : kRows));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles * (p.rows < p.tile_rows ? p.rows : p.tile_rows));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute at;
@@ -681,21 +765,38 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, decode_combine_kernel<D, QT>, p, C::P_OFF);
 }
 
+template <int D, int CT, int QT>
+cudaError_t launch_r(const DecodeParams& p, cudaStream_t st) {
+  return p.tile_rows == 8 ? launch_t<D, CT, QT, 1>(p, st) : launch_t<D, CT, QT, 2>(p, st);
+}
+
 template <int D>
 cudaError_t launch_d(const DecodeParams& p, int qt, int ct, cudaStream_t st) {
-  if (qt == kBF16) return ct == kE4M3 ? launch_t<D, kE4M3, kBF16>(p, st) : launch_t<D, kBF16, kBF16>(p, st);
-  return ct == kE4M3 ? launch_t<D, kE4M3, kF16>(p, st) : launch_t<D, kF16, kF16>(p, st);
+  if (qt == kBF16) return ct == kE4M3 ? launch_r<D, kE4M3, kBF16>(p, st) : launch_r<D, kBF16, kBF16>(p, st);
+  return ct == kE4M3 ? launch_r<D, kE4M3, kF16>(p, st) : launch_r<D, kF16, kF16>(p, st);
+}
+
+template <int D>
+int ctas_of_sm(int tile_rows, bool e4m3) {
+  if (e4m3) return tile_rows == 8 ? DecCfg<D, kE4M3, 1>::CTAS : DecCfg<D, kE4M3, 2>::CTAS;
+  return tile_rows == 8 ? DecCfg<D, kF16, 1>::CTAS : DecCfg<D, kF16, 2>::CTAS;
 }
 
 }  // namespace
 
-int decode_ctas(const DecodeParams& p, int num_sms) {
-  const long long tiles = static_cast<long long>(p.c.b) * p.c.h_kv * p.row_tiles * ((p.c.max_len + kTile - 1ll) / kTile);
-  return static_cast<int>(tiles < 2ll * num_sms ? (tiles < 1 ? 1 : tiles) : 2ll * num_sms);
+void decode_plan(DecodeParams* p, int d, int ct, int num_sms) {
+  p->tile_rows = p->rows <= 8 ? 8 : 16;
+  p->row_tiles = (p->rows + p->tile_rows - 1) / p->tile_rows;
+  const bool e4 = ct == kE4M3;
+  const int per_sm = d == 64 ? ctas_of_sm<64>(p->tile_rows, e4) : d == 128 ? ctas_of_sm<128>(p->tile_rows, e4)
+                                                                           : ctas_of_sm<256>(p->tile_rows, e4);
+  const long long tiles = static_cast<long long>(p->c.b) * p->c.h_kv * p->row_tiles * ((p->c.max_len + kTile - 1ll) / kTile);
+  const long long top = static_cast<long long>(per_sm) * num_sms;
+  p->ctas = static_cast<int>(tiles < top ? tiles : top);
 }
 
-size_t decode_workspace_bytes(const DecodeParams& p, int d, int num_sms, size_t* ml_offset) {
-  const size_t parts = 2 * static_cast<size_t>(decode_ctas(p, num_sms)) * kRows;
+size_t decode_workspace_bytes(const DecodeParams& p, int d, size_t* ml_offset) {
+  const size_t parts = 2 * static_cast<size_t>(p.ctas) * p.tile_rows;
   if (ml_offset) *ml_offset = parts * d * 4;
   return (parts * d * 4 + parts * 8 + 255) & ~size_t(255);
 }

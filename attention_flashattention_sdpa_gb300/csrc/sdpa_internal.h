@@ -269,16 +269,16 @@ struct DecodeParams {
   int causal;
   int h_q, s_q, group;
   int rows;                    // s_q * group: query rows that share a KV head
-  int row_tiles;               // ceil(rows / rows of a tile)
+  int tile_rows, row_tiles;    // rows of a block, and blocks: ceil(rows / tile_rows)
   float scale_log2;            // attn_scale * log2(e)
-  float* part_o;               // workspace: [2 * ctas][tile rows][d] unnormalised partial O
-  float* part_ml;              // workspace: [2 * ctas][tile rows][2] their max (log2 units) and sum
+  float* part_o;               // workspace: [2 * ctas][tile_rows][d] unnormalised partial O
+  float* part_ml;              // workspace: [2 * ctas][tile_rows][2] their max (log2 units) and sum
   int ctas;
 };
 
-// CTAs of a launch over `b` sequences (from the sizes alone, so that workspace and launch agree).
-int decode_ctas(const DecodeParams& p, int num_sms);
-size_t decode_workspace_bytes(const DecodeParams& p, int d, int num_sms, size_t* ml_offset);
+// Fills in the blocks of rows and the CTAs (from the sizes alone, so that workspace and launch agree).
+void decode_plan(DecodeParams* p, int d, int cache_dtype, int num_sms);
+size_t decode_workspace_bytes(const DecodeParams& p, int d, size_t* ml_offset);
 cudaError_t launch_decode(const DecodeParams& p, int d, int q_dtype, int cache_dtype, cudaStream_t st);
 
 }  // namespace sdpa

@@ -222,9 +222,8 @@ sdpa::DecodeParams decode_params(const sdpa_cache_t* c, const sdpa_decode_t* p) 
   prm.s_q = p->s_q;
   prm.group = p->h_q / c->h_kv;
   prm.rows = p->s_q * prm.group;
-  prm.row_tiles = (prm.rows + 15) / 16;
   prm.scale_log2 = p->attn_scale * 1.4426950408889634f;
-  prm.ctas = sdpa::decode_ctas(prm, sdpa::api_num_sms());
+  sdpa::decode_plan(&prm, c->d, c->dtype, sdpa::api_num_sms());
   return prm;
 }
 
@@ -319,7 +318,7 @@ sdpa_status_t sdpa_cache_read(const sdpa_cache_t* c, const sdpa_cache_rows_t* r,
 sdpa_status_t sdpa_decode_workspace_size(const sdpa_cache_t* c, const sdpa_decode_t* p, size_t* bytes) {
   if (bytes == nullptr) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "bytes is NULL");
   SDPA_TRY(check_decode_sizes(c, p));
-  *bytes = sdpa::decode_workspace_bytes(decode_params(c, p), c->d, sdpa::api_num_sms(), nullptr);
+  *bytes = sdpa::decode_workspace_bytes(decode_params(c, p), c->d, nullptr);
   return static_cast<sdpa_status_t>(sdpa::api_ok());
 }
 
@@ -331,7 +330,7 @@ sdpa_status_t sdpa_decode(const sdpa_cache_t* c, const sdpa_decode_t* p, const v
   if (reinterpret_cast<uintptr_t>(lse) % 4) SDPA_REFUSE(SDPA_ERR_LAYOUT, "lse must be 4-byte aligned");
   sdpa::DecodeParams prm = decode_params(c, p);
   size_t ml = 0;
-  const size_t need = sdpa::decode_workspace_bytes(prm, c->d, sdpa::api_num_sms(), &ml);
+  const size_t need = sdpa::decode_workspace_bytes(prm, c->d, &ml);
   if (workspace == nullptr || workspace_bytes < need)
     SDPA_REFUSE(SDPA_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given%s", need, workspace_bytes,
                 workspace ? "" : " (NULL)");
