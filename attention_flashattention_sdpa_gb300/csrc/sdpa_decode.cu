@@ -26,23 +26,17 @@
 // E4M3 caches: codes widen exactly to F16; a key's scale multiplies its score, and the scale of
 // its value joins the exponent, w = 2^(s + log2 vs - max), so that O = sum w v_code and
 // l = sum w / vs.  The row max then bounds w whatever the scales, and no product with vs is rounded.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
 #include <type_traits>
 
-#include "ptx.cuh"
-#include "sdpa_internal.h"
+#include "sdpa_decode.cuh"
 
 namespace sdpa {
 namespace {
 
-using namespace ptx;
-
 constexpr int kWarps = 4;
 constexpr int kSlice = 16;                 // keys of a warp's slice
-constexpr int kTile = kWarps * kSlice;     // keys of a tile
+constexpr int kTile = kWarps * kSlice;     // keys of a tile (decode_plan's tile_shift)
+static_assert(kTile == 64);
 constexpr int kThreads = kWarps * 32;
 
 // NR: blocks of 8 query rows that a CTA works on at once.
@@ -111,125 +105,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two_codes), __NV_E4M3);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-template <bool BF>
-__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
-  if constexpr (BF) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-
-template <bool BF>
-__device__ __forceinline__ float2 unpack_pair(uint32_t w) {
-  if constexpr (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
-// Clears the halves of a 16-bit pair that are infinite or NaN; `found` gathers whether any was.
-template <bool BF>
-__device__ __forceinline__ uint32_t finite_pair(uint32_t w, bool& found) {
-  constexpr uint32_t kExp = BF ? 0x7F80u : 0x7C00u;
-  if ((w & kExp) == kExp) {
-    w &= 0xFFFF0000u;
-    found = true;
-  }
-  if ((w & (kExp << 16)) == (kExp << 16)) {
-    w &= 0x0000FFFFu;
-    found = true;
-  }
-  return w;
-}
-
-// ---- the batch as one row of tiles -----------------------------------------------------------
-
-struct SeqLens {
-  int len_q, len_kv;
-};
-
-__device__ __forceinline__ SeqLens seq_lens(const DecodeParams& p, int bi) {
-  SeqLens L;
-  L.len_q = p.seq_lens_q ? min(max(__ldg(p.seq_lens_q + bi), 0), p.s_q) : p.s_q;
-  L.len_kv = min(max(__ldg(p.c.seq_lens_kv + bi), 0), p.c.max_len);
-  return L;
-}
-
-// Tiles of one block of rows of sequence bi (none where no row takes part).
-__device__ __forceinline__ int seq_tiles(const DecodeParams& p, int bi) {
-  const SeqLens L = seq_lens(p, bi);
-  return L.len_q == 0 ? 0 : (L.len_kv + kTile - 1) / kTile;
-}
-
-// Sum of seq_tiles over sequences [0, n), by a whole warp.
-__device__ long long tiles_before(const DecodeParams& p, int n, int lane) {
-  long long t = 0;
-  for (int i = lane; i < n; i += 32) t += seq_tiles(p, i);
-#pragma unroll
-  for (int o = 16; o > 0; o /= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
-  return t;
-}
-
-// CTAs that have a run: no more than tiles, so that none of them is empty.
-__device__ __forceinline__ int working_ctas(const DecodeParams& p, long long total) {
-  return total < p.ctas ? static_cast<int>(total) : p.ctas;
-}
-
-// First tile of CTA c's run, and the CTA whose run holds tile t, of `total` tiles over g CTAs.
-__device__ __forceinline__ long long run_start(long long total, int c, int g) { return total * c / g; }
-__device__ __forceinline__ int cta_of(long long total, long long t, int g) {
-  return static_cast<int>(((t + 1) * g - 1) / total);
-}
-
-// Element offset of query row r (token r / group, head hk * group + r % group).
-__device__ __forceinline__ int64_t row_offset(const DecodeParams& p, const int64_t (&st)[3], int bi, int hk, int r) {
-  return bi * st[0] + (hk * p.group + r % p.group) * st[1] + (r / p.group) * st[2];
-}
-
-__device__ __forceinline__ bool tree_sees(const DecodeParams& p, int bi, int token, int j) {
-  const uint32_t* w = p.tree_mask + bi * p.tree_mask_stride + static_cast<int64_t>(token) * p.tree_words;
-  return (__ldg(w + j / 32) >> (j % 32)) & 1u;
-}
-
-// Whether query row r sees position `key` (< len_kv) of its sequence.
-__device__ __forceinline__ bool row_sees(const DecodeParams& p, int bi, const SeqLens& L, int token, int key) {
-  const int j = key - (L.len_kv - L.len_q);
-  if (p.causal) return j <= token;
-  if (p.tree_mask && j >= 0) return tree_sees(p, bi, token, j);
-  return true;
-}
-
-template <int DT>
-__device__ __forceinline__ void store_o(void* o, int64_t at, float x) {
-  static_cast<uint16_t*>(o)[at] = static_cast<uint16_t>(pack_pair<DT == kBF16>(x, 0.f) & 0xFFFFu);
-}
-
-// Infinities and NaNs of the drafted tokens' values: the products ran without them (a hidden
-// one times a weight of zero would be NaN); the rows that see them get them here.
-template <int D, int CT>
-__device__ float add_nonfinite(const DecodeParams& p, int bi, int hk, const SeqLens& L, int r, int d, int key0, int key1,
-                               float x) {
-  const int token = r / p.group;
-  // From the first slice that holds a new token (all of it was cleared).
-  for (int key = max(key0, (L.len_kv - L.len_q) & ~(kSlice - 1)); key < key1; ++key) {
-    if (!row_sees(p, bi, L, token, key)) continue;
-    const int page = __ldg(p.c.page_table + bi * p.c.page_table_stride + key / p.c.page_size);
-    if (page < 0 || page >= p.c.num_pages) continue;
-    const uint8_t* row = p.c.v + page * p.c.v_st[0] + hk * p.c.v_st[1] + (key % p.c.page_size) * p.c.v_st[2];
-    float v;
-    if (CT == kE4M3) v = (row[d] & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : 0.f;
-    else v = unpack_pair<CT == kBF16>(reinterpret_cast<const uint16_t*>(row)[d]).x;
-    if (!isfinite(v)) x += v;
-  }
-  return x;
 }
 
 // ---- main kernel -----------------------------------------------------------------------------
@@ -664,18 +539,20 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
 }
 
 // Joins the partial results of every block of rows that more than one CTA worked on, and writes
-// the rows that no key reaches.  One CTA a row: its lanes weigh the parts side by side (a part is
-// a maximum, a sum and d values), then each warp adds up every fourth part, 8 loads in flight,
-// and the four sums meet.  The order is that of the parts, so results do not change between calls.
-template <int D, int QT>
+// the rows that no key reaches.  WG warps share a row: its lanes weigh the parts side by side (a
+// part is a maximum, a sum and d values), then each warp adds up every WG-th part, 8 loads in
+// flight, and the sums meet.  The order is that of the parts, so results do not change between calls.
+template <int D, int QT, int WG>
 __global__ void __launch_bounds__(kThreads) decode_combine_kernel(const __grid_constant__ DecodeParams p, float p_off) {
   constexpr int EL = D / 32;          // elements a lane owns
+  constexpr int RPC = kWarps / WG;    // rows of a CTA
   __shared__ float s_sum[kWarps][D];
   __shared__ float s_l[kWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int rows_blk = min(p.rows, p.tile_rows);
+  const int sub = warp % WG;
+  const int per_unit = (min(p.rows, p.tile_rows) + RPC - 1) / RPC;
   const int per_seq = p.c.h_kv * p.row_tiles;
-  const int unit = blockIdx.x / rows_blk, r = blockIdx.x % rows_blk;
+  const int unit = blockIdx.x / per_unit, r = blockIdx.x % per_unit * RPC + warp / WG;
   const int bi = unit / per_seq, blk = unit % per_seq;
   const int hk = blk / p.row_tiles, row = blk % p.row_tiles * p.tile_rows + r, token = row / p.group;
   const int n_tiles = seq_tiles(p, bi);
@@ -688,60 +565,91 @@ __global__ void __launch_bounds__(kThreads) decode_combine_kernel(const __grid_c
     n = cta_of(total, t0 + n_tiles - 1, working_ctas(p, total)) - c0 + 1;
   }
   griddep_wait();   // (by every CTA, so that this grid never ends before the one it follows)
-  if (n == 1 || row >= p.rows) return;       // finished by that CTA
+  if (n == 1) return;                        // finished by that CTA
+  const bool on = r < p.tile_rows && row < p.rows;
   // Part k: the first holds its block's first tile and is that CTA's second part.
   auto part = [&](int k) { return static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)) * p.tile_rows + r; };
   float m = -INFINITY;
-  for (int k = lane; k < n; k += 32) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * part(k));
-    if (ml.y != 0.f) m = fmaxf(m, ml.x);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float x[EL], l = 0.f;
 #pragma unroll
   for (int e = 0; e < EL; ++e) x[e] = 0.f;
-  for (int k0 = warp; k0 < n; k0 += 8 * kWarps) {
-    float f[8], v[8][EL];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int k = k0 + u * kWarps;
-      f[u] = 0.f;
-#pragma unroll
-      for (int e = 0; e < EL; ++e) v[u][e] = 0.f;
-      if (k < n) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * part(k));
-        const float* src = p.part_o + part(k) * D + lane * EL;
-#pragma unroll
-        for (int e = 0; e < EL; e += 2) {
-          const float2 w = *reinterpret_cast<const float2*>(src + e);
-          v[u][e] = w.x;
-          v[u][e + 1] = w.y;
-        }
-        // A part without a visible key has sum 0 and weighs nothing.  (All sums NaN: m stays -inf.)
-        if (ml.y != 0.f) {
-          f[u] = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
-          l += ml.y * f[u];
-        }
-      }
+  if (on) {
+    for (int k = lane; k < n; k += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * part(k));
+      if (ml.y != 0.f) m = fmaxf(m, ml.x);
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
+    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int k0 = sub; k0 < n; k0 += 8 * WG) {
+      float f[8], v[8][EL];
 #pragma unroll
-      for (int e = 0; e < EL; ++e) x[e] += f[u] == 0.f ? 0.f : v[u][e] * f[u];
+      for (int u = 0; u < 8; ++u) {
+        const int k = k0 + u * WG;
+        f[u] = 0.f;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) v[u][e] = 0.f;
+        if (k < n) {
+          const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * part(k));
+          const float* src = p.part_o + part(k) * D + lane * EL;
+#pragma unroll
+          for (int e = 0; e < EL; e += 2) {
+            const float2 w = *reinterpret_cast<const float2*>(src + e);
+            v[u][e] = w.x;
+            v[u][e + 1] = w.y;
+          }
+          // A part without a visible key has sum 0 and weighs nothing.  (All sums NaN: m stays -inf.)
+          if (ml.y != 0.f) {
+            f[u] = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
+            l += ml.y * f[u];
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int e = 0; e < EL; ++e) x[e] += f[u] == 0.f ? 0.f : v[u][e] * f[u];
+    }
   }
+  const int64_t at = on ? row_offset(p, p.o_st, bi, hk, row) : 0;
+  const int64_t lse_at = (static_cast<int64_t>(bi) * p.h_q + hk * p.group + row % p.group) * p.s_q + token;
+  auto lse_of = [&](bool none, float sum) { return none ? -INFINITY : (m - p_off + __log2f(sum)) * 0.6931471805599453f; };
+  if constexpr (WG == 1) {
+    if (!on) return;
+    const bool none = token >= L.len_q || l == 0.f;
+    const float inv = none ? 0.f : 1.f / l;
 #pragma unroll
-  for (int e = 0; e < EL; ++e) s_sum[warp][lane * EL + e] = x[e];
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-  const bool none = token >= L.len_q || l == 0.f;
-  const int64_t at = row_offset(p, p.o_st, bi, hk, row);
-  for (int d = threadIdx.x; d < D; d += kThreads)
-    store_o<QT>(p.o, at + d, none ? 0.f : ((s_sum[0][d] + s_sum[1][d]) + (s_sum[2][d] + s_sum[3][d])) / l);
-  if (p.lse && threadIdx.x == 0)
-    p.lse[(static_cast<int64_t>(bi) * p.h_q + hk * p.group + row % p.group) * p.s_q + token] =
-        none ? -INFINITY : (m - p_off + __log2f(l)) * 0.6931471805599453f;
+    for (int e = 0; e < EL; e += 2)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at + lane * EL + e) =
+          none ? 0u : pack_pair<QT == kBF16>(x[e] * inv, x[e + 1] * inv);
+    if (p.lse && lane == 0) p.lse[lse_at] = lse_of(none, l);
+  } else {
+#pragma unroll
+    for (int e = 0; e < EL; ++e) s_sum[warp][lane * EL + e] = x[e];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (!on) return;
+    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+    const bool none = token >= L.len_q || l == 0.f;
+    for (int d = threadIdx.x; d < D; d += kThreads)
+      store_o<QT>(p.o, at + d, none ? 0.f : ((s_sum[0][d] + s_sum[1][d]) + (s_sum[2][d] + s_sum[3][d])) / l);
+    if (p.lse && threadIdx.x == 0) p.lse[lse_at] = lse_of(none, l);
+  }
+}
+
+template <int D, int QT>
+cudaError_t combine_t(const DecodeParams& p, float p_off, cudaStream_t st) {
+  // Blocks of 256 rows have few parts each: a warp a row; else four warps a row.
+  const int rows = p.rows < p.tile_rows ? p.rows : p.tile_rows, rpc = p.wide ? kWarps : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles * ((rows + rpc - 1) / rpc));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, p.wide ? decode_combine_kernel<D, QT, 1> : decode_combine_kernel<D, QT, kWarps>, p, p_off);
 }
 
 template <int D, int CT, int QT, int NR>
@@ -753,16 +661,7 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   kern<<<p.ctas, kThreads, C::SMEM, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles * (p.rows < p.tile_rows ? p.rows : p.tile_rows));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_combine_kernel<D, QT>, p, C::P_OFF);
+  return combine_t<D, QT>(p, C::P_OFF, st);
 }
 
 template <int D, int CT, int QT>
@@ -785,12 +684,15 @@ int ctas_of_sm(int tile_rows, bool e4m3) {
 }  // namespace
 
 void decode_plan(DecodeParams* p, int d, int ct, int num_sms) {
-  p->tile_rows = p->rows <= 8 ? 8 : 16;
+  p->wide = d <= 128 && p->rows > 16;
+  p->tile_rows = p->wide ? 256 : p->rows <= 8 ? 8 : 16;
   p->row_tiles = (p->rows + p->tile_rows - 1) / p->tile_rows;
+  p->tile_shift = p->wide ? 7 : 6;
   const bool e4 = ct == kE4M3;
-  const int per_sm = d == 64 ? ctas_of_sm<64>(p->tile_rows, e4) : d == 128 ? ctas_of_sm<128>(p->tile_rows, e4)
-                                                                           : ctas_of_sm<256>(p->tile_rows, e4);
-  const long long tiles = static_cast<long long>(p->c.b) * p->c.h_kv * p->row_tiles * ((p->c.max_len + kTile - 1ll) / kTile);
+  const int per_sm = p->wide ? 1 : d == 64 ? ctas_of_sm<64>(p->tile_rows, e4) : d == 128 ? ctas_of_sm<128>(p->tile_rows, e4)
+                                                                                         : ctas_of_sm<256>(p->tile_rows, e4);
+  const long long keys = 1ll << p->tile_shift;
+  const long long tiles = static_cast<long long>(p->c.b) * p->c.h_kv * p->row_tiles * ((p->c.max_len + keys - 1) / keys);
   const long long top = static_cast<long long>(per_sm) * num_sms;
   p->ctas = static_cast<int>(tiles < top ? tiles : top);
 }
@@ -799,6 +701,13 @@ size_t decode_workspace_bytes(const DecodeParams& p, int d, size_t* ml_offset) {
   const size_t parts = 2 * static_cast<size_t>(p.ctas) * p.tile_rows;
   if (ml_offset) *ml_offset = parts * d * 4;
   return (parts * d * 4 + parts * 8 + 255) & ~size_t(255);
+}
+
+cudaError_t launch_decode_combine(const DecodeParams& p, int d, int qt, int ct, cudaStream_t st) {
+  const float p_off = ct == kBF16 ? DecCfg<64, kBF16, 1>::P_OFF : DecCfg<64, kF16, 1>::P_OFF;
+  if (d == 64) return qt == kBF16 ? combine_t<64, kBF16>(p, p_off, st) : combine_t<64, kF16>(p, p_off, st);
+  if (d == 128) return qt == kBF16 ? combine_t<128, kBF16>(p, p_off, st) : combine_t<128, kF16>(p, p_off, st);
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_decode(const DecodeParams& p, int d, int qt, int ct, cudaStream_t st) {

@@ -1,0 +1,139 @@
+// sdpa_decode.cuh — what the kernels of attention over a cache share: the split of a batch into runs of
+// tiles, what a row sees, 16-bit packing.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "ptx.cuh"
+#include "sdpa_internal.h"
+
+namespace sdpa {
+
+using namespace ptx;
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two_codes), __NV_E4M3);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+  if constexpr (BF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+template <bool BF>
+__device__ __forceinline__ float2 unpack_pair(uint32_t w) {
+  if constexpr (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Clears the halves of a 16-bit pair that are infinite or NaN; `found` gathers whether any was.
+template <bool BF>
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w, bool& found) {
+  constexpr uint32_t kExp = BF ? 0x7F80u : 0x7C00u;
+  if ((w & kExp) == kExp) {
+    w &= 0xFFFF0000u;
+    found = true;
+  }
+  if ((w & (kExp << 16)) == (kExp << 16)) {
+    w &= 0x0000FFFFu;
+    found = true;
+  }
+  return w;
+}
+
+// ---- the batch as one row of tiles -----------------------------------------------------------
+
+struct SeqLens {
+  int len_q, len_kv;
+};
+
+__device__ __forceinline__ SeqLens seq_lens(const DecodeParams& p, int bi) {
+  SeqLens L;
+  L.len_q = p.seq_lens_q ? min(max(__ldg(p.seq_lens_q + bi), 0), p.s_q) : p.s_q;
+  L.len_kv = min(max(__ldg(p.c.seq_lens_kv + bi), 0), p.c.max_len);
+  return L;
+}
+
+// Tiles of one block of rows of sequence bi (none where no row takes part).
+__device__ __forceinline__ int seq_tiles(const DecodeParams& p, int bi) {
+  const SeqLens L = seq_lens(p, bi);
+  return L.len_q == 0 ? 0 : (L.len_kv + (1 << p.tile_shift) - 1) >> p.tile_shift;
+}
+
+// Sum of seq_tiles over sequences [0, n), by a whole warp.
+__device__ __forceinline__ long long tiles_before(const DecodeParams& p, int n, int lane) {
+  long long t = 0;
+  for (int i = lane; i < n; i += 32) t += seq_tiles(p, i);
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+
+// CTAs that have a run: no more than tiles, so that none of them is empty.
+__device__ __forceinline__ int working_ctas(const DecodeParams& p, long long total) {
+  return total < p.ctas ? static_cast<int>(total) : p.ctas;
+}
+
+// First tile of CTA c's run, and the CTA whose run holds tile t, of `total` tiles over g CTAs.
+__device__ __forceinline__ long long run_start(long long total, int c, int g) { return total * c / g; }
+__device__ __forceinline__ int cta_of(long long total, long long t, int g) {
+  return static_cast<int>(((t + 1) * g - 1) / total);
+}
+
+// Element offset of query row r (token r / group, head hk * group + r % group).
+__device__ __forceinline__ int64_t row_offset(const DecodeParams& p, const int64_t (&st)[3], int bi, int hk, int r) {
+  return bi * st[0] + (hk * p.group + r % p.group) * st[1] + (r / p.group) * st[2];
+}
+
+__device__ __forceinline__ bool tree_sees(const DecodeParams& p, int bi, int token, int j) {
+  const uint32_t* w = p.tree_mask + bi * p.tree_mask_stride + static_cast<int64_t>(token) * p.tree_words;
+  return (__ldg(w + j / 32) >> (j % 32)) & 1u;
+}
+
+// Whether query row r sees position `key` (< len_kv) of its sequence.
+__device__ __forceinline__ bool row_sees(const DecodeParams& p, int bi, const SeqLens& L, int token, int key) {
+  const int j = key - (L.len_kv - L.len_q);
+  if (p.causal) return j <= token;
+  if (p.tree_mask && j >= 0) return tree_sees(p, bi, token, j);
+  return true;
+}
+
+template <int DT>
+__device__ __forceinline__ void store_o(void* o, int64_t at, float x) {
+  static_cast<uint16_t*>(o)[at] = static_cast<uint16_t>(pack_pair<DT == kBF16>(x, 0.f) & 0xFFFFu);
+}
+
+// Infinities and NaNs of the drafted tokens' values: the products ran without them (a hidden
+// one times a weight of zero would be NaN); the rows that see them get them here.
+template <int D, int CT>
+__device__ __noinline__ float add_nonfinite(const DecodeParams& p, int bi, int hk, const SeqLens& L, int r, int d, int key0, int key1,
+                               float x) {
+  const int token = r / p.group;
+  // From the first tile that may hold a new token (all of it may have been cleared; a value added
+  // twice is still the same infinity or NaN).
+  for (int key = max(key0, (L.len_kv - L.len_q) & ~127); key < key1; ++key) {
+    if (!row_sees(p, bi, L, token, key)) continue;
+    const int page = __ldg(p.c.page_table + bi * p.c.page_table_stride + key / p.c.page_size);
+    if (page < 0 || page >= p.c.num_pages) continue;
+    const uint8_t* row = p.c.v + page * p.c.v_st[0] + hk * p.c.v_st[1] + (key % p.c.page_size) * p.c.v_st[2];
+    float v;
+    if (CT == kE4M3)
+      v = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_f16x2(row[d]) & 0xFFFFu))) *
+          __ldg(p.c.v_scale + (static_cast<int64_t>(page) * p.c.h_kv + hk) * p.c.page_size + key % p.c.page_size);
+    else
+      v = unpack_pair<CT == kBF16>(reinterpret_cast<const uint16_t*>(row)[d]).x;
+    if (!isfinite(v)) x += v;
+  }
+  return x;
+}
+
+}  // namespace sdpa

@@ -342,10 +342,24 @@ sdpa_status_t sdpa_decode(const sdpa_cache_t* c, const sdpa_decode_t* p, const v
   prm.part_o = static_cast<float*>(workspace);
   prm.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ml);
   if (sdpa::api_log_level() >= 1)
-    fprintf(stderr, "[sdpa] decode b=%d h_q=%d h_kv=%d s_q=%d d=%d dt=%d cache=%d page=%d ctas=%d ws=%zu\n", c->b, p->h_q,
-            c->h_kv, p->s_q, c->d, p->dtype, c->dtype, c->page_size, prm.ctas, need);
+    fprintf(stderr, "[sdpa] decode b=%d h_q=%d h_kv=%d s_q=%d d=%d dt=%d cache=%d page=%d block=%d ctas=%d ws=%zu\n", c->b, p->h_q,
+            c->h_kv, p->s_q, c->d, p->dtype, c->dtype, c->page_size, prm.tile_rows, prm.ctas, need);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  cudaError_t e = sdpa::launch_decode(prm, c->d, p->dtype, c->dtype, stream);
+  cudaError_t e;
+  if (prm.wide) {
+    CUtensorMap tm_k, tm_v;
+    const int box = sdpa::decode_wide_box(c->page_size);
+    const bool swizzle = c->dtype != SDPA_DTYPE_E4M3;
+    const sdpa_strides_t &ks = c->k_strides, &vs = c->v_strides;
+    SDPA_TRY(static_cast<sdpa_status_t>(sdpa::api_make_map(&tm_k, "k cache", c->k, {ks.b, ks.h, ks.s, ks.d}, c->num_pages,
+                                                           c->h_kv, c->page_size, c->d, c->dtype, box, swizzle)));
+    SDPA_TRY(static_cast<sdpa_status_t>(sdpa::api_make_map(&tm_v, "v cache", c->v, {vs.b, vs.h, vs.s, vs.d}, c->num_pages,
+                                                           c->h_kv, c->page_size, c->d, c->dtype, box, swizzle)));
+    e = sdpa::launch_decode_wide(prm, tm_k, tm_v, sdpa::api_wait_limit(), c->d, p->dtype, c->dtype, stream);
+    if (e == cudaSuccess) e = sdpa::launch_decode_combine(prm, c->d, p->dtype, c->dtype, stream);
+  } else {
+    e = sdpa::launch_decode(prm, c->d, p->dtype, c->dtype, stream);
+  }
   return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, "sdpa_decode"));
 }
 

@@ -258,7 +258,7 @@ def test_oracle_attention_is_dense_attention():
     rng = np.random.default_rng(1)
     kv = rng.normal(size=(2, 2, 1, 16, 4))
     q = rng.normal(size=(1, 1, 2, 4))
-    o, lse, _ = so.attend(q, kv[0], kv[1], None, None, np.array([[1, 0]]), (20,), None, 0.5, True)
+    o, lse = so.attend(q, kv[0], kv[1], None, None, np.array([[1, 0]]), (20,), None, 0.5, True)[:2]
     k = np.concatenate([kv[0][1, 0], kv[0][0, 0][:4]])
     v = np.concatenate([kv[1][1, 0], kv[1][0, 0][:4]])
     for r in range(2):

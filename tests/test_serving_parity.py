@@ -5,8 +5,8 @@ import torch
 
 from oracle import serving_oracle as so
 from sdpa_testlib import check_guard, f64, guarded_empty_like, lib
-from serving_testlib import (DT, HALF_STEP, TINY, assert_attend_close, make_cache, random_tree, randn, run_decode,
-                             values_of)
+from serving_testlib import (DT, HALF_STEP, TINY, assert_attend_close, kv_rounding, make_cache, random_tree, randn,
+                             run_decode, values_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -213,11 +213,12 @@ def test_pages_outside_the_cache_hold_nothing():
     k, v = torch.empty(2, 2, 64, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 2, 64, 128, dtype=torch.bfloat16, device="cuda")
     m.sdpa_cache_read(*c.where(), k, v)
     assert (k[0, :, 16:32] == 0).all() and (k[0, :, 48:] == 0).all() and (k[0, :, 32:48] != 0).any()
-    q = bshd(g, "bf16", 2, 4, 3, 128)
-    o, lse = run_decode(c, q)
-    kv, vv, _, _, table = c.np()
-    ref = so.attend(f64(q), kv, vv, None, None, table, (64, 40), None, 128 ** -0.5)
-    assert_attend_close(o, lse, ref, "bf16", "bf16")
+    for s in (3, 20):
+        q = bshd(g, "bf16", 2, 4, s, 128)
+        o, lse = run_decode(c, q)
+        kv, vv, _, _, table = c.np()
+        ref = so.attend(f64(q), kv, vv, None, None, table, (64, 40), None, 128 ** -0.5)
+        assert_attend_close(o, lse, ref, "bf16", "bf16")
 
 
 # ---- attention -------------------------------------------------------------------------------
@@ -237,6 +238,13 @@ ATTEND = [
     ((70,), None, 64, 16, 2, 128, 32, "bf16", "bf16", "tree", True),
     ((400, 130), None, 40, 4, 1, 256, 16, "e4m3", "f16", "tree", True),
     ((260,), None, 5, 12, 12, 256, 16, "f16", "f16", None, True),
+    # more than 16 rows a KV head
+    ((300, 0, 128, 1), (20, 20, 3, 20), 20, 2, 1, 128, 48, "e4m3", "bf16", "causal", True),
+    ((129, 500), None, 70, 12, 3, 128, 16, "f16", "f16", "tree", True),          # 280 rows: a block and 24 rows
+    ((257, 64, 33), (9, 0, 33), 33, 8, 1, 64, 64, "e4m3", "bf16", "tree", False),
+    ((1025, 40), None, 17, 1, 1, 64, 80, "bf16", "bf16", None, True),
+    ((384,), None, 3, 48, 2, 128, 128, "e4m3", "f16", None, True),
+    ((700, 690), None, 257, 1, 1, 128, 32, "bf16", "bf16", "causal", True),
 ]
 
 
@@ -249,10 +257,11 @@ def test_decode(lens, lens_q, s, h_q, h_kv, d, page, kind, dtype, mask, slot_maj
     o, lse = run_decode(c, q, lens_q=lens_q, causal="bottom_right" if mask == "causal" else False, tree=tree)
     kv, vv, ks, vs, table = c.np()
     ref = so.attend(f64(q), kv, vv, ks, vs, table, lens, lens_q, d ** -0.5, mask == "causal", tree)
-    assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16")
+    assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q // h_kv, d))
 
 
-@pytest.mark.parametrize("kind,d,h_q,s", [("bf16", 128, 8, 1), ("e4m3", 128, 8, 1), ("f16", 64, 4, 3), ("e4m3", 256, 2, 2)])
+@pytest.mark.parametrize("kind,d,h_q,s", [("bf16", 128, 8, 1), ("e4m3", 128, 8, 1), ("f16", 64, 4, 3), ("e4m3", 256, 2, 2),
+                                          ("e4m3", 128, 4, 5), ("bf16", 128, 1, 18), ("f16", 64, 2, 140)])
 def test_decode_long_ragged(kind, d, h_q, s):
     """Long and short sequences in one batch: blocks of rows split over many CTAs, and CTAs that hold several."""
     g = torch.Generator().manual_seed(13)
@@ -263,7 +272,7 @@ def test_decode_long_ragged(kind, d, h_q, s):
     o, lse = run_decode(c, q, causal="bottom_right" if s > 1 else False)
     kv, vv, ks, vs, table = c.np()
     ref = so.attend(f64(q), kv, vv, ks, vs, table, lens, None, d ** -0.5, s > 1)
-    assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16")
+    assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q, d))
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
@@ -274,11 +283,15 @@ def test_decode_peaked_scores(kind):
     q = bshd(g, dtype, 1, 4, 1, 128)
     c = make_cache((3001,), 1, 128, 16, kind, seed=16)
     kv, vv, ks, vs, table = c.np()
-    for scale in (1.0, -0.7, 0.0):
+    for scale, rows in ((1.0, 1), (-0.7, 1), (0.0, 1), (1.0, 5), (-0.7, 5), (0.0, 5)):
+        if rows > 1 and scale and kind == "e4m3":
+            continue      # K's rounding to F16 moves scores of 2^6 by more than the bound below: see test_decode
+        if rows > 1:
+            q = bshd(g, dtype, 1, 4, rows, 128)
         o, lse = run_decode(c, q, scale=scale)
         ref = so.attend(f64(q), kv, vv, ks, vs, table, (3001,), None, scale)
         # scores up to 2^6 now: their errors grow with the scale (eight times the default's bound)
-        O, L, spread = ref
+        O, L, spread = ref[:3]
         tol = (HALF_STEP["bf16" if kind == "bf16" else "f16"] + 2.0 ** -10) * spread + HALF_STEP[dtype] * np.abs(O) * 1.01 + TINY[dtype]
         assert (np.abs(f64(o) - O) <= tol).all()
         assert (np.abs(f64(lse) - L) <= 2.0 ** -10 + 2.0 ** -20 * np.abs(L)).all()
