@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
     }
     for (int i = 0; i < 6; ++i) {
       mbar_init(&bars.kv_full[i], E4 ? 128 : 1);
-      mbar_init(&bars.kv_empty[i], 1);
+      mbar_init(&bars.kv_empty[i], E4 ? 1 : 1 + 4);   // the MMAs that read the slot, and the clearing warps
       mbar_init(&bars.kv_clean[i], 128);
     }
     mbar_init(&bars.drain, 1);
@@ -484,35 +484,41 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
           }
         }
       } else {
+        // Every tile's phase is followed, and its slot returned, by these warps too: a parity says
+        // nothing about a phase that lies further back or ahead.
         for (int j = sg.tile0; ok && j < sg.tile1; ++j) {
-          if (needs_cleaning(p, sg, j)) {
-            const int v = it + 1, s = v % NS;
-            ok = mbar_wait_warp(&bars.kv_full[s], (v / NS) & 1, wt);
-            if (!ok) break;
-            const bool tail = masked && (j + 1) * kKeys > sg.off;
-            const int r = w4 * 32 + lane;
-            const bool on = j * kKeys + r < sg.L.len_kv;
-            if (!on || tail) {
 #pragma unroll 1
-              for (int u = 0; u < D / 8; ++u) {
-                uint4* at = reinterpret_cast<uint4*>(sRing + s * C::TILE + (u / 8) * 16384 + r * 128 + ((u % 8) ^ (r & 7)) * 16);
-                if (!on) {
-                  *at = make_uint4(0, 0, 0, 0);
-                } else {
-                  uint4 x = *at;
-                  x.x = finite_pair<BF>(x.x, found);
-                  x.y = finite_pair<BF>(x.y, found);
-                  x.z = finite_pair<BF>(x.z, found);
-                  x.w = finite_pair<BF>(x.w, found);
-                  *at = x;
+          for (int kv = 0; ok && kv < 2; ++kv, ++it) {
+            const int s = it % NS;
+            ok = mbar_wait_warp(&bars.kv_full[s], (it / NS) & 1, wt);
+            if (!ok) break;
+            if (kv && needs_cleaning(p, sg, j)) {
+              const bool tail = masked && (j + 1) * kKeys > sg.off;
+              const int r = w4 * 32 + lane;
+              const bool on = j * kKeys + r < sg.L.len_kv;
+              if (!on || tail) {
+#pragma unroll 1
+                for (int u = 0; u < D / 8; ++u) {
+                  uint4* at = reinterpret_cast<uint4*>(sRing + s * C::TILE + (u / 8) * 16384 + r * 128 + ((u % 8) ^ (r & 7)) * 16);
+                  if (!on) {
+                    *at = make_uint4(0, 0, 0, 0);
+                  } else {
+                    uint4 x = *at;
+                    x.x = finite_pair<BF>(x.x, found);
+                    x.y = finite_pair<BF>(x.y, found);
+                    x.z = finite_pair<BF>(x.z, found);
+                    x.w = finite_pair<BF>(x.w, found);
+                    *at = x;
+                  }
                 }
               }
+              if (found) s_found[n_seg % 8] = n_seg + 1;
+              fence_proxy_async_smem();
+              mbar_arrive(&bars.kv_clean[s]);
             }
-            if (found) s_found[n_seg % 8] = n_seg + 1;
-            fence_proxy_async_smem();
-            mbar_arrive(&bars.kv_clean[s]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.kv_empty[s]);
           }
-          it += 2;
         }
       }
       ++n_seg;

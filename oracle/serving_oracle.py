@@ -68,13 +68,13 @@ def slots(page_table, page_size, num_pages, lens_kv, lens_q, s):
 def dense(values, scales, page_table, i, n):
     """Positions 0..n-1 of sequence i as [h, n, d] in fp64, and which of them exist."""
     pages, h, ps, d = values.shape
-    out, live = np.zeros((h, n, d)), np.zeros(n, dtype=bool)
-    for j in range(n):
-        page = page_table[i, j // ps]
-        if 0 <= page < pages:
-            out[:, j] = values[page, :, j % ps] * (1.0 if scales is None else scales[page, :, j % ps, None])
-            live[j] = True
-    return out, live
+    at = np.arange(n)
+    page = page_table[i, at // ps]
+    live = (page >= 0) & (page < pages)
+    x = values[np.where(live, page, 0), :, at % ps]                    # [n, h, d]
+    if scales is not None:
+        x = x * scales[np.where(live, page, 0), :, at % ps][..., None]
+    return np.where(live[:, None, None], x, 0.0).transpose(1, 0, 2), live
 
 
 def attend(q, k_values, v_values, k_scales, v_scales, page_table, lens_kv, lens_q, scale, causal=False, tree=None):

@@ -275,6 +275,21 @@ def test_decode_long_ragged(kind, d, h_q, s):
     assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q, d))
 
 
+@pytest.mark.parametrize("kind,s,h_q", [("bf16", 1, 8), ("bf16", 17, 8), ("e4m3", 17, 8), ("e4m3", 3, 64)])
+def test_decode_many_tiles_a_cta(kind, s, h_q):
+    """Runs of many tiles, so that every ring wraps often; what lies behind each sequence is NaN."""
+    g, d, h_kv = torch.Generator().manual_seed(31), 128, 8
+    lens = tuple(2500 + 61 * i for i in range(12))
+    c = make_cache(lens, h_kv, d, 48, kind, seed=32)
+    q = bshd(g, "bf16", len(lens), h_q, s, d)
+    o, lse = run_decode(c, q, causal="bottom_right")
+    again, _ = run_decode(c, q, causal="bottom_right")
+    assert torch.equal(o, again)
+    kv, vv, ks, vs, table = c.np()
+    ref = so.attend(f64(q), kv, vv, ks, vs, table, lens, None, d ** -0.5, True)
+    assert_attend_close(o, lse, ref, "bf16", "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q // h_kv, d))
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
 def test_decode_peaked_scores(kind):
     """One key far above the rest, late in a long context; scales that make scores large; a negative scale."""
