@@ -529,8 +529,7 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
         w.y = pack_pair<QT == kBF16>(x.z * inv, x.w * inv);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row_offset(p, p.o_st, bi, hk, row) + d) = w;
         if (p.lse && d == 0)
-          p.lse[(static_cast<int64_t>(bi) * p.h_q + hk * p.group + row % p.group) * p.s_q + token] =
-              none ? -INFINITY : (mb - C::P_OFF + __log2f(lb)) * 0.6931471805599453f;
+          p.lse[lse_offset(p, bi, hk, row)] = none ? -INFINITY : natural_lse(mb - C::P_OFF, lb);
       }
     }
     __syncthreads();   // the ring and the exchange arrays are free again
@@ -539,117 +538,67 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
 }
 
 // Joins the partial results of every block of rows that more than one CTA worked on, and writes
-// the rows that no key reaches.  WG warps share a row: its lanes weigh the parts side by side (a
-// part is a maximum, a sum and d values), then each warp adds up every WG-th part, 8 loads in
-// flight, and the sums meet.  The order is that of the parts, so results do not change between calls.
-template <int D, int QT, int WG>
+// the rows that no key reaches.  One CTA a row: its lanes weigh the parts side by side (a part is
+// a maximum, a sum and d values), then each warp adds up every fourth part, 8 loads in flight,
+// and the four sums meet.  The order is that of the parts, so results do not change between calls.
+template <int D, int QT>
 __global__ void __launch_bounds__(kThreads) decode_combine_kernel(const __grid_constant__ DecodeParams p, float p_off) {
   constexpr int EL = D / 32;          // elements a lane owns
-  constexpr int RPC = kWarps / WG;    // rows of a CTA
   __shared__ float s_sum[kWarps][D];
   __shared__ float s_l[kWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int sub = warp % WG;
-  const int per_unit = (min(p.rows, p.tile_rows) + RPC - 1) / RPC;
-  const int per_seq = p.c.h_kv * p.row_tiles;
-  const int unit = blockIdx.x / per_unit, r = blockIdx.x % per_unit * RPC + warp / WG;
-  const int bi = unit / per_seq, blk = unit % per_seq;
-  const int hk = blk / p.row_tiles, row = blk % p.row_tiles * p.tile_rows + r, token = row / p.group;
-  const int n_tiles = seq_tiles(p, bi);
-  const SeqLens L = seq_lens(p, bi);
-  int c0 = 0, n = 0;                  // parts: CTAs c0 .. c0 + n - 1 (none where there are no tiles)
-  if (n_tiles > 0) {
-    const long long total = tiles_before(p, p.c.b, lane) * per_seq;
-    const long long t0 = tiles_before(p, bi, lane) * per_seq + static_cast<long long>(blk) * n_tiles;
-    c0 = cta_of(total, t0, working_ctas(p, total));
-    n = cta_of(total, t0 + n_tiles - 1, working_ctas(p, total)) - c0 + 1;
-  }
+  const int per_unit = min(p.rows, p.tile_rows);
+  const Parts u = find_parts(p, blockIdx.x / per_unit, lane);
+  const int r = blockIdx.x % per_unit, row = u.r0 + r, token = row / p.group;
   griddep_wait();   // (by every CTA, so that this grid never ends before the one it follows)
-  if (n == 1) return;                        // finished by that CTA
-  const bool on = r < p.tile_rows && row < p.rows;
-  // Part k: the first holds its block's first tile and is that CTA's second part.
-  auto part = [&](int k) { return static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)) * p.tile_rows + r; };
+  if (u.n == 1 || row >= p.rows) return;     // finished by that CTA
   float m = -INFINITY;
+  for (int k = lane; k < u.n; k += 32) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (u.part(k) * p.tile_rows + r));
+    if (ml.y != 0.f) m = fmaxf(m, ml.x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float x[EL], l = 0.f;
 #pragma unroll
   for (int e = 0; e < EL; ++e) x[e] = 0.f;
-  if (on) {
-    for (int k = lane; k < n; k += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * part(k));
-      if (ml.y != 0.f) m = fmaxf(m, ml.x);
-    }
+  for (int k0 = warp; k0 < u.n; k0 += 8 * kWarps) {
+    float f[8], v[8][EL];
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int k0 = sub; k0 < n; k0 += 8 * WG) {
-      float f[8], v[8][EL];
+    for (int i = 0; i < 8; ++i) {
+      const int k = k0 + i * kWarps;
+      f[i] = 0.f;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int k = k0 + u * WG;
-        f[u] = 0.f;
+      for (int e = 0; e < EL; ++e) v[i][e] = 0.f;
+      if (k < u.n) {
+        const int64_t at = u.part(k) * p.tile_rows + r;
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
+        const float* src = p.part_o + at * D + lane * EL;
 #pragma unroll
-        for (int e = 0; e < EL; ++e) v[u][e] = 0.f;
-        if (k < n) {
-          const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * part(k));
-          const float* src = p.part_o + part(k) * D + lane * EL;
-#pragma unroll
-          for (int e = 0; e < EL; e += 2) {
-            const float2 w = *reinterpret_cast<const float2*>(src + e);
-            v[u][e] = w.x;
-            v[u][e + 1] = w.y;
-          }
-          // A part without a visible key has sum 0 and weighs nothing.  (All sums NaN: m stays -inf.)
-          if (ml.y != 0.f) {
-            f[u] = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
-            l += ml.y * f[u];
-          }
+        for (int e = 0; e < EL; e += 2) {
+          const float2 w = *reinterpret_cast<const float2*>(src + e);
+          v[i][e] = w.x;
+          v[i][e + 1] = w.y;
         }
+        f[i] = part_weight(ml, m);
+        l += ml.y * f[i];
       }
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-#pragma unroll
-        for (int e = 0; e < EL; ++e) x[e] += f[u] == 0.f ? 0.f : v[u][e] * f[u];
     }
-  }
-  const int64_t at = on ? row_offset(p, p.o_st, bi, hk, row) : 0;
-  const int64_t lse_at = (static_cast<int64_t>(bi) * p.h_q + hk * p.group + row % p.group) * p.s_q + token;
-  auto lse_of = [&](bool none, float sum) { return none ? -INFINITY : (m - p_off + __log2f(sum)) * 0.6931471805599453f; };
-  if constexpr (WG == 1) {
-    if (!on) return;
-    const bool none = token >= L.len_q || l == 0.f;
-    const float inv = none ? 0.f : 1.f / l;
 #pragma unroll
-    for (int e = 0; e < EL; e += 2)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at + lane * EL + e) =
-          none ? 0u : pack_pair<QT == kBF16>(x[e] * inv, x[e + 1] * inv);
-    if (p.lse && lane == 0) p.lse[lse_at] = lse_of(none, l);
-  } else {
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int e = 0; e < EL; ++e) s_sum[warp][lane * EL + e] = x[e];
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    if (!on) return;
-    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-    const bool none = token >= L.len_q || l == 0.f;
-    for (int d = threadIdx.x; d < D; d += kThreads)
-      store_o<QT>(p.o, at + d, none ? 0.f : ((s_sum[0][d] + s_sum[1][d]) + (s_sum[2][d] + s_sum[3][d])) / l);
-    if (p.lse && threadIdx.x == 0) p.lse[lse_at] = lse_of(none, l);
+      for (int e = 0; e < EL; ++e) x[e] += f[i] == 0.f ? 0.f : v[i][e] * f[i];
   }
-}
-
-template <int D, int QT>
-cudaError_t combine_t(const DecodeParams& p, float p_off, cudaStream_t st) {
-  // Blocks of 256 rows have few parts each: a warp a row; else four warps a row.
-  const int rows = p.rows < p.tile_rows ? p.rows : p.tile_rows, rpc = p.wide ? kWarps : 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles * ((rows + rpc - 1) / rpc));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, p.wide ? decode_combine_kernel<D, QT, 1> : decode_combine_kernel<D, QT, kWarps>, p, p_off);
+#pragma unroll
+  for (int e = 0; e < EL; ++e) s_sum[warp][lane * EL + e] = x[e];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  const bool none = token >= u.L.len_q || l == 0.f;
+  const int64_t at = row_offset(p, p.o_st, u.bi, u.hk, row);
+  for (int d = threadIdx.x; d < D; d += kThreads)
+    store_o<QT>(p.o, at + d, none ? 0.f : ((s_sum[0][d] + s_sum[1][d]) + (s_sum[2][d] + s_sum[3][d])) / l);
+  if (p.lse && threadIdx.x == 0) p.lse[lse_offset(p, u.bi, u.hk, row)] = none ? -INFINITY : natural_lse(m - p_off, l);
 }
 
 template <int D, int CT, int QT, int NR>
@@ -661,7 +610,9 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   kern<<<p.ctas, kThreads, C::SMEM, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return combine_t<D, QT>(p, C::P_OFF, st);
+  return launch_after(decode_combine_kernel<D, QT>,
+                      dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles * (p.rows < p.tile_rows ? p.rows : p.tile_rows)),
+                      dim3(kThreads), st, p, C::P_OFF);
 }
 
 template <int D, int CT, int QT>
@@ -701,13 +652,6 @@ size_t decode_workspace_bytes(const DecodeParams& p, int d, size_t* ml_offset) {
   const size_t parts = 2 * static_cast<size_t>(p.ctas) * p.tile_rows;
   if (ml_offset) *ml_offset = parts * d * 4;
   return (parts * d * 4 + parts * 8 + 255) & ~size_t(255);
-}
-
-cudaError_t launch_decode_combine(const DecodeParams& p, int d, int qt, int ct, cudaStream_t st) {
-  const float p_off = ct == kBF16 ? DecCfg<64, kBF16, 1>::P_OFF : DecCfg<64, kF16, 1>::P_OFF;
-  if (d == 64) return qt == kBF16 ? combine_t<64, kBF16>(p, p_off, st) : combine_t<64, kF16>(p, p_off, st);
-  if (d == 128) return qt == kBF16 ? combine_t<128, kBF16>(p, p_off, st) : combine_t<128, kF16>(p, p_off, st);
-  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_decode(const DecodeParams& p, int d, int qt, int ct, cudaStream_t st) {

@@ -107,6 +107,12 @@ __device__ __forceinline__ bool row_sees(const DecodeParams& p, int bi, const Se
   return true;
 }
 
+// Element of lse [b][h_q][s_q], and its value for a maximum m (log2 units) and a sum of 2^(x - m).
+__device__ __forceinline__ int64_t lse_offset(const DecodeParams& p, int bi, int hk, int r) {
+  return (static_cast<int64_t>(bi) * p.h_q + hk * p.group + r % p.group) * p.s_q + r / p.group;
+}
+__device__ __forceinline__ float natural_lse(float m, float l) { return (m + __log2f(l)) * 0.6931471805599453f; }
+
 template <int DT>
 __device__ __forceinline__ void store_o(void* o, int64_t at, float x) {
   static_cast<uint16_t*>(o)[at] = static_cast<uint16_t>(pack_pair<DT == kBF16>(x, 0.f) & 0xFFFFu);
@@ -134,6 +140,57 @@ __device__ __noinline__ float add_nonfinite(const DecodeParams& p, int bi, int h
     if (!isfinite(v)) x += v;
   }
   return x;
+}
+
+// ---- joining partial results ---------------------------------------------------------------------
+
+// The parts of one block of rows: CTAs c0 .. c0 + n - 1 of the launch (n = 0: no key reaches it).
+struct Parts {
+  int bi, hk, r0, c0, n;
+  SeqLens L;
+  // Part k among [2 * ctas]: the first holds the block's first tile and is that CTA's second part.
+  __device__ __forceinline__ int64_t part(int k) const { return 2 * (c0 + k) + (k == 0 ? 1 : 0); }
+};
+
+// By a whole warp.
+__device__ __forceinline__ Parts find_parts(const DecodeParams& p, int unit, int lane) {
+  Parts u;
+  const int per_seq = p.c.h_kv * p.row_tiles, blk = unit % per_seq;
+  u.bi = unit / per_seq;
+  u.hk = blk / p.row_tiles;
+  u.r0 = blk % p.row_tiles * p.tile_rows;
+  u.L = seq_lens(p, u.bi);
+  u.c0 = u.n = 0;
+  const int n_tiles = seq_tiles(p, u.bi);
+  if (n_tiles > 0) {
+    const long long total = tiles_before(p, p.c.b, lane) * per_seq;
+    const long long t0 = tiles_before(p, u.bi, lane) * per_seq + static_cast<long long>(blk) * n_tiles;
+    const int g = working_ctas(p, total);
+    u.c0 = cta_of(total, t0, g);
+    u.n = cta_of(total, t0 + n_tiles - 1, g) - u.c0 + 1;
+  }
+  return u;
+}
+
+// Weight of a part (its maximum, its sum) under the common maximum m.  A part without a visible
+// key has sum 0 and weighs nothing; where all sums are NaN, m stays -inf and they stay NaN.
+__device__ __forceinline__ float part_weight(float2 ml, float m) {
+  return ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
+}
+
+// Launches a kernel that may start while the one ahead of it on the stream finishes.
+template <typename... A, typename... B>
+cudaError_t launch_after(void (*kern)(A...), dim3 grid, dim3 block, cudaStream_t st, B... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 }  // namespace sdpa

@@ -9,10 +9,10 @@
 //   warp 1       MMA issuer: S = Q K^T into TMEM, O += P V with P read from TMEM.
 //   warps 4-11   two softmax warpgroups, one for each 128-row tile; thread r owns row r: loads it
 //                into shared memory, the running max and sum, P, and the segment's results.
-//   warps 12-15  E4M3 caches: every tile is widened to F16 on its way from the TMA's stage to the
-//                ring; 16-bit caches: only V tiles that end behind the sequence or hold drafted
-//                tokens are touched (rows that do not exist and values that are not finite are
-//                cleared: a weight of zero does not hide a NaN in a product).
+//   warps 12-15  E4M3 caches: widen K to F16 on its way from the TMA's stage to the ring (and warps
+//                16-19 V); 16-bit caches: clear, in V tiles that end behind the sequence or hold
+//                drafted tokens, rows that do not exist and values that are not finite (a weight of
+//                zero does not hide a NaN in a product).
 //
 // E4M3: a tile's codes are multiplied by scale / 2^E (E: the exponent of the tile's largest scale)
 // as a sum of two F16 factors, so one rounding to F16's 11 bits is left, whatever the scales; 2^E
@@ -25,13 +25,16 @@
 namespace sdpa {
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int kKeys = 128;
 constexpr int kLog2Keys = 7;
 
 template <int D, int CT>
 struct WideCfg {
   static constexpr bool E4 = CT == kE4M3;
+  static constexpr int THREADS = E4 ? 640 : 512;
+  // Registers of the producer's, the softmax and the widening or clearing warpgroups, out of 96
+  // (E4M3) or 128 a thread at launch: 64 + 2 x 152 + 2 x 56 = 5 x 96, 64 + 2 x 184 + 80 = 4 x 128.
+  static constexpr int REGS0 = 64, REGS_SOFTMAX = E4 ? 152 : 184, REGS_WIDEN = E4 ? 56 : 80;
   static constexpr int TILE = 128 * D * 2;                // a 16-bit tile of 128 rows
   static constexpr int RAW = E4 ? 128 * D : 0;            // an E4M3 tile as loaded
   static constexpr int NCHUNK = D / 64;                   // 128-byte columns of a 16-bit tile
@@ -119,7 +122,7 @@ struct WideParams {
 };
 
 template <int D, int CT, int QT>
-__global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_constant__ WideParams wp) {
+__global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel(const __grid_constant__ WideParams wp) {
   using C = WideCfg<D, CT>;
   constexpr bool E4 = C::E4;
   constexpr bool BF = CT == kBF16;     // type of the products' operands
@@ -214,9 +217,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
   bool producer = false;
   int kv_issued = 0;     // tiles whose copies the producer issued
 
-  // Registers (512 threads, 128 each at launch): 64 + 80 + 2 x 184 = 4 x 128.
   if (warp < 4) {
-    regs_dec<64>();
+    regs_dec<C::REGS0>();
     if (warp == 0) {
       // ================================ pages and TMA =====================================
       producer = lane == 0;
@@ -367,121 +369,133 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
       }
     }
   } else if (warp >= 12) {
-    regs_dec<80>();
+    regs_dec<C::REGS_WIDEN>();
     // ============================ widening / clearing =========================================
-    const int w4 = warp - 12;
+    const int w4 = warp % 4;
     const bool masked = p.causal != 0 || p.tree_mask != nullptr;
     bool ok = true;
     int it = 0, n_seg = 0, n_tile = 0;
     while (ok && walk.next(p, sg)) {
       bool found = false;
       if constexpr (E4) {
+        // Tiles of K (warps 12-15) or of V (16-19).  Scales of a tile: the lane's own row
+        // (32 w4 + lane), and four of the 128 for the largest; K's warps find both exponents.
+        const bool is_v = warp >= 16;
         const int32_t* pages = p.c.page_table + sg.bi * p.c.page_table_stride;
-        // Scales of a tile: lane's own row (32 w4 + lane), and four of the 128 for the maximum.
-        struct Scales {
-          float own[2];
-          float4 four[2];
-          bool on_own;
-          int left;         // existing keys from this lane's first of four on
+        const int ps = p.c.page_size, col_step = kKeys / ps, slot_step = kKeys % ps;
+        struct Spot {      // a key of this lane, moving tile by tile
+          int key, col, slot;
         };
-        auto page_at = [&](int key) -> int {
-          if (key >= sg.L.len_kv) return -1;
-          const int pg = __ldg(pages + key / p.c.page_size);
+        auto spot_at = [&](int key) { return Spot{key, key / ps, key % ps}; };
+        auto step = [&](Spot& x) {
+          x.key += kKeys;
+          x.col += col_step;
+          x.slot += slot_step;
+          if (x.slot >= ps) {
+            x.slot -= ps;
+            ++x.col;
+          }
+        };
+        auto page_at = [&](const Spot& x) -> int {
+          if (x.key >= min(sg.tile1 * kKeys, sg.L.len_kv)) return -1;
+          const int pg = __ldg(pages + x.col);
           return pg < p.c.num_pages ? pg : -1;
         };
-        auto fetch = [&](int j, int pg_own, int pg_four) {
-          Scales s;
-          const int own = j * kKeys + w4 * 32 + lane, four = j * kKeys + lane * 4;
-          s.on_own = pg_own >= 0;
-          s.left = pg_four >= 0 ? sg.L.len_kv - four : 0;
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const float* base = kv ? p.c.v_scale : p.c.k_scale;
-            s.own[kv] = 0.f;
-            s.four[kv] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (pg_own >= 0)
-              s.own[kv] = __ldg(base + (static_cast<int64_t>(pg_own) * p.c.h_kv + sg.hk) * p.c.page_size + own % p.c.page_size);
-            if (pg_four >= 0)
-              s.four[kv] = __ldg(reinterpret_cast<const float4*>(
-                  base + (static_cast<int64_t>(pg_four) * p.c.h_kv + sg.hk) * p.c.page_size + four % p.c.page_size));
-          }
-          return s;
+        auto scale_at = [&](const Spot& x, int pg) {
+          return (static_cast<int64_t>(pg) * p.c.h_kv + sg.hk) * ps + x.slot;
         };
-        Scales nxt = fetch(sg.tile0, page_at(sg.tile0 * kKeys + w4 * 32 + lane), page_at(sg.tile0 * kKeys + lane * 4));
-        int pg_own = -1, pg_four = -1;
-        if (sg.tile0 + 1 < sg.tile1) {
-          pg_own = page_at((sg.tile0 + 1) * kKeys + w4 * 32 + lane);
-          pg_four = page_at((sg.tile0 + 1) * kKeys + lane * 4);
-        }
+        const float4 kZero4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        float nxt_own = 0.f;
+        float4 nxt_k = kZero4, nxt_v = kZero4;
+        bool nxt_on = false;
+        int nxt_left = 0;
+        auto fetch = [&](const Spot& own, int pg_own, const Spot& four, int pg_four) {
+          nxt_on = pg_own >= 0;
+          nxt_left = pg_four >= 0 ? sg.L.len_kv - four.key : 0;
+          nxt_own = 0.f;
+          nxt_k = nxt_v = kZero4;
+          if (pg_own >= 0) nxt_own = __ldg((is_v ? p.c.v_scale : p.c.k_scale) + scale_at(own, pg_own));
+          if (pg_four >= 0) {
+            if (!is_v) nxt_k = __ldg(reinterpret_cast<const float4*>(p.c.k_scale + scale_at(four, pg_four)));
+            nxt_v = __ldg(reinterpret_cast<const float4*>(p.c.v_scale + scale_at(four, pg_four)));
+          }
+        };
+        Spot own = spot_at(sg.tile0 * kKeys + w4 * 32 + lane), four = spot_at(sg.tile0 * kKeys + lane * 4);
+        fetch(own, page_at(own), four, page_at(four));
+        step(own);
+        step(four);
+        int pg_own = page_at(own), pg_four = page_at(four);     // of tile j + 1
         for (int j = sg.tile0; ok && j < sg.tile1; ++j) {
-          const Scales cur = nxt;
-          if (j + 1 < sg.tile1) nxt = fetch(j + 1, pg_own, pg_four);
-          if (j + 2 < sg.tile1) {
-            pg_own = page_at((j + 2) * kKeys + w4 * 32 + lane);
-            pg_four = page_at((j + 2) * kKeys + lane * 4);
-          }
-          int ex[2];
-          uint32_t fh[2], fl[2];      // scale / 2^E of the lane's own row as two F16, each twice in a word
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const float4 f = cur.four[kv];
-            uint32_t m = max(max(scale_bits(f.x, cur.left > 0), scale_bits(f.y, cur.left > 1)),
-                             max(scale_bits(f.z, cur.left > 2), scale_bits(f.w, cur.left > 3)));
-            m = __reduce_max_sync(0xffffffffu, m);
-            ex[kv] = exponent_of(m);
-            const float s = cur.on_own ? cur.own[kv] * pow2(-ex[kv]) : 0.f;
-            const __half h = __float2half_rn(s);
-            const __half l = __float2half_rn(s - __half2float(h));
-            fh[kv] = __half_as_ushort(h) * 0x10001u;
-            fl[kv] = __half_as_ushort(l) * 0x10001u;
-          }
+          const float cur = nxt_own;
+          const float4 cur_k = nxt_k, cur_v = nxt_v;
+          const bool on = nxt_on;
+          const int left = nxt_left;
+          fetch(own, pg_own, four, pg_four);
+          step(own);
+          step(four);
+          pg_own = page_at(own);
+          pg_four = page_at(four);
+          auto largest = [&](const float4& f) {
+            return exponent_of(__reduce_max_sync(0xffffffffu, max(max(scale_bits(f.x, left > 0), scale_bits(f.y, left > 1)),
+                                                                  max(scale_bits(f.z, left > 2), scale_bits(f.w, left > 3)))));
+          };
+          const int ev = largest(cur_v), ex = is_v ? ev : largest(cur_k);
           if (threadIdx.x == 12 * 32) {
-            s_ek[n_tile % 8] = ex[0];
-            s_ev[n_tile % 8] = ex[1];
+            s_ek[n_tile % 8] = ex;
+            s_ev[n_tile % 8] = ev;
           }
           ++n_tile;
-          const bool tail = masked && (j + 1) * kKeys > sg.off;
-          const int rows_on = min(max(sg.L.len_kv - j * kKeys - w4 * 32, 0), 32);
-#pragma unroll 1
-          for (int kv = 0; ok && kv < 2; ++kv) {
-            const int rs = it % C::NRAW, s = it % NS;
-            ok = mbar_wait_warp(&bars.raw_full[rs], (it / C::NRAW) & 1, wt) &&
-                 mbar_wait_warp(&bars.kv_empty[s], ((it / NS) & 1) ^ 1, wt);
-            if (!ok) break;
-            // A lane takes 8 codes at a time: rows of D / 8 lanes, 256 bytes of codes a warp.
-            constexpr int LR = D / 8, RI = 32 / LR;      // lanes of a row, rows of an instruction
-            const uint8_t* src = sRaw + rs * C::RAW + w4 * 32 * D + lane * 8;
-            uint8_t* dst = sRing + s * C::TILE;
-            const int u = lane % LR;                      // 16-byte unit of the 16-bit row
-            const uint32_t my_h = kv ? fh[1] : fh[0], my_l = kv ? fl[1] : fl[0];
-#pragma unroll 4
-            for (int i = 0; i < 32 / RI; ++i) {
-              const int lr = i * RI + lane / LR, r = w4 * 32 + lr;
-              const uint2 in = *reinterpret_cast<const uint2*>(src + i * 256);
-              const uint32_t h = __shfl_sync(0xffffffffu, my_h, lr), l = __shfl_sync(0xffffffffu, my_l, lr);
-              const __half2 h2 = *reinterpret_cast<const __half2*>(&h), l2 = *reinterpret_cast<const __half2*>(&l);
-              uint32_t out[4] = {e4m3x2_to_f16x2(in.x & 0xFFFFu), e4m3x2_to_f16x2(in.x >> 16),
-                                 e4m3x2_to_f16x2(in.y & 0xFFFFu), e4m3x2_to_f16x2(in.y >> 16)};
+          // scale / 2^E of the lane's row as two F16, each twice in a word
+          const float f = on ? cur * pow2(-ex) : 0.f;
+          const __half fh = __float2half_rn(f), fl = __float2half_rn(f - __half2float(fh));
+          const __half2 h2 = __half2half2(fh), l2 = __half2half2(fl);
+          const bool tail = is_v && masked && (j + 1) * kKeys > sg.off;
+          const int mine = it + (is_v ? 1 : 0);
+          it += 2;
+          const int rs = mine % C::NRAW, s = mine % NS;
+          ok = mbar_wait_warp(&bars.raw_full[rs], (mine / C::NRAW) & 1, wt) &&
+               mbar_wait_warp(&bars.kv_empty[s], ((mine / NS) & 1) ^ 1, wt);
+          if (!ok) break;
+          // A lane takes its row, 16 codes at a time; the swizzles of both tiles put the 8 rows
+          // of a quarter-warp into 8 different 16-byte columns.
+          const int r = w4 * 32 + lane, sw = D == 128 ? r & 7 : (r >> 1) & 3;
+          const uint8_t* src = sRaw + rs * C::RAW + r * D;
+          uint8_t* dst = sRing + s * C::TILE + r * 128;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __half2 x = *reinterpret_cast<const __half2*>(&out[e]);
-                const __half2 y = __hfma2(x, h2, __hmul2(x, l2));
+          for (int c0 = 0; c0 < D / 16; c0 += 4) {
+            uint4 in[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              in[x] = *reinterpret_cast<const uint4*>(src + ((c0 + x) ^ sw) * 16);
+              if (!on) in[x] = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+              uint32_t out[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                out[e] = e4m3x2_to_f16x2(e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
+                const __half2 v = *reinterpret_cast<const __half2*>(&out[e]);
+                const __half2 y = __hfma2(v, h2, __hmul2(v, l2));
                 out[e] = *reinterpret_cast<const uint32_t*>(&y);
               }
-              if (kv && lr >= rows_on) out[0] = out[1] = out[2] = out[3] = 0u;
-              if (kv && tail) {
+              if (tail) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) out[e] = finite_pair<false>(out[e], found);
+                for (int e = 0; e < 8; ++e) out[e] = finite_pair<false>(out[e], found);
               }
-              *reinterpret_cast<uint4*>(dst + (u / 8) * 16384 + r * 128 + ((u % 8) ^ (r & 7)) * 16) =
-                  make_uint4(out[0], out[1], out[2], out[3]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int u = 2 * (c0 + x) + h;    // 16-byte unit of the 16-bit row
+                *reinterpret_cast<uint4*>(dst + (u / 8) * 16384 + ((u % 8) ^ (r & 7)) * 16) =
+                    make_uint4(out[4 * h], out[4 * h + 1], out[4 * h + 2], out[4 * h + 3]);
+              }
             }
-            if (kv && found) s_found[n_seg % 8] = n_seg + 1;
-            fence_proxy_async_smem();
-            mbar_arrive(&bars.kv_full[s]);
-            mbar_arrive(&bars.raw_empty[rs]);
-            ++it;
           }
+          if (found) s_found[n_seg % 8] = n_seg + 1;
+          fence_proxy_async_smem();
+          mbar_arrive(&bars.kv_full[s]);
+          mbar_arrive(&bars.raw_empty[rs]);
         }
       } else {
         // Every tile's phase is followed, and its slot returned, by these warps too: a parity says
@@ -524,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
       ++n_seg;
     }
   } else {
-    regs_inc<184>();
+    regs_inc<C::REGS_SOFTMAX>();
     // ============================ softmax, results ==============================================
     const int t = (warp - 4) / 4, quad = warp % 4;
     const int r = quad * 32 + lane;
@@ -534,19 +548,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
     bool ok = true;
     int n_seg = 0, n_tile = 0;
     uint32_t blk = 0, on = 0;      // blocks and segments of this tile so far
-    while (ok && walk.next(p, sg)) {
-      const int n_blk = sg.tile1 - sg.tile0;
-      if (t == 1 && p.rows - sg.r0 <= 128) {   // no rows for the second tile
-        n_tile += n_blk;
-        ++n_seg;
-        continue;
+    // Segments that have rows for this tile; the blocks and segments passed over are counted.
+    auto advance = [&](Segment& to, int& tiles, int& segs) {
+      tiles = segs = 0;
+      while (walk.next(p, to)) {
+        if (t == 0 || p.rows - to.r0 > 128) return true;
+        tiles += to.tile1 - to.tile0;
+        ++segs;
       }
-      const int row = sg.r0 + t * 128 + r, token = row / p.group;
-      const bool live = row < p.rows && token < sg.L.len_q;
-      // ---- Q: this thread's row (the last S of the segment before has been read) -------------------
+      return false;
+    };
+    // This thread's row of Q of a segment to shared memory; returns the factor on its scores.  To
+    // be called when the last S of the segment before has been read.
+    auto load_q = [&](const Segment& g) -> float {
+      const int row = g.r0 + t * 128 + r;
+      const bool live = row < p.rows && row / p.group < g.L.len_q;
       float cs = wp.abs_scale_log2;
       {
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (live ? row_offset(p, p.q_st, sg.bi, sg.hk, row) : 0);
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (live ? row_offset(p, p.q_st, g.bi, g.hk, row) : 0);
         uint4 x[D / 8];
 #pragma unroll
         for (int u = 0; u < D / 8; ++u) x[u] = live ? *reinterpret_cast<const uint4*>(src + u * 8) : make_uint4(0, 0, 0, 0);
@@ -577,6 +596,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
         fence_proxy_async_smem();
         mbar_arrive(&bars.q_full[t]);
       }
+      return cs;
+    };
+    int skip_tiles, skip_segs;
+    bool more = advance(sg, skip_tiles, skip_segs);
+    float cs = more ? load_q(sg) : 0.f;
+    while (ok && more) {
+      n_tile += skip_tiles;
+      n_seg += skip_segs;
+      const int row = sg.r0 + t * 128 + r, token = row / p.group;
+      const bool live = row < p.rows && token < sg.L.len_q;
       // ---- pages that do not exist (none, as a rule) -------------------------------------------------
       const int32_t* pages = p.c.page_table + sg.bi * p.c.page_table_stride;
       bool bad = false;
@@ -592,9 +621,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
       for (int j = sg.tile0; j < sg.tile1; ++j, ++blk) {
         if (!mbar_wait_warp(&bars.s_full[t], blk & 1, wt)) { ok = false; break; }
         tc_fence_after();
-        uint32_t sv[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[c * 32]));
         float cst = cs, ev = 0.f, back = 1.f;
         if constexpr (E4) {
           cst = cs * pow2(s_ek[n_tile % 8]);
@@ -603,27 +629,25 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
           back = pow2(-e);
         }
         ++n_tile;
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) reg_fence32(&sv[c * 32]);
         const int key0 = j * kKeys;
-        if (key0 + kKeys > sg.L.len_kv || (masked && key0 + kKeys > sg.off) || bad) {
-          // Visible columns as four words.
+        const bool need = key0 + kKeys > sg.L.len_kv || (masked && key0 + kKeys > sg.off) || bad;
+        uint32_t vis[4];       // visible columns
+        if (need) {
           int lim = sg.L.len_kv - 1;
           if (p.causal) lim = min(lim, sg.off + token);
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const int k0 = key0 + 32 * w, n = lim - k0 + 1;
-            uint32_t vis = n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+            uint32_t v = n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
             const int j0 = k0 - sg.off;
             if (p.tree_mask && j0 > -32 && live) {
               const uint32_t* words = p.tree_mask + sg.bi * p.tree_mask_stride + static_cast<int64_t>(token) * p.tree_words;
               if (j0 >= 0) {
                 const uint32_t lo = j0 / 32 < p.tree_words ? __ldg(words + j0 / 32) : 0u;
                 const uint32_t hi = j0 / 32 + 1 < p.tree_words ? __ldg(words + j0 / 32 + 1) : 0u;
-                vis &= __funnelshift_r(lo, hi, j0 % 32);
+                v &= __funnelshift_r(lo, hi, j0 % 32);
               } else {
-                vis &= (__ldg(words) << -j0) | ((1u << -j0) - 1u);
+                v &= (__ldg(words) << -j0) | ((1u << -j0) - 1u);
               }
             }
             if (bad) {
@@ -632,21 +656,39 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
                 const int key = k0 + 16 * h;
                 if (key >= sg.L.len_kv) continue;
                 const int pg = __ldg(pages + key / p.c.page_size);
-                if (pg < 0 || pg >= p.c.num_pages) vis &= h ? 0x0000FFFFu : 0xFFFF0000u;
+                if (pg < 0 || pg >= p.c.num_pages) v &= h ? 0x0000FFFFu : 0xFFFF0000u;
               }
             }
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((vis >> c) & 1u)) sv[32 * w + c] = __float_as_uint(-INFINITY);
+            vis[w] = v;
           }
         }
+        // The row's 128 scores come in halves of 64 columns: the second for its maximum, then the
+        // first, which stays for its exponentials, then the second again.  P takes the columns of
+        // the first quarter and then of the second, both read by then.
+        uint32_t sv[64];
+        auto load_half = [&](int h) {
+          tmem_ld32(s_addr + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+          tmem_ld32(s_addr + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+          tmem_ld_wait();
+          reg_fence32(&sv[0]);
+          reg_fence32(&sv[32]);
+          if (need) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (!(((h ? vis[2 + c / 32] : vis[c / 32]) >> (c % 32)) & 1u)) sv[c] = __float_as_uint(-INFINITY);
+          }
+        };
         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-          mx0 = max3(mx0, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-          mx1 = max3(mx1, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
-          mx2 = max3(mx2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
-          mx3 = max3(mx3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+        for (int h = 1; h >= 0; --h) {
+          load_half(h);
+#pragma unroll
+          for (int c = 0; c < 64; c += 8) {
+            mx0 = max3(mx0, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+            mx1 = max3(mx1, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+            mx2 = max3(mx2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
+            mx3 = max3(mx3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+          }
         }
         const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cst, ev);
         float alpha = 1.f;
@@ -657,19 +699,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
         const float nm = m_ref == -INFINITY ? 0.f : C::P_OFF - m_ref + ev;
         const float2 cs2 = make_float2(cst, cst), nm2 = make_float2(nm, nm);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-        uint32_t pk[64];
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-          const float2 x01 = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), cs2, nm2);
-          const float2 x23 = fma2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), cs2, nm2);
-          const float2 p01 = make_float2(ex2(x01.x), ex2(x01.y)), p23 = make_float2(ex2(x23.x), ex2(x23.y));
-          acc0 = add2(acc0, p01);
-          acc1 = add2(acc1, p23);
-          pk[c / 2] = pack_pair<BF>(p01.x, p01.y);
-          pk[c / 2 + 1] = pack_pair<BF>(p23.x, p23.y);
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1) load_half(1);
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const float2 x01 = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), cs2, nm2);
+            const float2 x23 = fma2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), cs2, nm2);
+            const float2 p01 = make_float2(ex2(x01.x), ex2(x01.y)), p23 = make_float2(ex2(x23.x), ex2(x23.y));
+            acc0 = add2(acc0, p01);
+            acc1 = add2(acc1, p23);
+            pk[c / 2] = pack_pair<BF>(p01.x, p01.y);
+            pk[c / 2 + 1] = pack_pair<BF>(p23.x, p23.y);
+          }
+          tmem_st32(s_addr + h * 32, pk);
         }
-        tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-        tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
         l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y)) * back;
         // The block before has added to O already: its P V was issued ahead of this block's S.
         if (j > sg.tile0 && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -689,12 +734,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
         mbar_arrive(&bars.p_full[t]);
       }
       if (!ok) break;
+      // ---- the next segment's Q, so that its first S runs while this one's results leave ----------
+      Segment next;
+      more = advance(next, skip_tiles, skip_segs);
+      cs = more ? load_q(next) : 0.f;
       // ---- the segment's result: this thread's row ------------------------------------------------
       if (!mbar_wait_warp(&bars.o_full[t], on & 1, wt)) { ok = false; break; }
       ++on;
       tc_fence_after();
       const bool whole = sg.tile0 == 0 && sg.tile1 == sg.n_tiles;
-      const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (sg.tile0 == 0 ? 1 : 0)) * 256 + t * 128 + r;
+      const int64_t part = 2 * blockIdx.x + (sg.tile0 == 0 ? 1 : 0);
       const bool none = !live || l == 0.f;
       const float inv = none ? 0.f : 1.f / l;
       const bool fix = live && s_found[n_seg % 8] == n_seg + 1;
@@ -712,10 +761,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
                                                          min(sg.tile1 * kKeys, sg.L.len_kv), __uint_as_float(ov[i])));
         }
         if (!whole) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c * 32);
+          float4* dst = reinterpret_cast<float4*>(p.part_o) + (part * (D / 4) + c * 8) * 256 + t * 128 + r;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]), __uint_as_float(ov[4 * i + 2]),
+            dst[i * 256] = make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]), __uint_as_float(ov[4 * i + 2]),
                                  __uint_as_float(ov[4 * i + 3]));
         } else {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + out + c * 32);
@@ -733,13 +782,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
       }
       if (row < p.rows) {
         if (!whole)
-          *reinterpret_cast<float2*>(p.part_ml + 2 * part) = make_float2(m_ref, l);
+          *reinterpret_cast<float2*>(p.part_ml + 2 * (part * 256 + t * 128 + r)) = make_float2(m_ref, l);
         else if (p.lse)
-          p.lse[(static_cast<int64_t>(sg.bi) * p.h_q + sg.hk * p.group + row % p.group) * p.s_q + token] =
-              none ? -INFINITY : (m_ref - C::P_OFF + __log2f(l)) * 0.6931471805599453f;
+          p.lse[lse_offset(p, sg.bi, sg.hk, row)] = none ? -INFINITY : natural_lse(m_ref - C::P_OFF, l);
       }
       tc_fence_before();     // O has been read: the next segment's first P V follows a later arrival
       ++n_seg;
+      sg = next;
     }
   }
 
@@ -757,13 +806,64 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
   }
 }
 
+// Joins the parts of blocks that more than one CTA worked on, and writes the rows that no key
+// reaches: 32 rows (lanes) by 32 elements (a warp has four) a CTA, in the parts' order.
+template <int D, int QT>
+__global__ void __launch_bounds__(256) decode_wide_combine_kernel(const __grid_constant__ DecodeParams p, float p_off) {
+  __shared__ uint2 s_out[32][9];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int groups = (min(p.rows, 256) + 31) / 32;
+  const Parts u = find_parts(p, blockIdx.x / groups, lane);
+  const int r = blockIdx.x % groups * 32 + lane, row = u.r0 + r, chunk = blockIdx.y * 8 + warp;
+  griddep_wait();   // (by every CTA, so that this grid never ends before the one it follows)
+  if (u.n == 1) return;
+  const bool on = row < p.rows;
+  float m = -INFINITY, l = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (on) {
+#pragma unroll 4
+    for (int k = 0; k < u.n; ++k) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (u.part(k) * 256 + r));
+      if (ml.y != 0.f) m = fmaxf(m, ml.x);
+    }
+#pragma unroll 4
+    for (int k = 0; k < u.n; ++k) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (u.part(k) * 256 + r));
+      const float4 v = reinterpret_cast<const float4*>(p.part_o)[(u.part(k) * (D / 4) + chunk) * 256 + r];
+      const float f = part_weight(ml, m);
+      l += ml.y * f;
+      x.x += f == 0.f ? 0.f : v.x * f;
+      x.y += f == 0.f ? 0.f : v.y * f;
+      x.z += f == 0.f ? 0.f : v.z * f;
+      x.w += f == 0.f ? 0.f : v.w * f;
+    }
+    const bool none = row / p.group >= u.L.len_q || l == 0.f;
+    const float inv = none ? 0.f : 1.f / l;
+    s_out[lane][warp] = none ? make_uint2(0, 0)
+                             : make_uint2(pack_pair<QT == kBF16>(x.x * inv, x.y * inv), pack_pair<QT == kBF16>(x.z * inv, x.w * inv));
+    if (p.lse && chunk == 0) p.lse[lse_offset(p, u.bi, u.hk, row)] = none ? -INFINITY : natural_lse(m - p_off, l);
+  }
+  __syncthreads();
+  // 64 bytes of a row by 8 neighbouring threads.
+  const int r2 = threadIdx.x / 8, row2 = blockIdx.x % groups * 32 + r2 + u.r0;
+  if (row2 < p.rows)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row_offset(p, p.o_st, u.bi, u.hk, row2) + blockIdx.y * 32 +
+                              threadIdx.x % 8 * 4) = s_out[r2][threadIdx.x % 8];
+}
+
 template <int D, int CT, int QT>
 cudaError_t launch_t(const WideParams& wp, cudaStream_t st) {
   auto kern = decode_wide_kernel<D, CT, QT>;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), WideCfg<D, CT>::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<wp.d.ctas, kThreads, WideCfg<D, CT>::SMEM, st>>>(wp);
-  return cudaGetLastError();
+  const DecodeParams& p = wp.d;
+  kern<<<p.ctas, WideCfg<D, CT>::THREADS, WideCfg<D, CT>::SMEM, st>>>(wp);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int groups = ((p.rows < 256 ? p.rows : 256) + 31) / 32;
+  return launch_after(decode_wide_combine_kernel<D, QT>,
+                      dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles * groups, D / 32), dim3(256), st, p,
+                      WideCfg<D, CT>::P_OFF);
 }
 
 template <int D>
@@ -779,6 +879,8 @@ int decode_wide_box(int page_size) {
   while (page_size % box != 0) box /= 2;
   return box;
 }
+
+int decode_wide_swizzle(int d, int cache_dtype) { return cache_dtype == kE4M3 && d == 64 ? 64 : 128; }
 
 cudaError_t launch_decode_wide(const DecodeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, long long wait_limit,
                                int d, int qt, int ct, cudaStream_t st) {

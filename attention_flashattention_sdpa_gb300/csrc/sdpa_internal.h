@@ -193,10 +193,9 @@ int api_ok();
 int api_finish(cudaError_t e, cudaStream_t stream, const char* what);
 // Checks that a logical [b][h][s][d] view is 16-byte aligned with positive strides.
 int api_check_view(const char* name, const void* ptr, const int64_t (&st)[4], int b, int h, int s, int d, int es);
-// Tensor map of such a view: 128 bytes of d x box_rows rows, 128-byte swizzle; or, not swizzled,
-// all d elements x box_rows rows.
+// Tensor map of such a view: 128 (or 64) bytes of d x box_rows rows, 128-byte (64-byte) swizzle.
 int api_make_map(CUtensorMap* map, const char* name, const void* ptr, const int64_t (&st)[4], int b, int h, int s,
-                 int d, int dt, int box_rows, bool swizzle = true);
+                 int d, int dt, int box_rows, int swizzle = 128);
 int api_num_sms();
 int api_log_level();
 long long api_wait_limit();
@@ -274,7 +273,8 @@ struct DecodeParams {
   int tile_shift;              // log2 of the keys of a tile
   int wide;                    // blocks of 256 rows on tcgen05 tiles (else 8 or 16 rows a block)
   float scale_log2;            // attn_scale * log2(e)
-  float* part_o;               // workspace: [2 * ctas][tile_rows][d] unnormalised partial O
+  float* part_o;               // workspace: [2 * ctas][tile_rows][d] unnormalised partial O (wide:
+                               // [2 * ctas][d / 4][256][4], rows side by side)
   float* part_ml;              // workspace: [2 * ctas][tile_rows][2] their max (log2 units) and sum
   int ctas;
 };
@@ -283,11 +283,12 @@ struct DecodeParams {
 void decode_plan(DecodeParams* p, int d, int cache_dtype, int num_sms);
 size_t decode_workspace_bytes(const DecodeParams& p, int d, size_t* ml_offset);
 cudaError_t launch_decode(const DecodeParams& p, int d, int q_dtype, int cache_dtype, cudaStream_t st);
-// The main kernel of wide blocks (maps: not swizzled for E4M3), then the join of its parts.
+// Wide blocks: the main kernel, then the join of its parts.  Maps: boxes of decode_wide_box rows of
+// the cache, swizzled by decode_wide_swizzle bytes.
 cudaError_t launch_decode_wide(const DecodeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, long long wait_limit,
                                int d, int q_dtype, int cache_dtype, cudaStream_t st);
-cudaError_t launch_decode_combine(const DecodeParams& p, int d, int q_dtype, int cache_dtype, cudaStream_t st);
-int decode_wide_box(int page_size);   // rows of its TMA boxes
+int decode_wide_box(int page_size);
+int decode_wide_swizzle(int d, int cache_dtype);
 uint32_t decode_take_device_error();
 
 }  // namespace sdpa
