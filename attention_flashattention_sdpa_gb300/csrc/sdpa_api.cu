@@ -156,7 +156,7 @@ sdpa_status_t check_view(const char* name, const void* ptr, const sdpa_strides_t
 }
 
 sdpa_status_t make_map(CUtensorMap* map, const char* name, const void* ptr, const sdpa_strides_t& st,
-                       int b, int h, int s, int d, int dt, int box_rows, int swizzle = 128) {
+                       int b, int h, int s, int d, int dt, int box_rows) {
   auto fn = encode_fn();
   if (fn == nullptr)
     return fail(SDPA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the CUDA driver");
@@ -169,10 +169,10 @@ sdpa_status_t make_map(CUtensorMap* map, const char* name, const void* ptr, cons
   for (int i = 0; i < 3; ++i)
     if (sizes[i] == 1) sb[i] = ((fallback + 15) / 16) * 16;
   cuuint64_t strides[3] = {(cuuint64_t)sb[0], (cuuint64_t)sb[1], (cuuint64_t)sb[2]};
-  cuuint32_t box[4] = {(cuuint32_t)(swizzle / es), (cuuint32_t)box_rows, 1, 1};
+  cuuint32_t box[4] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows, 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, map_dtype(dt), 4, const_cast<void*>(ptr), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(SDPA_ERR_LAYOUT, "%s: cuTensorMapEncodeTiled rejected the view (CUresult %d)",
@@ -333,8 +333,8 @@ int api_check_view(const char* name, const void* ptr, const int64_t (&st)[4], in
 }
 
 int api_make_map(CUtensorMap* map, const char* name, const void* ptr, const int64_t (&st)[4], int b, int h, int s,
-                 int d, int dt, int box_rows, int swizzle) {
-  return make_map(map, name, ptr, sdpa_strides_t{st[0], st[1], st[2], st[3]}, b, h, s, d, dt, box_rows, swizzle);
+                 int d, int dt, int box_rows) {
+  return make_map(map, name, ptr, sdpa_strides_t{st[0], st[1], st[2], st[3]}, b, h, s, d, dt, box_rows);
 }
 
 int api_num_sms() { return num_sms(); }

@@ -4,56 +4,69 @@
 // The split of the batch is that of sdpa_decode.cu with tiles of 128 keys and blocks of 256 rows:
 // one persistent CTA an SM walks an equal run of tiles, segment by segment (a segment: the part
 // of its run in one (sequence, KV head, block of rows)).  Roles:
-//   warp 0       pages and TMA: K and V tiles, box by box (a box lies in one page) into a ring;
-//                boxes of missing pages and behind the sequence are filled with zeros.
+//   warp 0       pages and TMA: K and V tiles, box by box (a box lies in one page); boxes of missing
+//                pages and behind the sequence are filled with zeros.  E4M3: the scales follow by
+//                bulk copies.
 //   warp 1       MMA issuer: S = Q K^T into TMEM, O += P V with P read from TMEM.
-//   warps 4-11   two softmax warpgroups, one for each 128-row tile; thread r owns row r: loads it
-//                into shared memory, the running max and sum, P, and the segment's results.
-//   warps 12-15  E4M3 caches: widen K to F16 on its way from the TMA's stage to the ring (and warps
-//                16-19 V); 16-bit caches: clear, in V tiles that end behind the sequence or hold
-//                drafted tokens, rows that do not exist and values that are not finite (a weight of
-//                zero does not hide a NaN in a product).
+//   warps 4-11   two softmax warpgroups; thread r owns a row: loads it into shared memory, the
+//                running max and sum, P, and the segment's results.  A block of more than 128 rows
+//                has a 128-row tile for each; in a smaller one both take the same rows and every
+//                second tile of keys, so that one computes while the other's products run.
+//   warps 12-15  E4M3: widen V to F16 on its way from the TMA's stage to the ring; 16-bit: clear, in
+//                V tiles that end behind the sequence or hold drafted tokens, rows that do not exist
+//                and values that are not finite (a weight of zero does not hide a NaN in a product).
 //
-// E4M3: a tile's codes are multiplied by scale / 2^E (E: the exponent of the tile's largest scale)
-// as a sum of two F16 factors, so one rounding to F16's 11 bits is left, whatever the scales; 2^E
-// of K joins the factor on the scores and 2^E of V the exponent, both once a tile.
+// E4M3 K enters the products as it is stored.  Q is split into E4M3 terms q = q1 + q2 (+ q3 for F16),
+// each the rounding of what the ones before leave: 4 bits a term hold BF16's 8 (F16's 11), and two
+// E4M3 products cost what one 16-bit product does.  A key's scale multiplies its column of S.
+// V's codes are multiplied by scale / 2^E (E: the exponent of the tile's largest scale) as a sum of
+// two F16 factors, so one rounding to F16's 11 bits is left, whatever the scales; 2^E joins the
+// exponent of the weights.  (Splitting P the same way would lose weights below 2^-17 of a row's
+// largest; widening K too left the tile waiting: 3.3 us for 128 keys.)
 //
 // Bound: the tensor cores (4 x 128 x 128 x d MMAs a block of two tiles) and the exponentials, as
-// the prompt's forward pass; reading the cache once bounds it for 64 rows and fewer.
+// the prompt's forward pass; reading the cache once bounds it for few rows.
 #include "sdpa_decode.cuh"
 
 namespace sdpa {
 namespace {
 
 constexpr int kKeys = 128;
-constexpr int kLog2Keys = 7;
+constexpr int kThreads = 512;
 
-template <int D, int CT>
+template <int D, int CT, int QT>
 struct WideCfg {
   static constexpr bool E4 = CT == kE4M3;
-  static constexpr int THREADS = E4 ? 640 : 512;
-  // Registers of the producer's, the softmax and the widening or clearing warpgroups, out of 96
-  // (E4M3) or 128 a thread at launch: 64 + 2 x 152 + 2 x 56 = 5 x 96, 64 + 2 x 184 + 80 = 4 x 128.
-  static constexpr int REGS0 = 64, REGS_SOFTMAX = E4 ? 152 : 184, REGS_WIDEN = E4 ? 56 : 80;
+  // Registers of the producer's, the softmax and the widening or clearing warpgroups, out of 128 a
+  // thread at launch: 64 + 2 x 184 + 80 = 4 x 128.
+  static constexpr int REGS0 = 64, REGS_SOFTMAX = 184, REGS_WIDEN = 80;
   static constexpr int TILE = 128 * D * 2;                // a 16-bit tile of 128 rows
-  static constexpr int RAW = E4 ? 128 * D : 0;            // an E4M3 tile as loaded
+  static constexpr int RAW = 128 * 128;                   // an E4M3 tile: rows of 128 bytes (d = 64: half zeros)
   static constexpr int NCHUNK = D / 64;                   // 128-byte columns of a 16-bit tile
-  static constexpr int Q_BYTES = 2 * TILE;
-  static constexpr int NS = D == 128 ? (E4 ? 3 : 4) : 6;  // ring of 16-bit tiles
-  static constexpr int NRAW = E4 ? 4 : 0;
-  static constexpr int SMEM = Q_BYTES + NS * TILE + NRAW * RAW + 1024;
-  static constexpr int KSTEPS = D / 16;
+  static constexpr int TERMS = E4 ? (QT == kBF16 ? 2 : 3) : 1;   // of Q
+  static constexpr int Q_TERM = E4 ? RAW : TILE;          // one term of a tile of Q
+  static constexpr int Q_TILE = TERMS * Q_TERM;
+  static constexpr int K_TILE = E4 ? RAW : TILE;
+  static constexpr int NK = E4 ? 3 : (D == 128 ? 2 : 3);
+  static constexpr int NV = E4 ? (TERMS == 3 && D == 128 ? 1 : 2) : (D == 128 ? 2 : 3);
+  static constexpr int NR = E4 ? 2 : 0;                   // stages of V as loaded
+  static constexpr int SC_K = E4 ? 8 : 0;                 // scales of K and V, by tile count (1 KB each)
+  static constexpr int OFF_K = 2 * Q_TILE, OFF_V = OFF_K + NK * K_TILE, OFF_RAW = OFF_V + NV * TILE;
+  static constexpr int OFF_SCK = OFF_RAW + NR * RAW, OFF_SCV = OFF_SCK + SC_K * 1024;
+  static constexpr int SMEM = OFF_SCV + NR * 512 + 1024;
+  static constexpr int KSTEPS = E4 ? D / 32 : D / 16;     // MMAs of S, a term
   static constexpr int O_COL0 = 256;
   static constexpr float P_OFF = CT == kBF16 ? 0.f : 6.f;
   static constexpr float THRESH = 8.f;
-  static_assert(SMEM + 1536 <= 232448, "shared memory");
+  static_assert(SMEM + 1024 <= 232448, "shared memory");
   static_assert(O_COL0 + 2 * D <= 512, "TMEM");
 };
 
 struct alignas(8) WideBarriers {
   uint64_t q_full[2];
-  uint64_t raw_full[4], raw_empty[4];
-  uint64_t kv_full[6], kv_empty[6], kv_clean[6];
+  uint64_t k_full[4], k_empty[4];
+  uint64_t v_full[4], v_empty[4], v_clean[4];
+  uint64_t raw_full[2], raw_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t drain;
   uint32_t tmem_base;
@@ -64,6 +77,7 @@ struct alignas(8) WideBarriers {
 struct Segment {
   int bi, hk, r0, n_tiles, tile0, tile1, off;
   SeqLens L;
+  bool split;     // at most 128 rows: the warpgroups take every second tile of keys
 };
 
 // The run's position; every role walks it by itself.
@@ -89,6 +103,7 @@ struct Walk {
       g.tile1 = static_cast<int>(min(static_cast<long long>(n), t_end - t0));
       g.L = seq_lens(p, bi);
       g.off = g.L.len_kv - g.L.len_q;
+      g.split = p.rows - g.r0 <= 128;
       t = t0 + g.tile1;
       return true;
     }
@@ -106,10 +121,25 @@ __device__ __forceinline__ bool needs_cleaning(const DecodeParams& p, const Segm
 __device__ __forceinline__ int exponent_of(uint32_t bits) { return min(max(static_cast<int>(bits >> 23) - 127, -100), 100); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
-// Bits of scale s where the key exists and the scale is a finite positive number, else 0.
-__device__ __forceinline__ uint32_t scale_bits(float s, bool on) {
-  const uint32_t b = __float_as_uint(s);
-  return on && b < 0x7F800000u ? b : 0u;
+// Exponent of the largest finite scale of a tile's existing keys (`left` of 128), by a whole warp.
+__device__ __forceinline__ int largest_exponent(const float* scales, int left, int lane) {
+  const float4 f = *reinterpret_cast<const float4*>(scales + lane * 4);
+  auto bits = [&](float x, int i) {
+    const uint32_t b = __float_as_uint(x);
+    return lane * 4 + i < left && b < 0x7F800000u ? b : 0u;
+  };
+  return exponent_of(__reduce_max_sync(0xffffffffu, max(max(bits(f.x, 0), bits(f.y, 1)), max(bits(f.z, 2), bits(f.w, 3)))));
+}
+
+// Contiguous copy of a multiple of 16 bytes into shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
 struct WideParams {
@@ -122,21 +152,23 @@ struct WideParams {
 };
 
 template <int D, int CT, int QT>
-__global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel(const __grid_constant__ WideParams wp) {
-  using C = WideCfg<D, CT>;
+__global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_constant__ WideParams wp) {
+  using C = WideCfg<D, CT, QT>;
   constexpr bool E4 = C::E4;
-  constexpr bool BF = CT == kBF16;     // type of the products' operands
-  constexpr int NS = C::NS;
+  constexpr bool BF = CT == kBF16;     // type of the 16-bit operands
+  constexpr int NK = C::NK, NV = C::NV, NR = E4 ? C::NR : 1;
   const DecodeParams& p = wp.d;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sRing = smem + C::Q_BYTES;
-  uint8_t* sRaw = sRing + NS * C::TILE;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  uint8_t* sRaw = smem + C::OFF_RAW;
+  float* sScK = reinterpret_cast<float*>(smem + C::OFF_SCK);   // [8][2][128]: of K and of V
+  float* sScV = reinterpret_cast<float*>(smem + C::OFF_SCV);   // [NR][128]
   __shared__ WideBarriers bars;
   __shared__ Walk s_walk;
-  __shared__ volatile int s_ek[8], s_ev[8];    // exponents of a tile's scales, by tile count
   __shared__ volatile int s_found[8];          // segment count + 1 of a segment with cleared values
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -179,21 +211,21 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
     }
     if (lane == 0) s_walk = w;
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars.q_full[t], 128);
       mbar_init(&bars.s_full[t], 1);
       mbar_init(&bars.p_full[t], 128);
       mbar_init(&bars.o_full[t], 1);
+      mbar_init(&bars.raw_full[t], 1);
+      mbar_init(&bars.raw_empty[t], 128);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&bars.raw_full[i], 1);
-      mbar_init(&bars.raw_empty[i], 128);
-    }
-    for (int i = 0; i < 6; ++i) {
-      mbar_init(&bars.kv_full[i], E4 ? 128 : 1);
-      mbar_init(&bars.kv_empty[i], E4 ? 1 : 1 + 4);   // the MMAs that read the slot, and the clearing warps
-      mbar_init(&bars.kv_clean[i], 128);
+      mbar_init(&bars.k_full[i], 1);
+      mbar_init(&bars.k_empty[i], 1);
+      mbar_init(&bars.v_full[i], E4 ? 128 : 1);
+      mbar_init(&bars.v_empty[i], E4 ? 1 : 1 + 4);   // the MMAs that read the slot, and the clearing warps
+      mbar_init(&bars.v_clean[i], 128);
     }
     mbar_init(&bars.drain, 1);
     bars.abort = 0;
@@ -201,6 +233,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
     for (int i = 0; i < 8; ++i) s_found[i] = 0;
   }
   if (warp == 1) {
+    __syncwarp();
     tmem_alloc(&bars.tmem_base, 512);
     tmem_relinquish();
   }
@@ -215,7 +248,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
   Segment sg;
 
   bool producer = false;
-  int kv_issued = 0;     // tiles whose copies the producer issued
+  int issued = 0;          // tiles of K, and then of V, whose copies the producer issued
 
   if (warp < 4) {
     regs_dec<C::REGS0>();
@@ -227,7 +260,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         tma_prefetch_desc(&wp.tm_v);
       }
       bool ok = true;
-      int it = 0;
+      int n_tile = 0;
       const int boxes = kKeys / wp.box;     // boxes of a tile: 1, 2, 4 or 8
       while (ok && walk.next(p, sg)) {
         const int32_t* pages = p.c.page_table + sg.bi * p.c.page_table_stride;
@@ -247,121 +280,164 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         };
         int page, slot, next_page, next_slot;
         look_up(0, next_page, next_slot);
-        for (int j = sg.tile0; ok && j < sg.tile1; ++j) {
+        for (int j = sg.tile0; ok && j < sg.tile1; ++j, ++n_tile) {
           const int b0 = (j - sg.tile0) * boxes;
           if (b0 % 32 == 0) {
             page = next_page;
             slot = next_slot;
             look_up(b0 + 32, next_page, next_slot);
           }
+          const unsigned there = __ballot_sync(0xffffffffu, page < p.c.num_pages) >> (b0 % 32);   // bit x: box x exists
+          const int n_there = __popc(there & ((1u << boxes) - 1u));
           for (int kv = 0; ok && kv < 2; ++kv) {
-            uint8_t* dst;
-            uint64_t* bar;
-            if (lane == 0) {
-              if constexpr (E4) {
-                const int s = it % C::NRAW;
-                ok = mbar_wait(&bars.raw_empty[s], ((it / C::NRAW) & 1) ^ 1, wt);
-                dst = sRaw + s * C::RAW;
-                bar = &bars.raw_full[s];
-                if (ok) mbar_arrive_expect_tx(bar, C::RAW);
-              } else {
-                const int s = it % NS;
-                ok = mbar_wait(&bars.kv_empty[s], ((it / NS) & 1) ^ 1, wt);
-                dst = sRing + s * C::TILE;
-                bar = &bars.kv_full[s];
-                if (ok) mbar_arrive_expect_tx(bar, C::TILE);
-              }
-              if (ok) kv_issued = it + 1;
-            }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            // Where this tile goes, and the barrier that counts its bytes.
+            const int s = n_tile % (kv ? (E4 ? NR : NV) : NK);
+            const int turn = n_tile / (kv ? (E4 ? NR : NV) : NK);
+            uint64_t* full = kv ? (E4 ? &bars.raw_full[s] : &bars.v_full[s]) : &bars.k_full[s];
+            uint64_t* empty = kv ? (E4 ? &bars.raw_empty[s] : &bars.v_empty[s]) : &bars.k_empty[s];
+            uint8_t* dst = kv ? (E4 ? sRaw + s * C::RAW : sV + s * C::TILE) : sK + s * C::K_TILE;
+            float* sc = kv ? sScV + s * 128 : sScK + n_tile % 8 * 256;
+            ok = mbar_wait_warp(empty, (turn & 1) ^ 1, wt);
             if (!ok) break;
+            if constexpr (E4) {
+              if (n_there < boxes) {      // no scale where there is no key
+                for (int i = lane; i < kKeys; i += 32)
+                  if (!((there >> (i / wp.box)) & 1u)) {
+                    sc[i] = 0.f;
+                    if (!kv) sc[128 + i] = 0.f;
+                  }
+                __syncwarp();
+              }
+            }
+            if (lane == 0) {
+              mbar_arrive_expect_tx(full, E4 ? C::RAW + n_there * wp.box * (kv ? 4 : 8) : C::TILE);
+              ++issued;
+            }
             for (int x = 0; x < boxes; ++x) {
               const int pg = __shfl_sync(0xffffffffu, page, (b0 + x) % 32);
               const int sl = __shfl_sync(0xffffffffu, slot, (b0 + x) % 32);
               if (lane == 0) {
                 const CUtensorMap* map = kv ? &wp.tm_v : &wp.tm_k;
                 if constexpr (E4) {
-                  tma_load_4d(dst + x * wp.box * D, map, bar, 0, sl, sg.hk, pg);
+                  tma_load_4d(dst + x * wp.box * 128, map, full, 0, sl, sg.hk, pg);
+                  if (pg < p.c.num_pages) {
+                    const int64_t at = (static_cast<int64_t>(pg) * p.c.h_kv + sg.hk) * p.c.page_size + sl;
+                    if (!kv) bulk_load(sc + x * wp.box, p.c.k_scale + at, wp.box * 4, full);
+                    bulk_load(sc + (kv ? 0 : 128) + x * wp.box, p.c.v_scale + at, wp.box * 4, full);
+                  }
                 } else {
                   for (int c = 0; c < C::NCHUNK; ++c)
-                    tma_load_4d(dst + c * 16384 + x * wp.box * 128, map, bar, c * 64, sl, sg.hk, pg);
+                    tma_load_4d(dst + c * 16384 + x * wp.box * 128, map, full, c * 64, sl, sg.hk, pg);
                 }
               }
             }
-            ++it;
           }
         }
       }
     } else if (warp == 1) {
       // ================================ MMA issuer ========================================
       if (elect_one_sync()) {
-        const uint32_t fmt = BF ? 1u : 0u;
-        const uint32_t idesc_s = make_idesc(fmt, 128, 128, false, false);
-        const uint32_t idesc_pv = make_idesc(fmt, 128, D, false, true);
+        const uint32_t idesc_s = make_idesc(BF ? 1u : 0u, 128, 128, false, false);   // (0: F16 or E4M3)
+        const uint32_t idesc_pv = make_idesc(BF ? 1u : 0u, 128, D, false, true);
         bool ok = true;
-        int it = 0;
+        int nk = 0, nv = 0;               // tiles of K and V so far
         uint32_t clean_par = 0;           // by slot: parity of its next cleaning
         uint32_t q_par = 0, p_par = 0;    // by tile
-        auto wait_full = [&](bool cleaned) -> int {
-          const int s = it % NS;
-          if (!mbar_wait(&bars.kv_full[s], (it / NS) & 1, wt)) return -1;
-          if (!E4 && cleaned) {
-            if (!mbar_wait(&bars.kv_clean[s], (clean_par >> s) & 1, wt)) return -1;
-            clean_par ^= 1u << s;
-          }
-          ++it;
+        auto wait_k = [&]() -> int {
+          const int s = nk % NK;
+          if (!mbar_wait(&bars.k_full[s], (nk / NK) & 1, wt)) return -1;
+          ++nk;
           tc_fence_after();
           return s;
         };
-        auto issue_s = [&](int t, int s) {
-          const uint32_t qa = smem_u32(sQ + t * C::TILE), kb = smem_u32(sRing + s * C::TILE);
-#pragma unroll
-          for (int k = 0; k < C::KSTEPS; ++k) {
-            const uint32_t o = (k / 4) * 16384 + (k % 4) * 32;
-            mma_ss(tmem + t * 128, make_sdesc_sw128(qa + o, 16, 1024), make_sdesc_sw128(kb + o, 16, 1024), idesc_s, k > 0, false);
+        auto wait_v = [&](bool cleaned) -> int {
+          const int s = nv % NV;
+          if (!mbar_wait(&bars.v_full[s], (nv / NV) & 1, wt)) return -1;
+          if (!E4 && cleaned) {
+            if (!mbar_wait(&bars.v_clean[s], (clean_par >> s) & 1, wt)) return -1;
+            clean_par ^= 1u << s;
           }
+          ++nv;
+          tc_fence_after();
+          return s;
+        };
+        auto wait_p = [&](int t) {
+          if (!mbar_wait(&bars.p_full[t], (p_par >> t) & 1, wt)) return false;
+          p_par ^= 1u << t;
+          tc_fence_after();
+          return true;
+        };
+        // S of slot t from tile `tq` of Q.
+        auto issue_s = [&](int t, int tq, int s) {
+          const uint32_t qa = smem_u32(sQ + tq * C::Q_TILE), kb = smem_u32(sK + s * C::K_TILE);
+#pragma unroll
+          for (int term = 0; term < C::TERMS; ++term)
+#pragma unroll
+            for (int k = 0; k < C::KSTEPS; ++k) {
+              const uint32_t o = (k / 4) * 16384 + (k % 4) * 32;
+              mma_ss(tmem + t * 128, make_sdesc_sw128(qa + term * C::Q_TERM + o, 16, 1024), make_sdesc_sw128(kb + o, 16, 1024),
+                     idesc_s, term + k > 0, E4);
+            }
           tc_commit(&bars.s_full[t]);
         };
         auto issue_pv = [&](int t, int s, bool first) {
-          const uint32_t vb = smem_u32(sRing + s * C::TILE);
+          const uint32_t vb = smem_u32(sV + s * C::TILE);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             mma_ts(tmem + C::O_COL0 + t * D, tmem + t * 128 + k * 8, make_sdesc_sw128(vb + k * 16 * 128, 16384, 1024),
                    idesc_pv, (!first || k > 0) ? 1u : 0u, false);
         };
         while (ok && walk.next(p, sg)) {
-          const int n_t = p.rows - sg.r0 > 128 ? 2 : 1;
-          for (int t = 0; t < n_t && ok; ++t) {
+          const int n = sg.tile1 - sg.tile0;
+          for (int t = 0; t < (sg.split ? 1 : 2) && ok; ++t) {
             ok = mbar_wait(&bars.q_full[t], (q_par >> t) & 1, wt);
             q_par ^= 1u << t;
           }
           if (!ok) break;
           tc_fence_after();
-          const int k0 = wait_full(false);
-          if (k0 < 0) { ok = false; break; }
-          for (int t = 0; t < n_t; ++t) issue_s(t, k0);
-          tc_commit(&bars.kv_empty[k0]);
-          for (int j = sg.tile0; j < sg.tile1; ++j) {
-            const int vs = wait_full(needs_cleaning(p, sg, j));
-            if (vs < 0) { ok = false; break; }
-            int nk = -1;
-            for (int t = 0; t < n_t; ++t) {
-              if (!mbar_wait(&bars.p_full[t], (p_par >> t) & 1, wt)) { ok = false; break; }
-              p_par ^= 1u << t;
-              tc_fence_after();
-              issue_pv(t, vs, j == sg.tile0);
-              if (j + 1 == sg.tile1) tc_commit(&bars.o_full[t]);
-              if (t == n_t - 1) tc_commit(&bars.kv_empty[vs]);
-              if (j + 1 < sg.tile1) {
-                if (nk < 0) {
-                  nk = wait_full(false);
-                  if (nk < 0) { ok = false; break; }
-                }
-                issue_s(t, nk);
-                if (t == n_t - 1) tc_commit(&bars.kv_empty[nk]);
+          if (sg.split) {
+            // Slot i % 2 for tile i: S runs two tiles ahead of P V.
+            for (int i = 0; i < 2 && i < n; ++i) {
+              const int s = wait_k();
+              if (s < 0) { ok = false; break; }
+              issue_s(i, 0, s);
+              tc_commit(&bars.k_empty[s]);
+            }
+            for (int i = 0; ok && i < n; ++i) {
+              const int t = i & 1, vs = wait_v(needs_cleaning(p, sg, sg.tile0 + i));
+              if (vs < 0 || !wait_p(t)) { ok = false; break; }
+              issue_pv(t, vs, i < 2);
+              if (i + 2 >= n) tc_commit(&bars.o_full[t]);
+              tc_commit(&bars.v_empty[vs]);
+              if (i + 2 < n) {
+                const int s = wait_k();
+                if (s < 0) { ok = false; break; }
+                issue_s(t, 0, s);
+                tc_commit(&bars.k_empty[s]);
               }
             }
-            if (!ok) break;
+          } else {
+            const int k0 = wait_k();
+            if (k0 < 0) { ok = false; break; }
+            for (int t = 0; t < 2; ++t) issue_s(t, t, k0);
+            tc_commit(&bars.k_empty[k0]);
+            for (int i = 0; ok && i < n; ++i) {
+              const int vs = wait_v(needs_cleaning(p, sg, sg.tile0 + i));
+              if (vs < 0) { ok = false; break; }
+              int s = -1;
+              for (int t = 0; t < 2; ++t) {
+                if (!wait_p(t)) { ok = false; break; }
+                issue_pv(t, vs, i == 0);
+                if (i + 1 == n) tc_commit(&bars.o_full[t]);
+                if (t == 1) tc_commit(&bars.v_empty[vs]);
+                if (i + 1 < n) {
+                  if (t == 0) s = wait_k();
+                  if (s < 0) { ok = false; break; }
+                  issue_s(t, t, s);
+                  if (t == 1) tc_commit(&bars.k_empty[s]);
+                }
+              }
+            }
           }
         }
         tc_commit(&bars.drain);
@@ -371,102 +447,37 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
   } else if (warp >= 12) {
     regs_dec<C::REGS_WIDEN>();
     // ============================ widening / clearing =========================================
-    const int w4 = warp % 4;
+    const int w4 = warp % 4, r = w4 * 32 + lane;
     const bool masked = p.causal != 0 || p.tree_mask != nullptr;
     bool ok = true;
-    int it = 0, n_seg = 0, n_tile = 0;
+    int n_seg = 0, n_tile = 0;
     while (ok && walk.next(p, sg)) {
       bool found = false;
-      if constexpr (E4) {
-        // Tiles of K (warps 12-15) or of V (16-19).  Scales of a tile: the lane's own row
-        // (32 w4 + lane), and four of the 128 for the largest; K's warps find both exponents.
-        const bool is_v = warp >= 16;
-        const int32_t* pages = p.c.page_table + sg.bi * p.c.page_table_stride;
-        const int ps = p.c.page_size, col_step = kKeys / ps, slot_step = kKeys % ps;
-        struct Spot {      // a key of this lane, moving tile by tile
-          int key, col, slot;
-        };
-        auto spot_at = [&](int key) { return Spot{key, key / ps, key % ps}; };
-        auto step = [&](Spot& x) {
-          x.key += kKeys;
-          x.col += col_step;
-          x.slot += slot_step;
-          if (x.slot >= ps) {
-            x.slot -= ps;
-            ++x.col;
-          }
-        };
-        auto page_at = [&](const Spot& x) -> int {
-          if (x.key >= min(sg.tile1 * kKeys, sg.L.len_kv)) return -1;
-          const int pg = __ldg(pages + x.col);
-          return pg < p.c.num_pages ? pg : -1;
-        };
-        auto scale_at = [&](const Spot& x, int pg) {
-          return (static_cast<int64_t>(pg) * p.c.h_kv + sg.hk) * ps + x.slot;
-        };
-        const float4 kZero4 = make_float4(0.f, 0.f, 0.f, 0.f);
-        float nxt_own = 0.f;
-        float4 nxt_k = kZero4, nxt_v = kZero4;
-        bool nxt_on = false;
-        int nxt_left = 0;
-        auto fetch = [&](const Spot& own, int pg_own, const Spot& four, int pg_four) {
-          nxt_on = pg_own >= 0;
-          nxt_left = pg_four >= 0 ? sg.L.len_kv - four.key : 0;
-          nxt_own = 0.f;
-          nxt_k = nxt_v = kZero4;
-          if (pg_own >= 0) nxt_own = __ldg((is_v ? p.c.v_scale : p.c.k_scale) + scale_at(own, pg_own));
-          if (pg_four >= 0) {
-            if (!is_v) nxt_k = __ldg(reinterpret_cast<const float4*>(p.c.k_scale + scale_at(four, pg_four)));
-            nxt_v = __ldg(reinterpret_cast<const float4*>(p.c.v_scale + scale_at(four, pg_four)));
-          }
-        };
-        Spot own = spot_at(sg.tile0 * kKeys + w4 * 32 + lane), four = spot_at(sg.tile0 * kKeys + lane * 4);
-        fetch(own, page_at(own), four, page_at(four));
-        step(own);
-        step(four);
-        int pg_own = page_at(own), pg_four = page_at(four);     // of tile j + 1
-        for (int j = sg.tile0; ok && j < sg.tile1; ++j) {
-          const float cur = nxt_own;
-          const float4 cur_k = nxt_k, cur_v = nxt_v;
-          const bool on = nxt_on;
-          const int left = nxt_left;
-          fetch(own, pg_own, four, pg_four);
-          step(own);
-          step(four);
-          pg_own = page_at(own);
-          pg_four = page_at(four);
-          auto largest = [&](const float4& f) {
-            return exponent_of(__reduce_max_sync(0xffffffffu, max(max(scale_bits(f.x, left > 0), scale_bits(f.y, left > 1)),
-                                                                  max(scale_bits(f.z, left > 2), scale_bits(f.w, left > 3)))));
-          };
-          const int ev = largest(cur_v), ex = is_v ? ev : largest(cur_k);
-          if (threadIdx.x == 12 * 32) {
-            s_ek[n_tile % 8] = ex;
-            s_ev[n_tile % 8] = ev;
-          }
-          ++n_tile;
-          // scale / 2^E of the lane's row as two F16, each twice in a word
-          const float f = on ? cur * pow2(-ex) : 0.f;
+      for (int j = sg.tile0; ok && j < sg.tile1; ++j, ++n_tile) {
+        const int s = n_tile % NV;
+        const bool tail = masked && (j + 1) * kKeys > sg.off;
+        const bool on = j * kKeys + r < sg.L.len_kv;
+        if constexpr (E4) {
+          const int rs = n_tile % NR;
+          ok = mbar_wait_warp(&bars.raw_full[rs], (n_tile / NR) & 1, wt);
+          if (!ok) break;
+          const float* sc = sScV + rs * 128;
+          const int ev = largest_exponent(sc, sg.L.len_kv - j * kKeys, lane);   // (by every lane)
+          const float f = on ? sc[r] * pow2(-ev) : 0.f;
           const __half fh = __float2half_rn(f), fl = __float2half_rn(f - __half2float(fh));
           const __half2 h2 = __half2half2(fh), l2 = __half2half2(fl);
-          const bool tail = is_v && masked && (j + 1) * kKeys > sg.off;
-          const int mine = it + (is_v ? 1 : 0);
-          it += 2;
-          const int rs = mine % C::NRAW, s = mine % NS;
-          ok = mbar_wait_warp(&bars.raw_full[rs], (mine / C::NRAW) & 1, wt) &&
-               mbar_wait_warp(&bars.kv_empty[s], ((mine / NS) & 1) ^ 1, wt);
+          ok = mbar_wait_warp(&bars.v_empty[s], ((n_tile / NV) & 1) ^ 1, wt);
           if (!ok) break;
-          // A lane takes its row, 16 codes at a time; the swizzles of both tiles put the 8 rows
-          // of a quarter-warp into 8 different 16-byte columns.
-          const int r = w4 * 32 + lane, sw = D == 128 ? r & 7 : (r >> 1) & 3;
-          const uint8_t* src = sRaw + rs * C::RAW + r * D;
-          uint8_t* dst = sRing + s * C::TILE + r * 128;
+          // A lane takes its row, 16 codes at a time; the swizzles of both tiles put the 8 rows of a
+          // quarter-warp into 8 different 16-byte columns.
+          const uint8_t* src = sRaw + rs * C::RAW + r * 128;
+          uint8_t* dst = sV + s * C::TILE + r * 128;
 #pragma unroll
           for (int c0 = 0; c0 < D / 16; c0 += 4) {
             uint4 in[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              in[x] = *reinterpret_cast<const uint4*>(src + ((c0 + x) ^ sw) * 16);
+              in[x] = *reinterpret_cast<const uint4*>(src + ((c0 + x) ^ (r & 7)) * 16);
               if (!on) in[x] = make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
@@ -494,45 +505,36 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           }
           if (found) s_found[n_seg % 8] = n_seg + 1;
           fence_proxy_async_smem();
-          mbar_arrive(&bars.kv_full[s]);
+          mbar_arrive(&bars.v_full[s]);
           mbar_arrive(&bars.raw_empty[rs]);
-        }
-      } else {
-        // Every tile's phase is followed, and its slot returned, by these warps too: a parity says
-        // nothing about a phase that lies further back or ahead.
-        for (int j = sg.tile0; ok && j < sg.tile1; ++j) {
+        } else {
+          // Every tile's phase is followed, and its slot returned, by these warps too: a parity says
+          // nothing about a phase that lies further back or ahead.
+          ok = mbar_wait_warp(&bars.v_full[s], (n_tile / NV) & 1, wt);
+          if (!ok) break;
+          if (needs_cleaning(p, sg, j)) {
+            if (!on || tail) {
 #pragma unroll 1
-          for (int kv = 0; ok && kv < 2; ++kv, ++it) {
-            const int s = it % NS;
-            ok = mbar_wait_warp(&bars.kv_full[s], (it / NS) & 1, wt);
-            if (!ok) break;
-            if (kv && needs_cleaning(p, sg, j)) {
-              const bool tail = masked && (j + 1) * kKeys > sg.off;
-              const int r = w4 * 32 + lane;
-              const bool on = j * kKeys + r < sg.L.len_kv;
-              if (!on || tail) {
-#pragma unroll 1
-                for (int u = 0; u < D / 8; ++u) {
-                  uint4* at = reinterpret_cast<uint4*>(sRing + s * C::TILE + (u / 8) * 16384 + r * 128 + ((u % 8) ^ (r & 7)) * 16);
-                  if (!on) {
-                    *at = make_uint4(0, 0, 0, 0);
-                  } else {
-                    uint4 x = *at;
-                    x.x = finite_pair<BF>(x.x, found);
-                    x.y = finite_pair<BF>(x.y, found);
-                    x.z = finite_pair<BF>(x.z, found);
-                    x.w = finite_pair<BF>(x.w, found);
-                    *at = x;
-                  }
+              for (int u = 0; u < D / 8; ++u) {
+                uint4* at = reinterpret_cast<uint4*>(sV + s * C::TILE + (u / 8) * 16384 + r * 128 + ((u % 8) ^ (r & 7)) * 16);
+                if (!on) {
+                  *at = make_uint4(0, 0, 0, 0);
+                } else {
+                  uint4 x = *at;
+                  x.x = finite_pair<BF>(x.x, found);
+                  x.y = finite_pair<BF>(x.y, found);
+                  x.z = finite_pair<BF>(x.z, found);
+                  x.w = finite_pair<BF>(x.w, found);
+                  *at = x;
                 }
               }
-              if (found) s_found[n_seg % 8] = n_seg + 1;
-              fence_proxy_async_smem();
-              mbar_arrive(&bars.kv_clean[s]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.kv_empty[s]);
+            if (found) s_found[n_seg % 8] = n_seg + 1;
+            fence_proxy_async_smem();
+            mbar_arrive(&bars.v_clean[s]);
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.v_empty[s]);
         }
       }
       ++n_seg;
@@ -547,65 +549,80 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
     const bool masked = p.causal != 0 || p.tree_mask != nullptr;
     bool ok = true;
     int n_seg = 0, n_tile = 0;
-    uint32_t blk = 0, on = 0;      // blocks and segments of this tile so far
-    // Segments that have rows for this tile; the blocks and segments passed over are counted.
-    auto advance = [&](Segment& to, int& tiles, int& segs) {
-      tiles = segs = 0;
-      while (walk.next(p, to)) {
-        if (t == 0 || p.rows - to.r0 > 128) return true;
-        tiles += to.tile1 - to.tile0;
-        ++segs;
-      }
-      return false;
-    };
-    // This thread's row of Q of a segment to shared memory; returns the factor on its scores.  To
-    // be called when the last S of the segment before has been read.
+    uint32_t n_own = 0, n_other = 0;   // S of this warpgroup's slot and of the other so far
+    uint32_t n_o = 0;              // results of this slot so far
+    // This thread's row of Q of a segment to shared memory (one warpgroup's where both take the
+    // same rows); returns the factor on its scores.  To be called when the last S of the segment
+    // before has been read.
     auto load_q = [&](const Segment& g) -> float {
-      const int row = g.r0 + t * 128 + r;
+      const int row = g.r0 + (g.split ? 0 : t * 128) + r;
       const bool live = row < p.rows && row / p.group < g.L.len_q;
+      const bool store = !g.split || t == 0;
       float cs = wp.abs_scale_log2;
-      {
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (live ? row_offset(p, p.q_st, g.bi, g.hk, row) : 0);
-        uint4 x[D / 8];
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) + (live ? row_offset(p, p.q_st, g.bi, g.hk, row) : 0);
+      uint4 x[D / 8];
 #pragma unroll
-        for (int u = 0; u < D / 8; ++u) x[u] = live ? *reinterpret_cast<const uint4*>(src + u * 8) : make_uint4(0, 0, 0, 0);
-        uint32_t* w = reinterpret_cast<uint32_t*>(x);
-        if (wp.negate) {
+      for (int u = 0; u < D / 8; ++u) x[u] = live ? *reinterpret_cast<const uint4*>(src + u * 8) : make_uint4(0, 0, 0, 0);
+      uint32_t* w = reinterpret_cast<uint32_t*>(x);
+      if (wp.negate) {
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i) w[i] ^= 0x80008000u;
-        }
-        if constexpr (E4 && QT == kBF16) {
-          // To F16 by a power of two that brings the largest element to [256, 512).
-          uint32_t m = 0;
+        for (int i = 0; i < D / 2; ++i) w[i] ^= 0x80008000u;
+      }
+      uint8_t* q_row = sQ + t * C::Q_TILE + r * 128;
+      if constexpr (E4) {
+        // A power of two brings the largest element to [128, 256), half of E4M3's range; the terms
+        // are then exact down to 2^-10 (F16: 2^-7) of it, and off by 2^-19 of it below.
+        uint32_t m = 0;
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-          const int ex = static_cast<int>(m >> 7);
-          const int sh = (ex == 0 || ex == 255) ? 0 : min(127 + 8 - ex, 126);
-          const float up = pow2(sh);
-          cs *= pow2(-sh);
+        for (int i = 0; i < D / 2; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+        const float big = QT == kBF16 ? __uint_as_float(m << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(m)));
+        const int ex = static_cast<int>(__float_as_uint(big) >> 23);     // (F16's subnormals are normal in fp32)
+        const int sh = (ex == 0 || ex == 255) ? 0 : min(127 + 7 - ex, 126);
+        // (E4M3 has no infinity: a row that holds one, or a NaN, becomes NaN.)
+        const float up = ex == 255 ? __uint_as_float(0x7FC00000u) : pow2(sh);
+        cs *= pow2(-sh);
+        if (store) {
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i) {
-            const float2 f = unpack_pair<true>(w[i]);
-            w[i] = pack_pair<false>(f.x * up, f.y * up);
+          for (int u = 0; u < D / 16; ++u) {
+            uint32_t term[C::TERMS][4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float2 f = unpack_pair<QT == kBF16>(w[u * 8 + i]);
+              f.x *= up;
+              f.y *= up;
+#pragma unroll
+              for (int k = 0; k < C::TERMS; ++k) {
+                const uint32_t c2 = e4m3_pair(f.x, f.y);
+                term[k][i / 2] = i % 2 ? term[k][i / 2] | (c2 << 16) : c2 & 0xFFFFu;
+                const float2 back = unpack_pair<false>(e4m3x2_to_f16x2(c2 & 0xFFFFu));
+                f.x -= back.x;
+                f.y -= back.y;
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < C::TERMS; ++k)
+              *reinterpret_cast<uint4*>(q_row + k * C::Q_TERM + (u ^ (r & 7)) * 16) =
+                  make_uint4(term[k][0], term[k][1], term[k][2], term[k][3]);
           }
         }
-        uint8_t* q_row = sQ + t * C::TILE + r * 128;
+      } else if (store) {
 #pragma unroll
         for (int u = 0; u < D / 8; ++u)
           *reinterpret_cast<uint4*>(q_row + (u / 8) * 16384 + ((u % 8) ^ (r & 7)) * 16) = x[u];
+      }
+      if (store) {
         fence_proxy_async_smem();
         mbar_arrive(&bars.q_full[t]);
       }
       return cs;
     };
-    int skip_tiles, skip_segs;
-    bool more = advance(sg, skip_tiles, skip_segs);
+    bool more = walk.next(p, sg);
     float cs = more ? load_q(sg) : 0.f;
     while (ok && more) {
-      n_tile += skip_tiles;
-      n_seg += skip_segs;
-      const int row = sg.r0 + t * 128 + r, token = row / p.group;
+      const int row = sg.r0 + (sg.split ? 0 : t * 128) + r, token = row / p.group;
       const bool live = row < p.rows && token < sg.L.len_q;
+      const int n = sg.tile1 - sg.tile0;
+      const int step = sg.split ? 2 : 1, first = sg.split ? t : 0;
       // ---- pages that do not exist (none, as a rule) -------------------------------------------------
       const int32_t* pages = p.c.page_table + sg.bi * p.c.page_table_stride;
       bool bad = false;
@@ -618,27 +635,44 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         bad = __any_sync(0xffffffffu, bad) != 0;
       }
       float m_ref = -INFINITY, l = 0.f;
-      for (int j = sg.tile0; j < sg.tile1; ++j, ++blk) {
-        if (!mbar_wait_warp(&bars.s_full[t], blk & 1, wt)) { ok = false; break; }
+      for (int i = first; i < n; i += step, ++n_own) {
+        if (!mbar_wait_warp(&bars.s_full[t], n_own & 1, wt)) { ok = false; break; }
         tc_fence_after();
-        float cst = cs, ev = 0.f, back = 1.f;
+        const int key0 = (sg.tile0 + i) * kKeys;
+        // E4M3: exponent of the tile's largest V scale (in the weights), and its way back out of l.
+        float ev = 0.f, back = 1.f;
+        const float* sc = sScK + (n_tile + i) % 8 * 256;
         if constexpr (E4) {
-          cst = cs * pow2(s_ek[n_tile % 8]);
-          const int e = s_ev[n_tile % 8];
+          const int e = largest_exponent(sc + 128, sg.L.len_kv - key0, lane);
           ev = static_cast<float>(e);
           back = pow2(-e);
         }
-        ++n_tile;
-        const int key0 = j * kKeys;
-        const bool need = key0 + kKeys > sg.L.len_kv || (masked && key0 + kKeys > sg.off) || bad;
-        uint32_t vis[4];       // visible columns
-        if (need) {
+        uint32_t sv[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[c * 32]));
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) reg_fence32(&sv[c * 32]);
+        if constexpr (E4) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 4) {
+            const float4 ks = *reinterpret_cast<const float4*>(sc + c);
+            const float2 a = mul2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), make_float2(ks.x, ks.y));
+            const float2 b = mul2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), make_float2(ks.z, ks.w));
+            sv[c] = __float_as_uint(a.x);
+            sv[c + 1] = __float_as_uint(a.y);
+            sv[c + 2] = __float_as_uint(b.x);
+            sv[c + 3] = __float_as_uint(b.y);
+          }
+        }
+        if (key0 + kKeys > sg.L.len_kv || (masked && key0 + kKeys > sg.off) || bad) {
+          // Visible columns as four words.
           int lim = sg.L.len_kv - 1;
           if (p.causal) lim = min(lim, sg.off + token);
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const int k0 = key0 + 32 * w, n = lim - k0 + 1;
-            uint32_t v = n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+            const int k0 = key0 + 32 * w, in = lim - k0 + 1;
+            uint32_t v = in <= 0 ? 0u : in >= 32 ? 0xFFFFFFFFu : (1u << in) - 1u;
             const int j0 = k0 - sg.off;
             if (p.tree_mask && j0 > -32 && live) {
               const uint32_t* words = p.tree_mask + sg.bi * p.tree_mask_stride + static_cast<int64_t>(token) * p.tree_words;
@@ -659,54 +693,37 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
                 if (pg < 0 || pg >= p.c.num_pages) v &= h ? 0x0000FFFFu : 0xFFFF0000u;
               }
             }
-            vis[w] = v;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((v >> c) & 1u)) sv[32 * w + c] = __float_as_uint(-INFINITY);
           }
         }
-        // The row's 128 scores come in halves of 64 columns: the second for its maximum, then the
-        // first, which stays for its exponentials, then the second again.  P takes the columns of
-        // the first quarter and then of the second, both read by then.
-        uint32_t sv[64];
-        auto load_half = [&](int h) {
-          tmem_ld32(s_addr + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-          tmem_ld32(s_addr + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-          tmem_ld_wait();
-          reg_fence32(&sv[0]);
-          reg_fence32(&sv[32]);
-          if (need) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (!(((h ? vis[2 + c / 32] : vis[c / 32]) >> (c % 32)) & 1u)) sv[c] = __float_as_uint(-INFINITY);
-          }
-        };
+        __syncwarp();
         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-        for (int h = 1; h >= 0; --h) {
-          load_half(h);
-#pragma unroll
-          for (int c = 0; c < 64; c += 8) {
-            mx0 = max3(mx0, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-            mx1 = max3(mx1, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
-            mx2 = max3(mx2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
-            mx3 = max3(mx3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
-          }
+        for (int c = 0; c < 128; c += 8) {
+          mx0 = max3(mx0, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+          mx1 = max3(mx1, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+          mx2 = max3(mx2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
+          mx3 = max3(mx3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
         }
-        const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cst, ev);
+        const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cs, ev);
         float alpha = 1.f;
         if (m_cand > m_ref + C::THRESH) {
           alpha = ex2(m_ref - m_cand);
           m_ref = m_cand;
         }
         const float nm = m_ref == -INFINITY ? 0.f : C::P_OFF - m_ref + ev;
-        const float2 cs2 = make_float2(cst, cst), nm2 = make_float2(nm, nm);
+        const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(nm, nm);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (h == 1) load_half(1);
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 4) {
-            const float2 x01 = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), cs2, nm2);
-            const float2 x23 = fma2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), cs2, nm2);
+            const uint32_t* x = &sv[64 * h + c];
+            const float2 x01 = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), cs2, nm2);
+            const float2 x23 = fma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), cs2, nm2);
             const float2 p01 = make_float2(ex2(x01.x), ex2(x01.y)), p23 = make_float2(ex2(x23.x), ex2(x23.y));
             acc0 = add2(acc0, p01);
             acc1 = add2(acc1, p23);
@@ -717,7 +734,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         }
         l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y)) * back;
         // The block before has added to O already: its P V was issued ahead of this block's S.
-        if (j > sg.tile0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (i > first && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t ov[32];
@@ -725,7 +742,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
             tmem_ld_wait();
             reg_fence32(ov);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
             tmem_st32(o_addr + c * 32, ov);
           }
         }
@@ -734,51 +751,63 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         mbar_arrive(&bars.p_full[t]);
       }
       if (!ok) break;
+      n_other += sg.split ? (n + t) / 2 : n;
+      n_tile += n;
       // ---- the next segment's Q, so that its first S runs while this one's results leave ----------
       Segment next;
-      more = advance(next, skip_tiles, skip_segs);
-      cs = more ? load_q(next) : 0.f;
+      more = walk.next(p, next);
+      if (more) {
+        // Where both warpgroups shared the rows, the other slot's last S has to be done with Q too.
+        if (sg.split && t == 0 && n > 1 && !mbar_wait_warp(&bars.s_full[1], (n_other - 1) & 1, wt)) { ok = false; break; }
+        cs = load_q(next);
+      }
       // ---- the segment's result: this thread's row ------------------------------------------------
-      if (!mbar_wait_warp(&bars.o_full[t], on & 1, wt)) { ok = false; break; }
-      ++on;
-      tc_fence_after();
-      const bool whole = sg.tile0 == 0 && sg.tile1 == sg.n_tiles;
+      const bool any = first < n;      // (one tile of keys alone: nothing for the second warpgroup)
+      if (any) {
+        if (!mbar_wait_warp(&bars.o_full[t], n_o & 1, wt)) { ok = false; break; }
+        ++n_o;
+        tc_fence_after();
+      }
+      const bool whole = !sg.split && sg.tile0 == 0 && sg.tile1 == sg.n_tiles;
       const int64_t part = 2 * blockIdx.x + (sg.tile0 == 0 ? 1 : 0);
       const bool none = !live || l == 0.f;
       const float inv = none ? 0.f : 1.f / l;
       const bool fix = live && s_found[n_seg % 8] == n_seg + 1;
       const int64_t out = row < p.rows ? row_offset(p, p.o_st, sg.bi, sg.hk, row) : 0;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; any && c < D / 32; ++c) {
         uint32_t ov[32];
+        __syncwarp();          // (the TMEM load is the whole warp's)
         tmem_ld32(o_addr + c * 32, ov);
         tmem_ld_wait();
         reg_fence32(ov);
-        if (row >= p.rows) continue;
-        if (fix) {
-          for (int i = 0; i < 32; ++i)
-            ov[i] = __float_as_uint(add_nonfinite<D, CT>(p, sg.bi, sg.hk, sg.L, row, c * 32 + i, sg.tile0 * kKeys,
-                                                         min(sg.tile1 * kKeys, sg.L.len_kv), __uint_as_float(ov[i])));
-        }
-        if (!whole) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o) + (part * (D / 4) + c * 8) * 256 + t * 128 + r;
+        if (row < p.rows) {
+          if (fix) {
+            for (int e = 0; e < 32; ++e)
+              ov[e] = __float_as_uint(add_nonfinite<D, CT>(p, sg.bi, sg.hk, sg.L, row, c * 32 + e, sg.tile0 * kKeys,
+                                                           min(sg.tile1 * kKeys, sg.L.len_kv), __uint_as_float(ov[e])));
+          }
+          if (!whole) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o) + (part * (D / 4) + c * 8) * 256 + t * 128 + r;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i * 256] = make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]), __uint_as_float(ov[4 * i + 2]),
-                                 __uint_as_float(ov[4 * i + 3]));
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + out + c * 32);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+            for (int e = 0; e < 8; ++e)
+              dst[e * 256] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                                         __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + out + c * 32);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float a = __uint_as_float(ov[8 * i + 2 * e]), b = __uint_as_float(ov[8 * i + 2 * e + 1]);
-              w[e] = none ? 0u : pack_pair<QT == kBF16>(a * inv, b * inv);
+              uint32_t w[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float a = __uint_as_float(ov[8 * e + 2 * x]), b = __uint_as_float(ov[8 * e + 2 * x + 1]);
+                w[x] = none ? 0u : pack_pair<QT == kBF16>(a * inv, b * inv);
+              }
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
+        __syncwarp();
       }
       if (row < p.rows) {
         if (!whole)
@@ -796,9 +825,11 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
   __syncthreads();
   // If a role gave up, copies may still be in flight: let them land before the CTA ends.
   if (producer && *abort_flag) {
-    constexpr int N = E4 ? C::NRAW : NS;
-    for (int k = (kv_issued > N ? kv_issued - N : 0); k < kv_issued; ++k)
-      mbar_wait_drain(E4 ? &bars.raw_full[k % N] : &bars.kv_full[k % N], (k / N) & 1);
+    constexpr int N = E4 ? NR : NV;
+    const int n_k = (issued + 1) / 2, n_v = issued / 2;
+    for (int k = (n_k > NK ? n_k - NK : 0); k < n_k; ++k) mbar_wait_drain(&bars.k_full[k % NK], (k / NK) & 1);
+    for (int k = (n_v > N ? n_v - N : 0); k < n_v; ++k)
+      mbar_wait_drain(E4 ? &bars.raw_full[k % N] : &bars.v_full[k % N], (k / N) & 1);
   }
   if (warp == 1) {
     tc_fence_after();
@@ -807,7 +838,8 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
 }
 
 // Joins the parts of blocks that more than one CTA worked on, and writes the rows that no key
-// reaches: 32 rows (lanes) by 32 elements (a warp has four) a CTA, in the parts' order.
+// reaches: 32 rows (lanes) by 32 elements (a warp has four) a CTA, in the parts' order.  A part of a
+// block of at most 128 rows is two, one of each warpgroup.
 template <int D, int QT>
 __global__ void __launch_bounds__(256) decode_wide_combine_kernel(const __grid_constant__ DecodeParams p, float p_off) {
   __shared__ uint2 s_out[32][9];
@@ -815,21 +847,32 @@ __global__ void __launch_bounds__(256) decode_wide_combine_kernel(const __grid_c
   const int groups = (min(p.rows, 256) + 31) / 32;
   const Parts u = find_parts(p, blockIdx.x / groups, lane);
   const int r = blockIdx.x % groups * 32 + lane, row = u.r0 + r, chunk = blockIdx.y * 8 + warp;
+  const bool split = p.rows - u.r0 <= 128;
   griddep_wait();   // (by every CTA, so that this grid never ends before the one it follows)
-  if (u.n == 1) return;
+  if (u.n == 1 && !split) return;
   const bool on = row < p.rows;
+  const int n = split ? 2 * u.n : u.n;
+  // Part k's place among [2 * ctas][256] rows of ml, and its float4 of O.
+  auto ml_of = [&](int k) {
+    const int64_t at = split ? u.part(k / 2) * 256 + k % 2 * 128 + r : u.part(k) * 256 + r;
+    return *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
+  };
+  auto o_of = [&](int k) {
+    const int64_t at = split ? (u.part(k / 2) * (D / 4) + chunk) * 256 + k % 2 * 128 + r : (u.part(k) * (D / 4) + chunk) * 256 + r;
+    return reinterpret_cast<const float4*>(p.part_o)[at];
+  };
   float m = -INFINITY, l = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   if (on) {
 #pragma unroll 4
-    for (int k = 0; k < u.n; ++k) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (u.part(k) * 256 + r));
+    for (int k = 0; k < n; ++k) {
+      const float2 ml = ml_of(k);
       if (ml.y != 0.f) m = fmaxf(m, ml.x);
     }
 #pragma unroll 4
-    for (int k = 0; k < u.n; ++k) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (u.part(k) * 256 + r));
-      const float4 v = reinterpret_cast<const float4*>(p.part_o)[(u.part(k) * (D / 4) + chunk) * 256 + r];
+    for (int k = 0; k < n; ++k) {
+      const float2 ml = ml_of(k);
+      const float4 v = o_of(k);
       const float f = part_weight(ml, m);
       l += ml.y * f;
       x.x += f == 0.f ? 0.f : v.x * f;
@@ -853,17 +896,17 @@ __global__ void __launch_bounds__(256) decode_wide_combine_kernel(const __grid_c
 
 template <int D, int CT, int QT>
 cudaError_t launch_t(const WideParams& wp, cudaStream_t st) {
+  using C = WideCfg<D, CT, QT>;
   auto kern = decode_wide_kernel<D, CT, QT>;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), WideCfg<D, CT>::SMEM);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   const DecodeParams& p = wp.d;
-  kern<<<p.ctas, WideCfg<D, CT>::THREADS, WideCfg<D, CT>::SMEM, st>>>(wp);
+  kern<<<p.ctas, kThreads, C::SMEM, st>>>(wp);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int groups = ((p.rows < 256 ? p.rows : 256) + 31) / 32;
   return launch_after(decode_wide_combine_kernel<D, QT>,
-                      dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles * groups, D / 32), dim3(256), st, p,
-                      WideCfg<D, CT>::P_OFF);
+                      dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles * groups, D / 32), dim3(256), st, p, C::P_OFF);
 }
 
 template <int D>
@@ -879,8 +922,6 @@ int decode_wide_box(int page_size) {
   while (page_size % box != 0) box /= 2;
   return box;
 }
-
-int decode_wide_swizzle(int d, int cache_dtype) { return cache_dtype == kE4M3 && d == 64 ? 64 : 128; }
 
 cudaError_t launch_decode_wide(const DecodeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, long long wait_limit,
                                int d, int qt, int ct, cudaStream_t st) {

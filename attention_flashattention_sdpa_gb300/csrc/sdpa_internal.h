@@ -193,9 +193,9 @@ int api_ok();
 int api_finish(cudaError_t e, cudaStream_t stream, const char* what);
 // Checks that a logical [b][h][s][d] view is 16-byte aligned with positive strides.
 int api_check_view(const char* name, const void* ptr, const int64_t (&st)[4], int b, int h, int s, int d, int es);
-// Tensor map of such a view: 128 (or 64) bytes of d x box_rows rows, 128-byte (64-byte) swizzle.
+// Tensor map of such a view: boxes of 128 bytes of d x box_rows rows, 128-byte swizzle.
 int api_make_map(CUtensorMap* map, const char* name, const void* ptr, const int64_t (&st)[4], int b, int h, int s,
-                 int d, int dt, int box_rows, int swizzle = 128);
+                 int d, int dt, int box_rows);
 int api_num_sms();
 int api_log_level();
 long long api_wait_limit();
@@ -284,11 +284,10 @@ void decode_plan(DecodeParams* p, int d, int cache_dtype, int num_sms);
 size_t decode_workspace_bytes(const DecodeParams& p, int d, size_t* ml_offset);
 cudaError_t launch_decode(const DecodeParams& p, int d, int q_dtype, int cache_dtype, cudaStream_t st);
 // Wide blocks: the main kernel, then the join of its parts.  Maps: boxes of decode_wide_box rows of
-// the cache, swizzled by decode_wide_swizzle bytes.
+// the cache (api_make_map).
 cudaError_t launch_decode_wide(const DecodeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, long long wait_limit,
                                int d, int q_dtype, int cache_dtype, cudaStream_t st);
 int decode_wide_box(int page_size);
-int decode_wide_swizzle(int d, int cache_dtype);
 uint32_t decode_take_device_error();
 
 }  // namespace sdpa

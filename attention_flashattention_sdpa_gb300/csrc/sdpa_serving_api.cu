@@ -349,12 +349,11 @@ sdpa_status_t sdpa_decode(const sdpa_cache_t* c, const sdpa_decode_t* p, const v
   if (prm.wide) {
     CUtensorMap tm_k, tm_v;
     const int box = sdpa::decode_wide_box(c->page_size);
-    const int swizzle = sdpa::decode_wide_swizzle(c->d, c->dtype);
     const sdpa_strides_t &ks = c->k_strides, &vs = c->v_strides;
     SDPA_TRY(static_cast<sdpa_status_t>(sdpa::api_make_map(&tm_k, "k cache", c->k, {ks.b, ks.h, ks.s, ks.d}, c->num_pages,
-                                                           c->h_kv, c->page_size, c->d, c->dtype, box, swizzle)));
+                                                           c->h_kv, c->page_size, c->d, c->dtype, box)));
     SDPA_TRY(static_cast<sdpa_status_t>(sdpa::api_make_map(&tm_v, "v cache", c->v, {vs.b, vs.h, vs.s, vs.d}, c->num_pages,
-                                                           c->h_kv, c->page_size, c->d, c->dtype, box, swizzle)));
+                                                           c->h_kv, c->page_size, c->d, c->dtype, box)));
     e = sdpa::launch_decode_wide(prm, tm_k, tm_v, sdpa::api_wait_limit(), c->d, p->dtype, c->dtype, stream);
   } else {
     e = sdpa::launch_decode(prm, c->d, p->dtype, c->dtype, stream);
