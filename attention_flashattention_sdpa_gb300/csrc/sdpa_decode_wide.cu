@@ -4,9 +4,9 @@
 // The split of the batch is that of sdpa_decode.cu with tiles of 128 keys and blocks of 256 rows:
 // one persistent CTA an SM walks an equal run of tiles, segment by segment (a segment: the part
 // of its run in one (sequence, KV head, block of rows)).  Roles:
-//   warp 0       pages and TMA: K and V tiles, box by box (a box lies in one page); boxes of missing
-//                pages and behind the sequence are filled with zeros.  E4M3: the scales follow by
-//                bulk copies.
+//   warps 0, 2   pages and TMA of K and of V, box by box (a box lies in one page), a lane a box; boxes
+//                of missing pages and behind the sequence are filled with zeros.  E4M3: the scales
+//                follow by bulk copies.  (One thread for all of them took 4200 cycles a tile.)
 //   warp 1       MMA issuer: S = Q K^T into TMEM, O += P V with P read from TMEM.
 //   warps 4-11   two softmax warpgroups; thread r owns a row: loads it into shared memory, the
 //                running max and sum, P, and the segment's results.  A block of more than 128 rows
@@ -38,8 +38,8 @@ template <int D, int CT, int QT>
 struct WideCfg {
   static constexpr bool E4 = CT == kE4M3;
   // Registers of the producer's, the softmax and the widening or clearing warpgroups, out of 128 a
-  // thread at launch: 64 + 2 x 184 + 80 = 4 x 128.
-  static constexpr int REGS0 = 64, REGS_SOFTMAX = 184, REGS_WIDEN = 80;
+  // thread at launch: 96 + 2 x 168 + 80 = 4 x 128.
+  static constexpr int REGS0 = 96, REGS_SOFTMAX = 168, REGS_WIDEN = 80;
   static constexpr int TILE = 128 * D * 2;                // a 16-bit tile of 128 rows
   static constexpr int RAW = 128 * 128;                   // an E4M3 tile: rows of 128 bytes (d = 64: half zeros)
   static constexpr int NCHUNK = D / 64;                   // 128-byte columns of a 16-bit tile
@@ -248,20 +248,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
   Segment sg;
 
   bool producer = false;
-  int issued = 0;          // tiles of K, and then of V, whose copies the producer issued
+  int issued = 0;          // tiles whose copies this producer issued
 
   if (warp < 4) {
     regs_dec<C::REGS0>();
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
       // ================================ pages and TMA =====================================
+      const bool is_v = warp == 2;
       producer = lane == 0;
-      if (lane == 0) {
-        tma_prefetch_desc(&wp.tm_k);
-        tma_prefetch_desc(&wp.tm_v);
-      }
-      bool ok = true;
-      int n_tile = 0;
+      const CUtensorMap* map = is_v ? &wp.tm_v : &wp.tm_k;
+      if (lane == 0) tma_prefetch_desc(map);
+      const int slots = is_v ? (E4 ? NR : NV) : NK;
+      uint64_t* full0 = is_v ? (E4 ? bars.raw_full : bars.v_full) : bars.k_full;
+      uint64_t* empty0 = is_v ? (E4 ? bars.raw_empty : bars.v_empty) : bars.k_empty;
+      uint8_t* dst0 = is_v ? (E4 ? sRaw : sV) : sK;
+      const int dst_step = is_v ? (E4 ? C::RAW : C::TILE) : C::K_TILE;
       const int boxes = kKeys / wp.box;     // boxes of a tile: 1, 2, 4 or 8
+      const unsigned all = (1u << boxes) - 1u;
+      // Lane x + 8 y issues copy y of box x: of 16-bit tiles the 128-byte columns, of E4M3 ones the
+      // codes, the scales of this tile (K's or V's) and, with K, those of V.
+      const int bx = lane % 8, by = lane / 8;
+      constexpr int kCopies = E4 ? 3 : C::NCHUNK;
+      bool ok = true;
+      int s = 0, turn = 0;
       while (ok && walk.next(p, sg)) {
         const int32_t* pages = p.c.page_table + sg.bi * p.c.page_table_stride;
         // Lane l: page and slot of box l of 32 consecutive boxes; missing ones get the page behind
@@ -280,57 +289,48 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
         };
         int page, slot, next_page, next_slot;
         look_up(0, next_page, next_slot);
-        for (int j = sg.tile0; ok && j < sg.tile1; ++j, ++n_tile) {
-          const int b0 = (j - sg.tile0) * boxes;
+        for (int b0 = 0; b0 < n_box; b0 += boxes) {
           if (b0 % 32 == 0) {
             page = next_page;
             slot = next_slot;
             look_up(b0 + 32, next_page, next_slot);
           }
-          const unsigned there = __ballot_sync(0xffffffffu, page < p.c.num_pages) >> (b0 % 32);   // bit x: box x exists
-          const int n_there = __popc(there & ((1u << boxes) - 1u));
-          for (int kv = 0; ok && kv < 2; ++kv) {
-            // Where this tile goes, and the barrier that counts its bytes.
-            const int s = n_tile % (kv ? (E4 ? NR : NV) : NK);
-            const int turn = n_tile / (kv ? (E4 ? NR : NV) : NK);
-            uint64_t* full = kv ? (E4 ? &bars.raw_full[s] : &bars.v_full[s]) : &bars.k_full[s];
-            uint64_t* empty = kv ? (E4 ? &bars.raw_empty[s] : &bars.v_empty[s]) : &bars.k_empty[s];
-            uint8_t* dst = kv ? (E4 ? sRaw + s * C::RAW : sV + s * C::TILE) : sK + s * C::K_TILE;
-            float* sc = kv ? sScV + s * 128 : sScK + n_tile % 8 * 256;
-            ok = mbar_wait_warp(empty, (turn & 1) ^ 1, wt);
-            if (!ok) break;
-            if constexpr (E4) {
-              if (n_there < boxes) {      // no scale where there is no key
-                for (int i = lane; i < kKeys; i += 32)
-                  if (!((there >> (i / wp.box)) & 1u)) {
-                    sc[i] = 0.f;
-                    if (!kv) sc[128 + i] = 0.f;
-                  }
-                __syncwarp();
-              }
-            }
-            if (lane == 0) {
-              mbar_arrive_expect_tx(full, E4 ? C::RAW + n_there * wp.box * (kv ? 4 : 8) : C::TILE);
-              ++issued;
-            }
-            for (int x = 0; x < boxes; ++x) {
-              const int pg = __shfl_sync(0xffffffffu, page, (b0 + x) % 32);
-              const int sl = __shfl_sync(0xffffffffu, slot, (b0 + x) % 32);
-              if (lane == 0) {
-                const CUtensorMap* map = kv ? &wp.tm_v : &wp.tm_k;
-                if constexpr (E4) {
-                  tma_load_4d(dst + x * wp.box * 128, map, full, 0, sl, sg.hk, pg);
-                  if (pg < p.c.num_pages) {
-                    const int64_t at = (static_cast<int64_t>(pg) * p.c.h_kv + sg.hk) * p.c.page_size + sl;
-                    if (!kv) bulk_load(sc + x * wp.box, p.c.k_scale + at, wp.box * 4, full);
-                    bulk_load(sc + (kv ? 0 : 128) + x * wp.box, p.c.v_scale + at, wp.box * 4, full);
-                  }
-                } else {
-                  for (int c = 0; c < C::NCHUNK; ++c)
-                    tma_load_4d(dst + c * 16384 + x * wp.box * 128, map, full, c * 64, sl, sg.hk, pg);
+          const int pg = __shfl_sync(0xffffffffu, page, (b0 + bx) % 32), sl = __shfl_sync(0xffffffffu, slot, (b0 + bx) % 32);
+          const unsigned there = __ballot_sync(0xffffffffu, pg < p.c.num_pages) & all;   // bit x: box x exists
+          if (!mbar_wait_warp(empty0 + s, (turn & 1) ^ 1, wt)) { ok = false; break; }
+          uint64_t* full = full0 + s;
+          uint8_t* dst = dst0 + s * dst_step;
+          float* sc = is_v ? sScV + s * 128 : sScK + issued % 8 * 256;
+          if constexpr (E4) {
+            if (there != all) {      // no scale where there is no key
+              for (int i = lane; i < kKeys; i += 32)
+                if (!((there >> (i / wp.box)) & 1u)) {
+                  sc[i] = 0.f;
+                  if (!is_v) sc[128 + i] = 0.f;
                 }
-              }
             }
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive_expect_tx(full, E4 ? C::RAW + __popc(there) * wp.box * (is_v ? 4 : 8) : C::TILE);
+          ++issued;
+          __syncwarp();
+          if (bx < boxes && by < kCopies) {
+            if constexpr (E4) {
+              if (by == 0) {
+                tma_load_4d(dst + bx * wp.box * 128, map, full, 0, sl, sg.hk, pg);
+              } else if (pg < p.c.num_pages && !(is_v && by == 2)) {
+                const float* src = is_v || by == 2 ? p.c.v_scale : p.c.k_scale;
+                bulk_load(sc + (by - 1) * 128 + bx * wp.box,
+                          src + (static_cast<int64_t>(pg) * p.c.h_kv + sg.hk) * p.c.page_size + sl, wp.box * 4, full);
+              }
+            } else {
+              tma_load_4d(dst + by * 16384 + bx * wp.box * 128, map, full, by * 64, sl, sg.hk, pg);
+            }
+          }
+          __syncwarp();
+          if (++s == slots) {
+            s = 0;
+            ++turn;
           }
         }
       }
@@ -647,26 +647,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
           ev = static_cast<float>(e);
           back = pow2(-e);
         }
-        uint32_t sv[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[c * 32]));
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) reg_fence32(&sv[c * 32]);
-        if constexpr (E4) {
-#pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            const float4 ks = *reinterpret_cast<const float4*>(sc + c);
-            const float2 a = mul2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), make_float2(ks.x, ks.y));
-            const float2 b = mul2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), make_float2(ks.z, ks.w));
-            sv[c] = __float_as_uint(a.x);
-            sv[c + 1] = __float_as_uint(a.y);
-            sv[c + 2] = __float_as_uint(b.x);
-            sv[c + 3] = __float_as_uint(b.y);
-          }
-        }
-        if (key0 + kKeys > sg.L.len_kv || (masked && key0 + kKeys > sg.off) || bad) {
-          // Visible columns as four words.
+        const bool need = key0 + kKeys > sg.L.len_kv || (masked && key0 + kKeys > sg.off) || bad;
+        uint32_t vis[4];       // visible columns
+        if (need) {
           int lim = sg.L.len_kv - 1;
           if (p.causal) lim = min(lim, sg.off + token);
 #pragma unroll
@@ -688,24 +671,55 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int key = k0 + 16 * h;
-                if (key >= sg.L.len_kv) continue;
-                const int pg = __ldg(pages + key / p.c.page_size);
-                if (pg < 0 || pg >= p.c.num_pages) v &= h ? 0x0000FFFFu : 0xFFFF0000u;
+                if (key < sg.L.len_kv) {
+                  const int pg = __ldg(pages + key / p.c.page_size);
+                  if (pg < 0 || pg >= p.c.num_pages) v &= h ? 0x0000FFFFu : 0xFFFF0000u;
+                }
               }
             }
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((v >> c) & 1u)) sv[32 * w + c] = __float_as_uint(-INFINITY);
+            vis[w] = v;
           }
+          __syncwarp();
         }
-        __syncwarp();
+        // The row's 128 scores come in halves of 64 columns: the second for its maximum, then the
+        // first, which stays for its exponentials, then the second again.  P takes the columns of
+        // the first quarter and then of the second, both read by then.
+        uint32_t sv[64];
+        auto load_half = [&](int h) {
+          tmem_ld32(s_addr + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+          tmem_ld32(s_addr + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+          tmem_ld_wait();
+          reg_fence32(&sv[0]);
+          reg_fence32(&sv[32]);
+          if constexpr (E4) {
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+              const float4 ks = *reinterpret_cast<const float4*>(sc + h * 64 + c);
+              const float2 a = mul2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), make_float2(ks.x, ks.y));
+              const float2 b = mul2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), make_float2(ks.z, ks.w));
+              sv[c] = __float_as_uint(a.x);
+              sv[c + 1] = __float_as_uint(a.y);
+              sv[c + 2] = __float_as_uint(b.x);
+              sv[c + 3] = __float_as_uint(b.y);
+            }
+          }
+          if (need) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (!((vis[2 * h + c / 32] >> (c % 32)) & 1u)) sv[c] = __float_as_uint(-INFINITY);
+          }
+        };
         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-          mx0 = max3(mx0, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-          mx1 = max3(mx1, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
-          mx2 = max3(mx2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
-          mx3 = max3(mx3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+        for (int h = 1; h >= 0; --h) {
+          load_half(h);
+#pragma unroll
+          for (int c = 0; c < 64; c += 8) {
+            mx0 = max3(mx0, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+            mx1 = max3(mx1, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+            mx2 = max3(mx2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
+            mx3 = max3(mx3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+          }
         }
         const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cs, ev);
         float alpha = 1.f;
@@ -718,12 +732,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          if (h == 1) load_half(1);
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 4) {
-            const uint32_t* x = &sv[64 * h + c];
-            const float2 x01 = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), cs2, nm2);
-            const float2 x23 = fma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), cs2, nm2);
+            const float2 x01 = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), cs2, nm2);
+            const float2 x23 = fma2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), cs2, nm2);
             const float2 p01 = make_float2(ex2(x01.x), ex2(x01.y)), p23 = make_float2(ex2(x23.x), ex2(x23.y));
             acc0 = add2(acc0, p01);
             acc1 = add2(acc1, p23);
@@ -825,11 +839,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
   __syncthreads();
   // If a role gave up, copies may still be in flight: let them land before the CTA ends.
   if (producer && *abort_flag) {
-    constexpr int N = E4 ? NR : NV;
-    const int n_k = (issued + 1) / 2, n_v = issued / 2;
-    for (int k = (n_k > NK ? n_k - NK : 0); k < n_k; ++k) mbar_wait_drain(&bars.k_full[k % NK], (k / NK) & 1);
-    for (int k = (n_v > N ? n_v - N : 0); k < n_v; ++k)
-      mbar_wait_drain(E4 ? &bars.raw_full[k % N] : &bars.v_full[k % N], (k / N) & 1);
+    const int n = warp == 0 ? NK : E4 ? NR : NV;
+    uint64_t* full = warp == 0 ? bars.k_full : E4 ? bars.raw_full : bars.v_full;
+    for (int k = (issued > n ? issued - n : 0); k < issued; ++k) mbar_wait_drain(full + k % n, (k / n) & 1);
   }
   if (warp == 1) {
     tc_fence_after();
