@@ -12,17 +12,17 @@
 //                running max and sum, P, and the segment's results.  A block of more than 128 rows
 //                has a 128-row tile for each; in a smaller one both take the same rows and every
 //                second tile of keys, so that one computes while the other's products run.
-//   warps 12-15  E4M3: widen V to F16 on its way from the TMA's stage to the ring; 16-bit: clear, in
-//                V tiles that end behind the sequence or hold drafted tokens, rows that do not exist
-//                and values that are not finite (a weight of zero does not hide a NaN in a product).
+//   warps 12-15  E4M3: widen K to F16 on its way from the TMA's stage to the ring (and warps 16-19 V);
+//                16-bit: clear, in V tiles that end behind the sequence or hold drafted tokens, rows
+//                that do not exist and values that are not finite (a weight of zero does not hide a
+//                NaN in a product).
 //
-// E4M3 K enters the products as it is stored.  Q is split into E4M3 terms q = q1 + q2 (+ q3 for F16),
-// each the rounding of what the ones before leave: 4 bits a term hold BF16's 8 (F16's 11), and two
-// E4M3 products cost what one 16-bit product does.  A key's scale multiplies its column of S.
-// V's codes are multiplied by scale / 2^E (E: the exponent of the tile's largest scale) as a sum of
-// two F16 factors, so one rounding to F16's 11 bits is left, whatever the scales; 2^E joins the
-// exponent of the weights.  (Splitting P the same way would lose weights below 2^-17 of a row's
-// largest; widening K too left the tile waiting: 3.3 us for 128 keys.)
+// E4M3: a tile's codes are multiplied by scale / 2^E (E: the exponent of the tile's largest scale) as
+// a sum of two F16 factors, so one rounding to F16's 11 bits is left, whatever the scales; 2^E of K
+// joins the factor on the scores and 2^E of V the exponent of the weights, both once a tile.
+// (K as stored against Q split into E4M3 terms was exact and spared its widening, but a key's scale
+// then multiplies each column of S in the softmax warps, which bound the tile: 2.8 us for 128 keys
+// by 256 rows.)
 //
 // Bound: the tensor cores (4 x 128 x 128 x d MMAs a block of two tiles) and the exponentials, as
 // the prompt's forward pass; reading the cache once bounds it for few rows.
@@ -32,29 +32,26 @@ namespace sdpa {
 namespace {
 
 constexpr int kKeys = 128;
-constexpr int kThreads = 512;
 
-template <int D, int CT, int QT>
+template <int D, int CT>
 struct WideCfg {
   static constexpr bool E4 = CT == kE4M3;
-  // Registers of the producer's, the softmax and the widening or clearing warpgroups, out of 128 a
-  // thread at launch: 96 + 2 x 168 + 80 = 4 x 128.
-  static constexpr int REGS0 = 96, REGS_SOFTMAX = 168, REGS_WIDEN = 80;
+  static constexpr int THREADS = E4 ? 640 : 512;
+  // Registers of the producers', the softmax and the widening or clearing warpgroups, out of 96
+  // (E4M3) or 128 a thread at launch: 64 + 2 x 152 + 2 x 56 = 5 x 96, 96 + 2 x 168 + 80 = 4 x 128.
+  static constexpr int REGS0 = E4 ? 64 : 96, REGS_SOFTMAX = E4 ? 152 : 168, REGS_WIDEN = E4 ? 56 : 80;
   static constexpr int TILE = 128 * D * 2;                // a 16-bit tile of 128 rows
   static constexpr int RAW = 128 * 128;                   // an E4M3 tile: rows of 128 bytes (d = 64: half zeros)
   static constexpr int NCHUNK = D / 64;                   // 128-byte columns of a 16-bit tile
-  static constexpr int TERMS = E4 ? (QT == kBF16 ? 2 : 3) : 1;   // of Q
-  static constexpr int Q_TERM = E4 ? RAW : TILE;          // one term of a tile of Q
-  static constexpr int Q_TILE = TERMS * Q_TERM;
-  static constexpr int K_TILE = E4 ? RAW : TILE;
-  static constexpr int NK = E4 ? 3 : (D == 128 ? 2 : 3);
-  static constexpr int NV = E4 ? (TERMS == 3 && D == 128 ? 1 : 2) : (D == 128 ? 2 : 3);
-  static constexpr int NR = E4 ? 2 : 0;                   // stages of V as loaded
-  static constexpr int SC_K = E4 ? 8 : 0;                 // scales of K and V, by tile count (1 KB each)
-  static constexpr int OFF_K = 2 * Q_TILE, OFF_V = OFF_K + NK * K_TILE, OFF_RAW = OFF_V + NV * TILE;
-  static constexpr int OFF_SCK = OFF_RAW + NR * RAW, OFF_SCV = OFF_SCK + SC_K * 1024;
-  static constexpr int SMEM = OFF_SCV + NR * 512 + 1024;
-  static constexpr int KSTEPS = E4 ? D / 32 : D / 16;     // MMAs of S, a term
+  // Slots of 16-bit K and V tiles, and stages of E4M3 K and V tiles with their scales (K's with those of
+  // V).  K and V have slots of their own: a wait for a parity may not skip phases, and in a ring of
+  // three that they shared, each would follow only every second phase of a slot.
+  static constexpr int NK = D == 128 ? (E4 ? 1 : 2) : (E4 ? 2 : 3), NV = D == 128 ? 2 : 3;
+  static constexpr int RK = E4 ? 2 : 0, RV = E4 ? (D == 128 ? 1 : 2) : 0;
+  static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + NK * TILE, OFF_RAW = OFF_V + NV * TILE;
+  static constexpr int OFF_SC = OFF_RAW + (RK + RV) * RAW;
+  static constexpr int SMEM = OFF_SC + (RK + RV) * 1024 + 1024;
+  static constexpr int KSTEPS = D / 16;
   static constexpr int O_COL0 = 256;
   static constexpr float P_OFF = CT == kBF16 ? 0.f : 6.f;
   static constexpr float THRESH = 8.f;
@@ -64,9 +61,8 @@ struct WideCfg {
 
 struct alignas(8) WideBarriers {
   uint64_t q_full[2];
-  uint64_t k_full[4], k_empty[4];
-  uint64_t v_full[4], v_empty[4], v_clean[4];
-  uint64_t raw_full[2], raw_empty[2];
+  uint64_t full[6], empty[6], clean[6];     // 16-bit tiles: K's slots, then V's
+  uint64_t raw_full[4], raw_empty[4];       // E4M3 tiles: K's stages, then V's
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t drain;
   uint32_t tmem_base;
@@ -138,10 +134,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes,
                : "memory");
 }
 
-__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-
 struct WideParams {
   DecodeParams d;
   CUtensorMap tm_k, tm_v;
@@ -152,23 +144,30 @@ struct WideParams {
 };
 
 template <int D, int CT, int QT>
-__global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_constant__ WideParams wp) {
-  using C = WideCfg<D, CT, QT>;
+__global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel(const __grid_constant__ WideParams wp) {
+  using C = WideCfg<D, CT>;
   constexpr bool E4 = C::E4;
   constexpr bool BF = CT == kBF16;     // type of the 16-bit operands
-  constexpr int NK = C::NK, NV = C::NV, NR = E4 ? C::NR : 1;
+  // Slot or stage of tile n of K or V, and the turn it is in there.
+  struct Place {
+    int at, turn;
+  };
+  auto slot_of = [](bool is_v, int n) { return is_v ? Place{C::NK + n % C::NV, n / C::NV} : Place{n % C::NK, n / C::NK}; };
+  auto stage_of = [](bool is_v, int n) {
+    if constexpr (E4) return is_v ? Place{C::RK + n % C::RV, n / C::RV} : Place{n % C::RK, n / C::RK};
+    else return Place{0, 0};
+  };
   const DecodeParams& p = wp.d;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sK = smem + C::OFF_K;
-  uint8_t* sV = smem + C::OFF_V;
+  uint8_t* sRing = smem + C::OFF_K;
   uint8_t* sRaw = smem + C::OFF_RAW;
-  float* sScK = reinterpret_cast<float*>(smem + C::OFF_SCK);   // [8][2][128]: of K and of V
-  float* sScV = reinterpret_cast<float*>(smem + C::OFF_SCV);   // [NR][128]
+  float* sSc = reinterpret_cast<float*>(smem + C::OFF_SC);   // [stage][2][128]
   __shared__ WideBarriers bars;
   __shared__ Walk s_walk;
+  __shared__ volatile int s_ek[8], s_ev[8];    // exponents of a tile's scales, by tile count
   __shared__ volatile int s_found[8];          // segment count + 1 of a segment with cleared values
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -217,15 +216,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
       mbar_init(&bars.s_full[t], 1);
       mbar_init(&bars.p_full[t], 128);
       mbar_init(&bars.o_full[t], 1);
-      mbar_init(&bars.raw_full[t], 1);
-      mbar_init(&bars.raw_empty[t], 128);
+    }
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(&bars.full[i], E4 ? 128 : 1);
+      mbar_init(&bars.empty[i], E4 ? 1 : 1 + 4);     // the MMAs that read the slot, and the clearing warps
+      mbar_init(&bars.clean[i], 128);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&bars.k_full[i], 1);
-      mbar_init(&bars.k_empty[i], 1);
-      mbar_init(&bars.v_full[i], E4 ? 128 : 1);
-      mbar_init(&bars.v_empty[i], E4 ? 1 : 1 + 4);   // the MMAs that read the slot, and the clearing warps
-      mbar_init(&bars.v_clean[i], 128);
+      mbar_init(&bars.raw_full[i], 1);
+      mbar_init(&bars.raw_empty[i], 128);
     }
     mbar_init(&bars.drain, 1);
     bars.abort = 0;
@@ -258,11 +257,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
       producer = lane == 0;
       const CUtensorMap* map = is_v ? &wp.tm_v : &wp.tm_k;
       if (lane == 0) tma_prefetch_desc(map);
-      const int slots = is_v ? (E4 ? NR : NV) : NK;
-      uint64_t* full0 = is_v ? (E4 ? bars.raw_full : bars.v_full) : bars.k_full;
-      uint64_t* empty0 = is_v ? (E4 ? bars.raw_empty : bars.v_empty) : bars.k_empty;
-      uint8_t* dst0 = is_v ? (E4 ? sRaw : sV) : sK;
-      const int dst_step = is_v ? (E4 ? C::RAW : C::TILE) : C::K_TILE;
       const int boxes = kKeys / wp.box;     // boxes of a tile: 1, 2, 4 or 8
       const unsigned all = (1u << boxes) - 1u;
       // Lane x + 8 y issues copy y of box x: of 16-bit tiles the 128-byte columns, of E4M3 ones the
@@ -270,7 +264,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
       const int bx = lane % 8, by = lane / 8;
       constexpr int kCopies = E4 ? 3 : C::NCHUNK;
       bool ok = true;
-      int s = 0, turn = 0;
       while (ok && walk.next(p, sg)) {
         const int32_t* pages = p.c.page_table + sg.bi * p.c.page_table_stride;
         // Lane l: page and slot of box l of 32 consecutive boxes; missing ones get the page behind
@@ -297,10 +290,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
           }
           const int pg = __shfl_sync(0xffffffffu, page, (b0 + bx) % 32), sl = __shfl_sync(0xffffffffu, slot, (b0 + bx) % 32);
           const unsigned there = __ballot_sync(0xffffffffu, pg < p.c.num_pages) & all;   // bit x: box x exists
-          if (!mbar_wait_warp(empty0 + s, (turn & 1) ^ 1, wt)) { ok = false; break; }
-          uint64_t* full = full0 + s;
-          uint8_t* dst = dst0 + s * dst_step;
-          float* sc = is_v ? sScV + s * 128 : sScK + issued % 8 * 256;
+          const Place at = E4 ? stage_of(is_v, issued) : slot_of(is_v, issued);
+          const int s = at.at;
+          if (!mbar_wait_warp(E4 ? &bars.raw_empty[s] : &bars.empty[s], (at.turn & 1) ^ 1, wt)) { ok = false; break; }
+          uint64_t* full = E4 ? &bars.raw_full[s] : &bars.full[s];
+          uint8_t* dst = E4 ? sRaw + s * C::RAW : sRing + s * C::TILE;
+          float* sc = sSc + s * 256;
           if constexpr (E4) {
             if (there != all) {      // no scale where there is no key
               for (int i = lane; i < kKeys; i += 32)
@@ -328,37 +323,31 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
             }
           }
           __syncwarp();
-          if (++s == slots) {
-            s = 0;
-            ++turn;
-          }
         }
       }
     } else if (warp == 1) {
       // ================================ MMA issuer ========================================
       if (elect_one_sync()) {
-        const uint32_t idesc_s = make_idesc(BF ? 1u : 0u, 128, 128, false, false);   // (0: F16 or E4M3)
+        const uint32_t idesc_s = make_idesc(BF ? 1u : 0u, 128, 128, false, false);
         const uint32_t idesc_pv = make_idesc(BF ? 1u : 0u, 128, D, false, true);
         bool ok = true;
         int nk = 0, nv = 0;               // tiles of K and V so far
         uint32_t clean_par = 0;           // by slot: parity of its next cleaning
         uint32_t q_par = 0, p_par = 0;    // by tile
-        auto wait_k = [&]() -> int {
-          const int s = nk % NK;
-          if (!mbar_wait(&bars.k_full[s], (nk / NK) & 1, wt)) return -1;
-          ++nk;
+        // Slots of the next tile of K and of V.
+        auto wait_tile = [&](Place x) -> int {
+          if (!mbar_wait(&bars.full[x.at], x.turn & 1, wt)) return -1;
           tc_fence_after();
-          return s;
+          return x.at;
         };
+        auto wait_k = [&]() -> int { return wait_tile(slot_of(false, nk++)); };
         auto wait_v = [&](bool cleaned) -> int {
-          const int s = nv % NV;
-          if (!mbar_wait(&bars.v_full[s], (nv / NV) & 1, wt)) return -1;
-          if (!E4 && cleaned) {
-            if (!mbar_wait(&bars.v_clean[s], (clean_par >> s) & 1, wt)) return -1;
+          const int s = wait_tile(slot_of(true, nv++));
+          if (!E4 && cleaned && s >= 0) {
+            if (!mbar_wait(&bars.clean[s], (clean_par >> s) & 1, wt)) return -1;
             clean_par ^= 1u << s;
+            tc_fence_after();
           }
-          ++nv;
-          tc_fence_after();
           return s;
         };
         auto wait_p = [&](int t) {
@@ -369,19 +358,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
         };
         // S of slot t from tile `tq` of Q.
         auto issue_s = [&](int t, int tq, int s) {
-          const uint32_t qa = smem_u32(sQ + tq * C::Q_TILE), kb = smem_u32(sK + s * C::K_TILE);
+          const uint32_t qa = smem_u32(sQ + tq * C::TILE), kb = smem_u32(sRing + s * C::TILE);
 #pragma unroll
-          for (int term = 0; term < C::TERMS; ++term)
-#pragma unroll
-            for (int k = 0; k < C::KSTEPS; ++k) {
-              const uint32_t o = (k / 4) * 16384 + (k % 4) * 32;
-              mma_ss(tmem + t * 128, make_sdesc_sw128(qa + term * C::Q_TERM + o, 16, 1024), make_sdesc_sw128(kb + o, 16, 1024),
-                     idesc_s, term + k > 0, E4);
-            }
+          for (int k = 0; k < C::KSTEPS; ++k) {
+            const uint32_t o = (k / 4) * 16384 + (k % 4) * 32;
+            mma_ss(tmem + t * 128, make_sdesc_sw128(qa + o, 16, 1024), make_sdesc_sw128(kb + o, 16, 1024), idesc_s, k > 0, false);
+          }
           tc_commit(&bars.s_full[t]);
         };
         auto issue_pv = [&](int t, int s, bool first) {
-          const uint32_t vb = smem_u32(sV + s * C::TILE);
+          const uint32_t vb = smem_u32(sRing + s * C::TILE);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             mma_ts(tmem + C::O_COL0 + t * D, tmem + t * 128 + k * 8, make_sdesc_sw128(vb + k * 16 * 128, 16384, 1024),
@@ -401,26 +387,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
               const int s = wait_k();
               if (s < 0) { ok = false; break; }
               issue_s(i, 0, s);
-              tc_commit(&bars.k_empty[s]);
+              tc_commit(&bars.empty[s]);
             }
             for (int i = 0; ok && i < n; ++i) {
               const int t = i & 1, vs = wait_v(needs_cleaning(p, sg, sg.tile0 + i));
               if (vs < 0 || !wait_p(t)) { ok = false; break; }
               issue_pv(t, vs, i < 2);
               if (i + 2 >= n) tc_commit(&bars.o_full[t]);
-              tc_commit(&bars.v_empty[vs]);
+              tc_commit(&bars.empty[vs]);
               if (i + 2 < n) {
                 const int s = wait_k();
                 if (s < 0) { ok = false; break; }
                 issue_s(t, 0, s);
-                tc_commit(&bars.k_empty[s]);
+                tc_commit(&bars.empty[s]);
               }
             }
           } else {
             const int k0 = wait_k();
             if (k0 < 0) { ok = false; break; }
             for (int t = 0; t < 2; ++t) issue_s(t, t, k0);
-            tc_commit(&bars.k_empty[k0]);
+            tc_commit(&bars.empty[k0]);
             for (int i = 0; ok && i < n; ++i) {
               const int vs = wait_v(needs_cleaning(p, sg, sg.tile0 + i));
               if (vs < 0) { ok = false; break; }
@@ -429,12 +415,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
                 if (!wait_p(t)) { ok = false; break; }
                 issue_pv(t, vs, i == 0);
                 if (i + 1 == n) tc_commit(&bars.o_full[t]);
-                if (t == 1) tc_commit(&bars.v_empty[vs]);
+                if (t == 1) tc_commit(&bars.empty[vs]);
                 if (i + 1 < n) {
                   if (t == 0) s = wait_k();
                   if (s < 0) { ok = false; break; }
                   issue_s(t, t, s);
-                  if (t == 1) tc_commit(&bars.k_empty[s]);
+                  if (t == 1) tc_commit(&bars.empty[s]);
                 }
               }
             }
@@ -454,24 +440,33 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
     while (ok && walk.next(p, sg)) {
       bool found = false;
       for (int j = sg.tile0; ok && j < sg.tile1; ++j, ++n_tile) {
-        const int s = n_tile % NV;
         const bool tail = masked && (j + 1) * kKeys > sg.off;
         const bool on = j * kKeys + r < sg.L.len_kv;
         if constexpr (E4) {
-          const int rs = n_tile % NR;
-          ok = mbar_wait_warp(&bars.raw_full[rs], (n_tile / NR) & 1, wt);
+          const bool is_v = warp >= 16;
+          const Place from = stage_of(is_v, n_tile), to = slot_of(is_v, n_tile);
+          const int rs = from.at, s = to.at, left = sg.L.len_kv - j * kKeys;
+          ok = mbar_wait_warp(&bars.raw_full[rs], from.turn & 1, wt);
           if (!ok) break;
-          const float* sc = sScV + rs * 128;
-          const int ev = largest_exponent(sc, sg.L.len_kv - j * kKeys, lane);   // (by every lane)
-          const float f = on ? sc[r] * pow2(-ev) : 0.f;
+          const float* sc = sSc + rs * 256;
+          const int ex = largest_exponent(sc, left, lane);
+          if (!is_v) {
+            const int ev = largest_exponent(sc + 128, left, lane);
+            if (threadIdx.x == 12 * 32) {
+              s_ek[n_tile % 8] = ex;
+              s_ev[n_tile % 8] = ev;
+            }
+          }
+          // scale / 2^E of the lane's row as two F16, each twice in a word
+          const float f = on ? sc[r] * pow2(-ex) : 0.f;
           const __half fh = __float2half_rn(f), fl = __float2half_rn(f - __half2float(fh));
           const __half2 h2 = __half2half2(fh), l2 = __half2half2(fl);
-          ok = mbar_wait_warp(&bars.v_empty[s], ((n_tile / NV) & 1) ^ 1, wt);
+          ok = mbar_wait_warp(&bars.empty[s], (to.turn & 1) ^ 1, wt);
           if (!ok) break;
           // A lane takes its row, 16 codes at a time; the swizzles of both tiles put the 8 rows of a
           // quarter-warp into 8 different 16-byte columns.
           const uint8_t* src = sRaw + rs * C::RAW + r * 128;
-          uint8_t* dst = sV + s * C::TILE + r * 128;
+          uint8_t* dst = sRing + s * C::TILE + r * 128;
 #pragma unroll
           for (int c0 = 0; c0 < D / 16; c0 += 4) {
             uint4 in[4];
@@ -491,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
                 const __half2 y = __hfma2(v, h2, __hmul2(v, l2));
                 out[e] = *reinterpret_cast<const uint32_t*>(&y);
               }
-              if (tail) {
+              if (is_v && tail) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) out[e] = finite_pair<false>(out[e], found);
               }
@@ -505,36 +500,41 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
           }
           if (found) s_found[n_seg % 8] = n_seg + 1;
           fence_proxy_async_smem();
-          mbar_arrive(&bars.v_full[s]);
+          mbar_arrive(&bars.full[s]);
           mbar_arrive(&bars.raw_empty[rs]);
         } else {
           // Every tile's phase is followed, and its slot returned, by these warps too: a parity says
           // nothing about a phase that lies further back or ahead.
-          ok = mbar_wait_warp(&bars.v_full[s], (n_tile / NV) & 1, wt);
-          if (!ok) break;
-          if (needs_cleaning(p, sg, j)) {
-            if (!on || tail) {
 #pragma unroll 1
-              for (int u = 0; u < D / 8; ++u) {
-                uint4* at = reinterpret_cast<uint4*>(sV + s * C::TILE + (u / 8) * 16384 + r * 128 + ((u % 8) ^ (r & 7)) * 16);
-                if (!on) {
-                  *at = make_uint4(0, 0, 0, 0);
-                } else {
-                  uint4 x = *at;
-                  x.x = finite_pair<BF>(x.x, found);
-                  x.y = finite_pair<BF>(x.y, found);
-                  x.z = finite_pair<BF>(x.z, found);
-                  x.w = finite_pair<BF>(x.w, found);
-                  *at = x;
+          for (int kv = 0; ok && kv < 2; ++kv) {
+            const Place x = slot_of(kv != 0, n_tile);
+            const int s = x.at;
+            ok = mbar_wait_warp(&bars.full[s], x.turn & 1, wt);
+            if (!ok) break;
+            if (kv && needs_cleaning(p, sg, j)) {
+              if (!on || tail) {
+#pragma unroll 1
+                for (int u = 0; u < D / 8; ++u) {
+                  uint4* at = reinterpret_cast<uint4*>(sRing + s * C::TILE + (u / 8) * 16384 + r * 128 + ((u % 8) ^ (r & 7)) * 16);
+                  if (!on) {
+                    *at = make_uint4(0, 0, 0, 0);
+                  } else {
+                    uint4 x = *at;
+                    x.x = finite_pair<BF>(x.x, found);
+                    x.y = finite_pair<BF>(x.y, found);
+                    x.z = finite_pair<BF>(x.z, found);
+                    x.w = finite_pair<BF>(x.w, found);
+                    *at = x;
+                  }
                 }
               }
+              if (found) s_found[n_seg % 8] = n_seg + 1;
+              fence_proxy_async_smem();
+              mbar_arrive(&bars.clean[s]);
             }
-            if (found) s_found[n_seg % 8] = n_seg + 1;
-            fence_proxy_async_smem();
-            mbar_arrive(&bars.v_clean[s]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.empty[s]);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.v_empty[s]);
         }
       }
       ++n_seg;
@@ -568,49 +568,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
 #pragma unroll
         for (int i = 0; i < D / 2; ++i) w[i] ^= 0x80008000u;
       }
-      uint8_t* q_row = sQ + t * C::Q_TILE + r * 128;
-      if constexpr (E4) {
-        // A power of two brings the largest element to [128, 256), half of E4M3's range; the terms
-        // are then exact down to 2^-10 (F16: 2^-7) of it, and off by 2^-19 of it below.
+      if constexpr (E4 && QT == kBF16) {
+        // To F16 by a power of two that brings the largest element to [256, 512).
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < D / 2; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-        const float big = QT == kBF16 ? __uint_as_float(m << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(m)));
-        const int ex = static_cast<int>(__float_as_uint(big) >> 23);     // (F16's subnormals are normal in fp32)
-        const int sh = (ex == 0 || ex == 255) ? 0 : min(127 + 7 - ex, 126);
-        // (E4M3 has no infinity: a row that holds one, or a NaN, becomes NaN.)
-        const float up = ex == 255 ? __uint_as_float(0x7FC00000u) : pow2(sh);
+        const int ex = static_cast<int>(m >> 7);
+        const int sh = (ex == 0 || ex == 255) ? 0 : min(127 + 8 - ex, 126);
+        const float up = pow2(sh);
         cs *= pow2(-sh);
-        if (store) {
 #pragma unroll
-          for (int u = 0; u < D / 16; ++u) {
-            uint32_t term[C::TERMS][4];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float2 f = unpack_pair<QT == kBF16>(w[u * 8 + i]);
-              f.x *= up;
-              f.y *= up;
-#pragma unroll
-              for (int k = 0; k < C::TERMS; ++k) {
-                const uint32_t c2 = e4m3_pair(f.x, f.y);
-                term[k][i / 2] = i % 2 ? term[k][i / 2] | (c2 << 16) : c2 & 0xFFFFu;
-                const float2 back = unpack_pair<false>(e4m3x2_to_f16x2(c2 & 0xFFFFu));
-                f.x -= back.x;
-                f.y -= back.y;
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < C::TERMS; ++k)
-              *reinterpret_cast<uint4*>(q_row + k * C::Q_TERM + (u ^ (r & 7)) * 16) =
-                  make_uint4(term[k][0], term[k][1], term[k][2], term[k][3]);
-          }
+        for (int i = 0; i < D / 2; ++i) {
+          const float2 f = unpack_pair<true>(w[i]);
+          w[i] = pack_pair<false>(f.x * up, f.y * up);
         }
-      } else if (store) {
+      }
+      if (store) {
+        uint8_t* q_row = sQ + t * C::TILE + r * 128;
 #pragma unroll
         for (int u = 0; u < D / 8; ++u)
           *reinterpret_cast<uint4*>(q_row + (u / 8) * 16384 + ((u % 8) ^ (r & 7)) * 16) = x[u];
-      }
-      if (store) {
         fence_proxy_async_smem();
         mbar_arrive(&bars.q_full[t]);
       }
@@ -639,11 +616,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
         if (!mbar_wait_warp(&bars.s_full[t], n_own & 1, wt)) { ok = false; break; }
         tc_fence_after();
         const int key0 = (sg.tile0 + i) * kKeys;
-        // E4M3: exponent of the tile's largest V scale (in the weights), and its way back out of l.
-        float ev = 0.f, back = 1.f;
-        const float* sc = sScK + (n_tile + i) % 8 * 256;
+        // E4M3: the tile's exponents, K's in the factor on the scores, V's in the weights' exponent and
+        // out of l again.
+        float cst = cs, ev = 0.f, back = 1.f;
         if constexpr (E4) {
-          const int e = largest_exponent(sc + 128, sg.L.len_kv - key0, lane);
+          cst = cs * pow2(s_ek[(n_tile + i) % 8]);
+          const int e = s_ev[(n_tile + i) % 8];
           ev = static_cast<float>(e);
           back = pow2(-e);
         }
@@ -691,18 +669,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
           tmem_ld_wait();
           reg_fence32(&sv[0]);
           reg_fence32(&sv[32]);
-          if constexpr (E4) {
-#pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-              const float4 ks = *reinterpret_cast<const float4*>(sc + h * 64 + c);
-              const float2 a = mul2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), make_float2(ks.x, ks.y));
-              const float2 b = mul2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), make_float2(ks.z, ks.w));
-              sv[c] = __float_as_uint(a.x);
-              sv[c + 1] = __float_as_uint(a.y);
-              sv[c + 2] = __float_as_uint(b.x);
-              sv[c + 3] = __float_as_uint(b.y);
-            }
-          }
           if (need) {
 #pragma unroll
             for (int c = 0; c < 64; ++c)
@@ -721,14 +687,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
             mx3 = max3(mx3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
           }
         }
-        const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cs, ev);
+        const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cst, ev);
         float alpha = 1.f;
         if (m_cand > m_ref + C::THRESH) {
           alpha = ex2(m_ref - m_cand);
           m_ref = m_cand;
         }
         const float nm = m_ref == -INFINITY ? 0.f : C::P_OFF - m_ref + ev;
-        const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(nm, nm);
+        const float2 cs2 = make_float2(cst, cst), nm2 = make_float2(nm, nm);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -839,9 +805,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_wide_kernel(const __grid_c
   __syncthreads();
   // If a role gave up, copies may still be in flight: let them land before the CTA ends.
   if (producer && *abort_flag) {
-    const int n = warp == 0 ? NK : E4 ? NR : NV;
-    uint64_t* full = warp == 0 ? bars.k_full : E4 ? bars.raw_full : bars.v_full;
-    for (int k = (issued > n ? issued - n : 0); k < issued; ++k) mbar_wait_drain(full + k % n, (k / n) & 1);
+    const int n = warp == 2 ? (E4 ? C::RV : C::NV) : (E4 ? C::RK : C::NK);
+    for (int k = max(issued - n, 0); k < issued; ++k) {
+      const Place x = E4 ? stage_of(warp == 2, k) : slot_of(warp == 2, k);
+      mbar_wait_drain(E4 ? &bars.raw_full[x.at] : &bars.full[x.at], x.turn & 1);
+    }
   }
   if (warp == 1) {
     tc_fence_after();
@@ -908,12 +876,12 @@ __global__ void __launch_bounds__(256) decode_wide_combine_kernel(const __grid_c
 
 template <int D, int CT, int QT>
 cudaError_t launch_t(const WideParams& wp, cudaStream_t st) {
-  using C = WideCfg<D, CT, QT>;
+  using C = WideCfg<D, CT>;
   auto kern = decode_wide_kernel<D, CT, QT>;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   const DecodeParams& p = wp.d;
-  kern<<<p.ctas, kThreads, C::SMEM, st>>>(wp);
+  kern<<<p.ctas, C::THREADS, C::SMEM, st>>>(wp);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int groups = ((p.rows < 256 ? p.rows : 256) + 31) / 32;
