@@ -288,6 +288,10 @@ def _stream(stream, like=None) -> int:
     global _RAW_STREAM
     if stream is not None:
         return int(stream)
+    if _RAW_STREAM and like is not None:
+        dev = like.get_device()
+        if dev >= 0:
+            return _RAW_STREAM(dev)
     import torch
     if _RAW_STREAM is None:
         _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", False)
@@ -415,74 +419,105 @@ def sdpa_rope_table(rot: int, base: float = 10000.0, *, scaling: str = "none", f
     return out.to(device), att.value
 
 
+def _bad(message: str):
+    raise ValueError(message)
+
+
+class _Lazy:
+    """What the calls below need of torch, looked up once (a call of a few µs is not to import or to
+    compare names)."""
+    torch = None
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.int32, cls.int64, cls.float32 = torch.int32, torch.int64, torch.float32
+        cls.words = (torch.int32, getattr(torch, "uint32", torch.int32))
+        cls.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        cls.torch = torch
+        try:
+            dtype_code(torch.empty(0, dtype=torch.float16))
+        except KeyError:      # pragma: no cover
+            pass
+        return cls
+
+
 def _code(t, name: str) -> int:
-    try:
-        return dtype_code(t)
-    except KeyError:
-        raise ValueError(f"{name}: dtype {t.dtype} is not one the library takes") from None
-
-
-def _need(ok: bool, message: str):
-    if not ok:
-        raise ValueError(message)
+    c = _DTYPES.get(t.dtype)
+    return _bad(f"{name}: dtype {t.dtype} is not one the library takes") if c is None else c
 
 
 def _launch(fn, stream, like, *args):
     """Calls ``fn(*args, stream)`` with the device of ``like`` current."""
-    import torch
-    dev = like.device.index
-    if dev == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream, like)))
+    dev = like.get_device()
+    if dev == _Lazy.device():
+        st = fn(*args, int(stream) if stream is not None else _stream(None, like))
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream, like)))
+        with _Lazy.torch.cuda.device(dev):
+            st = fn(*args, int(stream) if stream is not None else _stream(None, like))
+    if st != 0:
+        _check(st)
 
 
 def _same_device(like, *tensors):
-    dev = like.device
-    if dev.type != "cuda":
+    dev = like.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors must be on one device ({dev} and {t.device} given)")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be on one device ({like.device} and {t.device} given)")
 
 
-def _ints(t, name: str, shape, dtype: str = "torch.int32"):
-    """A dense integer tensor of this shape (and nothing where it is None)."""
-    if t is not None:
-        _need(str(t.dtype) == dtype and tuple(t.shape) == shape and t.is_contiguous(),
-              f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+def _dense(t, name: str, dtype, shape):
+    """A contiguous tensor of this type and shape; its address."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _positions(positions, b: int, s: int):
-    """(pointer, elements between batches) of positions [b, s], or [s] or [1, s] for every batch."""
+    """(address, elements between batches) of positions [b, s], or [s] or [1, s] for every batch."""
     if positions is None:
         return 0, 0
-    _need(str(positions.dtype) == "torch.int32" and tuple(positions.shape) in ((b, s), (1, s), (s,))
-          and (s == 1 or positions.stride(-1) == 1) and (positions.dim() == 1 or positions.stride(0) >= 0),
-          f"positions must be int32 of shape ({b}, {s}), (1, {s}) or ({s},) with a unit last stride")
-    shared = positions.dim() == 1 or (positions.shape[0] == 1 and b > 1)
-    return positions.data_ptr(), 0 if shared else positions.stride(0)
+    shape, stride = positions.shape, positions.stride()
+    if positions.dtype is not _Lazy.int32 or shape not in ((b, s), (1, s), (s,)) or (s > 1 and stride[-1] != 1):
+        raise ValueError(f"positions must be int32 of shape ({b}, {s}), (1, {s}) or ({s},) with a unit last stride")
+    return positions.data_ptr(), 0 if len(shape) == 1 or (shape[0] == 1 and b > 1) else stride[0]
+
+
+def _table(t, name: str):
+    if t.dtype is not _Lazy.int64 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be the int64 tensor of sdpa_rope_table")
+    return t.data_ptr(), 2 * t.shape[0]
 
 
 def _rope(fn, q, k, q_out, k_out, table, positions, interleaved, attn_factor, stream):
-    _need(q.dim() == 4, "tensors are logical [b, h, s, d] views")
-    b, h_q, s, d = q.shape
-    dt, h_k = _code(q, "q"), 0
-    _need(q_out.shape == q.shape and q_out.dtype == q.dtype, "q_out must have q's shape and dtype")
-    _need((k is None) == (k_out is None), "k and k_out go together")
+    if _Lazy.torch is None:
+        _Lazy.load()
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("tensors are logical [b, h, s, d] views")
+    b, h_q, s, d = shape
+    dtype = q.dtype
+    if q_out.shape != shape or q_out.dtype is not dtype:
+        raise ValueError("q_out must have q's shape and dtype")
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    h_k, k_ptr, k_out_ptr, k_st, k_out_st = 0, None, None, _NO_STRIDES, _NO_STRIDES
     if k is not None:
-        _need(k.dim() == 4 and k.shape[0] == b and k.shape[2:] == q.shape[2:] and k.dtype == q.dtype,
-              "k must be [b, h_k, s, d] with q's b, s, d and dtype")
-        _need(k_out.shape == k.shape and k_out.dtype == k.dtype, "k_out must have k's shape and dtype")
-        h_k = k.shape[1]
-    _need(str(table.dtype) == "torch.int64" and table.dim() == 1 and table.is_contiguous(),
-          "table must be the int64 tensor of sdpa_rope_table")
+        ks = k.shape
+        if len(ks) != 4 or ks[0] != b or ks[2] != s or ks[3] != d or k.dtype is not dtype:
+            raise ValueError("k must be [b, h_k, s, d] with q's b, s, d and dtype")
+        if k_out.shape != ks or k_out.dtype is not dtype:
+            raise ValueError("k_out must have k's shape and dtype")
+        h_k, k_ptr, k_out_ptr, k_st, k_out_st = ks[1], k.data_ptr(), k_out.data_ptr(), k.stride(), k_out.stride()
+    dt = _code(q, "q")
+    tab, rot = _table(table, "table")
     pos, pos_stride = _positions(positions, b, s)
     _same_device(q, k, q_out, k_out, table, positions)
-    p = _PACK_ROPE(b, h_q, h_k, s, d, 2 * table.shape[0], dt, 1 if interleaved else 0, float(attn_factor),
-                   table.data_ptr(), pos, pos_stride, *q.stride(), *_st4(k), *q_out.stride(), *_st4(k_out))
-    _launch(fn, stream, q, p, q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out))
+    p = _PACK_ROPE(b, h_q, h_k, s, d, rot, dt, 1 if interleaved else 0, attn_factor, tab, pos, pos_stride, *q.stride(), *k_st,
+                   *q_out.stride(), *k_out_st)
+    _launch(fn, stream, q, p, q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr)
 
 
 def sdpa_rope_fwd(q, k, q_out, k_out, table, positions=None, *, interleaved: bool = False,
@@ -502,30 +537,32 @@ def sdpa_rope_bwd(dq_out, dk_out, dq, dk, table, positions=None, *, interleaved:
 
 
 def _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale):
-    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype,
-          "k_cache and v_cache must be [pages, h_kv, page_size, d] views of one shape and dtype")
-    pages, h_kv, page_size, d = k_cache.shape
-    _need(page_table.dim() == 2 and str(page_table.dtype) == "torch.int32"
-          and (page_table.shape[1] == 1 or page_table.stride(1) == 1),
-          "page_table must be int32 [b, max_pages] with a unit last stride")
-    b, wide = page_table.shape
-    _ints(seq_lens_kv, "seq_lens_kv", (b,))
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _ints(t, n, (pages, h_kv, page_size), "torch.float32")
+    """The packed descriptor of a cache, its shape, and the number of sequences."""
+    if _Lazy.torch is None:
+        _Lazy.load()
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not k_cache.dtype:
+        raise ValueError("k_cache and v_cache must be [pages, h_kv, page_size, d] views of one shape and dtype")
+    pages, h_kv, page_size, d = shape
+    ts, tst = page_table.shape, page_table.stride()
+    if len(ts) != 2 or page_table.dtype is not _Lazy.int32 or (ts[1] > 1 and tst[1] != 1):
+        raise ValueError("page_table must be int32 [b, max_pages] with a unit last stride")
+    lens = _dense(seq_lens_kv, "seq_lens_kv", _Lazy.int32, ts[:1])
+    ks = 0 if k_scale is None else _dense(k_scale, "k_scale", _Lazy.float32, shape[:3])
+    vs = 0 if v_scale is None else _dense(v_scale, "v_scale", _Lazy.float32, shape[:3])
     _same_device(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
-    return _PACK_CACHE(pages, page_size, h_kv, d, _code(k_cache, "k_cache"), b, wide, k_cache.data_ptr(),
-                       v_cache.data_ptr(), *k_cache.stride(), *v_cache.stride(), _p0(k_scale), _p0(v_scale),
-                       page_table.data_ptr(), page_table.stride(0), seq_lens_kv.data_ptr())
+    return _PACK_CACHE(pages, page_size, h_kv, d, _code(k_cache, "k_cache"), ts[0], ts[1], k_cache.data_ptr(), v_cache.data_ptr(),
+                       *k_cache.stride(), *v_cache.stride(), ks, vs, page_table.data_ptr(), tst[0], lens), shape, ts[0]
 
 
-def _cache_rows(k, v, k_cache, page_table):
-    _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype,
-          "k and v must be [b, h_kv, s, d] views of one shape and dtype")
-    b, h, s, d = k.shape
-    _need(b == page_table.shape[0] and h == k_cache.shape[1] and d == k_cache.shape[3],
-          "k and v must have the cache's h_kv and d and a row of the page table for each sequence")
+def _cache_rows(k, v, k_cache, shape, n: int):
+    ks = k.shape
+    if len(ks) != 4 or v.shape != ks or v.dtype is not k.dtype:
+        raise ValueError("k and v must be [b, h_kv, s, d] views of one shape and dtype")
+    if ks[0] != n or ks[1] != shape[1] or ks[3] != shape[3]:
+        raise ValueError("k and v must have the cache's h_kv and d and a row of the page table for each sequence")
     _same_device(k_cache, k, v)
-    return b, s
+    return ks
 
 
 def sdpa_cache_write(k, v, k_cache, v_cache, page_table, seq_lens_kv, *, seq_lens_q=None, k_scale=None,
@@ -537,22 +574,20 @@ def sdpa_cache_write(k, v, k_cache, v_cache, page_table, seq_lens_kv, *, seq_len
     v_scale, fp32 [pages, h_kv, page_size]).  page_table: int32 [b, max_pages]; seq_lens_kv: int32 [b] tokens
     of each sequence with these; seq_lens_q: int32 [b] of them new (None: s).  Row i goes to position
     len_kv - len_q + i.  With ``rope_table`` K is rotated first (positions None: each row's position)."""
-    c = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
-    b, s = _cache_rows(k, v, k_cache, page_table)
-    _ints(seq_lens_q, "seq_lens_q", (b,))
-    _same_device(k_cache, seq_lens_q, rope_table, positions)
-    rope, at = None, 0
+    c, shape, n = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
+    b, _, s, _ = _cache_rows(k, v, k_cache, shape, n)
+    lens_q = 0 if seq_lens_q is None else _dense(seq_lens_q, "seq_lens_q", _Lazy.int32, (b,))
+    at = 0
     if rope_table is not None:
-        _need(str(rope_table.dtype) == "torch.int64" and rope_table.dim() == 1 and rope_table.is_contiguous(),
-              "rope_table must be the int64 tensor of sdpa_rope_table")
+        tab, rot = _table(rope_table, "rope_table")
         pos, pos_stride = _positions(positions, b, s)
-        rope = ctypes.create_string_buffer(_PACK_ROPE(
-            0, 0, 0, 0, 0, 2 * rope_table.shape[0], 0, 1 if interleaved else 0, float(attn_factor),
-            rope_table.data_ptr(), pos, pos_stride, *(_NO_STRIDES * 4)))
+        rope = ctypes.create_string_buffer(_PACK_ROPE(0, 0, 0, 0, 0, rot, 0, 1 if interleaved else 0, attn_factor, tab, pos,
+                                                      pos_stride, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES))
         at = ctypes.addressof(rope)
-    else:
-        _need(positions is None, "positions are those of a rope_table")
-    r = _PACK_ROWS(s, _code(k, "k"), *k.stride(), *v.stride(), _p0(seq_lens_q), at)
+    elif positions is not None:
+        raise ValueError("positions are those of a rope_table")
+    _same_device(k_cache, seq_lens_q, rope_table, positions)
+    r = _PACK_ROWS(s, _code(k, "k"), *k.stride(), *v.stride(), lens_q, at)
     _launch(lib.sdpa_cache_write, stream, k_cache, c, r, k.data_ptr(), v.data_ptr())
 
 
@@ -560,41 +595,42 @@ def sdpa_cache_read(k_cache, v_cache, page_table, seq_lens_kv, k, v, *, k_scale=
                     stream=None) -> None:
     """Reads positions 0 .. s-1 of each sequence into dense k, v ([b, h_kv, s, d], f16/bf16); rows at
     and behind its length are zeros.  Arguments as in :func:`sdpa_cache_write`."""
-    c = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
-    _, s = _cache_rows(k, v, k_cache, page_table)
-    r = _PACK_ROWS(s, _code(k, "k"), *k.stride(), *v.stride(), 0, 0)
+    c, shape, n = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
+    ks = _cache_rows(k, v, k_cache, shape, n)
+    r = _PACK_ROWS(ks[2], _code(k, "k"), *k.stride(), *v.stride(), 0, 0)
     _launch(lib.sdpa_cache_read, stream, k_cache, c, r, k.data_ptr(), v.data_ptr())
 
 
-def _decode(q, k_cache, page_table, o, seq_lens_q, attn_scale, causal, tree_mask):
-    _need(q.dim() == 4 and o.shape == q.shape and o.dtype == q.dtype, "q and o must be [b, h_q, s_q, d] views of one shape and dtype")
-    b, h_q, s_q, d = q.shape
-    _need(b == page_table.shape[0] and d == k_cache.shape[3], "q must have the cache's d and a row of the page table for each sequence")
-    _ints(seq_lens_q, "seq_lens_q", (b,))
-    stride = 0
+def _decode(q, k_cache, shape, n, o, seq_lens_q, attn_scale, causal, tree_mask):
+    qs = q.shape
+    if len(qs) != 4 or o.shape != qs or o.dtype is not q.dtype:
+        raise ValueError("q and o must be [b, h_q, s_q, d] views of one shape and dtype")
+    b, h_q, s_q, d = qs
+    if b != n or d != shape[3]:
+        raise ValueError("q must have the cache's d and a row of the page table for each sequence")
+    lens_q = 0 if seq_lens_q is None else _dense(seq_lens_q, "seq_lens_q", _Lazy.int32, (b,))
+    tree, tree_stride = 0, 0
     if tree_mask is not None:
-        words = (s_q + 31) // 32
-        _need(str(tree_mask.dtype) in ("torch.int32", "torch.uint32") and tree_mask.dim() == 3
-              and tree_mask.shape[0] in (1, b) and tree_mask.shape[1:] == (s_q, words)
-              and tree_mask[0].is_contiguous() and tree_mask.stride(0) >= 0,
-              f"tree_mask must be int32 ({b} or 1, {s_q}, {words}), dense in its last two dimensions")
-        stride = tree_mask.stride(0) if tree_mask.shape[0] == b and b > 1 else 0
+        ts, words = tree_mask.shape, (s_q + 31) // 32
+        st = tree_mask.stride()
+        if tree_mask.dtype not in _Lazy.words or ts not in ((b, s_q, words), (1, s_q, words)) \
+                or (words > 1 and st[2] != 1) or (s_q > 1 and st[1] != words):
+            raise ValueError(f"tree_mask must be int32 ({b} or 1, {s_q}, {words}), dense in its last two dimensions")
+        tree, tree_stride = tree_mask.data_ptr(), st[0] if ts[0] > 1 else 0
     _same_device(k_cache, q, o, seq_lens_q, tree_mask)
-    scale = 1.0 / math.sqrt(d) if attn_scale is None else float(attn_scale)
-    return _PACK_DECODE(h_q, s_q, _code(q, "q"), causal_code(causal), scale, *q.stride(), *o.stride(),
-                        _p0(seq_lens_q), _p0(tree_mask), stride)
+    return _PACK_DECODE(h_q, s_q, _code(q, "q"), causal_code(causal), 1.0 / math.sqrt(d) if attn_scale is None else attn_scale,
+                        *q.stride(), *o.stride(), lens_q, tree, tree_stride)
 
 
 def sdpa_decode_workspace_size(q, k_cache, v_cache, page_table, seq_lens_kv, *, k_scale=None, v_scale=None,
                                tree_mask=None) -> int:
     """Workspace bytes of :func:`sdpa_decode` for these sizes (whatever the lengths)."""
-    c = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
-    p = _decode(q, k_cache, page_table, q, None, 1.0, False, tree_mask)
-    n = ctypes.c_size_t(0)
-    import torch
-    with torch.cuda.device(q.device):
-        _check(lib.sdpa_decode_workspace_size(c, p, ctypes.byref(n)))
-    return n.value
+    c, shape, n = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
+    p = _decode(q, k_cache, shape, n, q, None, 1.0, False, tree_mask)
+    size = ctypes.c_size_t(0)
+    with _Lazy.torch.cuda.device(q.device):
+        _check(lib.sdpa_decode_workspace_size(c, p, ctypes.byref(size)))
+    return size.value
 
 
 def sdpa_decode(q, k_cache, v_cache, page_table, seq_lens_kv, o, lse=None, *, workspace, seq_lens_q=None,
@@ -607,11 +643,11 @@ def sdpa_decode(q, k_cache, v_cache, page_table, seq_lens_kv, o, lse=None, *, wo
     row i set where drafted token i sees drafted token j (itself among them); earlier positions are seen by
     all.  seq_lens_q: rows that take part (None: all).  workspace: sdpa_decode_workspace_size bytes, not
     shared with a call that may run at the same time."""
-    c = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
-    p = _decode(q, k_cache, page_table, o, seq_lens_q, attn_scale, causal, tree_mask)
-    if lse is not None:
-        _ints(lse, "lse", tuple(q.shape[:3]), "torch.float32")
-    _need(workspace is not None and workspace.is_contiguous(), "workspace must be a contiguous tensor")
+    c, shape, n = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
+    p = _decode(q, k_cache, shape, n, o, seq_lens_q, attn_scale, causal, tree_mask)
+    lse_ptr = None if lse is None else _dense(lse, "lse", _Lazy.float32, q.shape[:3])
+    if workspace is None or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor")
     _same_device(k_cache, lse, workspace)
-    _launch(lib.sdpa_decode, stream, k_cache, c, p, q.data_ptr(), o.data_ptr(), _ptr(lse), workspace.data_ptr(),
+    _launch(lib.sdpa_decode, stream, k_cache, c, p, q.data_ptr(), o.data_ptr(), lse_ptr, workspace.data_ptr(),
             workspace.numel() * workspace.element_size())

@@ -26,6 +26,8 @@
 //
 // Bound: the tensor cores (4 x 128 x 128 x d MMAs a block of two tiles) and the exponentials, as
 // the prompt's forward pass; reading the cache once bounds it for few rows.
+#include <type_traits>
+
 #include "sdpa_decode.cuh"
 
 namespace sdpa {
@@ -467,17 +469,11 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           // quarter-warp into 8 different 16-byte columns.
           const uint8_t* src = sRaw + rs * C::RAW + r * 128;
           uint8_t* dst = sRing + s * C::TILE + r * 128;
+          auto widen = [&](auto clear) {
 #pragma unroll
-          for (int c0 = 0; c0 < D / 16; c0 += 4) {
-            uint4 in[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              in[x] = *reinterpret_cast<const uint4*>(src + ((c0 + x) ^ (r & 7)) * 16);
-              if (!on) in[x] = make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+            for (int ch = 0; ch < D / 16; ++ch) {
+              const uint4 in = *reinterpret_cast<const uint4*>(src + (ch ^ (r & 7)) * 16);
+              const uint32_t w[4] = {in.x, in.y, in.z, in.w};
               uint32_t out[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
@@ -485,19 +481,18 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
                 const __half2 v = *reinterpret_cast<const __half2*>(&out[e]);
                 const __half2 y = __hfma2(v, h2, __hmul2(v, l2));
                 out[e] = *reinterpret_cast<const uint32_t*>(&y);
-              }
-              if (is_v && tail) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) out[e] = finite_pair<false>(out[e], found);
+                if constexpr (decltype(clear)::value) out[e] = on ? finite_pair<false>(out[e], found) : 0u;
               }
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int u = 2 * (c0 + x) + h;    // 16-byte unit of the 16-bit row
+                const int u = 2 * ch + h;          // 16-byte unit of the 16-bit row
                 *reinterpret_cast<uint4*>(dst + (u / 8) * 16384 + ((u % 8) ^ (r & 7)) * 16) =
                     make_uint4(out[4 * h], out[4 * h + 1], out[4 * h + 2], out[4 * h + 3]);
               }
             }
-          }
+          };
+          if (is_v && (tail || left < kKeys)) widen(std::true_type{});
+          else widen(std::false_type{});
           if (found) s_found[n_seg % 8] = n_seg + 1;
           fence_proxy_async_smem();
           mbar_arrive(&bars.full[s]);
