@@ -56,13 +56,19 @@ __device__ __forceinline__ int clamp_len(const int32_t* lens, int i, int top) {
   return lens ? min(max(__ldg(lens + i), 0), top) : top;
 }
 
-template <int DT>
-__device__ __forceinline__ void load_item(const void* base, int64_t row, int lo, int hi, float (&x)[16]) {
-  const uint16_t* p = static_cast<const uint16_t*>(base) + row;
+// An item of a row as it lies in memory, and widened.
+struct Raw {
   uint4 u[2];
-  u[0] = *reinterpret_cast<const uint4*>(p + lo);
-  u[1] = *reinterpret_cast<const uint4*>(p + hi);
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+};
+
+__device__ __forceinline__ Raw load_raw(const void* base, int64_t row, int lo, int hi) {
+  const uint16_t* p = static_cast<const uint16_t*>(base) + row;
+  return Raw{{*reinterpret_cast<const uint4*>(p + lo), *reinterpret_cast<const uint4*>(p + hi)}};
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack_item(const Raw& r, float (&x)[16]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(r.u);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 f = unpack16<DT>(w[i]);
@@ -122,28 +128,39 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
   if (!__any_sync(0xffffffffu, live)) return;
 
   RopeItem it{m * 16, m * 16 + 8, false};
+  if constexpr (ROPE == 1) it = rope_item(p.r, m);
+  const int h0 = grp * per, h_end = min(p.c.h_kv, h0 + per);
+  // A head's K and V are loaded while the one before it is worked on, the first while the angles
+  // are computed.
+  Raw k_next, v_next;
+  auto fetch = [&](int h) {
+    if (live && h < h_end) {
+      k_next = load_raw(p.k, bi * p.k_st[0] + h * p.k_st[1] + si * p.k_st[2], it.lo, it.hi);
+      v_next = load_raw(p.v, bi * p.v_st[0] + h * p.v_st[1] + si * p.v_st[2], m * 16, m * 16 + 8);
+    }
+  };
+  fetch(h0);
   int rpos = pos;
   float c[8], s[8];
   if constexpr (ROPE != 0) {
     if (p.r.positions && live) rpos = p.r.positions[bi * p.r.positions_stride + si];
   }
   if constexpr (ROPE == 1) {
-    it = rope_item(p.r, m);
     if (it.turned && live) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) rope_angle(p.r, __ldg(p.r.table + m * 8 + i), rpos, c[i], s[i]);
     }
   }
-  const int h_end = min(p.c.h_kv, (grp + 1) * per);
   // Every lane of the warp runs the same number of turns (the shuffles need them all).
   for (int j = 0; j < per; ++j) {
-    const int h = grp * per + j;
+    const int h = h0 + j;
     const bool on = live && h < h_end;
     float x[16], y[16];
+    const Raw k_now = k_next, v_now = v_next;
+    if (j + 1 < per) fetch(h + 1);
     if (on) {
-      const int64_t krow = bi * p.k_st[0] + h * p.k_st[1] + si * p.k_st[2];
-      load_item<DT>(p.k, krow, it.lo, it.hi, x);
-      load_item<DT>(p.v, bi * p.v_st[0] + h * p.v_st[1] + si * p.v_st[2], m * 16, m * 16 + 8, y);
+      unpack_item<DT>(k_now, x);
+      unpack_item<DT>(v_now, y);
       if constexpr (ROPE == 1) {
         if (it.turned) {
           if (p.r.interleaved) rope_turn(true, x, c, s);
@@ -152,6 +169,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
       }
       if constexpr (ROPE == 2) {
         // 16 neighbours; each finds its own partner and angle.
+        const int64_t krow = bi * p.k_st[0] + h * p.k_st[1] + si * p.k_st[2];
         const int half = p.r.rot / 2;
 #pragma unroll 1
         for (int i = 0; i < 16; ++i) {
@@ -178,46 +196,67 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
   }
 }
 
-// One thread: 16 elements of K and of V of one row.
+// One thread: 16 elements of K and of V of one token, for up to kReadHeads heads whose loads are in
+// flight together.
+constexpr int kReadHeads = 1;
+
 template <int D, int DT, int CT>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheRowsParams p) {
-  constexpr int LANES = D / 16;
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheRowsParams p, int groups) {
+  constexpr int LANES = D / 16, N = CT == kE4M3 ? 1 : 2;     // 16-byte loads of an item
   const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int m = static_cast<int>(idx % LANES);
   const int64_t row = idx / LANES;
-  const int h = static_cast<int>(row % p.c.h_kv);
-  const int64_t tok = row / p.c.h_kv;
+  const int h0 = static_cast<int>(row % groups) * kReadHeads;
+  const int64_t tok = row / groups;
   if (tok >= static_cast<int64_t>(p.c.b) * p.s) return;
   const int bi = static_cast<int>(tok / p.s), si = static_cast<int>(tok % p.s);
   Slot at{-1, 0};
   if (si < clamp_len(p.c.seq_lens_kv, bi, p.c.max_len)) at = find_slot(p.c, bi, si);
+  uint4 in[kReadHeads][2][N];
+  float scale[kReadHeads][2];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (at.page >= 0) {
-      const int64_t* st = t ? p.c.v_st : p.c.k_st;
-      const uint8_t* src = (t ? p.c.v : p.c.k) + at.page * st[0] + h * st[1] + at.slot * st[2];
+  for (int j = 0; j < kReadHeads; ++j)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      scale[j][t] = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) in[j][t][i] = make_uint4(0, 0, 0, 0);
+      const int h = h0 + j;
+      if (at.page >= 0 && h < p.c.h_kv) {
+        const int64_t* st = t ? p.c.v_st : p.c.k_st;
+        const uint8_t* src = (t ? p.c.v : p.c.k) + at.page * st[0] + h * st[1] + at.slot * st[2] + m * 16 * N;
+#pragma unroll
+        for (int i = 0; i < N; ++i) in[j][t][i] = __ldg(reinterpret_cast<const uint4*>(src + i * 16));
+        if constexpr (CT == kE4M3)
+          scale[j][t] = __ldg((t ? p.c.v_scale : p.c.k_scale) + (at.page * p.c.h_kv + h) * p.c.page_size + at.slot);
+      }
+    }
+#pragma unroll
+  for (int j = 0; j < kReadHeads; ++j)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int h = h0 + j;
+      if (h >= p.c.h_kv) continue;
+      uint4 out[2];
       if constexpr (CT == kE4M3) {
-        const float scale = __ldg((t ? p.c.v_scale : p.c.k_scale) + (at.page * p.c.h_kv + h) * p.c.page_size + at.slot);
-        const uint4 in = __ldg(reinterpret_cast<const uint4*>(src + m * 16));
-        const uint32_t iw[4] = {in.x, in.y, in.z, in.w};
+        const uint4 x = in[j][t][0];
+        const uint32_t iw[4] = {x.x, x.y, x.z, x.w};
         uint32_t* ow = reinterpret_cast<uint32_t*>(out);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(iw[i / 2] >> (16 * (i % 2))), __NV_E4M3);
           const float2 f = __half22float2(__half2(hr));
-          ow[i] = pack16<DT>(f.x * scale, f.y * scale);
+          ow[i] = pack16<DT>(f.x * scale[j][t], f.y * scale[j][t]);
         }
       } else {
-        out[0] = __ldg(reinterpret_cast<const uint4*>(src + m * 32));
-        out[1] = __ldg(reinterpret_cast<const uint4*>(src + m * 32 + 16));
+        out[0] = in[j][t][0];
+        out[1] = in[j][t][N - 1];
       }
+      const int64_t* st = t ? p.v_st : p.k_st;
+      uint16_t* dst = static_cast<uint16_t*>(t ? p.v : p.k) + bi * st[0] + h * st[1] + si * st[2] + m * 16;
+      reinterpret_cast<uint4*>(dst)[0] = out[0];
+      reinterpret_cast<uint4*>(dst)[1] = out[1];
     }
-    const int64_t* st = t ? p.v_st : p.k_st;
-    uint16_t* dst = static_cast<uint16_t*>(t ? p.v : p.k) + bi * st[0] + h * st[1] + si * st[2] + m * 16;
-    reinterpret_cast<uint4*>(dst)[0] = out[0];
-    reinterpret_cast<uint4*>(dst)[1] = out[1];
-  }
 }
 
 template <int D, int DT, int CT>
@@ -237,9 +276,10 @@ cudaError_t write_t(const CacheRowsParams& p, int num_sms, cudaStream_t st) {
 
 template <int D, int DT, int CT>
 cudaError_t read_t(const CacheRowsParams& p, cudaStream_t st) {
-  const int64_t blocks = (static_cast<int64_t>(p.c.b) * p.s * p.c.h_kv * (D / 16) + kThreads - 1) / kThreads;
+  const int groups = (p.c.h_kv + kReadHeads - 1) / kReadHeads;
+  const int64_t blocks = (static_cast<int64_t>(p.c.b) * p.s * groups * (D / 16) + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  cache_read_kernel<D, DT, CT><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
+  cache_read_kernel<D, DT, CT><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p, groups);
   return cudaGetLastError();
 }
 

@@ -3,8 +3,9 @@
 // backward pass turns the other way).
 //
 // Bound: memory, 4 bytes an element.  A thread owns 16 elements of a token's head (8 pairs:
-// two 16-byte loads and stores) and walks several heads of that token, so that the 8 angles
-// are computed once for all of them.
+// two 16-byte loads and stores) and walks 8 heads of that token, so that the 8 angles are computed
+// once for all of them.  Measured at 2 x 8192 tokens, 16 + 16 heads of 128: 43.7 us, 6.14 TB/s, 91% of
+// a copy; 4 or 2 heads a thread 46-55 us, the first loads ahead of the angles 46-52.
 #include "sdpa_rope.cuh"
 
 namespace sdpa {
@@ -24,28 +25,35 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   if (grp >= groups) return;
   const int bi = static_cast<int>(tok / p.s), si = static_cast<int>(tok % p.s);
   const RopeItem it = rope_item(p.r, m);
+  const int h1 = min(p.h_all, (grp + 1) * per);
+  auto row_of = [&](int h, bool out) {
+    const int t = h >= p.h_q;
+    const int64_t(&st)[3] = out ? p.out_st[t] : p.in_st[t];
+    const int64_t at = bi * st[0] + (h - (t ? p.h_q : 0)) * st[1] + si * st[2];
+    return static_cast<uint16_t*>(out ? p.out[t] : const_cast<void*>(p.in[t])) + at;
+  };
+  uint4 u[kUnroll][2];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      if (h0 + j >= h1) continue;
+      const uint16_t* row = row_of(h0 + j, false);
+      u[j][0] = *reinterpret_cast<const uint4*>(row + it.lo);
+      u[j][1] = *reinterpret_cast<const uint4*>(row + it.hi);
+    }
+  };
   float c[8], s[8];
   if (it.turned) {
     const int pos = p.r.positions ? p.r.positions[bi * p.r.positions_stride + si] : si;
 #pragma unroll
     for (int i = 0; i < 8; ++i) rope_angle(p.r, __ldg(p.r.table + m * 8 + i), pos, c[i], s[i]);
   }
-  const int h1 = min(p.h_all, (grp + 1) * per);
   for (int h0 = grp * per; h0 < h1; h0 += kUnroll) {
-    uint4 u[kUnroll][2];
+    load(h0);
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-      const int h = h0 + j, t = h >= p.h_q;
-      if (h >= h1) continue;
-      const uint16_t* row = static_cast<const uint16_t*>(p.in[t]) + bi * p.in_st[t][0] +
-                            (h - (t ? p.h_q : 0)) * p.in_st[t][1] + si * p.in_st[t][2];
-      u[j][0] = *reinterpret_cast<const uint4*>(row + it.lo);
-      u[j][1] = *reinterpret_cast<const uint4*>(row + it.hi);
-    }
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      const int h = h0 + j, t = h >= p.h_q;
-      if (h >= h1 || (!it.turned && p.in_place[t])) continue;
+      const int h = h0 + j;
+      if (h >= h1 || (!it.turned && p.in_place[h >= p.h_q])) continue;
       uint32_t* w = reinterpret_cast<uint32_t*>(u[j]);
       if (it.turned) {
         float x[16];
@@ -59,8 +67,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = pack16<DT>(x[2 * i], x[2 * i + 1]);
       }
-      uint16_t* row = static_cast<uint16_t*>(p.out[t]) + bi * p.out_st[t][0] +
-                      (h - (t ? p.h_q : 0)) * p.out_st[t][1] + si * p.out_st[t][2];
+      uint16_t* row = row_of(h, true);
       *reinterpret_cast<uint4*>(row + it.lo) = u[j][0];
       *reinterpret_cast<uint4*>(row + it.hi) = u[j][1];
     }
