@@ -78,15 +78,50 @@ __device__ __forceinline__ long long tiles_before(const DecodeParams& p, int n, 
   return t;
 }
 
-// CTAs that have a run: no more than tiles, so that none of them is empty.
-__device__ __forceinline__ int working_ctas(const DecodeParams& p, long long total) {
-  return total < p.ctas ? static_cast<int>(total) : p.ctas;
+// Teams that have a run: no more than tiles, so that none of them is empty.
+__device__ __forceinline__ int working_teams(const DecodeParams& p, long long total) {
+  return total < p.teams ? static_cast<int>(total) : p.teams;
 }
 
-// First tile of CTA c's run, and the CTA whose run holds tile t, of `total` tiles over g CTAs.
+// First tile of team c's run, and the team whose run holds tile t, of `total` tiles over g teams.
 __device__ __forceinline__ long long run_start(long long total, int c, int g) { return total * c / g; }
-__device__ __forceinline__ int cta_of(long long total, long long t, int g) {
+__device__ __forceinline__ int team_of(long long total, long long t, int g) {
   return static_cast<int>(((t + 1) * g - 1) / total);
+}
+
+// The run of this CTA's team, and the sequence that holds its first tile; by a whole warp.
+struct Run {
+  long long t, t_end, base;     // tiles [t, t_end) of the batch; base: the first of sequence bi
+  int bi;
+};
+
+__device__ __forceinline__ Run find_run(const DecodeParams& p, int team, int lane) {
+  Run r{0, 0, 0, 0};
+  const long long total = tiles_before(p, p.c.b, lane);
+  const int g = working_teams(p, total);
+  if (team >= g) return r;
+  r.t = run_start(total, team, g);
+  r.t_end = run_start(total, team + 1, g);
+  for (;;) {
+    const int i = r.bi + lane;
+    const long long n = i < p.c.b ? seq_tiles(p, i) : 0;
+    long long incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, r.base + incl > r.t);
+    if (hit != 0) {
+      const int k = __ffs(hit) - 1;
+      r.base += __shfl_sync(0xffffffffu, incl - n, k);
+      r.bi += k;
+      return r;
+    }
+    r.base += __shfl_sync(0xffffffffu, incl, 31);
+    r.bi += 32;
+    if (r.bi >= p.c.b) return Run{0, 0, 0, 0};   // not reached: t < total
+  }
 }
 
 // Element offset of query row r (token r / group, head hk * group + r % group).
@@ -144,30 +179,33 @@ __device__ __noinline__ float add_nonfinite(const DecodeParams& p, int bi, int h
 
 // ---- joining partial results ---------------------------------------------------------------------
 
-// The parts of one block of rows: CTAs c0 .. c0 + n - 1 of the launch (n = 0: no key reaches it).
+// The parts of one block of rows: teams c0 .. c0 + n - 1 (n = 0: no key reaches it).
 struct Parts {
   int bi, hk, r0, c0, n;
+  int blk, blocks;       // block of rows among those of a sequence
   SeqLens L;
-  // Part k among [2 * ctas]: the first holds the block's first tile and is that CTA's second part.
-  __device__ __forceinline__ int64_t part(int k) const { return 2 * (c0 + k) + (k == 0 ? 1 : 0); }
+  // Part k among [2 * ctas]: the first holds the sequence's first tile and is its CTA's second part.
+  __device__ __forceinline__ int64_t part(int k) const {
+    return 2 * (static_cast<int64_t>(c0 + k) * blocks + blk) + (k == 0 ? 1 : 0);
+  }
 };
 
 // By a whole warp.
 __device__ __forceinline__ Parts find_parts(const DecodeParams& p, int unit, int lane) {
   Parts u;
-  const int per_seq = p.c.h_kv * p.row_tiles, blk = unit % per_seq;
-  u.bi = unit / per_seq;
-  u.hk = blk / p.row_tiles;
-  u.r0 = blk % p.row_tiles * p.tile_rows;
+  u.blocks = p.c.h_kv * p.row_tiles;
+  u.blk = unit % u.blocks;
+  u.bi = unit / u.blocks;
+  u.hk = u.blk / p.row_tiles;
+  u.r0 = u.blk % p.row_tiles * p.tile_rows;
   u.L = seq_lens(p, u.bi);
   u.c0 = u.n = 0;
   const int n_tiles = seq_tiles(p, u.bi);
   if (n_tiles > 0) {
-    const long long total = tiles_before(p, p.c.b, lane) * per_seq;
-    const long long t0 = tiles_before(p, u.bi, lane) * per_seq + static_cast<long long>(blk) * n_tiles;
-    const int g = working_ctas(p, total);
-    u.c0 = cta_of(total, t0, g);
-    u.n = cta_of(total, t0 + n_tiles - 1, g) - u.c0 + 1;
+    const long long total = tiles_before(p, p.c.b, lane), t0 = tiles_before(p, u.bi, lane);
+    const int g = working_teams(p, total);
+    u.c0 = team_of(total, t0, g);
+    u.n = team_of(total, t0 + n_tiles - 1, g) - u.c0 + 1;
   }
   return u;
 }

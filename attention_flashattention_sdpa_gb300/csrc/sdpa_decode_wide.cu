@@ -2,8 +2,8 @@
 // and short chunks whose s_q tokens times the heads of a group fill tcgen05 tiles.
 //
 // The split of the batch is that of sdpa_decode.cu with tiles of 128 keys and blocks of 256 rows:
-// one persistent CTA an SM walks an equal run of tiles, segment by segment (a segment: the part
-// of its run in one (sequence, KV head, block of rows)).  Roles:
+// one persistent CTA an SM walks a run of tiles for its KV head and block of rows, segment by segment
+// (a segment: the part of the run in one sequence).  Roles:
 //   warps 0, 2   pages and TMA of K and of V, box by box (a box lies in one page), a lane a box; boxes
 //                of missing pages and behind the sequence are filled with zeros.  E4M3: the scales
 //                follow by bulk copies.  (One thread for all of them took 4200 cycles a tile.)
@@ -66,43 +66,35 @@ struct alignas(8) WideBarriers {
   uint64_t full[6], empty[6], clean[6];     // 16-bit tiles: K's slots, then V's
   uint64_t raw_full[4], raw_empty[4];       // E4M3 tiles: K's stages, then V's
   uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t ml_full, o1_free;                // split: the second warpgroup's maxima and sums are there; its O is read
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
 };
 
-// A part of this CTA's run: tiles [tile0, tile1) of one (sequence, KV head, block of rows).
+// A part of this CTA's run: tiles [tile0, tile1) of one sequence.
 struct Segment {
-  int bi, hk, r0, n_tiles, tile0, tile1, off;
+  int bi, n_tiles, tile0, tile1, off;
   SeqLens L;
-  bool split;     // at most 128 rows: the warpgroups take every second tile of keys
 };
 
 // The run's position; every role walks it by itself.
-struct Walk {
-  long long t, t_end, base;
-  int bi;
+struct Walk : Run {
   __device__ __forceinline__ bool next(const DecodeParams& p, Segment& g) {
-    const int per_seq = p.c.h_kv * p.row_tiles;
     while (t < t_end) {
       const int n = seq_tiles(p, bi);
-      if (t >= base + static_cast<long long>(n) * per_seq) {
-        base += static_cast<long long>(n) * per_seq;
+      if (t >= base + n) {
+        base += n;
         ++bi;
         continue;
       }
-      const int blk = static_cast<int>((t - base) / n);
-      const long long t0 = base + static_cast<long long>(blk) * n;
       g.bi = bi;
-      g.hk = blk / p.row_tiles;
-      g.r0 = blk % p.row_tiles * 256;
       g.n_tiles = n;
-      g.tile0 = static_cast<int>(t - t0);
-      g.tile1 = static_cast<int>(min(static_cast<long long>(n), t_end - t0));
+      g.tile0 = static_cast<int>(t - base);
+      g.tile1 = static_cast<int>(min(static_cast<long long>(n), t_end - base));
       g.L = seq_lens(p, bi);
       g.off = g.L.len_kv - g.L.len_q;
-      g.split = p.rows - g.r0 <= 128;
-      t = t0 + g.tile1;
+      t = base + g.tile1;
       return true;
     }
     return false;
@@ -170,46 +162,18 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
   __shared__ WideBarriers bars;
   __shared__ Walk s_walk;
   __shared__ volatile int s_ek[8], s_ev[8];    // exponents of a tile's scales, by tile count
+  __shared__ float2 s_ml[128];                 // split: the second warpgroup's maximum and sum of each row
   __shared__ volatile int s_found[8];          // segment count + 1 of a segment with cleared values
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-  // ---- set-up: this CTA's run ----------------------------------------------------------------
-  const int per_seq = p.c.h_kv * p.row_tiles;
+  // ---- set-up: this CTA's block of rows, the same of every sequence, and its team's run ----------
+  const int blocks = p.c.h_kv * p.row_tiles, blk = blockIdx.x % blocks;
+  const int hk = blk / p.row_tiles, r0 = blk % p.row_tiles * 256;
+  const bool split = p.rows - r0 <= 128;   // at most 128 rows: the warpgroups take every second tile of keys
   if (warp == 0) {
-    const long long total = tiles_before(p, p.c.b, lane) * per_seq;
-    const int n_cta = working_ctas(p, total);
     Walk w;
-    w.t = w.t_end = 0;
-    w.base = 0;
-    w.bi = 0;
-    if (static_cast<int>(blockIdx.x) < n_cta) {
-      w.t = run_start(total, blockIdx.x, n_cta);
-      w.t_end = run_start(total, blockIdx.x + 1, n_cta);
-      for (;;) {
-        const int i = w.bi + lane;
-        const long long n = i < p.c.b ? static_cast<long long>(seq_tiles(p, i)) * per_seq : 0;
-        long long incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += x;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, w.base + incl > w.t);
-        if (hit != 0) {
-          const int k = __ffs(hit) - 1;
-          w.base += __shfl_sync(0xffffffffu, incl - n, k);
-          w.bi += k;
-          break;
-        }
-        w.base += __shfl_sync(0xffffffffu, incl, 31);
-        w.bi += 32;
-        if (w.bi >= p.c.b) {   // not reached: t < total
-          w.t = w.t_end;
-          break;
-        }
-      }
-    }
+    static_cast<Run&>(w) = find_run(p, blockIdx.x / blocks, lane);
     if (lane == 0) s_walk = w;
   }
   if (threadIdx.x == 32) {
@@ -228,6 +192,8 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
       mbar_init(&bars.raw_full[i], 1);
       mbar_init(&bars.raw_empty[i], 128);
     }
+    mbar_init(&bars.ml_full, 128);
+    mbar_init(&bars.o1_free, 128);
     mbar_init(&bars.drain, 1);
     bars.abort = 0;
     fence_mbar_init();
@@ -314,14 +280,14 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           if (bx < boxes && by < kCopies) {
             if constexpr (E4) {
               if (by == 0) {
-                tma_load_4d(dst + bx * wp.box * 128, map, full, 0, sl, sg.hk, pg);
+                tma_load_4d(dst + bx * wp.box * 128, map, full, 0, sl, hk, pg);
               } else if (pg < p.c.num_pages && !(is_v && by == 2)) {
                 const float* src = is_v || by == 2 ? p.c.v_scale : p.c.k_scale;
                 bulk_load(sc + (by - 1) * 128 + bx * wp.box,
-                          src + (static_cast<int64_t>(pg) * p.c.h_kv + sg.hk) * p.c.page_size + sl, wp.box * 4, full);
+                          src + (static_cast<int64_t>(pg) * p.c.h_kv + hk) * p.c.page_size + sl, wp.box * 4, full);
               }
             } else {
-              tma_load_4d(dst + by * 16384 + bx * wp.box * 128, map, full, by * 64, sl, sg.hk, pg);
+              tma_load_4d(dst + by * 16384 + bx * wp.box * 128, map, full, by * 64, sl, hk, pg);
             }
           }
           __syncwarp();
@@ -377,13 +343,13 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         };
         while (ok && walk.next(p, sg)) {
           const int n = sg.tile1 - sg.tile0;
-          for (int t = 0; t < (sg.split ? 1 : 2) && ok; ++t) {
+          for (int t = 0; t < (split ? 1 : 2) && ok; ++t) {
             ok = mbar_wait(&bars.q_full[t], (q_par >> t) & 1, wt);
             q_par ^= 1u << t;
           }
           if (!ok) break;
           tc_fence_after();
-          if (sg.split) {
+          if (split) {
             // Slot i % 2 for tile i: S runs two tiles ahead of P V.
             for (int i = 0; i < 2 && i < n; ++i) {
               const int s = wait_k();
@@ -545,16 +511,17 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
     bool ok = true;
     int n_seg = 0, n_tile = 0;
     uint32_t n_own = 0, n_other = 0;   // S of this warpgroup's slot and of the other so far
-    uint32_t n_o = 0;              // results of this slot so far
+    uint32_t n_o[2] = {0, 0};      // results of each slot so far
+    bool o1_pending = false;       // split, second warpgroup: its O of the segment before may still be read
     // This thread's row of Q of a segment to shared memory (one warpgroup's where both take the
     // same rows); returns the factor on its scores.  To be called when the last S of the segment
     // before has been read.
     auto load_q = [&](const Segment& g) -> float {
-      const int row = g.r0 + (g.split ? 0 : t * 128) + r;
+      const int row = r0 + (split ? 0 : t * 128) + r;
       const bool live = row < p.rows && row / p.group < g.L.len_q;
-      const bool store = !g.split || t == 0;
+      const bool store = !split || t == 0;
       float cs = wp.abs_scale_log2;
-      const uint16_t* src = static_cast<const uint16_t*>(p.q) + (live ? row_offset(p, p.q_st, g.bi, g.hk, row) : 0);
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) + (live ? row_offset(p, p.q_st, g.bi, hk, row) : 0);
       uint4 x[D / 8];
 #pragma unroll
       for (int u = 0; u < D / 8; ++u) x[u] = live ? *reinterpret_cast<const uint4*>(src + u * 8) : make_uint4(0, 0, 0, 0);
@@ -591,10 +558,10 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
     bool more = walk.next(p, sg);
     float cs = more ? load_q(sg) : 0.f;
     while (ok && more) {
-      const int row = sg.r0 + (sg.split ? 0 : t * 128) + r, token = row / p.group;
+      const int row = r0 + (split ? 0 : t * 128) + r, token = row / p.group;
       const bool live = row < p.rows && token < sg.L.len_q;
       const int n = sg.tile1 - sg.tile0;
-      const int step = sg.split ? 2 : 1, first = sg.split ? t : 0;
+      const int step = split ? 2 : 1, first = split ? t : 0;
       // ---- pages that do not exist (none, as a rule) -------------------------------------------------
       const int32_t* pages = p.c.page_table + sg.bi * p.c.page_table_stride;
       bool bad = false;
@@ -723,43 +690,81 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         }
         tmem_st_wait();
         tc_fence_before();
+        if (o1_pending) {              // this tile's P V overwrites O
+          if (!mbar_wait_warp(&bars.o1_free, (n_seg - 1) & 1, wt)) { ok = false; break; }
+          o1_pending = false;
+        }
         mbar_arrive(&bars.p_full[t]);
       }
       if (!ok) break;
-      n_other += sg.split ? (n + t) / 2 : n;
+      n_other += split ? (n + t) / 2 : n;
       n_tile += n;
       // ---- the next segment's Q, so that its first S runs while this one's results leave ----------
       Segment next;
       more = walk.next(p, next);
       if (more) {
         // Where both warpgroups shared the rows, the other slot's last S has to be done with Q too.
-        if (sg.split && t == 0 && n > 1 && !mbar_wait_warp(&bars.s_full[1], (n_other - 1) & 1, wt)) { ok = false; break; }
+        if (split && t == 0 && n > 1 && !mbar_wait_warp(&bars.s_full[1], (n_other - 1) & 1, wt)) { ok = false; break; }
         cs = load_q(next);
       }
       // ---- the segment's result: this thread's row ------------------------------------------------
-      const bool any = first < n;      // (one tile of keys alone: nothing for the second warpgroup)
-      if (any) {
-        if (!mbar_wait_warp(&bars.o_full[t], n_o & 1, wt)) { ok = false; break; }
-        ++n_o;
-        tc_fence_after();
+      // Split, second warpgroup: its part of a row's keys goes to the first one's thread of that row,
+      // the O of both lying in the same TMEM lane.
+      if (split && t == 1) {
+        if (o1_pending && !mbar_wait_warp(&bars.o1_free, (n_seg - 1) & 1, wt)) { ok = false; break; }
+        s_ml[r] = make_float2(m_ref, l);
+        mbar_arrive(&bars.ml_full);
+        o1_pending = true;
+        ++n_seg;
+        sg = next;
+        continue;
       }
-      const bool whole = !sg.split && sg.tile0 == 0 && sg.tile1 == sg.n_tiles;
-      const int64_t part = 2 * blockIdx.x + (sg.tile0 == 0 ? 1 : 0);
+      if (!mbar_wait_warp(&bars.o_full[t], n_o[0] & 1, wt)) { ok = false; break; }
+      ++n_o[0];
+      const bool two = split && n > 1;
+      float f0 = 1.f, f1 = 0.f;
+      if (split) {
+        if (!mbar_wait_warp(&bars.ml_full, n_seg & 1, wt)) { ok = false; break; }
+        if (two) {
+          if (!mbar_wait_warp(&bars.o_full[1], n_o[1] & 1, wt)) { ok = false; break; }
+          ++n_o[1];
+          const float2 ml0 = make_float2(m_ref, l), ml1 = s_ml[r];
+          const float m = fmaxf(l != 0.f ? m_ref : -INFINITY, ml1.y != 0.f ? ml1.x : -INFINITY);
+          f0 = part_weight(ml0, m);
+          f1 = part_weight(ml1, m);
+          l = (f0 == 0.f ? 0.f : l * f0) + (f1 == 0.f ? 0.f : ml1.y * f1);
+          m_ref = m;
+        }
+      }
+      tc_fence_after();
+      const bool whole = sg.tile0 == 0 && sg.tile1 == sg.n_tiles;
+      const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (sg.tile0 == 0 ? 1 : 0);
       const bool none = !live || l == 0.f;
       const float inv = none ? 0.f : 1.f / l;
       const bool fix = live && s_found[n_seg % 8] == n_seg + 1;
-      const int64_t out = row < p.rows ? row_offset(p, p.o_st, sg.bi, sg.hk, row) : 0;
+      const int64_t out = row < p.rows ? row_offset(p, p.o_st, sg.bi, hk, row) : 0;
 #pragma unroll 1
-      for (int c = 0; any && c < D / 32; ++c) {
+      for (int c = 0; c < D / 32; ++c) {
         uint32_t ov[32];
-        __syncwarp();          // (the TMEM load is the whole warp's)
+        __syncwarp();          // (the TMEM loads are the whole warp's)
         tmem_ld32(o_addr + c * 32, ov);
-        tmem_ld_wait();
-        reg_fence32(ov);
+        if (two) {
+          uint32_t o1[32];
+          tmem_ld32(o_addr + D + c * 32, o1);
+          tmem_ld_wait();
+          reg_fence32(ov);
+          reg_fence32(o1);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            ov[e] = __float_as_uint((f0 == 0.f ? 0.f : __uint_as_float(ov[e]) * f0) + (f1 == 0.f ? 0.f : __uint_as_float(o1[e]) * f1));
+        } else {
+          tmem_ld_wait();
+          reg_fence32(ov);
+        }
         if (row < p.rows) {
           if (fix) {
             for (int e = 0; e < 32; ++e)
-              ov[e] = __float_as_uint(add_nonfinite<D, CT>(p, sg.bi, sg.hk, sg.L, row, c * 32 + e, sg.tile0 * kKeys,
+              ov[e] = __float_as_uint(add_nonfinite<D, CT>(p, sg.bi, hk, sg.L, row, c * 32 + e, sg.tile0 * kKeys,
                                                            min(sg.tile1 * kKeys, sg.L.len_kv), __uint_as_float(ov[e])));
           }
           if (!whole) {
@@ -788,9 +793,10 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         if (!whole)
           *reinterpret_cast<float2*>(p.part_ml + 2 * (part * 256 + t * 128 + r)) = make_float2(m_ref, l);
         else if (p.lse)
-          p.lse[lse_offset(p, sg.bi, sg.hk, row)] = none ? -INFINITY : natural_lse(m_ref - C::P_OFF, l);
+          p.lse[lse_offset(p, sg.bi, hk, row)] = none ? -INFINITY : natural_lse(m_ref - C::P_OFF, l);
       }
       tc_fence_before();     // O has been read: the next segment's first P V follows a later arrival
+      if (split) mbar_arrive(&bars.o1_free);
       ++n_seg;
       sg = next;
     }
@@ -812,9 +818,8 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
   }
 }
 
-// Joins the parts of blocks that more than one CTA worked on, and writes the rows that no key
-// reaches: 32 rows (lanes) by 32 elements (a warp has four) a CTA, in the parts' order.  A part of a
-// block of at most 128 rows is two, one of each warpgroup.
+// Joins the parts of sequences that more than one team worked on, and writes the rows that no key
+// reaches: 32 rows (lanes) by 32 elements (a warp has four) a CTA, in the parts' order.
 template <int D, int QT>
 __global__ void __launch_bounds__(256) decode_wide_combine_kernel(const __grid_constant__ DecodeParams p, float p_off) {
   __shared__ uint2 s_out[32][9];
@@ -822,32 +827,21 @@ __global__ void __launch_bounds__(256) decode_wide_combine_kernel(const __grid_c
   const int groups = (min(p.rows, 256) + 31) / 32;
   const Parts u = find_parts(p, blockIdx.x / groups, lane);
   const int r = blockIdx.x % groups * 32 + lane, row = u.r0 + r, chunk = blockIdx.y * 8 + warp;
-  const bool split = p.rows - u.r0 <= 128;
   griddep_wait();   // (by every CTA, so that this grid never ends before the one it follows)
-  if (u.n == 1 && !split) return;
+  if (u.n == 1) return;
   const bool on = row < p.rows;
-  const int n = split ? 2 * u.n : u.n;
-  // Part k's place among [2 * ctas][256] rows of ml, and its float4 of O.
-  auto ml_of = [&](int k) {
-    const int64_t at = split ? u.part(k / 2) * 256 + k % 2 * 128 + r : u.part(k) * 256 + r;
-    return *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
-  };
-  auto o_of = [&](int k) {
-    const int64_t at = split ? (u.part(k / 2) * (D / 4) + chunk) * 256 + k % 2 * 128 + r : (u.part(k) * (D / 4) + chunk) * 256 + r;
-    return reinterpret_cast<const float4*>(p.part_o)[at];
-  };
   float m = -INFINITY, l = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   if (on) {
 #pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float2 ml = ml_of(k);
+    for (int k = 0; k < u.n; ++k) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (u.part(k) * 256 + r));
       if (ml.y != 0.f) m = fmaxf(m, ml.x);
     }
 #pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float2 ml = ml_of(k);
-      const float4 v = o_of(k);
+    for (int k = 0; k < u.n; ++k) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (u.part(k) * 256 + r));
+      const float4 v = reinterpret_cast<const float4*>(p.part_o)[(u.part(k) * (D / 4) + chunk) * 256 + r];
       const float f = part_weight(ml, m);
       l += ml.y * f;
       x.x += f == 0.f ? 0.f : v.x * f;

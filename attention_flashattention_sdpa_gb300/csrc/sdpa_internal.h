@@ -276,7 +276,7 @@ struct DecodeParams {
   float* part_o;               // workspace: [2 * ctas][tile_rows][d] unnormalised partial O (wide:
                                // [2 * ctas][d / 4][256][4], rows side by side)
   float* part_ml;              // workspace: [2 * ctas][tile_rows][2] their max (log2 units) and sum
-  int ctas;
+  int teams, ctas;             // runs of tiles, and CTAs: one for each run, KV head and block of rows
 };
 
 // Fills in the blocks of rows and the CTAs (from the sizes alone, so that workspace and launch agree).

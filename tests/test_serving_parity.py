@@ -290,6 +290,23 @@ def test_decode_many_tiles_a_cta(kind, s, h_q):
     assert_attend_close(o, lse, ref, "bf16", "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q // h_kv, d))
 
 
+@pytest.mark.parametrize("kind,d,s,h_q,h_kv", [("bf16", 128, 1, 2, 1), ("e4m3", 128, 18, 1, 1), ("bf16", 64, 20, 2, 1), ("f16", 128, 150, 1, 1),
+                                               ("e4m3", 64, 70, 40, 10), ("e4m3", 256, 2, 4, 4)])
+def test_decode_many_short_sequences(kind, d, s, h_q, h_kv):
+    """More sequences than CTAs, so that a run holds several whole ones, some empty and some of one token."""
+    g = torch.Generator().manual_seed(33)
+    b = 400 if h_kv == 1 else 60
+    lens = tuple((i * 37) % 150 if i % 7 else (i // 7) % 3 for i in range(b))
+    dtype = "f16" if kind == "f16" else "bf16"
+    c = make_cache(lens, h_kv, d, 16, kind, seed=34)
+    q = bshd(g, dtype, b, h_q, s, d)
+    o, lse = run_decode(c, q, causal="bottom_right")
+    rows = [i for i in range(b) if b <= 60 or i % 9 == 0]
+    kv, vv, ks, vs, table = c.np()
+    ref = so.attend(f64(q)[rows], kv, vv, ks, vs, table[rows], [lens[i] for i in rows], None, d ** -0.5, True)
+    assert_attend_close(o[rows], lse[rows], ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q // h_kv, d))
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
 def test_decode_peaked_scores(kind):
     """One key far above the rest, late in a long context; scales that make scores large; a negative scale."""
