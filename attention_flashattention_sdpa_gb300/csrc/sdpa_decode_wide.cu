@@ -45,19 +45,19 @@ struct WideCfg {
   static constexpr int TILE = 128 * D * 2;                // a 16-bit tile of 128 rows
   static constexpr int RAW = 128 * 128;                   // an E4M3 tile: rows of 128 bytes (d = 64: half zeros)
   static constexpr int NCHUNK = D / 64;                   // 128-byte columns of a 16-bit tile
-  // Slots of 16-bit K and V tiles, and stages of E4M3 K and V tiles with their scales (K's with those of
-  // V).  K and V have slots of their own: a wait for a parity may not skip phases, and in a ring of
-  // three that they shared, each would follow only every second phase of a slot.
+  // Slots of 16-bit K and V tiles, and stages of E4M3 K and V tiles with their scales.  K and V have
+  // slots of their own: a wait for a parity may not skip phases, and in a ring of three that they
+  // shared, each would follow only every second phase of a slot.
   static constexpr int NK = D == 128 ? (E4 ? 1 : 2) : (E4 ? 2 : 3), NV = D == 128 ? 2 : 3;
-  static constexpr int RK = E4 ? 2 : 0, RV = E4 ? (D == 128 ? 1 : 2) : 0;
+  static constexpr int RK = E4 ? 2 : 0, RV = E4 ? 2 : 0;
   static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + NK * TILE, OFF_RAW = OFF_V + NV * TILE;
-  static constexpr int OFF_SC = OFF_RAW + (RK + RV) * RAW;
-  static constexpr int SMEM = OFF_SC + (RK + RV) * 1024 + 1024;
+  static constexpr int OFF_SC = OFF_RAW + (RK + RV) * RAW, OFF_CTL = OFF_SC + (RK + RV) * 512;
+  static constexpr int SMEM = OFF_CTL + 1024;
   static constexpr int KSTEPS = D / 16;
   static constexpr int O_COL0 = 256;
   static constexpr float P_OFF = CT == kBF16 ? 0.f : 6.f;
   static constexpr float THRESH = 8.f;
-  static_assert(SMEM + 1024 <= 232448, "shared memory");
+  static_assert(SMEM <= 232448, "shared memory");
   static_assert(O_COL0 + 2 * D <= 512, "TMEM");
 };
 
@@ -67,6 +67,7 @@ struct alignas(8) WideBarriers {
   uint64_t raw_full[4], raw_empty[4];       // E4M3 tiles: K's stages, then V's
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t ml_full, o1_free;                // split: the second warpgroup's maxima and sums are there; its O is read
+  uint64_t ev_full[4];                      // E4M3: the exponent of a tile's V scales is known
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -100,6 +101,15 @@ struct Walk : Run {
     return false;
   }
 };
+
+// What the roles share besides tiles.
+struct Control {
+  WideBarriers bars;
+  Walk walk;
+  int ek[8], ev[8];      // E4M3: exponents of a tile's scales, by tile count
+  int found[8];          // segment count + 1 of a segment with cleared values
+};
+static_assert(sizeof(Control) <= 1024);
 
 // Whether V's tile of a 16-bit cache has to be cleared of what no row may meet.
 __device__ __forceinline__ bool needs_cleaning(const DecodeParams& p, const Segment& g, int tile) {
@@ -153,17 +163,24 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
   };
   const DecodeParams& p = wp.d;
 
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // All of it dynamic, without static arrays: it then begins on the 1024-byte boundary that the
+  // swizzled tiles need (checked), with no room lost to alignment.
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) % 1024 != 0) {
+    if (threadIdx.x == 0) atomicOr(&g_device_error, kErrSmemAlign);
+    return;
+  }
   uint8_t* sQ = smem;
   uint8_t* sRing = smem + C::OFF_K;
   uint8_t* sRaw = smem + C::OFF_RAW;
-  float* sSc = reinterpret_cast<float*>(smem + C::OFF_SC);   // [stage][2][128]
-  __shared__ WideBarriers bars;
-  __shared__ Walk s_walk;
-  __shared__ volatile int s_ek[8], s_ev[8];    // exponents of a tile's scales, by tile count
-  __shared__ float2 s_ml[128];                 // split: the second warpgroup's maximum and sum of each row
-  __shared__ volatile int s_found[8];          // segment count + 1 of a segment with cleared values
+  float* sSc = reinterpret_cast<float*>(smem + C::OFF_SC);   // [stage][128]
+  // Split: the second warpgroup's maximum and sum of each row (the second tile of Q is not used).
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::TILE);
+  Control& ctl = *reinterpret_cast<Control*>(smem + C::OFF_CTL);
+  WideBarriers& bars = ctl.bars;
+  volatile int* s_ek = ctl.ek;
+  volatile int* s_ev = ctl.ev;
+  volatile int* s_found = ctl.found;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
@@ -174,7 +191,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
   if (warp == 0) {
     Walk w;
     static_cast<Run&>(w) = find_run(p, blockIdx.x / blocks, lane);
-    if (lane == 0) s_walk = w;
+    if (lane == 0) ctl.walk = w;
   }
   if (threadIdx.x == 32) {
     for (int t = 0; t < 2; ++t) {
@@ -192,6 +209,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
       mbar_init(&bars.raw_full[i], 1);
       mbar_init(&bars.raw_empty[i], 128);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&bars.ev_full[i], 1);
     mbar_init(&bars.ml_full, 128);
     mbar_init(&bars.o1_free, 128);
     mbar_init(&bars.drain, 1);
@@ -211,7 +229,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
   const uint32_t tmem = bars.tmem_base;
   volatile int* abort_flag = &bars.abort;
   const Waiter wt{abort_flag, wp.wait_limit};
-  Walk walk = s_walk;
+  Walk walk = ctl.walk;
   Segment sg;
 
   bool producer = false;
@@ -228,9 +246,9 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
       const int boxes = kKeys / wp.box;     // boxes of a tile: 1, 2, 4 or 8
       const unsigned all = (1u << boxes) - 1u;
       // Lane x + 8 y issues copy y of box x: of 16-bit tiles the 128-byte columns, of E4M3 ones the
-      // codes, the scales of this tile (K's or V's) and, with K, those of V.
+      // codes and the scales.
       const int bx = lane % 8, by = lane / 8;
-      constexpr int kCopies = E4 ? 3 : C::NCHUNK;
+      constexpr int kCopies = E4 ? 2 : C::NCHUNK;
       bool ok = true;
       while (ok && walk.next(p, sg)) {
         const int32_t* pages = p.c.page_table + sg.bi * p.c.page_table_stride;
@@ -263,28 +281,24 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           if (!mbar_wait_warp(E4 ? &bars.raw_empty[s] : &bars.empty[s], (at.turn & 1) ^ 1, wt)) { ok = false; break; }
           uint64_t* full = E4 ? &bars.raw_full[s] : &bars.full[s];
           uint8_t* dst = E4 ? sRaw + s * C::RAW : sRing + s * C::TILE;
-          float* sc = sSc + s * 256;
+          float* sc = sSc + s * 128;
           if constexpr (E4) {
             if (there != all) {      // no scale where there is no key
               for (int i = lane; i < kKeys; i += 32)
-                if (!((there >> (i / wp.box)) & 1u)) {
-                  sc[i] = 0.f;
-                  if (!is_v) sc[128 + i] = 0.f;
-                }
+                if (!((there >> (i / wp.box)) & 1u)) sc[i] = 0.f;
             }
             __syncwarp();
           }
-          if (lane == 0) mbar_arrive_expect_tx(full, E4 ? C::RAW + __popc(there) * wp.box * (is_v ? 4 : 8) : C::TILE);
+          if (lane == 0) mbar_arrive_expect_tx(full, E4 ? C::RAW + __popc(there) * wp.box * 4 : C::TILE);
           ++issued;
           __syncwarp();
           if (bx < boxes && by < kCopies) {
             if constexpr (E4) {
               if (by == 0) {
                 tma_load_4d(dst + bx * wp.box * 128, map, full, 0, sl, hk, pg);
-              } else if (pg < p.c.num_pages && !(is_v && by == 2)) {
-                const float* src = is_v || by == 2 ? p.c.v_scale : p.c.k_scale;
-                bulk_load(sc + (by - 1) * 128 + bx * wp.box,
-                          src + (static_cast<int64_t>(pg) * p.c.h_kv + hk) * p.c.page_size + sl, wp.box * 4, full);
+              } else if (pg < p.c.num_pages) {
+                bulk_load(sc + bx * wp.box, (is_v ? p.c.v_scale : p.c.k_scale) +
+                          (static_cast<int64_t>(pg) * p.c.h_kv + hk) * p.c.page_size + sl, wp.box * 4, full);
               }
             } else {
               tma_load_4d(dst + by * 16384 + bx * wp.box * 128, map, full, by * 64, sl, hk, pg);
@@ -416,14 +430,11 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           const int rs = from.at, s = to.at, left = sg.L.len_kv - j * kKeys;
           ok = mbar_wait_warp(&bars.raw_full[rs], from.turn & 1, wt);
           if (!ok) break;
-          const float* sc = sSc + rs * 256;
-          const int ex = largest_exponent(sc, left, lane);
-          if (!is_v) {
-            const int ev = largest_exponent(sc + 128, left, lane);
-            if (threadIdx.x == 12 * 32) {
-              s_ek[n_tile % 8] = ex;
-              s_ev[n_tile % 8] = ev;
-            }
+          const float* sc = sSc + rs * 128;
+          const int ex = largest_exponent(sc, left, lane);      // (by every lane)
+          if (warp % 4 == 0 && lane == 0) {
+            (is_v ? s_ev : s_ek)[n_tile % 8] = ex;
+            if (is_v) mbar_arrive(&bars.ev_full[n_tile % 4]);
           }
           // scale / 2^E of the lane's row as two F16, each twice in a word
           const float f = on ? sc[r] * pow2(-ex) : 0.f;
@@ -582,8 +593,10 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         // out of l again.
         float cst = cs, ev = 0.f, back = 1.f;
         if constexpr (E4) {
-          cst = cs * pow2(s_ek[(n_tile + i) % 8]);
-          const int e = s_ev[(n_tile + i) % 8];
+          const int tile = n_tile + i;
+          if (!mbar_wait_warp(&bars.ev_full[tile % 4], (tile / 4) & 1, wt)) { ok = false; break; }
+          cst = cs * pow2(s_ek[tile % 8]);
+          const int e = s_ev[tile % 8];
           ev = static_cast<float>(e);
           back = pow2(-e);
         }

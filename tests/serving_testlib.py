@@ -109,7 +109,7 @@ def pack_tree(see: np.ndarray) -> torch.Tensor:
 
 def kv_rounding(kind, rows, d):
     """Relative rounding of an E4M3 cache's elements in the products of `rows` query rows a KV head."""
-    return 2.0 ** -11 if kind == "e4m3" and rows > 16 and d <= 128 else 0.0
+    return 2.0 ** -11 if kind == "e4m3" and rows > 32 and d <= 128 else 0.0
 
 
 def run_decode(cache: PagedCache, q, *, lens_q=None, causal=False, tree=None, scale=None, with_lse=True, stream=None):
