@@ -86,7 +86,9 @@ __device__ __forceinline__ int working_teams(const DecodeParams& p, long long to
 // First tile of team c's run, and the team whose run holds tile t, of `total` tiles over g teams.
 __device__ __forceinline__ long long run_start(long long total, int c, int g) { return total * c / g; }
 __device__ __forceinline__ int team_of(long long total, long long t, int g) {
-  return static_cast<int>(((t + 1) * g - 1) / total);
+  const long long x = (t + 1) * g - 1;
+  if (x < (1ll << 31) && total < (1ll << 31)) return static_cast<int>(x) / static_cast<int>(total);
+  return static_cast<int>(x / total);
 }
 
 // The run of this CTA's team, and the sequence that holds its first tile; by a whole warp.
@@ -202,7 +204,17 @@ __device__ __forceinline__ Parts find_parts(const DecodeParams& p, int unit, int
   u.c0 = u.n = 0;
   const int n_tiles = seq_tiles(p, u.bi);
   if (n_tiles > 0) {
-    const long long total = tiles_before(p, p.c.b, lane), t0 = tiles_before(p, u.bi, lane);
+    long long total = 0, t0 = 0;      // tiles of all sequences, and of those before this one
+    for (int i = lane; i < p.c.b; i += 32) {
+      const int x = seq_tiles(p, i);
+      total += x;
+      if (i < u.bi) t0 += x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+      t0 += __shfl_xor_sync(0xffffffffu, t0, o);
+    }
     const int g = working_teams(p, total);
     u.c0 = team_of(total, t0, g);
     u.n = team_of(total, t0 + n_tiles - 1, g) - u.c0 + 1;

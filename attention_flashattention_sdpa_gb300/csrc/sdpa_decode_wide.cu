@@ -524,43 +524,55 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
     uint32_t n_own = 0, n_other = 0;   // S of this warpgroup's slot and of the other so far
     uint32_t n_o[2] = {0, 0};      // results of each slot so far
     bool o1_pending = false;       // split, second warpgroup: its O of the segment before may still be read
-    // This thread's row of Q of a segment to shared memory (one warpgroup's where both take the
-    // same rows); returns the factor on its scores.  To be called when the last S of the segment
-    // before has been read.
+    // This warp's 32 rows of Q of a segment to shared memory (one warpgroup's where both take the same
+    // rows), a row by D / 8 lanes; returns the factor on the scores of this thread's row.  To be
+    // called when the last S of the segment before has been read.  (Few instructions: what runs once
+    // a segment is fetched cold each time; a row a thread, unrolled, took 8-10 thousand cycles.)
     auto load_q = [&](const Segment& g) -> float {
-      const int row = r0 + (split ? 0 : t * 128) + r;
-      const bool live = row < p.rows && row / p.group < g.L.len_q;
+      constexpr int LR = D / 8, RI = 32 / LR;        // lanes of a row, rows of an instruction
       const bool store = !split || t == 0;
+      const int u = lane % LR;
       float cs = wp.abs_scale_log2;
-      const uint16_t* src = static_cast<const uint16_t*>(p.q) + (live ? row_offset(p, p.q_st, g.bi, hk, row) : 0);
-      uint4 x[D / 8];
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32; i0 += 8 * RI) {
+        uint4 x[8];
 #pragma unroll
-      for (int u = 0; u < D / 8; ++u) x[u] = live ? *reinterpret_cast<const uint4*>(src + u * 8) : make_uint4(0, 0, 0, 0);
-      uint32_t* w = reinterpret_cast<uint32_t*>(x);
-      if (wp.negate) {
+        for (int i = 0; i < 8; ++i) {
+          const int row = r0 + (split ? 0 : t * 128) + quad * 32 + i0 + i * RI + lane / LR;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (row < p.rows && row / p.group < g.L.len_q)
+            x[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row_offset(p, p.q_st, g.bi, hk, row) + u * 8);
+        }
 #pragma unroll
-        for (int i = 0; i < D / 2; ++i) w[i] ^= 0x80008000u;
-      }
-      if constexpr (E4 && QT == kBF16) {
-        // To F16 by a power of two that brings the largest element to [256, 512).
-        uint32_t m = 0;
+        for (int i = 0; i < 8; ++i) {
+          const int lr = i0 + i * RI + lane / LR, rr = quad * 32 + lr;
+          uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-        for (int i = 0; i < D / 2; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-        const int ex = static_cast<int>(m >> 7);
-        const int sh = (ex == 0 || ex == 255) ? 0 : min(127 + 8 - ex, 126);
-        const float up = pow2(sh);
-        cs *= pow2(-sh);
+          for (int e = 0; e < 4; ++e) w[e] ^= wp.negate ? 0x80008000u : 0u;
+          if constexpr (E4 && QT == kBF16) {
+            // To F16 by a power of two that brings the row's largest element to [256, 512).
+            uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < D / 2; ++i) {
-          const float2 f = unpack_pair<true>(w[i]);
-          w[i] = pack_pair<false>(f.x * up, f.y * up);
+            for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+#pragma unroll
+            for (int o = 1; o < LR; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const int ex = static_cast<int>(m >> 7);
+            const int sh = (ex == 0 || ex == 255) ? 0 : min(127 + 8 - ex, 126);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack_pair<true>(w[e]);
+              w[e] = pack_pair<false>(f.x * pow2(sh), f.y * pow2(sh));
+            }
+            // The row's own thread is lane lr.
+            const int mine = __shfl_sync(0xffffffffu, sh, lane % RI * LR);
+            if (lane / RI == i0 / RI + i) cs *= pow2(-mine);
+          }
+          if (store)
+            *reinterpret_cast<uint4*>(sQ + t * C::TILE + (u / 8) * 16384 + rr * 128 + ((u % 8) ^ (rr & 7)) * 16) =
+                make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       if (store) {
-        uint8_t* q_row = sQ + t * C::TILE + r * 128;
-#pragma unroll
-        for (int u = 0; u < D / 8; ++u)
-          *reinterpret_cast<uint4*>(q_row + (u / 8) * 16384 + ((u % 8) ^ (r & 7)) * 16) = x[u];
         fence_proxy_async_smem();
         mbar_arrive(&bars.q_full[t]);
       }
@@ -636,44 +648,46 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         }
         // The row's 128 scores come in halves of 64 columns: the second for its maximum, then the
         // first, which stays for its exponentials, then the second again.  P takes the columns of
-        // the first quarter and then of the second, both read by then.
-        uint32_t sv[64];
-        auto load_half = [&](int h) {
+        // the first quarter and then of the second, both read by then.  (One body for the three
+        // steps: instruction fetch, not registers, limits an unrolled one.)
+        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+        float alpha = 1.f;
+        float2 cs2 = make_float2(cst, cst), nm2 = make_float2(0.f, 0.f);
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int st = 0; st < 3; ++st) {
+          const int h = st == 1 ? 0 : 1;
+          uint32_t sv[64];
           tmem_ld32(s_addr + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
           tmem_ld32(s_addr + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
           tmem_ld_wait();
           reg_fence32(&sv[0]);
           reg_fence32(&sv[32]);
           if (need) {
+            const uint32_t v0 = h ? vis[2] : vis[0], v1 = h ? vis[3] : vis[1];
 #pragma unroll
             for (int c = 0; c < 64; ++c)
-              if (!((vis[2 * h + c / 32] >> (c % 32)) & 1u)) sv[c] = __float_as_uint(-INFINITY);
+              if (!(((c < 32 ? v0 : v1) >> (c % 32)) & 1u)) sv[c] = __float_as_uint(-INFINITY);
           }
-        };
-        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+          if (st < 2) {
 #pragma unroll
-        for (int h = 1; h >= 0; --h) {
-          load_half(h);
-#pragma unroll
-          for (int c = 0; c < 64; c += 8) {
-            mx0 = max3(mx0, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-            mx1 = max3(mx1, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
-            mx2 = max3(mx2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
-            mx3 = max3(mx3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+            for (int c = 0; c < 64; c += 8) {
+              mx0 = max3(mx0, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+              mx1 = max3(mx1, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+              mx2 = max3(mx2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
+              mx3 = max3(mx3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+            }
           }
-        }
-        const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cst, ev);
-        float alpha = 1.f;
-        if (m_cand > m_ref + C::THRESH) {
-          alpha = ex2(m_ref - m_cand);
-          m_ref = m_cand;
-        }
-        const float nm = m_ref == -INFINITY ? 0.f : C::P_OFF - m_ref + ev;
-        const float2 cs2 = make_float2(cst, cst), nm2 = make_float2(nm, nm);
-        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1) load_half(1);
+          if (st == 0) continue;
+          if (st == 1) {
+            const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cst, ev);
+            if (m_cand > m_ref + C::THRESH) {
+              alpha = ex2(m_ref - m_cand);
+              m_ref = m_cand;
+            }
+            const float nm = m_ref == -INFINITY ? 0.f : C::P_OFF - m_ref + ev;
+            nm2 = make_float2(nm, nm);
+          }
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 4) {
@@ -685,6 +699,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
             pk[c / 2] = pack_pair<BF>(p01.x, p01.y);
             pk[c / 2 + 1] = pack_pair<BF>(p23.x, p23.y);
           }
+          __syncwarp();
           tmem_st32(s_addr + h * 32, pk);
         }
         l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y)) * back;
@@ -832,20 +847,22 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
 }
 
 // Joins the parts of sequences that more than one team worked on, and writes the rows that no key
-// reaches: 32 rows (lanes) by 32 elements (a warp has four) a CTA, in the parts' order.
+// reaches: 32 rows a CTA, a lane a row, every warp D / 32 groups of four elements, in the parts' order.
 template <int D, int QT>
 __global__ void __launch_bounds__(256) decode_wide_combine_kernel(const __grid_constant__ DecodeParams p, float p_off) {
-  __shared__ uint2 s_out[32][9];
+  constexpr int NG = D / 32;
+  __shared__ uint2 s_out[32][D / 4 + 1];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int groups = (min(p.rows, 256) + 31) / 32;
   const Parts u = find_parts(p, blockIdx.x / groups, lane);
-  const int r = blockIdx.x % groups * 32 + lane, row = u.r0 + r, chunk = blockIdx.y * 8 + warp;
+  const int r = blockIdx.x % groups * 32 + lane, row = u.r0 + r;
   griddep_wait();   // (by every CTA, so that this grid never ends before the one it follows)
   if (u.n == 1) return;
-  const bool on = row < p.rows;
   float m = -INFINITY, l = 0.f;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (on) {
+  float4 x[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) x[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (row < p.rows) {
 #pragma unroll 4
     for (int k = 0; k < u.n; ++k) {
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (u.part(k) * 256 + r));
@@ -854,26 +871,34 @@ __global__ void __launch_bounds__(256) decode_wide_combine_kernel(const __grid_c
 #pragma unroll 4
     for (int k = 0; k < u.n; ++k) {
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (u.part(k) * 256 + r));
-      const float4 v = reinterpret_cast<const float4*>(p.part_o)[(u.part(k) * (D / 4) + chunk) * 256 + r];
       const float f = part_weight(ml, m);
       l += ml.y * f;
-      x.x += f == 0.f ? 0.f : v.x * f;
-      x.y += f == 0.f ? 0.f : v.y * f;
-      x.z += f == 0.f ? 0.f : v.z * f;
-      x.w += f == 0.f ? 0.f : v.w * f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const float4 v = reinterpret_cast<const float4*>(p.part_o)[(u.part(k) * (D / 4) + g * 8 + warp) * 256 + r];
+        x[g].x += f == 0.f ? 0.f : v.x * f;
+        x[g].y += f == 0.f ? 0.f : v.y * f;
+        x[g].z += f == 0.f ? 0.f : v.z * f;
+        x[g].w += f == 0.f ? 0.f : v.w * f;
+      }
     }
     const bool none = row / p.group >= u.L.len_q || l == 0.f;
     const float inv = none ? 0.f : 1.f / l;
-    s_out[lane][warp] = none ? make_uint2(0, 0)
-                             : make_uint2(pack_pair<QT == kBF16>(x.x * inv, x.y * inv), pack_pair<QT == kBF16>(x.z * inv, x.w * inv));
-    if (p.lse && chunk == 0) p.lse[lse_offset(p, u.bi, u.hk, row)] = none ? -INFINITY : natural_lse(m - p_off, l);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+      s_out[lane][g * 8 + warp] = none ? make_uint2(0, 0)
+                                       : make_uint2(pack_pair<QT == kBF16>(x[g].x * inv, x[g].y * inv),
+                                                    pack_pair<QT == kBF16>(x[g].z * inv, x[g].w * inv));
+    if (p.lse && warp == 0) p.lse[lse_offset(p, u.bi, u.hk, row)] = none ? -INFINITY : natural_lse(m - p_off, l);
   }
   __syncthreads();
-  // 64 bytes of a row by 8 neighbouring threads.
-  const int r2 = threadIdx.x / 8, row2 = blockIdx.x % groups * 32 + r2 + u.r0;
-  if (row2 < p.rows)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row_offset(p, p.o_st, u.bi, u.hk, row2) + blockIdx.y * 32 +
-                              threadIdx.x % 8 * 4) = s_out[r2][threadIdx.x % 8];
+  // A row of D / 4 words by as many neighbouring threads.
+  for (int i = threadIdx.x; i < 32 * (D / 4); i += 256) {
+    const int r2 = i / (D / 4), row2 = u.r0 + blockIdx.x % groups * 32 + r2;
+    if (row2 < p.rows)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row_offset(p, p.o_st, u.bi, u.hk, row2) + i % (D / 4) * 4) =
+          s_out[r2][i % (D / 4)];
+  }
 }
 
 template <int D, int CT, int QT>
@@ -888,7 +913,7 @@ cudaError_t launch_t(const WideParams& wp, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int groups = ((p.rows < 256 ? p.rows : 256) + 31) / 32;
   return launch_after(decode_wide_combine_kernel<D, QT>,
-                      dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles * groups, D / 32), dim3(256), st, p, C::P_OFF);
+                      dim3(static_cast<unsigned>(p.c.b) * p.c.h_kv * p.row_tiles * groups), dim3(256), st, p, C::P_OFF);
 }
 
 template <int D>
