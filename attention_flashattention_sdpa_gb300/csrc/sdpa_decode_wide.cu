@@ -526,22 +526,26 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
     bool o1_pending = false;       // split, second warpgroup: its O of the segment before may still be read
     // This warp's 32 rows of Q of a segment to shared memory (one warpgroup's where both take the same
     // rows), a row by D / 8 lanes; returns the factor on the scores of this thread's row.  To be
-    // called when the last S of the segment before has been read.  (Few instructions: what runs once
-    // a segment is fetched cold each time; a row a thread, unrolled, took 8-10 thousand cycles.)
+    // called when the last S of the segment before has been read.  (A row a thread took 8-10 thousand
+    // cycles: 32 rows for each warp instruction.)
+    const int my_row = r0 + (split ? 0 : t * 128) + r, my_token = my_row / p.group;
+    const int64_t q_row = (static_cast<int64_t>(hk) * p.group + my_row % p.group) * p.q_st[1] + my_token * p.q_st[2];
     auto load_q = [&](const Segment& g) -> float {
       constexpr int LR = D / 8, RI = 32 / LR;        // lanes of a row, rows of an instruction
       const bool store = !split || t == 0;
       const int u = lane % LR;
       float cs = wp.abs_scale_log2;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) + g.bi * p.q_st[0] + u * 8;
+      const unsigned live = __ballot_sync(0xffffffffu, my_row < p.rows && my_token < g.L.len_q);
 #pragma unroll 1
       for (int i0 = 0; i0 < 32; i0 += 8 * RI) {
         uint4 x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int row = r0 + (split ? 0 : t * 128) + quad * 32 + i0 + i * RI + lane / LR;
+          const int lr = i0 + i * RI + lane / LR;
+          const int64_t at = __shfl_sync(0xffffffffu, q_row, lr);
           x[i] = make_uint4(0, 0, 0, 0);
-          if (row < p.rows && row / p.group < g.L.len_q)
-            x[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row_offset(p, p.q_st, g.bi, hk, row) + u * 8);
+          if ((live >> lr) & 1u) x[i] = *reinterpret_cast<const uint4*>(q + at);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -581,10 +585,17 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
     bool more = walk.next(p, sg);
     float cs = more ? load_q(sg) : 0.f;
     while (ok && more) {
-      const int row = r0 + (split ? 0 : t * 128) + r, token = row / p.group;
+      const int row = my_row, token = my_token;
       const bool live = row < p.rows && token < sg.L.len_q;
       const int n = sg.tile1 - sg.tile0;
       const int step = split ? 2 : 1, first = split ? t : 0;
+      Segment next;
+      more = walk.next(p, next);
+      if (more && row < p.rows) {      // its Q starts towards L2
+        const uint16_t* q = static_cast<const uint16_t*>(p.q) + next.bi * p.q_st[0] + q_row;
+        prefetch_l2(q);
+        if (D > 64) prefetch_l2(q + 64);
+      }
       // ---- pages that do not exist (none, as a rule) -------------------------------------------------
       const int32_t* pages = p.c.page_table + sg.bi * p.c.page_table_stride;
       bool bad = false;
@@ -728,8 +739,6 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
       n_other += split ? (n + t) / 2 : n;
       n_tile += n;
       // ---- the next segment's Q, so that its first S runs while this one's results leave ----------
-      Segment next;
-      more = walk.next(p, next);
       if (more) {
         // Where both warpgroups shared the rows, the other slot's last S has to be done with Q too.
         if (split && t == 0 && n > 1 && !mbar_wait_warp(&bars.s_full[1], (n_other - 1) & 1, wt)) { ok = false; break; }
