@@ -14,7 +14,7 @@
 namespace sdpa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr float kE4M3Max = 448.f;
 constexpr float kAmaxMin = 8.673617379884035e-19f;  // 2^-60
 
@@ -110,14 +110,11 @@ __device__ __forceinline__ void store_item(uint8_t* row, float* scale_at, int m,
 
 // ROPE: 0 none, 1 rot a multiple of 16, 2 any even rot.
 template <int D, int DT, int CT, int ROPE>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheRowsParams p, int per) {
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheRowsParams p, int per,
+                                                            bool small) {
   constexpr int LANES = D / 16;
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int m = static_cast<int>(idx % LANES);
-  const int64_t tokens = static_cast<int64_t>(p.c.b) * p.s;
-  const int64_t tok = (idx / LANES) % tokens;
-  const int grp = static_cast<int>(idx / LANES / tokens);
-  const int bi = static_cast<int>(tok / p.s), si = static_cast<int>(tok % p.s);
+  const Spot who = find_spot(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, LANES, p.c.b, p.s, small);
+  const int m = who.m, grp = who.grp, bi = who.bi, si = who.si;
   const int len_q = clamp_len(p.seq_lens_q, bi, p.s);
   const int len_kv = clamp_len(p.c.seq_lens_kv, bi, p.c.max_len);
   const int pos = len_kv - len_q + si;
@@ -196,67 +193,52 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
   }
 }
 
-// One thread: 16 elements of K and of V of one token, for up to kReadHeads heads whose loads are in
-// flight together.
-constexpr int kReadHeads = 1;
-
+// One thread: 16 elements of K and of V of one row.  (Two or four heads a thread, their loads in
+// flight together, were slower: 21.7 and 22.6 us against 19.5 for 2 x 8192 tokens of 8 heads.)
 template <int D, int DT, int CT>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheRowsParams p, int groups) {
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheRowsParams p, bool small) {
   constexpr int LANES = D / 16, N = CT == kE4M3 ? 1 : 2;     // 16-byte loads of an item
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int m = static_cast<int>(idx % LANES);
-  const int64_t row = idx / LANES;
-  const int h0 = static_cast<int>(row % groups) * kReadHeads;
-  const int64_t tok = row / groups;
-  if (tok >= static_cast<int64_t>(p.c.b) * p.s) return;
-  const int bi = static_cast<int>(tok / p.s), si = static_cast<int>(tok % p.s);
+  const Spot who = find_spot(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, LANES * p.c.h_kv, p.c.b, p.s, small);
+  const int m = who.m % LANES, h = who.m / LANES, bi = who.bi, si = who.si;
+  if (who.grp > 0) return;
   Slot at{-1, 0};
   if (si < clamp_len(p.c.seq_lens_kv, bi, p.c.max_len)) at = find_slot(p.c, bi, si);
-  uint4 in[kReadHeads][2][N];
-  float scale[kReadHeads][2];
+  uint4 in[2][N];
+  float scale[2] = {0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < kReadHeads; ++j)
+  for (int t = 0; t < 2; ++t) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      scale[j][t] = 0.f;
+    for (int i = 0; i < N; ++i) in[t][i] = make_uint4(0, 0, 0, 0);
+    if (at.page >= 0) {
+      const int64_t* st = t ? p.c.v_st : p.c.k_st;
+      const uint8_t* src = (t ? p.c.v : p.c.k) + at.page * st[0] + h * st[1] + at.slot * st[2] + m * 16 * N;
 #pragma unroll
-      for (int i = 0; i < N; ++i) in[j][t][i] = make_uint4(0, 0, 0, 0);
-      const int h = h0 + j;
-      if (at.page >= 0 && h < p.c.h_kv) {
-        const int64_t* st = t ? p.c.v_st : p.c.k_st;
-        const uint8_t* src = (t ? p.c.v : p.c.k) + at.page * st[0] + h * st[1] + at.slot * st[2] + m * 16 * N;
-#pragma unroll
-        for (int i = 0; i < N; ++i) in[j][t][i] = __ldg(reinterpret_cast<const uint4*>(src + i * 16));
-        if constexpr (CT == kE4M3)
-          scale[j][t] = __ldg((t ? p.c.v_scale : p.c.k_scale) + (at.page * p.c.h_kv + h) * p.c.page_size + at.slot);
-      }
+      for (int i = 0; i < N; ++i) in[t][i] = __ldg(reinterpret_cast<const uint4*>(src + i * 16));
+      if constexpr (CT == kE4M3)
+        scale[t] = __ldg((t ? p.c.v_scale : p.c.k_scale) + (at.page * p.c.h_kv + h) * p.c.page_size + at.slot);
     }
+  }
 #pragma unroll
-  for (int j = 0; j < kReadHeads; ++j)
+  for (int t = 0; t < 2; ++t) {
+    uint4 out[2];
+    if constexpr (CT == kE4M3) {
+      const uint32_t iw[4] = {in[t][0].x, in[t][0].y, in[t][0].z, in[t][0].w};
+      uint32_t* ow = reinterpret_cast<uint32_t*>(out);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int h = h0 + j;
-      if (h >= p.c.h_kv) continue;
-      uint4 out[2];
-      if constexpr (CT == kE4M3) {
-        const uint4 x = in[j][t][0];
-        const uint32_t iw[4] = {x.x, x.y, x.z, x.w};
-        uint32_t* ow = reinterpret_cast<uint32_t*>(out);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(iw[i / 2] >> (16 * (i % 2))), __NV_E4M3);
-          const float2 f = __half22float2(__half2(hr));
-          ow[i] = pack16<DT>(f.x * scale[j][t], f.y * scale[j][t]);
-        }
-      } else {
-        out[0] = in[j][t][0];
-        out[1] = in[j][t][N - 1];
+      for (int i = 0; i < 8; ++i) {
+        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(iw[i / 2] >> (16 * (i % 2))), __NV_E4M3);
+        const float2 f = __half22float2(__half2(hr));
+        ow[i] = pack16<DT>(f.x * scale[t], f.y * scale[t]);
       }
-      const int64_t* st = t ? p.v_st : p.k_st;
-      uint16_t* dst = static_cast<uint16_t*>(t ? p.v : p.k) + bi * st[0] + h * st[1] + si * st[2] + m * 16;
-      reinterpret_cast<uint4*>(dst)[0] = out[0];
-      reinterpret_cast<uint4*>(dst)[1] = out[1];
+    } else {
+      out[0] = in[t][0];
+      out[1] = in[t][N - 1];
     }
+    const int64_t* st = t ? p.v_st : p.k_st;
+    uint16_t* dst = static_cast<uint16_t*>(t ? p.v : p.k) + bi * st[0] + h * st[1] + si * st[2] + m * 16;
+    reinterpret_cast<uint4*>(dst)[0] = out[0];
+    reinterpret_cast<uint4*>(dst)[1] = out[1];
+  }
 }
 
 template <int D, int DT, int CT>
@@ -268,18 +250,18 @@ cudaError_t write_t(const CacheRowsParams& p, int num_sms, cudaStream_t st) {
   const int64_t blocks = (tokens * (D / 16) * groups + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(blocks);
-  if (!p.rope) cache_write_kernel<D, DT, CT, 0><<<grid, kThreads, 0, st>>>(p, per);
-  else if (p.r.rot % 16 == 0) cache_write_kernel<D, DT, CT, 1><<<grid, kThreads, 0, st>>>(p, per);
-  else cache_write_kernel<D, DT, CT, 2><<<grid, kThreads, 0, st>>>(p, per);
+  const bool small = blocks * kThreads < (int64_t(1) << 31);
+  if (!p.rope) cache_write_kernel<D, DT, CT, 0><<<grid, kThreads, 0, st>>>(p, per, small);
+  else if (p.r.rot % 16 == 0) cache_write_kernel<D, DT, CT, 1><<<grid, kThreads, 0, st>>>(p, per, small);
+  else cache_write_kernel<D, DT, CT, 2><<<grid, kThreads, 0, st>>>(p, per, small);
   return cudaGetLastError();
 }
 
 template <int D, int DT, int CT>
 cudaError_t read_t(const CacheRowsParams& p, cudaStream_t st) {
-  const int groups = (p.c.h_kv + kReadHeads - 1) / kReadHeads;
-  const int64_t blocks = (static_cast<int64_t>(p.c.b) * p.s * groups * (D / 16) + kThreads - 1) / kThreads;
+  const int64_t blocks = (static_cast<int64_t>(p.c.b) * p.s * p.c.h_kv * (D / 16) + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  cache_read_kernel<D, DT, CT><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p, groups);
+  cache_read_kernel<D, DT, CT><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p, blocks * kThreads < (int64_t(1) << 31));
   return cudaGetLastError();
 }
 

@@ -11,19 +11,16 @@
 namespace sdpa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kUnroll = 4;     // heads whose loads are in flight together
 
 // rot and d multiples of 16.  One thread: item m of token (bi, si), heads [h0, h0 + per).
 template <int DT, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p, int per, int groups) {
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p, int per, int groups, bool small) {
   const int items = p.d / 16;
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int m = static_cast<int>(idx % items);
-  const int64_t tok = (idx / items) % (static_cast<int64_t>(p.b) * p.s);
-  const int grp = static_cast<int>(idx / items / (static_cast<int64_t>(p.b) * p.s));
+  const Spot at = find_spot(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, items, p.b, p.s, small);
+  const int m = at.m, grp = at.grp, bi = at.bi, si = at.si;
   if (grp >= groups) return;
-  const int bi = static_cast<int>(tok / p.s), si = static_cast<int>(tok % p.s);
   const RopeItem it = rope_item(p.r, m);
   const int h1 = min(p.h_all, (grp + 1) * per);
   auto row_of = [&](int h, bool out) {
@@ -76,14 +73,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 
 // Any even rot and any d: one thread takes one pair (or two elements behind the rotated part).
 template <int DT, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constant__ RopeParams p, int per, int groups) {
+__global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constant__ RopeParams p, int per, int groups, bool small) {
   const int items = p.d / 2, half = p.r.rot / 2;
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int m = static_cast<int>(idx % items);
-  const int64_t tok = (idx / items) % (static_cast<int64_t>(p.b) * p.s);
-  const int grp = static_cast<int>(idx / items / (static_cast<int64_t>(p.b) * p.s));
+  const Spot at = find_spot(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, items, p.b, p.s, small);
+  const int m = at.m, grp = at.grp, bi = at.bi, si = at.si;
   if (grp >= groups) return;
-  const int bi = static_cast<int>(tok / p.s), si = static_cast<int>(tok % p.s);
   const bool turned = m < half;
   const int ia = turned && !INTER ? m : 2 * m, ib = turned && !INTER ? m + half : 2 * m + 1;
   float c = 1.f, s = 0.f;
@@ -119,10 +113,11 @@ cudaError_t launch_t(const RopeParams& p, int num_sms, cudaStream_t st) {
   const int groups = (p.h_all + per - 1) / per;
   const int64_t blocks = (tokens * items * groups + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const bool small = blocks * kThreads < (int64_t(1) << 31);
   if (vec)
-    rope_kernel<DT, INTER><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p, per, groups);
+    rope_kernel<DT, INTER><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p, per, groups, small);
   else
-    rope_any_kernel<DT, INTER><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p, per, groups);
+    rope_any_kernel<DT, INTER><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p, per, groups, small);
   return cudaGetLastError();
 }
 
