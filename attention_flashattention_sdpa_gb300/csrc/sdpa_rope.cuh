@@ -12,23 +12,28 @@ namespace sdpa {
 // cos and sin (times the factor) of one pair at position `pos`.  The table holds the turns per
 // position as 64-bit binary fractions, so pos * table[i] modulo 2^64 is the angle's exact fraction
 // of a turn: no loss however far the position.  The nearest quarter turn is taken off in whole
-// numbers as well; the rest x, at most pi/4, loses 2^-25 of itself as fp32.  There the Taylor
-// series end after x^9 (sin, off by 2e-9) and x^8 (cos, off by 3e-8, half a step of fp32).
+// numbers as well.  The rest, at most pi/4, is x + dx: what the conversion to fp32 rounds off joins
+// again by sin(x + dx) = sin x + dx cos x.  The Taylor series end after x^9 (sin, off by 2e-9) and
+// x^8 (cos, off by 3e-8, half a step of fp32).
 __device__ __forceinline__ void rope_angle(const RopeArgs& r, int64_t turns, int pos, float& c, float& s) {
   const uint64_t phase = static_cast<uint64_t>(turns) * static_cast<uint64_t>(static_cast<int64_t>(pos));
   const uint32_t top = static_cast<uint32_t>(phase >> 32);
   const uint32_t quarter = (top + (1u << 29)) >> 30;                   // 0..4
   const int32_t rest = static_cast<int32_t>(top - (quarter << 30));    // [-2^29, 2^29) of 2^32 a turn
-  const float x = static_cast<float>(rest) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+  constexpr float kHi = 1.4629180792671596e-9f;                        // 2 pi / 2^32 as fp32, and what that leaves
+  constexpr float kLo = static_cast<float>(1.4629180792671596e-9 - static_cast<double>(kHi));
+  const float n = static_cast<float>(rest);
+  const float x = n * kHi;
+  const float dx = fmaf(n, kHi, -x) + fmaf(n, kLo, static_cast<float>(rest - static_cast<int32_t>(n)) * kHi);
   const float y = x * x;
   float sp = fmaf(y, 1.f / 362880.f, -1.f / 5040.f);
   sp = fmaf(y, sp, 1.f / 120.f);
   sp = fmaf(y, sp, -1.f / 6.f);
-  const float sr = fmaf(x * y, sp, x);
   float cp = fmaf(y, 1.f / 40320.f, -1.f / 720.f);
   cp = fmaf(y, cp, 1.f / 24.f);
   cp = fmaf(y, cp, -0.5f);
-  const float cr = fmaf(y, cp, 1.f);
+  const float cr = fmaf(y, cp, 1.f) - x * dx;
+  const float sr = x + fmaf(x * y, sp, dx);
   const float sw = quarter & 1 ? cr : sr, cw = quarter & 1 ? sr : cr;
   const float f = r.factor;
   c = (quarter + 1) & 2 ? -f * cw : f * cw;
