@@ -17,12 +17,11 @@
 //                that do not exist and values that are not finite (a weight of zero does not hide a
 //                NaN in a product).
 //
-// E4M3: a tile's codes are multiplied by scale / 2^E (E: the exponent of the tile's largest scale) as
-// a sum of two F16 factors, so one rounding to F16's 11 bits is left, whatever the scales; 2^E of K
-// joins the factor on the scores and 2^E of V the exponent of the weights, both once a tile.
-// (K as stored against Q split into E4M3 terms was exact and spared its widening, but a key's scale
-// then multiplies each column of S in the softmax warps, which bound the tile: 2.8 us for 128 keys
-// by 256 rows.)
+// E4M3: K's codes become F16 as they are, so S of codes is exact up to the fp32 sums; the softmax warps
+// multiply each of its columns by the key's scale in fp32.  V's codes are multiplied by scale / 2^E (E:
+// the exponent of the tile's largest scale) as a sum of two F16 factors, so one rounding to F16's 11
+// bits is left, as P's, whatever the scales; 2^E joins the exponent of the weights once a tile.
+// (K times its scale in F16 too left the scores off by 2^-12 of themselves, which the LSE shows.)
 //
 // Bound: the tensor cores (4 x 128 x 128 x d MMAs a block of two tiles) and the exponentials, as
 // the prompt's forward pass; reading the cache once bounds it for few rows.
@@ -51,8 +50,12 @@ struct WideCfg {
   static constexpr int NK = D == 128 ? (E4 ? 1 : 2) : (E4 ? 2 : 3), NV = D == 128 ? 2 : 3;
   static constexpr int RK = E4 ? 2 : 0, RV = E4 ? 2 : 0;
   static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + NK * TILE, OFF_RAW = OFF_V + NV * TILE;
-  static constexpr int OFF_SC = OFF_RAW + (RK + RV) * RAW, OFF_CTL = OFF_SC + (RK + RV) * 512;
-  static constexpr int SMEM = OFF_CTL + 1024;
+  // Scales: V's stages, and K's in a ring that the softmax warps read.  A slot of K is free once S of
+  // the tile NK back is done, and that S followed the weights of the tile before it, or (split) two
+  // before it: NK + 2 tiles' scales never meet.
+  static constexpr int KS = E4 ? NK + 2 : 0;
+  static constexpr int OFF_SC = OFF_RAW + (RK + RV) * RAW, OFF_KS = OFF_SC + RV * 512, OFF_CTL = OFF_KS + KS * 512;
+  static constexpr int SMEM = OFF_CTL + 512;
   static constexpr int KSTEPS = D / 16;
   static constexpr int O_COL0 = 256;
   static constexpr float P_OFF = CT == kBF16 ? 0.f : 6.f;
@@ -67,7 +70,7 @@ struct alignas(8) WideBarriers {
   uint64_t raw_full[4], raw_empty[4];       // E4M3 tiles: K's stages, then V's
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t ml_full, o1_free;                // split: the second warpgroup's maxima and sums are there; its O is read
-  uint64_t ev_full[4];                      // E4M3: the exponent of a tile's V scales is known
+  uint64_t sc_full[4];                      // E4M3: a tile's K scales and the exponent of its V scales are there
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -106,10 +109,10 @@ struct Walk : Run {
 struct Control {
   WideBarriers bars;
   Walk walk;
-  int ek[8], ev[8];      // E4M3: exponents of a tile's scales, by tile count
+  int ev[8];             // E4M3: exponent of a tile's V scales, by tile count
   int found[8];          // segment count + 1 of a segment with cleared values
 };
-static_assert(sizeof(Control) <= 1024);
+static_assert(sizeof(Control) <= 512);
 
 // Whether V's tile of a 16-bit cache has to be cleared of what no row may meet.
 __device__ __forceinline__ bool needs_cleaning(const DecodeParams& p, const Segment& g, int tile) {
@@ -173,12 +176,12 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
   uint8_t* sQ = smem;
   uint8_t* sRing = smem + C::OFF_K;
   uint8_t* sRaw = smem + C::OFF_RAW;
-  float* sSc = reinterpret_cast<float*>(smem + C::OFF_SC);   // [stage][128]
+  float* sSc = reinterpret_cast<float*>(smem + C::OFF_SC);   // V's scales [stage][128]
+  float* sKs = reinterpret_cast<float*>(smem + C::OFF_KS);   // K's scales [tile % KS][128]
   // Split: the second warpgroup's maximum and sum of each row (the second tile of Q is not used).
   float2* s_ml = reinterpret_cast<float2*>(smem + C::TILE);
   Control& ctl = *reinterpret_cast<Control*>(smem + C::OFF_CTL);
   WideBarriers& bars = ctl.bars;
-  volatile int* s_ek = ctl.ek;
   volatile int* s_ev = ctl.ev;
   volatile int* s_found = ctl.found;
 
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
       mbar_init(&bars.raw_full[i], 1);
       mbar_init(&bars.raw_empty[i], 128);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&bars.ev_full[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars.sc_full[i], 4 + 1);
     mbar_init(&bars.ml_full, 128);
     mbar_init(&bars.o1_free, 128);
     mbar_init(&bars.drain, 1);
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
       const int boxes = kKeys / wp.box;     // boxes of a tile: 1, 2, 4 or 8
       const unsigned all = (1u << boxes) - 1u;
       // Lane x + 8 y issues copy y of box x: of 16-bit tiles the 128-byte columns, of E4M3 ones the
-      // codes and the scales.
+      // codes and V's scales.
       const int bx = lane % 8, by = lane / 8;
       constexpr int kCopies = E4 ? 2 : C::NCHUNK;
       bool ok = true;
@@ -281,24 +284,25 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           if (!mbar_wait_warp(E4 ? &bars.raw_empty[s] : &bars.empty[s], (at.turn & 1) ^ 1, wt)) { ok = false; break; }
           uint64_t* full = E4 ? &bars.raw_full[s] : &bars.full[s];
           uint8_t* dst = E4 ? sRaw + s * C::RAW : sRing + s * C::TILE;
-          float* sc = sSc + s * 128;
-          if constexpr (E4) {
+          const bool scales = E4 && is_v;
+          float* sc = sSc + (s - C::RK) * 128;
+          if (scales) {
             if (there != all) {      // no scale where there is no key
               for (int i = lane; i < kKeys; i += 32)
                 if (!((there >> (i / wp.box)) & 1u)) sc[i] = 0.f;
             }
             __syncwarp();
           }
-          if (lane == 0) mbar_arrive_expect_tx(full, E4 ? C::RAW + __popc(there) * wp.box * 4 : C::TILE);
+          if (lane == 0) mbar_arrive_expect_tx(full, E4 ? C::RAW + (scales ? __popc(there) * wp.box * 4 : 0) : C::TILE);
           ++issued;
           __syncwarp();
           if (bx < boxes && by < kCopies) {
             if constexpr (E4) {
               if (by == 0) {
                 tma_load_4d(dst + bx * wp.box * 128, map, full, 0, sl, hk, pg);
-              } else if (pg < p.c.num_pages) {
-                bulk_load(sc + bx * wp.box, (is_v ? p.c.v_scale : p.c.k_scale) +
-                          (static_cast<int64_t>(pg) * p.c.h_kv + hk) * p.c.page_size + sl, wp.box * 4, full);
+              } else if (scales && pg < p.c.num_pages) {
+                bulk_load(sc + bx * wp.box, p.c.v_scale + (static_cast<int64_t>(pg) * p.c.h_kv + hk) * p.c.page_size + sl,
+                          wp.box * 4, full);
               }
             } else {
               tma_load_4d(dst + by * 16384 + bx * wp.box * 128, map, full, by * 64, sl, hk, pg);
@@ -421,6 +425,22 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
     int n_seg = 0, n_tile = 0;
     while (ok && walk.next(p, sg)) {
       bool found = false;
+      // K's widening warps: page of the lane's key in a tile of this segment (-1: none), and its scale
+      // (0 where there is no key); both are asked for ahead.
+      auto page_of = [&](int j) {
+        const int key = j * kKeys + r;
+        return key < sg.L.len_kv ? __ldg(p.c.page_table + sg.bi * p.c.page_table_stride + key / p.c.page_size) : -1;
+      };
+      auto scale_of = [&](int j, int page) {
+        if (page < 0 || page >= p.c.num_pages) return 0.f;
+        return __ldg(p.c.k_scale + (static_cast<int64_t>(page) * p.c.h_kv + hk) * p.c.page_size + (j * kKeys + r) % p.c.page_size);
+      };
+      int page1 = -1;          // of the next tile
+      float scale0 = 0.f;      // of this one
+      if (E4 && warp < 16) {
+        scale0 = scale_of(sg.tile0, page_of(sg.tile0));
+        page1 = sg.tile0 + 1 < sg.tile1 ? page_of(sg.tile0 + 1) : -1;
+      }
       for (int j = sg.tile0; ok && j < sg.tile1; ++j, ++n_tile) {
         const bool tail = masked && (j + 1) * kKeys > sg.off;
         const bool on = j * kKeys + r < sg.L.len_kv;
@@ -430,23 +450,34 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           const int rs = from.at, s = to.at, left = sg.L.len_kv - j * kKeys;
           ok = mbar_wait_warp(&bars.raw_full[rs], from.turn & 1, wt);
           if (!ok) break;
-          const float* sc = sSc + rs * 128;
-          const int ex = largest_exponent(sc, left, lane);      // (by every lane)
-          if (warp % 4 == 0 && lane == 0) {
-            (is_v ? s_ev : s_ek)[n_tile % 8] = ex;
-            if (is_v) mbar_arrive(&bars.ev_full[n_tile % 4]);
+          __half2 h2 = __float2half2_rn(0.f), l2 = h2;
+          if (is_v) {
+            const float* sc = sSc + (rs - C::RK) * 128;
+            const int ex = largest_exponent(sc, left, lane);      // (by every lane)
+            if (warp % 4 == 0 && lane == 0) {
+              s_ev[n_tile % 8] = ex;
+              mbar_arrive(&bars.sc_full[n_tile % 4]);
+            }
+            // scale / 2^E of the lane's row as two F16, each twice in a word
+            const float f = on ? sc[r] * pow2(-ex) : 0.f;
+            const __half fh = __float2half_rn(f), fl = __float2half_rn(f - __half2float(fh));
+            h2 = __half2half2(fh);
+            l2 = __half2half2(fl);
           }
-          // scale / 2^E of the lane's row as two F16, each twice in a word
-          const float f = on ? sc[r] * pow2(-ex) : 0.f;
-          const __half fh = __float2half_rn(f), fl = __float2half_rn(f - __half2float(fh));
-          const __half2 h2 = __half2half2(fh), l2 = __half2half2(fl);
           ok = mbar_wait_warp(&bars.empty[s], (to.turn & 1) ^ 1, wt);
           if (!ok) break;
+          if (!is_v) {
+            sKs[n_tile % (C::KS > 0 ? C::KS : 1) * 128 + r] = scale0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.sc_full[n_tile % 4]);
+            scale0 = scale_of(j + 1, page1);
+            page1 = j + 2 < sg.tile1 ? page_of(j + 2) : -1;
+          }
           // A lane takes its row, 16 codes at a time; the swizzles of both tiles put the 8 rows of a
           // quarter-warp into 8 different 16-byte columns.
           const uint8_t* src = sRaw + rs * C::RAW + r * 128;
           uint8_t* dst = sRing + s * C::TILE + r * 128;
-          auto widen = [&](auto clear) {
+          auto widen = [&](auto scale, auto clear) {
 #pragma unroll
             for (int ch = 0; ch < D / 16; ++ch) {
               const uint4 in = *reinterpret_cast<const uint4*>(src + (ch ^ (r & 7)) * 16);
@@ -455,9 +486,11 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 out[e] = e4m3x2_to_f16x2(e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
-                const __half2 v = *reinterpret_cast<const __half2*>(&out[e]);
-                const __half2 y = __hfma2(v, h2, __hmul2(v, l2));
-                out[e] = *reinterpret_cast<const uint32_t*>(&y);
+                if constexpr (decltype(scale)::value) {
+                  const __half2 v = *reinterpret_cast<const __half2*>(&out[e]);
+                  const __half2 y = __hfma2(v, h2, __hmul2(v, l2));
+                  out[e] = *reinterpret_cast<const uint32_t*>(&y);
+                }
                 if constexpr (decltype(clear)::value) out[e] = on ? finite_pair<false>(out[e], found) : 0u;
               }
 #pragma unroll
@@ -468,8 +501,9 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
               }
             }
           };
-          if (is_v && (tail || left < kKeys)) widen(std::true_type{});
-          else widen(std::false_type{});
+          if (!is_v) widen(std::false_type{}, std::false_type{});
+          else if (tail || left < kKeys) widen(std::true_type{}, std::true_type{});
+          else widen(std::true_type{}, std::false_type{});
           if (found) s_found[n_seg % 8] = n_seg + 1;
           fence_proxy_async_smem();
           mbar_arrive(&bars.full[s]);
@@ -612,16 +646,16 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         if (!mbar_wait_warp(&bars.s_full[t], n_own & 1, wt)) { ok = false; break; }
         tc_fence_after();
         const int key0 = (sg.tile0 + i) * kKeys;
-        // E4M3: the tile's exponents, K's in the factor on the scores, V's in the weights' exponent and
-        // out of l again.
-        float cst = cs, ev = 0.f, back = 1.f;
+        // E4M3: the exponent of the tile's V, in the weights' exponent and out of l again; K's scales.
+        float ev = 0.f, back = 1.f;
+        const float* ks = nullptr;
         if constexpr (E4) {
           const int tile = n_tile + i;
-          if (!mbar_wait_warp(&bars.ev_full[tile % 4], (tile / 4) & 1, wt)) { ok = false; break; }
-          cst = cs * pow2(s_ek[tile % 8]);
+          if (!mbar_wait_warp(&bars.sc_full[tile % 4], (tile / 4) & 1, wt)) { ok = false; break; }
           const int e = s_ev[tile % 8];
           ev = static_cast<float>(e);
           back = pow2(-e);
+          ks = sKs + tile % C::KS * 128;
         }
         const bool need = key0 + kKeys > sg.L.len_kv || (masked && key0 + kKeys > sg.off) || bad;
         uint32_t vis[4];       // visible columns
@@ -663,7 +697,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         // steps: instruction fetch, not registers, limits an unrolled one.)
         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
         float alpha = 1.f;
-        float2 cs2 = make_float2(cst, cst), nm2 = make_float2(0.f, 0.f);
+        float2 cs2 = make_float2(cs, cs), nm2 = make_float2(0.f, 0.f);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int st = 0; st < 3; ++st) {
@@ -674,6 +708,18 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           tmem_ld_wait();
           reg_fence32(&sv[0]);
           reg_fence32(&sv[32]);
+          if constexpr (E4) {
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+              const float4 k = *reinterpret_cast<const float4*>(ks + h * 64 + c);
+              const float2 a = mul2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), make_float2(k.x, k.y));
+              const float2 b = mul2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), make_float2(k.z, k.w));
+              sv[c] = __float_as_uint(a.x);
+              sv[c + 1] = __float_as_uint(a.y);
+              sv[c + 2] = __float_as_uint(b.x);
+              sv[c + 3] = __float_as_uint(b.y);
+            }
+          }
           if (need) {
             const uint32_t v0 = h ? vis[2] : vis[0], v1 = h ? vis[3] : vis[1];
 #pragma unroll
@@ -691,7 +737,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           }
           if (st == 0) continue;
           if (st == 1) {
-            const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cst, ev);
+            const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cs, ev);
             if (m_cand > m_ref + C::THRESH) {
               alpha = ex2(m_ref - m_cand);
               m_ref = m_cand;

@@ -78,15 +78,14 @@ def dense(values, scales, page_table, i, n):
 
 
 def attend(q, k_values, v_values, k_scales, v_scales, page_table, lens_kv, lens_q, scale, causal=False, tree=None):
-    """O, LSE and spread = sum_j P_j |v_j| (the scale of O's weight errors) of q [b, h_q, s, d], and, for an
-    implementation that rounds K's elements: what a unit relative error of each changes at most in O and in LSE.
-    A score is then off by at most r_j = |scale| sum_d |q_d k_jd|, LSE by sum_j P_j r_j, O by
-    sum_j P_j r_j |v_j - O| (first order).  tree: bool [b, s, s] (row i sees drafted token j), or None."""
+    """O, LSE, spread = sum_j P_j |v_j| (the scale of O's weight errors) of q [b, h_q, s, d], and reach =
+    sum_j P_j |scale| sum_d |q_d k_jd|, the scale of LSE's errors from the sums of the scores.
+    tree: bool [b, s, s] (row i sees drafted token j), or None."""
     b, h_q, s, d = q.shape
     h_kv, ps = k_values.shape[1], k_values.shape[2]
     o, spread = np.zeros(q.shape), np.zeros(q.shape)
     lse = np.full((b, h_q, s), -np.inf)
-    o_reach, l_reach = np.zeros(q.shape), np.zeros((b, h_q, s))
+    reach = np.zeros((b, h_q, s))
     for i in range(b):
         n = min(max(lens_kv[i], 0), page_table.shape[1] * ps)
         m = min(max(lens_q[i], 0), s) if lens_q is not None else s
@@ -112,7 +111,5 @@ def attend(q, k_values, v_values, k_scales, v_scales, page_table, lens_kv, lens_
                 o[i, h, r] = p @ vv / l
                 spread[i, h, r] = p @ np.abs(vv) / l
                 lse[i, h, r] = big + math.log(l)
-                reach = abs(scale) * (np.abs(k[h * h_kv // h_q][see]) @ np.abs(q[i, h, r]))
-                l_reach[i, h, r] = p @ reach / l
-                o_reach[i, h, r] = (p * reach) @ np.abs(vv - o[i, h, r]) / l
-    return o, lse, spread, o_reach, l_reach
+                reach[i, h, r] = abs(scale) * (p @ (np.abs(k[h * h_kv // h_q][see]) @ np.abs(q[i, h, r]))) / l
+    return o, lse, spread, reach
