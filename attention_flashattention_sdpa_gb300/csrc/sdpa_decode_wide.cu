@@ -691,17 +691,16 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           }
           __syncwarp();
         }
-        // The row's 128 scores come in halves of 64 columns: the second for its maximum, then the
-        // first, which stays for its exponentials, then the second again.  P takes the columns of
-        // the first quarter and then of the second, both read by then.  (One body for the three
-        // steps: instruction fetch, not registers, limits an unrolled one.)
-        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+        // The row's 128 scores come in halves of 64 columns, each with its own step of the running
+        // maximum; P takes the columns of the first quarter and then of the second, both read by then.
+        // The reference m_ref is an integer, so the rare step between the halves scales the first
+        // half's P, already rounded, exactly.  (One body for both: instruction fetch, not registers,
+        // limits an unrolled one.)
         float alpha = 1.f;
-        float2 cs2 = make_float2(cs, cs), nm2 = make_float2(0.f, 0.f);
+        const float2 cs2 = make_float2(cs, cs);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll 1
-        for (int st = 0; st < 3; ++st) {
-          const int h = st == 1 ? 0 : 1;
+        for (int h = 0; h < 2; ++h) {
           uint32_t sv[64];
           tmem_ld32(s_addr + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
           tmem_ld32(s_addr + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
@@ -726,25 +725,38 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
             for (int c = 0; c < 64; ++c)
               if (!(((c < 32 ? v0 : v1) >> (c % 32)) & 1u)) sv[c] = __float_as_uint(-INFINITY);
           }
-          if (st < 2) {
+          float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 64; c += 8) {
-              mx0 = max3(mx0, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-              mx1 = max3(mx1, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
-              mx2 = max3(mx2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
-              mx3 = max3(mx3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+          for (int c = 0; c < 64; c += 8) {
+            mx0 = max3(mx0, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+            mx1 = max3(mx1, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+            mx2 = max3(mx2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
+            mx3 = max3(mx3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+          }
+          const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cs, ev);
+          const bool up = m_cand > m_ref + C::THRESH;
+          if (__any_sync(0xffffffffu, up)) {
+            const float m_new = up ? ceilf(m_cand) : m_ref, a = up ? ex2(m_ref - m_new) : 1.f;
+            m_ref = m_new;
+            alpha *= a;
+            if (h == 1) {
+              acc0 = mul2(acc0, make_float2(a, a));
+              acc1 = mul2(acc1, make_float2(a, a));
+              uint32_t pv[32];
+              tmem_st_wait();
+              tmem_ld32(s_addr, pv);
+              tmem_ld_wait();
+              reg_fence32(pv);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float2 f = unpack_pair<BF>(pv[e]);
+                pv[e] = pack_pair<BF>(f.x * a, f.y * a);
+              }
+              tmem_st32(s_addr, pv);
             }
           }
-          if (st == 0) continue;
-          if (st == 1) {
-            const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cs, ev);
-            if (m_cand > m_ref + C::THRESH) {
-              alpha = ex2(m_ref - m_cand);
-              m_ref = m_cand;
-            }
-            const float nm = m_ref == -INFINITY ? 0.f : C::P_OFF - m_ref + ev;
-            nm2 = make_float2(nm, nm);
-          }
+          const float nm = m_ref == -INFINITY ? 0.f : C::P_OFF - m_ref + ev;
+          const float2 nm2 = make_float2(nm, nm);
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 4) {
