@@ -610,8 +610,9 @@ int ctas_of_sm(int tile_rows, bool e4m3) {
 }  // namespace
 
 void decode_plan(DecodeParams* p, int d, int ct, int num_sms) {
-  // Many rows: measured at 8 x 8192 tokens, 8 KV heads of 128: E4M3 66 us against 77 for 32 rows, 90
-  // against 78 for 48; BF16 63 against 54 for 24 (8 or 16 rows a block first, the wide blocks second).
+  // Many rows: measured at 8 x 8192 tokens, 8 KV heads of 128, blocks of 8 or 16 rows against the wide
+  // ones: E4M3 65 us against 78 for 32 rows, 87 against 78 for 40; BF16 62 against 58 for 24 (d = 64:
+  // E4M3 47 against 53, 63 against 53; BF16 42 against 38).
   p->wide = d <= 128 && p->rows > (ct == kE4M3 ? 32 : 16);
   p->tile_rows = p->wide ? 256 : p->rows <= 8 ? 8 : 16;
   p->row_tiles = (p->rows + p->tile_rows - 1) / p->tile_rows;
