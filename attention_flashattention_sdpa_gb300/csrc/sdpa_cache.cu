@@ -6,7 +6,9 @@
 //
 // Bound: memory.  A row of d elements is spread over d / 16 lanes of 16 elements each, which find
 // the row's largest value by shuffles; a thread walks heads of one token, so that its angles and
-// its page are looked up once.
+// its page are looked up once.  Measured, 8 heads of 128, E4M3 from or to BF16: 4 prompts of 5001 to
+// 8192 tokens written, K rotated, 38.8 us (4.6 TB/s, 68% of a copy: the roundings of a row wait for
+// its largest value), 32 single tokens 3.0 us; 2 x 8192 tokens read 19.2 us (5.1 TB/s, 76%).
 #include <cuda_fp8.h>
 
 #include "sdpa_rope.cuh"

@@ -29,6 +29,11 @@
 // E4M3 caches: codes widen exactly to F16; a key's scale multiplies its score, and the scale of
 // its value joins the exponent, w = 2^(s + log2 vs - max), so that O = sum w v_code and
 // l = sum w / vs.  The row max then bounds w whatever the scales, and no product with vs is rounded.
+//
+// Measured, groups of 8 heads, d = 128: 32 sequences of 1000 to 16384 tokens, E4M3, 110 us (5.65 TB/s, 83%
+// of a copy; BF16 131000 tokens of one sequence 86 us, 6.25 TB/s, 92%); 1000 tokens of one sequence 7 us, of
+// which reading is 0.6: two launches that start inside each other, a load's latency for the lengths, the
+// page, the keys, and the parts.
 #include <type_traits>
 
 #include "sdpa_decode.cuh"
@@ -313,9 +318,13 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
         const float* sc = reinterpret_cast<const float*>(st + 2 * kSlice * C::RB);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float ks = sc[g + 8 * u], vs = g + 8 * u < valid ? sc[kSlice + g + 8 * u] : 1.f;
+          // A scale of zero (codes of a row of zeros) counts as 2^-69, the least that sdpa_cache_write
+          // gives; one of NaN reaches l by the weights alone, so that hidden keys leave it as it is.
+          const float ks = sc[g + 8 * u];
+          float vs = g + 8 * u < valid ? sc[kSlice + g + 8 * u] : 1.f;
+          vs = vs == 0.f ? 0x1p-69f : vs;
           const float lv = __log2f(vs);
-          rvs[u] = __fdividef(1.f, vs);
+          rvs[u] = vs != vs ? 0.f : __fdividef(1.f, vs);
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
             s[n][2 * u] = fmaf(s[n][2 * u], cs[n][0] * ks, lv);

@@ -237,7 +237,7 @@ struct CacheArgs {
   int64_t page_table_stride;
   const int32_t* seq_lens_kv;
   int num_pages, page_size, h_kv, b, max_pages;
-  int max_len;                 // min(max_pages * page_size, 2^31 - 1)
+  int max_len;                 // min(max_pages * page_size, 2^30)
 };
 
 struct CacheRowsParams {

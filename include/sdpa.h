@@ -318,7 +318,7 @@ SDPA_API sdpa_status_t sdpa_rope_bwd(const sdpa_rope_t* p, const void* dq_out, c
 /* A paged key/value cache.  Position j of sequence i lives in page page_table[i][j / page_size],
  * slot j % page_size.  Keys and values are logical [num_pages][h_kv][page_size][d] views (the
  * fields b, h, s, d of the strides are page, head, slot, element), so a page may be stored
- * head-major or slot-major.  E4M3 caches have an fp32 scale for each token and head:
+ * head-major or slot-major.  E4M3 caches have an fp32 scale >= 0 for each token and head:
  * value = code * scale. */
 typedef struct {
   int32_t num_pages;        /* >= 1 */

@@ -348,6 +348,50 @@ def test_decode_few_keys_lse(kind, rows):
         assert (err <= 2.0 ** -18 * reach[b, :, :n] + 2.0 ** -20 * (1 + np.abs(L[b, :, :n]))).all(), err.max()
 
 
+@pytest.mark.parametrize("s,h_q", [(5, 2), (20, 8)])
+@pytest.mark.parametrize("spoil", [float("nan"), float("inf")])
+def test_hidden_tokens_may_have_any_scale(s, h_q, spoil):
+    """A drafted token written as NaN or infinity (its scale is one then) reaches exactly the rows that see it."""
+    g = torch.Generator().manual_seed(23)
+    n, bad = 50, s // 2
+    c = make_cache((n,), 1, 128, 16, "e4m3", seed=24)
+    q = bshd(g, "bf16", 1, h_q, s, 128)
+    tree = random_tree(s, 4)[None]
+    tree[0, :, bad] = False
+    tree[0, bad, bad] = True
+    clean, clean_lse = run_decode(c, q, tree=tree)
+    pos = n - s + bad
+    pg, sl = c.page_table[0, pos // 16].item(), pos % 16
+    seen = torch.zeros(s, dtype=torch.bool)
+    seen[bad] = True
+    for scales in ((c.v_scale,), (c.k_scale,), (c.k_scale, c.v_scale)):
+        kept = [t[pg, 0, sl].clone() for t in scales]
+        for t in scales:
+            t[pg, 0, sl] = spoil
+        o, lse = run_decode(c, q, tree=tree)
+        assert torch.equal(o[0, :, ~seen], clean[0, :, ~seen]) and torch.equal(lse[0, :, ~seen], clean_lse[0, :, ~seen])
+        if spoil != spoil or scales[-1] is c.v_scale:      # (a score of -inf is a weight of zero)
+            assert not torch.isfinite(o[0, :, seen]).any()
+        for t, x in zip(scales, kept):
+            t[pg, 0, sl] = x
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_decode_zero_scales(rows):
+    """Rows of zeros whose scale is zero count in the sums and add nothing."""
+    g = torch.Generator().manual_seed(25)
+    c = make_cache((300, 40), 2, 128, 16, "e4m3", seed=26)
+    q = bshd(g, "bf16", 2, 4, rows, 128)
+    for t, sc in ((c.k, c.k_scale), (c.v, c.v_scale)):
+        zero = torch.rand(sc.shape, generator=g).cuda() < 0.6
+        sc[zero] = 0.0
+        t.view(torch.uint8)[zero] = 0
+    kv, vv, ks, vs, table = c.np()
+    o, lse = run_decode(c, q)
+    ref = so.attend(f64(q), kv, vv, ks, vs, table, (300, 40), None, 128 ** -0.5)
+    assert_attend_close(o, lse, ref, "bf16", "f16", kv_rounding=kv_rounding("e4m3", rows * 2, 128))
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
 @pytest.mark.parametrize("s,h_q", [(5, 2), (20, 8)])
 def test_hidden_tokens_may_hold_anything(kind, s, h_q):
