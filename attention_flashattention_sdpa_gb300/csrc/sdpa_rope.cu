@@ -4,9 +4,8 @@
 //
 // Bound: memory, 4 bytes an element.  A thread owns 16 elements of a token's head (8 pairs:
 // two 16-byte loads and stores) and walks 8 heads of that token, so that the 8 angles are computed
-// once for all of them.  Measured at 2 x 8192 tokens, 16 + 16 heads of 128: 43.2 us, 6.21 TB/s, 92% of
-// a copy's 6.77; 4 or 2 heads a thread 46-55 us, the first loads ahead of the angles 46-52, blocks of 256
-// threads 43.7.
+// once for all of them.  Measured at 2 x 8192 tokens, 16 + 16 heads of 128: 43.6 us, 6.15 TB/s, 91% of
+// a copy's 6.77; 4 or 2 heads a thread 46-55 us, the first loads ahead of the angles 46-52.
 #include "sdpa_rope.cuh"
 
 namespace sdpa {
