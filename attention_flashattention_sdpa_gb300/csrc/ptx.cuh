@@ -453,5 +453,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Largest magnitude of three; a NaN among them stays one.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 }  // namespace ptx
 }  // namespace sdpa

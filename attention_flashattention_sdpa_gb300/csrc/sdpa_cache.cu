@@ -7,7 +7,7 @@
 // Bound: memory.  A row of d elements is spread over d / 16 lanes of 16 elements each, which find
 // the row's largest value by shuffles; a thread walks heads of one token, so that its angles and
 // its page are looked up once.  Measured, 8 heads of 128, E4M3 from or to BF16: 4 prompts of 5001 to
-// 8192 tokens written, K rotated, 38.8 us (4.6 TB/s, 68% of a copy: the roundings of a row wait for
+// 8192 tokens written, K rotated, 36.5 us (4.9 TB/s, 73% of a copy: the roundings of a row wait for
 // its largest value), 32 single tokens 3.0 us; 2 x 8192 tokens read 19.2 us (5.1 TB/s, 76%).
 #include <cuda_fp8.h>
 
@@ -26,16 +26,33 @@ __device__ __forceinline__ uint32_t pack4_e4m3(float a, float b, float c, float 
   return (lo & 0xFFFFu) | (hi << 16);
 }
 
-// Largest magnitude over the LANES lanes of a row.  As bits of non-negative fp32 values the
-// order of unsigned integers is that of the values, with infinity and then NaN above them all.
+// Scales of a row of K and of one of V held 16 elements a lane by the LANES lanes from m = 0 on, and
+// what multiplies the elements, for both rows in every lane.  The lanes of even m find K's largest
+// magnitude and divide, those of odd m V's.
+struct RowScales {
+  float k, v, k_inv, v_inv;
+};
+
 template <int LANES>
-__device__ __forceinline__ float row_amax(const float (&x)[16]) {
-  uint32_t m = 0;
+__device__ __forceinline__ RowScales row_scales(const float (&x)[16], const float (&y)[16], int m) {
+  auto lane_max = [](const float (&e)[16]) {
+    float a = 0.f, b = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 16; i += 4) {
+      a = ptx::max3_abs_nan(a, e[i], e[i + 1]);
+      b = ptx::max3_abs_nan(b, e[i + 2], e[i + 3]);
+    }
+    return ptx::max3_abs_nan(a, b, 0.f);
+  };
+  const float ak = lane_max(x), av = lane_max(y);
+  const bool odd = m & 1;
+  float a = odd ? av : ak;
+  a = ptx::max3_abs_nan(a, __shfl_xor_sync(0xffffffffu, odd ? ak : av, 1), 0.f);
 #pragma unroll
-  for (int o = 1; o < LANES; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return __uint_as_float(m);
+  for (int o = 2; o < LANES; o *= 2) a = ptx::max3_abs_nan(a, __shfl_xor_sync(0xffffffffu, a, o), 0.f);
+  const float scale = (a < kAmaxMin ? kAmaxMin : a) / kE4M3Max, inv = 1.f / scale;   // a NaN stays one
+  const float other = __shfl_xor_sync(0xffffffffu, scale, 1), other_inv = __shfl_xor_sync(0xffffffffu, inv, 1);
+  return odd ? RowScales{other, scale, other_inv, inv} : RowScales{scale, other, inv, other_inv};
 }
 
 struct Slot {
@@ -82,26 +99,24 @@ __device__ __forceinline__ void unpack_item(const Raw& r, float (&x)[16]) {
 // Stores an item (16 values, runs at lo and hi) of one row; lane 0 of the row stores its scale.
 template <int D, int CT>
 __device__ __forceinline__ void store_item(uint8_t* row, float* scale_at, int m, int lo, int hi, const float (&x)[16],
-                                           bool live) {
+                                           float scale, float inv, bool live) {
+  if (!live) return;
   if constexpr (CT == kE4M3) {
-    const float amax = row_amax<D / 16>(x);
-    const float scale = (amax < kAmaxMin ? kAmaxMin : amax) / kE4M3Max;   // a NaN stays one
-    const float inv = 1.f / scale;
-    if (!live) return;
-    uint2 a, b;
-    a.x = pack4_e4m3(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    a.y = pack4_e4m3(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-    b.x = pack4_e4m3(x[8] * inv, x[9] * inv, x[10] * inv, x[11] * inv);
-    b.y = pack4_e4m3(x[12] * inv, x[13] * inv, x[14] * inv, x[15] * inv);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = make_float2(inv, inv), a = ptx::mul2(make_float2(x[4 * i], x[4 * i + 1]), f),
+                   b = ptx::mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), f);
+      w[i] = pack4_e4m3(a.x, a.y, b.x, b.y);
+    }
     if (hi == lo + 8) {
-      *reinterpret_cast<uint4*>(row + lo) = make_uint4(a.x, a.y, b.x, b.y);
+      *reinterpret_cast<uint4*>(row + lo) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
-      *reinterpret_cast<uint2*>(row + lo) = a;
-      *reinterpret_cast<uint2*>(row + hi) = b;
+      *reinterpret_cast<uint2*>(row + lo) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(row + hi) = make_uint2(w[2], w[3]);
     }
     if (m == 0) *scale_at = scale;
   } else {
-    if (!live) return;
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = pack16<CT>(x[2 * i], x[2 * i + 1]);
@@ -111,8 +126,10 @@ __device__ __forceinline__ void store_item(uint8_t* row, float* scale_at, int m,
 }
 
 // ROPE: 0 none, 1 rot a multiple of 16, 2 any even rot.
+// (A floor of one block an SM lets the compiler hold a few more registers, 122, still four blocks: 38.5 ->
+// 36.5 us.)
 template <int D, int DT, int CT, int ROPE>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheRowsParams p, int per,
+__global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_constant__ CacheRowsParams p, int per,
                                                             bool small) {
   constexpr int LANES = D / 16;
   const Spot who = find_spot(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, LANES, p.c.b, p.s, small);
@@ -139,6 +156,16 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     }
   };
   fetch(h0);
+  if constexpr (CT == kE4M3) {
+    // The row's other heads start towards L2, a line a lane: 38.3 -> 36.5 us for the prompts above, 16 heads
+    // 44.0 -> 41.0.  (16-bit caches, copied without that much work between, were slower so: 44.6 -> 47.8.)
+    constexpr int LINES = D / 64;
+    for (int i = m; live && i < (h_end - h0 - 1) * LINES; i += LANES) {
+      const int h = h0 + 1 + i / LINES, e = i % LINES * 64;
+      ptx::prefetch_l2(static_cast<const uint16_t*>(p.k) + bi * p.k_st[0] + h * p.k_st[1] + si * p.k_st[2] + e);
+      ptx::prefetch_l2(static_cast<const uint16_t*>(p.v) + bi * p.v_st[0] + h * p.v_st[1] + si * p.v_st[2] + e);
+    }
+  }
   int rpos = pos;
   float c[8], s[8];
   if constexpr (ROPE != 0) {
@@ -187,11 +214,13 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = y[i] = 0.f;
     }
+    RowScales rs{0.f, 0.f, 0.f, 0.f};
+    if constexpr (CT == kE4M3) rs = row_scales<LANES>(x, y, m);
     const int64_t sc = (at.page * p.c.h_kv + h) * p.c.page_size + at.slot;
     store_item<D, CT>(p.c.k + at.page * p.c.k_st[0] + h * p.c.k_st[1] + at.slot * p.c.k_st[2], p.c.k_scale + sc, m,
-                      it.lo, it.hi, x, on);
+                      it.lo, it.hi, x, rs.k, rs.k_inv, on);
     store_item<D, CT>(p.c.v + at.page * p.c.v_st[0] + h * p.c.v_st[1] + at.slot * p.c.v_st[2], p.c.v_scale + sc, m,
-                      m * 16, m * 16 + 8, y, on);
+                      m * 16, m * 16 + 8, y, rs.v, rs.v_inv, on);
   }
 }
 

@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "ptx.cuh"
 #include "sdpa_internal.h"
 
 namespace sdpa {
@@ -110,14 +111,19 @@ __device__ __forceinline__ RopeItem rope_item(const RopeArgs& r, int m) {
   return it;
 }
 
-// Rotates 16 values of an item (x[0..8) at lo, x[8..16) at hi) by its 8 angles.
+// Rotates 16 values of an item (x[0..8) at lo, x[8..16) at hi) by its 8 angles, two at a time.
 __device__ __forceinline__ void rope_turn(bool interleaved, float (&x)[16], const float (&c)[8], const float (&s)[8]) {
+  const int step = interleaved ? 2 : 1, b0 = interleaved ? 1 : 8;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ia = interleaved ? 2 * i : i, ib = interleaved ? 2 * i + 1 : i + 8;
-    const float a = x[ia], b = x[ib];
-    x[ia] = a * c[i] - b * s[i];
-    x[ib] = a * s[i] + b * c[i];
+  for (int i = 0; i < 8; i += 2) {
+    float &a0 = x[i * step], &a1 = x[(i + 1) * step], &b0r = x[i * step + b0], &b1r = x[(i + 1) * step + b0];
+    const float2 a = make_float2(a0, a1), b = make_float2(b0r, b1r);
+    const float2 cc = make_float2(c[i], c[i + 1]), ss = make_float2(s[i], s[i + 1]);
+    const float2 y = ptx::fma2(b, make_float2(-ss.x, -ss.y), ptx::mul2(a, cc)), z = ptx::fma2(a, ss, ptx::mul2(b, cc));
+    a0 = y.x;
+    a1 = y.y;
+    b0r = z.x;
+    b1r = z.y;
   }
 }
 
