@@ -21,7 +21,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const Spot at = find_spot(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, items, p.b, p.s, small);
   const int m = at.m, grp = at.grp, bi = at.bi, si = at.si;
   if (grp >= groups) return;
-  const RopeItem it = rope_item(p.r, m);
+  // Eight elements of each half of the rotated part, or of what lies behind it, so that neighbouring
+  // lanes read and write neighbouring 16 bytes (16 neighbouring elements of interleaved pairs: 31.5 us
+  // against 31.1 for the backward pass of 4999 tokens, 64 + 8 heads, half of each rotated).
+  const bool turned = m * 16 < p.r.rot;
+  const int start = turned ? 0 : p.r.rot, m8 = m * 8 - start / 2, width = turned ? p.r.rot : p.d - p.r.rot;
+  const RopeItem it{start + m8, start + width / 2 + m8, turned};
   const int h1 = min(p.h_all, (grp + 1) * per);
   auto row_of = [&](int h, bool out) {
     const int t = h >= p.h_q;
@@ -43,7 +48,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   if (it.turned) {
     const int pos = p.r.positions ? p.r.positions[bi * p.r.positions_stride + si] : si;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rope_angle(p.r, __ldg(p.r.table + m * 8 + i), pos, c[i], s[i]);
+    for (int i = 0; i < 8; ++i) {
+      const int pair = !INTER ? m * 8 + i : i < 4 ? m * 4 + i : p.r.rot / 4 + m * 4 + i - 4;
+      rope_angle(p.r, __ldg(p.r.table + pair), pos, c[i], s[i]);
+    }
   }
   for (int h0 = grp * per; h0 < h1; h0 += kUnroll) {
     load(h0);
