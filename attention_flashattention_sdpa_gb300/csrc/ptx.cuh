@@ -453,6 +453,25 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// All threads of a cluster's CTAs meet; what they wrote to shared memory before is seen after.
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Shared memory of CTA `rank` of the cluster, at this CTA's address.
+__device__ __forceinline__ float2 ld_cluster_f2(const void* at, int rank) {
+  float2 v;
+  asm volatile("{\n.reg .u32 a;\nmapa.shared::cluster.u32 a, %2, %3;\nld.shared::cluster.v2.f32 {%0, %1}, [a];\n}"
+               : "=f"(v.x), "=f"(v.y) : "r"(smem_u32(at)), "r"(rank) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(const void* at, int rank) {
+  float4 v;
+  asm volatile("{\n.reg .u32 a;\nmapa.shared::cluster.u32 a, %4, %5;\nld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(smem_u32(at)), "r"(rank) : "memory");
+  return v;
+}
+
 // Largest magnitude of three; a NaN among them stays one.
 __device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
   float d;

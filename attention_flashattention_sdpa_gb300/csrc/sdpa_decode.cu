@@ -8,7 +8,8 @@
 // the same time share DRAM pages (runs over (head, tile) pairs, a head at a time, read 128-byte rows
 // at 4.6 instead of 5.2 TB/s and 64-byte rows at 3.7 instead of 5.0).  A sequence that lies in one
 // run is finished there; the others leave unnormalised partial results (O, running max, sum) that
-// decode_combine_kernel joins, in a fixed order.
+// decode_combine_kernel joins, in a fixed order.  Short sequences go to a cluster of CTAs each (and
+// block of rows) instead, whose parts meet in its shared memory: one launch.
 //
 // Bound: reading the cache once.  With 8 rows a key costs 2 x 8 x d multiply-adds for 2 d elements
 // read, far below what the tensor cores do in the time of the read; so the products are warp-level
@@ -31,9 +32,8 @@
 // l = sum w / vs.  The row max then bounds w whatever the scales, and no product with vs is rounded.
 //
 // Measured, groups of 8 heads, d = 128: 32 sequences of 1000 to 16384 tokens, E4M3, 110 us (5.65 TB/s, 83%
-// of a copy; BF16 131000 tokens of one sequence 86 us, 6.25 TB/s, 92%); 1000 tokens of one sequence 7 us, of
-// which reading is 0.6: two launches that start inside each other, a load's latency for the lengths, the
-// page, the keys, and the parts.
+// of a copy; BF16 131000 tokens of one sequence 86 us, 6.25 TB/s, 92%); 1000 tokens of one sequence 6.9 us, of
+// which reading is 0.6: the launch, a load's latency for the lengths, the page and the keys, the cluster.
 #include <type_traits>
 
 #include "sdpa_decode.cuh"
@@ -46,6 +46,7 @@ constexpr int kSlice = 16;                 // keys of a warp's slice
 constexpr int kTile = kWarps * kSlice;     // keys of a tile (decode_plan's tile_shift)
 static_assert(kTile == 64);
 constexpr int kThreads = kWarps * 32;
+constexpr int kMaxCluster = 8;
 
 // NR: blocks of 8 query rows that a CTA works on at once.
 template <int D, int CT, int NR>
@@ -126,16 +127,26 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
   __shared__ int s_found;
+  __shared__ float2 s_part[ROWS];   // clusters: this CTA's maximum and sum of each row
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, c = lane % 4;
   uint8_t* ring = smem + warp * C::NS * C::STAGE;
 
-  // This CTA's block of rows, the same of every sequence, and its team's run.
-  const int blocks = p.c.h_kv * p.row_tiles, blk = blockIdx.x % blocks;
+  // This CTA's block of rows, the same of every sequence, and its team's run; or, in a cluster, its
+  // share of one sequence.
+  const int cl = p.cluster, unit = cl ? static_cast<int>(blockIdx.x) / cl : static_cast<int>(blockIdx.x);
+  const int blocks = p.c.h_kv * p.row_tiles, blk = unit % blocks;
   const int hk = blk / p.row_tiles, r0 = (blk % p.row_tiles) * ROWS;
   griddep_launch_dependents();
-  Run run = find_run(p, blockIdx.x / blocks, lane);
+  Run run;
+  if (cl) {
+    const int k = blockIdx.x % cl, n = seq_tiles(p, unit / blocks);
+    run = Run{static_cast<long long>(n) * k / cl, static_cast<long long>(n) * (k + 1) / cl, 0, unit / blocks};
+    if (threadIdx.x < ROWS) s_part[threadIdx.x] = make_float2(-INFINITY, 0.f);
+  } else {
+    run = find_run(p, unit / blocks, lane);
+  }
 
   // cp.async: lane's chunk of rows (lane / CH) + x * RPX of a slice.
   constexpr int RPX = 32 / C::CH;
@@ -500,7 +511,10 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
         x.z = add_nonfinite<D, CT>(p, bi, hk, L, row, d + 2, k0, k1, x.z);
         x.w = add_nonfinite<D, CT>(p, bi, hk, L, row, d + 3, k0, k1, x.w);
       }
-      if (!whole) {
+      if (cl) {      // over the first warp's part, which no other thread reads here
+        *reinterpret_cast<float4*>(merge + r * D + d) = x;
+        if (d == 0) s_part[r] = make_float2(mb, lb);
+      } else if (!whole) {
         const int64_t at = static_cast<int64_t>(part) * ROWS + r;
         *reinterpret_cast<float4*>(p.part_o + at * D + d) = x;
         if (d == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(mb, lb);
@@ -518,6 +532,51 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
     }
     __syncthreads();   // the ring and the exchange arrays are free again
     run.t = run.base + tile1;
+  }
+
+  // ---- a cluster's results meet in shared memory, its CTAs joining a share of the elements each -----
+  if (cl) {
+    __syncwarp();
+    cluster_sync_all();
+    const int bi = unit / blocks, live = min(ROWS, p.rows - r0);
+    const SeqLens L = seq_lens(p, bi);
+    for (int idx = (blockIdx.x % cl) * kThreads + threadIdx.x; idx < live * (D / 4); idx += cl * kThreads) {
+      const int r = idx / (D / 4), d = idx % (D / 4) * 4;
+      float2 ml[kMaxCluster];
+      float4 v[kMaxCluster];
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < cl) {
+          ml[k] = ld_cluster_f2(&s_part[r], k);
+          v[k] = ld_cluster_f4(smem + (r * D + d) * 4, k);
+        }
+      }
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k)
+        if (ml[k].y != 0.f) m = fmaxf(m, ml[k].x);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        const float f = part_weight(ml[k], m);     // 0 where a CTA had no key: its part was not written
+        l += ml[k].y * f;
+        x.x += f == 0.f ? 0.f : v[k].x * f;
+        x.y += f == 0.f ? 0.f : v[k].y * f;
+        x.z += f == 0.f ? 0.f : v[k].z * f;
+        x.w += f == 0.f ? 0.f : v[k].w * f;
+      }
+      const int row = r0 + r;
+      const bool none = row / p.group >= L.len_q || l == 0.f;
+      const float inv = none ? 0.f : 1.f / l;
+      const uint2 w = none ? make_uint2(0, 0)
+                           : make_uint2(pack_pair<QT == kBF16>(x.x * inv, x.y * inv), pack_pair<QT == kBF16>(x.z * inv, x.w * inv));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row_offset(p, p.o_st, bi, hk, row) + d) = w;
+      if (p.lse && d == 0) p.lse[lse_offset(p, bi, hk, row)] = none ? -INFINITY : natural_lse(m - C::P_OFF, l);
+    }
+    __syncwarp();
+    cluster_sync_all();    // nobody leaves while its shared memory is read
   }
 }
 
@@ -591,6 +650,20 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   auto kern = decode_kernel<D, CT, QT, NR>;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
+  if (p.cluster) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = p.cluster;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+  }
   kern<<<p.ctas, kThreads, C::SMEM, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -646,11 +719,30 @@ void decode_plan(DecodeParams* p, int d, int ct, int num_sms) {
   const long long tiles = static_cast<long long>(p->c.b) * ((p->c.max_len + keys - 1) / keys);
   p->teams = static_cast<int>(teams < tiles ? teams : tiles);
   p->ctas = p->teams * blocks;
+  // Short sequences (by the page table's columns: lengths are on the device): a cluster of CTAs for
+  // each sequence and block of rows, which join in shared memory and spare the second launch (about
+  // the time of 10 tiles), where all of them fit on the GPU at once (clusters of CTAs that fill an SM
+  // leave some SMs out) and no CTA gets more than 20 tiles, or 10 more than a team would.  Measured, clusters
+  // against teams, 32 heads over 8 of 128, BF16: 1 x 1000 tokens 6.9 against 7.2 us, 4 x 1000 8.1 against
+  // 9.9, 4 x 4000 16.4 against 19.8, 32 x 10..1000 19.3 against 22.1; 1 x 8000 14.8 against 13.6.  A call from
+  // Python, which pays for two launches, takes 11.5 us against 13.5.
+  p->cluster = 0;
+  if (!p->wide) {
+    const long long cap = (p->c.max_len + keys - 1) / keys, units = static_cast<long long>(p->c.b) * blocks;
+    const long long room = per_sm == 1 ? top * 3 / 4 : top, of_team = p->c.b * cap / (top / blocks > 0 ? top / blocks : 1);
+    int cl = 1;
+    while (cl < kMaxCluster && cl < cap && units * cl * 2 <= room) cl *= 2;
+    const long long mine = (cap + cl - 1) / cl;
+    if (units * cl <= room && mine <= 20 && mine <= of_team + 10) {
+      p->cluster = cl;
+      p->ctas = static_cast<int>(units) * cl;
+    }
+  }
 }
 
 size_t decode_workspace_bytes(const DecodeParams& p, int d, size_t* ml_offset) {
   // A single team finishes every sequence itself and leaves no parts.
-  const size_t parts = p.teams > 1 ? 2 * static_cast<size_t>(p.ctas) * p.tile_rows : 0;
+  const size_t parts = p.teams > 1 && !p.cluster ? 2 * static_cast<size_t>(p.ctas) * p.tile_rows : 0;
   if (ml_offset) *ml_offset = parts * d * 4;
   return (parts * d * 4 + parts * 8 + 256) & ~size_t(255);
 }

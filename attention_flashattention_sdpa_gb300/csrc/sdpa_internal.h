@@ -277,6 +277,7 @@ struct DecodeParams {
                                // [2 * ctas][d / 4][256][4], rows side by side)
   float* part_ml;              // workspace: [2 * ctas][tile_rows][2] their max (log2 units) and sum
   int teams, ctas;             // runs of tiles, and CTAs: one for each run, KV head and block of rows
+  int cluster;                 // not 0: short sequences, each block of rows of each by a cluster of this many CTAs
 };
 
 // Fills in the blocks of rows and the CTAs (from the sizes alone, so that workspace and launch agree).

@@ -327,6 +327,23 @@ def test_decode_peaked_scores(kind):
         assert (np.abs(f64(lse) - L) <= 2.0 ** -10 + 2.0 ** -20 * np.abs(L)).all()
 
 
+@pytest.mark.parametrize("kind,d,rows,h_kv", [("bf16", 128, 1, 2), ("e4m3", 128, 2, 3), ("f16", 64, 13, 12), ("e4m3", 64, 1, 1), ("bf16", 256, 3, 1),
+                                              ("e4m3", 256, 2, 2)])
+@pytest.mark.parametrize("lens", [(0, 1, 64, 65), (1000,), (17,), (129, 1279, 700), (40, 0, 512) + (60,) * 70])
+def test_decode_short_sequences(kind, d, rows, h_kv, lens):
+    """One CTA to eight for a sequence, some of them without a tile; a table that could hold more."""
+    dtype = "f16" if kind == "f16" else "bf16"
+    g = torch.Generator().manual_seed(31)
+    q = bshd(g, dtype, len(lens), 2 * h_kv, rows, d)
+    c = make_cache(lens, h_kv, d, 64, kind, seed=32, v_spread=1000.0 if kind == "e4m3" else 1.0)
+    kv, vv, ks, vs, table = c.np()
+    o, lse = run_decode(c, q, causal="bottom_right")
+    ref = so.attend(f64(q), kv, vv, ks, vs, table, lens, None, d ** -0.5, True)
+    assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16")
+    again, lse2 = run_decode(c, q, causal="bottom_right")
+    assert torch.equal(o, again) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
 @pytest.mark.parametrize("rows", [1, 12, 40])
 def test_decode_few_keys_lse(kind, rows):
