@@ -447,9 +447,8 @@ def _code(t, name: str) -> int:
     return _bad(f"{name}: dtype {t.dtype} is not one the library takes") if c is None else c
 
 
-def _launch(fn, stream, like, *args):
-    """Calls ``fn(*args, stream)`` with the device of ``like`` current."""
-    dev = like.get_device()
+def _launch(fn, stream, like, dev, *args):
+    """Calls ``fn(*args, stream)`` with ``dev``, the device of ``like``, current."""
     if dev == _Lazy.device():
         st = fn(*args, int(stream) if stream is not None else _stream(None, like))
     else:
@@ -460,12 +459,14 @@ def _launch(fn, stream, like, *args):
 
 
 def _same_device(like, *tensors):
+    """Index of the CUDA device that all of them (None aside) are on."""
     dev = like.get_device()
     if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors must be on one device ({like.device} and {t.device} given)")
+    return dev
 
 
 def _dense(t, name: str, dtype, shape):
@@ -514,10 +515,10 @@ def _rope(fn, q, k, q_out, k_out, table, positions, interleaved, attn_factor, st
     dt = _code(q, "q")
     tab, rot = _table(table, "table")
     pos, pos_stride = _positions(positions, b, s)
-    _same_device(q, k, q_out, k_out, table, positions)
+    dev = _same_device(q, k, q_out, k_out, table, positions)
     p = _PACK_ROPE(b, h_q, h_k, s, d, rot, dt, 1 if interleaved else 0, attn_factor, tab, pos, pos_stride, *q.stride(), *k_st,
                    *q_out.stride(), *k_out_st)
-    _launch(fn, stream, q, p, q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr)
+    _launch(fn, stream, q, dev, p, q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr)
 
 
 def sdpa_rope_fwd(q, k, q_out, k_out, table, positions=None, *, interleaved: bool = False,
@@ -550,7 +551,6 @@ def _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale):
     lens = _dense(seq_lens_kv, "seq_lens_kv", _Lazy.int32, ts[:1])
     ks = 0 if k_scale is None else _dense(k_scale, "k_scale", _Lazy.float32, shape[:3])
     vs = 0 if v_scale is None else _dense(v_scale, "v_scale", _Lazy.float32, shape[:3])
-    _same_device(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
     return _PACK_CACHE(pages, page_size, h_kv, d, _code(k_cache, "k_cache"), ts[0], ts[1], k_cache.data_ptr(), v_cache.data_ptr(),
                        *k_cache.stride(), *v_cache.stride(), ks, vs, page_table.data_ptr(), tst[0], lens), shape, ts[0]
 
@@ -561,7 +561,6 @@ def _cache_rows(k, v, k_cache, shape, n: int):
         raise ValueError("k and v must be [b, h_kv, s, d] views of one shape and dtype")
     if ks[0] != n or ks[1] != shape[1] or ks[3] != shape[3]:
         raise ValueError("k and v must have the cache's h_kv and d and a row of the page table for each sequence")
-    _same_device(k_cache, k, v)
     return ks
 
 
@@ -586,9 +585,9 @@ def sdpa_cache_write(k, v, k_cache, v_cache, page_table, seq_lens_kv, *, seq_len
         at = ctypes.addressof(rope)
     elif positions is not None:
         raise ValueError("positions are those of a rope_table")
-    _same_device(k_cache, seq_lens_q, rope_table, positions)
+    dev = _same_device(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale, k, v, seq_lens_q, rope_table, positions)
     r = _PACK_ROWS(s, _code(k, "k"), *k.stride(), *v.stride(), lens_q, at)
-    _launch(lib.sdpa_cache_write, stream, k_cache, c, r, k.data_ptr(), v.data_ptr())
+    _launch(lib.sdpa_cache_write, stream, k_cache, dev, c, r, k.data_ptr(), v.data_ptr())
 
 
 def sdpa_cache_read(k_cache, v_cache, page_table, seq_lens_kv, k, v, *, k_scale=None, v_scale=None,
@@ -597,8 +596,9 @@ def sdpa_cache_read(k_cache, v_cache, page_table, seq_lens_kv, k, v, *, k_scale=
     and behind its length are zeros.  Arguments as in :func:`sdpa_cache_write`."""
     c, shape, n = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
     ks = _cache_rows(k, v, k_cache, shape, n)
+    dev = _same_device(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale, k, v)
     r = _PACK_ROWS(ks[2], _code(k, "k"), *k.stride(), *v.stride(), 0, 0)
-    _launch(lib.sdpa_cache_read, stream, k_cache, c, r, k.data_ptr(), v.data_ptr())
+    _launch(lib.sdpa_cache_read, stream, k_cache, dev, c, r, k.data_ptr(), v.data_ptr())
 
 
 def _decode(q, k_cache, shape, n, o, seq_lens_q, attn_scale, causal, tree_mask):
@@ -617,7 +617,6 @@ def _decode(q, k_cache, shape, n, o, seq_lens_q, attn_scale, causal, tree_mask):
                 or (words > 1 and st[2] != 1) or (s_q > 1 and st[1] != words):
             raise ValueError(f"tree_mask must be int32 ({b} or 1, {s_q}, {words}), dense in its last two dimensions")
         tree, tree_stride = tree_mask.data_ptr(), st[0] if ts[0] > 1 else 0
-    _same_device(k_cache, q, o, seq_lens_q, tree_mask)
     return _PACK_DECODE(h_q, s_q, _code(q, "q"), causal_code(causal), 1.0 / math.sqrt(d) if attn_scale is None else attn_scale,
                         *q.stride(), *o.stride(), lens_q, tree, tree_stride)
 
@@ -628,7 +627,7 @@ def sdpa_decode_workspace_size(q, k_cache, v_cache, page_table, seq_lens_kv, *, 
     c, shape, n = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
     p = _decode(q, k_cache, shape, n, q, None, 1.0, False, tree_mask)
     size = ctypes.c_size_t(0)
-    with _Lazy.torch.cuda.device(q.device):
+    with _Lazy.torch.cuda.device(_same_device(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale, q, tree_mask)):
         _check(lib.sdpa_decode_workspace_size(c, p, ctypes.byref(size)))
     return size.value
 
@@ -648,6 +647,6 @@ def sdpa_decode(q, k_cache, v_cache, page_table, seq_lens_kv, o, lse=None, *, wo
     lse_ptr = None if lse is None else _dense(lse, "lse", _Lazy.float32, q.shape[:3])
     if workspace is None or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor")
-    _same_device(k_cache, lse, workspace)
-    _launch(lib.sdpa_decode, stream, k_cache, c, p, q.data_ptr(), o.data_ptr(), lse_ptr, workspace.data_ptr(),
+    dev = _same_device(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale, q, o, seq_lens_q, tree_mask, lse, workspace)
+    _launch(lib.sdpa_decode, stream, k_cache, dev, c, p, q.data_ptr(), o.data_ptr(), lse_ptr, workspace.data_ptr(),
             workspace.numel() * workspace.element_size())

@@ -65,7 +65,7 @@ struct DecCfg {
   static constexpr int STAGE = 2 * kSlice * RB + SC_BYTES;
   static constexpr int MERGE = kWarps * ROWS * D * 4;   // the warps' partial O at the end of a run
   static constexpr int CTAS = RB > 256 ? 1 : (D * NR > 256 || RB > 128 ? 2 : 3);   // of an SM
-  static constexpr int NS_FIT = (232448 / CTAS - 3072) / (kWarps * STAGE);
+  static constexpr int NS_FIT = (232448 / CTAS - 3 * 1024) / (kWarps * STAGE);
   static constexpr int NS = NS_FIT > 6 ? 6 : NS_FIT;
   static constexpr int RING = kWarps * NS * STAGE;
   static constexpr int SMEM = RING > MERGE ? RING : MERGE;
