@@ -137,6 +137,7 @@ def _packer(cls=Problem):
 _PACK = _packer()
 _PACK_ROPE, _PACK_CACHE, _PACK_ROWS, _PACK_DECODE = (_packer(c).pack for c in (Rope, Cache, CacheRows, Decode))
 _NO_STRIDES = (0, 0, 0, 1)
+_NO_ROPE_STRIDES = 4 * _NO_STRIDES
 
 
 def causal_code(causal) -> int:
@@ -580,8 +581,8 @@ def sdpa_cache_write(k, v, k_cache, v_cache, page_table, seq_lens_kv, *, seq_len
     if rope_table is not None:
         tab, rot = _table(rope_table, "rope_table")
         pos, pos_stride = _positions(positions, b, s)
-        rope = ctypes.create_string_buffer(_PACK_ROPE(0, 0, 0, 0, 0, rot, 0, 1 if interleaved else 0, attn_factor, tab, pos,
-                                                      pos_stride, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES))
+        rope = Rope.from_buffer_copy(_PACK_ROPE(0, 0, 0, 0, 0, rot, 0, 1 if interleaved else 0, attn_factor, tab, pos, pos_stride,
+                                                *_NO_ROPE_STRIDES))
         at = ctypes.addressof(rope)
     elif positions is not None:
         raise ValueError("positions are those of a rope_table")
