@@ -8,7 +8,7 @@
 // the row's largest value by shuffles; a thread walks heads of one token, so that its angles and
 // its page are looked up once.  Measured, 8 heads of 128, E4M3 from or to BF16: 4 prompts of 5001 to
 // 8192 tokens written, K rotated, 36.5 us (4.9 TB/s, 73% of a copy: the roundings of a row wait for
-// its largest value), 32 single tokens 3.0 us; 2 x 8192 tokens read 18.1 us (5.5 TB/s, 81%).
+// its largest value), 32 single tokens 3.0 us; 2 x 8192 tokens read 17.5 us (5.6 TB/s, 83%).
 #include <cuda_fp8.h>
 
 #include <type_traits>
@@ -229,9 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_c
 }
 
 // One thread: 16 elements of K and of V of one row, eight of each half of it, so that neighbouring
-// lanes write neighbouring 16 bytes.  (Two or four heads a thread, their loads in flight together, were
-// slower: 21.7 and 22.6 us against 19.5 for 2 x 8192 tokens of 8 heads; 16 neighbouring elements 19.2 against
-// 18.1.)
+// lanes write neighbouring 16 bytes (16 neighbouring elements: 19.2 us against 17.5 for 2 x 8192 tokens of
+// 8 heads).  Two or four heads a thread, their loads in flight together, are no faster: 17.8 and 17.5 us.
 template <int D, int DT, int CT>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheRowsParams p, bool small) {
   constexpr int LANES = D / 16, ES = CT == kE4M3 ? 1 : 2;
@@ -268,8 +267,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(iw[e / 2] >> (16 * (e % 2))), __NV_E4M3);
-          const float2 f = __half22float2(__half2(hr));
-          ow[e] = pack16<DT>(f.x * scale[t], f.y * scale[t]);
+          const float2 f = ptx::mul2(__half22float2(__half2(hr)), make_float2(scale[t], scale[t]));
+          ow[e] = pack16<DT>(f.x, f.y);
         }
         out = make_uint4(ow[0], ow[1], ow[2], ow[3]);
       } else {
