@@ -547,3 +547,38 @@ def test_results_do_not_change_from_call_to_call():
     for _ in range(3):
         again = run_decode(c, q, causal="bottom_right")
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("kind,h_q,s,columns", [("bf16", 8, 1, 16), ("e4m3", 8, 1, 400), ("bf16", 8, 12, 60), ("e4m3", 8, 40, 60)])
+def test_calls_at_once_and_captured_lengths(kind, h_q, s, columns):
+    """Two streams at once give what they give one after the other; one captured call serves every length."""
+    m, g = lib(), torch.Generator().manual_seed(41)
+    page = 16
+    lens = (columns * page, 37)
+    c = make_cache(lens, 2, 128, page, kind, seed=42, wide=columns)
+    qs = [bshd(g, "bf16", 2, h_q, s, 128) for _ in range(2)]
+    alone = [run_decode(c, q, causal="bottom_right") for q in qs]
+    n = m.sdpa_decode_workspace_size(qs[0], *c.where(), **c.scales())
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in qs]
+    outs = [(torch.empty_like(q), torch.empty(2, h_q, s, device="cuda")) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for st, q, w, (o, lse) in zip(streams, qs, ws, outs):
+            with torch.cuda.stream(st):
+                m.sdpa_decode(q, *c.where(), o, lse, workspace=w, causal="bottom_right", **c.scales())
+    torch.cuda.synchronize()
+    for (o, lse), (o1, lse1) in zip(outs, alone):
+        assert torch.equal(o, o1) and torch.equal(lse, lse1)
+    graph, (o, lse) = torch.cuda.CUDAGraph(), outs[0]
+    with torch.cuda.graph(graph):
+        m.sdpa_decode(qs[0], *c.where(), o, lse, workspace=ws[0], causal="bottom_right", **c.scales())
+    for now in ((1, 1), (0, 20), (columns * page // 2 + 3, 37), (columns * page, 0)):
+        c.lens.copy_(torch.tensor(now, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = o.clone(), lse.clone()
+        want = run_decode(c, qs[0], causal="bottom_right")
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        if now[1] == 0:
+            assert not got[0][1].any() and torch.isneginf(got[1][1]).all()
