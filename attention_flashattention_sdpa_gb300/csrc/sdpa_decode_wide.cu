@@ -21,7 +21,9 @@
 // multiply each of its columns by the key's scale in fp32.  V's codes are multiplied by scale / 2^E (2^E:
 // about 1/64 of the tile's largest scale) as a sum of two F16 factors, so one rounding to F16's 11
 // bits is left, as P's (of rows 2^-28 as large as others of their tile, to fewer: F16 ends there);
-// 2^E joins the exponent of the weights once a tile.
+// 2^E joins the exponent of the weights once a tile.  Where the results are F16, whose own rounding does not
+// cover that one, V's codes take only the scale's first 7 bits, which F16 holds exactly, and the weights the
+// rest of it (FOLD).
 // (K times its scale in F16 too left the scores off by 2^-12 of themselves, which the LSE shows.)
 //
 // Bound: the tensor cores (4 x 128 x 128 x d MMAs a block of two tiles) and the exponentials, as
@@ -76,6 +78,7 @@ struct alignas(8) WideBarriers {
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t ml_full, o1_free;                // split: the second warpgroup's maxima and sums are there; its O is read
   uint64_t sc_full[4];                      // E4M3: a tile's K scales and the exponent of its V scales are there
+  uint64_t sc_read[2];                      // FOLD: the widening warps have read a stage's V scales
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -161,6 +164,8 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
   using C = WideCfg<D, CT>;
   constexpr bool E4 = C::E4;
   constexpr bool BF = CT == kBF16;     // type of the 16-bit operands
+  // F16 results of an E4M3 cache: V without a rounding of its own, what its scale has beyond 7 bits in P.
+  constexpr bool FOLD = E4 && QT == kF16;
   // Slot or stage of tile n of K or V, and the turn it is in there.
   struct Place {
     int at, turn;
@@ -218,7 +223,8 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
       mbar_init(&bars.raw_full[i], 1);
       mbar_init(&bars.raw_empty[i], 128);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&bars.sc_full[i], 4 + 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars.sc_full[i], 4 + (FOLD ? 4 : 1));
+    for (int i = 0; i < 2; ++i) mbar_init(&bars.sc_read[i], 4);
     mbar_init(&bars.ml_full, 128);
     mbar_init(&bars.o1_free, 128);
     mbar_init(&bars.drain, 1);
@@ -288,6 +294,11 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           const Place at = E4 ? stage_of(is_v, issued) : slot_of(is_v, issued);
           const int s = at.at;
           if (!mbar_wait_warp(E4 ? &bars.raw_empty[s] : &bars.empty[s], (at.turn & 1) ^ 1, wt)) { ok = false; break; }
+          if (FOLD && is_v && issued >= C::RV) {
+            // The stage's scales, now the factors on P, are read until P V of their tile.
+            const Place x = slot_of(true, issued - C::RV);
+            if (!mbar_wait_warp(&bars.empty[x.at], x.turn & 1, wt)) { ok = false; break; }
+          }
           uint64_t* full = E4 ? &bars.raw_full[s] : &bars.full[s];
           uint8_t* dst = E4 ? sRaw + s * C::RAW : sRing + s * C::TILE;
           const bool scales = E4 && is_v;
@@ -458,17 +469,30 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           if (!ok) break;
           __half2 h2 = __float2half2_rn(0.f), l2 = h2;
           if (is_v) {
-            const float* sc = sSc + (rs - C::RK) * 128;
+            float* sc = sSc + (rs - C::RK) * 128;
             const int ex = largest_exponent(sc, left, lane);      // (by every lane)
-            if (warp % 4 == 0 && lane == 0) {
-              s_ev[n_tile % 8] = ex;
-              mbar_arrive(&bars.sc_full[n_tile % 4]);
-            }
-            // scale / 2^E of the lane's row as two F16, each twice in a word
             const float f = on ? sc[r] * pow2(-ex) : 0.f;
-            const __half fh = __float2half_rn(f), fl = __float2half_rn(f - __half2float(fh));
-            h2 = __half2half2(fh);
-            l2 = __half2half2(fl);
+            if (warp % 4 == 0 && lane == 0) s_ev[n_tile % 8] = ex;
+            if constexpr (FOLD) {
+              // Seven bits of scale / 2^E, whose product with a code F16 holds exactly; the rest (a factor
+              // of 1 to 1 + 2^-6) takes the scale's place for the softmax warps once all have read it.
+              const __half fh = __float2half_rz(__uint_as_float(__float_as_uint(f) & 0xFFFE0000u));
+              const float ff = __half2float(fh);
+              h2 = __half2half2(fh);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars.sc_read[n_tile % 2]);
+              ok = mbar_wait_warp(&bars.sc_read[n_tile % 2], (n_tile / 2) & 1, wt);
+              if (!ok) break;
+              sc[r] = ff > 0.f && f < INFINITY ? __fdividef(f, ff) : 1.f;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars.sc_full[n_tile % 4]);
+            } else {
+              if (warp % 4 == 0 && lane == 0) mbar_arrive(&bars.sc_full[n_tile % 4]);
+              // scale / 2^E of the lane's row as two F16, each twice in a word
+              const __half fh = __float2half_rn(f), fl = __float2half_rn(f - __half2float(fh));
+              h2 = __half2half2(fh);
+              l2 = __half2half2(fl);
+            }
           }
           ok = mbar_wait_warp(&bars.empty[s], (to.turn & 1) ^ 1, wt);
           if (!ok) break;
@@ -494,7 +518,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
                 out[e] = e4m3x2_to_f16x2(e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
                 if constexpr (decltype(scale)::value) {
                   const __half2 v = *reinterpret_cast<const __half2*>(&out[e]);
-                  const __half2 y = __hfma2(v, h2, __hmul2(v, l2));
+                  const __half2 y = FOLD ? __hmul2(v, h2) : __hfma2(v, h2, __hmul2(v, l2));
                   out[e] = *reinterpret_cast<const uint32_t*>(&y);
                 }
                 if constexpr (decltype(clear)::value) out[e] = on ? finite_pair<false>(out[e], found) : 0u;
@@ -654,7 +678,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         const int key0 = (sg.tile0 + i) * kKeys;
         // E4M3: the exponent of the tile's V, in the weights' exponent and out of l again; K's scales.
         float ev = 0.f, back = 1.f;
-        const float* ks = nullptr;
+        const float *ks = nullptr, *vr = nullptr;
         if constexpr (E4) {
           const int tile = n_tile + i;
           if (!mbar_wait_warp(&bars.sc_full[tile % 4], (tile / 4) & 1, wt)) { ok = false; break; }
@@ -662,6 +686,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           ev = static_cast<float>(e);
           back = pow2(-e);
           ks = sKs + tile % C::KS * 128;
+          vr = sSc + tile % C::RV * 128;
         }
         const bool need = key0 + kKeys > sg.L.len_kv || (masked && key0 + kKeys > sg.off) || bad;
         uint32_t vis[4];       // visible columns
@@ -768,9 +793,14 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           for (int c = 0; c < 64; c += 4) {
             const float2 x01 = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), cs2, nm2);
             const float2 x23 = fma2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), cs2, nm2);
-            const float2 p01 = make_float2(ex2(x01.x), ex2(x01.y)), p23 = make_float2(ex2(x23.x), ex2(x23.y));
+            float2 p01 = make_float2(ex2(x01.x), ex2(x01.y)), p23 = make_float2(ex2(x23.x), ex2(x23.y));
             acc0 = add2(acc0, p01);
             acc1 = add2(acc1, p23);
+            if constexpr (FOLD) {
+              const float4 f = *reinterpret_cast<const float4*>(vr + h * 64 + c);
+              p01 = mul2(p01, make_float2(f.x, f.y));
+              p23 = mul2(p23, make_float2(f.z, f.w));
+            }
             pk[c / 2] = pack_pair<BF>(p01.x, p01.y);
             pk[c / 2 + 1] = pack_pair<BF>(p23.x, p23.y);
           }

@@ -107,9 +107,10 @@ def pack_tree(see: np.ndarray) -> torch.Tensor:
     return torch.from_numpy(w.view(np.int32))
 
 
-def kv_rounding(kind, rows, d):
-    """Relative rounding of an E4M3 cache's values in the products of `rows` query rows a KV head."""
-    return 2.0 ** -11 if kind == "e4m3" and rows > 32 and d <= 128 else 0.0
+def kv_rounding(kind, rows, d, dtype):
+    """Relative rounding of an E4M3 cache's values in the products of `rows` query rows a KV head (results in
+    FP16: none, the weights carry what F16 has no room for)."""
+    return 2.0 ** -11 if kind == "e4m3" and rows > 32 and d <= 128 and dtype == "bf16" else 0.0
 
 
 def run_decode(cache: PagedCache, q, *, lens_q=None, causal=False, tree=None, scale=None, with_lse=True, stream=None):

@@ -244,6 +244,9 @@ ATTEND = [
     ((257, 64, 33), (9, 0, 33), 33, 8, 1, 64, 64, "e4m3", "bf16", "tree", False),
     ((1025, 40), None, 17, 1, 1, 64, 80, "bf16", "bf16", None, True),
     ((384,), None, 3, 48, 2, 128, 128, "e4m3", "f16", None, True),
+    ((1500, 700, 0, 300), (70, 9, 70, 70), 70, 8, 2, 128, 64, "e4m3", "f16", "tree", True),
+    ((1030, 77), None, 12, 12, 1, 64, 16, "e4m3", "f16", "causal", False),
+    ((900, 500), None, 10, 8, 1, 128, 16, "e4m3", "f16", "tree", True),
     ((700, 690), None, 257, 1, 1, 128, 32, "bf16", "bf16", "causal", True),
 ]
 
@@ -257,7 +260,7 @@ def test_decode(lens, lens_q, s, h_q, h_kv, d, page, kind, dtype, mask, slot_maj
     o, lse = run_decode(c, q, lens_q=lens_q, causal="bottom_right" if mask == "causal" else False, tree=tree)
     kv, vv, ks, vs, table = c.np()
     ref = so.attend(f64(q), kv, vv, ks, vs, table, lens, lens_q, d ** -0.5, mask == "causal", tree)
-    assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q // h_kv, d))
+    assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q // h_kv, d, dtype))
 
 
 @pytest.mark.parametrize("kind,d,h_q,s", [("bf16", 128, 8, 1), ("e4m3", 128, 8, 1), ("f16", 64, 4, 3), ("e4m3", 256, 2, 2),
@@ -272,22 +275,23 @@ def test_decode_long_ragged(kind, d, h_q, s):
     o, lse = run_decode(c, q, causal="bottom_right" if s > 1 else False)
     kv, vv, ks, vs, table = c.np()
     ref = so.attend(f64(q), kv, vv, ks, vs, table, lens, None, d ** -0.5, s > 1)
-    assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q, d))
+    assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q, d, dtype))
 
 
-@pytest.mark.parametrize("kind,s,h_q", [("bf16", 1, 8), ("bf16", 17, 8), ("e4m3", 17, 8), ("e4m3", 3, 64)])
-def test_decode_many_tiles_a_cta(kind, s, h_q):
+@pytest.mark.parametrize("kind,s,h_q,dtype", [("bf16", 1, 8, "bf16"), ("bf16", 17, 8, "bf16"), ("e4m3", 17, 8, "bf16"), ("e4m3", 3, 64, "bf16"),
+                                              ("e4m3", 5, 64, "bf16"), ("e4m3", 5, 64, "f16"), ("e4m3", 17, 64, "f16")])
+def test_decode_many_tiles_a_cta(kind, s, h_q, dtype):
     """Runs of many tiles, so that every ring wraps often; what lies behind each sequence is NaN."""
     g, d, h_kv = torch.Generator().manual_seed(31), 128, 8
     lens = tuple(2500 + 61 * i for i in range(12))
     c = make_cache(lens, h_kv, d, 48, kind, seed=32)
-    q = bshd(g, "bf16", len(lens), h_q, s, d)
+    q = bshd(g, dtype, len(lens), h_q, s, d)
     o, lse = run_decode(c, q, causal="bottom_right")
     again, _ = run_decode(c, q, causal="bottom_right")
     assert torch.equal(o, again)
     kv, vv, ks, vs, table = c.np()
     ref = so.attend(f64(q), kv, vv, ks, vs, table, lens, None, d ** -0.5, True)
-    assert_attend_close(o, lse, ref, "bf16", "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q // h_kv, d))
+    assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q // h_kv, d, dtype))
 
 
 @pytest.mark.parametrize("kind,d,s,h_q,h_kv", [("bf16", 128, 1, 2, 1), ("e4m3", 128, 18, 1, 1), ("bf16", 64, 20, 2, 1), ("f16", 128, 150, 1, 1),
@@ -304,7 +308,7 @@ def test_decode_many_short_sequences(kind, d, s, h_q, h_kv):
     rows = [i for i in range(b) if b <= 60 or i % 9 == 0]
     kv, vv, ks, vs, table = c.np()
     ref = so.attend(f64(q)[rows], kv, vv, ks, vs, table[rows], [lens[i] for i in rows], None, d ** -0.5, True)
-    assert_attend_close(o[rows], lse[rows], ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q // h_kv, d))
+    assert_attend_close(o[rows], lse[rows], ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q // h_kv, d, dtype))
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
@@ -322,7 +326,7 @@ def test_decode_peaked_scores(kind):
         ref = so.attend(f64(q), kv, vv, ks, vs, table, (3001,), None, scale)
         # scores up to 2^6 now: their errors grow with the scale (eight times the default's bound)
         O, L, spread = ref[:3]
-        tol = (HALF_STEP["bf16" if kind == "bf16" else "f16"] + 2.0 ** -10 + kv_rounding(kind, 4 * rows, 128)) * spread + HALF_STEP[dtype] * np.abs(O) * 1.01 + TINY[dtype]
+        tol = (HALF_STEP["bf16" if kind == "bf16" else "f16"] + 2.0 ** -10 + kv_rounding(kind, 4 * rows, 128, dtype)) * spread + HALF_STEP[dtype] * np.abs(O) * 1.01 + TINY[dtype]
         assert (np.abs(f64(o) - O) <= tol).all()
         assert (np.abs(f64(lse) - L) <= 2.0 ** -10 + 2.0 ** -20 * np.abs(L)).all()
 
@@ -406,7 +410,7 @@ def test_decode_zero_scales(rows):
     kv, vv, ks, vs, table = c.np()
     o, lse = run_decode(c, q)
     ref = so.attend(f64(q), kv, vv, ks, vs, table, (300, 40), None, 128 ** -0.5)
-    assert_attend_close(o, lse, ref, "bf16", "f16", kv_rounding=kv_rounding("e4m3", rows * 2, 128))
+    assert_attend_close(o, lse, ref, "bf16", "f16", kv_rounding=kv_rounding("e4m3", rows * 2, 128, "bf16"))
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])

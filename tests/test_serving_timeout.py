@@ -36,7 +36,7 @@ for kind, dtype in (("bf16", "bf16"), ("e4m3", "bf16")):
     call()
     kv, vv, ks, vs, table = c.np()
     ref = so.attend(f64(q), kv, vv, ks, vs, table, (700, 300), None, 128 ** -0.5, True)
-    assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, 40, 128))
+    assert_attend_close(o, lse, ref, dtype, "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, 40, 128, dtype))
 print("WAIT_TIMEOUT_OK")
 '''
 
