@@ -5,14 +5,15 @@
 // one persistent CTA an SM walks a run of tiles for its KV head and block of rows, segment by segment
 // (a segment: the part of the run in one sequence).  Roles:
 //   warps 0, 2   pages and TMA of K and of V, box by box (a box lies in one page), a lane a box; boxes
-//                of missing pages and behind the sequence are filled with zeros.  E4M3: the scales
+//                of missing pages and behind the sequence are filled with zeros.  E4M3: V's scales
 //                follow by bulk copies.  (One thread for all of them took 4200 cycles a tile.)
 //   warp 1       MMA issuer: S = Q K^T into TMEM, O += P V with P read from TMEM.
 //   warps 4-11   two softmax warpgroups; thread r owns a row: loads it into shared memory, the
 //                running max and sum, P, and the segment's results.  A block of more than 128 rows
 //                has a 128-row tile for each; in a smaller one both take the same rows and every
 //                second tile of keys, so that one computes while the other's products run.
-//   warps 12-15  E4M3: widen K to F16 on its way from the TMA's stage to the ring (and warps 16-19 V);
+//   warps 12-15  E4M3: widen K to F16 on its way from the TMA's stage to the ring (and warps 16-19 V), and
+//                fetch K's scales;
 //                16-bit: clear, in V tiles that end behind the sequence or hold drafted tokens, rows
 //                that do not exist and values that are not finite (a weight of zero does not hide a
 //                NaN in a product).
@@ -28,7 +29,7 @@
 //
 // Bound: the tensor cores (4 x 128 x 128 x d MMAs a block of two tiles) and the exponentials, as
 // the prompt's forward pass; reading the cache once bounds it for few rows.  Measured, 8 sequences of 4000
-// to 8192 tokens, trees of 64 tokens, 64 heads over 8 of 128: BF16 105 us (990 TFLOP/s), E4M3 153 (675; 2.5
+// to 8192 tokens, trees of 64 tokens, 64 heads over 8 of 128: BF16 105 us (990 TFLOP/s), E4M3 154 (670; F16 results 160; 2.5
 // us for 128 keys by 256 rows against 1.75: the warps that widen and the scales of K share the
 // schedulers and the shared memory with the softmax, and K has one slot where BF16 has two).  35 to
 // 45 us of either are the first fetch of the code, Q, the last results and the parts.
