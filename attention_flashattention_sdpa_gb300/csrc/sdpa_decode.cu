@@ -28,8 +28,12 @@
 // of up to 8 heads: 209 us against 92 us of reading at 32 sequences of 1K..16K tokens.)
 //
 // E4M3 caches: codes widen exactly to F16; a key's scale multiplies its score, and the scale of
-// its value joins the exponent, w = 2^(s + log2 vs - max), so that O = sum w v_code and
-// l = sum w / vs.  The row max then bounds w whatever the scales, and no product with vs is rounded.
+// its value, over 2^v, its weight: w = 2^(s - m) vs / 2^v, O = 2^v sum w v_code / l, l = sum 2^(s - m).  2^v is a running
+// maximum as m is one, above the scales that a row sees, so that F16 holds w whatever the scales; l, and LSE,
+// depend on Q and K alone.  (log2 vs in the exponent and l = sum w / vs saves a multiplication a score, but is infinite
+// for a subnormal vs, and loses ordinary keys beside a vs 2^110 times as large.)  F16's least step is 2^-30 of the
+// largest w that these bounds allow, so beside its half step of its own a key's part of O is off by at most
+// 2^-31 448 2^v times the row's largest weight: far below E4M3's own rounding of the row with that scale.
 //
 // Measured, groups of 8 heads, d = 128: 32 sequences of 1000 to 16384 tokens, E4M3, 110 us (5.65 TB/s, 83%
 // of a copy; BF16 131000 tokens of one sequence 86 us, 6.25 TB/s, 92%); 1000 tokens of one sequence 6.9 us, of
@@ -73,6 +77,12 @@ struct DecCfg {
   static constexpr float THRESH = 8.f;                  // the running max moves when exceeded by this much
   static_assert(NS >= 2 && NS * 5 <= 32, "ring");
 };
+
+// Bounds of v: 2^-v and 2^v are both fp32 values, and w stays below 2^15 (scales reach 2^128).  Up to +-kNearV,
+// far wider than rows of 16-bit elements ever need, v joins the exponents of a row's weights and of its sum, so
+// that a weight costs one multiplication by vs; what v is beyond that takes another one (`wild`).
+constexpr int kMinV = -125, kMaxV = 127, kNearV = 60;
+__device__ __forceinline__ int near_v(int v) { return min(max(v, -kNearV), kNearV); }
 
 // Position of 16-byte chunk `ch` of row `r` in a stage: neighbouring rows differ in bit 2 (the
 // key reads of a quarter-warp are two rows of four chunks), rows 2c in bits 1-2 (the value
@@ -126,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
   constexpr int ROWS = C::ROWS, NT = C::NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
+  __shared__ int s_v[E4 ? kWarps : 1][ROWS];     // E4M3: v of each row
   __shared__ int s_found;
   __shared__ float2 s_part[ROWS];   // clusters: this CTA's maximum and sum of each row
 
@@ -268,12 +279,22 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
 
     float o[NR][NT][4];
     float m_ref[NR][2], l[NR][2];
+    float v_min = 0.f;         // E4M3: 2^v of the warp's row with the least
+    bool wild = E4;            // E4M3: v of some row is beyond +-kNearV
+    float nm[NR][2];           // what a row's scores take to the exponent of their weights
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
       m_ref[n][0] = m_ref[n][1] = -INFINITY;
+      nm[n][0] = nm[n][1] = E4 ? kNearV : 0.f;
       l[n][0] = l[n][1] = 0.f;
+    }
+    // E4M3: v of row 2c + u of block n (written by every lane that holds the row; seldom read or written).
+    int* const v_row = s_v[E4 ? warp : 0] + 2 * c;
+    if constexpr (E4) {
+      for (int r = lane; r < ROWS; r += 32) s_v[warp][r] = kMinV;
+      __syncwarp();
     }
     bool found = false;
     if (threadIdx.x == 0) s_found = 0;
@@ -324,22 +345,17 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
       }
 
       // ---- scale (log2 units), mask ----------------------------------------------------------------
-      float rvs[2] = {1.f, 1.f};   // 1 / scale of this lane's keys' values (E4M3)
+      float vs[2];               // E4M3: scales of this lane's keys' values
       if constexpr (E4) {
         const float* sc = reinterpret_cast<const float*>(st + 2 * kSlice * C::RB);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          // A scale of zero (codes of a row of zeros) counts as 2^-69, the least that sdpa_cache_write
-          // gives; one of NaN reaches l by the weights alone, so that hidden keys leave it as it is.
           const float ks = sc[g + 8 * u];
-          float vs = g + 8 * u < valid ? sc[kSlice + g + 8 * u] : 1.f;
-          vs = vs == 0.f ? 0x1p-69f : vs;
-          const float lv = __log2f(vs);
-          rvs[u] = vs != vs ? 0.f : __fdividef(1.f, vs);
+          vs[u] = sc[kSlice + g + 8 * u];
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
-            s[n][2 * u] = fmaf(s[n][2 * u], cs[n][0] * ks, lv);
-            s[n][2 * u + 1] = fmaf(s[n][2 * u + 1], cs[n][1] * ks, lv);
+            s[n][2 * u] *= cs[n][0] * ks;
+            s[n][2 * u + 1] *= cs[n][1] * ks;
           }
         }
       } else {
@@ -348,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][e] *= cs[n][e % 2];
       }
+      uint32_t hidden = 0;        // bit 4 n + e
       if (valid < kSlice || tail) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -356,7 +373,10 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
             const int kk = g + 8 * (e / 2), r = r0 + n * 8 + 2 * c + e % 2, token = r / p.group;
             bool see = kk < valid;
             if (see && tail && r < p.rows && token < L.len_q) see = row_sees(p, bi, L, token, key0 + kk);
-            if (!see) s[n][e] = -INFINITY;
+            if (!see) {
+              s[n][e] = -INFINITY;
+              hidden |= 1u << (4 * n + e);
+            }
           }
       }
 
@@ -366,7 +386,9 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) over |= s[n][e] > m_ref[n][e % 2] + C::THRESH;
-      if (__any_sync(0xffffffffu, over)) {
+      if constexpr (E4) over |= vs[0] > v_min || vs[1] > v_min;
+      const bool move = __any_sync(0xffffffffu, over);
+      if (move) {
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
           float alpha[2];
@@ -380,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
             if (mx > m_ref[n][u] + C::THRESH) {
               alpha[u] = ex2(m_ref[n][u] - mx);
               m_ref[n][u] = mx;
+              nm[n][u] = C::P_OFF - mx - (E4 ? near_v(v_row[n * 8 + u]) : 0);
             }
             l[n][u] *= alpha[u];
           }
@@ -389,20 +412,81 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
             for (int e = 0; e < 4; ++e) o[n][x][e] *= alpha[e % 2];
         }
       }
+      // ---- 2^v: moved to two to four times the largest finite scale that a row sees when that exceeds it (an
+      // infinite scale or a NaN spoils O as it is) ---------------------------------------------------------
+      if constexpr (E4) {
+        if (move && __any_sync(0xffffffffu, vs[0] > v_min || vs[1] > v_min)) {
+          uint32_t top[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) top[k] = vs[k] < INFINITY ? __float_as_uint(fabsf(vs[k])) : 0u;
+          const uint32_t of_all = __reduce_max_sync(0xffffffffu, max(top[0], top[1]));
+          const bool same = __all_sync(0xffffffffu, hidden == 0);       // every row sees every key
+          int least = kMaxV, most = kMinV;
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            float alpha[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t t = of_all;
+              if (!same) {
+                t = max((hidden >> (4 * n + u)) & 1u ? 0u : top[0], (hidden >> (4 * n + u + 2)) & 1u ? 0u : top[1]);
+                t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                t = max(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                t = max(t, __shfl_xor_sync(0xffffffffu, t, 16));
+              }
+              const int before = v_row[n * 8 + u], need = static_cast<int>(t >> 23) - 126;
+              const int now = before >= need ? before : min(need + 1, kMaxV), step = near_v(before) - near_v(now);
+              alpha[u] = pow2(max(before - now, -126));
+              l[n][u] *= pow2(step);
+              nm[n][u] += static_cast<float>(step);
+              __syncwarp();
+              v_row[n * 8 + u] = now;
+              least = min(least, now);
+              most = max(most, now);
+            }
+            if (i > 0) {
+#pragma unroll
+              for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][x][e] *= alpha[e % 2];
+            }
+          }
+#pragma unroll
+          for (int x = 1; x < 4; x *= 2) {
+            least = min(least, __shfl_xor_sync(0xffffffffu, least, x));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
+          }
+          __syncwarp();
+          v_min = pow2(least);
+          wild = least < -kNearV || most > kNearV;
+        }
+      }
       // ---- weights, sums, P^T ------------------------------------------------------------------------
       uint32_t pb[NR][2];
 #pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        const float nm0 = m_ref[n][0] == -INFINITY ? 0.f : C::P_OFF - m_ref[n][0];
-        const float nm1 = m_ref[n][1] == -INFINITY ? 0.f : C::P_OFF - m_ref[n][1];
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float w0 = ex2(s[n][2 * u] + nm0), w1 = ex2(s[n][2 * u + 1] + nm1);
-          l[n][0] = fmaf(w0, rvs[u], l[n][0]);
-          l[n][1] = fmaf(w1, rvs[u], l[n][1]);
-          pb[n][u] = transpose8x8(pack_pair<BF>(w0, w1));
+        for (int e = 0; e < 4; ++e) {
+          s[n][e] = ex2(s[n][e] + nm[n][e % 2]);
+          l[n][e % 2] += s[n][e];
+          if constexpr (E4) s[n][e] *= vs[e / 2];
+        }
+      if constexpr (E4) {
+        if (wild || hidden) {
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int v = v_row[n * 8 + e % 2];
+              s[n][e] *= pow2(near_v(v) - v);
+              if ((hidden >> (4 * n + e)) & 1u) s[n][e] = 0.f;     // whatever the scale of a hidden key
+            }
         }
       }
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) pb[n][u] = transpose8x8(pack_pair<BF>(s[n][2 * u], s[n][2 * u + 1]));
 
       // ---- O^T += V^T P^T; lane's part of a value: d = (8 j + g) * EPV + 0 .. EPV - 1 --------------------
       auto product = [&](auto clear) {
@@ -455,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
     for (int n = 0; n < NR; ++n)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+        if constexpr (E4) l[n][u] *= pow2(near_v(v_row[n * 8 + u]));
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) l[n][u] += __shfl_xor_sync(0xffffffffu, l[n][u], x);
         if (g == 0) {
@@ -474,7 +559,12 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
         for (int w = 1; w < kWarps; ++w) big = fmaxf(big, s_m[w][r]);
         // A warp that saw no key (sum 0) adds nothing; a sum of NaN with no maximum stays NaN.
         const bool none = m_ref[n][u] == -INFINITY;
-        const float f = none ? 1.f : ex2(m_ref[n][u] - big);
+        float f = none ? 1.f : ex2(m_ref[n][u] - big);
+        if constexpr (E4) {
+          int v = s_v[0][r];
+          for (int w = 1; w < kWarps; ++w) v = max(v, s_v[w][r]);
+          f *= pow2(max(s_v[warp][r] - v, -126));
+        }
         float* row = merge + (warp * ROWS + r) * D + g * C::EPV;
 #pragma unroll
         for (int j = 0; j < C::VJ; ++j)
@@ -510,6 +600,20 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
         x.y = add_nonfinite<D, CT>(p, bi, hk, L, row, d + 1, k0, k1, x.y);
         x.z = add_nonfinite<D, CT>(p, bi, hk, L, row, d + 2, k0, k1, x.z);
         x.w = add_nonfinite<D, CT>(p, bi, hk, L, row, d + 3, k0, k1, x.w);
+      }
+      if constexpr (E4) {
+        // 2^v joins.  Where O would pass fp32's range with it, O and the sum are brought down and the
+        // reference up, to a sum of 2^-12: sums over the parts then stay in range where the values do.
+        int v = s_v[0][r];
+        for (int w = 1; w < kWarps; ++w) v = max(v, s_v[w][r]);
+        float up = pow2(v);
+        if (v > kNearV && lb > 0.f && lb < INFINITY) {
+          const int e = static_cast<int>(__float_as_uint(lb) >> 23) - 127 + 12;
+          up *= pow2(-e);
+          lb *= pow2(-e);
+          mb += static_cast<float>(e);
+        }
+        x = make_float4(x.x * up, x.y * up, x.z * up, x.w * up);
       }
       if (cl) {      // over the first warp's part, which no other thread reads here
         *reinterpret_cast<float4*>(merge + r * D + d) = x;

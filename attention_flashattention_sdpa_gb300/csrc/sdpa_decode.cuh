@@ -35,6 +35,9 @@ __device__ __forceinline__ float2 unpack_pair(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// 2^e, e in -126 .. 127.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
 // Clears the halves of a 16-bit pair that are infinite or NaN; `found` gathers whether any was.
 template <bool BF>
 __device__ __forceinline__ uint32_t finite_pair(uint32_t w, bool& found) {

@@ -131,7 +131,6 @@ __device__ __forceinline__ bool needs_cleaning(const DecodeParams& p, const Segm
 
 // Exponent e of a positive fp32 given as bits (2^e <= x < 2^(e+1)), kept where 2^e and 2^-e are normal.
 __device__ __forceinline__ int exponent_of(uint32_t bits) { return min(max(static_cast<int>(bits >> 23) - 127, -100), 100); }
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // Exponent, less 6, of the largest finite scale of a tile's existing keys (`left` of 128), by a whole
 // warp: scales over 2^it are below 128, times codes of up to 448 below F16's 65504.

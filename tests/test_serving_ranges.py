@@ -1,0 +1,134 @@
+"""Attention over an E4M3 cache at the ends of the range of its scales (GPU)."""
+import numpy as np
+import pytest
+import torch
+
+from sdpa_testlib import f64
+from serving_testlib import DT, HALF_STEP, TINY, kv_rounding, make_cache, randn, run_decode, values_of
+
+pytestmark = pytest.mark.gpu
+
+
+def queries(seed, dtype, s, h_q, d):
+    x = randn(torch.Generator().manual_seed(seed), 1, s, h_q, d).to(DT[dtype]).cuda()
+    return x.permute(0, 2, 1, 3)
+
+
+def definition(c, n, q, scale):
+    """Of one sequence over one KV head, every key seen, in 64 bits: the weights [rows, n] (rows: [h_q, s]), LSE, V's
+    codes [n, d] and scales [n], and reach [rows, n] = |scale| sum_d |q_d k_jd|."""
+    pages = c.page_table.cpu().numpy()[0][np.arange(n) // c.k.shape[2]]
+    slot = np.arange(n) % c.k.shape[2]
+    k = values_of(c.k)[pages, 0, slot] * f64(c.k_scale)[pages, 0, slot][:, None]
+    rows = f64(q)[0].reshape(-1, q.shape[-1])
+    x = scale * (rows @ k.T)
+    big = x.max(-1, keepdims=True)
+    p = np.exp(x - big)
+    total = p.sum(-1, keepdims=True)
+    return p / total, (big + np.log(total))[:, 0], values_of(c.v)[pages, 0, slot], f64(c.v_scale)[pages, 0, slot], \
+        abs(scale) * (np.abs(rows) @ np.abs(k).T)
+
+
+def check(c, n, q, dtype, o, lse, scale):
+    """The bounds of assert_attend_close with the scores' error written out (d / 16 steps of a tensor core's sum, each off
+    by 2^-21 of reach; ex2, log2 and up to 32 moves of the reference: 2^-17), and what F16 operands of the
+    products add where the scales of V differ much.
+
+    Blocks of many rows: V's F16 elements are code * f, f = scale / 2^E < 128 with the tile's largest scale at 64 2^E or
+    more.  Below F16's normal range f is off by half of its least step, 2^-25, the element by 448 times that and half
+    a step of its own: under 2^-16 of 2^E, 2^-22 of the tile's largest scale, times the key's weight.  Weights of both
+    kernels: off by half of F16's least step, 2^-25, where the largest of a row is 2^5 or more (an offset of 2^6, an
+    integer reference) and 2^E is up to a 32nd of the largest scale while f < 128, so by 2^-27 of the largest weight
+    times the largest scale, times the code."""
+    p, L, codes, vs, reach = definition(c, n, q, scale)
+    v = codes * vs[:, None]
+    want, spread = p @ v, p @ np.abs(v)
+    rows, d = q.shape[1] * q.shape[2], q.shape[3]
+    score = d / 16 * 2.0 ** -21 * reach
+    extra = vs.max() * (2.0 ** -22 + 2.0 ** -27 * p.max(-1, keepdims=True) * np.abs(codes).sum(0))
+    tol = (HALF_STEP["f16"] + 2.0 ** -17 + score.max(-1, keepdims=True) + kv_rounding("e4m3", rows, d, dtype)) * spread + extra + \
+        HALF_STEP[dtype] * np.abs(want) * 1.01 + TINY[dtype]
+    got = f64(o)[0].reshape(want.shape)
+    assert np.isfinite(got).all(), "O is not finite"
+    worst = (np.abs(got - want) / tol).max()
+    assert worst <= 1, f"O: {worst:.2f} of the tolerance"
+    err = np.abs(f64(lse).reshape(-1) - L)
+    assert (err <= (p * score).sum(-1) + 2.0 ** -17 + 2.0 ** -20 * np.abs(L)).all(), f"LSE: max err {err.max():.3e}"
+
+
+def scaled(pattern, c, g):
+    """Puts a pattern into V's scales (of every slot; those behind the sequence do not count)."""
+    vs = c.v_scale
+    pick = torch.rand(vs.shape, generator=g).cuda()
+    if pattern == "mixed":                   # next to ordinary ones, scales that count for nothing, one kind subnormal
+        vs.copy_(torch.where(pick < 0.4, 1.0, torch.where(pick < 0.7, 1e-30, 1e-40)))
+    elif pattern == "tiny":
+        vs.copy_(1e-30 * (1 + pick))
+    elif pattern == "subnormal":
+        vs.copy_(1e-40 * (1 + pick))
+    elif pattern == "zero":
+        vs.zero_()
+    elif pattern == "zero next to the largest":
+        vs.copy_(torch.where(pick < 0.5, 0.0, torch.where(pick < 0.98, 0.01, 2.0 ** 118)))
+    elif pattern == "large":                 # a few rows of up to 448 * 2^118, in BF16's range
+        vs.copy_(torch.where(pick < 0.02, 2.0 ** 118, 0.01))
+    elif pattern == "one largest":           # a scale beyond 2^126, of codes that leave the values in range
+        vs.fill_(0.01)
+        pg, sl = c.page_table[0, 1].item(), 3
+        vs[pg, 0, sl] = 1.5 * 2.0 ** 126
+        c.v[pg, 0, sl] = torch.where(torch.arange(c.v.shape[3], device="cuda") % 2 == 0, 1.0, -0.5).to(c.v.dtype)
+
+
+PATTERNS = ["mixed", "tiny", "subnormal", "zero", "large", "zero next to the largest", "one largest"]
+
+
+# One token (a cluster a sequence; with many columns of the page table, runs of tiles that are joined), 12 rows (blocks of 16).
+@pytest.mark.parametrize("columns", [None, 4096])
+@pytest.mark.parametrize("s,h_q,d", [(1, 4, 128), (3, 4, 64), (1, 4, 256)])
+@pytest.mark.parametrize("pattern", PATTERNS)
+def test_scales_of_values(pattern, s, h_q, d, columns):
+    g, n = torch.Generator().manual_seed(50), 1500
+    c = make_cache((n,), 1, d, 16, "e4m3", seed=51, wide=columns)
+    scaled(pattern, c, g)
+    q = queries(52, "bf16", s, h_q, d)
+    # scores of some +-20, so that the weights of single keys differ by many powers of two
+    scale = 5 * d ** -0.5
+    o, lse = run_decode(c, q, scale=scale)
+    check(c, n, q, "bf16", o, lse, scale)
+    if pattern == "zero":
+        assert not o.any()
+
+
+@pytest.mark.parametrize("columns", [None, 4096])
+@pytest.mark.parametrize("spoil", [float("nan"), float("inf")])
+@pytest.mark.parametrize("s", [1, 3])
+def test_lse_does_not_depend_on_the_scales_of_values(s, spoil, columns):
+    """A value scale that is not finite spoils O, and leaves LSE as it is."""
+    c = make_cache((700,), 1, 128, 16, "e4m3", seed=53, wide=columns)
+    q = queries(54, "bf16", s, 4, 128)
+    clean, clean_lse = run_decode(c, q)
+    c.v_scale[c.page_table[0, 20].item(), 0, 5] = spoil
+    o, lse = run_decode(c, q)
+    assert torch.equal(lse, clean_lse) and torch.isfinite(lse).all()
+    assert torch.isfinite(clean).all() and not torch.isfinite(o).any()
+
+
+@pytest.mark.parametrize("s,h_q", [(5, 2)])
+def test_hidden_tokens_may_have_the_largest_scales(s, h_q):
+    """A drafted token whose V is 2^118 times the others' changes nothing for the rows that do not see it."""
+    c = make_cache((60,), 1, 128, 16, "e4m3", seed=55)
+    q = queries(56, "bf16", s, h_q, 128)
+    bad = s // 2
+    tree = np.tril(np.ones((s, s), dtype=bool))[None]
+    tree[0, :, bad] = False
+    tree[0, bad, bad] = True
+    clean, clean_lse = run_decode(c, q, tree=tree)
+    pos = 60 - s + bad
+    c.v_scale[c.page_table[0, pos // 16].item(), 0, pos % 16] = 2.0 ** 118
+    o, lse = run_decode(c, q, tree=tree)
+    rest = [i for i in range(s) if i != bad]
+    assert torch.equal(o[:, :, rest], clean[:, :, rest]) and torch.equal(lse[:, :, rest], clean_lse[:, :, rest])
+    # The sum of the row that sees it is brought down by 2^e, e < 32, so that O stays in range, and e joins the reference
+    # m, |m| < 32 here: their sum, below 2^6, is off by half a step of 2^-18, times ln 2; a step of the result.
+    assert (lse - clean_lse).abs().max() <= 2.0 ** -19 + 2.0 ** -21
+    assert torch.isfinite(o).all() and (o[:, :, bad].abs().amax(-1) > 2.0 ** 90).all()
