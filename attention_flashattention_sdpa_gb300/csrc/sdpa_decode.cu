@@ -78,12 +78,6 @@ struct DecCfg {
   static_assert(NS >= 2 && NS * 5 <= 32, "ring");
 };
 
-// Bounds of v: 2^-v and 2^v are both fp32 values, and w stays below 2^15 (scales reach 2^128).  Up to +-kNearV,
-// far wider than rows of 16-bit elements ever need, v joins the exponents of a row's weights and of its sum, so
-// that a weight costs one multiplication by vs; what v is beyond that takes another one (`wild`).
-constexpr int kMinV = -125, kMaxV = 127, kNearV = 60;
-__device__ __forceinline__ int near_v(int v) { return min(max(v, -kNearV), kNearV); }
-
 // Position of 16-byte chunk `ch` of row `r` in a stage: neighbouring rows differ in bit 2 (the
 // key reads of a quarter-warp are two rows of four chunks), rows 2c in bits 1-2 (the value
 // reads are four even or odd rows of two chunks), so both are free of bank conflicts.
@@ -434,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
                 t = max(t, __shfl_xor_sync(0xffffffffu, t, 8));
                 t = max(t, __shfl_xor_sync(0xffffffffu, t, 16));
               }
-              const int before = v_row[n * 8 + u], need = static_cast<int>(t >> 23) - 126;
+              const int before = v_row[n * 8 + u], need = needed_v(t);
               const int now = before >= need ? before : min(need + 1, kMaxV), step = near_v(before) - near_v(now);
               alpha[u] = pow2(max(before - now, -126));
               l[n][u] *= pow2(step);

@@ -38,6 +38,15 @@ __device__ __forceinline__ float2 unpack_pair(uint32_t w) {
 // 2^e, e in -126 .. 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
+// E4M3 caches: the exponent v of a row, 2^v being above the scales of the values that it sees.
+// Bounds: 2^-v and 2^v are fp32 values, and weights over 2^v stay below 2^15 (scales reach 2^128).  Up to
+// +-kNearV, far wider than ordinary values need, v joins the exponents of a row's weights and of its sum, so that
+// a weight costs one multiplication by the scale; what v is beyond that takes another one (`wild`).
+constexpr int kMinV = -125, kMaxV = 127, kNearV = 60;
+__device__ __forceinline__ int near_v(int v) { return min(max(v, -kNearV), kNearV); }
+// For a scale given as the bits of its magnitude.
+__device__ __forceinline__ int needed_v(uint32_t bits) { return static_cast<int>(bits >> 23) - 126; }
+
 // Clears the halves of a 16-bit pair that are infinite or NaN; `found` gathers whether any was.
 template <bool BF>
 __device__ __forceinline__ uint32_t finite_pair(uint32_t w, bool& found) {

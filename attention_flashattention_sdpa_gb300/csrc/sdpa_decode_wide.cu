@@ -5,9 +5,10 @@
 // one persistent CTA an SM walks a run of tiles for its KV head and block of rows, segment by segment
 // (a segment: the part of the run in one sequence).  Roles:
 //   warps 0, 2   pages and TMA of K and of V, box by box (a box lies in one page), a lane a box; boxes
-//                of missing pages and behind the sequence are filled with zeros.  E4M3: V's scales
-//                follow by bulk copies.  (One thread for all of them took 4200 cycles a tile.)
+//                of missing pages and behind the sequence are filled with zeros.  (One thread for all of
+//                them took 4200 cycles a tile.)
 //   warp 1       MMA issuer: S = Q K^T into TMEM, O += P V with P read from TMEM.
+//   warp 3       E4M3: V's scales.
 //   warps 4-11   two softmax warpgroups; thread r owns a row: loads it into shared memory, the
 //                running max and sum, P, and the segment's results.  A block of more than 128 rows
 //                has a 128-row tile for each; in a smaller one both take the same rows and every
@@ -18,20 +19,18 @@
 //                that do not exist and values that are not finite (a weight of zero does not hide a
 //                NaN in a product).
 //
-// E4M3: K's codes become F16 as they are, so S of codes is exact up to the fp32 sums; the softmax warps
-// multiply each of its columns by the key's scale in fp32.  V's codes are multiplied by scale / 2^E (2^E:
-// about 1/64 of the tile's largest scale) as a sum of two F16 factors, so one rounding to F16's 11
-// bits is left, as P's (of rows 2^-28 as large as others of their tile, to fewer: F16 ends there);
-// 2^E joins the exponent of the weights once a tile.  Where the results are F16, whose own rounding does not
-// cover that one, V's codes take only the scale's first 7 bits, which F16 holds exactly, and the weights the
-// rest of it (FOLD).
-// (K times its scale in F16 too left the scores off by 2^-12 of themselves, which the LSE shows.)
+// E4M3: codes become F16 as they are.  S of codes is exact up to the fp32 sums, and the softmax warps multiply
+// each of its columns by the key's scale in fp32; the scale of its value joins the weight, over 2^v of the row, as
+// in sdpa_decode.cu: weights are rounded once, V not at all, l and LSE know nothing of V's scales, and a hidden
+// key's scale touches no other row.  (V times scale over a power of two of the tile, in F16, instead: two roundings,
+// and rows lost the keys beside a drafted one with a scale 2^20 times theirs, hidden or not.  K times
+// its scale in F16 left the scores off by 2^-12 of themselves, which the LSE shows.)
 //
 // Bound: the tensor cores (4 x 128 x 128 x d MMAs a block of two tiles) and the exponentials, as
 // the prompt's forward pass; reading the cache once bounds it for few rows.  Measured, 8 sequences of 4000
-// to 8192 tokens, trees of 64 tokens, 64 heads over 8 of 128: BF16 105 us (990 TFLOP/s), E4M3 154 (670; F16 results 160; 2.5
-// us for 128 keys by 256 rows against 1.75: the warps that widen and the scales of K share the
-// schedulers and the shared memory with the softmax, and K has one slot where BF16 has two).  35 to
+// to 8192 tokens, trees of 64 tokens, 64 heads over 8 of 128: BF16 105 us (990 TFLOP/s), E4M3 152 (680; F16 results 137: the
+// warps that widen and the scales, 64 reads of 16 bytes a row and tile, share the schedulers and the shared
+// memory with the softmax, and K has one slot where BF16 has two).  35 to
 // 45 us of either are the first fetch of the code, Q, the last results and the parts.
 #include <type_traits>
 
@@ -58,11 +57,12 @@ struct WideCfg {
   static constexpr int NK = D == 128 ? (E4 ? 1 : 2) : (E4 ? 2 : 3), NV = D == 128 ? 2 : 3;
   static constexpr int RK = E4 ? 2 : 0, RV = E4 ? 2 : 0;
   static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + NK * TILE, OFF_RAW = OFF_V + NV * TILE;
-  // Scales: V's stages, and K's in a ring that the softmax warps read.  A slot of K is free once S of
-  // the tile NK back is done, and that S followed the weights of the tile before it, or (split) two
-  // before it: NK + 2 tiles' scales never meet.
-  static constexpr int KS = E4 ? NK + 2 : 0;
-  static constexpr int OFF_SC = OFF_RAW + (RK + RV) * RAW, OFF_KS = OFF_SC + RV * 512, OFF_CTL = OFF_KS + KS * 512;
+  // Scales, in rings that the softmax warps read, written when the tile's slot is free.  A slot of K is
+  // free once S of the tile NK back is done, and that S followed the weights of the tile before it, or (split)
+  // two before it: NK + 2 tiles' scales never meet.  A slot of V is free once P V of the tile NV back is
+  // done, which its weights preceded: NV tiles'.
+  static constexpr int KS = E4 ? NK + 2 : 0, VS = E4 ? NV : 0;
+  static constexpr int OFF_KS = OFF_RAW + (RK + RV) * RAW, OFF_VS = OFF_KS + KS * 512, OFF_CTL = OFF_VS + VS * 512;
   static constexpr int SMEM = OFF_CTL + 512;
   static constexpr int KSTEPS = D / 16;
   static constexpr int O_COL0 = 256;
@@ -78,8 +78,7 @@ struct alignas(8) WideBarriers {
   uint64_t raw_full[4], raw_empty[4];       // E4M3 tiles: K's stages, then V's
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t ml_full, o1_free;                // split: the second warpgroup's maxima and sums are there; its O is read
-  uint64_t sc_full[4];                      // E4M3: a tile's K scales and the exponent of its V scales are there
-  uint64_t sc_read[2];                      // FOLD: the widening warps have read a stage's V scales
+  uint64_t sc_full[4];                      // E4M3: a tile's scales are there
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -118,7 +117,7 @@ struct Walk : Run {
 struct Control {
   WideBarriers bars;
   Walk walk;
-  int ev[8];             // E4M3: exponent of a tile's V scales, by tile count
+  int ev[4];             // E4M3: v that a tile's V scales need, by tile count (as sc_full)
   int found[8];          // segment count + 1 of a segment with cleared values
 };
 static_assert(sizeof(Control) <= 512);
@@ -129,26 +128,10 @@ __device__ __forceinline__ bool needs_cleaning(const DecodeParams& p, const Segm
   return end > g.L.len_kv || ((p.causal || p.tree_mask) && end > g.off);
 }
 
-// Exponent e of a positive fp32 given as bits (2^e <= x < 2^(e+1)), kept where 2^e and 2^-e are normal.
-__device__ __forceinline__ int exponent_of(uint32_t bits) { return min(max(static_cast<int>(bits >> 23) - 127, -100), 100); }
-
-// Exponent, less 6, of the largest finite scale of a tile's existing keys (`left` of 128), by a whole
-// warp: scales over 2^it are below 128, times codes of up to 448 below F16's 65504.
-__device__ __forceinline__ int largest_exponent(const float* scales, int left, int lane) {
-  const float4 f = *reinterpret_cast<const float4*>(scales + lane * 4);
-  auto bits = [&](float x, int i) {
-    const uint32_t b = __float_as_uint(x);
-    return lane * 4 + i < left && b < 0x7F800000u ? b : 0u;
-  };
-  return exponent_of(__reduce_max_sync(0xffffffffu, max(max(bits(f.x, 0), bits(f.y, 1)), max(bits(f.z, 2), bits(f.w, 3))))) - 6;
-}
-
-// Contiguous copy of a multiple of 16 bytes into shared memory, counted on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
+// What a tile's V scales are divided by (log2) as they are stored, v_tile being the v that they need: nothing, unless
+// that is far from 0.  They are then below 2^68, and a weight times vs / 2^v, below 2^15, is a product of two fp32
+// values, one of them the exponential with the rest of 2^-v in its argument.
+__device__ __forceinline__ int scale_exponent(int v_tile) { return v_tile > kNearV ? kNearV : v_tile < -kNearV ? -kNearV : 0; }
 
 struct WideParams {
   DecodeParams d;
@@ -164,8 +147,6 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
   using C = WideCfg<D, CT>;
   constexpr bool E4 = C::E4;
   constexpr bool BF = CT == kBF16;     // type of the 16-bit operands
-  // F16 results of an E4M3 cache: V without a rounding of its own, what its scale has beyond 7 bits in P.
-  constexpr bool FOLD = E4 && QT == kF16;
   // Slot or stage of tile n of K or V, and the turn it is in there.
   struct Place {
     int at, turn;
@@ -187,10 +168,11 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
   uint8_t* sQ = smem;
   uint8_t* sRing = smem + C::OFF_K;
   uint8_t* sRaw = smem + C::OFF_RAW;
-  float* sSc = reinterpret_cast<float*>(smem + C::OFF_SC);   // V's scales [stage][128]
   float* sKs = reinterpret_cast<float*>(smem + C::OFF_KS);   // K's scales [tile % KS][128]
-  // Split: the second warpgroup's maximum and sum of each row (the second tile of Q is not used).
+  float* sVs = reinterpret_cast<float*>(smem + C::OFF_VS);   // V's scales [tile % VS][128]
+  // Split: the second warpgroup's maximum, sum and (E4M3) v of each row (the second tile of Q is not used).
   float2* s_ml = reinterpret_cast<float2*>(smem + C::TILE);
+  int* s_v = reinterpret_cast<int*>(smem + C::TILE + 128 * 8);
   Control& ctl = *reinterpret_cast<Control*>(smem + C::OFF_CTL);
   WideBarriers& bars = ctl.bars;
   volatile int* s_ev = ctl.ev;
@@ -223,8 +205,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
       mbar_init(&bars.raw_full[i], 1);
       mbar_init(&bars.raw_empty[i], 128);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&bars.sc_full[i], 4 + (FOLD ? 4 : 1));
-    for (int i = 0; i < 2; ++i) mbar_init(&bars.sc_read[i], 4);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars.sc_full[i], 4 + 1);
     mbar_init(&bars.ml_full, 128);
     mbar_init(&bars.o1_free, 128);
     mbar_init(&bars.drain, 1);
@@ -259,11 +240,9 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
       const CUtensorMap* map = is_v ? &wp.tm_v : &wp.tm_k;
       if (lane == 0) tma_prefetch_desc(map);
       const int boxes = kKeys / wp.box;     // boxes of a tile: 1, 2, 4 or 8
-      const unsigned all = (1u << boxes) - 1u;
-      // Lane x + 8 y issues copy y of box x: of 16-bit tiles the 128-byte columns, of E4M3 ones the
-      // codes and V's scales.
+      // Lane x + 8 y issues copy y of box x: of 16-bit tiles the 128-byte columns, of E4M3 ones the codes.
       const int bx = lane % 8, by = lane / 8;
-      constexpr int kCopies = E4 ? 2 : C::NCHUNK;
+      constexpr int kCopies = E4 ? 1 : C::NCHUNK;
       bool ok = true;
       while (ok && walk.next(p, sg)) {
         const int32_t* pages = p.c.page_table + sg.bi * p.c.page_table_stride;
@@ -290,37 +269,17 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
             look_up(b0 + 32, next_page, next_slot);
           }
           const int pg = __shfl_sync(0xffffffffu, page, (b0 + bx) % 32), sl = __shfl_sync(0xffffffffu, slot, (b0 + bx) % 32);
-          const unsigned there = __ballot_sync(0xffffffffu, pg < p.c.num_pages) & all;   // bit x: box x exists
           const Place at = E4 ? stage_of(is_v, issued) : slot_of(is_v, issued);
           const int s = at.at;
           if (!mbar_wait_warp(E4 ? &bars.raw_empty[s] : &bars.empty[s], (at.turn & 1) ^ 1, wt)) { ok = false; break; }
-          if (FOLD && is_v && issued >= C::RV) {
-            // The stage's scales, now the factors on P, are read until P V of their tile.
-            const Place x = slot_of(true, issued - C::RV);
-            if (!mbar_wait_warp(&bars.empty[x.at], x.turn & 1, wt)) { ok = false; break; }
-          }
           uint64_t* full = E4 ? &bars.raw_full[s] : &bars.full[s];
           uint8_t* dst = E4 ? sRaw + s * C::RAW : sRing + s * C::TILE;
-          const bool scales = E4 && is_v;
-          float* sc = sSc + (s - C::RK) * 128;
-          if (scales) {
-            if (there != all) {      // no scale where there is no key
-              for (int i = lane; i < kKeys; i += 32)
-                if (!((there >> (i / wp.box)) & 1u)) sc[i] = 0.f;
-            }
-            __syncwarp();
-          }
-          if (lane == 0) mbar_arrive_expect_tx(full, E4 ? C::RAW + (scales ? __popc(there) * wp.box * 4 : 0) : C::TILE);
+          if (lane == 0) mbar_arrive_expect_tx(full, E4 ? C::RAW : C::TILE);
           ++issued;
           __syncwarp();
           if (bx < boxes && by < kCopies) {
             if constexpr (E4) {
-              if (by == 0) {
-                tma_load_4d(dst + bx * wp.box * 128, map, full, 0, sl, hk, pg);
-              } else if (scales && pg < p.c.num_pages) {
-                bulk_load(sc + bx * wp.box, p.c.v_scale + (static_cast<int64_t>(pg) * p.c.h_kv + hk) * p.c.page_size + sl,
-                          wp.box * 4, full);
-              }
+              tma_load_4d(dst + bx * wp.box * 128, map, full, 0, sl, hk, pg);
             } else {
               tma_load_4d(dst + by * 16384 + bx * wp.box * 128, map, full, by * 64, sl, hk, pg);
             }
@@ -432,6 +391,61 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         tc_commit(&bars.drain);
         mbar_wait_drain(&bars.drain, 0);
       }
+    } else if (E4) {
+      // ================================ V's scales ========================================
+      bool ok = true;
+      int n_seg = 0, n_tile = 0;
+      while (ok && walk.next(p, sg)) {
+        // Lane l: page of keys 4 l .. 4 l + 3 of a tile (-1: none; pages hold multiples of 16), and their
+        // scales (0 where there is no key); both are asked for ahead.
+        auto page_of = [&](int j) {
+          const int key = j * kKeys + 4 * lane;
+          return key < sg.L.len_kv ? __ldg(p.c.page_table + sg.bi * p.c.page_table_stride + key / p.c.page_size) : -1;
+        };
+        auto scales_of = [&](int j, int page) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (page < 0 || page >= p.c.num_pages) return x;
+          const int key = j * kKeys + 4 * lane, left = sg.L.len_kv - key;
+          x = __ldg(reinterpret_cast<const float4*>(p.c.v_scale + (static_cast<int64_t>(page) * p.c.h_kv + hk) * p.c.page_size +
+                                                    key % p.c.page_size));
+          if (left < 2) x.y = 0.f;
+          if (left < 3) x.z = 0.f;
+          if (left < 4) x.w = 0.f;
+          return x;
+        };
+        float4 scales = scales_of(sg.tile0, page_of(sg.tile0));
+        int page1 = sg.tile0 + 1 < sg.tile1 ? page_of(sg.tile0 + 1) : -1;
+        for (int j = sg.tile0; j < sg.tile1; ++j, ++n_tile) {
+          auto magnitude = [](float x) {
+            const uint32_t b = __float_as_uint(fabsf(x));
+            return b < 0x7F800000u ? b : 0u;
+          };
+          const int need = needed_v(__reduce_max_sync(0xffffffffu, max(max(magnitude(scales.x), magnitude(scales.y)),
+                                                                       max(magnitude(scales.z), magnitude(scales.w)))));
+          const float by = pow2(-scale_exponent(need));
+          float x[4] = {scales.x * by, scales.y * by, scales.z * by, scales.w * by};
+          if ((p.causal || p.tree_mask) && (j + 1) * kKeys > sg.off) {
+            // A scale that is not finite, times the weight of zero of a row that does not see its key, would be
+            // NaN: rows that do see it get its values afterwards.
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!(fabsf(x[i]) < INFINITY)) {
+                x[i] = 0.f;
+                s_found[n_seg % 8] = n_seg + 1;
+              }
+          }
+          const Place to = slot_of(true, n_tile);
+          ok = mbar_wait_warp(&bars.empty[to.at], (to.turn & 1) ^ 1, wt);
+          if (!ok) break;
+          *reinterpret_cast<float4*>(sVs + n_tile % (C::VS > 0 ? C::VS : 1) * 128 + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+          if (lane == 0) s_ev[n_tile % 4] = need;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.sc_full[n_tile % 4]);
+          scales = scales_of(j + 1, page1);
+          page1 = j + 2 < sg.tile1 ? page_of(j + 2) : -1;
+        }
+        ++n_seg;
+      }
     }
   } else if (warp >= 12) {
     regs_dec<C::REGS_WIDEN>();
@@ -467,33 +481,6 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           const int rs = from.at, s = to.at, left = sg.L.len_kv - j * kKeys;
           ok = mbar_wait_warp(&bars.raw_full[rs], from.turn & 1, wt);
           if (!ok) break;
-          __half2 h2 = __float2half2_rn(0.f), l2 = h2;
-          if (is_v) {
-            float* sc = sSc + (rs - C::RK) * 128;
-            const int ex = largest_exponent(sc, left, lane);      // (by every lane)
-            const float f = on ? sc[r] * pow2(-ex) : 0.f;
-            if (warp % 4 == 0 && lane == 0) s_ev[n_tile % 8] = ex;
-            if constexpr (FOLD) {
-              // Seven bits of scale / 2^E, whose product with a code F16 holds exactly; the rest (a factor
-              // of 1 to 1 + 2^-6) takes the scale's place for the softmax warps once all have read it.
-              const __half fh = __float2half_rz(__uint_as_float(__float_as_uint(f) & 0xFFFE0000u));
-              const float ff = __half2float(fh);
-              h2 = __half2half2(fh);
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars.sc_read[n_tile % 2]);
-              ok = mbar_wait_warp(&bars.sc_read[n_tile % 2], (n_tile / 2) & 1, wt);
-              if (!ok) break;
-              sc[r] = ff > 0.f && f < INFINITY ? __fdividef(f, ff) : 1.f;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars.sc_full[n_tile % 4]);
-            } else {
-              if (warp % 4 == 0 && lane == 0) mbar_arrive(&bars.sc_full[n_tile % 4]);
-              // scale / 2^E of the lane's row as two F16, each twice in a word
-              const __half fh = __float2half_rn(f), fl = __float2half_rn(f - __half2float(fh));
-              h2 = __half2half2(fh);
-              l2 = __half2half2(fl);
-            }
-          }
           ok = mbar_wait_warp(&bars.empty[s], (to.turn & 1) ^ 1, wt);
           if (!ok) break;
           if (!is_v) {
@@ -507,7 +494,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           // quarter-warp into 8 different 16-byte columns.
           const uint8_t* src = sRaw + rs * C::RAW + r * 128;
           uint8_t* dst = sRing + s * C::TILE + r * 128;
-          auto widen = [&](auto scale, auto clear) {
+          auto widen = [&](auto clear) {
 #pragma unroll
             for (int ch = 0; ch < D / 16; ++ch) {
               const uint4 in = *reinterpret_cast<const uint4*>(src + (ch ^ (r & 7)) * 16);
@@ -516,11 +503,6 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 out[e] = e4m3x2_to_f16x2(e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
-                if constexpr (decltype(scale)::value) {
-                  const __half2 v = *reinterpret_cast<const __half2*>(&out[e]);
-                  const __half2 y = FOLD ? __hmul2(v, h2) : __hfma2(v, h2, __hmul2(v, l2));
-                  out[e] = *reinterpret_cast<const uint32_t*>(&y);
-                }
                 if constexpr (decltype(clear)::value) out[e] = on ? finite_pair<false>(out[e], found) : 0u;
               }
 #pragma unroll
@@ -531,9 +513,8 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
               }
             }
           };
-          if (!is_v) widen(std::false_type{}, std::false_type{});
-          else if (tail || left < kKeys) widen(std::true_type{}, std::true_type{});
-          else widen(std::true_type{}, std::false_type{});
+          if (is_v && (tail || left < kKeys)) widen(std::true_type{});
+          else widen(std::false_type{});
           if (found) s_found[n_seg % 8] = n_seg + 1;
           fence_proxy_async_smem();
           mbar_arrive(&bars.full[s]);
@@ -646,6 +627,19 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
       }
       return cs;
     };
+    // O of this thread's row times a factor; by a whole warp, when the products so far are done.
+    auto rescale_o = [&](float by) {
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32];
+        tmem_ld32(o_addr + c * 32, ov);
+        tmem_ld_wait();
+        reg_fence32(ov);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * by);
+        tmem_st32(o_addr + c * 32, ov);
+      }
+    };
     bool more = walk.next(p, sg);
     float cs = more ? load_q(sg) : 0.f;
     while (ok && more) {
@@ -672,21 +666,19 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         bad = __any_sync(0xffffffffu, bad) != 0;
       }
       float m_ref = -INFINITY, l = 0.f;
+      int v = kMinV;              // E4M3
       for (int i = first; i < n; i += step, ++n_own) {
         if (!mbar_wait_warp(&bars.s_full[t], n_own & 1, wt)) { ok = false; break; }
         tc_fence_after();
         const int key0 = (sg.tile0 + i) * kKeys;
-        // E4M3: the exponent of the tile's V, in the weights' exponent and out of l again; K's scales.
-        float ev = 0.f, back = 1.f;
-        const float *ks = nullptr, *vr = nullptr;
+        int v_tile = 0;             // E4M3: the v that the tile's values need; scales of K and V
+        const float *ks = nullptr, *vs = nullptr;
         if constexpr (E4) {
           const int tile = n_tile + i;
           if (!mbar_wait_warp(&bars.sc_full[tile % 4], (tile / 4) & 1, wt)) { ok = false; break; }
-          const int e = s_ev[tile % 8];
-          ev = static_cast<float>(e);
-          back = pow2(-e);
+          v_tile = s_ev[tile % 4];
           ks = sKs + tile % C::KS * 128;
-          vr = sSc + tile % C::RV * 128;
+          vs = sVs + tile % C::VS * 128;
         }
         const bool need = key0 + kKeys > sg.L.len_kv || (masked && key0 + kKeys > sg.off) || bad;
         uint32_t vis[4];       // visible columns
@@ -727,7 +719,33 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         // The reference m_ref is an integer, so the rare step between the halves scales the first
         // half's P, already rounded, exactly.  (One body for both: instruction fetch, not registers,
         // limits an unrolled one.)
-        float alpha = 1.f;
+        float alpha = 1.f, alpha_v = 1.f;
+        int shift = 0;              // E4M3: log2 of what vs / 2^v takes beyond the scales as they are stored
+        if constexpr (E4) {
+          const int s0 = scale_exponent(v_tile);
+          if (v_tile > v) {
+            int least = v_tile;
+            if (need) {      // keys that the row does not see may not move it: looked through one by one, being rare
+              uint32_t top = 0;
+#pragma unroll 1
+              for (int c = 0; c < 32; ++c) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                  if ((vis[w] >> c) & 1u) top = max(top, __float_as_uint(fabsf(vs[32 * w + c])));
+              }
+              least = top == 0 ? v : needed_v(top) + s0;
+            }
+            if (least > v) {
+              const int now = min(least + 1, kMaxV);      // (one more, so that it seldom moves again)
+              alpha_v = pow2(max(v - now, -126));
+              v = now;
+            }
+          }
+          __syncwarp();
+          // At -70 nothing is left of the weights in F16 (their scales are below 1 then); above 80 are rows that see
+          // scales of next to nothing beside a hidden one of over 2^60.
+          shift = min(max(s0 - v, -70), 80);
+        }
         const float2 cs2 = make_float2(cs, cs);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -764,7 +782,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
             mx2 = max3(mx2, __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
             mx3 = max3(mx3, __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
           }
-          const float m_cand = fmaf(max3(mx0, mx1, fmaxf(mx2, mx3)), cs, ev);
+          const float m_cand = max3(mx0, mx1, fmaxf(mx2, mx3)) * cs;
           const bool up = m_cand > m_ref + C::THRESH;
           if (__any_sync(0xffffffffu, up)) {
             const float m_new = up ? ceilf(m_cand) : m_ref, a = up ? ex2(m_ref - m_new) : 1.f;
@@ -786,7 +804,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
               tmem_st32(s_addr, pv);
             }
           }
-          const float nm = m_ref == -INFINITY ? 0.f : C::P_OFF - m_ref + ev;
+          const float nm = m_ref == -INFINITY ? 0.f : C::P_OFF - m_ref + (E4 ? static_cast<float>(shift) : 0.f);
           const float2 nm2 = make_float2(nm, nm);
           uint32_t pk[32];
 #pragma unroll
@@ -796,8 +814,8 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
             float2 p01 = make_float2(ex2(x01.x), ex2(x01.y)), p23 = make_float2(ex2(x23.x), ex2(x23.y));
             acc0 = add2(acc0, p01);
             acc1 = add2(acc1, p23);
-            if constexpr (FOLD) {
-              const float4 f = *reinterpret_cast<const float4*>(vr + h * 64 + c);
+            if constexpr (E4) {
+              const float4 f = *reinterpret_cast<const float4*>(vs + h * 64 + c);
               p01 = mul2(p01, make_float2(f.x, f.y));
               p23 = mul2(p23, make_float2(f.z, f.w));
             }
@@ -807,20 +825,10 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           __syncwarp();
           tmem_st32(s_addr + h * 32, pk);
         }
-        l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y)) * back;
+        l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y)) * (E4 ? pow2(-shift) : 1.f);
         // The block before has added to O already: its P V was issued ahead of this block's S.
-        if (i > first && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t ov[32];
-            tmem_ld32(o_addr + c * 32, ov);
-            tmem_ld_wait();
-            reg_fence32(ov);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-            tmem_st32(o_addr + c * 32, ov);
-          }
-        }
+        alpha *= alpha_v;
+        if (i > first && __any_sync(0xffffffffu, alpha != 1.f)) rescale_o(alpha);
         tmem_st_wait();
         tc_fence_before();
         if (o1_pending) {              // this tile's P V overwrites O
@@ -844,6 +852,7 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
       if (split && t == 1) {
         if (o1_pending && !mbar_wait_warp(&bars.o1_free, (n_seg - 1) & 1, wt)) { ok = false; break; }
         s_ml[r] = make_float2(m_ref, l);
+        if constexpr (E4) s_v[r] = v;
         mbar_arrive(&bars.ml_full);
         o1_pending = true;
         ++n_seg;
@@ -865,6 +874,23 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
           f1 = part_weight(ml1, m);
           l = (f0 == 0.f ? 0.f : l * f0) + (f1 == 0.f ? 0.f : ml1.y * f1);
           m_ref = m;
+          if constexpr (E4) {
+            const int v0 = v, v1 = s_v[r];
+            v = max(v0, v1);
+            f0 *= pow2(max(v0 - v, -126));
+            f1 *= pow2(max(v1 - v, -126));
+          }
+        }
+      }
+      // E4M3: 2^v joins O (and see sdpa_decode.cu on values near fp32's end).
+      float up = 1.f;
+      if constexpr (E4) {
+        up = pow2(v);
+        if (v > kNearV && l > 0.f && l < INFINITY) {
+          const int e = static_cast<int>(__float_as_uint(l) >> 23) - 127 + 12;
+          up *= pow2(-e);
+          l *= pow2(-e);
+          m_ref += static_cast<float>(e);
         }
       }
       tc_fence_after();
@@ -891,6 +917,10 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         } else {
           tmem_ld_wait();
           reg_fence32(ov);
+        }
+        if constexpr (E4) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * up);
         }
         if (row < p.rows) {
           if (fix) {

@@ -82,9 +82,10 @@ def scaled(pattern, c, g):
 PATTERNS = ["mixed", "tiny", "subnormal", "zero", "large", "zero next to the largest", "one largest"]
 
 
-# One token (a cluster a sequence; with many columns of the page table, runs of tiles that are joined), 12 rows (blocks of 16).
+# One token (a cluster a sequence; with many columns of the page table, runs of tiles that are joined), 12 rows (blocks of
+# 16), 40 rows (one tile of 128 for both softmax warpgroups), 280 rows (a tile for each, and 24 rows more).
 @pytest.mark.parametrize("columns", [None, 4096])
-@pytest.mark.parametrize("s,h_q,d", [(1, 4, 128), (3, 4, 64), (1, 4, 256)])
+@pytest.mark.parametrize("s,h_q,d", [(1, 4, 128), (3, 4, 64), (1, 4, 256), (10, 4, 128), (10, 4, 64), (70, 4, 128)])
 @pytest.mark.parametrize("pattern", PATTERNS)
 def test_scales_of_values(pattern, s, h_q, d, columns):
     g, n = torch.Generator().manual_seed(50), 1500
@@ -101,7 +102,7 @@ def test_scales_of_values(pattern, s, h_q, d, columns):
 
 @pytest.mark.parametrize("columns", [None, 4096])
 @pytest.mark.parametrize("spoil", [float("nan"), float("inf")])
-@pytest.mark.parametrize("s", [1, 3])
+@pytest.mark.parametrize("s", [1, 3, 40])
 def test_lse_does_not_depend_on_the_scales_of_values(s, spoil, columns):
     """A value scale that is not finite spoils O, and leaves LSE as it is."""
     c = make_cache((700,), 1, 128, 16, "e4m3", seed=53, wide=columns)
@@ -113,22 +114,57 @@ def test_lse_does_not_depend_on_the_scales_of_values(s, spoil, columns):
     assert torch.isfinite(clean).all() and not torch.isfinite(o).any()
 
 
-@pytest.mark.parametrize("s,h_q", [(5, 2)])
-def test_hidden_tokens_may_have_the_largest_scales(s, h_q):
+@pytest.mark.parametrize("others", ["ordinary", "zero"])
+@pytest.mark.parametrize("s,h_q", [(5, 2), (20, 8), (70, 4)])
+def test_hidden_tokens_may_have_the_largest_scales(s, h_q, others):
     """A drafted token whose V is 2^118 times the others' changes nothing for the rows that do not see it."""
-    c = make_cache((60,), 1, 128, 16, "e4m3", seed=55)
+    c = make_cache((90,), 1, 128, 16, "e4m3", seed=55)
+    if others == "zero":
+        c.v_scale.zero_()
     q = queries(56, "bf16", s, h_q, 128)
     bad = s // 2
     tree = np.tril(np.ones((s, s), dtype=bool))[None]
     tree[0, :, bad] = False
     tree[0, bad, bad] = True
     clean, clean_lse = run_decode(c, q, tree=tree)
-    pos = 60 - s + bad
+    pos = 90 - s + bad
     c.v_scale[c.page_table[0, pos // 16].item(), 0, pos % 16] = 2.0 ** 118
     o, lse = run_decode(c, q, tree=tree)
     rest = [i for i in range(s) if i != bad]
-    assert torch.equal(o[:, :, rest], clean[:, :, rest]) and torch.equal(lse[:, :, rest], clean_lse[:, :, rest])
-    # The sum of the row that sees it is brought down by 2^e, e < 32, so that O stays in range, and e joins the reference
-    # m, |m| < 32 here: their sum, below 2^6, is off by half a step of 2^-18, times ln 2; a step of the result.
-    assert (lse - clean_lse).abs().max() <= 2.0 ** -19 + 2.0 ** -21
+    off, was = (o - clean)[:, :, rest].double().abs(), clean[:, :, rest].double().abs()
+    if s * h_q <= 32:
+        assert not off.any() and torch.equal(lse[:, :, rest], clean_lse[:, :, rest])
+    # Blocks of many rows: the exponents of a tile's weights take the scale's 2^7 or less in, so that they are off by half of
+    # a step of 2^-16, the weights by 2^-17; the values are below 2^3, results are rounded to the next step or the one
+    # beside it.  The sum of the row that sees the token is brought down by 2^e, e < 32, so that O stays in range, and e
+    # joins the reference m, |m| < 32 here: below 2^6, off by half a step of 2^-18.  LSE has a step of its own too.
+    assert (off <= 2.0 ** -7 * was + 2.0 ** -14).all()
+    assert (lse - clean_lse).abs().max() <= 2.0 ** -17 + 2.0 ** -19 + 2.0 ** -21
     assert torch.isfinite(o).all() and (o[:, :, bad].abs().amax(-1) > 2.0 ** 90).all()
+
+
+@pytest.mark.parametrize("s,h_q", [(1, 4), (10, 4)])
+def test_long_sequence_of_zero_scales(s, h_q):
+    """Rows of V that are all zero count in the sums like any others, however many there are."""
+    n = 131072
+    c = make_cache((n,), 1, 64, 128, "e4m3", seed=57)
+    c.v_scale.zero_()
+    c.k_scale.zero_()              # every score 0: no key weighs less than the largest
+    q = queries(58, "bf16", s, h_q, 64)
+    o, lse = run_decode(c, q)
+    check(c, n, q, "bf16", o, lse, 0.125)
+    assert not o.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("s", [1, 10, 70])
+def test_scales_of_values_grow(s, dtype):
+    """Scales that grow by many powers of two along the sequence, and fall again; results in both types."""
+    n = 3000
+    c = make_cache((n,), 1, 128, 16, "e4m3", seed=59)
+    at = torch.arange(n, device="cuda")
+    size = 2.0 ** (-((at - n // 2).abs() // 100).float())        # 2^-15 .. 1 .. 2^-15
+    c.v_scale[c.page_table[0].long()[at // 16], 0, at % 16] = 0.01 * size
+    q = queries(60, dtype, s, 4, 128)
+    o, lse = run_decode(c, q)
+    check(c, n, q, dtype, o, lse, 128 ** -0.5)
