@@ -625,7 +625,8 @@ __global__ void __launch_bounds__(WideCfg<D, CT>::THREADS, 1) decode_wide_kernel
         fence_proxy_async_smem();
         mbar_arrive(&bars.q_full[t]);
       }
-      return cs;
+      // Not 0, for a scale and a row of next to nothing: hidden scores of -inf would become NaN.
+      return fmaxf(cs, 0x1p-149f);
     };
     // O of this thread's row times a factor; by a whole warp, when the products so far are done.
     auto rescale_o = [&](float by) {
@@ -1071,8 +1072,9 @@ cudaError_t launch_decode_wide(const DecodeParams& p, const CUtensorMap& tm_k, c
   wp.tm_v = tm_v;
   wp.box = decode_wide_box(p.c.page_size);
   wp.negate = p.scale_log2 < 0.f ? 1 : 0;
-  // A scale of zero: every visible key weighs the same (and hidden ones still come out as -inf).
-  wp.abs_scale_log2 = p.scale_log2 == 0.f ? 1e-30f : fabsf(p.scale_log2);
+  // A scale of zero as the least above it: products up to fp32's largest come to 2^-21, so every visible key weighs
+  // the same, and hidden ones still come out as -inf.
+  wp.abs_scale_log2 = p.scale_log2 == 0.f ? 0x1p-149f : fabsf(p.scale_log2);
   wp.wait_limit = wait_limit;
   if (d == 64) return launch_d<64>(wp, qt, ct, st);
   if (d == 128) return launch_d<128>(wp, qt, ct, st);

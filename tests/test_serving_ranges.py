@@ -168,3 +168,39 @@ def test_scales_of_values_grow(s, dtype):
     q = queries(60, dtype, s, 4, 128)
     o, lse = run_decode(c, q)
     check(c, n, q, dtype, o, lse, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("s", [1, 20])
+@pytest.mark.parametrize("kind,q_size,k_size,scale", [("e4m3", 2.0 ** -60, 1.0, 0.0), ("e4m3", 2.0 ** -100, 1.0, 1e-38),
+                                                      ("bf16", 1.0, 2.0 ** 110, 0.0), ("e4m3", 1.0, 2.0 ** 110, 0.0)])
+def test_scores_of_zero(kind, q_size, k_size, scale, s):
+    """A scale on the scores of zero, or so small that they are next to nothing: every visible key weighs the same, and those
+    behind the sequence nothing."""
+    n = 200
+    c = make_cache((n,), 1, 128, 16, kind, seed=61)
+    if kind == "e4m3":
+        c.k_scale *= k_size
+    else:
+        c.k *= k_size
+    q = queries(62, "bf16", s, 4, 128) * q_size
+    o, lse = run_decode(c, q, scale=scale)
+    pages, slot = c.page_table.cpu().numpy()[0][np.arange(n) // 16], np.arange(n) % 16
+    v = values_of(c.v)[pages, 0, slot] * (f64(c.v_scale)[pages, 0, slot][:, None] if kind == "e4m3" else 1.0)
+    weights = "f16" if kind == "e4m3" else "bf16"
+    # no rounding of a weight but its own and the scale's it holds; results to BF16
+    tol = (HALF_STEP[weights] + 2.0 ** -17) * np.abs(v).mean(0) + HALF_STEP["bf16"] * np.abs(v.mean(0)) * 1.01
+    assert (np.abs(f64(o)[0] - v.mean(0)) <= tol).all()
+    assert np.abs(f64(lse) - np.log(n)).max() <= 2.0 ** -17
+
+
+@pytest.mark.parametrize("s", [1, 20])
+def test_scores_of_zero_times_what_is_not_finite(s):
+    """Zero times an infinity of Q is a NaN, and no zero."""
+    c = make_cache((200,), 1, 128, 16, "bf16", seed=63)
+    q = queries(64, "bf16", s, 4, 128)
+    q[0, 1, s - 1, 5] = float("inf")
+    o, lse = run_decode(c, q, scale=0.0)
+    bad = torch.zeros(1, 4, s, dtype=torch.bool, device="cuda")
+    bad[0, 1, s - 1] = True
+    assert torch.isnan(lse[bad]).all() and torch.isnan(o[bad]).all()
+    assert torch.isfinite(lse[~bad]).all() and torch.isfinite(o[~bad]).all()
