@@ -435,11 +435,8 @@ class _Lazy:
         cls.int32, cls.int64, cls.float32 = torch.int32, torch.int64, torch.float32
         cls.words = (torch.int32, getattr(torch, "uint32", torch.int32))
         cls.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-        cls.torch = torch
-        try:
-            dtype_code(torch.empty(0, dtype=torch.float16))
-        except KeyError:      # pragma: no cover
-            pass
+        dtype_code(torch.empty(0, dtype=torch.float16))       # (fills the table of types)
+        cls.torch = torch        # last: what says that all of it is there, to other threads too
         return cls
 
 

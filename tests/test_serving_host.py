@@ -265,3 +265,37 @@ def test_oracle_attention_is_dense_attention():
         n = 19 + r
         p = np.exp(0.5 * k[:n] @ q[0, 0, r])
         assert np.allclose(o[0, 0, r], p @ v[:n] / p.sum()) and np.isclose(lse[0, 0, r], np.log(p.sum()))
+
+
+def test_first_calls_from_two_threads(m, monkeypatch):
+    """A call that comes while another thread's first one still looks up what it needs of torch finds all of it, too."""
+    import threading
+    q, table = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16), torch.zeros(32, dtype=torch.int64)
+    monkeypatch.setattr(m._Lazy, "torch", None)
+    monkeypatch.setattr(m, "_DTYPES", {})
+    look_up, inside, go = m.dtype_code, threading.Event(), threading.Event()
+
+    def slow(t):
+        if threading.current_thread().name == "first":
+            inside.set()
+            assert go.wait(30)
+        return look_up(t)
+
+    monkeypatch.setattr(m, "dtype_code", slow)
+    said = {}
+
+    def call():
+        try:
+            m.sdpa_rope_fwd(q, None, q, None, table)
+        except ValueError as e:
+            said[threading.current_thread().name] = str(e)
+
+    first = threading.Thread(target=call, name="first")
+    first.start()
+    assert inside.wait(30)
+    second = threading.Thread(target=call, name="second")
+    second.start()
+    second.join(30)
+    go.set()
+    first.join(30)
+    assert "CUDA" in said["second"] and "CUDA" in said["first"]      # the tensors are on the CPU; nothing else is wrong
