@@ -24,6 +24,10 @@
 //   O^T = V^T P^T wants pairs of keys in one register: a lane loads the same 16 bytes of two
 //   neighbouring keys and interleaves them with byte permutes.  P^T turns from one product's
 //   result layout to the other's operand layout by an 8x8 transposition (movmatrix).
+// A weight enters the second product as two 16-bit terms where results keep as many bits as one holds, so that O is
+// off by little more than its own rounding (131000 keys, BF16: 0.0017 of it, with one term 0.0023): beside the
+// reading the second MMA costs under 0.5%, with 16 rows 2%, with many blocks of them at d = 256 6%.  One term it is
+// for an E4M3 cache and BF16 results, whose rounding covers F16's, or 16 rows (8 to 13%).
 // (Query rows as the 16 rows instead cost twice the MMAs, exponentials and registers for groups
 // of up to 8 heads: 209 us against 92 us of reading at 32 sequences of 1K..16K tokens.)
 //
@@ -127,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
   using C = DecCfg<D, CT, NR>;
   constexpr bool E4 = CT == kE4M3;
   constexpr bool BF = CT == kBF16;           // type of the products' operands
+  constexpr bool TWO = !E4 || (QT == kF16 && NR == 1);   // weights as two terms
   constexpr int ROWS = C::ROWS, NT = C::NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
@@ -456,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
         }
       }
       // ---- weights, sums, P^T ------------------------------------------------------------------------
-      uint32_t pb[NR][2];
+      uint32_t pb[NR][2], pl[TWO ? NR : 1][2];
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -480,7 +485,14 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) pb[n][u] = transpose8x8(pack_pair<BF>(s[n][2 * u], s[n][2 * u + 1]));
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t w = pack_pair<BF>(s[n][2 * u], s[n][2 * u + 1]);
+          pb[n][u] = transpose8x8(w);
+          if constexpr (TWO) {
+            const float2 f = unpack_pair<BF>(w);
+            pl[n][u] = transpose8x8(pack_pair<BF>(s[n][2 * u] - f.x, s[n][2 * u + 1] - f.y));
+          }
+        }
 
       // ---- O^T += V^T P^T; lane's part of a value: d = (8 j + g) * EPV + 0 .. EPV - 1 --------------------
       auto product = [&](auto clear) {
@@ -519,7 +531,10 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
               for (int h = 0; h < 4; ++h) a[h] = finite_pair<BF>(a[h], found);
             }
 #pragma unroll
-            for (int n = 0; n < NR; ++n) mma16816<BF>(o[n][(j * C::EPV + x) / 2], a[0], a[1], a[2], a[3], pb[n][0], pb[n][1]);
+            for (int n = 0; n < NR; ++n) {
+              mma16816<BF>(o[n][(j * C::EPV + x) / 2], a[0], a[1], a[2], a[3], pb[n][0], pb[n][1]);
+              if constexpr (TWO) mma16816<BF>(o[n][(j * C::EPV + x) / 2], a[0], a[1], a[2], a[3], pl[n][0], pl[n][1]);
+            }
           }
         }
       };

@@ -204,3 +204,30 @@ def test_scores_of_zero_times_what_is_not_finite(s):
     bad[0, 1, s - 1] = True
     assert torch.isnan(lse[bad]).all() and torch.isnan(o[bad]).all()
     assert torch.isfinite(lse[~bad]).all() and torch.isfinite(o[~bad]).all()
+
+
+@pytest.mark.parametrize("kind,dtype,s,h_q,d", [("bf16", "bf16", 1, 8, 128), ("bf16", "bf16", 4, 3, 64), ("bf16", "bf16", 1, 2, 256),
+                                                ("f16", "f16", 1, 4, 128), ("f16", "f16", 4, 4, 256), ("e4m3", "f16", 1, 8, 128)])
+@pytest.mark.parametrize("columns", [None, 4096])
+def test_weights_of_few_rows_are_held_in_two_terms(kind, dtype, s, h_q, d, columns):
+    """O within the rounding of its store and of weights to twice the bits of one term (half a step of half a step).
+
+    The rest: scores as in check(); with |q k| scale below 2^5 a weight's exponent is off by under 2^-18, ex2 and sums by
+    2^-20, F16's least step by 2^-25 of weights of 2^6 (all keys together: 2^-20)."""
+    n = 1500
+    c = make_cache((n,), 1, d, 16, kind, seed=65, wide=columns)
+    q = queries(66, dtype, s, h_q, d)
+    o, _ = run_decode(c, q)
+    pages, slot = c.page_table.cpu().numpy()[0][np.arange(n) // 16], np.arange(n) % 16
+    by = (lambda t: f64(t)[pages, 0, slot][:, None]) if kind == "e4m3" else (lambda t: 1.0)
+    k, v = values_of(c.k)[pages, 0, slot] * by(c.k_scale), values_of(c.v)[pages, 0, slot] * by(c.v_scale)
+    rows = f64(q)[0].reshape(-1, d)
+    x = rows @ k.T * d ** -0.5
+    assert np.abs(x).max() < 32
+    p = np.exp(x - x.max(-1, keepdims=True))
+    p /= p.sum(-1, keepdims=True)
+    score = d / 16 * 2.0 ** -21 * (d ** -0.5 * (np.abs(rows) @ np.abs(k).T)).max(-1, keepdims=True)
+    want, spread = p @ v, p @ np.abs(v)
+    two = HALF_STEP["bf16" if kind == "bf16" else "f16"] ** 2
+    tol = (two + score + 2.0 ** -17) * spread + HALF_STEP[dtype] * np.abs(want) * 1.01 + TINY[dtype]
+    assert (np.abs(f64(o)[0].reshape(want.shape) - want) <= tol).all()
