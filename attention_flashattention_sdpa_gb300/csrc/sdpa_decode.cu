@@ -24,12 +24,13 @@
 //   O^T = V^T P^T wants pairs of keys in one register: a lane loads the same 16 bytes of two
 //   neighbouring keys and interleaves them with byte permutes.  P^T turns from one product's
 //   result layout to the other's operand layout by an 8x8 transposition (movmatrix).
-// A weight enters the second product as two 16-bit terms where results keep as many bits as one holds, so that O is
-// off by little more than its own rounding (131000 keys, BF16: 0.0017 of it, with one term 0.0023): beside the
-// reading the second MMA costs under 0.5%, with 16 rows 2%, with many blocks of them at d = 256 6%.  One term it is
-// for an E4M3 cache and BF16 results, whose rounding covers F16's, or 16 rows (8 to 13%).
 // (Query rows as the 16 rows instead cost twice the MMAs, exponentials and registers for groups
 // of up to 8 heads: 209 us against 92 us of reading at 32 sequences of 1K..16K tokens.)
+//
+// In blocks of 8 rows a weight enters the second product as two 16-bit terms where results keep as many bits as
+// one holds, so that O is off by little more than its own rounding (131000 keys, BF16: 0.0017 of it, with one
+// term 0.0023): beside the reading the second MMA costs under 0.5%.  One term it is for an E4M3 cache and BF16
+// results, whose rounding covers F16's, and for blocks of 16 rows, which it would slow by 2% (BF16, d = 128) to 13%.
 //
 // E4M3 caches: codes widen exactly to F16; a key's scale multiplies its score, and the scale of
 // its value, over 2^v, its weight: w = 2^(s - m) vs / 2^v, O = 2^v sum w v_code / l, l = sum 2^(s - m).  2^v is a running
@@ -40,7 +41,7 @@
 // 2^-31 448 2^v times the row's largest weight: far below E4M3's own rounding of the row with that scale.
 //
 // Measured, groups of 8 heads, d = 128: 32 sequences of 1000 to 16384 tokens, E4M3, 110 us (5.65 TB/s, 83%
-// of a copy; BF16 131000 tokens of one sequence 86 us, 6.25 TB/s, 92%); 1000 tokens of one sequence 6.9 us, of
+// of a copy; BF16 131000 tokens of one sequence 86 us, 6.25 TB/s, 92%); 1000 tokens of one sequence 7.0 us, of
 // which reading is 0.6: the launch, a load's latency for the lengths, the page and the keys, the cluster.
 #include <type_traits>
 
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, DecCfg<D, CT, NR>::CTAS) decode_kern
   using C = DecCfg<D, CT, NR>;
   constexpr bool E4 = CT == kE4M3;
   constexpr bool BF = CT == kBF16;           // type of the products' operands
-  constexpr bool TWO = !E4 || (QT == kF16 && NR == 1);   // weights as two terms
+  constexpr bool TWO = NR == 1 && (!E4 || QT == kF16);   // weights as two terms
   constexpr int ROWS = C::ROWS, NT = C::NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
@@ -806,8 +807,8 @@ int ctas_of_sm(int tile_rows, bool e4m3) {
 
 void decode_plan(DecodeParams* p, int d, int ct, int num_sms) {
   // Many rows: measured at 8 x 8192 tokens, 8 KV heads of 128, blocks of 8 or 16 rows against the wide
-  // ones: E4M3 65 us against 78 for 32 rows, 87 against 78 for 40; BF16 62 against 58 for 24 (d = 64:
-  // E4M3 47 against 53, 63 against 53; BF16 42 against 38).
+  // ones: E4M3 66 us against 79 for 32 rows, 89 against 80 for 40; BF16 62 against 58 for 24 (d = 64:
+  // E4M3 48 against 55, 63 against 55; BF16 42 against 37).
   p->wide = d <= 128 && p->rows > (ct == kE4M3 ? 32 : 16);
   p->tile_rows = p->wide ? 256 : p->rows <= 8 ? 8 : 16;
   p->row_tiles = (p->rows + p->tile_rows - 1) / p->tile_rows;
@@ -836,9 +837,9 @@ void decode_plan(DecodeParams* p, int d, int ct, int num_sms) {
   // each sequence and block of rows, which join in shared memory and spare the second launch (about
   // the time of 10 tiles), where all of them fit on the GPU at once (clusters of CTAs that fill an SM
   // leave some SMs out) and no CTA gets more than 20 tiles, or 10 more than a team would.  Measured, clusters
-  // against teams, 32 heads over 8 of 128, BF16: 1 x 1000 tokens 6.9 against 7.2 us, 4 x 1000 8.1 against
-  // 9.9, 4 x 4000 16.4 against 19.8, 32 x 10..1000 19.3 against 22.1; 1 x 8000 14.8 against 13.6.  A call from
-  // Python, which pays for two launches, takes 11.5 us against 13.5.
+  // against teams, 32 heads over 8 of 128, BF16: 1 x 1000 tokens 7.0 against 7.2 us, 4 x 1000 8.2 against
+  // 9.7, 4 x 4000 16.6 against 19.5, 32 x 10..1000 19.5 against 22.1; 1 x 8000 14.8 against 13.6.  A call from
+  // Python, which pays for two launches, takes 11 us against 13.
   p->cluster = 0;
   if (!p->wide) {
     const long long cap = (p->c.max_len + keys - 1) / keys, units = static_cast<long long>(p->c.b) * blocks;

@@ -26,12 +26,17 @@
 // and rows lost the keys beside a drafted one with a scale 2^20 times theirs, hidden or not.  K times
 // its scale in F16 left the scores off by 2^-12 of themselves, which the LSE shows.)
 //
+// Weights are rounded once, to the type of the products (BF16 8 bits: O of a BF16 cache is off by 0.0023 of itself
+// where its store alone gives 0.0017): a second term, as blocks of 8 rows in sdpa_decode.cu have it, would be half
+// as many tensor instructions again.
+//
 // Bound: the tensor cores (4 x 128 x 128 x d MMAs a block of two tiles) and the exponentials, as
 // the prompt's forward pass; reading the cache once bounds it for few rows.  Measured, 8 sequences of 4000
-// to 8192 tokens, trees of 64 tokens, 64 heads over 8 of 128: BF16 105 us (990 TFLOP/s), E4M3 152 (680; F16 results 137: the
-// warps that widen and the scales, 64 reads of 16 bytes a row and tile, share the schedulers and the shared
-// memory with the softmax, and K has one slot where BF16 has two).  35 to
-// 45 us of either are the first fetch of the code, Q, the last results and the parts.
+// to 8192 tokens, trees of 64 tokens, 64 heads over 8 of 128: BF16 105 us (990 TFLOP/s), E4M3 153 (677; F16 results 137).  128
+// keys by 256 rows take 1.9 us over BF16, 2.5 to 2.6 over E4M3, of 1.13 of MMA (the warps that widen and the
+// scales, 64 reads of 16 bytes a row and tile, share the schedulers and the shared memory with the softmax,
+// and K has one slot where BF16 has two); 28 us of a call over BF16, 35 (F16 Q) and 47 (BF16 Q) over E4M3, are
+// the first fetch of the code, Q, the last results and the parts.
 #include <type_traits>
 
 #include "sdpa_decode.cuh"
