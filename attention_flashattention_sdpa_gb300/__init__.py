@@ -639,7 +639,9 @@ def sdpa_decode(q, k_cache, v_cache, page_table, seq_lens_kv, o, lse=None, *, wo
     causal: False, or "bottom_right".  tree_mask: int32 [b or 1, s_q, ceil(s_q/32)], bit j%32 of word j/32 of
     row i set where drafted token i sees drafted token j (itself among them); earlier positions are seen by
     all.  seq_lens_q: rows that take part (None: all).  workspace: sdpa_decode_workspace_size bytes, not
-    shared with a call that may run at the same time."""
+    shared with a call that may run at the same time.  The work is split by the page table's columns: with
+    ``page_table[:, :n]``, n pages for the longest sequence, short ones take one launch instead of two (a
+    workspace for the whole table will do)."""
     c, shape, n = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
     p = _decode(q, k_cache, shape, n, o, seq_lens_q, attn_scale, causal, tree_mask)
     lse_ptr = None if lse is None else _dense(lse, "lse", _Lazy.float32, q.shape[:3])

@@ -11,8 +11,9 @@
 namespace sdpa {
 
 // cos and sin (times the factor) of one pair at position `pos`.  The table holds the turns per
-// position as 64-bit binary fractions, so pos * table[i] modulo 2^64 is the angle's exact fraction
-// of a turn: no loss however far the position.  The nearest quarter turn is taken off in whole
+// position as 64-bit binary fractions, so pos * table[i] modulo 2^64 is the angle's fraction of a turn, with
+// nothing lost to its size (what an entry, computed in fp64, lacks counts pos times: 5e-7 radians at 2^30
+// radians); its upper 32 bits, 1.5e-9 radians each, go on.  The nearest quarter turn is taken off in whole
 // numbers as well.  The rest, at most pi/4, is x + dx: what the conversion to fp32 rounds off joins
 // again by sin(x + dx) = sin x + dx cos x.  The Taylor series end after x^9 (sin, off by 2e-9) and
 // x^10 (cos, off by 2e-10); the factor multiplies the 1 of cos and the x of sin without a rounding of
@@ -20,7 +21,7 @@ namespace sdpa {
 __device__ __forceinline__ void rope_angle(const RopeArgs& r, int64_t turns, int pos, float& c, float& s) {
   const uint64_t phase = static_cast<uint64_t>(turns) * static_cast<uint64_t>(static_cast<int64_t>(pos));
   const uint32_t top = static_cast<uint32_t>(phase >> 32);
-  const uint32_t quarter = (top + (1u << 29)) >> 30;                   // 0..4
+  const uint32_t quarter = (top + (1u << 29)) >> 30;                   // 0..3: a sum of 2^32 is 0 again
   const int32_t rest = static_cast<int32_t>(top - (quarter << 30));    // [-2^29, 2^29) of 2^32 a turn
   constexpr float kHi = 1.4629180792671596e-9f;                        // 2 pi / 2^32 as fp32, and what that leaves
   constexpr float kLo = static_cast<float>(1.4629180792671596e-9 - static_cast<double>(kHi));

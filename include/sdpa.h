@@ -284,7 +284,9 @@ typedef struct {
 /* Fills table[0 .. rot/2) (HOST memory; the caller copies it to the device) with the turns per
  * position of each pair as 64-bit binary fractions, table[i] = f_i / (2 pi) * 2^64 mod 2^64, and
  * *attn_factor (may be NULL) with the factor on the rotated values.  A position times such a
- * fraction, modulo 2^64, is the angle as an exact fraction of a turn however far the position. */
+ * fraction, modulo 2^64, is the angle as a fraction of a turn with nothing lost to its size; what the entry
+ * itself lacks (computed in fp64: within 2^-51 of it) counts as often as the position says, 5e-7
+ * radians at 2^30 radians. */
 SDPA_API sdpa_status_t sdpa_rope_table(const sdpa_rope_table_t* cfg, int64_t* table, float* attn_factor);
 
 /* Rotary positions of Q and K in one call. */
@@ -319,7 +321,7 @@ SDPA_API sdpa_status_t sdpa_rope_bwd(const sdpa_rope_t* p, const void* dq_out, c
  * slot j % page_size.  Keys and values are logical [num_pages][h_kv][page_size][d] views (the
  * fields b, h, s, d of the strides are page, head, slot, element), so a page may be stored
  * head-major or slot-major.  E4M3 caches have an fp32 scale >= 0 for each token and head:
- * value = code * scale. */
+ * value = code * scale; any such scale will do, zero and subnormal ones included. */
 typedef struct {
   int32_t num_pages;        /* >= 1 */
   int32_t page_size;        /* tokens of a page: a multiple of 16 */
@@ -327,7 +329,9 @@ typedef struct {
   int32_t d;                /* 64, 128 or 256 */
   int32_t dtype;            /* F16, BF16 or E4M3 */
   int32_t b;                /* sequences */
-  int32_t max_pages;        /* columns of the page table */
+  int32_t max_pages;        /* columns of the page table.  sdpa_decode splits its work by them, since lengths are
+                               on the device: a view narrowed to the batch's longest sequence (the stride stays)
+                               spares short sequences a launch and a large workspace */
   void* k;
   void* v;
   sdpa_strides_t k_strides, v_strides;
@@ -388,7 +392,10 @@ SDPA_API sdpa_status_t sdpa_decode_workspace_size(const sdpa_cache_t* c, const s
 
 /* O (and LSE when lse != NULL: fp32 [b][h_q][s_q] dense, natural log) of the new tokens over the
  * cache.  Rows with no visible key, and rows >= len_q, give O = 0 and LSE = -inf.  Values at
- * hidden positions may hold anything, NaN included.
+ * hidden positions may hold anything, NaN included.  LSE depends on Q and K alone, whatever V and its scales are.
+ * Weights are rounded once to the cache's 16-bit type (E4M3: F16), or kept to twice its bits where at most 8 rows
+ * share a KV head and results keep as many.  Over an E4M3 cache a key adds to O within 2^-19 of the largest
+ * V scale that the row sees times its largest weight, however small its own: far below that scale's own rounding.
  *   workspace: >= sdpa_decode_workspace_size bytes, 256-byte aligned; contents on entry do not matter. */
 SDPA_API sdpa_status_t sdpa_decode(const sdpa_cache_t* c, const sdpa_decode_t* p, const void* q, void* o,
                                    float* lse, void* workspace, size_t workspace_bytes, void* stream);

@@ -129,3 +129,19 @@ def test_workspace_is_as_large_as_said(lens, columns, s, h_q, h_kv, d, kind):
     assert (buf[:65536] == 0x5A).all() and (buf[65536 + n:] == 0x5A).all()
     o2, lse2 = run_decode(c, q, causal="bottom_right")
     assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("kind,s,h_q", [("e4m3", 1, 8), ("bf16", 1, 8), ("e4m3", 20, 8)])
+def test_a_view_of_the_page_table(kind, s, h_q):
+    """The first columns of a wide table, with the workspace of all of them."""
+    m, lens = lib(), (300, 17, 0)
+    c = make_cache(lens, 2, 128, PAGE, kind, seed=90, wide=2000)
+    q = bshd(91, "bf16", 3, h_q, s, 128)
+    ws = torch.empty(m.sdpa_decode_workspace_size(q, *c.where(), **c.scales()), dtype=torch.uint8, device="cuda")
+    c.page_table = c.page_table[:, :19]
+    assert c.page_table.stride(0) == 2000
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    m.sdpa_decode(q, *c.where(), o, lse, workspace=ws, **c.scales(), causal="bottom_right")
+    kv, vv, ks, vs, table = c.np()
+    ref = so.attend(f64(q), kv, vv, ks, vs, table, lens, None, 128 ** -0.5, True)
+    assert_attend_close(o, lse, ref, "bf16", "bf16" if kind == "bf16" else "f16", kv_rounding=kv_rounding(kind, s * h_q // 2, 128, "bf16"))

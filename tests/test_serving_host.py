@@ -299,3 +299,18 @@ def test_first_calls_from_two_threads(m, monkeypatch):
     go.set()
     first.join(30)
     assert "CUDA" in said["second"] and "CUDA" in said["first"]      # the tensors are on the CPU; nothing else is wrong
+
+
+@pytest.mark.parametrize("h_q,h_kv,s_q,d,dtype", [(8, 2, 1, 128, 1), (32, 8, 1, 128, 2), (64, 1, 4, 64, 1), (16, 16, 3, 256, 2),
+                                                  (64, 8, 64, 128, 2), (320, 40, 128, 128, 1), (8, 2, 70, 256, 1)])
+def test_a_workspace_for_more_columns_serves_fewer(m, h_q, h_kv, s_q, d, dtype):
+    before, n = 0, ctypes.c_size_t(0)
+    for columns in (1, 2, 3, 7, 16, 20, 21, 60, 100, 500, 2048, 40000):
+        st = m.Strides(h_kv * 64 * d, 64 * d, d, 1)
+        scales = dict(k_scale=FAKE, v_scale=FAKE) if dtype == 2 else {}
+        c = _cache(m, page_size=64, h_kv=h_kv, d=d, dtype=dtype, b=3, max_pages=columns, page_table_stride=columns, k_strides=st,
+                   v_strides=st, **scales)
+        e = _decode(m, h_q=h_q, s_q=s_q, dtype=1)
+        assert m.lib.sdpa_decode_workspace_size(ctypes.addressof(c), ctypes.addressof(e), ctypes.byref(n)) == 0
+        assert n.value >= before
+        before = n.value
