@@ -396,6 +396,8 @@ SDPA_API sdpa_status_t sdpa_decode_workspace_size(const sdpa_cache_t* c, const s
  * Weights are rounded once to the cache's 16-bit type (E4M3: F16), or kept to twice its bits where at most 8 rows
  * share a KV head and results keep as many.  Over an E4M3 cache a key adds to O within 2^-19 of the largest
  * V scale that the row sees times its largest weight, however small its own: far below that scale's own rounding.
+ * Scores keep their fractions up to 2^24 (fp32); as in sdpa_fwd, rows with scores of 10^7 (F16, E4M3) or 10^9 (BF16)
+ * and more may come out as NaN where more than 16 rows share a KV head (E4M3: 32).
  *   workspace: >= sdpa_decode_workspace_size bytes, 256-byte aligned; contents on entry do not matter. */
 SDPA_API sdpa_status_t sdpa_decode(const sdpa_cache_t* c, const sdpa_decode_t* p, const void* q, void* o,
                                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
