@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from sdpa_testlib import f64
-from serving_testlib import DT, HALF_STEP, TINY, kv_rounding, make_cache, randn, run_decode, values_of
+from serving_testlib import DT, HALF_STEP, TINY, make_cache, randn, run_decode, values_of
 
 pytestmark = pytest.mark.gpu
 
@@ -31,22 +31,16 @@ def definition(c, n, q, scale):
 
 def check(c, n, q, dtype, o, lse, scale):
     """The bounds of assert_attend_close with the scores' error written out (d / 16 steps of a tensor core's sum, each off
-    by 2^-21 of reach; ex2, log2 and up to 32 moves of the reference: 2^-17), and what F16 operands of the
-    products add where the scales of V differ much.
-
-    Blocks of many rows: V's F16 elements are code * f, f = scale / 2^E < 128 with the tile's largest scale at 64 2^E or
-    more.  Below F16's normal range f is off by half of its least step, 2^-25, the element by 448 times that and half
-    a step of its own: under 2^-16 of 2^E, 2^-22 of the tile's largest scale, times the key's weight.  Weights of both
-    kernels: off by half of F16's least step, 2^-25, where the largest of a row is 2^5 or more (an offset of 2^6, an
-    integer reference) and 2^E is up to a 32nd of the largest scale while f < 128, so by 2^-27 of the largest weight
-    times the largest scale, times the code."""
+    by 2^-21 of reach; ex2, log2 and up to 32 moves of the reference: 2^-17), and what F16 weights add where the
+    scales of V differ much: a weight times its scale over 2^v is off by half of F16's least step, 2^-25, where the
+    row's largest weight is 2^5 or more (an offset of 2^6, an integer reference) and 2^v up to four times the largest
+    scale, so by 2^-28 of the largest weight times the largest scale, times the code."""
     p, L, codes, vs, reach = definition(c, n, q, scale)
     v = codes * vs[:, None]
     want, spread = p @ v, p @ np.abs(v)
-    rows, d = q.shape[1] * q.shape[2], q.shape[3]
-    score = d / 16 * 2.0 ** -21 * reach
-    extra = vs.max() * (2.0 ** -22 + 2.0 ** -27 * p.max(-1, keepdims=True) * np.abs(codes).sum(0))
-    tol = (HALF_STEP["f16"] + 2.0 ** -17 + score.max(-1, keepdims=True) + kv_rounding("e4m3", rows, d, dtype)) * spread + extra + \
+    score = q.shape[3] / 16 * 2.0 ** -21 * reach
+    extra = vs.max() * 2.0 ** -28 * p.max(-1, keepdims=True) * np.abs(codes).sum(0)
+    tol = (HALF_STEP["f16"] + 2.0 ** -17 + score.max(-1, keepdims=True)) * spread + extra + \
         HALF_STEP[dtype] * np.abs(want) * 1.01 + TINY[dtype]
     got = f64(o)[0].reshape(want.shape)
     assert np.isfinite(got).all(), "O is not finite"
