@@ -501,7 +501,7 @@ def _verify(st):
         twin = (up.unsqueeze(2) == up.unsqueeze(1)) & drafted & drafted.unsqueeze(1)
         same = (twin & (tokens.unsqueeze(2) == tokens.unsqueeze(1))).tril(-1).any(2)
         mass = torch.where(same, 0, mass)
-        left = int(UNIT) - (twin.tril(-1) * mass.unsqueeze(1)).sum(2)
+        left = (int(UNIT) - (twin.tril(-1) * mass.unsqueeze(1)).sum(2)).clamp_min(0)
         good = u * left.double() < mass.double()
         good &= ~(twin & good.unsqueeze(1)).tril(-1).any(2)                    # an earlier sibling was taken
     good |= ~drafted
@@ -656,7 +656,7 @@ def _verify64(st):
                 if st["draft_probs"] is not None:
                     good = uniform[i][j] * float(st["draft_probs"][i, j, row[j]]) < p
                 else:
-                    left = int(UNIT) - sum(whole(float(st["probs"][i, n, x])) for x in set(gone))
+                    left = max(0, int(UNIT) - sum(whole(float(st["probs"][i, n, x])) for x in set(gone)))
                     good = uniform[i][j] * left < (0 if row[j] in gone else whole(p))
                 if good:
                     step = j
