@@ -5,7 +5,8 @@ kernels of ``libsdpa_gb300.so``.  PyTorch supplies device memory and the current
 The binding keeps the C names: :func:`sdpa_fwd`, :func:`sdpa_bwd`,
 :func:`sdpa_workspace_size`, :func:`sdpa_last_error_string`, :func:`sdpa_device_error`; for serving
 :func:`sdpa_rope_fwd`, :func:`sdpa_rope_bwd`, :func:`sdpa_cache_write`, :func:`sdpa_cache_read` and
-:func:`sdpa_decode`.
+:func:`sdpa_decode`; around them :func:`sdpa_cache_fork`, :func:`sdpa_cache_grow`, :func:`sdpa_cache_free`,
+:func:`sdpa_cache_compact`, :func:`sdpa_cache_copy`, :func:`sdpa_cache_keep` and :func:`sdpa_verify`.
 
 Importing this package loads the library and raises ``ImportError`` if it has not been
 built (``python -m attention_flashattention_sdpa_gb300._build``); there is no fallback.
@@ -23,9 +24,10 @@ __all__ = [
     "sdpa_workspace_size", "sdpa_fwd", "sdpa_bwd", "sdpa_last_error_string", "causal_code",
     "sdpa_device_error", "sdpa_version", "sdpa_bwd_noalloc", "NOALLOC_SCRATCH_BYTES", "STATUS",
     "sdpa_dropout_mask_size", "sdpa_dropout_mask",
-    "RopeTable", "Rope", "Cache", "CacheRows", "Decode", "sdpa_rope_table", "sdpa_rope_fwd",
-    "sdpa_rope_bwd", "sdpa_cache_write", "sdpa_cache_read", "sdpa_decode",
-    "sdpa_decode_workspace_size",
+    "RopeTable", "Rope", "Cache", "CacheRows", "Decode", "RopeAxes", "sdpa_rope_table", "sdpa_rope_axes",
+    "sdpa_rope_fwd", "sdpa_rope_bwd", "sdpa_cache_write", "sdpa_cache_read", "sdpa_decode",
+    "sdpa_decode_workspace_size", "Pages", "Verify", "sdpa_cache_fork", "sdpa_cache_grow", "sdpa_cache_free",
+    "sdpa_cache_compact", "sdpa_cache_copy", "sdpa_cache_keep", "sdpa_verify",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsdpa_gb300.so")
@@ -34,7 +36,7 @@ STATUS = {0: "SDPA_OK", 1: "SDPA_ERR_INVALID_ARG", 2: "SDPA_ERR_UNSUPPORTED",
           3: "SDPA_ERR_LAYOUT", 4: "SDPA_ERR_WORKSPACE", 5: "SDPA_ERR_CUDA",
           6: "SDPA_ERR_TIMEOUT"}
 
-DTYPE_F16, DTYPE_BF16, DTYPE_E4M3, DTYPE_E5M2 = 0, 1, 2, 3
+DTYPE_F16, DTYPE_BF16, DTYPE_E4M3, DTYPE_E5M2, DTYPE_F32 = 0, 1, 2, 3, 4
 
 
 class SdpaError(RuntimeError):
@@ -88,6 +90,10 @@ class Rope(ctypes.Structure):
     ]
 
 
+class RopeAxes(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * 256), ("axis_stride", ctypes.c_int64)]
+
+
 class Cache(ctypes.Structure):
     _fields_ = [
         ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("h_kv", ctypes.c_int32),
@@ -115,6 +121,25 @@ class Decode(ctypes.Structure):
     ]
 
 
+class Pages(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("b", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p), ("page_table_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p),
+        ("ref_counts", ctypes.c_void_p), ("page_table_out", ctypes.c_void_p), ("page_table_out_stride", ctypes.c_int64),
+        ("ref_counts_out", ctypes.c_void_p),
+    ]
+
+
+class Verify(ctypes.Structure):
+    _fields_ = [
+        ("b", ctypes.c_int32), ("s", ctypes.c_int32), ("vocab", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("tokens", ctypes.c_void_p), ("parents", ctypes.c_void_p), ("seq_lens_q", ctypes.c_void_p),
+        ("uniform", ctypes.c_void_p), ("probs", ctypes.c_void_p), ("probs_b", ctypes.c_int64), ("probs_s", ctypes.c_int64),
+        ("draft_probs", ctypes.c_void_p), ("draft_b", ctypes.c_int64), ("draft_s", ctypes.c_int64),
+        ("accepted", ctypes.c_void_p), ("path", ctypes.c_void_p), ("new_tokens", ctypes.c_void_p),
+    ]
+
+
 def _packer(cls=Problem):
     """One struct.Struct that lays out a whole ctypes structure at the offsets ctypes gives it, so
     that it is marshalled by a single pack instead of one ctypes assignment per field."""
@@ -125,6 +150,8 @@ def _packer(cls=Problem):
         fmt.append("x" * (off - pos))
         if typ is Strides:
             fmt.append("qqqq")
+        elif typ is ctypes.c_uint8 * 256:
+            fmt.append("256s")
         else:
             fmt.append(codes[typ])
         pos = off + ctypes.sizeof(typ)
@@ -136,6 +163,7 @@ def _packer(cls=Problem):
 
 _PACK = _packer()
 _PACK_ROPE, _PACK_CACHE, _PACK_ROWS, _PACK_DECODE = (_packer(c).pack for c in (Rope, Cache, CacheRows, Decode))
+_PACK_AXES, _PACK_PAGES, _PACK_VERIFY = (_packer(c).pack for c in (RopeAxes, Pages, Verify))
 _NO_STRIDES = (0, 0, 0, 1)
 _NO_ROPE_STRIDES = 4 * _NO_STRIDES
 
@@ -181,15 +209,25 @@ def _load():
     # The serving structs are handed over as packed bytes.
     L.sdpa_rope_table.argtypes = [VP, VP, ctypes.POINTER(ctypes.c_float)]
     L.sdpa_rope_fwd.argtypes = L.sdpa_rope_bwd.argtypes = [VP, VP, VP, VP, VP, VP]
+    L.sdpa_rope_axes_fwd.argtypes = L.sdpa_rope_axes_bwd.argtypes = [VP, VP, VP, VP, VP, VP, VP]
+    L.sdpa_cache_write_axes.argtypes = [VP, VP, VP, VP, VP, VP]
+    L.sdpa_cache_fork.argtypes = [VP, VP, ctypes.c_int32, VP, VP]
+    L.sdpa_cache_grow.argtypes = [VP, VP, VP, VP, VP, VP]
+    L.sdpa_cache_free.argtypes = [VP, VP, VP]
+    L.sdpa_cache_compact.argtypes = L.sdpa_cache_copy.argtypes = [VP, VP, VP, ctypes.c_int32, VP]
+    L.sdpa_cache_keep.argtypes = [VP, VP, VP, ctypes.c_int32, VP, VP]
+    L.sdpa_verify.argtypes = [VP, VP]
     L.sdpa_cache_write.argtypes = L.sdpa_cache_read.argtypes = [VP, VP, VP, VP, VP]
     L.sdpa_decode_workspace_size.argtypes = [VP, VP, ctypes.POINTER(SZ)]
     L.sdpa_decode.argtypes = [VP, VP, VP, VP, VP, VP, SZ, VP]
     for f in (L.sdpa_rope_table, L.sdpa_rope_fwd, L.sdpa_rope_bwd, L.sdpa_cache_write, L.sdpa_cache_read,
-              L.sdpa_decode_workspace_size, L.sdpa_decode):
+              L.sdpa_decode_workspace_size, L.sdpa_decode, L.sdpa_rope_axes_fwd, L.sdpa_rope_axes_bwd, L.sdpa_cache_write_axes,
+              L.sdpa_cache_fork, L.sdpa_cache_grow, L.sdpa_cache_free, L.sdpa_cache_compact, L.sdpa_cache_copy, L.sdpa_cache_keep,
+              L.sdpa_verify):
         f.restype = ctypes.c_int
     L.sdpa_serving_struct_size.argtypes = [ctypes.c_int]
     L.sdpa_serving_struct_size.restype = SZ
-    for i, cls in enumerate((RopeTable, Rope, Cache, CacheRows, Decode)):
+    for i, cls in enumerate((RopeTable, Rope, Cache, CacheRows, Decode, RopeAxes, Pages, Verify)):
         if L.sdpa_serving_struct_size(i) != ctypes.sizeof(cls):
             raise ImportError(f"{cls.__name__}: layout mismatch between the library and the binding")
     if L.sdpa_problem_struct_size() != ctypes.sizeof(Problem):
@@ -420,6 +458,22 @@ def sdpa_rope_table(rot: int, base: float = 10000.0, *, scaling: str = "none", f
     return out.to(device), att.value
 
 
+def sdpa_rope_axes(sections, *, order: str = "blocks") -> bytes:
+    """The axis of each pair of a rotation with several axes, for ``axes=`` of the calls below: ``sections`` gives the number of
+    pairs of each axis (1 to 4 axes).  ``order``: "blocks" (the first axis's pairs, then the second's, ...), or "interleaved"
+    (dealt out in turns to the axes that still want one).  Any other order is as good: one byte a pair, its axis.
+
+    The frequencies are the table's, pair by pair; for axes with frequencies of their own, ``torch.cat`` of a table of each."""
+    sections = [int(n) for n in sections]
+    if not 1 <= len(sections) <= 4 or min(sections) < 1:
+        raise ValueError(f"sections are the pairs of 1 to 4 axes, one at least each, got {sections}")
+    if order == "blocks":
+        return bytes(a for a, n in enumerate(sections) for _ in range(n))
+    if order == "interleaved":
+        return bytes(a for turn in range(max(sections)) for a, n in enumerate(sections) if turn < n)
+    raise ValueError(f"unknown order {order!r}")
+
+
 def _bad(message: str):
     raise ValueError(message)
 
@@ -433,6 +487,7 @@ class _Lazy:
     def load(cls):
         import torch
         cls.int32, cls.int64, cls.float32 = torch.int32, torch.int64, torch.float32
+        cls.probs = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
         cls.words = (torch.int32, getattr(torch, "uint32", torch.int32))
         cls.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         dtype_code(torch.empty(0, dtype=torch.float16))       # (fills the table of types)
@@ -484,13 +539,27 @@ def _positions(positions, b: int, s: int):
     return positions.data_ptr(), 0 if len(shape) == 1 or (shape[0] == 1 and b > 1) else stride[0]
 
 
+def _axis_positions(positions, axes, rot: int, b: int, s: int):
+    """(address, elements between batches, packed axes) of positions [axes, b, s], or [axes, s] or [axes, 1, s] for every
+    batch."""
+    if type(axes) is not bytes or len(axes) != rot // 2:
+        raise ValueError(f"axes must be bytes, the axis of each of rot/2 = {rot // 2} pairs")
+    if positions is None or positions.dtype is not _Lazy.int32:
+        raise ValueError("axes need int32 positions")
+    shape, stride = positions.shape, positions.stride()
+    if len(shape) not in (2, 3) or shape[1:] not in ((b, s), (1, s), (s,)) or (s > 1 and stride[-1] != 1):
+        raise ValueError(f"positions must be of shape (axes, {b}, {s}), (axes, 1, {s}) or (axes, {s}) with a unit last stride")
+    return (positions.data_ptr(), 0 if len(shape) == 2 or (shape[1] == 1 and b > 1) else stride[1],
+            _PACK_AXES(shape[0], axes, stride[0]))
+
+
 def _table(t, name: str):
     if t.dtype is not _Lazy.int64 or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be the int64 tensor of sdpa_rope_table")
     return t.data_ptr(), 2 * t.shape[0]
 
 
-def _rope(fn, q, k, q_out, k_out, table, positions, interleaved, attn_factor, stream):
+def _rope(fn, fn_axes, q, k, q_out, k_out, table, positions, interleaved, attn_factor, axes, stream):
     if _Lazy.torch is None:
         _Lazy.load()
     shape = q.shape
@@ -512,27 +581,35 @@ def _rope(fn, q, k, q_out, k_out, table, positions, interleaved, attn_factor, st
         h_k, k_ptr, k_out_ptr, k_st, k_out_st = ks[1], k.data_ptr(), k_out.data_ptr(), k.stride(), k_out.stride()
     dt = _code(q, "q")
     tab, rot = _table(table, "table")
-    pos, pos_stride = _positions(positions, b, s)
+    if axes is None:
+        pos, pos_stride = _positions(positions, b, s)
+    else:
+        pos, pos_stride, several = _axis_positions(positions, axes, rot, b, s)
     dev = _same_device(q, k, q_out, k_out, table, positions)
     p = _PACK_ROPE(b, h_q, h_k, s, d, rot, dt, 1 if interleaved else 0, attn_factor, tab, pos, pos_stride, *q.stride(), *k_st,
                    *q_out.stride(), *k_out_st)
-    _launch(fn, stream, q, dev, p, q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr)
+    if axes is None:
+        _launch(fn, stream, q, dev, p, q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr)
+    else:
+        _launch(fn_axes, stream, q, dev, p, several, q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr)
 
 
 def sdpa_rope_fwd(q, k, q_out, k_out, table, positions=None, *, interleaved: bool = False,
-                  attn_factor: float = 1.0, stream=None) -> None:
+                  attn_factor: float = 1.0, axes: Optional[bytes] = None, stream=None) -> None:
     """Rotary positions of Q and K ([b, h, s, d] views, f16/bf16) into q_out and k_out, which may be q
     and k themselves; ``k`` and ``k_out`` may be None.
 
     table: int64 CUDA tensor of :func:`sdpa_rope_table` (rot = twice its length; the elements of a head
-    behind rot are copied).  positions: int32 [b, s] or [s], or None: 0, 1, ... in every batch."""
-    _rope(lib.sdpa_rope_fwd, q, k, q_out, k_out, table, positions, interleaved, attn_factor, stream)
+    behind rot are copied).  positions: int32 [b, s] or [s], or None: 0, 1, ... in every batch.
+    axes: None, or the axis of each pair (:func:`sdpa_rope_axes`); positions are then int32 [axes, b, s] or [axes, s], and
+    pair i turns by the position on its own axis."""
+    _rope(lib.sdpa_rope_fwd, lib.sdpa_rope_axes_fwd, q, k, q_out, k_out, table, positions, interleaved, attn_factor, axes, stream)
 
 
 def sdpa_rope_bwd(dq_out, dk_out, dq, dk, table, positions=None, *, interleaved: bool = False,
-                  attn_factor: float = 1.0, stream=None) -> None:
+                  attn_factor: float = 1.0, axes: Optional[bytes] = None, stream=None) -> None:
     """Gradients of :func:`sdpa_rope_fwd`: dq, dk (overwritten) from the gradients of its outputs."""
-    _rope(lib.sdpa_rope_bwd, dq_out, dk_out, dq, dk, table, positions, interleaved, attn_factor, stream)
+    _rope(lib.sdpa_rope_bwd, lib.sdpa_rope_axes_bwd, dq_out, dk_out, dq, dk, table, positions, interleaved, attn_factor, axes, stream)
 
 
 def _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale):
@@ -564,28 +641,35 @@ def _cache_rows(k, v, k_cache, shape, n: int):
 
 def sdpa_cache_write(k, v, k_cache, v_cache, page_table, seq_lens_kv, *, seq_lens_q=None, k_scale=None,
                      v_scale=None, rope_table=None, positions=None, interleaved: bool = False,
-                     attn_factor: float = 1.0, stream=None) -> None:
+                     attn_factor: float = 1.0, axes: Optional[bytes] = None, stream=None) -> None:
     """Writes the new rows k, v ([b, h_kv, s, d], f16/bf16) into a paged cache.
 
     k_cache, v_cache: [pages, h_kv, page_size, d] views (f16, bf16 or float8_e4m3fn; E4M3 needs k_scale and
     v_scale, fp32 [pages, h_kv, page_size]).  page_table: int32 [b, max_pages]; seq_lens_kv: int32 [b] tokens
     of each sequence with these; seq_lens_q: int32 [b] of them new (None: s).  Row i goes to position
-    len_kv - len_q + i.  With ``rope_table`` K is rotated first (positions None: each row's position)."""
+    len_kv - len_q + i.  With ``rope_table`` K is rotated first (positions None: each row's position; with ``axes`` as in
+    :func:`sdpa_rope_fwd`)."""
     c, shape, n = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
     b, _, s, _ = _cache_rows(k, v, k_cache, shape, n)
     lens_q = 0 if seq_lens_q is None else _dense(seq_lens_q, "seq_lens_q", _Lazy.int32, (b,))
     at = 0
     if rope_table is not None:
         tab, rot = _table(rope_table, "rope_table")
-        pos, pos_stride = _positions(positions, b, s)
+        if axes is None:
+            pos, pos_stride = _positions(positions, b, s)
+        else:
+            pos, pos_stride, several = _axis_positions(positions, axes, rot, b, s)
         rope = Rope.from_buffer_copy(_PACK_ROPE(0, 0, 0, 0, 0, rot, 0, 1 if interleaved else 0, attn_factor, tab, pos, pos_stride,
                                                 *_NO_ROPE_STRIDES))
         at = ctypes.addressof(rope)
-    elif positions is not None:
-        raise ValueError("positions are those of a rope_table")
+    elif positions is not None or axes is not None:
+        raise ValueError("positions and axes are those of a rope_table")
     dev = _same_device(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale, k, v, seq_lens_q, rope_table, positions)
     r = _PACK_ROWS(s, _code(k, "k"), *k.stride(), *v.stride(), lens_q, at)
-    _launch(lib.sdpa_cache_write, stream, k_cache, dev, c, r, k.data_ptr(), v.data_ptr())
+    if axes is None:
+        _launch(lib.sdpa_cache_write, stream, k_cache, dev, c, r, k.data_ptr(), v.data_ptr())
+    else:
+        _launch(lib.sdpa_cache_write_axes, stream, k_cache, dev, c, r, several, k.data_ptr(), v.data_ptr())
 
 
 def sdpa_cache_read(k_cache, v_cache, page_table, seq_lens_kv, k, v, *, k_scale=None, v_scale=None,
@@ -650,3 +734,163 @@ def sdpa_decode(q, k_cache, v_cache, page_table, seq_lens_kv, o, lse=None, *, wo
     dev = _same_device(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale, q, o, seq_lens_q, tree_mask, lse, workspace)
     _launch(lib.sdpa_decode, stream, k_cache, dev, c, p, q.data_ptr(), o.data_ptr(), lse_ptr, workspace.data_ptr(),
             workspace.numel() * workspace.element_size())
+
+
+# ---- pages: who owns which, and pages and rows moved ------------------------------------------
+
+def _page_table(t, name: str, shape=None):
+    """(address, shape, elements between rows) of an int32 page table with a unit last stride."""
+    ts, st = t.shape, t.stride()
+    if len(ts) != 2 or t.dtype is not _Lazy.int32 or (ts[1] > 1 and st[1] != 1) or (shape is not None and ts != shape):
+        raise ValueError(f"{name} must be int32 {'[b, max_pages]' if shape is None else tuple(shape)} with a unit last stride")
+    return t.data_ptr(), ts, st[0]
+
+
+def _pages(page_table, seq_lens, ref_counts, table_out, refs_out, page_size, b_out=None):
+    """The packed descriptor and the number of rows; outputs that are None are the inputs."""
+    if _Lazy.torch is None:
+        _Lazy.load()
+    at, shape, stride = _page_table(page_table, "page_table")
+    lens = _dense(seq_lens, "seq_lens", _Lazy.int32, shape[:1])
+    if ref_counts.dim() != 1:
+        raise ValueError("ref_counts must be int32 [num_pages]")
+    n = ref_counts.shape
+    refs = _dense(ref_counts, "ref_counts", _Lazy.int32, n)
+    out_at, out_stride, refs_at = at, stride, refs
+    if table_out is not None:
+        out_at, _, out_stride = _page_table(table_out, "page_table_out", shape if b_out is None else (b_out, shape[1]))
+    if refs_out is not None:
+        refs_at = _dense(refs_out, "ref_counts_out", _Lazy.int32, n)
+    return _PACK_PAGES(n[0], page_size, shape[0], shape[1], at, stride, lens, refs, out_at, out_stride, refs_at), shape[0]
+
+
+def _pairs(src, dst):
+    """Addresses and length of a list of pages."""
+    if src.dim() != 1:
+        raise ValueError("src and dst must be int32 of one dimension")
+    return _dense(src, "src", _Lazy.int32, src.shape), _dense(dst, "dst", _Lazy.int32, src.shape), src.shape[0]
+
+
+def sdpa_cache_fork(page_table, seq_lens, parents, ref_counts, page_table_out, seq_lens_out, ref_counts_out=None, *,
+                    page_size: int, stream=None) -> None:
+    """Row i of ``page_table_out`` (int32 [b_out, max_pages]) takes over sequence ``parents[i]`` (int32 [b_out]; outside
+    0..b-1: none) of ``page_table`` with its pages, shared, and its length (``seq_lens_out``: int32 [b_out]).  Old rows
+    that nobody takes over are freed.
+
+    ref_counts: int32 [num_pages] owners of each page, updated into ref_counts_out (None: in place)."""
+    if parents.dim() != 1:
+        raise ValueError("parents must be int32 [b_out]")
+    n = parents.shape[0]
+    p, _ = _pages(page_table, seq_lens, ref_counts, page_table_out, ref_counts_out, page_size, n)
+    parents_at = _dense(parents, "parents", _Lazy.int32, (n,))
+    lens_at = _dense(seq_lens_out, "seq_lens_out", _Lazy.int32, (n,))
+    dev = _same_device(page_table, seq_lens, parents, ref_counts, page_table_out, seq_lens_out, ref_counts_out)
+    _launch(lib.sdpa_cache_fork, stream, page_table, dev, p, parents_at, n, lens_at)
+
+
+def sdpa_cache_grow(page_table, seq_lens, new_lens, ref_counts, src, dst, missing, *, page_size: int, page_table_out=None,
+                    ref_counts_out=None, stream=None) -> None:
+    """Pages for sequences that grow from ``seq_lens`` to ``new_lens`` (int32 [b]), the lowest free ones (count 0) first.
+
+    A partly filled page that others own too is replaced: (src[i], dst[i]) (int32 [b]; -1: none) is the copy that row i needs
+    before it is written, by :func:`sdpa_cache_copy` in every layer's cache.  All or nothing: ``missing`` (int32 [1]) is 0, or
+    the number of pages that lacked, and nothing has changed then.  Outputs that are None: in place."""
+    p, b = _pages(page_table, seq_lens, ref_counts, page_table_out, ref_counts_out, page_size)
+    new_at = _dense(new_lens, "new_lens", _Lazy.int32, (b,))
+    src_at, dst_at, n = _pairs(src, dst)
+    if n != b:
+        raise ValueError(f"src and dst must have an entry for each of {b} rows")
+    missing_at = _dense(missing, "missing", _Lazy.int32, (1,))
+    dev = _same_device(page_table, seq_lens, new_lens, ref_counts, src, dst, missing, page_table_out, ref_counts_out)
+    _launch(lib.sdpa_cache_grow, stream, page_table, dev, p, new_at, src_at, dst_at, missing_at)
+
+
+def sdpa_cache_free(page_table, seq_lens, keep_lens, ref_counts, *, page_size: int, page_table_out=None, ref_counts_out=None,
+                    stream=None) -> None:
+    """Gives back the pages behind ``keep_lens`` (int32 [b]) tokens of each sequence: their entries become -1, their
+    pages lose an owner.  Outputs that are None: in place."""
+    p, b = _pages(page_table, seq_lens, ref_counts, page_table_out, ref_counts_out, page_size)
+    keep_at = _dense(keep_lens, "keep_lens", _Lazy.int32, (b,))
+    dev = _same_device(page_table, seq_lens, keep_lens, ref_counts, page_table_out, ref_counts_out)
+    _launch(lib.sdpa_cache_free, stream, page_table, dev, p, keep_at)
+
+
+def sdpa_cache_compact(page_table, seq_lens, ref_counts, src, dst, *, page_size: int, page_table_out=None, ref_counts_out=None,
+                       stream=None) -> None:
+    """Moves the pages in use together at the front of the cache, at most ``src.numel()`` of them: (src[k], dst[k]) (int32,
+    src ascending, -1 behind the last) are the copies to make by :func:`sdpa_cache_copy`.  Outputs that are None: in place."""
+    p, _ = _pages(page_table, seq_lens, ref_counts, page_table_out, ref_counts_out, page_size)
+    src_at, dst_at, n = _pairs(src, dst)
+    dev = _same_device(page_table, seq_lens, ref_counts, src, dst, page_table_out, ref_counts_out)
+    _launch(lib.sdpa_cache_compact, stream, page_table, dev, p, src_at, dst_at, n)
+
+
+def _stored(k_cache, v_cache, k_scale, v_scale):
+    """The packed descriptor of a cache without a page table."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not k_cache.dtype:
+        raise ValueError("k_cache and v_cache must be [pages, h_kv, page_size, d] views of one shape and dtype")
+    pages, h_kv, page_size, d = shape
+    ks = 0 if k_scale is None else _dense(k_scale, "k_scale", _Lazy.float32, shape[:3])
+    vs = 0 if v_scale is None else _dense(v_scale, "v_scale", _Lazy.float32, shape[:3])
+    return _PACK_CACHE(pages, page_size, h_kv, d, _code(k_cache, "k_cache"), 0, 0, k_cache.data_ptr(), v_cache.data_ptr(),
+                       *k_cache.stride(), *v_cache.stride(), ks, vs, 0, 0, 0)
+
+
+def sdpa_cache_copy(k_cache, v_cache, src, dst, *, k_scale=None, v_scale=None, stream=None) -> None:
+    """Copies pages ``src[i]`` to ``dst[i]`` (int32; pairs with an entry outside the cache are passed over) of K, V and their
+    scales.  No page may be the target of two pairs, nor target of one and source of another."""
+    if _Lazy.torch is None:
+        _Lazy.load()
+    c = _stored(k_cache, v_cache, k_scale, v_scale)
+    src_at, dst_at, n = _pairs(src, dst)
+    dev = _same_device(k_cache, v_cache, src, dst, k_scale, v_scale)
+    _launch(lib.sdpa_cache_copy, stream, k_cache, dev, c, src_at, dst_at, n)
+
+
+def sdpa_cache_keep(k_cache, v_cache, page_table, seq_lens_kv, path, accepted, *, seq_lens_q=None, k_scale=None, v_scale=None,
+                    stream=None) -> None:
+    """Of the newest s tokens of each sequence (seq_lens_q: int32 [b] of them, None: all s) row ``path[i, j]`` moves to row j for
+    j < ``accepted[i]``: int32 [b, s] and [b] of :func:`sdpa_verify`.  The sequences' lengths are then seq_lens_kv -
+    seq_lens_q + accepted, which is the caller's to note."""
+    c, _, n = _cache(k_cache, v_cache, page_table, seq_lens_kv, k_scale, v_scale)
+    if path.dim() != 2:
+        raise ValueError("path must be int32 [b, s]")
+    s = path.shape[1]
+    path_at, accepted_at = _dense(path, "path", _Lazy.int32, (n, s)), _dense(accepted, "accepted", _Lazy.int32, (n,))
+    lens_q = 0 if seq_lens_q is None else _dense(seq_lens_q, "seq_lens_q", _Lazy.int32, (n,))
+    dev = _same_device(k_cache, v_cache, page_table, seq_lens_kv, path, accepted, seq_lens_q, k_scale, v_scale)
+    _launch(lib.sdpa_cache_keep, stream, k_cache, dev, c, path_at, accepted_at, s, lens_q)
+
+
+def sdpa_verify(tokens, probs, uniform, accepted, path, new_tokens, *, parents=None, draft_probs=None, seq_lens_q=None,
+                stream=None) -> None:
+    """Drafted tokens verified against the target's probabilities, so that the tokens kept are distributed as the target's own.
+
+    tokens: int32 [b, s], row 0 the newest decided token, the others drafted, row i behind row ``parents[i]`` < i (int32
+    [b, s]; None: a chain).  probs: [b, s, vocab] (f16, bf16, f32), the target's distribution behind each row; draft_probs:
+    the same of the draft, from which row i of a chain was drawn (None: whatever drafted it).  uniform: fp32 [b, s] in [0, 1).
+    seq_lens_q: int32 [b] rows that take part (None: all).
+
+    accepted: int32 [b] rows kept, row 0 among them; path: int32 [b, s], those rows; new_tokens: int32 [b, s], the accepted
+    drafts and the token drawn behind them, ``accepted`` in all; -1 behind those.  Rules in ``include/sdpa.h``."""
+    if _Lazy.torch is None:
+        _Lazy.load()
+    shape = probs.shape
+    if len(shape) != 3 or (shape[2] > 1 and probs.stride(2) != 1) or probs.dtype not in _Lazy.probs:
+        raise ValueError("probs must be float16, bfloat16 or float32 [b, s, vocab] with a unit last stride")
+    b, s, vocab = shape
+    rows, int32 = shape[:2], _Lazy.int32
+    draft_at = draft_b = draft_s = 0
+    if draft_probs is not None:
+        if draft_probs.shape != shape or draft_probs.dtype is not probs.dtype or (vocab > 1 and draft_probs.stride(2) != 1):
+            raise ValueError("draft_probs must have probs' shape and dtype, and a unit last stride")
+        draft_at, (draft_b, draft_s, _) = draft_probs.data_ptr(), draft_probs.stride()
+    p = _PACK_VERIFY(b, s, vocab, _Lazy.probs[probs.dtype], _dense(tokens, "tokens", int32, rows),
+                     0 if parents is None else _dense(parents, "parents", int32, rows),
+                     0 if seq_lens_q is None else _dense(seq_lens_q, "seq_lens_q", int32, shape[:1]),
+                     _dense(uniform, "uniform", _Lazy.float32, rows), probs.data_ptr(), probs.stride(0), probs.stride(1),
+                     draft_at, draft_b, draft_s, _dense(accepted, "accepted", int32, shape[:1]), _dense(path, "path", int32, rows),
+                     _dense(new_tokens, "new_tokens", int32, rows))
+    dev = _same_device(probs, tokens, uniform, accepted, path, new_tokens, parents, draft_probs, seq_lens_q)
+    _launch(lib.sdpa_verify, stream, probs, dev, p)

@@ -130,7 +130,8 @@ __device__ __forceinline__ void store_item(uint8_t* row, float* scale_at, int m,
 // ROPE: 0 none, 1 rot a multiple of 16, 2 any even rot.
 // (A floor of one block an SM lets the compiler hold a few more registers, 122, still four blocks: 38.5 ->
 // 36.5 us.)
-template <int D, int DT, int CT, int ROPE>
+// AXES: K has several positions a token.
+template <int D, int DT, int CT, int ROPE, bool AXES>
 __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_constant__ CacheRowsParams p, int per,
                                                             bool small) {
   constexpr int LANES = D / 16;
@@ -170,15 +171,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_c
       ptx::prefetch_l2(static_cast<const uint16_t*>(p.v) + bi * p.v_st[0] + h * p.v_st[1] + si * p.v_st[2] + e);
     }
   }
-  int rpos = pos;
+  RopePos<AXES> rpos = {};
   float c[8], s[8];
   if constexpr (ROPE != 0) {
-    if (p.r.positions && live) rpos = p.r.positions[bi * p.r.positions_stride + si];
+    if (live) rpos = rope_pos<AXES>(p.r, bi, si, pos);
   }
   if constexpr (ROPE == 1) {
     if (it.turned && live) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) rope_angle(p.r, __ldg(p.r.table + m * 8 + i), rpos, c[i], s[i]);
+      for (int i = 0; i < 8; ++i)
+        rope_angle(p.r, __ldg(p.r.table + m * 8 + i), rpos.of(axes_from<AXES>(p.r, m * 8) >> (2 * i)), c[i], s[i]);
     }
   }
   // Every lane of the warp runs the same number of turns (the shuffles need them all).
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_c
           const bool first = p.r.interleaved ? e % 2 == 0 : e < half;
           const int other = p.r.interleaved ? e ^ 1 : (first ? e + half : e - half);
           float cc, ss;
-          rope_angle(p.r, __ldg(p.r.table + pair), rpos, cc, ss);
+          rope_angle(p.r, __ldg(p.r.table + pair), rpos.of(axes_from<AXES>(p.r, pair)), cc, ss);
           const float a = load16<DT>(p.k, krow + e), b = load16<DT>(p.k, krow + other);
           x[i] = first ? a * cc - b * ss : b * ss + a * cc;
         }
@@ -289,9 +291,12 @@ cudaError_t write_t(const CacheRowsParams& p, int num_sms, cudaStream_t st) {
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(blocks);
   const bool small = blocks * kThreads < (int64_t(1) << 31);
-  if (!p.rope) cache_write_kernel<D, DT, CT, 0><<<grid, kThreads, 0, st>>>(p, per, small);
-  else if (p.r.rot % 16 == 0) cache_write_kernel<D, DT, CT, 1><<<grid, kThreads, 0, st>>>(p, per, small);
-  else cache_write_kernel<D, DT, CT, 2><<<grid, kThreads, 0, st>>>(p, per, small);
+  const bool vec = p.r.rot % 16 == 0;
+  if (!p.rope) cache_write_kernel<D, DT, CT, 0, false><<<grid, kThreads, 0, st>>>(p, per, small);
+  else if (vec && p.r.axes) cache_write_kernel<D, DT, CT, 1, true><<<grid, kThreads, 0, st>>>(p, per, small);
+  else if (vec) cache_write_kernel<D, DT, CT, 1, false><<<grid, kThreads, 0, st>>>(p, per, small);
+  else if (p.r.axes) cache_write_kernel<D, DT, CT, 2, true><<<grid, kThreads, 0, st>>>(p, per, small);
+  else cache_write_kernel<D, DT, CT, 2, false><<<grid, kThreads, 0, st>>>(p, per, small);
   return cudaGetLastError();
 }
 

@@ -14,7 +14,7 @@ namespace sdpa {
 constexpr int kBlockM = 128;  // query rows per Q tile (one TMEM lane per row)
 constexpr int kBlockN = 128;  // key/value rows per KV block
 
-enum DType : int { kF16 = 0, kBF16 = 1, kE4M3 = 2 };
+enum DType : int { kF16 = 0, kBF16 = 1, kE4M3 = 2, kF32 = 4 };
 
 // Forward pass.  Tensor maps are 4-D (d, s, h, b) views over the caller's strides,
 // 128-byte swizzled, box = (128 bytes of d, 128 rows, 1, 1).
@@ -202,6 +202,9 @@ long long api_wait_limit();
 
 // ---- rotary positions ----------------------------------------------------------------------
 
+constexpr int kMaxAxes = 4;          // positions of one token
+constexpr int kMaxAxisPairs = 256;   // pairs of a head (d = 512)
+
 // What one row's rotation needs (in sdpa_rope_fwd/bwd and inside sdpa_cache_write).
 struct RopeArgs {
   const int64_t* table;       // turns per position of each pair, 64-bit binary fractions
@@ -211,6 +214,10 @@ struct RopeArgs {
   int interleaved;
   int sign;                   // +1 forward, -1 backward (the transposed rotation)
   float factor;
+  // Several axes (0: one position a token): the positions of each, and each pair's axis in two bits.
+  int axes;
+  int64_t axis_stride;
+  uint32_t axis_of[kMaxAxisPairs / 16];
 };
 
 struct RopeParams {
@@ -253,6 +260,78 @@ struct CacheRowsParams {
 
 cudaError_t launch_cache_write(const CacheRowsParams& p, int row_dtype, int cache_dtype, int num_sms, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheRowsParams& p, int row_dtype, int cache_dtype, cudaStream_t st);
+
+// ---- pages of a cache, and who owns them ---------------------------------------------------
+
+constexpr int kMaxPageRows = 4096;   // sequences of one grow (their wanted pages stand in shared memory)
+
+struct PagesParams {
+  const int32_t* page_table;
+  int64_t table_stride;
+  const int32_t* seq_lens;
+  const int32_t* ref_counts;     // [num_pages]
+  int32_t* page_table_out;       // may be page_table (fork: not)
+  int64_t table_out_stride;
+  int32_t* ref_counts_out;       // may be ref_counts
+  int num_pages, page_size, b, max_pages;
+  int max_len;                   // min(max_pages * page_size, 2^30)
+};
+
+cudaError_t launch_fork(const PagesParams& p, const int32_t* parents, int b_out, int32_t* seq_lens_out, cudaStream_t st);
+cudaError_t launch_grow(const PagesParams& p, const int32_t* new_lens, int32_t* src, int32_t* dst, int32_t* missing, cudaStream_t st);
+cudaError_t launch_free(const PagesParams& p, const int32_t* keep_lens, cudaStream_t st);
+cudaError_t launch_compact(const PagesParams& p, int32_t* src, int32_t* dst, int pairs, cudaStream_t st);
+
+// One tensor of a cache as units of 16 bytes: BYTE strides of a page, of its inner rows and of groups of those.
+struct CopyTensor {
+  uint8_t* base;
+  int64_t page, outer, inner;
+  int inner_n;                   // rows of the inner dimension
+  int row_units;
+  int units;                     // of a page (0: no such tensor)
+};
+
+struct CopyParams {
+  CopyTensor t[4];               // K, V, their scales
+  int num_pages;
+  int first_item[4], items_per_pair;   // filled in by launch_copy
+};
+
+cudaError_t launch_copy(CopyParams p, const int32_t* src, const int32_t* dst, int pairs, int num_sms, cudaStream_t st);
+
+struct KeepParams {
+  CacheArgs c;
+  const int32_t* seq_lens_q;
+  const int32_t* path;           // [b][s]
+  const int32_t* accepted;       // [b]
+  int s;
+  int row_units;                 // 16-byte units of one head's row
+  int blocks;                    // of one sequence; filled in by launch_keep
+};
+
+cudaError_t launch_keep(KeepParams p, cudaStream_t st);
+
+// ---- drafted tokens verified ---------------------------------------------------------------
+
+constexpr int kVerifyRows = 1024;    // rows of one sequence (its tree stands in shared memory)
+
+struct VerifyParams {
+  const int32_t* tokens;         // [b][s]
+  const int32_t* parents;        // [b][s], or nullptr: a chain
+  const int32_t* seq_lens_q;     // [b], or nullptr
+  const float* uniform;          // [b][s]
+  const void* probs;             // strides in elements
+  int64_t probs_b, probs_s;
+  const void* draft;             // or nullptr
+  int64_t draft_b, draft_s;
+  int32_t* accepted;             // [b]
+  int32_t* path;                 // [b][s]
+  int32_t* new_tokens;           // [b][s]
+  int b, s, vocab;
+};
+
+// dtype: kF16, kBF16 or kF32.
+cudaError_t launch_verify(const VerifyParams& p, int dtype, int num_sms, cudaStream_t st);
 
 // ---- attention over the cache --------------------------------------------------------------
 

@@ -15,7 +15,9 @@ constexpr int kThreads = 128;
 constexpr int kUnroll = 4;     // heads whose loads are in flight together
 
 // rot and d multiples of 16.  One thread: item m of token (bi, si), heads [h0, h0 + per).
-template <int DT, bool INTER>
+// AXES: several positions a token; a thread's pairs are neighbours, so that their axes come as 16 bits of the
+// parameters (two runs of 8 where pairs are interleaved).
+template <int DT, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p, int per, int groups, bool small) {
   const int items = p.d / 16;
   const Spot at = find_spot(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, items, p.b, p.s, small);
@@ -46,11 +48,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   };
   float c[8], s[8];
   if (it.turned) {
-    const int pos = p.r.positions ? p.r.positions[bi * p.r.positions_stride + si] : si;
+    const RopePos<AXES> pos = rope_pos<AXES>(p.r, bi, si, si);
+    uint32_t axes = axes_from<AXES>(p.r, INTER ? m * 4 : m * 8);
+    if (INTER) axes = (axes & 0xFFu) | axes_from<AXES>(p.r, p.r.rot / 4 + m * 4) << 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int pair = !INTER ? m * 8 + i : i < 4 ? m * 4 + i : p.r.rot / 4 + m * 4 + i - 4;
-      rope_angle(p.r, __ldg(p.r.table + pair), pos, c[i], s[i]);
+      rope_angle(p.r, __ldg(p.r.table + pair), pos.of(axes >> (2 * i)), c[i], s[i]);
     }
   }
   for (int h0 = grp * per; h0 < h1; h0 += kUnroll) {
@@ -80,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 }
 
 // Any even rot and any d: one thread takes one pair (or two elements behind the rotated part).
-template <int DT, bool INTER>
+template <int DT, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constant__ RopeParams p, int per, int groups, bool small) {
   const int items = p.d / 2, half = p.r.rot / 2;
   const Spot at = find_spot(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, items, p.b, p.s, small);
@@ -90,8 +94,7 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
   const int ia = turned && !INTER ? m : 2 * m, ib = turned && !INTER ? m + half : 2 * m + 1;
   float c = 1.f, s = 0.f;
   if (turned) {
-    const int pos = p.r.positions ? p.r.positions[bi * p.r.positions_stride + si] : si;
-    rope_angle(p.r, __ldg(p.r.table + m), pos, c, s);
+    rope_angle(p.r, __ldg(p.r.table + m), rope_pos<AXES>(p.r, bi, si, si).of(axes_from<AXES>(p.r, m)), c, s);
   }
   const int h1 = min(p.h_all, (grp + 1) * per);
   for (int h = grp * per; h < h1; ++h) {
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
   }
 }
 
-template <int DT, bool INTER>
+template <int DT, bool INTER, bool AXES>
 cudaError_t launch_t(const RopeParams& p, int num_sms, cudaStream_t st) {
   const bool vec = p.d % 16 == 0 && p.r.rot % 16 == 0;
   const int64_t tokens = static_cast<int64_t>(p.b) * p.s, items = p.d / (vec ? 16 : 2);
@@ -123,17 +126,22 @@ cudaError_t launch_t(const RopeParams& p, int num_sms, cudaStream_t st) {
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const bool small = blocks * kThreads < (int64_t(1) << 31);
   if (vec)
-    rope_kernel<DT, INTER><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p, per, groups, small);
+    rope_kernel<DT, INTER, AXES><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p, per, groups, small);
   else
-    rope_any_kernel<DT, INTER><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p, per, groups, small);
+    rope_any_kernel<DT, INTER, AXES><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p, per, groups, small);
   return cudaGetLastError();
+}
+
+template <int DT, bool INTER>
+cudaError_t launch_a(const RopeParams& p, int num_sms, cudaStream_t st) {
+  return p.r.axes ? launch_t<DT, INTER, true>(p, num_sms, st) : launch_t<DT, INTER, false>(p, num_sms, st);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeParams& p, int dtype, int num_sms, cudaStream_t st) {
-  if (dtype == kBF16) return p.r.interleaved ? launch_t<kBF16, true>(p, num_sms, st) : launch_t<kBF16, false>(p, num_sms, st);
-  return p.r.interleaved ? launch_t<kF16, true>(p, num_sms, st) : launch_t<kF16, false>(p, num_sms, st);
+  if (dtype == kBF16) return p.r.interleaved ? launch_a<kBF16, true>(p, num_sms, st) : launch_a<kBF16, false>(p, num_sms, st);
+  return p.r.interleaved ? launch_a<kF16, true>(p, num_sms, st) : launch_a<kF16, false>(p, num_sms, st);
 }
 
 }  // namespace sdpa

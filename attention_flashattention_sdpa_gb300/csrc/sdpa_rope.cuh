@@ -44,6 +44,45 @@ __device__ __forceinline__ void rope_angle(const RopeArgs& r, int64_t turns, int
   s = ((quarter & 2) != 0) != (r.sign < 0) ? -sw : sw;
 }
 
+// The positions of a token, one for each axis (axes that there are not: 0).
+template <bool AXES>
+struct RopePos;
+
+template <>
+struct RopePos<false> {
+  int p;
+  __device__ __forceinline__ int of(uint32_t) const { return p; }
+};
+
+template <>
+struct RopePos<true> {
+  int p[kMaxAxes];
+  // The position on axis a & 3: two selections by its bits (an index into registers would go through memory).
+  __device__ __forceinline__ int of(uint32_t a) const {
+    const int lo = a & 1u ? p[1] : p[0], hi = a & 1u ? p[3] : p[2];
+    return a & 2u ? hi : lo;
+  }
+};
+
+template <bool AXES>
+__device__ __forceinline__ RopePos<AXES> rope_pos(const RopeArgs& r, int bi, int si, int plain) {
+  RopePos<AXES> x;
+  if constexpr (AXES) {
+    const int32_t* at = r.positions + bi * r.positions_stride + si;
+#pragma unroll
+    for (int a = 0; a < kMaxAxes; ++a) x.p[a] = a < r.axes ? __ldg(at + a * r.axis_stride) : 0;
+  } else {
+    x.p = r.positions ? r.positions[bi * r.positions_stride + si] : plain;
+  }
+  return x;
+}
+
+// Axes of the pairs from `pair` on, two bits each, the first in the lowest; 16 - pair % 16 of them.
+template <bool AXES>
+__device__ __forceinline__ uint32_t axes_from(const RopeArgs& r, int pair) {
+  return AXES ? r.axis_of[pair >> 4] >> (2 * (pair & 15)) : 0u;
+}
+
 template <int DT>
 __device__ __forceinline__ float2 unpack16(uint32_t w) {
   if (DT == kBF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));

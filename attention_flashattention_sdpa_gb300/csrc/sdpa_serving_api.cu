@@ -1,5 +1,5 @@
-// sdpa_serving_api.cu — C entry points of the rotary positions, the paged cache and the attention
-// over it: argument checks on the host, then one or two launches.  As everywhere in this library
+// sdpa_serving_api.cu — C entry points of the rotary positions, the paged cache, its pages, the attention
+// over it and the verification of drafts: argument checks on the host, then one or two launches.  As everywhere in this library
 // nothing is allocated or synchronised, and what is not supported is refused with a message.
 #include <cmath>
 #include <cstdio>
@@ -49,8 +49,28 @@ sdpa_status_t check_turn(const sdpa_rope_t* p, int d) {
   return SDPA_OK;
 }
 
-sdpa::RopeArgs turn_of(const sdpa_rope_t* p, int sign) {
+// The axes of a rotation's pairs, for one that has several.
+sdpa_status_t check_axes(const sdpa_rope_t* p, const sdpa_rope_axes_t* a) {
+  if (a == nullptr) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "axes descriptor is NULL");
+  if (a->axes < 1 || a->axes > sdpa::kMaxAxes)
+    SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "%d axes not supported (1..%d)", a->axes, sdpa::kMaxAxes);
+  if (a->axis_stride < 0) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "axis_stride must not be negative");
+  if (p->positions == nullptr) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "axes need positions");
+  for (int i = 0; i < p->rot / 2; ++i)
+    if (a->axis[i] >= a->axes)
+      SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "axis[%d] must be below axes (%d), got %d", i, a->axes, a->axis[i]);
+  return SDPA_OK;
+}
+
+// `a`: checked, or NULL: one position a token.
+sdpa::RopeArgs turn_of(const sdpa_rope_t* p, const sdpa_rope_axes_t* a, int sign) {
   sdpa::RopeArgs r;
+  memset(&r, 0, sizeof(r));
+  if (a) {
+    r.axes = a->axes;
+    r.axis_stride = a->axis_stride;
+    for (int i = 0; i < p->rot / 2; ++i) r.axis_of[i / 16] |= static_cast<uint32_t>(a->axis[i]) << (2 * (i % 16));
+  }
   r.table = p->table;
   r.positions = p->positions;
   r.positions_stride = p->positions_stride;
@@ -61,8 +81,8 @@ sdpa::RopeArgs turn_of(const sdpa_rope_t* p, int sign) {
   return r;
 }
 
-sdpa_status_t rope(const sdpa_rope_t* p, const void* q, const void* k, void* q_out, void* k_out, int sign,
-                   void* stream_, const char* what) {
+sdpa_status_t rope(const sdpa_rope_t* p, bool several, const sdpa_rope_axes_t* a, const void* q, const void* k, void* q_out,
+                   void* k_out, int sign, void* stream_, const char* what) {
   if (p == nullptr) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "rope descriptor is NULL");
   if (p->b < 1 || p->h_q < 1 || p->h_k < 0 || p->s < 1)
     SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "sizes must be >= 1 (b=%d h_q=%d h_k=%d s=%d)", p->b, p->h_q, p->h_k, p->s);
@@ -70,6 +90,7 @@ sdpa_status_t rope(const sdpa_rope_t* p, const void* q, const void* k, void* q_o
     SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "head dim %d not supported (a multiple of 8, 8..512)", p->d);
   if (!is16(p->dtype)) SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "rotary positions take F16 or BF16 (dtype %d)", p->dtype);
   SDPA_TRY(check_turn(p, p->d));
+  if (several) SDPA_TRY(check_axes(p, a));
   SDPA_TRY(view("q", q, p->q, p->b, p->h_q, p->s, p->d, 2));
   SDPA_TRY(view("q_out", q_out, p->q_out, p->b, p->h_q, p->s, p->d, 2));
   if (p->h_k > 0) {
@@ -80,7 +101,7 @@ sdpa_status_t rope(const sdpa_rope_t* p, const void* q, const void* k, void* q_o
     SDPA_REFUSE(SDPA_ERR_LAYOUT, "an output that is its input must have its strides");
   sdpa::RopeParams prm;
   memset(&prm, 0, sizeof(prm));
-  prm.r = turn_of(p, sign);
+  prm.r = turn_of(p, several ? a : nullptr, sign);
   prm.in[0] = q;
   prm.in[1] = k;
   prm.out[0] = q_out;
@@ -97,18 +118,19 @@ sdpa_status_t rope(const sdpa_rope_t* p, const void* q, const void* k, void* q_o
   prm.h_q = p->h_q;
   prm.h_all = p->h_q + p->h_k;
   if (sdpa::api_log_level() >= 1)
-    fprintf(stderr, "[sdpa] %s b=%d h_q=%d h_k=%d s=%d d=%d rot=%d dt=%d\n", what, p->b, p->h_q, p->h_k, p->s, p->d,
-            p->rot, p->dtype);
+    fprintf(stderr, "[sdpa] %s b=%d h_q=%d h_k=%d s=%d d=%d rot=%d dt=%d axes=%d\n", what, p->b, p->h_q, p->h_k, p->s, p->d,
+            p->rot, p->dtype, prm.r.axes);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   cudaError_t e = sdpa::launch_rope(prm, p->dtype, sdpa::api_num_sms(), stream);
   return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, what));
 }
 
-sdpa_status_t check_cache(const sdpa_cache_t* c) {
+// What a cache holds: its pages, without the table of a batch.
+sdpa_status_t check_stored(const sdpa_cache_t* c) {
   if (c == nullptr) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "cache descriptor is NULL");
-  if (c->num_pages < 1 || c->h_kv < 1 || c->b < 1 || c->max_pages < 1 || c->page_size < 1)
-    SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "cache sizes must be >= 1 (num_pages=%d page_size=%d h_kv=%d b=%d max_pages=%d)",
-                c->num_pages, c->page_size, c->h_kv, c->b, c->max_pages);
+  if (c->num_pages < 1 || c->h_kv < 1 || c->page_size < 1)
+    SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "cache sizes must be >= 1 (num_pages=%d page_size=%d h_kv=%d)", c->num_pages, c->page_size,
+                c->h_kv);
   if (c->page_size % 16 != 0)
     SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "page_size %d not supported (a multiple of 16)", c->page_size);
   if (c->d != 64 && c->d != 128 && c->d != 256)
@@ -125,6 +147,14 @@ sdpa_status_t check_cache(const sdpa_cache_t* c) {
   } else if (c->k_scale || c->v_scale) {
     SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "a 16-bit cache takes no k_scale and v_scale");
   }
+  return SDPA_OK;
+}
+
+sdpa_status_t check_cache(const sdpa_cache_t* c) {
+  if (c != nullptr && (c->num_pages < 1 || c->h_kv < 1 || c->b < 1 || c->max_pages < 1 || c->page_size < 1))
+    SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "cache sizes must be >= 1 (num_pages=%d page_size=%d h_kv=%d b=%d max_pages=%d)",
+                c->num_pages, c->page_size, c->h_kv, c->b, c->max_pages);
+  SDPA_TRY(check_stored(c));
   if (!c->page_table || !c->seq_lens_kv)
     SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "page_table and seq_lens_kv must not be NULL");
   if (reinterpret_cast<uintptr_t>(c->page_table) % 4 || reinterpret_cast<uintptr_t>(c->seq_lens_kv) % 4)
@@ -132,6 +162,11 @@ sdpa_status_t check_cache(const sdpa_cache_t* c) {
   if (c->b > 1 && c->page_table_stride < c->max_pages)
     SDPA_REFUSE(SDPA_ERR_LAYOUT, "page_table_stride below max_pages");
   return SDPA_OK;
+}
+
+int max_tokens(int max_pages, int page_size) {
+  const int64_t cap = static_cast<int64_t>(max_pages) * page_size;
+  return static_cast<int>(cap < kMaxLen ? cap : kMaxLen);
 }
 
 sdpa::CacheArgs cache_args(const sdpa_cache_t* c) {
@@ -152,9 +187,100 @@ sdpa::CacheArgs cache_args(const sdpa_cache_t* c) {
   a.h_kv = c->h_kv;
   a.b = c->b;
   a.max_pages = c->max_pages;
-  const int64_t cap = static_cast<int64_t>(c->max_pages) * c->page_size;
-  a.max_len = static_cast<int>(cap < kMaxLen ? cap : kMaxLen);
+  a.max_len = max_tokens(c->max_pages, c->page_size);
   return a;
+}
+
+// 32-bit words on the device that a call needs.
+sdpa_status_t words(const char* name, const void* ptr) {
+  if (ptr == nullptr) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "%s: null pointer", name);
+  if (reinterpret_cast<uintptr_t>(ptr) % 4) SDPA_REFUSE(SDPA_ERR_LAYOUT, "%s must be 4-byte aligned", name);
+  return SDPA_OK;
+}
+
+// Whether n words at a and m at b have any in common.
+bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * static_cast<uintptr_t>(m) && y < x + 4 * static_cast<uintptr_t>(n);
+}
+
+// Words from the first to the last entry of a page table.
+int64_t table_words(int rows, int columns, int64_t stride) { return (rows - 1) * stride + columns; }
+
+// `rows_out`: rows of the table that is written; `in_place`: it may be the one that is read.
+sdpa_status_t check_pages(const sdpa_pages_t* p, int rows_out, bool in_place) {
+  if (p == nullptr) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "pages descriptor is NULL");
+  if (p->num_pages < 1 || p->page_size < 1 || p->b < 1 || p->max_pages < 1 || rows_out < 1)
+    SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "sizes must be >= 1 (num_pages=%d page_size=%d b=%d max_pages=%d, %d rows out)", p->num_pages,
+                p->page_size, p->b, p->max_pages, rows_out);
+  if (p->page_size % 16 != 0)
+    SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "page_size %d not supported (a multiple of 16)", p->page_size);
+  SDPA_TRY(words("page_table", p->page_table));
+  SDPA_TRY(words("seq_lens", p->seq_lens));
+  SDPA_TRY(words("ref_counts", p->ref_counts));
+  SDPA_TRY(words("page_table_out", p->page_table_out));
+  SDPA_TRY(words("ref_counts_out", p->ref_counts_out));
+  if ((p->b > 1 && p->page_table_stride < p->max_pages) || (rows_out > 1 && p->page_table_out_stride < p->max_pages))
+    SDPA_REFUSE(SDPA_ERR_LAYOUT, "page_table_stride below max_pages");
+  if (static_cast<int64_t>(p->b) * p->max_pages >= (int64_t(1) << 38) || static_cast<int64_t>(rows_out) * p->max_pages >= (int64_t(1) << 38))
+    SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "b*max_pages too large");
+  const bool same = p->page_table_out == p->page_table;
+  if (same ? !in_place || (p->b > 1 && p->page_table_out_stride != p->page_table_stride)
+           : overlap(p->page_table, table_words(p->b, p->max_pages, p->page_table_stride), p->page_table_out,
+                     table_words(rows_out, p->max_pages, p->page_table_out_stride)))
+    SDPA_REFUSE(SDPA_ERR_LAYOUT, in_place ? "page_table_out must be page_table with its stride, or lie apart from it"
+                                          : "page_table_out must lie apart from page_table");
+  if (p->ref_counts_out != p->ref_counts && overlap(p->ref_counts, p->num_pages, p->ref_counts_out, p->num_pages))
+    SDPA_REFUSE(SDPA_ERR_LAYOUT, "ref_counts_out must be ref_counts or lie apart from it");
+  return SDPA_OK;
+}
+
+sdpa::PagesParams pages_params(const sdpa_pages_t* p) {
+  sdpa::PagesParams prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.page_table = p->page_table;
+  prm.table_stride = p->page_table_stride;
+  prm.seq_lens = p->seq_lens;
+  prm.ref_counts = p->ref_counts;
+  prm.page_table_out = p->page_table_out;
+  prm.table_out_stride = p->page_table_out_stride;
+  prm.ref_counts_out = p->ref_counts_out;
+  prm.num_pages = p->num_pages;
+  prm.page_size = p->page_size;
+  prm.b = p->b;
+  prm.max_pages = p->max_pages;
+  prm.max_len = max_tokens(p->max_pages, p->page_size);
+  return prm;
+}
+
+void log_pages(const char* what, const sdpa_pages_t* p, int n) {
+  if (sdpa::api_log_level() >= 1)
+    fprintf(stderr, "[sdpa] %s b=%d max_pages=%d num_pages=%d page=%d n=%d\n", what, p->b, p->max_pages, p->num_pages, p->page_size, n);
+}
+
+// A cache's K or V as units of 16 bytes, in the order of memory: the dimension of the smaller stride is the inner one.
+sdpa::CopyTensor copy_tensor(void* base, const sdpa_strides_t& st, const sdpa_cache_t* c, int es) {
+  sdpa::CopyTensor t;
+  const bool slots_inside = st.s <= st.h;
+  t.base = static_cast<uint8_t*>(base);
+  t.page = st.b * es;
+  t.inner = (slots_inside ? st.s : st.h) * es;
+  t.outer = (slots_inside ? st.h : st.s) * es;
+  t.inner_n = slots_inside ? c->page_size : c->h_kv;
+  t.row_units = c->d * es / 16;
+  t.units = c->h_kv * c->page_size * t.row_units;
+  return t;
+}
+
+sdpa::CopyTensor copy_scales(float* base, const sdpa_cache_t* c) {
+  sdpa::CopyTensor t;
+  memset(&t, 0, sizeof(t));
+  if (base == nullptr) return t;
+  t.base = reinterpret_cast<uint8_t*>(base);
+  t.page = static_cast<int64_t>(c->h_kv) * c->page_size * 4;
+  t.inner_n = 1;
+  t.row_units = t.units = c->h_kv * c->page_size / 4;
+  return t;
 }
 
 sdpa_status_t check_rows(const sdpa_cache_t* c, const sdpa_cache_rows_t* r, const void* k, const void* v) {
@@ -180,6 +306,27 @@ sdpa::CacheRowsParams rows_params(const sdpa_cache_t* c, const sdpa_cache_rows_t
   prm.s = r->s;
   prm.d = c->d;
   return prm;
+}
+
+sdpa_status_t write(const sdpa_cache_t* c, const sdpa_cache_rows_t* r, bool several, const sdpa_rope_axes_t* a, const void* k,
+                    const void* v, void* stream_, const char* what) {
+  SDPA_TRY(check_rows(c, r, k, v));
+  if (reinterpret_cast<uintptr_t>(r->seq_lens_q) % 4) SDPA_REFUSE(SDPA_ERR_LAYOUT, "seq_lens_q must be 4-byte aligned");
+  if (r->rope) SDPA_TRY(check_turn(r->rope, c->d));
+  if (several) {
+    if (!r->rope) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "axes need a rope descriptor");
+    SDPA_TRY(check_axes(r->rope, a));
+  }
+  sdpa::CacheRowsParams prm = rows_params(c, r, k, v);
+  prm.seq_lens_q = r->seq_lens_q;
+  prm.rope = r->rope != nullptr;
+  if (r->rope) prm.r = turn_of(r->rope, several ? a : nullptr, 1);
+  if (sdpa::api_log_level() >= 1)
+    fprintf(stderr, "[sdpa] cache_write b=%d h_kv=%d s=%d d=%d dt=%d cache=%d rot=%d axes=%d\n", c->b, c->h_kv, r->s, c->d,
+            r->dtype, c->dtype, r->rope ? r->rope->rot : 0, prm.r.axes);
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  cudaError_t e = sdpa::launch_cache_write(prm, r->dtype, c->dtype, sdpa::api_num_sms(), stream);
+  return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, what));
 }
 
 // Sizes and options of an attention call (all that its workspace depends on).
@@ -281,28 +428,31 @@ sdpa_status_t sdpa_rope_table(const sdpa_rope_table_t* cfg, int64_t* table, floa
 }
 
 sdpa_status_t sdpa_rope_fwd(const sdpa_rope_t* p, const void* q, const void* k, void* q_out, void* k_out, void* stream) {
-  return rope(p, q, k, q_out, k_out, 1, stream, "sdpa_rope_fwd");
+  return rope(p, false, nullptr, q, k, q_out, k_out, 1, stream, "sdpa_rope_fwd");
 }
 
 sdpa_status_t sdpa_rope_bwd(const sdpa_rope_t* p, const void* dq_out, const void* dk_out, void* dq, void* dk, void* stream) {
-  return rope(p, dq_out, dk_out, dq, dk, -1, stream, "sdpa_rope_bwd");
+  return rope(p, false, nullptr, dq_out, dk_out, dq, dk, -1, stream, "sdpa_rope_bwd");
+}
+
+sdpa_status_t sdpa_rope_axes_fwd(const sdpa_rope_t* p, const sdpa_rope_axes_t* a, const void* q, const void* k, void* q_out,
+                                 void* k_out, void* stream) {
+  return rope(p, true, a, q, k, q_out, k_out, 1, stream, "sdpa_rope_axes_fwd");
+}
+
+sdpa_status_t sdpa_rope_axes_bwd(const sdpa_rope_t* p, const sdpa_rope_axes_t* a, const void* dq_out, const void* dk_out,
+                                 void* dq, void* dk, void* stream) {
+  return rope(p, true, a, dq_out, dk_out, dq, dk, -1, stream, "sdpa_rope_axes_bwd");
 }
 
 sdpa_status_t sdpa_cache_write(const sdpa_cache_t* c, const sdpa_cache_rows_t* r, const void* k, const void* v,
-                               void* stream_) {
-  SDPA_TRY(check_rows(c, r, k, v));
-  if (reinterpret_cast<uintptr_t>(r->seq_lens_q) % 4) SDPA_REFUSE(SDPA_ERR_LAYOUT, "seq_lens_q must be 4-byte aligned");
-  if (r->rope) SDPA_TRY(check_turn(r->rope, c->d));
-  sdpa::CacheRowsParams prm = rows_params(c, r, k, v);
-  prm.seq_lens_q = r->seq_lens_q;
-  prm.rope = r->rope != nullptr;
-  if (r->rope) prm.r = turn_of(r->rope, 1);
-  if (sdpa::api_log_level() >= 1)
-    fprintf(stderr, "[sdpa] cache_write b=%d h_kv=%d s=%d d=%d dt=%d cache=%d rot=%d\n", c->b, c->h_kv, r->s, c->d,
-            r->dtype, c->dtype, r->rope ? r->rope->rot : 0);
-  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  cudaError_t e = sdpa::launch_cache_write(prm, r->dtype, c->dtype, sdpa::api_num_sms(), stream);
-  return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, "sdpa_cache_write"));
+                               void* stream) {
+  return write(c, r, false, nullptr, k, v, stream, "sdpa_cache_write");
+}
+
+sdpa_status_t sdpa_cache_write_axes(const sdpa_cache_t* c, const sdpa_cache_rows_t* r, const sdpa_rope_axes_t* a,
+                                    const void* k, const void* v, void* stream) {
+  return write(c, r, true, a, k, v, stream, "sdpa_cache_write_axes");
 }
 
 sdpa_status_t sdpa_cache_read(const sdpa_cache_t* c, const sdpa_cache_rows_t* r, void* k, void* v, void* stream_) {
@@ -361,6 +511,148 @@ sdpa_status_t sdpa_decode(const sdpa_cache_t* c, const sdpa_decode_t* p, const v
   return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, "sdpa_decode"));
 }
 
+sdpa_status_t sdpa_cache_fork(const sdpa_pages_t* p, const int32_t* parents, int32_t b_out, int32_t* seq_lens_out, void* stream_) {
+  SDPA_TRY(check_pages(p, b_out, false));
+  SDPA_TRY(words("parents", parents));
+  SDPA_TRY(words("seq_lens_out", seq_lens_out));
+  if (overlap(p->seq_lens, p->b, seq_lens_out, b_out)) SDPA_REFUSE(SDPA_ERR_LAYOUT, "seq_lens_out must lie apart from seq_lens");
+  if (overlap(parents, b_out, seq_lens_out, b_out)) SDPA_REFUSE(SDPA_ERR_LAYOUT, "seq_lens_out must lie apart from parents");
+  log_pages("fork", p, b_out);
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  cudaError_t e = sdpa::launch_fork(pages_params(p), parents, b_out, seq_lens_out, stream);
+  return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, "sdpa_cache_fork"));
+}
+
+sdpa_status_t sdpa_cache_grow(const sdpa_pages_t* p, const int32_t* new_lens, int32_t* src, int32_t* dst, int32_t* missing,
+                              void* stream_) {
+  SDPA_TRY(check_pages(p, p ? p->b : 1, true));
+  if (p->b > sdpa::kMaxPageRows) SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "%d rows not supported (1..%d)", p->b, sdpa::kMaxPageRows);
+  SDPA_TRY(words("new_lens", new_lens));
+  SDPA_TRY(words("src", src));
+  SDPA_TRY(words("dst", dst));
+  SDPA_TRY(words("missing", missing));
+  if (overlap(src, p->b, dst, p->b)) SDPA_REFUSE(SDPA_ERR_LAYOUT, "src and dst must lie apart");
+  log_pages("grow", p, 0);
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  cudaError_t e = sdpa::launch_grow(pages_params(p), new_lens, src, dst, missing, stream);
+  return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, "sdpa_cache_grow"));
+}
+
+sdpa_status_t sdpa_cache_free(const sdpa_pages_t* p, const int32_t* keep_lens, void* stream_) {
+  SDPA_TRY(check_pages(p, p ? p->b : 1, true));
+  SDPA_TRY(words("keep_lens", keep_lens));
+  log_pages("free", p, 0);
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  cudaError_t e = sdpa::launch_free(pages_params(p), keep_lens, stream);
+  return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, "sdpa_cache_free"));
+}
+
+sdpa_status_t sdpa_cache_compact(const sdpa_pages_t* p, int32_t* src, int32_t* dst, int32_t pairs, void* stream_) {
+  SDPA_TRY(check_pages(p, p ? p->b : 1, true));
+  if (pairs < 1) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "sizes must be >= 1 (pairs=%d)", pairs);
+  SDPA_TRY(words("src", src));
+  SDPA_TRY(words("dst", dst));
+  if (overlap(src, pairs, dst, pairs)) SDPA_REFUSE(SDPA_ERR_LAYOUT, "src and dst must lie apart");
+  log_pages("compact", p, pairs);
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  cudaError_t e = sdpa::launch_compact(pages_params(p), src, dst, pairs, stream);
+  return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, "sdpa_cache_compact"));
+}
+
+sdpa_status_t sdpa_cache_copy(const sdpa_cache_t* c, const int32_t* src, const int32_t* dst, int32_t pairs, void* stream_) {
+  SDPA_TRY(check_stored(c));
+  if (pairs < 1) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "sizes must be >= 1 (pairs=%d)", pairs);
+  SDPA_TRY(words("src", src));
+  SDPA_TRY(words("dst", dst));
+  const int es = c->dtype == SDPA_DTYPE_E4M3 ? 1 : 2;
+  if (static_cast<int64_t>(c->h_kv) * c->page_size * c->d >= (int64_t(1) << 31)) SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "h_kv*page_size*d too large");
+  sdpa::CopyParams prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.t[0] = copy_tensor(c->k, c->k_strides, c, es);
+  prm.t[1] = copy_tensor(c->v, c->v_strides, c, es);
+  prm.t[2] = copy_scales(c->k_scale, c);
+  prm.t[3] = copy_scales(c->v_scale, c);
+  prm.num_pages = c->num_pages;
+  if (sdpa::api_log_level() >= 1)
+    fprintf(stderr, "[sdpa] copy pairs=%d h_kv=%d d=%d cache=%d page=%d\n", pairs, c->h_kv, c->d, c->dtype, c->page_size);
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  cudaError_t e = sdpa::launch_copy(prm, src, dst, pairs, sdpa::api_num_sms(), stream);
+  return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, "sdpa_cache_copy"));
+}
+
+sdpa_status_t sdpa_cache_keep(const sdpa_cache_t* c, const int32_t* path, const int32_t* accepted, int32_t s,
+                              const int32_t* seq_lens_q, void* stream_) {
+  SDPA_TRY(check_cache(c));
+  if (s < 1) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "sizes must be >= 1 (s=%d)", s);
+  SDPA_TRY(words("path", path));
+  SDPA_TRY(words("accepted", accepted));
+  if (reinterpret_cast<uintptr_t>(seq_lens_q) % 4) SDPA_REFUSE(SDPA_ERR_LAYOUT, "seq_lens_q must be 4-byte aligned");
+  sdpa::KeepParams prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.c = cache_args(c);
+  prm.seq_lens_q = seq_lens_q;
+  prm.path = path;
+  prm.accepted = accepted;
+  prm.s = s;
+  prm.row_units = c->d * (c->dtype == SDPA_DTYPE_E4M3 ? 1 : 2) / 16;
+  if (static_cast<int64_t>(c->h_kv) * (prm.row_units + 1) >= (int64_t(1) << 30)) SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "h_kv too large");
+  if (sdpa::api_log_level() >= 1)
+    fprintf(stderr, "[sdpa] keep b=%d s=%d h_kv=%d d=%d cache=%d page=%d\n", c->b, s, c->h_kv, c->d, c->dtype, c->page_size);
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  cudaError_t e = sdpa::launch_keep(prm, stream);
+  return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, "sdpa_cache_keep"));
+}
+
+sdpa_status_t sdpa_verify(const sdpa_verify_t* p, void* stream_) {
+  if (p == nullptr) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "verify descriptor is NULL");
+  if (p->b < 1 || p->s < 1 || p->vocab < 1)
+    SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "sizes must be >= 1 (b=%d s=%d vocab=%d)", p->b, p->s, p->vocab);
+  if (p->s > sdpa::kVerifyRows) SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "%d rows not supported (1..%d)", p->s, sdpa::kVerifyRows);
+  if (p->vocab > (1 << 20)) SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "vocabulary of %d not supported (1..2^20)", p->vocab);
+  if (p->b > (1 << 24)) SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "b too large");
+  if (!is16(p->dtype) && p->dtype != SDPA_DTYPE_F32)
+    SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "probabilities are F16, BF16 or F32 (dtype %d)", p->dtype);
+  if (p->parents && p->draft_probs)
+    SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "draft_probs are those of a chain: parents must be NULL");
+  const int es = p->dtype == SDPA_DTYPE_F32 ? 4 : 2;
+  SDPA_TRY(words("tokens", p->tokens));
+  SDPA_TRY(words("uniform", p->uniform));
+  SDPA_TRY(words("accepted", p->accepted));
+  SDPA_TRY(words("path", p->path));
+  SDPA_TRY(words("new_tokens", p->new_tokens));
+  if (reinterpret_cast<uintptr_t>(p->parents) % 4 || reinterpret_cast<uintptr_t>(p->seq_lens_q) % 4)
+    SDPA_REFUSE(SDPA_ERR_LAYOUT, "parents and seq_lens_q must be 4-byte aligned");
+  if (p->probs == nullptr) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "probs: null pointer");
+  if (reinterpret_cast<uintptr_t>(p->probs) % es || reinterpret_cast<uintptr_t>(p->draft_probs) % es)
+    SDPA_REFUSE(SDPA_ERR_LAYOUT, "probs and draft_probs must be aligned to their elements");
+  if (p->probs_b < 0 || p->probs_s < 0 || p->draft_b < 0 || p->draft_s < 0)
+    SDPA_REFUSE(SDPA_ERR_LAYOUT, "strides of probs and draft_probs must not be negative");
+  sdpa::VerifyParams prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.tokens = p->tokens;
+  prm.parents = p->parents;
+  prm.seq_lens_q = p->seq_lens_q;
+  prm.uniform = p->uniform;
+  prm.probs = p->probs;
+  prm.probs_b = p->probs_b;
+  prm.probs_s = p->probs_s;
+  prm.draft = p->draft_probs;
+  prm.draft_b = p->draft_b;
+  prm.draft_s = p->draft_s;
+  prm.accepted = p->accepted;
+  prm.path = p->path;
+  prm.new_tokens = p->new_tokens;
+  prm.b = p->b;
+  prm.s = p->s;
+  prm.vocab = p->vocab;
+  if (sdpa::api_log_level() >= 1)
+    fprintf(stderr, "[sdpa] verify b=%d s=%d vocab=%d dt=%d tree=%d draft=%d\n", p->b, p->s, p->vocab, p->dtype, p->parents != nullptr,
+            p->draft_probs != nullptr);
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  cudaError_t e = sdpa::launch_verify(prm, p->dtype, sdpa::api_num_sms(), stream);
+  return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, "sdpa_verify"));
+}
+
 size_t sdpa_serving_struct_size(int which) {
   switch (which) {
     case 0: return sizeof(sdpa_rope_table_t);
@@ -368,6 +660,9 @@ size_t sdpa_serving_struct_size(int which) {
     case 2: return sizeof(sdpa_cache_t);
     case 3: return sizeof(sdpa_cache_rows_t);
     case 4: return sizeof(sdpa_decode_t);
+    case 5: return sizeof(sdpa_rope_axes_t);
+    case 6: return sizeof(sdpa_pages_t);
+    case 7: return sizeof(sdpa_verify_t);
     default: return 0;
   }
 }

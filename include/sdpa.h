@@ -68,7 +68,8 @@ typedef enum {
   SDPA_DTYPE_F16 = 0,         /* IEEE binary16 */
   SDPA_DTYPE_BF16 = 1,        /* bfloat16 */
   SDPA_DTYPE_E4M3 = 2,        /* OCP FP8 E4M3 (finite max 448): Q, K, V (forward and backward) */
-  SDPA_DTYPE_E5M2 = 3         /* OCP FP8 E5M2 (max 57344): dO of an FP8 backward pass only */
+  SDPA_DTYPE_E5M2 = 3,        /* OCP FP8 E5M2 (max 57344): dO of an FP8 backward pass only */
+  SDPA_DTYPE_F32 = 4          /* IEEE binary32: probabilities of sdpa_verify only */
 } sdpa_dtype_t;
 
 /* Element strides of a logical [b][h][s][d] view.  d must be 1. */
@@ -317,6 +318,22 @@ SDPA_API sdpa_status_t sdpa_rope_fwd(const sdpa_rope_t* p, const void* q, const 
 SDPA_API sdpa_status_t sdpa_rope_bwd(const sdpa_rope_t* p, const void* dq_out, const void* dk_out, void* dq,
                                      void* dk, void* stream);
 
+/* Positions with several axes (time, row and column of an image's or a clip's tokens, say): pair i of a head turns by the
+ * position on its own axis, t = positions[axis[i]] * f_i; the table holds f_i pair by pair, as ever (for axes with
+ * frequencies of their own, one axis's table behind the other's). */
+typedef struct {
+  int32_t axes;             /* 1..4 */
+  uint8_t axis[256];        /* the axis of each of the rot/2 pairs, below `axes` */
+  int64_t axis_stride;      /* elements between two axes of positions */
+} sdpa_rope_axes_t;
+
+/* sdpa_rope_fwd and sdpa_rope_bwd with p->positions DEVICE [axes][b][s] (not NULL; positions_stride between batches, 0:
+ * one row for all). */
+SDPA_API sdpa_status_t sdpa_rope_axes_fwd(const sdpa_rope_t* p, const sdpa_rope_axes_t* a, const void* q, const void* k,
+                                          void* q_out, void* k_out, void* stream);
+SDPA_API sdpa_status_t sdpa_rope_axes_bwd(const sdpa_rope_t* p, const sdpa_rope_axes_t* a, const void* dq_out,
+                                          const void* dk_out, void* dq, void* dk, void* stream);
+
 /* A paged key/value cache.  Position j of sequence i lives in page page_table[i][j / page_size],
  * slot j % page_size.  Keys and values are logical [num_pages][h_kv][page_size][d] views (the
  * fields b, h, s, d of the strides are page, head, slot, element), so a page may be stored
@@ -365,6 +382,10 @@ typedef struct {
 SDPA_API sdpa_status_t sdpa_cache_write(const sdpa_cache_t* c, const sdpa_cache_rows_t* r, const void* k,
                                         const void* v, void* stream);
 
+/* sdpa_cache_write with r->rope (not NULL) and its positions DEVICE [axes][b][s] (not NULL). */
+SDPA_API sdpa_status_t sdpa_cache_write_axes(const sdpa_cache_t* c, const sdpa_cache_rows_t* r, const sdpa_rope_axes_t* a,
+                                             const void* k, const void* v, void* stream);
+
 /* Reads positions 0 .. s-1 of each sequence into dense rows, code * scale rounded once; rows at
  * len_kv and behind are zeros (as sdpa_fwd with seq_lens_kv wants its padding). */
 SDPA_API sdpa_status_t sdpa_cache_read(const sdpa_cache_t* c, const sdpa_cache_rows_t* r, void* k, void* v,
@@ -402,8 +423,106 @@ SDPA_API sdpa_status_t sdpa_decode_workspace_size(const sdpa_cache_t* c, const s
 SDPA_API sdpa_status_t sdpa_decode(const sdpa_cache_t* c, const sdpa_decode_t* p, const void* q, void* o,
                                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Pages: who owns which page of a cache, and pages and rows moved inside it.
+ *
+ * Every page has a count of its owners: the rows of page tables that reach it, and what else the caller counts
+ * (a prefix that it keeps for later, say).  A page is free iff its count is 0.  The calls below change
+ * counts and page tables on the device, without a copy to the host; they touch no keys and values, since the layers
+ * of a model share a page table: where pages have to be copied they list them, and sdpa_cache_copy is
+ * called for each layer's cache.
+ *
+ * A sequence of n tokens reaches columns 0 .. ceil(n / page_size) - 1 of its row; other columns are neither read nor
+ * counted.  Lengths are clamped as in sdpa_cache_t.  Entries outside [0, num_pages) are missing pages: they have
+ * no count.  Counts must be at least the number of reaching entries.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct {
+  int32_t num_pages;            /* >= 1 */
+  int32_t page_size;            /* a multiple of 16 */
+  int32_t b;                    /* rows of page_table: sequences */
+  int32_t max_pages;            /* columns */
+  const int32_t* page_table;    /* DEVICE [b][max_pages] */
+  int64_t page_table_stride;
+  const int32_t* seq_lens;      /* DEVICE [b]: tokens of each sequence */
+  const int32_t* ref_counts;    /* DEVICE [num_pages] */
+  int32_t* page_table_out;      /* DEVICE: may be page_table with its stride, otherwise apart from it (sdpa_cache_fork: always) */
+  int64_t page_table_out_stride;
+  int32_t* ref_counts_out;      /* DEVICE [num_pages]: may be ref_counts, otherwise apart from it */
+} sdpa_pages_t;
+
+/* Row i < b_out of the new table takes over sequence parents[i] with its pages (shared, none copied): parents DEVICE [b_out],
+ * a value outside [0, b) gives an empty sequence.  Columns not reached are -1.  seq_lens_out: DEVICE [b_out].  The old
+ * rows' ownership ends: sequences that nobody takes over are freed.  (A sequence that goes on beside its copies
+ * is one of its own parents.)  Outputs lie apart from page_table and seq_lens. */
+SDPA_API sdpa_status_t sdpa_cache_fork(const sdpa_pages_t* p, const int32_t* parents, int32_t b_out, int32_t* seq_lens_out,
+                                       void* stream);
+
+/* Room for sequences to grow from seq_lens to new_lens (DEVICE [b]; a shorter one changes nothing).  Every column that
+ * new_lens reaches and seq_lens does not gets a free page, lowest first in the order of rows and columns.  A
+ * partly filled page that others own too is replaced as well, by all of the rows that grow in it but the last owner: the free page takes its
+ * column's place in that order, and (src[i], dst[i]) is the copy that row i needs before it is written
+ * (DEVICE [b] each; -1, -1: none).  All or nothing: *missing (DEVICE) is 0, or the number of pages that
+ * lacked, and nothing is changed then (outputs that lie apart are copies).  At most 4096 rows. */
+SDPA_API sdpa_status_t sdpa_cache_grow(const sdpa_pages_t* p, const int32_t* new_lens, int32_t* src, int32_t* dst,
+                                       int32_t* missing, void* stream);
+
+/* Gives back the columns that seq_lens reaches and keep_lens (DEVICE [b], clamped to [0, seq_lens]) does not: their entries
+ * become -1, their pages lose an owner. */
+SDPA_API sdpa_status_t sdpa_cache_free(const sdpa_pages_t* p, const int32_t* keep_lens, void* stream);
+
+/* Moves pages together, so that n pages in use are pages 0 .. n-1: the k-th page in use at or behind n becomes the k-th free
+ * one before it, at most `pairs` of them in one call.  src and dst (DEVICE [pairs], src ascending, -1 behind the
+ * last) list the copies to make before the pages are read again; src pages are free from then on.  Owners that are not in
+ * this page table find their pages' new names in the lists. */
+SDPA_API sdpa_status_t sdpa_cache_compact(const sdpa_pages_t* p, int32_t* src, int32_t* dst, int32_t pairs, void* stream);
+
+/* Copies pages src[i] to dst[i] of K, V and their scales (DEVICE [pairs] each).  Pairs with an entry outside
+ * [0, num_pages) are passed over.  No page may be the target of two pairs, nor target of one and source of another.
+ * Of c the page table, b, max_pages and seq_lens_kv are not read. */
+SDPA_API sdpa_status_t sdpa_cache_copy(const sdpa_cache_t* c, const int32_t* src, const int32_t* dst, int32_t pairs, void* stream);
+
+/* Keeps some of the newest tokens: of the last len_q positions of each sequence (seq_lens_q DEVICE [b], clamped to [0, s], or
+ * NULL: s), row path[i][j] moves to row j for all j < accepted[i].  path: DEVICE [b][s], ascending in the
+ * part that is read (as sdpa_verify gives it); entries outside [0, len_q) move nothing.  accepted: DEVICE [b].  Lengths are the
+ * caller's: seq_lens_kv - len_q + accepted afterwards; rows behind that are left as they come.  K, V and their scales. */
+SDPA_API sdpa_status_t sdpa_cache_keep(const sdpa_cache_t* c, const int32_t* path, const int32_t* accepted, int32_t s,
+                                       const int32_t* seq_lens_q, void* stream);
+
+/* Drafted tokens verified against the target's probabilities (speculative sampling: Leviathan et al., Chen et al., 2023; without
+ * draft_probs a tree of candidates as in Miao et al., 2023). */
+typedef struct {
+  int32_t b;                    /* sequences */
+  int32_t s;                    /* rows of each, 1..1024: row 0 the newest token that is decided, the others drafted */
+  int32_t vocab;                /* 1..2^20 */
+  int32_t dtype;                /* F16, BF16 or F32, of probs and draft_probs */
+  const int32_t* tokens;        /* DEVICE [b][s]; row 0's is not read.  A token outside [0, vocab) is refused */
+  const int32_t* parents;       /* DEVICE [b][s]: the row that row i > 0 follows, below i (rows with any other value, and rows
+                                   behind those, are never accepted); row 0's is not read.  NULL: a chain, i - 1 */
+  const int32_t* seq_lens_q;    /* DEVICE [b] rows that take part (clamped to [0, s]; 0: nothing is accepted and no token drawn), or NULL: s */
+  const float* uniform;         /* DEVICE [b][s]: random numbers in [0, 1): row 0's draws the new token, the others test their rows */
+  const void* probs;            /* DEVICE [b][s][vocab], strides below (elements; vocab: 1): the target's distribution behind each row */
+  int64_t probs_b, probs_s;
+  const void* draft_probs;      /* DEVICE [b][s][vocab], or NULL: the distribution that row i > 0 was drawn from.  Chains only */
+  int64_t draft_b, draft_s;
+  int32_t* accepted;            /* DEVICE [b]: accepted rows, row 0 among them */
+  int32_t* path;                /* DEVICE [b][s]: those rows in order, -1 behind them */
+  int32_t* new_tokens;          /* DEVICE [b][s]: the tokens of rows path[1..], and the new one: `accepted` tokens, -1 behind them */
+} sdpa_verify_t;
+
+/* Children of an accepted row n are tried in ascending order.  Child i with token x is accepted iff
+ *   uniform[i] * draft_probs[i][x] < probs[n][x]                                    with draft_probs, or
+ *   uniform[i] * max(0, 1 - sum of probs[n][x'] of refused siblings) < probs[n][x]  without (a token that an earlier sibling has
+ *                                                                                   too is refused).
+ * The new token is drawn behind the last accepted row n: from max(probs[n] - draft_probs[i], 0) where a chain's row i was refused,
+ * from probs[n] without its children's tokens where there are no draft_probs; from probs[n] where that leaves nothing.
+ * Tokens so chosen are distributed as the target's own.  In sums and draws a probability counts as a whole number of 2^-42
+ * (values outside [0, 1] as the nearer end, NaN as 0): the new token is the first whose running sum exceeds
+ * floor(uniform[0] * 2^31) / 2^31 of the total, whatever the order of the sums.  Where the total is 0 it is -1. */
+SDPA_API sdpa_status_t sdpa_verify(const sdpa_verify_t* p, void* stream);
+
 /* sizeof of the structs above as compiled into the library: which = 0 sdpa_rope_table_t,
- * 1 sdpa_rope_t, 2 sdpa_cache_t, 3 sdpa_cache_rows_t, 4 sdpa_decode_t (0 for any other). */
+ * 1 sdpa_rope_t, 2 sdpa_cache_t, 3 sdpa_cache_rows_t, 4 sdpa_decode_t, 5 sdpa_rope_axes_t, 6 sdpa_pages_t,
+ * 7 sdpa_verify_t (0 for any other). */
 SDPA_API size_t sdpa_serving_struct_size(int which);
 
 /* Message for the last non-OK status returned on the calling thread ("" if none).  The
