@@ -289,6 +289,7 @@ struct CopyTensor {
   int inner_n;                   // rows of the inner dimension
   int row_units;
   int units;                     // of a page (0: no such tensor)
+  int flat;                      // a page is one piece; filled in by launch_copy
 };
 
 struct CopyParams {

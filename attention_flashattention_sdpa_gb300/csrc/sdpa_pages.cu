@@ -12,11 +12,9 @@
 //   keep     rows of the newest tokens move to the front of them
 //
 // The first four are integer work on tables of a few hundred thousand entries at most, bound by latency: one
-// cluster of 8 CTAs each, whose barrier stands between the passes that depend on each other (counts before
-// ids, copies of counts before atomics on them), so that each is one launch and needs no workspace.  Atomics are
-// sums of integers: their order changes nothing.
-#include <type_traits>
-
+// cluster of CTAs each (a single CTA for small tables), whose barrier stands between the passes that depend on each
+// other (counts before ids, copies of counts before atomics on them), so that each is one launch and needs no
+// workspace.  Atomics are sums of integers: their order changes nothing.
 #include "ptx.cuh"
 #include "sdpa_internal.h"
 
@@ -24,20 +22,36 @@ namespace sdpa {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kCluster = 8;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kChunk = 128;          // columns of a row that a warp takes at once
+constexpr int kEach = 4;             // counts a thread takes at once
+constexpr int kTile = kThreads * kEach;
 
-// The CTA's share of n items in runs of kThreads * kEach, and this thread's number in the cluster.
-__device__ __forceinline__ int cluster_rank() { return static_cast<int>(blockIdx.x); }
-__device__ __forceinline__ int64_t cluster_thread() { return static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; }
+// The CTAs of a launch are one cluster: of one CTA for small work, of 8 otherwise.
+__device__ __forceinline__ int rank() { return static_cast<int>(blockIdx.x); }
+__device__ __forceinline__ int ranks() { return static_cast<int>(gridDim.x); }
+
+__device__ __forceinline__ void sync_all() {
+  if (gridDim.x > 1) ptx::cluster_sync_all();
+  else __syncthreads();
+}
+
+// Whatever ran before is done; what comes next may be put in place meanwhile (it waits here in its turn).
+__device__ __forceinline__ void begin() {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+}
 
 struct Range {
   int lo, hi;
 };
 
-__device__ __forceinline__ Range share(int n) {
-  const int per = (n + kCluster - 1) / kCluster;
-  return {min(n, cluster_rank() * per), min(n, (cluster_rank() + 1) * per)};
+// Pages that CTA `k` looks after.
+__device__ __forceinline__ Range share(int n, int k) {
+  const int per = (n + ranks() - 1) / ranks();
+  return {static_cast<int>(min(static_cast<int64_t>(n), static_cast<int64_t>(k) * per)),
+          static_cast<int>(min(static_cast<int64_t>(n), static_cast<int64_t>(k + 1) * per))};
 }
 
 // Exclusive prefix sum over the CTA's threads of x; the total in `total`.  `tmp`: kWarps + 1 words.
@@ -51,116 +65,151 @@ __device__ __forceinline__ int block_scan(int x, int* tmp, int& total) {
   }
   if (lane == 31) tmp[warp] = inc;
   __syncthreads();
-  if (warp == 0) {
-    const int mine = tmp[lane];
-    int w = mine;
+  // (Every warp adds up the warps for itself: one barrier less than a warp that does it for all.)
+  int w = tmp[lane];
+  const int mine = w;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    tmp[lane] = w - mine;
-    if (lane == 31) tmp[kWarps] = w;
+  for (int o = 1; o < 32; o *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
-  __syncthreads();
-  const int before = tmp[warp] + inc - x;
-  total = tmp[kWarps];
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w - mine, warp) + inc - x;
   __syncthreads();
   return before;
 }
 
-__device__ __forceinline__ int clamp_tokens(const int32_t* lens, int i, int top) { return min(max(__ldg(lens + i), 0), top); }
-
-__device__ __forceinline__ bool is_page(int page, int n) { return page >= 0 && page < n; }
-
-// Word `at` of CTA `rank`'s shared memory.
-__device__ __forceinline__ int ld_cluster(const int* at, int rank) {
-  uint32_t a;
-  int x;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(at)), "r"(rank));
-  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
-  return x;
+__device__ __forceinline__ int block_sum(int x, int* tmp) {
+  x = __reduce_add_sync(0xffffffffu, x);
+  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = x;
+  __syncthreads();
+  const int total = __reduce_add_sync(0xffffffffu, tmp[threadIdx.x & 31]);
+  __syncthreads();
+  return total;
 }
 
-// Counts as they are, where they are wanted elsewhere; the barrier before anyone adds to them.
-__device__ __forceinline__ void copy_counts(const PagesParams& p) {
-  if (p.ref_counts_out == p.ref_counts) return;
-  for (int64_t i = cluster_thread(); i < p.num_pages; i += kCluster * kThreads) p.ref_counts_out[i] = p.ref_counts[i];
+// x of every CTA, in every CTA: all[k] is that of CTA k afterwards (the barrier is the cluster's).  The CTAs of the cluster
+// have all begun by the first barrier, so this one comes first where it is the first.
+__device__ __forceinline__ void exchange(int x, int* all, bool first) {
+  if (gridDim.x == 1) {
+    if (threadIdx.x == 0) all[0] = x;
+    __syncthreads();
+    return;
+  }
+  if (first) ptx::cluster_sync_all();
+  if (threadIdx.x < gridDim.x) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(all + rank())), "r"(threadIdx.x));
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+  }
   ptx::cluster_sync_all();
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+__device__ __forceinline__ int clamp_tokens(const int32_t* lens, int i, int top) { return min(max(__ldg(lens + i), 0), top); }
+
+__device__ __forceinline__ int columns_of(const PagesParams& p, int len) {
+  return static_cast<int>((static_cast<int64_t>(len) + p.page_size - 1) / p.page_size);
+}
+
+__device__ __forceinline__ bool is_page(int page, int n) { return page >= 0 && page < n; }
+
+// f(row, first column) for every piece of kChunk columns of `rows` rows, a warp each.
+template <typename F>
+__device__ __forceinline__ void for_chunks(int rows, int columns, F f) {
+  const uint32_t chunks = (columns + kChunk - 1) / kChunk, n = chunks * rows;
+  for (uint32_t x = rank() * kWarps + (threadIdx.x >> 5); x < n; x += ranks() * kWarps) {
+    const uint32_t i = x / chunks;
+    f(static_cast<int>(i), static_cast<int>((x - i * chunks) * kChunk));
+  }
+}
+
+// Counts as they are, where they are wanted elsewhere, before anyone adds to them.
+__device__ __forceinline__ void copy_counts(const PagesParams& p) {
+  if (p.ref_counts_out == p.ref_counts) return;
+  for (int64_t i = rank() * kThreads + threadIdx.x; i < p.num_pages; i += ranks() * kThreads) p.ref_counts_out[i] = p.ref_counts[i];
+  sync_all();
+}
+
+__global__ void __launch_bounds__(kThreads)
     fork_kernel(const __grid_constant__ PagesParams p, const int32_t* parents, int b_out, int32_t* seq_lens_out) {
+  begin();
   copy_counts(p);
-  // The new rows first, entry by entry, then the old ones' ownership ends.
-  const int64_t made = static_cast<int64_t>(b_out) * p.max_pages, gone = static_cast<int64_t>(p.b) * p.max_pages;
-  for (int64_t x = cluster_thread(); x < made + gone; x += kCluster * kThreads) {
-    const bool is_new = x < made;
-    const int64_t y = is_new ? x : x - made;
-    const int i = static_cast<int>(y / p.max_pages), c = static_cast<int>(y - static_cast<int64_t>(i) * p.max_pages);
-    const int j = is_new ? __ldg(parents + i) : i;
-    const bool there = j >= 0 && j < p.b;
-    const int len = there ? clamp_tokens(p.seq_lens, j, p.max_len) : 0;
-    const int page = c * static_cast<int64_t>(p.page_size) < len ? __ldg(p.page_table + j * p.table_stride + c) : -1;
-    if (is_page(page, p.num_pages)) atomicAdd(p.ref_counts_out + page, is_new ? 1 : -1);
-    if (is_new) {
-      p.page_table_out[i * p.table_out_stride + c] = page;
-      if (c == 0) seq_lens_out[i] = len;
+  const int lane = threadIdx.x & 31;
+  // The new rows, and the old ones, whose ownership ends.
+  for_chunks(b_out + p.b, p.max_pages, [&](int x, int c0) {
+    const bool is_new = x < b_out;
+    const int j = is_new ? __ldg(parents + x) : x - b_out, len = j >= 0 && j < p.b ? clamp_tokens(p.seq_lens, j, p.max_len) : 0;
+    const int reach = columns_of(p, len);
+    if (is_new && c0 == 0 && lane == 0) seq_lens_out[x] = len;
+    int page[kChunk / 32];
+#pragma unroll
+    for (int k = 0; k < kChunk / 32; ++k) {
+      const int c = c0 + lane + 32 * k;
+      page[k] = c < reach ? __ldg(p.page_table + j * p.table_stride + c) : -1;
     }
-  }
+#pragma unroll
+    for (int k = 0; k < kChunk / 32; ++k) {
+      const int c = c0 + lane + 32 * k;
+      if (is_page(page[k], p.num_pages)) atomicAdd(p.ref_counts_out + page[k], is_new ? 1 : -1);
+      if (is_new && c < p.max_pages) p.page_table_out[x * p.table_out_stride + c] = page[k];
+    }
+  });
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
-    free_kernel(const __grid_constant__ PagesParams p, const int32_t* keep_lens) {
+__global__ void __launch_bounds__(kThreads) free_kernel(const __grid_constant__ PagesParams p, const int32_t* keep_lens) {
+  begin();
   copy_counts(p);
-  const int64_t n = static_cast<int64_t>(p.b) * p.max_pages;
+  const int lane = threadIdx.x & 31;
   const bool in_place = p.page_table_out == p.page_table;
-  for (int64_t x = cluster_thread(); x < n; x += kCluster * kThreads) {
-    const int i = static_cast<int>(x / p.max_pages), c = static_cast<int>(x - static_cast<int64_t>(i) * p.max_pages);
+  for_chunks(p.b, p.max_pages, [&](int i, int c0) {
     const int len = clamp_tokens(p.seq_lens, i, p.max_len), keep = min(len, max(0, __ldg(keep_lens + i)));
-    const int64_t first = c * static_cast<int64_t>(p.page_size);
-    const bool ends = first >= keep && first < len;
-    if (in_place && !ends) continue;
-    const int page = p.page_table[i * p.table_stride + c];
-    if (ends && is_page(page, p.num_pages)) atomicSub(p.ref_counts_out + page, 1);
-    p.page_table_out[i * p.table_out_stride + c] = ends ? -1 : page;
-  }
+    const int first = columns_of(p, keep), end = columns_of(p, len);
+    int page[kChunk / 32];
+#pragma unroll
+    for (int k = 0; k < kChunk / 32; ++k) {
+      const int c = c0 + lane + 32 * k;
+      page[k] = c < p.max_pages && (!in_place || (c >= first && c < end)) ? p.page_table[i * p.table_stride + c] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kChunk / 32; ++k) {
+      const int c = c0 + lane + 32 * k;
+      const bool ends = c >= first && c < end;
+      if (ends && is_page(page[k], p.num_pages)) atomicSub(p.ref_counts_out + page[k], 1);
+      if (ends || (!in_place && c < p.max_pages)) p.page_table_out[i * p.table_out_stride + c] = ends ? -1 : page[k];
+    }
+  });
 }
 
-// Rows of a grow that are looked at: their pages' order, and which page each copies.
 struct GrowShared {
   int base[kMaxPageRows + 1];   // pages wanted by the rows before this one
-  int tail[kMaxPageRows];       // a partly filled page that has other owners, or -1; -2 - page where it is kept after all
-  int tmp[kWarps + 1];
-  int free_here;
+  int tail[kMaxPageRows];       // the partly filled page to replace, or -1; -2 - page: it has other owners, but is kept
+  int tmp[kWarps];
+  int free[kMaxCluster];        // free pages of each CTA's share
 };
 
 struct GrowRow {
-  int tail;            // column of the partly filled page
+  int tail;            // column of the partly filled page that is written on, or -1
   int first, end;      // columns to fill
 };
 
 __device__ __forceinline__ GrowRow grow_row(const PagesParams& p, const int32_t* new_lens, int i) {
   const int old_len = clamp_tokens(p.seq_lens, i, p.max_len), new_len = clamp_tokens(new_lens, i, p.max_len);
   GrowRow r;
-  r.first = (old_len + p.page_size - 1) / p.page_size;
-  r.end = max(r.first, (new_len + p.page_size - 1) / p.page_size);
-  r.tail = new_len > old_len && old_len % p.page_size ? old_len / p.page_size : -1;
+  r.first = columns_of(p, old_len);
+  r.end = max(r.first, columns_of(p, new_len));
+  r.tail = new_len > old_len && r.first * static_cast<int64_t>(p.page_size) != old_len ? r.first - 1 : -1;
   return r;
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads)
     grow_kernel(const __grid_constant__ PagesParams p, const int32_t* new_lens, int32_t* src, int32_t* dst, int32_t* missing) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  GrowShared& sh = *reinterpret_cast<GrowShared*>(smem_raw);
-  const int rank = cluster_rank(), tid = threadIdx.x;
-
-  // Free pages of this CTA's share.
-  const Range mine = share(p.num_pages);
-  int free_count = 0, total = 0;
+  __shared__ GrowShared sh;
+  begin();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const Range mine = share(p.num_pages, rank());
+  int free_count = 0;
   for (int i = mine.lo + tid; i < mine.hi; i += kThreads) free_count += p.ref_counts[i] == 0;
-  block_scan(free_count, sh.tmp, total);
-  if (tid == 0) sh.free_here = total;
+  free_count = block_sum(free_count, sh.tmp);
 
   // Every CTA looks at all rows: their partly filled pages that others own too ...
   for (int i = tid; i < p.b; i += kThreads) {
@@ -171,10 +220,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   }
   __syncthreads();
   // ... of which, row after row, all but the last owner take a copy, ...
-  int row_base = 0;
+  int wanted = 0;
   for (int i0 = 0; i0 < p.b; i0 += kThreads) {
     const int i = i0 + tid;
-    int want = 0;
+    int want = 0, total = 0;
     bool keeps = false;
     if (i < p.b) {
       const GrowRow r = grow_row(p, new_lens, i);
@@ -189,180 +238,237 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     }
     const int before = block_scan(want, sh.tmp, total);
     if (i < p.b) {
-      sh.base[i] = row_base + before;
-      if (keeps) sh.tail[i] = -2 - sh.tail[i];    // (still told from another page by the rows behind it)
+      sh.base[i] = wanted + before;
+      if (keeps) sh.tail[i] = -2 - sh.tail[i];
     }
-    row_base += total;
+    wanted += total;
     __syncthreads();
   }
-  if (tid == 0) sh.base[p.b] = row_base;
+  if (tid == 0) sh.base[p.b] = wanted;
   // ... and how many pages that makes.  Behind the barrier the counts and the table may change.
-  ptx::cluster_sync_all();
-  int before = 0, all = 0;
-  for (int k = 0; k < kCluster; ++k) {
-    const int n = ld_cluster(&sh.free_here, k);
-    before += k < rank ? n : 0;
-    all += n;
-  }
-  const bool granted = row_base <= all;
-  if (rank == 0 && tid == 0) *missing = granted ? 0 : row_base - all;
+  exchange(free_count, sh.free, true);
+  const int there = lane < ranks() ? sh.free[lane] : 0;
+  const int all = __reduce_add_sync(0xffffffffu, there);
+  int before = __reduce_add_sync(0xffffffffu, lane < rank() ? there : 0);
+  const bool granted = wanted <= all;
+  if (rank() == 0 && tid == 0) *missing = granted ? 0 : wanted - all;
 
   // Entries that stay as they are.
-  if (p.page_table_out != p.page_table) {
-    const int64_t n = static_cast<int64_t>(p.b) * p.max_pages;
-    for (int64_t x = cluster_thread(); x < n; x += kCluster * kThreads) {
-      const int i = static_cast<int>(x / p.max_pages), c = static_cast<int>(x - static_cast<int64_t>(i) * p.max_pages);
+  if (p.page_table_out != p.page_table)
+    for_chunks(p.b, p.max_pages, [&](int i, int c0) {
       const GrowRow r = grow_row(p, new_lens, i);
-      const bool filled = (c >= r.first && c < r.end) || (c == r.tail && sh.tail[i] >= 0);
-      if (!(granted && filled)) p.page_table_out[i * p.table_out_stride + c] = p.page_table[i * p.table_stride + c];
-    }
-  }
-  for (int i = static_cast<int>(cluster_thread()); i < p.b; i += kCluster * kThreads) {
+      const int tail = sh.tail[i] >= 0 ? r.tail : -1;
+#pragma unroll
+      for (int k = 0; k < kChunk / 32; ++k) {
+        const int c = c0 + lane + 32 * k;
+        if (c < p.max_pages && !(granted && ((c >= r.first && c < r.end) || c == tail)))
+          p.page_table_out[i * p.table_out_stride + c] = p.page_table[i * p.table_stride + c];
+      }
+    });
+  for (int i = rank() * kThreads + tid; i < p.b; i += ranks() * kThreads) {
     const bool copied = granted && sh.tail[i] >= 0;
     src[i] = copied ? sh.tail[i] : -1;
     if (!copied) dst[i] = -1;
   }
   // The k-th free page goes to the row whose run of wanted pages holds k.
   const bool elsewhere = p.ref_counts_out != p.ref_counts;
-  for (int i0 = mine.lo; i0 < mine.hi; i0 += kThreads) {
-    if (!elsewhere && (!granted || before >= row_base)) break;
-    const int page = i0 + tid;
-    const int count = page < mine.hi ? p.ref_counts[page] : 1;
-    const int k = before + block_scan(count == 0, sh.tmp, total);
-    before += total;
-    const bool given = granted && count == 0 && k < row_base;
-    if (page < mine.hi && (elsewhere || given)) p.ref_counts_out[page] = given ? 1 : count;
-    if (!given) continue;
-    int lo = 0, hi = p.b;                        // base[lo] <= k < base[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (sh.base[mid] <= k) lo = mid;
-      else hi = mid;
+  for (int i0 = mine.lo; i0 < mine.hi; i0 += kTile) {
+    if (!elsewhere && (!granted || before >= wanted)) break;
+    int count[kEach], here = 0, total = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int page = i0 + tid * kEach + e;
+      count[e] = page < mine.hi ? p.ref_counts[page] : 1;
+      here += count[e] == 0;
     }
-    const GrowRow r = grow_row(p, new_lens, lo);
-    const int nth = k - sh.base[lo], copies = sh.tail[lo] >= 0;
-    if (nth < copies) dst[lo] = page;
-    p.page_table_out[lo * p.table_out_stride + (nth < copies ? r.tail : r.first + nth - copies)] = page;
+    int k = before + block_scan(here, sh.tmp, total);
+    before += total;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int page = i0 + tid * kEach + e;
+      const bool given = granted && count[e] == 0 && k < wanted;
+      if (page < mine.hi && (elsewhere || given)) p.ref_counts_out[page] = given ? 1 : count[e];
+      if (given) {
+        int lo = 0, hi = p.b;                    // base[lo] <= k < base[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (sh.base[mid] <= k) lo = mid;
+          else hi = mid;
+        }
+        const GrowRow r = grow_row(p, new_lens, lo);
+        const int nth = k - sh.base[lo], copies = sh.tail[lo] >= 0;
+        if (nth < copies) dst[lo] = page;
+        p.page_table_out[lo * p.table_out_stride + (nth < copies ? r.tail : r.first + nth - copies)] = page;
+      }
+      k += count[e] == 0;
+    }
   }
-  // (Also what keeps every CTA here while its words are read.)
-  ptx::cluster_sync_all();
-  for (int i = static_cast<int>(cluster_thread()); i < p.b; i += kCluster * kThreads)
-    if (granted && sh.tail[i] >= 0) atomicSub(p.ref_counts_out + sh.tail[i], 1);
+  if (!granted) return;
+  sync_all();
+  for (int i = rank() * kThreads + tid; i < p.b; i += ranks() * kThreads)
+    if (sh.tail[i] >= 0) atomicSub(p.ref_counts_out + sh.tail[i], 1);
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
-    compact_plan_kernel(const __grid_constant__ PagesParams p, int32_t* src, int32_t* dst, int pairs) {
-  __shared__ int tmp[kWarps + 1], s_used, s_movers, s_holes;
-  const int rank = cluster_rank(), tid = threadIdx.x;
-  const Range mine = share(p.num_pages);
-  int used = 0, total = 0;
-  for (int i = mine.lo + tid; i < mine.hi; i += kThreads) used += p.ref_counts[i] != 0;
-  block_scan(used, tmp, total);
-  if (tid == 0) s_used = total;
-  ptx::cluster_sync_all();
+__global__ void __launch_bounds__(kThreads)
+    compact_kernel(const __grid_constant__ PagesParams p, int32_t* src, int32_t* dst, int pairs) {
+  __shared__ int tmp[kWarps], s_used[kMaxCluster];
+  begin();
+  const int tid = threadIdx.x, lane = tid & 31;
+  auto used_in = [&](int lo, int hi) {
+    int used = 0;
+    for (int i = lo + tid; i < hi; i += kThreads) used += p.ref_counts[i] != 0;
+    return block_sum(used, tmp);
+  };
+  const Range mine = share(p.num_pages, rank());
+  exchange(used_in(mine.lo, mine.hi), s_used, true);
   int n = 0;
-  for (int k = 0; k < kCluster; ++k) n += ld_cluster(&s_used, k);
-  int movers = 0, holes = 0;
-  for (int i = mine.lo + tid; i < mine.hi; i += kThreads) {
-    const bool in_use = p.ref_counts[i] != 0;
-    movers += in_use && i >= n;
-    holes += !in_use && i < n;
-  }
-  block_scan(movers, tmp, total);
-  if (tid == 0) s_movers = total;
-  block_scan(holes, tmp, total);
-  if (tid == 0) s_holes = total;
-  ptx::cluster_sync_all();
-  int mover0 = 0, hole0 = 0, moves = 0;
-  for (int k = 0; k < kCluster; ++k) {
-    const int m = ld_cluster(&s_movers, k), h = ld_cluster(&s_holes, k);
-    mover0 += k < rank ? m : 0;
-    hole0 += k < rank ? h : 0;
-    moves += m;
+  for (int k = 0; k < ranks(); ++k) n += s_used[k];
+  // Every share lies before n or at and behind it, but for one, of which every CTA counts the part behind.
+  int cut = 0;
+  while (cut < ranks() - 1 && share(p.num_pages, cut).hi <= n) ++cut;
+  const Range at_cut = share(p.num_pages, cut);
+  const int cut_movers = used_in(max(n, at_cut.lo), at_cut.hi);
+  int mover = rank() > cut ? cut_movers : 0, hole = 0, moves = cut_movers;
+  for (int k = 0; k < ranks(); ++k) {
+    const Range r = share(p.num_pages, k);
+    if (k > cut) moves += s_used[k];
+    if (k > cut && k < rank()) mover += s_used[k];
+    if (k < cut && k < rank()) hole += r.hi - r.lo - s_used[k];
   }
   moves = min(moves, pairs);        // (as many holes as movers)
   const bool elsewhere = p.ref_counts_out != p.ref_counts;
-  for (int i0 = mine.lo; i0 < mine.hi; i0 += kThreads) {
-    const int i = i0 + tid;
-    const int count = i < mine.hi ? p.ref_counts[i] : 0;
-    const bool mover = i < mine.hi && count != 0 && i >= n, hole = i < mine.hi && count == 0 && i < n;
-    // (A share lies on one side of n, but for the one that n cuts: one scan serves both but there.)
-    const int m = mover0 + block_scan(mover, tmp, total);
-    mover0 += total;
-    const int h = hole0 + block_scan(hole, tmp, total);
-    hole0 += total;
-    if (mover && m < moves) src[m] = i;
-    if (hole && h < moves) dst[h] = i;
-    if (elsewhere && i < mine.hi && !(mover && m < moves) && !(hole && h < moves)) p.ref_counts_out[i] = count;
+  for (int i0 = mine.lo; i0 < mine.hi; i0 += kTile) {
+    int count[kEach], here = 0, total = 0;      // holes in the upper 16 bits, movers in the lower
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = i0 + tid * kEach + e;
+      count[e] = i < mine.hi ? p.ref_counts[i] : 0;
+      if (i < mine.hi) here += i >= n ? count[e] != 0 : (count[e] == 0) << 16;
+    }
+    const int before = block_scan(here, tmp, total);
+    int m = mover + (before & 0xffff), h = hole + (before >> 16);
+    mover += total & 0xffff;
+    hole += total >> 16;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = i0 + tid * kEach + e;
+      if (i >= mine.hi) break;
+      const bool moved = i >= n && count[e] != 0, filled = i < n && count[e] == 0;
+      if (moved && m < moves) src[m] = i;
+      if (filled && h < moves) dst[h] = i;
+      if (elsewhere && !(moved && m < moves) && !(filled && h < moves)) p.ref_counts_out[i] = count[e];
+      m += moved;
+      h += filled;
+    }
   }
-  for (int64_t k = moves + cluster_thread(); k < pairs; k += kCluster * kThreads) src[k] = dst[k] = -1;
-  ptx::cluster_sync_all();
-  // The counts move along, once both lists are written.
-  for (int64_t k = cluster_thread(); k < moves; k += kCluster * kThreads) {
+  for (int64_t k = moves + rank() * kThreads + tid; k < pairs; k += ranks() * kThreads) src[k] = dst[k] = -1;
+  sync_all();
+  // Once both lists are written: the counts move along, ...
+  for (int k = rank() * kThreads + tid; k < moves; k += ranks() * kThreads) {
     const int a = src[k], b = dst[k], count = p.ref_counts[a];
     p.ref_counts_out[b] = count;
     p.ref_counts_out[a] = 0;
   }
+  // ... and the table's entries take their new names: src ascends, so bisection finds them.
+  const bool in_place = p.page_table_out == p.page_table;
+  for_chunks(p.b, p.max_pages, [&](int i, int c0) {
+    const int reach = columns_of(p, clamp_tokens(p.seq_lens, i, p.max_len));
+#pragma unroll
+    for (int k = 0; k < kChunk / 32; ++k) {
+      const int c = c0 + lane + 32 * k;
+      if (c >= (in_place ? reach : p.max_pages)) continue;
+      const int page = p.page_table[i * p.table_stride + c];
+      int to = page;
+      if (c < reach && page >= n && page < p.num_pages) {
+        int lo = 0, hi = moves;                    // the first entry that is at least the page
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (src[mid] < page) lo = mid + 1;
+          else hi = mid;
+        }
+        if (lo < moves && src[lo] == page) to = dst[lo];
+      }
+      if (!in_place || to != page) p.page_table_out[i * p.table_out_stride + c] = to;
+    }
+  });
 }
 
-// Names in the table: src is in ascending order, so a page's new one is found by bisection.
-__global__ void __launch_bounds__(256) compact_rename_kernel(const __grid_constant__ PagesParams p, const int32_t* src,
-                                                             const int32_t* dst, int pairs) {
-  const int64_t n = static_cast<int64_t>(p.b) * p.max_pages;
-  const bool in_place = p.page_table_out == p.page_table;
-  const int64_t x = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (x >= n) return;
-  const int i = static_cast<int>(x / p.max_pages), c = static_cast<int>(x - static_cast<int64_t>(i) * p.max_pages);
-  const bool reached = c * static_cast<int64_t>(p.page_size) < clamp_tokens(p.seq_lens, i, p.max_len);
-  if (in_place && !reached) return;
-  const int old_page = p.page_table[i * p.table_stride + c];
-  int page = old_page;
-  if (reached && is_page(page, p.num_pages)) {
-    int lo = 0, hi = pairs;                    // the first entry that is -1 or at least the page
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2, at = __ldg(src + mid);
-      if (at >= 0 && at < page) lo = mid + 1;
-      else hi = mid;
-    }
-    if (lo < pairs && __ldg(src + lo) == page) page = __ldg(dst + lo);
-  }
-  if (!in_place || page != old_page) p.page_table_out[i * p.table_out_stride + c] = page;
+// A cluster of CTAs pays where the work is more than latency.  Measured (graph): 
+unsigned cluster_for(int64_t words) { return words <= 16384 ? 1u : static_cast<unsigned>(kMaxCluster); }
+
+// Launched while the kernel before still runs; begin() waits for it.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, bool cluster, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = grid;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster && grid > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+int64_t words_of(const PagesParams& p, int rows) { return static_cast<int64_t>(rows) * p.max_pages + p.num_pages; }
 
 // ---- pages copied, rows kept ---------------------------------------------------------------
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyEach = 4;                                  // 16-byte units a thread has in flight
-constexpr int kCopyUnits = kCopyThreads * kCopyEach;
+constexpr int kCopyWarps = kCopyThreads / 32;
+constexpr int kCopyEach = 8;                    // units of 16 bytes that a lane has in flight
+constexpr int kCopyUnits = 32 * kCopyEach;      // of an item
 
-// One item: kCopyUnits units of 16 bytes of K, of V or of the scales of one pair of pages.  A page's units in the
-// order of memory: units of a row, rows of the inner dimension (slot or head, whichever stride is smaller), the
-// outer one.
+// An item, a warp's: 4 KB of K, of V or of the scales of one pair of pages.  A page's units come in the order of memory: units
+// of a row, rows of the inner dimension (slot or head, whichever stride is smaller), the outer one.  A warp looks at
+// 32 of its items at once, so that pairs that are none cost next to nothing.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p, const int32_t* src,
                                                             const int32_t* dst, int64_t items) {
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int pair = static_cast<int>(item / p.items_per_pair);
-    const int from = __ldg(src + pair), to = __ldg(dst + pair);
-    if (!is_page(from, p.num_pages) || !is_page(to, p.num_pages) || from == to) continue;
-    const int part = static_cast<int>(item - static_cast<int64_t>(pair) * p.items_per_pair);
-    const int t = part >= p.first_item[3] ? 3 : part >= p.first_item[2] ? 2 : part >= p.first_item[1] ? 1 : 0;
-    const CopyTensor& x = p.t[t];
-    const uint8_t* a = x.base + from * x.page;
-    uint8_t* b = x.base + to * x.page;
-    const int u0 = (part - p.first_item[t]) * kCopyUnits + threadIdx.x;
-    uint4 v[kCopyEach];
-    int64_t at[kCopyEach];
-#pragma unroll
-    for (int k = 0; k < kCopyEach; ++k) {
-      const int u = u0 + k * kCopyThreads;
-      if (u >= x.units) continue;
-      const int row = u / x.row_units, outer = row / x.inner_n;
-      at[k] = outer * x.outer + (row - outer * x.inner_n) * x.inner + static_cast<int64_t>(u - row * x.row_units) * 16;
-      v[k] = *reinterpret_cast<const uint4*>(a + at[k]);
+  begin();
+  const int lane = threadIdx.x & 31;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kCopyWarps;
+  // Neighbouring items lie on neighbouring SMs.
+  for (int64_t first = static_cast<int64_t>(threadIdx.x / 32) * gridDim.x + blockIdx.x; first < items; first += 32 * step) {
+    const int64_t mine = first + lane * step;
+    int pair = 0, from = -1, to = -1;
+    if (mine < items) {
+      pair = static_cast<int>(mine / p.items_per_pair);
+      from = __ldg(src + pair);
+      to = __ldg(dst + pair);
     }
+    const int mine_part = static_cast<int>(mine - static_cast<int64_t>(pair) * p.items_per_pair);
+    uint32_t live = __ballot_sync(0xffffffffu, is_page(from, p.num_pages) && is_page(to, p.num_pages) && from != to);
+    for (; live; live &= live - 1) {
+      const int who = __ffs(live) - 1;
+      const int part = __shfl_sync(0xffffffffu, mine_part, who);
+      const int64_t a_page = __shfl_sync(0xffffffffu, from, who), b_page = __shfl_sync(0xffffffffu, to, who);
+      const int t = part >= p.first_item[3] ? 3 : part >= p.first_item[2] ? 2 : part >= p.first_item[1] ? 1 : 0;
+      const CopyTensor& x = p.t[t];
+      const uint8_t* a = x.base + a_page * x.page;
+      uint8_t* b = x.base + b_page * x.page;
+      const int u0 = (part - p.first_item[t]) * kCopyUnits + lane;
+      uint4 v[kCopyEach];
+      int64_t at[kCopyEach];
 #pragma unroll
-    for (int k = 0; k < kCopyEach; ++k)
-      if (u0 + k * kCopyThreads < x.units) *reinterpret_cast<uint4*>(b + at[k]) = v[k];
+      for (int k = 0; k < kCopyEach; ++k) {
+        const int u = u0 + k * 32;
+        if (u >= x.units) continue;
+        if (x.flat) {
+          at[k] = static_cast<int64_t>(u) * 16;
+        } else {
+          const int row = u / x.row_units, outer = row / x.inner_n;
+          at[k] = outer * x.outer + (row - outer * x.inner_n) * x.inner + static_cast<int64_t>(u - row * x.row_units) * 16;
+        }
+        v[k] = *reinterpret_cast<const uint4*>(a + at[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kCopyEach; ++k)
+        if (u0 + k * 32 < x.units) *reinterpret_cast<uint4*>(b + at[k]) = v[k];
+    }
   }
 }
 
@@ -372,6 +478,7 @@ constexpr int kKeepEach = 8;
 // path[j] >= j, and the kept rows ascend, so row j is written when nothing behind it reads it any more: eight
 // rows are read, then written.
 __global__ void __launch_bounds__(128) keep_kernel(const __grid_constant__ KeepParams p) {
+  begin();
   const int units = p.row_units + (p.c.k_scale ? 1 : 0), per = p.c.h_kv * units;
   const int i = blockIdx.x / p.blocks, idx = (blockIdx.x - i * p.blocks) * 128 + threadIdx.x;
   if (idx >= 2 * per) return;
@@ -418,45 +525,37 @@ __global__ void __launch_bounds__(128) keep_kernel(const __grid_constant__ KeepP
 }  // namespace
 
 cudaError_t launch_fork(const PagesParams& p, const int32_t* parents, int b_out, int32_t* seq_lens_out, cudaStream_t st) {
-  fork_kernel<<<kCluster, kThreads, 0, st>>>(p, parents, b_out, seq_lens_out);
-  return cudaGetLastError();
+  return launch(fork_kernel, cluster_for(words_of(p, p.b) + words_of(p, b_out)), kThreads, true, st, p, parents, b_out, seq_lens_out);
 }
 
 cudaError_t launch_free(const PagesParams& p, const int32_t* keep_lens, cudaStream_t st) {
-  free_kernel<<<kCluster, kThreads, 0, st>>>(p, keep_lens);
-  return cudaGetLastError();
+  return launch(free_kernel, cluster_for(words_of(p, p.b)), kThreads, true, st, p, keep_lens);
 }
 
 cudaError_t launch_grow(const PagesParams& p, const int32_t* new_lens, int32_t* src, int32_t* dst, int32_t* missing, cudaStream_t st) {
-  grow_kernel<<<kCluster, kThreads, sizeof(GrowShared), st>>>(p, new_lens, src, dst, missing);
-  return cudaGetLastError();
+  return launch(grow_kernel, cluster_for(words_of(p, p.b)), kThreads, true, st, p, new_lens, src, dst, missing);
 }
 
 cudaError_t launch_compact(const PagesParams& p, int32_t* src, int32_t* dst, int pairs, cudaStream_t st) {
-  compact_plan_kernel<<<kCluster, kThreads, 0, st>>>(p, src, dst, pairs);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int64_t blocks = (static_cast<int64_t>(p.b) * p.max_pages + 255) / 256;
-  compact_rename_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(p, src, dst, pairs);
-  return cudaGetLastError();
+  return launch(compact_kernel, cluster_for(words_of(p, p.b)), kThreads, true, st, p, src, dst, pairs);
 }
 
 cudaError_t launch_copy(CopyParams p, const int32_t* src, const int32_t* dst, int pairs, int num_sms, cudaStream_t st) {
   for (int t = 0; t < 4; ++t) {
+    CopyTensor& x = p.t[t];
+    x.flat = x.inner == x.row_units * 16 && x.outer == x.inner * x.inner_n;
     p.first_item[t] = p.items_per_pair;
-    p.items_per_pair += (p.t[t].units + kCopyUnits - 1) / kCopyUnits;
+    p.items_per_pair += (x.units + kCopyUnits - 1) / kCopyUnits;
   }
   const int64_t items = static_cast<int64_t>(pairs) * p.items_per_pair, most = static_cast<int64_t>(num_sms) * 8;
-  copy_kernel<<<static_cast<unsigned>(items < most ? items : most), kCopyThreads, 0, st>>>(p, src, dst, items);
-  return cudaGetLastError();
+  return launch(copy_kernel, static_cast<unsigned>(items < most ? items : most), kCopyThreads, false, st, p, src, dst, items);
 }
 
 cudaError_t launch_keep(KeepParams p, cudaStream_t st) {
   p.blocks = (2 * p.c.h_kv * (p.row_units + (p.c.k_scale ? 1 : 0)) + 127) / 128;
   const int64_t blocks = static_cast<int64_t>(p.blocks) * p.c.b;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  keep_kernel<<<static_cast<unsigned>(blocks), 128, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch(keep_kernel, static_cast<unsigned>(blocks), 128, false, st, p);
 }
 
 }  // namespace sdpa

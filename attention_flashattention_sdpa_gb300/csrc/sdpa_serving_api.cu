@@ -222,7 +222,7 @@ sdpa_status_t check_pages(const sdpa_pages_t* p, int rows_out, bool in_place) {
   SDPA_TRY(words("ref_counts_out", p->ref_counts_out));
   if ((p->b > 1 && p->page_table_stride < p->max_pages) || (rows_out > 1 && p->page_table_out_stride < p->max_pages))
     SDPA_REFUSE(SDPA_ERR_LAYOUT, "page_table_stride below max_pages");
-  if (static_cast<int64_t>(p->b) * p->max_pages >= (int64_t(1) << 38) || static_cast<int64_t>(rows_out) * p->max_pages >= (int64_t(1) << 38))
+  if (p->b > (1 << 24) || rows_out > (1 << 24) || (static_cast<int64_t>(p->b) + rows_out) * p->max_pages >= (int64_t(1) << 38))
     SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "b*max_pages too large");
   const bool same = p->page_table_out == p->page_table;
   if (same ? !in_place || (p->b > 1 && p->page_table_out_stride != p->page_table_stride)
@@ -261,6 +261,7 @@ void log_pages(const char* what, const sdpa_pages_t* p, int n) {
 // A cache's K or V as units of 16 bytes, in the order of memory: the dimension of the smaller stride is the inner one.
 sdpa::CopyTensor copy_tensor(void* base, const sdpa_strides_t& st, const sdpa_cache_t* c, int es) {
   sdpa::CopyTensor t;
+  memset(&t, 0, sizeof(t));
   const bool slots_inside = st.s <= st.h;
   t.base = static_cast<uint8_t*>(base);
   t.page = st.b * es;
@@ -277,7 +278,7 @@ sdpa::CopyTensor copy_scales(float* base, const sdpa_cache_t* c) {
   memset(&t, 0, sizeof(t));
   if (base == nullptr) return t;
   t.base = reinterpret_cast<uint8_t*>(base);
-  t.page = static_cast<int64_t>(c->h_kv) * c->page_size * 4;
+  t.page = t.inner = t.outer = static_cast<int64_t>(c->h_kv) * c->page_size * 4;
   t.inner_n = 1;
   t.row_units = t.units = c->h_kv * c->page_size / 4;
   return t;

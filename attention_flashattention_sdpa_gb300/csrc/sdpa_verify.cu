@@ -24,11 +24,12 @@
 namespace sdpa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 4;                      // vectors a thread has in flight
+constexpr int kMaxCluster = 8;
+constexpr int kAhead = 2;                      // vectors a thread has in flight
 constexpr float kUnit = 4398046511104.f;       // 2^42
-constexpr int kMaxSteps = 520;                 // steps of 32 vectors in a warp's piece: 2^20 / 4 / 16 / 32, and what rounds up
+constexpr int kMaxSteps = 130;                 // steps of 32 vectors in a warp's piece: at most 2^20 / 4 / (8 * 8) / 32, and what rounds up
 
 template <typename T>
 __device__ __forceinline__ float widen(T x) {
@@ -58,8 +59,20 @@ __device__ __forceinline__ Vec<T> load_vec(const T* row, int first, int n, bool 
   return v;
 }
 
+// A mass p 2^42 as h 2^22 + l: h = floor(p 2^20), and l = p 2^42 - h 2^22 rounded to the nearest (ties to even, as for the
+// sum of both: h 2^22 is even).  Both come out of the last bits of fp32 sums with 2^23, at the rate of fp32
+// arithmetic (a conversion to 64 bits has the rate of fp64: 36 us against 16 for 64 rows of 131072).  Sums of up to 2^9 of either fit 32 bits.
+struct Mass {
+  uint32_t h, l;
+  __device__ __forceinline__ long long whole() const { return (static_cast<long long>(h) << 22) + l; }
+};
+
 // NaN and what is below zero counts nothing, what is above one counts one.
-__device__ __forceinline__ long long mass_of(float p) { return __float2ll_rn(fminf(fmaxf(p, 0.f), 1.f) * kUnit); }
+__device__ __forceinline__ Mass mass_of(float p) {
+  const float x = __saturatef(p), top = __fmaf_rz(x, 1048576.f, 8388608.f), rest = fmaf(x, 1048576.f, 8388608.f - top);
+  const float low = __fmaf_rn(rest, 4194304.f, 8388608.f);
+  return {__float_as_uint(top) - 0x4B000000u, __float_as_uint(low) - 0x4B000000u};
+}
 
 __device__ __forceinline__ long long warp_sum(long long x) {
 #pragma unroll
@@ -77,13 +90,23 @@ __device__ __forceinline__ long long warp_scan(long long x, int lane) {
   return x;
 }
 
-__device__ __forceinline__ long long ld_cluster(const long long* at, int rank) {
+__device__ __forceinline__ void st_cluster(long long* at, int rank, long long x) {
   uint32_t a;
-  long long x;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(at)), "r"(rank));
-  asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(x) : "r"(a) : "memory");
-  return x;
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(x) : "memory");
 }
+
+// Of n <= 32 masses (lane i has the i-th) the one that target falls into; target becomes its place in that one.
+__device__ __forceinline__ int pick(long long mass, int n, long long& target, int lane) {
+  const long long to = warp_scan(lane < n ? mass : 0, lane);
+  const int k = min(n - 1, __popc(__ballot_sync(0xffffffffu, lane < n && to <= target)));
+  const long long before = __shfl_sync(0xffffffffu, to - mass, k);
+  target -= before;
+  return k;
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 struct Shared {
   long long mass[kVerifyRows];      // of each drafted token behind its parent (0 where an earlier sibling has it too)
@@ -95,7 +118,7 @@ struct Shared {
   long long gone_mass[kVerifyRows];
   int accepted, refused, n_gone;    // refused: the row of the refused draft of a chain, or -1
   long long warp[kWarps];
-  long long cta;
+  long long cta[2][kMaxCluster];    // of every CTA of the cluster, in each turn
   long long step[kMaxSteps];
 };
 
@@ -117,7 +140,7 @@ __device__ void walk(const VerifyParams& p, Shared& sh, int bi, int len) {
     const float pr = known ? widen(probs[par * p.probs_s + x]) : 0.f;
     sh.token[j] = x;
     sh.parent[j] = node ? par : -1;
-    sh.mass[j] = mass_of(pr);
+    sh.mass[j] = mass_of(pr).whole();
     if (p.draft) {
       const float q = known ? widen(draft[j * p.draft_s + x]) : 0.f;
       // The product of two fp32 values is exact in fp64.
@@ -207,14 +230,19 @@ __device__ void walk(const VerifyParams& p, Shared& sh, int bi, int len) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyParams p, int cluster) {
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_constant__ VerifyParams p, int cluster) {
   constexpr int N = Vec<T>::N;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
   const int bi = blockIdx.x / cluster, rank = blockIdx.x - bi * cluster;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  cluster_arrive();
+  // The kernel before is done (and the next one may be put in place, to wait here in its turn).
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   const int len = p.seq_lens_q ? min(max(__ldg(p.seq_lens_q + bi), 0), p.s) : p.s;
   const int64_t at = static_cast<int64_t>(bi) * p.s;
+  const float u0 = __ldg(p.uniform + at);
   if (len > 0) walk<T>(p, sh, bi, len);
   const int accepted = len > 0 ? sh.accepted : 0;
   // Behind the new token there is none; the token itself is written by the CTA that finds it.
@@ -225,7 +253,10 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
       if (j != accepted - 1) p.new_tokens[at + j] = j < accepted ? sh.token[sh.path[j + 1]] : -1;
     }
   }
-  if (len == 0) return;       // (the whole cluster)
+  if (len == 0) {             // (the whole cluster)
+    cluster_wait();
+    return;
+  }
 
   const int last = sh.path[accepted - 1], refused = sh.refused;
   const T* row = static_cast<const T*>(p.probs) + bi * p.probs_b + last * p.probs_s;
@@ -249,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
   bool diff = less != nullptr;
   int n_gone = sh.n_gone;
   const int piece = rank * kWarps + warp, v_lo = min(vectors, piece * per), v_hi = min(vectors, v_lo + per);
-  long long total = 0, before = 0;
+  long long total = 0, target = 0;
   for (int turn = 0; turn < 2; ++turn) {
     long long sum = 0;
     for (int v0 = v_lo + lane; v0 < v_hi; v0 += 32 * kAhead) {
@@ -257,12 +288,18 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
         if (v0 + 32 * k < v_hi) x[k] = value(v0 + 32 * k, diff);
+      Mass part = {0, 0};
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (v0 + 32 * k >= v_hi) continue;
 #pragma unroll
-        for (int e = 0; e < N; ++e) sum += mass_of(x[k].x[e]);
+        for (int e = 0; e < N; ++e) {
+          const Mass m = mass_of(x[k].x[e]);
+          part.h += m.h;
+          part.l += m.l;
+        }
       }
+      sum += part.whole();
     }
     for (int g = lane; g < n_gone; g += 32)
       if (sh.gone_mass[g] > 0) {
@@ -272,20 +309,25 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     sum = warp_sum(sum);
     if (lane == 0) sh.warp[warp] = sum;
     __syncthreads();
-    if (tid == 0) {
-      long long all = 0;
-      for (int w = 0; w < kWarps; ++w) all += sh.warp[w];
-      sh.cta = all;
+    if (warp == 0) {
+      // The CTA's sum goes to every CTA of the cluster.
+      const long long all = warp_sum(lane < kWarps ? sh.warp[lane] : 0);
+      if (turn == 0) cluster_wait();           // they have all begun
+      if (lane < cluster) st_cluster(&sh.cta[turn][rank], lane, all);
+    } else if (turn == 0) {
+      cluster_wait();
     }
     ptx::cluster_sync_all();
-    total = before = 0;
-    for (int k = 0; k < cluster; ++k) {
-      const long long x = ld_cluster(&sh.cta, k);
-      before += k < rank ? x : 0;
-      total += x;
+    const long long mine = lane < cluster ? sh.cta[turn][lane] : 0;
+    total = warp_sum(mine);
+    // floor(u 2^31) total / 2^31: below the total.
+    const unsigned long long part = min(__float2uint_rd(u0 * 2147483648.f), 0x7fffffffu), all = total;
+    target = static_cast<long long>((all >> 32) * part * 2 + (((all & 0xffffffffull) * part) >> 31));
+    if (total > 0) {
+      if (pick(mine, cluster, target, lane) != rank) return;
+      break;
     }
-    ptx::cluster_sync_all();       // nobody writes or leaves while its sums are read
-    if (total > 0 || (!diff && n_gone == 0)) break;
+    if (!diff && n_gone == 0) break;
     diff = false;
     n_gone = 0;
   }
@@ -294,13 +336,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     if (rank == 0 && tid == 0) *out = -1;
     return;
   }
-  // floor(u 2^31) total / 2^31: below the total.
-  const unsigned long long part = min(__float2uint_rd(__ldg(p.uniform + at) * 2147483648.f), 0x7fffffffu);
-  long long target = static_cast<long long>((static_cast<unsigned long long>(total) >> 32) * part * 2 +
-                                            (((static_cast<unsigned long long>(total) & 0xffffffffull) * part) >> 31)) - before;
-  if (target < 0 || target >= sh.cta) return;
-  int w = 0;
-  for (; w < kWarps - 1 && target >= sh.warp[w]; ++w) target -= sh.warp[w];
+  const int w = pick(lane < kWarps ? sh.warp[lane] : 0, kWarps, target, lane);
   // The piece of warp w once more, a step of 32 vectors a warp.
   const int lo = min(vectors, (rank * kWarps + w) * per), hi = min(vectors, lo + per), steps = (hi - lo + 31) / 32;
   auto left_of = [&](int v, long long (&mass)[N]) {
@@ -308,7 +344,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     if (v < hi) {
       const Vec<T> x = value(v, diff);
 #pragma unroll
-      for (int e = 0; e < N; ++e) mass[e] = mass_of(x.x[e]);
+      for (int e = 0; e < N; ++e) mass[e] = mass_of(x.x[e]).whole();
       for (int g = 0; g < n_gone; ++g) {
 #pragma unroll
         for (int e = 0; e < N; ++e)
@@ -319,22 +355,32 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     }
     return sum;
   };
-  for (int k = warp; k < steps; k += kWarps) {
-    long long mass[N];
-    const long long sum = warp_sum(left_of(lo + 32 * k + lane, mass));
-    if (lane == 0) sh.step[k] = sum;
+  long long mass[N], sum = 0;
+  int k = warp;
+  for (; k < steps; k += kWarps) {
+    sum = left_of(lo + 32 * k + lane, mass);
+    const long long all = warp_sum(sum);
+    if (lane == 0) sh.step[k] = all;
   }
   __syncthreads();
-  if (warp > 0) return;
-  int k = 0;
-  for (; k < steps - 1 && target >= sh.step[k]; ++k) target -= sh.step[k];
-  long long mass[N];
-  const long long sum = left_of(lo + 32 * k + lane, mass);
+  int step = 0;
+  for (int k0 = 0; k0 < steps; k0 += 32) {
+    const int n = min(32, steps - k0);
+    const long long mine = lane < n ? sh.step[k0 + lane] : 0, all = warp_sum(mine);
+    if (target < all || k0 + 32 >= steps) {
+      step = k0 + pick(mine, n, target, lane);
+      break;
+    }
+    target -= all;
+  }
+  // The warp that had this step goes on: its values are at hand where it had no other behind it.
+  if (step % kWarps != warp) return;
+  if (step + kWarps < steps) sum = left_of(lo + 32 * step + lane, mass);
   long long to = warp_scan(sum, lane) - sum;       // before this lane
   if (target < to || target >= to + sum) return;
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    if (target >= to && target < to + mass[e]) *out = (lo + 32 * k + lane) * N - off + e;
+    if (target >= to && target < to + mass[e]) *out = (lo + 32 * step + lane) * N - off + e;
     to += mass[e];
   }
 }
@@ -349,12 +395,14 @@ cudaError_t launch_t(const VerifyParams& p, int num_sms, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = cluster;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, verify_kernel<T>, p, cluster);
 }
 
