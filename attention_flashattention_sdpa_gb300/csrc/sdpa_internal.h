@@ -277,9 +277,9 @@ struct PagesParams {
   int max_len;                   // min(max_pages * page_size, 2^30)
 };
 
-cudaError_t launch_fork(const PagesParams& p, const int32_t* parents, int b_out, int32_t* seq_lens_out, cudaStream_t st);
+cudaError_t launch_fork(PagesParams p, const int32_t* parents, int b_out, int32_t* seq_lens_out, int num_sms, cudaStream_t st);
 cudaError_t launch_grow(const PagesParams& p, const int32_t* new_lens, int32_t* src, int32_t* dst, int32_t* missing, cudaStream_t st);
-cudaError_t launch_free(const PagesParams& p, const int32_t* keep_lens, cudaStream_t st);
+cudaError_t launch_free(PagesParams p, const int32_t* keep_lens, int num_sms, cudaStream_t st);
 cudaError_t launch_compact(const PagesParams& p, int32_t* src, int32_t* dst, int pairs, cudaStream_t st);
 
 // One tensor of a cache as units of 16 bytes: BYTE strides of a page, of its inner rows and of groups of those.

@@ -520,7 +520,7 @@ sdpa_status_t sdpa_cache_fork(const sdpa_pages_t* p, const int32_t* parents, int
   if (overlap(parents, b_out, seq_lens_out, b_out)) SDPA_REFUSE(SDPA_ERR_LAYOUT, "seq_lens_out must lie apart from parents");
   log_pages("fork", p, b_out);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  cudaError_t e = sdpa::launch_fork(pages_params(p), parents, b_out, seq_lens_out, stream);
+  cudaError_t e = sdpa::launch_fork(pages_params(p), parents, b_out, seq_lens_out, sdpa::api_num_sms(), stream);
   return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, "sdpa_cache_fork"));
 }
 
@@ -544,7 +544,7 @@ sdpa_status_t sdpa_cache_free(const sdpa_pages_t* p, const int32_t* keep_lens, v
   SDPA_TRY(words("keep_lens", keep_lens));
   log_pages("free", p, 0);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  cudaError_t e = sdpa::launch_free(pages_params(p), keep_lens, stream);
+  cudaError_t e = sdpa::launch_free(pages_params(p), keep_lens, sdpa::api_num_sms(), stream);
   return static_cast<sdpa_status_t>(sdpa::api_finish(e, stream, "sdpa_cache_free"));
 }
 

@@ -14,9 +14,13 @@
 //
 // Bound: reading one row of p (and one of q) of each sequence.  The tests need a few single values, which a
 // thread each fetches at once; a cluster of CTAs shares a row, sums meet in its shared memory, and the CTA
-// that the drawn number falls into reads the piece of the row once more, from L2.
+// that the drawn number falls into reads the piece of the row once more, from L2.  Measured: 64 rows of 131072 fp32 values
+// of p and q 10.0 us (5.8 TB/s, 87% of a copy), one of 32000 5.6: the launch, and five latencies in a row (tokens, their
+// probabilities, the row, the cluster's barrier, the piece).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "sdpa_internal.h"
@@ -27,51 +31,70 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kAhead = 2;                      // vectors a thread has in flight
+constexpr int kAhead = 4;                      // vectors a thread has in flight (2: 10.8 us for 64 rows of 131072, 4: 10.0)
 constexpr float kUnit = 4398046511104.f;       // 2^42
-constexpr int kMaxSteps = 130;                 // steps of 32 vectors in a warp's piece: at most 2^20 / 4 / (8 * 8) / 32, and what rounds up
+constexpr int kMaxSteps = 520;                 // steps of 32 vectors in a warp's piece: at most 2^20 / 4 / (2 * 8) / 32, and what rounds up
 
 template <typename T>
 __device__ __forceinline__ float widen(T x) {
   return static_cast<float>(x);
 }
 
-// 16 bytes of a row as values.
+// 16 bytes of a row as they lie there, and as values.
 template <typename T>
 struct Vec {
   static constexpr int N = 16 / sizeof(T);
   float x[N];
 };
 
-// Elements [first, first + N) of a row of n; those outside are 0.  `wide`: first is at a multiple of 16 bytes.
 template <typename T>
-__device__ __forceinline__ Vec<T> load_vec(const T* row, int first, int n, bool wide) {
+__device__ __forceinline__ Vec<T> unpack(const uint4& u) {
+  const T* e = reinterpret_cast<const T*>(&u);
   Vec<T> v;
-  if (wide && first >= 0 && first + Vec<T>::N <= n) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + first));
-    const T* e = reinterpret_cast<const T*>(&u);
 #pragma unroll
-    for (int i = 0; i < Vec<T>::N; ++i) v.x[i] = widen(e[i]);
-  } else {
+  for (int i = 0; i < Vec<T>::N; ++i) v.x[i] = widen(e[i]);
+  return v;
+}
+
+// Elements [first, first + N) of a row of n one by one; those outside are 0.
+template <typename T>
+__device__ __forceinline__ Vec<T> load_each(const T* row, int first, int n) {
+  Vec<T> v;
 #pragma unroll
-    for (int i = 0; i < Vec<T>::N; ++i) v.x[i] = first + i >= 0 && first + i < n ? widen(row[first + i]) : 0.f;
-  }
+  for (int i = 0; i < Vec<T>::N; ++i) v.x[i] = first + i >= 0 && first + i < n ? widen(__ldg(row + first + i)) : 0.f;
   return v;
 }
 
 // A mass p 2^42 as h 2^22 + l: h = floor(p 2^20), and l = p 2^42 - h 2^22 rounded to the nearest (ties to even, as for the
-// sum of both: h 2^22 is even).  Both come out of the last bits of fp32 sums with 2^23, at the rate of fp32
-// arithmetic (a conversion to 64 bits has the rate of fp64: 36 us against 16 for 64 rows of 131072).  Sums of up to 2^9 of either fit 32 bits.
-struct Mass {
-  uint32_t h, l;
-  __device__ __forceinline__ long long whole() const { return (static_cast<long long>(h) << 22) + l; }
+// sum of both: h 2^22 is even).  Both are the last bits of fp32 sums with 2^23, at the rate of fp32 arithmetic, two
+// elements an instruction (a conversion to 64 bits has the rate of fp64: 31 us against 14 for 64 rows of 131072, then).
+// Sums of 2^9 to 2^10 of either fit 32 bits.
+constexpr uint32_t kBits = 0x4B000000u;        // of 2^23
+
+__device__ __forceinline__ float2 fma2_rz(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rz.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+
+struct Masses {
+  uint32_t h0, h1, l0, l1;      // of two elements, each kBits too large
 };
 
 // NaN and what is below zero counts nothing, what is above one counts one.
-__device__ __forceinline__ Mass mass_of(float p) {
-  const float x = __saturatef(p), top = __fmaf_rz(x, 1048576.f, 8388608.f), rest = fmaf(x, 1048576.f, 8388608.f - top);
-  const float low = __fmaf_rn(rest, 4194304.f, 8388608.f);
-  return {__float_as_uint(top) - 0x4B000000u, __float_as_uint(low) - 0x4B000000u};
+__device__ __forceinline__ Masses masses_of(float p0, float p1) {
+  const float2 x = make_float2(__saturatef(p0), __saturatef(p1)), big = make_float2(8388608.f, 8388608.f);
+  const float2 two20 = make_float2(1048576.f, 1048576.f), top = fma2_rz(x, two20, big);
+  const float2 floors = ptx::fma2(top, make_float2(-1.f, -1.f), big);
+  const float2 low = ptx::fma2(ptx::fma2(x, two20, floors), make_float2(4194304.f, 4194304.f), big);
+  return {__float_as_uint(top.x), __float_as_uint(top.y), __float_as_uint(low.x), __float_as_uint(low.y)};
+}
+
+__device__ __forceinline__ long long mass_of(float p) {
+  const Masses m = masses_of(p, 0.f);
+  return (static_cast<long long>(m.h0 - kBits) << 22) + (m.l0 - kBits);
 }
 
 __device__ __forceinline__ long long warp_sum(long long x) {
@@ -108,23 +131,41 @@ __device__ __forceinline__ int pick(long long mass, int n, long long& target, in
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-struct Shared {
-  long long mass[kVerifyRows];      // of each drafted token behind its parent (0 where an earlier sibling has it too)
-  int32_t parent[kVerifyRows];      // -1: not a node
-  int32_t token[kVerifyRows];
-  uint8_t good[kVerifyRows];
-  int32_t path[kVerifyRows];
-  int32_t gone[kVerifyRows];        // tokens that are not drawn any more
-  long long gone_mass[kVerifyRows];
+// What a CTA knows of its sequence's rows, s entries each.
+struct Rows {
+  long long* mass;          // of each drafted token behind its parent (0 where an earlier sibling has it too)
+  long long* gone_mass;
+  int32_t* gone;            // tokens that are not drawn any more
+  int32_t* parent;          // -1: not a node
+  int32_t* token;
+  int32_t* path;
+  uint8_t* good;
+};
+
+constexpr int kRowBytes = 2 * 8 + 4 * 4 + 1;
+
+__device__ __forceinline__ Rows rows_at(uint8_t* smem, int s) {
+  Rows r;
+  r.mass = reinterpret_cast<long long*>(smem);
+  r.gone_mass = r.mass + s;
+  r.gone = reinterpret_cast<int32_t*>(r.gone_mass + s);
+  r.parent = r.gone + s;
+  r.token = r.parent + s;
+  r.path = r.token + s;
+  r.good = reinterpret_cast<uint8_t*>(r.path + s);
+  return r;
+}
+
+struct Sums {
   int accepted, refused, n_gone;    // refused: the row of the refused draft of a chain, or -1
   long long warp[kWarps];
   long long cta[2][kMaxCluster];    // of every CTA of the cluster, in each turn
   long long step[kMaxSteps];
 };
 
-// Which rows are accepted: sh.path, sh.accepted; what may not be drawn: sh.refused (a chain with q), sh.gone.
+// Which rows are accepted: r.path, sh.accepted; what may not be drawn: sh.refused (a chain with q), r.gone.
 template <typename T>
-__device__ void walk(const VerifyParams& p, Shared& sh, int bi, int len) {
+__device__ void walk(const VerifyParams& p, const Rows& r, Sums& sh, int bi, int len) {
   const int tid = threadIdx.x;
   const T* probs = static_cast<const T*>(p.probs) + bi * p.probs_b;
   const T* draft = static_cast<const T*>(p.draft) + bi * p.draft_b;
@@ -138,13 +179,13 @@ __device__ void walk(const VerifyParams& p, Shared& sh, int bi, int len) {
     const int par = j == 0 ? -1 : p.parents ? __ldg(p.parents + at + j) : j - 1;
     const bool node = j > 0 && par >= 0 && par < j, known = node && x >= 0 && x < p.vocab;
     const float pr = known ? widen(probs[par * p.probs_s + x]) : 0.f;
-    sh.token[j] = x;
-    sh.parent[j] = node ? par : -1;
-    sh.mass[j] = mass_of(pr).whole();
+    r.token[j] = x;
+    r.parent[j] = node ? par : -1;
+    r.mass[j] = mass_of(pr);
     if (p.draft) {
       const float q = known ? widen(draft[j * p.draft_s + x]) : 0.f;
       // The product of two fp32 values is exact in fp64.
-      sh.good[j] = j == 0 || (known && static_cast<double>(__ldg(p.uniform + at + j)) * q < static_cast<double>(pr));
+      r.good[j] = j == 0 || (known && static_cast<double>(__ldg(p.uniform + at + j)) * q < static_cast<double>(pr));
     }
   }
   __syncthreads();
@@ -152,17 +193,17 @@ __device__ void walk(const VerifyParams& p, Shared& sh, int bi, int len) {
     // A chain: up to the first that is not accepted.
     for (int j = tid; j < len; j += kThreads) {
       bool good = j == 0;
-      if (j > 0) good = p.draft ? sh.good[j] : __ldg(p.uniform + at + j) * static_cast<double>(kUnit) < static_cast<double>(sh.mass[j]);
+      if (j > 0) good = p.draft ? r.good[j] : __ldg(p.uniform + at + j) * static_cast<double>(kUnit) < static_cast<double>(r.mass[j]);
       if (!good) atomicMin(&sh.accepted, j);
     }
     __syncthreads();
     const int n = sh.accepted;
-    for (int j = tid; j < n; j += kThreads) sh.path[j] = j;
+    for (int j = tid; j < n; j += kThreads) r.path[j] = j;
     if (tid == 0) {
       sh.refused = p.draft && n < len ? n : -1;
       if (!p.draft && n < len) {
-        sh.gone[0] = sh.token[n];
-        sh.gone_mass[0] = sh.mass[n];
+        r.gone[0] = r.token[n];
+        r.gone_mass[0] = r.mass[n];
         sh.n_gone = 1;
       }
     }
@@ -175,33 +216,33 @@ __device__ void walk(const VerifyParams& p, Shared& sh, int bi, int len) {
   for (int k = 0; k < kVerifyRows / kThreads; ++k) {
     const int j = tid + k * kThreads;
     twin[k] = false;
-    if (j < len && sh.parent[j] >= 0)
-      for (int i = sh.parent[j] + 1; i < j; ++i) twin[k] |= sh.parent[i] == sh.parent[j] && sh.token[i] == sh.token[j];
+    if (j < len && r.parent[j] >= 0)
+      for (int i = r.parent[j] + 1; i < j; ++i) twin[k] |= r.parent[i] == r.parent[j] && r.token[i] == r.token[j];
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kVerifyRows / kThreads; ++k)
-    if (twin[k]) sh.mass[tid + k * kThreads] = 0;
+    if (twin[k]) r.mass[tid + k * kThreads] = 0;
   __syncthreads();
   for (int j = tid; j < len; j += kThreads) {
     long long left = static_cast<long long>(kUnit);
-    if (sh.parent[j] >= 0)
-      for (int i = sh.parent[j] + 1; i < j; ++i) left -= sh.parent[i] == sh.parent[j] ? sh.mass[i] : 0;
+    if (r.parent[j] >= 0)
+      for (int i = r.parent[j] + 1; i < j; ++i) left -= r.parent[i] == r.parent[j] ? r.mass[i] : 0;
     if (left < 0) left = 0;
-    sh.good[j] = sh.parent[j] >= 0 && __dmul_rn(static_cast<double>(__ldg(p.uniform + at + j)), static_cast<double>(left)) <
-                                          static_cast<double>(sh.mass[j]);
+    r.good[j] = r.parent[j] >= 0 && __dmul_rn(static_cast<double>(__ldg(p.uniform + at + j)), static_cast<double>(left)) <
+                                          static_cast<double>(r.mass[j]);
   }
   __syncthreads();
   if (tid < 32) {
     // From node to node: the first good child, all of them behind it.
     int n = 0, count = 1;
-    if (tid == 0) sh.path[0] = 0;
+    if (tid == 0) r.path[0] = 0;
     for (int j0 = 1; j0 < len;) {
       const int j = j0 + tid;
-      const uint32_t hit = __ballot_sync(0xffffffffu, j < len && sh.parent[j] == n && sh.good[j]);
+      const uint32_t hit = __ballot_sync(0xffffffffu, j < len && r.parent[j] == n && r.good[j]);
       if (hit) {
         n = j0 + __ffs(hit) - 1;
-        if (tid == 0) sh.path[count] = n;
+        if (tid == 0) r.path[count] = n;
         ++count;
         j0 = n + 1;
       } else {
@@ -211,12 +252,12 @@ __device__ void walk(const VerifyParams& p, Shared& sh, int bi, int len) {
     int gone = 0;
     for (int j0 = n + 1; j0 < len; j0 += 32) {
       const int j = j0 + tid;
-      const bool child = j < len && sh.parent[j] == n;
+      const bool child = j < len && r.parent[j] == n;
       const uint32_t hit = __ballot_sync(0xffffffffu, child);
       if (child) {
         const int k = gone + __popc(hit & ((1u << tid) - 1));
-        sh.gone[k] = sh.token[j];
-        sh.gone_mass[k] = sh.mass[j];
+        r.gone[k] = r.token[j];
+        r.gone_mass[k] = r.mass[j];
       }
       gone += __popc(hit);
     }
@@ -233,7 +274,8 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_constant__ VerifyParams p, int cluster) {
   constexpr int N = Vec<T>::N;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
+  __shared__ Sums sh;
+  const Rows r = rows_at(smem_raw, p.s);
   const int bi = blockIdx.x / cluster, rank = blockIdx.x - bi * cluster;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   cluster_arrive();
@@ -243,14 +285,14 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
   const int len = p.seq_lens_q ? min(max(__ldg(p.seq_lens_q + bi), 0), p.s) : p.s;
   const int64_t at = static_cast<int64_t>(bi) * p.s;
   const float u0 = __ldg(p.uniform + at);
-  if (len > 0) walk<T>(p, sh, bi, len);
+  if (len > 0) walk<T>(p, r, sh, bi, len);
   const int accepted = len > 0 ? sh.accepted : 0;
   // Behind the new token there is none; the token itself is written by the CTA that finds it.
   if (rank == 0) {
     if (tid == 0) p.accepted[bi] = accepted;
     for (int j = tid; j < p.s; j += kThreads) {
-      p.path[at + j] = j < accepted ? sh.path[j] : -1;
-      if (j != accepted - 1) p.new_tokens[at + j] = j < accepted ? sh.token[sh.path[j + 1]] : -1;
+      p.path[at + j] = j < accepted ? r.path[j] : -1;
+      if (j != accepted - 1) p.new_tokens[at + j] = j < accepted ? r.token[r.path[j + 1]] : -1;
     }
   }
   if (len == 0) {             // (the whole cluster)
@@ -258,18 +300,20 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
     return;
   }
 
-  const int last = sh.path[accepted - 1], refused = sh.refused;
+  const int last = r.path[accepted - 1], refused = sh.refused;
   const T* row = static_cast<const T*>(p.probs) + bi * p.probs_b + last * p.probs_s;
   const T* less = refused >= 0 ? static_cast<const T*>(p.draft) + bi * p.draft_b + refused * p.draft_s : nullptr;
   // Vectors of 16 bytes from the multiple of 16 at or before the row's start; each warp has a piece of them.
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
   const bool less_wide = less && reinterpret_cast<uintptr_t>(less) % 16 / sizeof(T) == static_cast<unsigned>(off);
   const int vectors = (off + p.vocab + N - 1) / N, pieces = cluster * kWarps, per = (vectors + pieces - 1) / pieces;
+  // (Vectors 0 and `inner` may hold elements that are not the row's.)
+  const int inner = (off + p.vocab) / N, inner0 = off ? 1 : 0;
   auto value = [&](int v, bool diff) {
     const int first = v * N - off;
-    Vec<T> x = load_vec(row, first, p.vocab, true);
+    Vec<T> x = v >= inner0 && v < inner ? unpack<T>(__ldg(reinterpret_cast<const uint4*>(row + first))) : load_each(row, first, p.vocab);
     if (diff) {
-      const Vec<T> y = load_vec(less, first, p.vocab, less_wide);
+      const Vec<T> y = load_each(less, first, p.vocab);
 #pragma unroll
       for (int e = 0; e < N; ++e) x.x[e] -= y.x[e];
     }
@@ -283,28 +327,60 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
   long long total = 0, target = 0;
   for (int turn = 0; turn < 2; ++turn) {
     long long sum = 0;
-    for (int v0 = v_lo + lane; v0 < v_hi; v0 += 32 * kAhead) {
-      Vec<T> x[kAhead];
+    uint32_t h = 0, l = 0, n = 0;
+    auto flush = [&] {
+      sum += (static_cast<long long>(h - n * kBits) << 22) + (l - n * kBits);
+      h = l = n = 0;
+    };
+    auto add = [&](const Vec<T>& x) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (v0 + 32 * k < v_hi) x[k] = value(v0 + 32 * k, diff);
-      Mass part = {0, 0};
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        if (v0 + 32 * k >= v_hi) continue;
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const Mass m = mass_of(x[k].x[e]);
-          part.h += m.h;
-          part.l += m.l;
-        }
+      for (int e = 0; e < N; e += 2) {
+        const Masses m = masses_of(x.x[e], x.x[e + 1]);
+        h += m.h0 + m.h1;
+        l += m.l0 + m.l1;
       }
-      sum += part.whole();
-    }
+      n += N;
+    };
+    // Whole vectors, kAhead of them loaded at once; MODE 0: the row, 1: less another row as aligned as it is, 2: less any other.
+    auto stream = [&](auto mode) {
+      constexpr int MODE = decltype(mode)::value;
+      const int hi = min(v_hi, inner);
+      int v = max(v_lo, inner0) + lane;
+      auto some = [&](auto count) {
+        constexpr int COUNT = decltype(count)::value;
+        uint4 a[COUNT], b[COUNT];
+        Vec<T> c[COUNT];
+#pragma unroll
+        for (int k = 0; k < COUNT; ++k) {
+          const int first = (v + 32 * k) * N - off;
+          a[k] = __ldg(reinterpret_cast<const uint4*>(row + first));
+          if constexpr (MODE == 1) b[k] = __ldg(reinterpret_cast<const uint4*>(less + first));
+          if constexpr (MODE == 2) c[k] = load_each(less, first, p.vocab);
+        }
+#pragma unroll
+        for (int k = 0; k < COUNT; ++k) {
+          Vec<T> x = unpack<T>(a[k]);
+          if constexpr (MODE == 1) c[k] = unpack<T>(b[k]);
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if constexpr (MODE != 0) x.x[e] -= c[k].x[e];
+          add(x);
+        }
+        if (n > 512) flush();
+      };
+      for (; v + 32 * (kAhead - 1) < hi; v += 32 * kAhead) some(std::integral_constant<int, kAhead>());
+      for (; v < hi; v += 32) some(std::integral_constant<int, 1>());
+    };
+    if (!diff) stream(std::integral_constant<int, 0>());
+    else if (less_wide) stream(std::integral_constant<int, 1>());
+    else stream(std::integral_constant<int, 2>());
+    if (lane == 0 && inner0 > 0 && v_lo == 0 && v_hi > 0) add(value(0, diff));
+    if (lane == 0 && inner >= max(v_lo, inner0) && inner < v_hi) add(value(inner, diff));
+    flush();
     for (int g = lane; g < n_gone; g += 32)
-      if (sh.gone_mass[g] > 0) {
-        const int v = (sh.gone[g] + off) / N;
-        if (v >= v_lo && v < v_hi) sum -= sh.gone_mass[g];
+      if (r.gone_mass[g] > 0) {
+        const int v = (r.gone[g] + off) / N;
+        if (v >= v_lo && v < v_hi) sum -= r.gone_mass[g];
       }
     sum = warp_sum(sum);
     if (lane == 0) sh.warp[warp] = sum;
@@ -344,11 +420,11 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
     if (v < hi) {
       const Vec<T> x = value(v, diff);
 #pragma unroll
-      for (int e = 0; e < N; ++e) mass[e] = mass_of(x.x[e]).whole();
+      for (int e = 0; e < N; ++e) mass[e] = mass_of(x.x[e]);
       for (int g = 0; g < n_gone; ++g) {
 #pragma unroll
         for (int e = 0; e < N; ++e)
-          if (sh.gone[g] == v * N - off + e) mass[e] = 0;
+          if (r.gone[g] == v * N - off + e) mass[e] = 0;
       }
 #pragma unroll
       for (int e = 0; e < N; ++e) sum += mass[e];
@@ -387,13 +463,14 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
 
 template <typename T>
 cudaError_t launch_t(const VerifyParams& p, int num_sms, cudaStream_t st) {
-  const int cluster = 8;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&verify_kernel<T>), sizeof(Shared));
-  if (e != cudaSuccess) return e;
+  // CTAs of a row: 8, or as many as leave all rows on the GPU at once (4 CTAs an SM), 2 at least.  Measured, 131072 fp32 values:
+  // 64 rows 9.6 us with 8, 12.4 with 4; 96 rows 16.2 and 14.8; 200 rows of 32000 18.5 with 8, 13.2 with 4, 10.7 with 2.
+  int cluster = kMaxCluster;
+  while (cluster > 2 && static_cast<int64_t>(p.b) * cluster > 4 * static_cast<int64_t>(num_sms)) cluster /= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.b) * cluster);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(Shared);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.s) * kRowBytes;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
