@@ -750,25 +750,27 @@ def _pages(page_table, seq_lens, ref_counts, table_out, refs_out, page_size, b_o
     """The packed descriptor and the number of rows; outputs that are None are the inputs."""
     if _Lazy.torch is None:
         _Lazy.load()
-    at, shape, stride = _page_table(page_table, "page_table")
-    lens = _dense(seq_lens, "seq_lens", _Lazy.int32, shape[:1])
-    if ref_counts.dim() != 1:
-        raise ValueError("ref_counts must be int32 [num_pages]")
+    int32 = _Lazy.int32
+    at, (b, columns), stride = _page_table(page_table, "page_table")
     n = ref_counts.shape
-    refs = _dense(ref_counts, "ref_counts", _Lazy.int32, n)
+    if len(n) != 1:
+        raise ValueError("ref_counts must be int32 [num_pages]")
+    refs = _dense(ref_counts, "ref_counts", int32, n)
     out_at, out_stride, refs_at = at, stride, refs
     if table_out is not None:
-        out_at, _, out_stride = _page_table(table_out, "page_table_out", shape if b_out is None else (b_out, shape[1]))
+        out_at, _, out_stride = _page_table(table_out, "page_table_out", (b if b_out is None else b_out, columns))
     if refs_out is not None:
-        refs_at = _dense(refs_out, "ref_counts_out", _Lazy.int32, n)
-    return _PACK_PAGES(n[0], page_size, shape[0], shape[1], at, stride, lens, refs, out_at, out_stride, refs_at), shape[0]
+        refs_at = _dense(refs_out, "ref_counts_out", int32, n)
+    return _PACK_PAGES(n[0], page_size, b, columns, at, stride, _dense(seq_lens, "seq_lens", int32, (b,)), refs, out_at, out_stride,
+                       refs_at), b
 
 
 def _pairs(src, dst):
     """Addresses and length of a list of pages."""
-    if src.dim() != 1:
+    n = src.shape
+    if len(n) != 1:
         raise ValueError("src and dst must be int32 of one dimension")
-    return _dense(src, "src", _Lazy.int32, src.shape), _dense(dst, "dst", _Lazy.int32, src.shape), src.shape[0]
+    return _dense(src, "src", _Lazy.int32, n), _dense(dst, "dst", _Lazy.int32, n), n[0]
 
 
 def sdpa_cache_fork(page_table, seq_lens, parents, ref_counts, page_table_out, seq_lens_out, ref_counts_out=None, *,

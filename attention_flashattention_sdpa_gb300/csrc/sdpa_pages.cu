@@ -476,10 +476,10 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
   }
 }
 
-constexpr int kKeepEach = 8;
+constexpr int kKeepEach = 4;
 
 // A thread: 16 bytes of one head's rows of K or V of one sequence (or its scales), all kept rows in ascending order.
-// path[j] >= j, and the kept rows ascend, so row j is written when nothing behind it reads it any more: eight
+// path[j] >= j, and the kept rows ascend, so row j is written when nothing behind it reads it any more: four
 // rows are read, then written.
 __global__ void __launch_bounds__(128) keep_kernel(const __grid_constant__ KeepParams p) {
   begin();

@@ -215,6 +215,9 @@ sdpa_status_t check_pages(const sdpa_pages_t* p, int rows_out, bool in_place) {
                 p->page_size, p->b, p->max_pages, rows_out);
   if (p->page_size % 16 != 0)
     SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "page_size %d not supported (a multiple of 16)", p->page_size);
+  if (p->num_pages > (1 << 30) || p->max_pages > (1 << 30)) SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "num_pages or max_pages too large (1..2^30)");
+  if (p->b > (1 << 24) || rows_out > (1 << 24) || (static_cast<int64_t>(p->b) + rows_out) * p->max_pages >= (int64_t(1) << 38))
+    SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "b*max_pages too large");
   SDPA_TRY(words("page_table", p->page_table));
   SDPA_TRY(words("seq_lens", p->seq_lens));
   SDPA_TRY(words("ref_counts", p->ref_counts));
@@ -222,8 +225,6 @@ sdpa_status_t check_pages(const sdpa_pages_t* p, int rows_out, bool in_place) {
   SDPA_TRY(words("ref_counts_out", p->ref_counts_out));
   if ((p->b > 1 && p->page_table_stride < p->max_pages) || (rows_out > 1 && p->page_table_out_stride < p->max_pages))
     SDPA_REFUSE(SDPA_ERR_LAYOUT, "page_table_stride below max_pages");
-  if (p->b > (1 << 24) || rows_out > (1 << 24) || (static_cast<int64_t>(p->b) + rows_out) * p->max_pages >= (int64_t(1) << 38))
-    SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "b*max_pages too large");
   const bool same = p->page_table_out == p->page_table;
   if (same ? !in_place || (p->b > 1 && p->page_table_out_stride != p->page_table_stride)
            : overlap(p->page_table, table_words(p->b, p->max_pages, p->page_table_stride), p->page_table_out,
@@ -528,6 +529,8 @@ sdpa_status_t sdpa_cache_grow(const sdpa_pages_t* p, const int32_t* new_lens, in
                               void* stream_) {
   SDPA_TRY(check_pages(p, p ? p->b : 1, true));
   if (p->b > sdpa::kMaxPageRows) SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "%d rows not supported (1..%d)", p->b, sdpa::kMaxPageRows);
+  if (static_cast<int64_t>(p->b) * p->max_pages >= (int64_t(1) << 31))     // (pages that one call may want are counted in 32 bits)
+    SDPA_REFUSE(SDPA_ERR_UNSUPPORTED, "b*max_pages too large (below 2^31)");
   SDPA_TRY(words("new_lens", new_lens));
   SDPA_TRY(words("src", src));
   SDPA_TRY(words("dst", dst));

@@ -31,7 +31,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kAhead = 4;                      // vectors a thread has in flight (2: 10.8 us for 64 rows of 131072, 4: 10.0)
+constexpr int kAhead = 2;                      // vectors a thread has in flight
 constexpr float kUnit = 4398046511104.f;       // 2^42
 constexpr int kMaxSteps = 520;                 // steps of 32 vectors in a warp's piece: at most 2^20 / 4 / (2 * 8) / 32, and what rounds up
 

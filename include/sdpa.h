@@ -437,10 +437,10 @@ SDPA_API sdpa_status_t sdpa_decode(const sdpa_cache_t* c, const sdpa_decode_t* p
  * no count.  Counts must be at least the number of reaching entries.
  * ------------------------------------------------------------------------------------------ */
 typedef struct {
-  int32_t num_pages;            /* >= 1 */
+  int32_t num_pages;            /* 1..2^30 */
   int32_t page_size;            /* a multiple of 16 */
-  int32_t b;                    /* rows of page_table: sequences */
-  int32_t max_pages;            /* columns */
+  int32_t b;                    /* rows of page_table: sequences, 1..2^24 */
+  int32_t max_pages;            /* columns, 1..2^30 */
   const int32_t* page_table;    /* DEVICE [b][max_pages] */
   int64_t page_table_stride;
   const int32_t* seq_lens;      /* DEVICE [b]: tokens of each sequence */

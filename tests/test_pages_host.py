@@ -140,7 +140,7 @@ BAD_PAGES = [
     (dict(ref_counts=0), 1, "ref_counts"), (dict(page_table_out=0), 1, "page_table_out"), (dict(ref_counts_out=0), 1, "ref_counts_out"),
     (dict(ref_counts=FAKE + 0x2002), 3, "4-byte"), (dict(page_table_stride=3), 3, "stride"), (dict(page_table_out_stride=3), 3, "stride"),
     (dict(page_table_out=FAKE + 16), 3, "apart"), (dict(ref_counts_out=FAKE + 0x2000 + 4), 3, "apart"),
-    (dict(b=(1 << 24) + 1), 2, "too large"), (dict(max_pages=1 << 30, page_table_stride=1 << 30, page_table_out_stride=1 << 30, b=300), 2, "too large"),
+    (dict(b=(1 << 24) + 1), 2, "too large"), (dict(num_pages=(1 << 30) + 1), 2, "too large"), (dict(max_pages=(1 << 30) + 1), 2, "too large"), (dict(max_pages=1 << 30, page_table_stride=1 << 30, page_table_out_stride=1 << 30, b=300), 2, "too large"),
 ]
 
 
@@ -167,6 +167,8 @@ def test_pages_refusals_of_each_call(m):
             (lambda: L.sdpa_cache_fork(addr(_pages(m, page_table_out=FAKE)), A, 3, B, None), 3, "apart"),
             (lambda: L.sdpa_cache_free(addr(same), A, None), 3, "stride"),
             (lambda: L.sdpa_cache_grow(addr(_pages(m, b=4097, page_table_out=FAKE)), A, B, C, C + 64, None), 2, "4097"),
+            (lambda: L.sdpa_cache_grow(addr(_pages(m, b=2048, max_pages=1 << 20, page_table_stride=1 << 20, page_table_out=FAKE, page_table_out_stride=1 << 20)),
+                                       A, B, C, C + 8192, None), 2, "2^31"),
             (lambda: L.sdpa_cache_grow(p, None, B, C, C + 64, None), 1, "new_lens"), (lambda: L.sdpa_cache_grow(p, A, None, C, C + 64, None), 1, "src"),
             (lambda: L.sdpa_cache_grow(p, A, B, C + 1, C + 64, None), 3, "dst"), (lambda: L.sdpa_cache_grow(p, A, B, C, None, None), 1, "missing"),
             (lambda: L.sdpa_cache_grow(p, A, B, B + 8, C, None), 3, "apart"), (lambda: L.sdpa_cache_free(p, None, None), 1, "keep_lens"),
