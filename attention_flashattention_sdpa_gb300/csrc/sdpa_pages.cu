@@ -126,8 +126,25 @@ __device__ __forceinline__ void for_chunks(int rows, int columns, F f) {
 // Counts as they are, where they are wanted elsewhere, before anyone adds to them.
 __device__ __forceinline__ void copy_counts(const PagesParams& p) {
   if (p.ref_counts_out == p.ref_counts) return;
-  for (int64_t i = rank() * kThreads + threadIdx.x; i < p.num_pages; i += ranks() * kThreads) p.ref_counts_out[i] = p.ref_counts[i];
+#pragma unroll 4
+  for (int i = rank() * kThreads + threadIdx.x; i < p.num_pages; i += ranks() * kThreads) p.ref_counts_out[i] = __ldg(p.ref_counts + i);
   sync_all();
+}
+
+// The number of pages in [lo, hi) that are in use, the CTA's own share on its way copied to where the counts are wanted.
+__device__ __forceinline__ int used_in(const PagesParams& p, int lo, int hi, bool copy, int* tmp) {
+  int used = 0;
+  for (int i0 = lo + threadIdx.x; i0 < hi; i0 += kTile) {
+    int count[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) count[e] = i0 + e * kThreads < hi ? p.ref_counts[i0 + e * kThreads] : 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      used += count[e] != 0;
+      if (copy && i0 + e * kThreads < hi) p.ref_counts_out[i0 + e * kThreads] = count[e];
+    }
+  }
+  return block_sum(used, tmp);
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -206,10 +223,17 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ GrowShared sh;
   begin();
   const int tid = threadIdx.x, lane = tid & 31;
+  // What is wanted elsewhere goes there as it is, before the barrier behind which it changes.
+  if (p.page_table_out != p.page_table)
+    for_chunks(p.b, p.max_pages, [&](int i, int c0) {
+#pragma unroll
+      for (int k = 0; k < kChunk / 32; ++k) {
+        const int c = c0 + lane + 32 * k;
+        if (c < p.max_pages) p.page_table_out[i * p.table_out_stride + c] = p.page_table[i * p.table_stride + c];
+      }
+    });
   const Range mine = share(p.num_pages, rank());
-  int free_count = 0;
-  for (int i = mine.lo + tid; i < mine.hi; i += kThreads) free_count += p.ref_counts[i] == 0;
-  free_count = block_sum(free_count, sh.tmp);
+  const int free_count = mine.hi - mine.lo - used_in(p, mine.lo, mine.hi, p.ref_counts_out != p.ref_counts, sh.tmp);
 
   // Every CTA looks at all rows: their partly filled pages that others own too ...
   for (int i = tid; i < p.b; i += kThreads) {
@@ -253,27 +277,14 @@ __global__ void __launch_bounds__(kThreads)
   const bool granted = wanted <= all;
   if (rank() == 0 && tid == 0) *missing = granted ? 0 : wanted - all;
 
-  // Entries that stay as they are.
-  if (p.page_table_out != p.page_table)
-    for_chunks(p.b, p.max_pages, [&](int i, int c0) {
-      const GrowRow r = grow_row(p, new_lens, i);
-      const int tail = sh.tail[i] >= 0 ? r.tail : -1;
-#pragma unroll
-      for (int k = 0; k < kChunk / 32; ++k) {
-        const int c = c0 + lane + 32 * k;
-        if (c < p.max_pages && !(granted && ((c >= r.first && c < r.end) || c == tail)))
-          p.page_table_out[i * p.table_out_stride + c] = p.page_table[i * p.table_stride + c];
-      }
-    });
   for (int i = rank() * kThreads + tid; i < p.b; i += ranks() * kThreads) {
     const bool copied = granted && sh.tail[i] >= 0;
     src[i] = copied ? sh.tail[i] : -1;
     if (!copied) dst[i] = -1;
   }
   // The k-th free page goes to the row whose run of wanted pages holds k.
-  const bool elsewhere = p.ref_counts_out != p.ref_counts;
-  for (int i0 = mine.lo; i0 < mine.hi; i0 += kTile) {
-    if (!elsewhere && (!granted || before >= wanted)) break;
+  if (!granted) return;
+  for (int i0 = mine.lo; i0 < mine.hi && before < wanted; i0 += kTile) {
     int count[kEach], here = 0, total = 0;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
@@ -286,9 +297,8 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int page = i0 + tid * kEach + e;
-      const bool given = granted && count[e] == 0 && k < wanted;
-      if (page < mine.hi && (elsewhere || given)) p.ref_counts_out[page] = given ? 1 : count[e];
-      if (given) {
+      if (count[e] == 0 && k < wanted) {
+        p.ref_counts_out[page] = 1;
         int lo = 0, hi = p.b;                    // base[lo] <= k < base[hi]
         while (hi - lo > 1) {
           const int mid = (lo + hi) / 2;
@@ -303,7 +313,6 @@ __global__ void __launch_bounds__(kThreads)
       k += count[e] == 0;
     }
   }
-  if (!granted) return;
   sync_all();
   for (int i = rank() * kThreads + tid; i < p.b; i += ranks() * kThreads)
     if (sh.tail[i] >= 0) atomicSub(p.ref_counts_out + sh.tail[i], 1);
@@ -314,20 +323,15 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ int tmp[kWarps], s_used[kMaxCluster];
   begin();
   const int tid = threadIdx.x, lane = tid & 31;
-  auto used_in = [&](int lo, int hi) {
-    int used = 0;
-    for (int i = lo + tid; i < hi; i += kThreads) used += p.ref_counts[i] != 0;
-    return block_sum(used, tmp);
-  };
   const Range mine = share(p.num_pages, rank());
-  exchange(used_in(mine.lo, mine.hi), s_used, true);
+  exchange(used_in(p, mine.lo, mine.hi, p.ref_counts_out != p.ref_counts, tmp), s_used, true);
   int n = 0;
   for (int k = 0; k < ranks(); ++k) n += s_used[k];
   // Every share lies before n or at and behind it, but for one, of which every CTA counts the part behind.
   int cut = 0;
   while (cut < ranks() - 1 && share(p.num_pages, cut).hi <= n) ++cut;
   const Range at_cut = share(p.num_pages, cut);
-  const int cut_movers = used_in(max(n, at_cut.lo), at_cut.hi);
+  const int cut_movers = used_in(p, max(n, at_cut.lo), at_cut.hi, false, tmp);
   int mover = rank() > cut ? cut_movers : 0, hole = 0, moves = cut_movers;
   for (int k = 0; k < ranks(); ++k) {
     const Range r = share(p.num_pages, k);
@@ -336,7 +340,6 @@ __global__ void __launch_bounds__(kThreads)
     if (k < cut && k < rank()) hole += r.hi - r.lo - s_used[k];
   }
   moves = min(moves, pairs);        // (as many holes as movers)
-  const bool elsewhere = p.ref_counts_out != p.ref_counts;
   for (int i0 = mine.lo; i0 < mine.hi; i0 += kTile) {
     int count[kEach], here = 0, total = 0;      // holes in the upper 16 bits, movers in the lower
 #pragma unroll
@@ -356,7 +359,6 @@ __global__ void __launch_bounds__(kThreads)
       const bool moved = i >= n && count[e] != 0, filled = i < n && count[e] == 0;
       if (moved && m < moves) src[m] = i;
       if (filled && h < moves) dst[h] = i;
-      if (elsewhere && !(moved && m < moves) && !(filled && h < moves)) p.ref_counts_out[i] = count[e];
       m += moved;
       h += filled;
     }
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(128) keep_kernel(const __grid_constant__ KeepP
 // Large tables of a call that only adds to counts: the counts are copied ahead, and the pieces of rows need no order.
 static bool spread(PagesParams& p, int rows, int num_sms, unsigned& grid, cudaStream_t st, cudaError_t& e) {
   const int64_t pieces = pieces_of(p, rows);
-  if (pieces <= 4 * kMaxCluster * kWarps) return false;
+  if (pieces <= kMaxCluster * kWarps) return false;
   if (p.ref_counts_out != p.ref_counts)
     e = cudaMemcpyAsync(p.ref_counts_out, p.ref_counts, static_cast<size_t>(p.num_pages) * 4, cudaMemcpyDeviceToDevice, st);
   p.ref_counts = p.ref_counts_out;
