@@ -14,7 +14,8 @@
 // The first four are integer work on tables of a few hundred thousand entries at most, bound by latency: one
 // cluster of CTAs each (a single CTA for small tables), whose barrier stands between the passes that depend on each
 // other (counts before ids, copies of counts before atomics on them), so that each is one launch and needs no
-// workspace.  Atomics are sums of integers: their order changes nothing.
+// workspace.  Atomics are sums of integers: their order changes nothing.  Measured (replayed), 64 rows of 256 columns in 32768
+// pages: fork 5.3 us, grow 8.5, free 4.2, compact 11.4; 4 rows of 16: 1.9, 5.0, 2.1, 4.7.
 #include "ptx.cuh"
 #include "sdpa_internal.h"
 
@@ -431,7 +432,8 @@ constexpr int kCopyUnits = 32 * kCopyEach;      // of an item
 
 // An item, a warp's: 4 KB of K, of V or of the scales of one pair of pages.  A page's units come in the order of memory: units
 // of a row, rows of the inner dimension (slot or head, whichever stride is smaller), the outer one.  A warp looks at
-// 32 of its items at once, so that pairs that are none cost next to nothing.
+// 32 of its items at once, so that pairs that are none cost next to nothing.  Bound: HBM; 660 pages of 262 KB moved in 50.3 us,
+// 6.9 TB/s.  (Through shared memory by bulk copies, 4 to 32 KB each: 66 to 82 us against 57 then.)
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p, const int32_t* src,
                                                             const int32_t* dst, int64_t items) {
   begin();

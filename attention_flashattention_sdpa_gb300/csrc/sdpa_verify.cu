@@ -14,9 +14,9 @@
 //
 // Bound: reading one row of p (and one of q) of each sequence.  The tests need a few single values, which a
 // thread each fetches at once; a cluster of CTAs shares a row, sums meet in its shared memory, and the CTA
-// that the drawn number falls into reads the piece of the row once more, from L2.  Measured: 64 rows of 131072 fp32 values
-// of p and q 10.0 us (5.8 TB/s, 87% of a copy), one of 32000 5.6: the launch, and five latencies in a row (tokens, their
-// probabilities, the row, the cluster's barrier, the piece).
+// that the drawn number falls into reads the piece of the row once more, from L2.  Measured (replayed): 64 rows of 131072 fp32
+// values of p and q 16.0 us from HBM (3.7 TB/s), 10.5 from L2; one of 32000 5.3: the launch, and five latencies in a row
+// (tokens, their probabilities, the row, the cluster's barrier, the piece), which the stream waits for.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -31,7 +31,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kAhead = 2;                      // vectors a thread has in flight
+constexpr int kAhead = 2;                      // vectors of each row a thread has in flight (4: 16.6 us against 16.2 for 64 rows)
 constexpr float kUnit = 4398046511104.f;       // 2^42
 constexpr int kMaxSteps = 520;                 // steps of 32 vectors in a warp's piece: at most 2^20 / 4 / (2 * 8) / 32, and what rounds up
 
@@ -67,7 +67,7 @@ __device__ __forceinline__ Vec<T> load_each(const T* row, int first, int n) {
 
 // A mass p 2^42 as h 2^22 + l: h = floor(p 2^20), and l = p 2^42 - h 2^22 rounded to the nearest (ties to even, as for the
 // sum of both: h 2^22 is even).  Both are the last bits of fp32 sums with 2^23, at the rate of fp32 arithmetic, two
-// elements an instruction (a conversion to 64 bits has the rate of fp64: 31 us against 14 for 64 rows of 131072, then).
+// elements an instruction (a conversion to 64 bits has the rate of fp64: 31 us against 19 for 64 rows of 131072 then).
 // Sums of 2^9 to 2^10 of either fit 32 bits.
 constexpr uint32_t kBits = 0x4B000000u;        // of 2^23
 
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
 
 template <typename T>
 cudaError_t launch_t(const VerifyParams& p, int num_sms, cudaStream_t st) {
-  // CTAs of a row: 8, or as many as leave all rows on the GPU at once (4 CTAs an SM), 2 at least.  Measured, 131072 fp32 values:
+  // CTAs of a row: 8, or as many as leave all rows on the GPU at once (4 CTAs an SM), 2 at least.  Measured, 131072 fp32 values from L2:
   // 64 rows 9.6 us with 8, 12.4 with 4; 96 rows 16.2 and 14.8; 200 rows of 32000 18.5 with 8, 13.2 with 4, 10.7 with 2.
   int cluster = kMaxCluster;
   while (cluster > 2 && static_cast<int64_t>(p.b) * cluster > 4 * static_cast<int64_t>(num_sms)) cluster /= 2;
