@@ -304,6 +304,32 @@ def test_keep(lens, lens_q, s, h, d, page, kind, slot_major, path_kind):
         assert np.array_equal(raw(x), w)
 
 
+@pytest.mark.parametrize("slot_major", [True, False])
+def test_offsets_beyond_32_bits(slot_major):
+    """A cache of 4.6 GB each of K and V: pages and rows at its far end."""
+    m, page, h, d, pages = lib(), 64, 8, 128, 70000
+    k, v = (torch.empty(pages, *((page, h) if slot_major else (h, page)), d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty(pages, h, page, device="cuda") for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    far = [0, 3, 5, 32768, 65536, 69998, 69999]
+    for x in (k, v):
+        x[far] = torch.randint(0, 120, (len(far), *x.shape[1:]), generator=g, device="cuda", dtype=torch.uint8)
+    for x in (ks, vs):
+        x[far] = torch.rand(len(far), h, page, generator=g, device="cuda")
+    view = lambda x: (x.view(torch.float8_e4m3fn).transpose(1, 2) if slot_major else x.view(torch.float8_e4m3fn))    # noqa: E731
+    was = [x[far].clone() for x in (k, v, ks, vs)]
+    m.sdpa_cache_copy(view(k), view(v), words([69999, 0, 65536]), words([3, 69998, 32768]), k_scale=ks, v_scale=vs)
+    for x, w in zip((k, v, ks, vs), was):
+        assert torch.equal(x[far], w[[0, 6, 2, 4, 4, 0, 6]])
+    was = [x[far].clone() for x in (k, v, ks, vs)]
+    # 10 new rows over the border of pages 69999 and 69998
+    m.sdpa_cache_keep(view(k), view(v), words([[69999, 69998]]), words([70]), words([[0, 3, 7, 9] + [-1] * 6]), words([4]), k_scale=ks, v_scale=vs)
+    for x, w, slot in zip((k, v, ks, vs), was, (1 if slot_major else 2,) * 2 + (2, 2)):
+        w = w.transpose(1, slot).contiguous()           # slots second
+        w[6, 61], w[6, 62], w[6, 63] = w[6, 63].clone(), w[5, 3].clone(), w[5, 5].clone()
+        assert torch.equal(x[far].transpose(1, slot), w)
+
+
 def test_pages_on_streams_and_captured():
     """Captured once, replayed on other lengths and tables; the calls follow each other without a wait."""
     m, page, b, columns = lib(), 16, 6, 40

@@ -226,6 +226,20 @@ def test_tokens_are_distributed_as_the_targets():
         assert (np.abs(share - p[0, 0]) <= 5 * np.sqrt(p[0, 0] * (1 - p[0, 0]) / n)).all()
 
 
+def test_offsets_beyond_32_bits():
+    """Sequences 2^31 + 9 elements apart."""
+    rng = np.random.default_rng(9)
+    b, s, vocab, apart = 3, 3, 501, (1 << 31) + 9
+    p, q = distributions(rng, b, s, vocab), distributions(rng, b, s, vocab)
+    big = [torch.empty((b - 1) * apart + s * vocab, dtype=torch.bfloat16, device="cuda").as_strided((b, s, vocab), (apart, vocab, 1)) for _ in range(2)]
+    for t, x in zip(big, (p, q)):
+        t.copy_(torch.from_numpy(x).bfloat16())
+    tokens = rng.integers(0, vocab, (b, s))
+    for u in (rng.random((b, s), dtype=np.float32), np.full((b, s), 0.9), np.zeros((b, s))):
+        check(tokens, big[0], u, draft=big[1])
+        check(tokens, big[0], u, np.array([[-1, 0, 0]] * b))
+
+
 def test_verify_on_streams_and_captured():
     rng = np.random.default_rng(8)
     b, s, vocab = 5, 4, 3001
