@@ -7,8 +7,8 @@
 // Bound: memory.  A row of d elements is spread over d / 16 lanes of 16 elements each, which find
 // the row's largest value by shuffles; a thread walks heads of one token, so that its angles and
 // its page are looked up once.  Measured, 8 heads of 128, E4M3 from or to BF16: 4 prompts of 5001 to
-// 8192 tokens written, K rotated, 36.5 us (4.9 TB/s, 73% of a copy: the roundings of a row wait for
-// its largest value), 32 single tokens 3.0 us; 2 x 8192 tokens read 17.5 us (5.6 TB/s, 83%).
+// 8192 tokens written, K rotated, 36.4 us (4.9 TB/s, 73% of a copy: the roundings of a row wait for
+// its largest value), 32 single tokens 2.9 us; 2 x 8192 tokens read 17.5 us (5.6 TB/s, 83%).
 #include <cuda_fp8.h>
 
 #include <type_traits>
@@ -19,6 +19,7 @@ namespace sdpa {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kSlots = 4;           // heads of a thread in shared memory: one worked on, the others on their way
 constexpr float kE4M3Max = 448.f;
 constexpr float kAmaxMin = 8.673617379884035e-19f;  // 2^-60
 
@@ -55,6 +56,10 @@ __device__ __forceinline__ RowScales row_scales(const float (&x)[16], const floa
   const float scale = (a < kAmaxMin ? kAmaxMin : a) / kE4M3Max, inv = 1.f / scale;   // a NaN stays one
   const float other = __shfl_xor_sync(0xffffffffu, scale, 1), other_inv = __shfl_xor_sync(0xffffffffu, inv, 1);
   return odd ? RowScales{other, scale, other_inv, inv} : RowScales{scale, other, inv, other_inv};
+}
+
+__device__ __forceinline__ void cp_async16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
 }
 
 struct Slot {
@@ -130,8 +135,11 @@ __device__ __forceinline__ void store_item(uint8_t* row, float* scale_at, int m,
 // ROPE: 0 none, 1 rot a multiple of 16, 2 any even rot.
 // (A floor of one block an SM lets the compiler hold a few more registers, 122, still four blocks: 38.5 ->
 // 36.5 us.)
-// AXES: K has several positions a token.
-template <int D, int DT, int CT, int ROPE, bool AXES>
+// AXES: K has several positions a token.  RING: a thread's next heads come through shared memory, each thread's in slots of
+// its own (it waits for its own copies alone); otherwise the next one comes into registers, which is faster where a thread has
+// few heads (1024 tokens of 8 heads in BF16: 4.4 us against 4.6).  With it, 2 x 8192 tokens to E4M3 25.4 -> 23.0 us, rotated by three
+// axes 26.4 -> 23.1 (prompts above 37.2 -> 36.4); with 3 slots 24.2, with 6 25.1.
+template <int D, int DT, int CT, int ROPE, bool AXES, bool RING>
 __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_constant__ CacheRowsParams p, int per,
                                                             bool small) {
   constexpr int LANES = D / 16;
@@ -154,14 +162,28 @@ __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_c
   // A head's K and V are loaded while the one before it is worked on, the first while the angles
   // are computed.
   Raw k_next, v_next;
+  __shared__ uint4 ring[RING ? kSlots : 1][4][RING ? kThreads : 1];
   auto fetch = [&](int h) {
-    if (live && h < h_end) {
+    const bool there = live && h < h_end;
+    if constexpr (RING) {
+      if (there) {
+        auto& to = ring[(h - h0) % kSlots];
+        const uint16_t* a = static_cast<const uint16_t*>(p.k) + bi * p.k_st[0] + h * p.k_st[1] + si * p.k_st[2];
+        const uint16_t* b = static_cast<const uint16_t*>(p.v) + bi * p.v_st[0] + h * p.v_st[1] + si * p.v_st[2] + m * 16;
+        cp_async16(&to[0][threadIdx.x], a + it.lo);
+        cp_async16(&to[1][threadIdx.x], a + it.hi);
+        cp_async16(&to[2][threadIdx.x], b);
+        cp_async16(&to[3][threadIdx.x], b + 8);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    } else if (there) {
       k_next = load_raw(p.k, bi * p.k_st[0] + h * p.k_st[1] + si * p.k_st[2], it.lo, it.hi);
       v_next = load_raw(p.v, bi * p.v_st[0] + h * p.v_st[1] + si * p.v_st[2], m * 16, m * 16 + 8);
     }
   };
-  fetch(h0);
-  if constexpr (CT == kE4M3) {
+#pragma unroll
+  for (int j = 0; j < (RING ? kSlots - 1 : 1); ++j) fetch(h0 + j);
+  if constexpr (CT == kE4M3 && !RING) {
     // The row's other heads start towards L2, a line a lane: 38.3 -> 36.5 us for the prompts above, 16 heads
     // 44.0 -> 41.0.  (16-bit caches, copied without that much work between, were slower so: 44.6 -> 47.8.)
     constexpr int LINES = D / 64;
@@ -188,8 +210,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_c
     const int h = h0 + j;
     const bool on = live && h < h_end;
     float x[16], y[16];
-    const Raw k_now = k_next, v_now = v_next;
-    if (j + 1 < per) fetch(h + 1);
+    Raw k_now, v_now;
+    if constexpr (RING) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
+      const auto& from = ring[j % kSlots];
+      k_now = Raw{{from[0][threadIdx.x], from[1][threadIdx.x]}};
+      v_now = Raw{{from[2][threadIdx.x], from[3][threadIdx.x]}};
+      fetch(h + kSlots - 1);        // into the slot of the head before this one
+    } else {
+      k_now = k_next;
+      v_now = v_next;
+      if (j + 1 < per) fetch(h + 1);
+    }
     if (on) {
       unpack_item<DT>(k_now, x);
       unpack_item<DT>(v_now, y);
@@ -284,19 +316,21 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 template <int D, int DT, int CT>
 cudaError_t write_t(const CacheRowsParams& p, int num_sms, cudaStream_t st) {
   const int64_t tokens = static_cast<int64_t>(p.c.b) * p.s;
-  int per = 8;   // heads a thread walks: as many as leave the GPU full
-  while (per > 1 && tokens * (D / 16) * ((p.c.h_kv + per - 1) / per) < static_cast<int64_t>(num_sms) * 1024) per /= 2;
+  // Heads a thread walks: as many as leave 512 threads an SM, what it holds at once (with twice as many, 4096 tokens of 8 heads 13.8
+  // us against 10.3).
+  int per = p.c.h_kv > 4 ? 8 : p.c.h_kv > 2 ? 4 : p.c.h_kv;
+  while (per > 1 && tokens * (D / 16) * ((p.c.h_kv + per - 1) / per) < static_cast<int64_t>(num_sms) * 512) per /= 2;
   const int groups = (p.c.h_kv + per - 1) / per;
   const int64_t blocks = (tokens * (D / 16) * groups + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(blocks);
   const bool small = blocks * kThreads < (int64_t(1) << 31);
-  const bool vec = p.r.rot % 16 == 0;
-  if (!p.rope) cache_write_kernel<D, DT, CT, 0, false><<<grid, kThreads, 0, st>>>(p, per, small);
-  else if (vec && p.r.axes) cache_write_kernel<D, DT, CT, 1, true><<<grid, kThreads, 0, st>>>(p, per, small);
-  else if (vec) cache_write_kernel<D, DT, CT, 1, false><<<grid, kThreads, 0, st>>>(p, per, small);
-  else if (p.r.axes) cache_write_kernel<D, DT, CT, 2, true><<<grid, kThreads, 0, st>>>(p, per, small);
-  else cache_write_kernel<D, DT, CT, 2, false><<<grid, kThreads, 0, st>>>(p, per, small);
+  auto run = [&](auto kernel) { kernel<<<grid, kThreads, 0, st>>>(p, per, small); };
+  const bool vec = p.r.rot % 16 == 0, ring = per >= 4;
+  if (!p.rope) run(ring ? cache_write_kernel<D, DT, CT, 0, false, true> : cache_write_kernel<D, DT, CT, 0, false, false>);
+  else if (vec && p.r.axes) run(ring ? cache_write_kernel<D, DT, CT, 1, true, true> : cache_write_kernel<D, DT, CT, 1, true, false>);
+  else if (vec) run(ring ? cache_write_kernel<D, DT, CT, 1, false, true> : cache_write_kernel<D, DT, CT, 1, false, false>);
+  else run(p.r.axes ? cache_write_kernel<D, DT, CT, 2, true, false> : cache_write_kernel<D, DT, CT, 2, false, false>);
   return cudaGetLastError();
 }
 
