@@ -89,15 +89,19 @@ __device__ __forceinline__ int block_sum(int x, int* tmp) {
   return total;
 }
 
-// x of every CTA, in every CTA: all[k] is that of CTA k afterwards (the barrier is the cluster's).  The CTAs of the cluster
-// have all begun by the first barrier, so this one comes first where it is the first.
-__device__ __forceinline__ void exchange(int x, int* all, bool first) {
+// x of every CTA, in every CTA: all[k] is that of CTA k afterwards (the barrier is the cluster's).  Once in a kernel that begins
+// with meet(): a CTA's shared memory is there for the others once it has begun.
+__device__ __forceinline__ void meet() {
+  if (gridDim.x > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void exchange(int x, int* all) {
   if (gridDim.x == 1) {
     if (threadIdx.x == 0) all[0] = x;
     __syncthreads();
     return;
   }
-  if (first) ptx::cluster_sync_all();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (threadIdx.x < gridDim.x) {
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(all + rank())), "r"(threadIdx.x));
@@ -222,6 +226,7 @@ __device__ __forceinline__ GrowRow grow_row(const PagesParams& p, const int32_t*
 __global__ void __launch_bounds__(kThreads)
     grow_kernel(const __grid_constant__ PagesParams p, const int32_t* new_lens, int32_t* src, int32_t* dst, int32_t* missing) {
   __shared__ GrowShared sh;
+  meet();
   begin();
   const int tid = threadIdx.x, lane = tid & 31;
   // What is wanted elsewhere goes there as it is, before the barrier behind which it changes.
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   if (tid == 0) sh.base[p.b] = wanted;
   // ... and how many pages that makes.  Behind the barrier the counts and the table may change.
-  exchange(free_count, sh.free, true);
+  exchange(free_count, sh.free);
   const int there = lane < ranks() ? sh.free[lane] : 0;
   const int all = __reduce_add_sync(0xffffffffu, there);
   int before = __reduce_add_sync(0xffffffffu, lane < rank() ? there : 0);
@@ -322,10 +327,11 @@ __global__ void __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(kThreads)
     compact_kernel(const __grid_constant__ PagesParams p, int32_t* src, int32_t* dst, int pairs) {
   __shared__ int tmp[kWarps], s_used[kMaxCluster];
+  meet();
   begin();
   const int tid = threadIdx.x, lane = tid & 31;
   const Range mine = share(p.num_pages, rank());
-  exchange(used_in(p, mine.lo, mine.hi, p.ref_counts_out != p.ref_counts, tmp), s_used, true);
+  exchange(used_in(p, mine.lo, mine.hi, p.ref_counts_out != p.ref_counts, tmp), s_used);
   int n = 0;
   for (int k = 0; k < ranks(); ++k) n += s_used[k];
   // Every share lies before n or at and behind it, but for one, of which every CTA counts the part behind.
