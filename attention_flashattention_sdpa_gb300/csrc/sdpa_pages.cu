@@ -15,7 +15,7 @@
 // cluster of CTAs each (a single CTA for small tables), whose barrier stands between the passes that depend on each
 // other (counts before ids, copies of counts before atomics on them), so that each is one launch and needs no
 // workspace.  Atomics are sums of integers: their order changes nothing.  Measured (replayed), 64 rows of 256 columns in 32768
-// pages: fork 5.3 us, grow 8.5, free 4.2, compact 11.4; 4 rows of 16: 1.9, 5.0, 2.1, 4.7.
+// pages: fork 5.2 us, grow 8.2, free 4.2, compact 10.8; 4 rows of 16: 1.7, 5.0, 2.0, 4.4.
 #include "ptx.cuh"
 #include "sdpa_internal.h"
 
