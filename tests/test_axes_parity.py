@@ -27,6 +27,10 @@ AXES = [
     (1, 2, 1, 3, 8, "bf16", False, False, (1,), "blocks", "near"),
     (1, 5, 3, 300, 512, "f16", False, True, (200, 50, 5, 1), "blocks", "far"),
     (2, 12, 12, 33, 64, "f16", True, True, (16, 16), "blocks", "one row"),
+    (2, 5, 2, 19, 72, "bf16", False, True, (12, 24), "blocks", "far"),               # multiples of 8, not of 16
+    (1, 9, 9, 40, 72, "f16", True, True, (18, 18), "interleaved", "near"),
+    (1, 3, 1, 11, 128, "bf16", True, False, (5, 6, 9), "interleaved", "far"),        # rot 40
+    (2, 2, 0, 6, 64, "f16", False, True, (3, 1), "blocks", "negative"),              # rot 8
 ]
 
 
@@ -72,7 +76,7 @@ def test_axes(b, h_q, h_k, s, d, dtype, inter, token_major, sections, order, kin
     assert torch.equal(q2, qo) and (k is None or torch.equal(k2, ko))
 
 
-@pytest.mark.parametrize("rot,inter", [(64, False), (64, True), (26, False), (26, True)])
+@pytest.mark.parametrize("rot,inter", [(64, False), (64, True), (26, False), (26, True), (40, False), (40, True)])
 def test_one_position_on_all_axes_is_the_plain_rotation(rot, inter):
     m, g = lib(), torch.Generator().manual_seed(4)
     q = bshd(g, "bf16", 2, 3, 21, 64)
