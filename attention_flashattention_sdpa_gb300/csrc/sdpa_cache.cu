@@ -194,15 +194,28 @@ __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_c
     }
   }
   RopePos<AXES> rpos = {};
-  float c[8], s[8];
+  float c[ROPE == 2 ? 16 : 8], s[ROPE == 2 ? 16 : 8];
   if constexpr (ROPE != 0) {
     if (live) rpos = rope_pos<AXES>(p.r, bi, si, pos);
   }
   if constexpr (ROPE == 1) {
     if (it.turned && live) {
+      // (Interleaved pairs as 16 neighbours instead: 48.8 us against 40.3 for 4 x 8192 tokens to E4M3, 66 against 49 in BF16.)
+      const int far = p.r.interleaved ? p.r.rot / 4 + m * 4 : m * 8 + 4, near = p.r.interleaved ? m * 4 : m * 8;   // pairs 4..7, 0..3
+      const uint32_t axes = (axes_from<AXES>(p.r, near) & 0xFFu) | axes_from<AXES>(p.r, far) << 8;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        rope_angle(p.r, __ldg(p.r.table + m * 8 + i), rpos.of(axes_from<AXES>(p.r, m * 8) >> (2 * i)), c[i], s[i]);
+        rope_angle(p.r, __ldg(p.r.table + (i < 4 ? near + i : far + i - 4)), rpos.of(axes >> (2 * i)), c[i], s[i]);
+    }
+  }
+  // 16 neighbours, each with an angle and a partner of its own, `other` elements away.
+  const int half = p.r.rot / 2, turns = ROPE == 2 ? min(16, p.r.rot - m * 16) : 0;
+  auto is_first = [&](int i) { return p.r.interleaved ? i % 2 == 0 : m * 16 + i < half; };
+  if constexpr (ROPE == 2) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int e = m * 16 + i, pair = p.r.interleaved ? e / 2 : e < half ? e : e - half;
+      if (live && i < turns) rope_angle(p.r, __ldg(p.r.table + pair), rpos.of(axes_from<AXES>(p.r, pair)), c[i], s[i]);
     }
   }
   // Every lane of the warp runs the same number of turns (the shuffles need them all).
@@ -232,20 +245,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_c
         }
       }
       if constexpr (ROPE == 2) {
-        // 16 neighbours; each finds its own partner and angle.
-        const int64_t krow = bi * p.k_st[0] + h * p.k_st[1] + si * p.k_st[2];
-        const int half = p.r.rot / 2;
-#pragma unroll 1
+        const int64_t krow = bi * p.k_st[0] + h * p.k_st[1] + si * p.k_st[2] + m * 16;
+        float a[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a[i] = x[i];
+#pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int e = m * 16 + i;
-          if (e >= p.r.rot) break;
-          const int pair = p.r.interleaved ? e / 2 : e % half;
-          const bool first = p.r.interleaved ? e % 2 == 0 : e < half;
-          const int other = p.r.interleaved ? e ^ 1 : (first ? e + half : e - half);
-          float cc, ss;
-          rope_angle(p.r, __ldg(p.r.table + pair), rpos.of(axes_from<AXES>(p.r, pair)), cc, ss);
-          const float a = load16<DT>(p.k, krow + e), b = load16<DT>(p.k, krow + other);
-          x[i] = first ? a * cc - b * ss : b * ss + a * cc;
+          if (i >= turns) continue;
+          const bool first = is_first(i);
+          const float b = p.r.interleaved ? a[i ^ 1] : load16<DT>(p.k, krow + i + (first ? half : -half));
+          x[i] = first ? a[i] * c[i] - b * s[i] : b * s[i] + a[i] * c[i];
         }
       }
     } else {

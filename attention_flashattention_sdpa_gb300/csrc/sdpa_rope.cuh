@@ -135,8 +135,9 @@ __device__ __forceinline__ Spot find_spot(int64_t idx, int items, int b, int s, 
   return x;
 }
 
-// A work item of 16 elements of a head, as two runs of 8: the two halves of 8 pairs (half
-// layout, inside the rotated part), or 16 neighbours.  rot and d are multiples of 16.
+// A work item of 16 elements of a head, as two runs of 8: inside the rotated part of each half of it (the halves of 8 pairs, or 4
+// adjacent pairs of each), so that neighbouring lanes read neighbouring 16 bytes; behind it 16 neighbours.  rot and d are
+// multiples of 16.
 struct RopeItem {
   int lo, hi;      // first element of each run
   bool turned;
@@ -145,9 +146,8 @@ struct RopeItem {
 __device__ __forceinline__ RopeItem rope_item(const RopeArgs& r, int m) {
   RopeItem it;
   it.turned = m * 16 < r.rot;
-  const bool halves = it.turned && !r.interleaved;
-  it.lo = halves ? m * 8 : m * 16;
-  it.hi = halves ? r.rot / 2 + m * 8 : m * 16 + 8;
+  it.lo = it.turned ? m * 8 : m * 16;
+  it.hi = it.turned ? r.rot / 2 + m * 8 : m * 16 + 8;
   return it;
 }
 
