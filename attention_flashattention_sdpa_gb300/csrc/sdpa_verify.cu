@@ -28,10 +28,10 @@
 namespace sdpa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kAhead = 2;                      // vectors of each row a thread has in flight (4: 16.6 us against 16.2 for 64 rows)
+constexpr int kMaxWarps = 16;
+// Vectors a thread has in flight: of one row (2: 64 rows of 131072 12.6 us, 4: 11.6), and of each of two (4: 16.6 us, 2: 16.0).
+constexpr int kAheadOne = 4, kAheadTwo = 2;
 constexpr float kUnit = 4398046511104.f;       // 2^42
 constexpr int kMaxSteps = 520;                 // steps of 32 vectors in a warp's piece: at most 2^20 / 4 / (2 * 8) / 32, and what rounds up
 
@@ -158,13 +158,13 @@ __device__ __forceinline__ Rows rows_at(uint8_t* smem, int s) {
 
 struct Sums {
   int accepted, refused, n_gone;    // refused: the row of the refused draft of a chain, or -1
-  long long warp[kWarps];
+  long long warp[kMaxWarps];
   long long cta[2][kMaxCluster];    // of every CTA of the cluster, in each turn
   long long step[kMaxSteps];
 };
 
 // Which rows are accepted: r.path, sh.accepted; what may not be drawn: sh.refused (a chain with q), r.gone.
-template <typename T>
+template <typename T, int THREADS>
 __device__ void walk(const VerifyParams& p, const Rows& r, Sums& sh, int bi, int len) {
   const int tid = threadIdx.x;
   const T* probs = static_cast<const T*>(p.probs) + bi * p.probs_b;
@@ -174,7 +174,7 @@ __device__ void walk(const VerifyParams& p, const Rows& r, Sums& sh, int bi, int
     sh.accepted = len;
     sh.n_gone = 0;
   }
-  for (int j = tid; j < len; j += kThreads) {
+  for (int j = tid; j < len; j += THREADS) {
     const int x = __ldg(p.tokens + at + j);
     const int par = j == 0 ? -1 : p.parents ? __ldg(p.parents + at + j) : j - 1;
     const bool node = j > 0 && par >= 0 && par < j, known = node && x >= 0 && x < p.vocab;
@@ -191,14 +191,14 @@ __device__ void walk(const VerifyParams& p, const Rows& r, Sums& sh, int bi, int
   __syncthreads();
   if (!p.parents) {
     // A chain: up to the first that is not accepted.
-    for (int j = tid; j < len; j += kThreads) {
+    for (int j = tid; j < len; j += THREADS) {
       bool good = j == 0;
       if (j > 0) good = p.draft ? r.good[j] : __ldg(p.uniform + at + j) * static_cast<double>(kUnit) < static_cast<double>(r.mass[j]);
       if (!good) atomicMin(&sh.accepted, j);
     }
     __syncthreads();
     const int n = sh.accepted;
-    for (int j = tid; j < n; j += kThreads) r.path[j] = j;
+    for (int j = tid; j < n; j += THREADS) r.path[j] = j;
     if (tid == 0) {
       sh.refused = p.draft && n < len ? n : -1;
       if (!p.draft && n < len) {
@@ -211,20 +211,20 @@ __device__ void walk(const VerifyParams& p, const Rows& r, Sums& sh, int bi, int
     return;
   }
   // A tree.  A token that an earlier sibling has counts nothing.
-  bool twin[kVerifyRows / kThreads];
+  bool twin[kVerifyRows / THREADS];
 #pragma unroll
-  for (int k = 0; k < kVerifyRows / kThreads; ++k) {
-    const int j = tid + k * kThreads;
+  for (int k = 0; k < kVerifyRows / THREADS; ++k) {
+    const int j = tid + k * THREADS;
     twin[k] = false;
     if (j < len && r.parent[j] >= 0)
       for (int i = r.parent[j] + 1; i < j; ++i) twin[k] |= r.parent[i] == r.parent[j] && r.token[i] == r.token[j];
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kVerifyRows / kThreads; ++k)
-    if (twin[k]) r.mass[tid + k * kThreads] = 0;
+  for (int k = 0; k < kVerifyRows / THREADS; ++k)
+    if (twin[k]) r.mass[tid + k * THREADS] = 0;
   __syncthreads();
-  for (int j = tid; j < len; j += kThreads) {
+  for (int j = tid; j < len; j += THREADS) {
     long long left = static_cast<long long>(kUnit);
     if (r.parent[j] >= 0)
       for (int i = r.parent[j] + 1; i < j; ++i) left -= r.parent[i] == r.parent[j] ? r.mass[i] : 0;
@@ -270,9 +270,9 @@ __device__ void walk(const VerifyParams& p, const Rows& r, Sums& sh, int bi, int
   __syncthreads();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_constant__ VerifyParams p, int cluster) {
-  constexpr int N = Vec<T>::N;
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const __grid_constant__ VerifyParams p, int cluster) {
+  constexpr int N = Vec<T>::N, WARPS = THREADS / 32;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ Sums sh;
   const Rows r = rows_at(smem_raw, p.s);
@@ -285,12 +285,12 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
   const int len = p.seq_lens_q ? min(max(__ldg(p.seq_lens_q + bi), 0), p.s) : p.s;
   const int64_t at = static_cast<int64_t>(bi) * p.s;
   const float u0 = __ldg(p.uniform + at);
-  if (len > 0) walk<T>(p, r, sh, bi, len);
+  if (len > 0) walk<T, THREADS>(p, r, sh, bi, len);
   const int accepted = len > 0 ? sh.accepted : 0;
   // Behind the new token there is none; the token itself is written by the CTA that finds it.
   if (rank == 0) {
     if (tid == 0) p.accepted[bi] = accepted;
-    for (int j = tid; j < p.s; j += kThreads) {
+    for (int j = tid; j < p.s; j += THREADS) {
       p.path[at + j] = j < accepted ? r.path[j] : -1;
       if (j != accepted - 1) p.new_tokens[at + j] = j < accepted ? r.token[r.path[j + 1]] : -1;
     }
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
   // Vectors of 16 bytes from the multiple of 16 at or before the row's start; each warp has a piece of them.
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
   const bool less_wide = less && reinterpret_cast<uintptr_t>(less) % 16 / sizeof(T) == static_cast<unsigned>(off);
-  const int vectors = (off + p.vocab + N - 1) / N, pieces = cluster * kWarps, per = (vectors + pieces - 1) / pieces;
+  const int vectors = (off + p.vocab + N - 1) / N, pieces = cluster * WARPS, per = (vectors + pieces - 1) / pieces;
   // (Vectors 0 and `inner` may hold elements that are not the row's.)
   const int inner = (off + p.vocab) / N, inner0 = off ? 1 : 0;
   auto value = [&](int v, bool diff) {
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
   // What is left of the distribution first; where that is nothing, the distribution.
   bool diff = less != nullptr;
   int n_gone = sh.n_gone;
-  const int piece = rank * kWarps + warp, v_lo = min(vectors, piece * per), v_hi = min(vectors, v_lo + per);
+  const int piece = rank * WARPS + warp, v_lo = min(vectors, piece * per), v_hi = min(vectors, v_lo + per);
   long long total = 0, target = 0;
   for (int turn = 0; turn < 2; ++turn) {
     long long sum = 0;
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
       }
       n += N;
     };
-    // Whole vectors, kAhead of them loaded at once; MODE 0: the row, 1: less another row as aligned as it is, 2: less any other.
+    // Whole vectors, several of them loaded at once; MODE 0: the row, 1: less another row as aligned as it is, 2: less any other.
     auto stream = [&](auto mode) {
       constexpr int MODE = decltype(mode)::value;
       const int hi = min(v_hi, inner);
@@ -368,7 +368,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
         }
         if (n > 512) flush();
       };
-      for (; v + 32 * (kAhead - 1) < hi; v += 32 * kAhead) some(std::integral_constant<int, kAhead>());
+      constexpr int AHEAD = MODE == 0 ? kAheadOne : kAheadTwo;
+      for (; v + 32 * (AHEAD - 1) < hi; v += 32 * AHEAD) some(std::integral_constant<int, AHEAD>());
       for (; v < hi; v += 32) some(std::integral_constant<int, 1>());
     };
     if (!diff) stream(std::integral_constant<int, 0>());
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
     __syncthreads();
     if (warp == 0) {
       // The CTA's sum goes to every CTA of the cluster.
-      const long long all = warp_sum(lane < kWarps ? sh.warp[lane] : 0);
+      const long long all = warp_sum(lane < WARPS ? sh.warp[lane] : 0);
       if (turn == 0) cluster_wait();           // they have all begun
       if (lane < cluster) st_cluster(&sh.cta[turn][rank], lane, all);
     } else if (turn == 0) {
@@ -412,9 +413,9 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
     if (rank == 0 && tid == 0) *out = -1;
     return;
   }
-  const int w = pick(lane < kWarps ? sh.warp[lane] : 0, kWarps, target, lane);
+  const int w = pick(lane < WARPS ? sh.warp[lane] : 0, WARPS, target, lane);
   // The piece of warp w once more, a step of 32 vectors a warp.
-  const int lo = min(vectors, (rank * kWarps + w) * per), hi = min(vectors, lo + per), steps = (hi - lo + 31) / 32;
+  const int lo = min(vectors, (rank * WARPS + w) * per), hi = min(vectors, lo + per), steps = (hi - lo + 31) / 32;
   auto left_of = [&](int v, long long (&mass)[N]) {
     long long sum = 0;
     if (v < hi) {
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
   };
   long long mass[N], sum = 0;
   int k = warp;
-  for (; k < steps; k += kWarps) {
+  for (; k < steps; k += WARPS) {
     sum = left_of(lo + 32 * k + lane, mass);
     const long long all = warp_sum(sum);
     if (lane == 0) sh.step[k] = all;
@@ -450,8 +451,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
     target -= all;
   }
   // The warp that had this step goes on: its values are at hand where it had no other behind it.
-  if (step % kWarps != warp) return;
-  if (step + kWarps < steps) sum = left_of(lo + 32 * step + lane, mass);
+  if (step % WARPS != warp) return;
+  if (step + WARPS < steps) sum = left_of(lo + 32 * step + lane, mass);
   long long to = warp_scan(sum, lane) - sum;       // before this lane
   if (target < to || target >= to + sum) return;
 #pragma unroll
@@ -463,13 +464,17 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
 
 template <typename T>
 cudaError_t launch_t(const VerifyParams& p, int num_sms, cudaStream_t st) {
-  // CTAs of a row: 8, or as many as leave all rows on the GPU at once (4 CTAs an SM), 2 at least.  Measured, 131072 fp32 values from L2:
+  // CTAs of a row: 8, or as many as leave all rows on the GPU at once (1024 threads an SM), 2 at least.  Measured, 131072 fp32 values from L2:
   // 64 rows 9.6 us with 8, 12.4 with 4; 96 rows 16.2 and 14.8; 200 rows of 32000 18.5 with 8, 13.2 with 4, 10.7 with 2.
   int cluster = kMaxCluster;
   while (cluster > 2 && static_cast<int64_t>(p.b) * cluster > 4 * static_cast<int64_t>(num_sms)) cluster /= 2;
+  // Twice the threads a CTA for fp32 rows while there are two vectors for each thread and all CTAs stay on the GPU: 16 rows of 131072 9.9 ->
+  // 8.2 us, one 7.1 -> 6.1; 64 rows 16 -> 20, one of 1000 4.1 -> 4.4.  (16-bit rows: 7.5 and 7.6; trees of 48 in a step 12.1 and 13.8.)
+  constexpr int kMore = sizeof(T) == 4 ? 512 : 256;
+  const bool more = static_cast<int64_t>(p.b) * kMaxCluster <= 2 * static_cast<int64_t>(num_sms) && p.vocab >= 2 * Vec<T>::N * kMore * kMaxCluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.b) * cluster);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(more ? kMore : 256);
   cfg.dynamicSmemBytes = static_cast<size_t>(p.s) * kRowBytes;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
@@ -480,7 +485,7 @@ cudaError_t launch_t(const VerifyParams& p, int num_sms, cudaStream_t st) {
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<T>, p, cluster);
+  return cudaLaunchKernelEx(&cfg, more ? verify_kernel<T, kMore> : verify_kernel<T, 256>, p, cluster);
 }
 
 }  // namespace
