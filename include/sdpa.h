@@ -485,7 +485,8 @@ SDPA_API sdpa_status_t sdpa_cache_copy(const sdpa_cache_t* c, const int32_t* src
 /* Keeps some of the newest tokens: of the last len_q positions of each sequence (seq_lens_q DEVICE [b], clamped to [0, s], or
  * NULL: s), row path[i][j] moves to row j for all j < accepted[i].  path: DEVICE [b][s], ascending in the
  * part that is read (as sdpa_verify gives it); entries outside [0, len_q) move nothing.  accepted: DEVICE [b].  Lengths are the
- * caller's: seq_lens_kv - len_q + accepted afterwards; rows behind that are left as they come.  K, V and their scales. */
+ * caller's: seq_lens_kv - len_q + accepted afterwards; rows behind that are left as they come.  K, V and their scales.  The pages
+ * of those positions are to be the sequence's own, as sdpa_cache_grow leaves them. */
 SDPA_API sdpa_status_t sdpa_cache_keep(const sdpa_cache_t* c, const int32_t* path, const int32_t* accepted, int32_t s,
                                        const int32_t* seq_lens_q, void* stream);
 
@@ -512,12 +513,12 @@ typedef struct {
 
 /* Children of an accepted row n are tried in ascending order.  Child i with token x is accepted iff
  *   uniform[i] * draft_probs[i][x] < probs[n][x]                                    with draft_probs, or
- *   uniform[i] * max(0, 1 - sum of probs[n][x'] of refused siblings) < probs[n][x]  without (a token that an earlier sibling has
- *                                                                                   too is refused).
+ *   uniform[i] * max(0, 1 - sum of probs[n][x'] of refused siblings) < probs[n][x]  without (in the whole numbers below; a token
+ *                                                                                   that an earlier sibling has too is refused).
  * The new token is drawn behind the last accepted row n: from max(probs[n] - draft_probs[i], 0) where a chain's row i was refused,
  * from probs[n] without its children's tokens where there are no draft_probs; from probs[n] where that leaves nothing.
  * Tokens so chosen are distributed as the target's own.  In sums and draws a probability counts as a whole number of 2^-42
- * (values outside [0, 1] as the nearer end, NaN as 0): the new token is the first whose running sum exceeds
+ * (values outside [0, 1] as the nearer end, NaN as 0; less than 2^-43 is nothing): the new token is the first whose running sum exceeds
  * floor(uniform[0] * 2^31) / 2^31 of the total, whatever the order of the sums.  Where the total is 0 it is -1. */
 SDPA_API sdpa_status_t sdpa_verify(const sdpa_verify_t* p, void* stream);
 
