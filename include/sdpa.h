@@ -518,7 +518,7 @@ typedef struct {
  * The new token is drawn behind the last accepted row n: from max(probs[n] - draft_probs[i], 0) where a chain's row i was refused,
  * from probs[n] without its children's tokens where there are no draft_probs; from probs[n] where that leaves nothing.
  * Tokens so chosen are distributed as the target's own.  In sums and draws a probability counts as a whole number of 2^-42
- * (values outside [0, 1] as the nearer end, NaN as 0; less than 2^-43 is nothing): the new token is the first whose running sum exceeds
+ * (values outside [0, 1] as the nearer end, NaN as 0; 2^-43 and less is nothing): the new token is the first whose running sum exceeds
  * floor(uniform[0] * 2^31) / 2^31 of the total, whatever the order of the sums.  Where the total is 0 it is -1. */
 SDPA_API sdpa_status_t sdpa_verify(const sdpa_verify_t* p, void* stream);
 
