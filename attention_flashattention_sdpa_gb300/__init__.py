@@ -875,7 +875,8 @@ def sdpa_verify(tokens, probs, uniform, accepted, path, new_tokens, *, parents=N
     seq_lens_q: int32 [b] rows that take part (None: all).
 
     accepted: int32 [b] rows kept, row 0 among them; path: int32 [b, s], those rows; new_tokens: int32 [b, s], the accepted
-    drafts and the token drawn behind them, ``accepted`` in all; -1 behind those.  Rules in ``include/sdpa.h``."""
+    drafts and the token drawn behind them, ``accepted`` in all; -1 behind those.  These lie apart from all inputs.  Rules in
+    ``include/sdpa.h``."""
     if _Lazy.torch is None:
         _Lazy.load()
     shape = probs.shape

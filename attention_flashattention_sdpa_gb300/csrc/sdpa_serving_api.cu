@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 
 #include "../../include/sdpa.h"
 #include "sdpa_internal.h"
@@ -202,6 +203,27 @@ sdpa_status_t words(const char* name, const void* ptr) {
 bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + 4 * static_cast<uintptr_t>(m) && y < x + 4 * static_cast<uintptr_t>(n);
+}
+
+// Words that a call reads or writes (none where `at` is NULL).
+struct Words {
+  const char* name;
+  const void* at;
+  int64_t n;
+};
+
+// What is written lies apart from what is read, and from what else is written: the CTAs of a call read and write in no order.
+sdpa_status_t apart(std::initializer_list<Words> written, std::initializer_list<Words> read) {
+  auto clear = [](const Words& w, const Words& x) {
+    return x.at == nullptr || !overlap(static_cast<const int32_t*>(w.at), w.n, static_cast<const int32_t*>(x.at), x.n);
+  };
+  for (const Words& w : written) {
+    for (const Words& x : read)
+      if (!clear(w, x)) SDPA_REFUSE(SDPA_ERR_LAYOUT, "%s must lie apart from %s", w.name, x.name);
+    for (const Words& x : written)
+      if (&x != &w && !clear(w, x)) SDPA_REFUSE(SDPA_ERR_LAYOUT, "%s must lie apart from %s", w.name, x.name);
+  }
+  return SDPA_OK;
 }
 
 // Words from the first to the last entry of a page table.
@@ -631,6 +653,9 @@ sdpa_status_t sdpa_verify(const sdpa_verify_t* p, void* stream_) {
     SDPA_REFUSE(SDPA_ERR_LAYOUT, "probs and draft_probs must be aligned to their elements");
   if (p->probs_b < 0 || p->probs_s < 0 || p->draft_b < 0 || p->draft_s < 0)
     SDPA_REFUSE(SDPA_ERR_LAYOUT, "strides of probs and draft_probs must not be negative");
+  const int64_t rows = static_cast<int64_t>(p->b) * p->s;
+  SDPA_TRY(apart({{"accepted", p->accepted, p->b}, {"path", p->path, rows}, {"new_tokens", p->new_tokens, rows}},
+                 {{"tokens", p->tokens, rows}, {"parents", p->parents, rows}, {"seq_lens_q", p->seq_lens_q, p->b}, {"uniform", p->uniform, rows}}));
   sdpa::VerifyParams prm;
   memset(&prm, 0, sizeof(prm));
   prm.tokens = p->tokens;

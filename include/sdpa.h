@@ -491,7 +491,8 @@ SDPA_API sdpa_status_t sdpa_cache_keep(const sdpa_cache_t* c, const int32_t* pat
                                        const int32_t* seq_lens_q, void* stream);
 
 /* Drafted tokens verified against the target's probabilities (speculative sampling: Leviathan et al., Chen et al., 2023; without
- * draft_probs a tree of candidates as in Miao et al., 2023). */
+ * draft_probs a tree of candidates as in Miao et al., 2023).  accepted, path and new_tokens lie apart from each other and from all
+ * that is read: a sequence's rows are read by several CTAs, and one of them writes. */
 typedef struct {
   int32_t b;                    /* sequences */
   int32_t s;                    /* rows of each, 1..1024: row 0 the newest token that is decided, the others drafted */
