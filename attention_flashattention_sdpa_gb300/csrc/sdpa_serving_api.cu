@@ -258,6 +258,18 @@ sdpa_status_t check_pages(const sdpa_pages_t* p, int rows_out, bool in_place) {
   return SDPA_OK;
 }
 
+// What a call for pages writes (its own lists, and the tables behind them) lies apart from what it reads, but for a table or counts
+// that are changed in place (check_pages).
+sdpa_status_t check_lists(const sdpa_pages_t* p, int rows_out, std::initializer_list<Words> lists, Words lens) {
+  const Words table = {"page_table", p->page_table, table_words(p->b, p->max_pages, p->page_table_stride)};
+  const Words table_out = {"page_table_out", p->page_table_out, table_words(rows_out, p->max_pages, p->page_table_out_stride)};
+  const Words counts = {"ref_counts", p->ref_counts, p->num_pages}, counts_out = {"ref_counts_out", p->ref_counts_out, p->num_pages};
+  const Words seq_lens = {"seq_lens", p->seq_lens, p->b};
+  SDPA_TRY(apart(lists, {table, table_out, counts, counts_out, seq_lens, lens}));
+  SDPA_TRY(apart({table_out}, {counts, counts_out, seq_lens, lens}));
+  return apart({counts_out}, {table, seq_lens, lens});
+}
+
 sdpa::PagesParams pages_params(const sdpa_pages_t* p) {
   sdpa::PagesParams prm;
   memset(&prm, 0, sizeof(prm));
@@ -539,8 +551,7 @@ sdpa_status_t sdpa_cache_fork(const sdpa_pages_t* p, const int32_t* parents, int
   SDPA_TRY(check_pages(p, b_out, false));
   SDPA_TRY(words("parents", parents));
   SDPA_TRY(words("seq_lens_out", seq_lens_out));
-  if (overlap(p->seq_lens, p->b, seq_lens_out, b_out)) SDPA_REFUSE(SDPA_ERR_LAYOUT, "seq_lens_out must lie apart from seq_lens");
-  if (overlap(parents, b_out, seq_lens_out, b_out)) SDPA_REFUSE(SDPA_ERR_LAYOUT, "seq_lens_out must lie apart from parents");
+  SDPA_TRY(check_lists(p, b_out, {{"seq_lens_out", seq_lens_out, b_out}}, {"parents", parents, b_out}));
   log_pages("fork", p, b_out);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   cudaError_t e = sdpa::launch_fork(pages_params(p), parents, b_out, seq_lens_out, sdpa::api_num_sms(), stream);
@@ -557,7 +568,7 @@ sdpa_status_t sdpa_cache_grow(const sdpa_pages_t* p, const int32_t* new_lens, in
   SDPA_TRY(words("src", src));
   SDPA_TRY(words("dst", dst));
   SDPA_TRY(words("missing", missing));
-  if (overlap(src, p->b, dst, p->b)) SDPA_REFUSE(SDPA_ERR_LAYOUT, "src and dst must lie apart");
+  SDPA_TRY(check_lists(p, p->b, {{"src", src, p->b}, {"dst", dst, p->b}, {"missing", missing, 1}}, {"new_lens", new_lens, p->b}));
   log_pages("grow", p, 0);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   cudaError_t e = sdpa::launch_grow(pages_params(p), new_lens, src, dst, missing, stream);
@@ -567,6 +578,7 @@ sdpa_status_t sdpa_cache_grow(const sdpa_pages_t* p, const int32_t* new_lens, in
 sdpa_status_t sdpa_cache_free(const sdpa_pages_t* p, const int32_t* keep_lens, void* stream_) {
   SDPA_TRY(check_pages(p, p ? p->b : 1, true));
   SDPA_TRY(words("keep_lens", keep_lens));
+  SDPA_TRY(check_lists(p, p->b, {}, {"keep_lens", keep_lens, p->b}));
   log_pages("free", p, 0);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   cudaError_t e = sdpa::launch_free(pages_params(p), keep_lens, sdpa::api_num_sms(), stream);
@@ -578,7 +590,7 @@ sdpa_status_t sdpa_cache_compact(const sdpa_pages_t* p, int32_t* src, int32_t* d
   if (pairs < 1) SDPA_REFUSE(SDPA_ERR_INVALID_ARG, "sizes must be >= 1 (pairs=%d)", pairs);
   SDPA_TRY(words("src", src));
   SDPA_TRY(words("dst", dst));
-  if (overlap(src, pairs, dst, pairs)) SDPA_REFUSE(SDPA_ERR_LAYOUT, "src and dst must lie apart");
+  SDPA_TRY(check_lists(p, p->b, {{"src", src, pairs}, {"dst", dst, pairs}}, {"", nullptr, 0}));
   log_pages("compact", p, pairs);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   cudaError_t e = sdpa::launch_compact(pages_params(p), src, dst, pairs, stream);

@@ -434,8 +434,9 @@ SDPA_API sdpa_status_t sdpa_decode(const sdpa_cache_t* c, const sdpa_decode_t* p
  *
  * A sequence of n tokens reaches columns 0 .. ceil(n / page_size) - 1 of its row; other columns are neither read nor
  * counted.  Lengths are clamped as in sdpa_cache_t.  Entries outside [0, num_pages) are missing pages: they have
- * no count.  Counts must be at least the number of reaching entries.  Lists and lengths that a call writes lie apart from
- * all that it reads.  Calls that change the same counts or the same table must not run at the same time.
+ * no count.  Counts must be at least the number of reaching entries.  What a call writes lies apart from what it reads and from
+ * what else it writes, but for a table or counts that are changed in place; anything else is refused.  Calls that
+ * change the same counts or the same table must not run at the same time.
  * ------------------------------------------------------------------------------------------ */
 typedef struct {
   int32_t num_pages;            /* 1..2^30 */

@@ -42,3 +42,59 @@ def test_verify_refuses_outputs_that_overlap(m, out, other):
 
 def test_verify_without_the_optional_inputs(m):
     assert verify(m, parents=0, seq_lens_q=0) == 5, m.sdpa_last_error_string()
+
+
+# ---- pages: 3 rows of 4 columns (6 words apart), 100 pages ---------------------------------------
+
+PAGES = dict(page_table=(FAKE, 16), seq_lens=(FAKE + 0x1000, 3), ref_counts=(FAKE + 0x2000, 100), page_table_out=(FAKE + 0x3000, 16),
+             ref_counts_out=(FAKE + 0x4000, 100))
+LISTS = dict(fork=dict(parents=(FAKE + 0x5000, 3), seq_lens_out=(FAKE + 0x6000, 3)),
+             grow=dict(new_lens=(FAKE + 0x5000, 3), src=(FAKE + 0x6000, 3), dst=(FAKE + 0x7000, 3), missing=(FAKE + 0x8000, 1)),
+             free=dict(keep_lens=(FAKE + 0x5000, 3)), compact=dict(src=(FAKE + 0x6000, 7), dst=(FAKE + 0x7000, 7)))
+OUT = {"page_table_out", "ref_counts_out", "seq_lens_out", "src", "dst", "missing"}
+
+
+def pages(m, call, in_place=(), **over):
+    at = {name: a for name, (a, _) in {**PAGES, **LISTS[call]}.items()}
+    at.update(over)
+    for name in in_place:
+        at[name + "_out"] = at[name]
+    p = m.Pages(num_pages=100, page_size=16, b=3, max_pages=4, page_table_stride=6, page_table_out_stride=6, **{n: at[n] for n in PAGES})
+    held, L = ctypes.addressof(p), m.lib
+    if call == "fork":
+        return L.sdpa_cache_fork(held, at["parents"], 3, at["seq_lens_out"], None)
+    if call == "grow":
+        return L.sdpa_cache_grow(held, at["new_lens"], at["src"], at["dst"], at["missing"], None)
+    if call == "free":
+        return L.sdpa_cache_free(held, at["keep_lens"], None)
+    return L.sdpa_cache_compact(held, at["src"], at["dst"], 7, None)
+
+
+@pytest.mark.parametrize("call", LISTS)
+def test_pages_refuse_what_overlaps(m, call):
+    """Every output on the first and the last word of every other operand, and right before and behind it."""
+    where = {**PAGES, **LISTS[call]}
+    for out in sorted(OUT & set(where)):
+        n = where[out][1]
+        for other, (at, words) in where.items():
+            if other == out:
+                continue
+            same = out == other + "_out" and other in ("page_table", "ref_counts")
+            for delta in (0, 4 * (words - 1), -4 * (n - 1)):
+                if same and delta == 0 and not (call == "fork" and out == "page_table_out"):
+                    continue             # in place
+                got = pages(m, call, **{out: at + delta})
+                assert got == 3 and "apart" in m.sdpa_last_error_string(), (out, other, delta, got)
+            for delta in (4 * words, -4 * n):
+                assert pages(m, call, **{out: at + delta}) == 5, (out, other, delta, m.sdpa_last_error_string())
+
+
+@pytest.mark.parametrize("call", LISTS)
+def test_pages_in_place(m, call):
+    where = ("ref_counts",) if call == "fork" else ("page_table", "ref_counts")
+    assert pages(m, call, in_place=where) == 5, m.sdpa_last_error_string()
+    for name in sorted({"src", "dst", "missing", "seq_lens_out"} & set(LISTS[call])):
+        for over in where:
+            assert pages(m, call, in_place=where, **{name: PAGES[over][0] + 4}) == 3 and "apart" in m.sdpa_last_error_string()
+    if "new_lens" in LISTS[call]:        # lengths that stay as they are
+        assert pages(m, call, in_place=where, new_lens=PAGES["seq_lens"][0]) == 5, m.sdpa_last_error_string()
