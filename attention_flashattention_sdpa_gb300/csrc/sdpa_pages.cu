@@ -38,7 +38,8 @@ __device__ __forceinline__ void sync_all() {
   else __syncthreads();
 }
 
-// Whatever ran before is done; what comes next may be put in place meanwhile (it waits here in its turn).
+// Whatever ran before is done; what comes next may be put in place meanwhile (it waits here in its turn).  What the kernels read
+// may have been written while they were already there, so it comes by plain loads, which stay behind the wait.
 __device__ __forceinline__ void begin() {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -110,7 +111,7 @@ __device__ __forceinline__ void exchange(int x, int* all) {
   ptx::cluster_sync_all();
 }
 
-__device__ __forceinline__ int clamp_tokens(const int32_t* lens, int i, int top) { return min(max(__ldg(lens + i), 0), top); }
+__device__ __forceinline__ int clamp_tokens(const int32_t* lens, int i, int top) { return min(max(lens[i], 0), top); }
 
 __device__ __forceinline__ int columns_of(const PagesParams& p, int len) {
   return static_cast<int>((static_cast<int64_t>(len) + p.page_size - 1) / p.page_size);
@@ -131,8 +132,15 @@ __device__ __forceinline__ void for_chunks(int rows, int columns, F f) {
 // Counts as they are, where they are wanted elsewhere, before anyone adds to them.
 __device__ __forceinline__ void copy_counts(const PagesParams& p) {
   if (p.ref_counts_out == p.ref_counts) return;
-#pragma unroll 4
-  for (int i = rank() * kThreads + threadIdx.x; i < p.num_pages; i += ranks() * kThreads) p.ref_counts_out[i] = __ldg(p.ref_counts + i);
+  const int step = ranks() * kThreads;
+  for (int64_t i0 = rank() * kThreads + threadIdx.x; i0 < p.num_pages; i0 += kEach * step) {
+    int count[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) count[e] = i0 + e * step < p.num_pages ? p.ref_counts[i0 + e * step] : 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (i0 + e * step < p.num_pages) p.ref_counts_out[i0 + e * step] = count[e];
+  }
   sync_all();
 }
 
@@ -160,14 +168,14 @@ __global__ void __launch_bounds__(kThreads)
   // The new rows, and the old ones, whose ownership ends.
   for_chunks(b_out + p.b, p.max_pages, [&](int x, int c0) {
     const bool is_new = x < b_out;
-    const int j = is_new ? __ldg(parents + x) : x - b_out, len = j >= 0 && j < p.b ? clamp_tokens(p.seq_lens, j, p.max_len) : 0;
+    const int j = is_new ? parents[x] : x - b_out, len = j >= 0 && j < p.b ? clamp_tokens(p.seq_lens, j, p.max_len) : 0;
     const int reach = columns_of(p, len);
     if (is_new && c0 == 0 && lane == 0) seq_lens_out[x] = len;
     int page[kChunk / 32];
 #pragma unroll
     for (int k = 0; k < kChunk / 32; ++k) {
       const int c = c0 + lane + 32 * k;
-      page[k] = c < reach ? __ldg(p.page_table + j * p.table_stride + c) : -1;
+      page[k] = c < reach ? p.page_table[j * p.table_stride + c] : -1;
     }
 #pragma unroll
     for (int k = 0; k < kChunk / 32; ++k) {
@@ -184,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) free_kernel(const __grid_constant__ 
   const int lane = threadIdx.x & 31;
   const bool in_place = p.page_table_out == p.page_table;
   for_chunks(p.b, p.max_pages, [&](int i, int c0) {
-    const int len = clamp_tokens(p.seq_lens, i, p.max_len), keep = min(len, max(0, __ldg(keep_lens + i)));
+    const int len = clamp_tokens(p.seq_lens, i, p.max_len), keep = min(len, max(0, keep_lens[i]));
     const int first = columns_of(p, keep), end = columns_of(p, len);
     int page[kChunk / 32];
 #pragma unroll
@@ -451,8 +459,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     int pair = 0, from = -1, to = -1;
     if (mine < items) {
       pair = static_cast<int>(mine / p.items_per_pair);
-      from = __ldg(src + pair);
-      to = __ldg(dst + pair);
+      from = src[pair];
+      to = dst[pair];
     }
     const int mine_part = static_cast<int>(mine - static_cast<int64_t>(pair) * p.items_per_pair);
     uint32_t live = __ballot_sync(0xffffffffu, is_page(from, p.num_pages) && is_page(to, p.num_pages) && from != to);
@@ -497,9 +505,9 @@ __global__ void __launch_bounds__(128) keep_kernel(const __grid_constant__ KeepP
   const int i = blockIdx.x / p.blocks, idx = (blockIdx.x - i * p.blocks) * 128 + threadIdx.x;
   if (idx >= 2 * per) return;
   const int which = idx / per, at = idx % per, h = at / units, u = at % units;
-  const int len_q = p.seq_lens_q ? min(max(__ldg(p.seq_lens_q + i), 0), p.s) : p.s;
+  const int len_q = p.seq_lens_q ? min(max(p.seq_lens_q[i], 0), p.s) : p.s;
   const int len_kv = clamp_tokens(p.c.seq_lens_kv, i, p.c.max_len);
-  const int n = min(min(max(__ldg(p.accepted + i), 0), p.s), len_q), start = len_kv - len_q;
+  const int n = min(min(max(p.accepted[i], 0), p.s), len_q), start = len_kv - len_q;
   const int64_t(&st)[3] = which ? p.c.v_st : p.c.k_st;
   uint8_t* base = which ? p.c.v : p.c.k;
   float* scale = which ? p.c.v_scale : p.c.k_scale;
@@ -507,7 +515,7 @@ __global__ void __launch_bounds__(128) keep_kernel(const __grid_constant__ KeepP
   auto slot_of = [&](int row, int64_t& to) {
     const int pos = start + row;
     if (row < 0 || row >= len_q || pos < 0 || pos >= len_kv) return false;
-    const int col = pos / p.c.page_size, page = __ldg(p.c.page_table + i * p.c.page_table_stride + col), slot = pos - col * p.c.page_size;
+    const int col = pos / p.c.page_size, page = p.c.page_table[i * p.c.page_table_stride + col], slot = pos - col * p.c.page_size;
     if (!is_page(page, p.c.num_pages)) return false;
     to = is_scale ? (static_cast<int64_t>(page) * p.c.h_kv + h) * p.c.page_size + slot : page * st[0] + h * st[1] + slot * st[2] + u * 16;
     return true;
@@ -520,7 +528,7 @@ __global__ void __launch_bounds__(128) keep_kernel(const __grid_constant__ KeepP
     for (int k = 0; k < kKeepEach; ++k) {
       const int j = j0 + k;
       int64_t from = 0;
-      const int row = j < n ? __ldg(p.path + static_cast<int64_t>(i) * p.s + j) : j;
+      const int row = j < n ? p.path[static_cast<int64_t>(i) * p.s + j] : j;
       on[k] = j < n && row != j && slot_of(row, from) && slot_of(j, to[k]);
       if (on[k]) {
         if (is_scale) v[k].x = __float_as_uint(scale[from]);

@@ -61,7 +61,7 @@ template <typename T>
 __device__ __forceinline__ Vec<T> load_each(const T* row, int first, int n) {
   Vec<T> v;
 #pragma unroll
-  for (int i = 0; i < Vec<T>::N; ++i) v.x[i] = first + i >= 0 && first + i < n ? widen(__ldg(row + first + i)) : 0.f;
+  for (int i = 0; i < Vec<T>::N; ++i) v.x[i] = first + i >= 0 && first + i < n ? widen(row[first + i]) : 0.f;
   return v;
 }
 
@@ -175,8 +175,8 @@ __device__ void walk(const VerifyParams& p, const Rows& r, Sums& sh, int bi, int
     sh.n_gone = 0;
   }
   for (int j = tid; j < len; j += THREADS) {
-    const int x = __ldg(p.tokens + at + j);
-    const int par = j == 0 ? -1 : p.parents ? __ldg(p.parents + at + j) : j - 1;
+    const int x = p.tokens[at + j];
+    const int par = j == 0 ? -1 : p.parents ? p.parents[at + j] : j - 1;
     const bool node = j > 0 && par >= 0 && par < j, known = node && x >= 0 && x < p.vocab;
     const float pr = known ? widen(probs[par * p.probs_s + x]) : 0.f;
     r.token[j] = x;
@@ -185,7 +185,7 @@ __device__ void walk(const VerifyParams& p, const Rows& r, Sums& sh, int bi, int
     if (p.draft) {
       const float q = known ? widen(draft[j * p.draft_s + x]) : 0.f;
       // The product of two fp32 values is exact in fp64.
-      r.good[j] = j == 0 || (known && static_cast<double>(__ldg(p.uniform + at + j)) * q < static_cast<double>(pr));
+      r.good[j] = j == 0 || (known && static_cast<double>(p.uniform[at + j]) * q < static_cast<double>(pr));
     }
   }
   __syncthreads();
@@ -193,7 +193,7 @@ __device__ void walk(const VerifyParams& p, const Rows& r, Sums& sh, int bi, int
     // A chain: up to the first that is not accepted.
     for (int j = tid; j < len; j += THREADS) {
       bool good = j == 0;
-      if (j > 0) good = p.draft ? r.good[j] : __ldg(p.uniform + at + j) * static_cast<double>(kUnit) < static_cast<double>(r.mass[j]);
+      if (j > 0) good = p.draft ? r.good[j] : p.uniform[at + j] * static_cast<double>(kUnit) < static_cast<double>(r.mass[j]);
       if (!good) atomicMin(&sh.accepted, j);
     }
     __syncthreads();
@@ -229,7 +229,7 @@ __device__ void walk(const VerifyParams& p, const Rows& r, Sums& sh, int bi, int
     if (r.parent[j] >= 0)
       for (int i = r.parent[j] + 1; i < j; ++i) left -= r.parent[i] == r.parent[j] ? r.mass[i] : 0;
     if (left < 0) left = 0;
-    r.good[j] = r.parent[j] >= 0 && __dmul_rn(static_cast<double>(__ldg(p.uniform + at + j)), static_cast<double>(left)) <
+    r.good[j] = r.parent[j] >= 0 && __dmul_rn(static_cast<double>(p.uniform[at + j]), static_cast<double>(left)) <
                                           static_cast<double>(r.mass[j]);
   }
   __syncthreads();
@@ -279,12 +279,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
   const int bi = blockIdx.x / cluster, rank = blockIdx.x - bi * cluster;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   cluster_arrive();
-  // The kernel before is done (and the next one may be put in place, to wait here in its turn).
+  // The kernel before is done (and the next one may be put in place, to wait here in its turn).  It may have written anything that is
+  // read below while this one was already there: plain loads, which stay behind the wait.
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int len = p.seq_lens_q ? min(max(__ldg(p.seq_lens_q + bi), 0), p.s) : p.s;
+  const int len = p.seq_lens_q ? min(max(p.seq_lens_q[bi], 0), p.s) : p.s;
   const int64_t at = static_cast<int64_t>(bi) * p.s;
-  const float u0 = __ldg(p.uniform + at);
+  const float u0 = p.uniform[at];
   if (len > 0) walk<T, THREADS>(p, r, sh, bi, len);
   const int accepted = len > 0 ? sh.accepted : 0;
   // Behind the new token there is none; the token itself is written by the CTA that finds it.
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
   const int inner = (off + p.vocab) / N, inner0 = off ? 1 : 0;
   auto value = [&](int v, bool diff) {
     const int first = v * N - off;
-    Vec<T> x = v >= inner0 && v < inner ? unpack<T>(__ldg(reinterpret_cast<const uint4*>(row + first))) : load_each(row, first, p.vocab);
+    Vec<T> x = v >= inner0 && v < inner ? unpack<T>(*reinterpret_cast<const uint4*>(row + first)) : load_each(row, first, p.vocab);
     if (diff) {
       const Vec<T> y = load_each(less, first, p.vocab);
 #pragma unroll
@@ -353,9 +354,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
 #pragma unroll
         for (int k = 0; k < COUNT; ++k) {
           const int first = (v + 32 * k) * N - off;
-          a[k] = __ldg(reinterpret_cast<const uint4*>(row + first));
-          if constexpr (MODE == 1) b[k] = __ldg(reinterpret_cast<const uint4*>(less + first));
-          if constexpr (MODE == 2) c[k] = load_each(less, first, p.vocab);
+          a[k] = *reinterpret_cast<const uint4*>(row + first);
+          if constexpr (MODE == 1) b[k] = *reinterpret_cast<const uint4*>(less + first);
+          if constexpr (MODE == 2) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) c[k].x[e] = widen(less[first + e]);      // (all of them are the row's)
+          }
         }
 #pragma unroll
         for (int k = 0; k < COUNT; ++k) {
