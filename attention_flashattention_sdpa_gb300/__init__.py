@@ -796,7 +796,9 @@ def sdpa_cache_grow(page_table, seq_lens, new_lens, ref_counts, src, dst, missin
 
     A partly filled page that others own too is replaced: (src[i], dst[i]) (int32 [b]; -1: none) is the copy that row i needs
     before it is written, by :func:`sdpa_cache_copy` in every layer's cache.  All or nothing: ``missing`` (int32 [1]) is 0, or
-    the number of pages that lacked, and nothing has changed then.  Outputs that are None: in place."""
+    the number of pages that lacked, and nothing has changed then: what follows goes on with the old lengths and no new rows
+    (``rows = torch.where(missing == 0, s, 0)`` as seq_lens_q), or rows of sequences that still share a page would overwrite each
+    other.  Outputs that are None: in place."""
     p, b = _pages(page_table, seq_lens, ref_counts, page_table_out, ref_counts_out, page_size)
     new_at = _dense(new_lens, "new_lens", _Lazy.int32, (b,))
     src_at, dst_at, n = _pairs(src, dst)

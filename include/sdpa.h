@@ -464,7 +464,9 @@ SDPA_API sdpa_status_t sdpa_cache_fork(const sdpa_pages_t* p, const int32_t* par
  * partly filled page that others own too is replaced as well, by all of the rows that grow in it but the last owner: the free page takes its
  * column's place in that order, and (src[i], dst[i]) is the copy that row i needs before it is written
  * (DEVICE [b] each; -1, -1: none).  All or nothing: *missing (DEVICE) is 0, or the number of pages that
- * lacked, and nothing is changed then (outputs that lie apart are copies).  At most 4096 rows. */
+ * lacked, and nothing is changed then (outputs that lie apart are copies).  What follows must take *missing into account: a
+ * program that does not wait for it gives the calls behind this one the old lengths and 0 new rows (seq_lens_q) where it is not
+ * 0, as new rows would go into pages that sequences still share.  At most 4096 rows. */
 SDPA_API sdpa_status_t sdpa_cache_grow(const sdpa_pages_t* p, const int32_t* new_lens, int32_t* src, int32_t* dst,
                                        int32_t* missing, void* stream);
 
