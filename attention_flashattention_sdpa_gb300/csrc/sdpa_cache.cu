@@ -133,12 +133,13 @@ __device__ __forceinline__ void store_item(uint8_t* row, float* scale_at, int m,
 }
 
 // ROPE: 0 none, 1 rot a multiple of 16, 2 any even rot.
-// (A floor of one block an SM lets the compiler hold a few more registers, 122, still four blocks: 38.5 ->
-// 36.5 us.)
+// (A floor of one block an SM leaves the compiler the registers it wants, for rotated rows to E4M3 112 with RING and 123 without, four
+// blocks an SM either way: 4 x 8192 tokens of 8 heads of 128 41.0 -> 40.1 us.)
 // AXES: K has several positions a token.  RING: a thread's next heads come through shared memory, each thread's in slots of
-// its own (it waits for its own copies alone); otherwise the next one comes into registers, which is faster where a thread has
-// few heads (1024 tokens of 8 heads in BF16: 4.4 us against 4.6).  With it, 2 x 8192 tokens to E4M3 25.4 -> 23.0 us, rotated by three
-// axes 26.4 -> 23.1 (prompts above 37.2 -> 36.4); with 3 slots 24.2, with 6 25.1.
+// its own (it waits for its own copies alone), where whole heads are rotated and a thread has four or more: 4 x 4096 tokens of 8 heads to E4M3
+// 25.3 -> 23.2 us, 4 x 8192 40.8 -> 40.1, to BF16 50.2 -> 48.4 (with 3 slots or 6 about 5% more).  Otherwise the next one comes into registers:
+// with too little arithmetic between its loads a thread waits for the copies (4 x 4096 tokens to E4M3, half of each head rotated, 24.5 us
+// against 26.2; none 20.2 against 30.4).
 template <int D, int DT, int CT, int ROPE, bool AXES, bool RING>
 __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_constant__ CacheRowsParams p, int per,
                                                             bool small) {
@@ -184,8 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_c
 #pragma unroll
   for (int j = 0; j < (RING ? kSlots - 1 : 1); ++j) fetch(h0 + j);
   if constexpr (CT == kE4M3 && !RING) {
-    // The row's other heads start towards L2, a line a lane: 38.3 -> 36.5 us for the prompts above, 16 heads
-    // 44.0 -> 41.0.  (16-bit caches, copied without that much work between, were slower so: 44.6 -> 47.8.)
+    // The row's other heads start towards L2, a line a lane: 4 x 8192 tokens of 8 heads, half of each rotated, 44.3 -> 41.1 us; not rotated
+    // 4 x 4096 21.0 -> 20.2, 4 x 8192 36.9 -> 37.9.  (16-bit caches, copied without that much work between, were slower so: 44.6 -> 47.8.)
     constexpr int LINES = D / 64;
     for (int i = m; live && i < (h_end - h0 - 1) * LINES; i += LANES) {
       const int h = h0 + 1 + i / LINES, e = i % LINES * 64;
@@ -325,18 +326,23 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 template <int D, int DT, int CT>
 cudaError_t write_t(const CacheRowsParams& p, int num_sms, cudaStream_t st) {
   const int64_t tokens = static_cast<int64_t>(p.c.b) * p.s;
-  // Heads a thread walks: as many as leave 512 threads an SM, what it holds at once (with twice as many, 4096 tokens of 8 heads 13.8
-  // us against 10.3).
+  const bool vec = p.r.rot % 16 == 0, whole = p.rope && p.r.rot == D;
+  // Heads a thread walks: as many as leave 512 threads an SM (with 1024, 4096 tokens of 8 heads, rotated, to E4M3: 14.1 us against 10.5).
+  // Long walks of heads that are mostly copied need more threads, 1024: walks of 4 and 8 heads that are not rotated (16384 tokens of 8 heads to
+  // E4M3: 19.8 us, 22.0 with 512), of 8 that are rotated in part.
+  const int cheap = !p.rope ? 4 : whole ? 16 : 8;       // walks as long as this need 1024
+  // (12 heads to E4M3 as three walks of 4, not as one of 8 and half a one: 16384 tokens of 64 elements, rotated, 19.7 us against 21.1.)
   int per = p.c.h_kv > 4 ? 8 : p.c.h_kv > 2 ? 4 : p.c.h_kv;
-  while (per > 1 && tokens * (D / 16) * ((p.c.h_kv + per - 1) / per) < static_cast<int64_t>(num_sms) * 512) per /= 2;
+  if (CT == kE4M3 && p.c.h_kv > 8 && (p.c.h_kv - 1) % 8 < 4) per = 4;
+  while (per > 1 && tokens * (D / 16) * ((p.c.h_kv + per - 1) / per) < static_cast<int64_t>(num_sms) * (per >= cheap ? 1024 : 512)) per /= 2;
   const int groups = (p.c.h_kv + per - 1) / per;
   const int64_t blocks = (tokens * (D / 16) * groups + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(blocks);
   const bool small = blocks * kThreads < (int64_t(1) << 31);
   auto run = [&](auto kernel) { kernel<<<grid, kThreads, 0, st>>>(p, per, small); };
-  const bool vec = p.r.rot % 16 == 0, ring = per >= 4;
-  if (!p.rope) run(ring ? cache_write_kernel<D, DT, CT, 0, false, true> : cache_write_kernel<D, DT, CT, 0, false, false>);
+  const bool ring = whole && per >= 4;
+  if (!p.rope) run(cache_write_kernel<D, DT, CT, 0, false, false>);
   else if (vec && p.r.axes) run(ring ? cache_write_kernel<D, DT, CT, 1, true, true> : cache_write_kernel<D, DT, CT, 1, true, false>);
   else if (vec) run(ring ? cache_write_kernel<D, DT, CT, 1, false, true> : cache_write_kernel<D, DT, CT, 1, false, false>);
   else run(p.r.axes ? cache_write_kernel<D, DT, CT, 2, true, false> : cache_write_kernel<D, DT, CT, 2, false, false>);
