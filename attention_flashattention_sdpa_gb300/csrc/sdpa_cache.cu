@@ -132,7 +132,7 @@ __device__ __forceinline__ void store_item(uint8_t* row, float* scale_at, int m,
   }
 }
 
-// ROPE: 0 none, 1 rot a multiple of 16, 2 any even rot.
+// ROPE: 0 none, 1 rot a multiple of 16; any even rot, 2 with the angles computed once for all heads, 3 for each head anew (walks of few heads).
 // (A floor of one block an SM leaves the compiler the registers it wants, for rotated rows to E4M3 112 with RING and 123 without, four
 // blocks an SM either way: 4 x 8192 tokens of 8 heads of 128 41.0 -> 40.1 us.)
 // AXES: K has several positions a token.  RING: a thread's next heads come through shared memory, each thread's in slots of
@@ -210,12 +210,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_c
     }
   }
   // 16 neighbours, each with an angle and a partner of its own, `other` elements away.
-  const int half = p.r.rot / 2, turns = ROPE == 2 ? min(16, p.r.rot - m * 16) : 0;
+  const int half = p.r.rot / 2, turns = ROPE >= 2 ? min(16, p.r.rot - m * 16) : 0;
   auto is_first = [&](int i) { return p.r.interleaved ? i % 2 == 0 : m * 16 + i < half; };
+  auto pair_of = [&](int i) { return p.r.interleaved ? (m * 16 + i) / 2 : m * 16 + i - (is_first(i) ? 0 : half); };
   if constexpr (ROPE == 2) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int e = m * 16 + i, pair = p.r.interleaved ? e / 2 : e < half ? e : e - half;
+      const int pair = pair_of(i);
       if (live && i < turns) rope_angle(p.r, __ldg(p.r.table + pair), rpos.of(axes_from<AXES>(p.r, pair)), c[i], s[i]);
     }
   }
@@ -256,6 +257,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_write_kernel(const __grid_c
           const bool first = is_first(i);
           const float b = p.r.interleaved ? a[i ^ 1] : load16<DT>(p.k, krow + i + (first ? half : -half));
           x[i] = first ? a[i] * c[i] - b * s[i] : b * s[i] + a[i] * c[i];
+        }
+      }
+      if constexpr (ROPE == 3) {
+        const int64_t krow = bi * p.k_st[0] + h * p.k_st[1] + si * p.k_st[2];
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+          const int e = m * 16 + i;
+          if (e >= p.r.rot) break;
+          const bool first = is_first(i);
+          const int pair = pair_of(i), other = p.r.interleaved ? e ^ 1 : first ? e + half : e - half;
+          float cc, ss;
+          rope_angle(p.r, __ldg(p.r.table + pair), rpos.of(axes_from<AXES>(p.r, pair)), cc, ss);
+          const float a = load16<DT>(p.k, krow + e), b = load16<DT>(p.k, krow + other);
+          x[i] = first ? a * cc - b * ss : b * ss + a * cc;
         }
       }
     } else {
@@ -328,13 +343,28 @@ cudaError_t write_t(const CacheRowsParams& p, int num_sms, cudaStream_t st) {
   const int64_t tokens = static_cast<int64_t>(p.c.b) * p.s;
   const bool vec = p.r.rot % 16 == 0, whole = p.rope && p.r.rot == D;
   // Heads a thread walks: as many as leave 512 threads an SM (with 1024, 4096 tokens of 8 heads, rotated, to E4M3: 14.1 us against 10.5).
-  // Long walks of heads that are mostly copied need more threads, 1024: walks of 4 and 8 heads that are not rotated (16384 tokens of 8 heads to
-  // E4M3: 19.8 us, 22.0 with 512), of 8 that are rotated in part.
-  const int cheap = !p.rope ? 4 : whole ? 16 : 8;       // walks as long as this need 1024
-  // (12 heads to E4M3 as three walks of 4, not as one of 8 and half a one: 16384 tokens of 64 elements, rotated, 19.7 us against 21.1.)
-  int per = p.c.h_kv > 4 ? 8 : p.c.h_kv > 2 ? 4 : p.c.h_kv;
-  if (CT == kE4M3 && p.c.h_kv > 8 && (p.c.h_kv - 1) % 8 < 4) per = 4;
-  while (per > 1 && tokens * (D / 16) * ((p.c.h_kv + per - 1) / per) < static_cast<int64_t>(num_sms) * (per >= cheap ? 1024 : 512)) per /= 2;
+  // Walks of `cheap` heads and more, which are mostly copied, need more threads, 1024: 4 and 8 that are not rotated (16384 tokens of 8 heads to
+  // E4M3: 19.8 us, 22.0 with 512), 8 that are rotated in part.
+  auto walk = [&](int per, int cheap) {
+    while (per > 1 && tokens * (D / 16) * ((p.c.h_kv + per - 1) / per) < static_cast<int64_t>(num_sms) * (per >= cheap ? 1024 : 512)) per /= 2;
+    return per;
+  };
+  const int longest = p.c.h_kv > 4 ? 8 : p.c.h_kv > 2 ? 4 : p.c.h_kv;
+  int per;
+  bool each = false;
+  if (p.rope && !vec) {
+    // Angles computed once for all heads cost 168 to 186 registers a thread.  They pay for walks of 2 heads and more of adjacent pairs in 16 bits
+    // (16384 tokens of 2 heads 19.3 us, with each head's anew 21.1), of 4 of halves (4096 of 16: 31.9 against 38) and of adjacent pairs to
+    // E4M3 (34.6 against 36.5), of 8 of halves to E4M3 (16384 of 8: 67 against 70).  One less: 16384 of 1 in 16 bits, pairs 16.5 against 13.7;
+    // to E4M3 16384 of 2, pairs 25.4 against 20.8, halves (4096 of 16) 42.3 against 35.6.
+    per = walk(longest, 16);
+    each = per < (CT == kE4M3 ? 2 : 1) * (p.r.interleaved ? 2 : 4);
+    if (each) per = walk(longest, 1);
+  } else {
+    // (12 heads to E4M3 as three walks of 4, not as one of 8 and half a one: 16384 tokens of 64 elements, rotated, 19.7 us against 21.1.)
+    const bool thirds = CT == kE4M3 && p.c.h_kv > 8 && (p.c.h_kv - 1) % 8 < 4;
+    per = walk(thirds ? 4 : longest, !p.rope ? 4 : whole ? 16 : 8);
+  }
   const int groups = (p.c.h_kv + per - 1) / per;
   const int64_t blocks = (tokens * (D / 16) * groups + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
@@ -345,6 +375,7 @@ cudaError_t write_t(const CacheRowsParams& p, int num_sms, cudaStream_t st) {
   if (!p.rope) run(cache_write_kernel<D, DT, CT, 0, false, false>);
   else if (vec && p.r.axes) run(ring ? cache_write_kernel<D, DT, CT, 1, true, true> : cache_write_kernel<D, DT, CT, 1, true, false>);
   else if (vec) run(ring ? cache_write_kernel<D, DT, CT, 1, false, true> : cache_write_kernel<D, DT, CT, 1, false, false>);
+  else if (each) run(p.r.axes ? cache_write_kernel<D, DT, CT, 3, true, false> : cache_write_kernel<D, DT, CT, 3, false, false>);
   else run(p.r.axes ? cache_write_kernel<D, DT, CT, 2, true, false> : cache_write_kernel<D, DT, CT, 2, false, false>);
   return cudaGetLastError();
 }
