@@ -15,8 +15,10 @@
 // Bound: reading one row of p (and one of q) of each sequence.  The tests need a few single values, which a
 // thread each fetches at once; a cluster of CTAs shares a row, sums meet in its shared memory, and the CTA
 // that the drawn number falls into reads the piece of the row once more, from L2.  Measured (replayed): 64 rows of 131072 fp32
-// values of p and q 16.0 us from HBM (3.7 TB/s), 10.5 from L2; one of 32000 5.3: the launch, and five latencies in a row
-// (tokens, their probabilities, the row, the cluster's barrier, the piece), which the stream waits for.
+// values of p and q 16.0 us from HBM (3.7 TB/s), 10.5 from L2; one of 32000 5.4: the launch, and five latencies in a row
+// (tokens, their probabilities, the row, the cluster's barrier, the piece), which the stream waits for; without q the random
+// numbers of the tests are one more, behind the probabilities.  Rows of q lie at another offset from 16 bytes than p's where the vocabulary is
+// no multiple of a vector, and come element by element then: 64 rows of 131073 16.5 us (BF16 15.3, of 131072 12.2).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -521,7 +521,9 @@ typedef struct {
  *                                                                                   that an earlier sibling has too is refused).
  * The new token is drawn behind the last accepted row n: from max(probs[n] - draft_probs[i], 0) where a chain's row i was refused,
  * from probs[n] without its children's tokens where there are no draft_probs; from probs[n] where that leaves nothing.
- * Tokens so chosen are distributed as the target's own.  In sums and draws a probability counts as a whole number of 2^-42
+ * Tokens so chosen are distributed as the target's own; without draft_probs as far as its rows sum to one, since the tests take
+ * the total for one and the draw goes by the sum that is there (rows in 16 bits are off by what their roundings add up to).
+ * Differences of probabilities are rounded to fp32.  In sums and draws a probability counts as a whole number of 2^-42
  * (values outside [0, 1] as the nearer end, NaN as 0; 2^-43 and less is nothing): the new token is the first whose running sum exceeds
  * floor(uniform[0] * 2^31) / 2^31 of the total, whatever the order of the sums.  Where the total is 0 it is -1. */
 SDPA_API sdpa_status_t sdpa_verify(const sdpa_verify_t* p, void* stream);
