@@ -1,5 +1,5 @@
-"""The step of drafted trees as README.md has it, with pages enough and with too few (GPU): a step that finds no room for its
-rows writes none, reads nothing back to the host, and leaves what the sequences hold as it is."""
+"""The step of drafted trees as the package's front page shows it, with pages enough and with too few (GPU): a step that finds no room
+for its rows writes none, reads nothing back to the host, and leaves what the sequences hold as it is."""
 import os
 import re
 
@@ -22,7 +22,7 @@ def readme_step():
     with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
         blocks = re.findall(r"```python\n(.*?)```", f.read(), re.S)
     step, = [x for x in blocks if "sdpa_cache_grow" in x]
-    return compile(step, "README.md", "exec")
+    return compile(step, "step", "exec")
 
 
 def state(kind, spare):
